@@ -10,7 +10,8 @@ integers, ``stream`` a ``cudaStream_t`` value):
     fa_decode_paged_fwd, fa_backward,
     fa_decode_fwd_noalloc, fa_status_string, fa_device_error, fa_last_cuda_error,
     fa_num_sms, fa_prefill_work_item, fa_prefill_rescale_count, fa_set_wait_limit_ns,
-    fa_prefill_fwd_host, fa_prefill_host_pieces
+    fa_prefill_fwd_host, fa_prefill_host_pieces, fa_qk_norm_rope, fa_qk_norm_rope_append,
+    fa_qk_norm_rope_backward, fa_decode_tree_fwd, fa_verify_tree, fa_compact_tree
 Tensor conveniences (contiguous CUDA tensors, caller-owned outputs):
     prefill(q, k, v, scale, causal, out=None, stream=None, lse=None)
     prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, scale, causal,
@@ -20,6 +21,19 @@ Tensor conveniences (contiguous CUDA tensors, caller-owned outputs):
                  lse=None)
     backward(q, k, v, o, dout, lse, scale, causal, stream=None) -> (dq, dk, dv)
     prefill_host(q, k, v, out, scale, causal, n_pieces=16, stream=None)
+    qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved=False,
+                 q_out=None, k_out=None, stream=None) -> (q_out, k_out)
+    qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, eps,
+                          interleaved=False, stream=None) -> (dq, dk, dq_weight, dk_weight)
+    qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table,
+                        seqlens, eps, positions=None, interleaved=False, q_out=None,
+                        stream=None) -> q_out
+    decode_tree(q, kpages, vpages, page_table, seqlens, parents, scale, out=None, stream=None,
+                lse=None)
+    verify_tree(target_probs, draft_probs, tokens, parents, uniforms, stream=None)
+                -> (path, count, next_token)
+    compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=None,
+                 stream=None) -> seqlens_out
     (lse=True allocates the fp32 log-sum-exp output; a tensor is used as is.)
 """
 import ctypes
@@ -38,7 +52,9 @@ EXPORTS = ("fa_prefill_fwd", "fa_prefill_fwd_lse", "fa_prefill_varlen_fwd", "fa_
            "fa_decode_fwd_lse", "fa_decode_paged_fwd", "fa_backward",
            "fa_decode_fwd_noalloc", "fa_status_string", "fa_device_error", "fa_last_cuda_error",
            "fa_num_sms", "fa_prefill_work_item", "fa_prefill_rescale_count",
-           "fa_set_wait_limit_ns", "fa_prefill_fwd_host", "fa_prefill_host_pieces")
+           "fa_set_wait_limit_ns", "fa_prefill_fwd_host", "fa_prefill_host_pieces",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_append", "fa_qk_norm_rope_backward",
+           "fa_decode_tree_fwd", "fa_verify_tree", "fa_compact_tree")
 
 _lib = None
 
@@ -104,6 +120,22 @@ def load(path: str = LIB_PATH):
     lib.fa_prefill_fwd_host.restype = i32
     lib.fa_prefill_host_pieces.argtypes = [i32, i32, i32, i32, i32, ip, ip, ip, ip, i32]
     lib.fa_prefill_host_pieces.restype = i32
+    i64 = ctypes.c_longlong
+    lib.fa_qk_norm_rope.argtypes = [vp] * 8 + [i64, i32, i32, i32, i32, i64, i64, f32, i32, i32,
+                                               vp]
+    lib.fa_qk_norm_rope.restype = i32
+    lib.fa_qk_norm_rope_append.argtypes = [vp] * 12 + [i32] * 9 + [i64, i64, i64, f32, i32, i32,
+                                                                   vp]
+    lib.fa_qk_norm_rope_append.restype = i32
+    lib.fa_qk_norm_rope_backward.argtypes = [vp] * 12 + [i64, i32, i32, i32, i32, i64, i64, f32,
+                                                         i32, i32, vp]
+    lib.fa_qk_norm_rope_backward.restype = i32
+    lib.fa_decode_tree_fwd.argtypes = [vp] * 8 + [i32] * 8 + [f32, i32, vp]
+    lib.fa_decode_tree_fwd.restype = i32
+    lib.fa_verify_tree.argtypes = [vp] * 8 + [i32] * 3 + [vp]
+    lib.fa_verify_tree.restype = i32
+    lib.fa_compact_tree.argtypes = [vp] * 7 + [i32] * 8 + [vp]
+    lib.fa_compact_tree.restype = i32
     _lib = lib
     return lib
 
@@ -174,6 +206,51 @@ def fa_decode_fwd_noalloc(q, kcache, vcache, valid_len_dev, o, B, Hq, Hkv, cap, 
     Returns FA_ERR_TOO_LARGE for requests whose partials do not fit."""
     return load().fa_decode_fwd_noalloc(q, kcache, vcache, valid_len_dev, o, B, Hq, Hkv, cap, D,
                                         scale, stream)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, T, Hq, Hkv, D,
+                    rot_dim, q_stride, k_stride, eps, interleaved, dtype, stream):
+    return load().fa_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, T,
+                                  Hq, Hkv, D, rot_dim, q_stride, k_stride, eps, interleaved,
+                                  dtype, stream)
+
+
+def fa_qk_norm_rope_append(q, k, v, q_out, kpages, vpages, q_weight, k_weight, inv_freq,
+                           positions, page_table, seqlens, B, N, Hq, Hkv, num_pages, page_size,
+                           max_pages, D, rot_dim, q_stride, k_stride, v_stride, eps, interleaved,
+                           dtype, stream):
+    return load().fa_qk_norm_rope_append(q, k, v, q_out, kpages, vpages, q_weight, k_weight,
+                                         inv_freq, positions, page_table, seqlens, B, N, Hq, Hkv,
+                                         num_pages, page_size, max_pages, D, rot_dim, q_stride,
+                                         k_stride, v_stride, eps, interleaved, dtype, stream)
+
+
+def fa_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq,
+                             dk, dq_weight, dk_weight, T, Hq, Hkv, D, rot_dim, q_stride, k_stride,
+                             eps, interleaved, dtype, stream):
+    return load().fa_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq,
+                                           positions, dq, dk, dq_weight, dk_weight, T, Hq, Hkv, D,
+                                           rot_dim, q_stride, k_stride, eps, interleaved, dtype,
+                                           stream)
+
+
+def fa_decode_tree_fwd(q, kpages, vpages, page_table, seqlens, parents, o, lse, B, N, Hq, Hkv,
+                       num_pages, page_size, max_pages, D, scale, dtype, stream):
+    return load().fa_decode_tree_fwd(q, kpages, vpages, page_table, seqlens, parents, o, lse, B,
+                                     N, Hq, Hkv, num_pages, page_size, max_pages, D, scale, dtype,
+                                     stream)
+
+
+def fa_verify_tree(target_probs, draft_probs, tokens, parents, uniforms, path, count, next_token,
+                   B, N, V, stream):
+    return load().fa_verify_tree(target_probs, draft_probs, tokens, parents, uniforms, path,
+                                 count, next_token, B, N, V, stream)
+
+
+def fa_compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out, layers, B, N,
+                    Hkv, num_pages, page_size, max_pages, D, stream):
+    return load().fa_compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out,
+                                  layers, B, N, Hkv, num_pages, page_size, max_pages, D, stream)
 
 
 def fa_status_string(status) -> str:
@@ -464,3 +541,299 @@ def backward(q, k, v, o, dout, lse, scale, causal, stream=None):
     if st != FA_OK:
         raise FAError(st, "fa_backward")
     return dq, dk, dv
+
+
+def _here(*tensors):
+    """The tensors share the current device (kernels launch on it)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensors must be on the current device (cuda:{dev})")
+
+
+def _allocating_on(stream):
+    """Context in which new tensors belong to the call's stream: their memory
+    is then not still in use, nor reused too early, by another stream."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _int32(t, name, shape):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    _check(t, name)
+
+
+def _heads(t, name):
+    """(leading shape, tokens, heads, D, token stride) of [..., H, D]: heads
+    contiguous, tokens at one stride (a slice of a packed projection is fine)."""
+    if t.dim() < 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [..., heads, D]")
+    lead, (H, D) = tuple(t.shape[:-2]), t.shape[-2:]
+    T = 1
+    for n in lead:
+        T *= n
+    want, ts = H * D, None  # stride of the innermost leading axis longer than 1
+    ok = T == 0 or H == 0 or ((D <= 1 or t.stride(-1) == 1) and (H <= 1 or t.stride(-2) == D))
+    if ok and T > 1 and H > 0:
+        step = None
+        for n, st in zip(reversed(lead), reversed(t.stride()[:-2])):
+            if n == 1:
+                continue
+            if ts is None:
+                ts = st
+            elif st != step:
+                ok = False
+            step = st * n
+    if not ok:
+        raise ValueError(f"{name}: heads must be contiguous and tokens at one stride")
+    return lead, T, H, D, want if ts is None else ts
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions):
+    import torch
+    lead, T, Hq, D, qs = _heads(q, "q")
+    lead_k, _, Hkv, Dk, ks = _heads(k, "k")
+    if lead_k != lead or Dk != D:
+        raise ValueError("q and k must share their leading shape and head dimension")
+    _dtype_code(q)
+    for t, n in ((k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t.dtype != q.dtype:
+            raise TypeError(f"{n} must have q's dtype")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if tuple(t.shape) != (D,):
+            raise ValueError(f"{n} must have shape ({D},)")
+        _check(t, n)
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a float32 CUDA tensor [rot_dim / 2]")
+    _check(inv_freq, "inv_freq")
+    if positions is not None:
+        _int32(positions, "positions", lead)
+    return lead, T, Hq, Hkv, D, qs, ks
+
+
+def _like(t, out, name):
+    import torch
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if out.dtype != t.dtype or tuple(out.shape) != tuple(t.shape):
+        raise ValueError(f"{name} must have the input's shape and dtype")
+    _check(out, name)
+    return out
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [...,Hq,D] and k [...,Hkv,D], times the
+    weights [D], then the rotation by position (int32 [...]): pair i turns by
+    position * inv_freq[i].  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
+    interleaved, rot = 2 * len(inv_freq); further elements pass through.  q and
+    k may be slices of one packed projection.  Returns contiguous (q_out, k_out)."""
+    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    _here(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)
+    with _allocating_on(stream):
+        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
+    st = fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                         q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
+                         positions.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
+                         float(eps), int(bool(interleaved)), _dtype_code(q),
+                         _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, eps,
+                          interleaved=False, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope from those of
+    its outputs (contiguous).  The weights' gradients are float32."""
+    import torch
+    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    for t, like, n in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
+        if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
+            raise ValueError(f"{n} must have the output's shape and dtype")
+        _check(t, n)
+    _here(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions)
+    with _allocating_on(stream):
+        dq, dk = _like(q, None, "dq"), _like(k, None, "dk")
+        dqw, dkw = (torch.empty(D, dtype=torch.float32, device=q.device) if H else
+                    torch.zeros(D, dtype=torch.float32, device=q.device) for H in (Hq, Hkv))
+    st = fa_qk_norm_rope_backward(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
+                                  k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+                                  inv_freq.data_ptr(), positions.data_ptr(), dq.data_ptr(),
+                                  dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), T, Hq, Hkv, D,
+                                  2 * inv_freq.numel(), qs, ks, float(eps),
+                                  int(bool(interleaved)), _dtype_code(q), _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table,
+                        seqlens, eps, positions=None, interleaved=False, q_out=None, stream=None):
+    """qk_norm_rope of N new tokens per sequence (q [B,N,Hq,D], k/v
+    [B,N,Hkv,D]), k and v written into the paged cache: token s of sequence b
+    goes to slot seqlens[b] - N + s (lengths include the new tokens).
+    positions: int32 [B,N], or None for the slot.  Returns q_out."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B,N,heads,D]")
+    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    B, N = lead
+    if tuple(v.shape) != tuple(k.shape):
+        raise ValueError("k and v shapes differ")
+    vs = _heads(v, "v")[4]
+    num_pages, page_size, Hp, Dp = kpages.shape
+    if (Hp, Dp) != (Hkv, D) or tuple(vpages.shape) != tuple(kpages.shape):
+        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
+    for t, n in ((v, "v"), (kpages, "kpages"), (vpages, "vpages")):
+        if t.dtype != q.dtype:
+            raise TypeError(f"{n} must have q's dtype")
+    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
+        _check(t, n)
+    max_pages = page_table.shape[-1]
+    _int32(page_table, "page_table", (B, max_pages))
+    _int32(seqlens, "seqlens", (B,))
+    _here(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table, seqlens, positions,
+          q_out)
+    with _allocating_on(stream):
+        q_out = _like(q, q_out, "q_out")
+    st = fa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                                kpages.data_ptr(), vpages.data_ptr(), q_weight.data_ptr(),
+                                k_weight.data_ptr(), inv_freq.data_ptr(),
+                                0 if positions is None else positions.data_ptr(),
+                                page_table.data_ptr(), seqlens.data_ptr(), B, N, Hq, Hkv,
+                                num_pages, page_size, max_pages, D, 2 * inv_freq.numel(), qs, ks,
+                                vs, float(eps), int(bool(interleaved)), _dtype_code(q),
+                                _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_qk_norm_rope_append")
+    return q_out
+
+
+def decode_tree(q, kpages, vpages, page_table, seqlens, parents, scale, out=None, stream=None,
+                lse=None):
+    """Attention of N drafted tree nodes per sequence over a paged cache.
+
+    q [B,N,Hq,D]; kpages/vpages [num_pages,page_size,Hkv,D], one dtype (bf16 or
+    fp16); page_table int32 [B,max_pages]; seqlens int32 [B] (lengths including
+    the N nodes, whose K/V are already in the cache); parents int32 [B,N] (a
+    lower node, -1 for a root, -2 for an unused slot).  Node s sees the keys
+    before the tree, its ancestors and itself.  Returns ``out`` like q, or (out,
+    lse) with lse [B,N,Hq] fp32 when lse is True or a tensor."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B,N,Hq,D]")
+    B, N, Hq, D = q.shape
+    num_pages, page_size, Hkv, Dp = kpages.shape
+    if Dp != D or tuple(vpages.shape) != tuple(kpages.shape):
+        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
+    code = _dtype_code(q)
+    if kpages.dtype != q.dtype or vpages.dtype != q.dtype:
+        raise TypeError("q, kpages, vpages must share a dtype")
+    for t, n in ((q, "q"), (kpages, "kpages"), (vpages, "vpages")):
+        _check(t, n)
+    max_pages = page_table.shape[-1]
+    _int32(page_table, "page_table", (B, max_pages))
+    _int32(seqlens, "seqlens", (B,))
+    _int32(parents, "parents", (B, N))
+    want_lse = lse is not None and lse is not False
+    _here(q, kpages, vpages, page_table, seqlens, parents, out, lse if lse is not True and want_lse
+          else None)
+    with _allocating_on(stream):
+        out = _like(q, out, "out")
+        if want_lse:
+            lse = _lse_tensor(lse, (B, N, Hq), q)
+    st = fa_decode_tree_fwd(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
+                            page_table.data_ptr(), seqlens.data_ptr(), parents.data_ptr(),
+                            out.data_ptr(), lse.data_ptr() if want_lse else 0, B, N, Hq, Hkv,
+                            num_pages, page_size, max_pages, D, float(scale), code,
+                            _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_decode_tree_fwd")
+    return (out, lse) if want_lse else out
+
+
+def verify_tree(target_probs, draft_probs, tokens, parents, uniforms, stream=None):
+    """The path of a drafted tree that the target accepts, and the next token.
+
+    target_probs [B,N,V] float32: the target's distribution after each node;
+    draft_probs [B,N,V] float32: the one each node's children were drawn from,
+    or None for drafts chosen outright; tokens, parents int32 [B,N] (node 0 is
+    the root); uniforms float32 [B,N] in [0,1) (entry 0 draws the next token).
+    Returns int32 (path [B,N], count [B], next_token [B]): the accepted nodes,
+    root first, padded with -1."""
+    import torch
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must be [B,N,V]")
+    B, N, V = target_probs.shape
+    for t, n, shape in ((target_probs, "target_probs", (B, N, V)),
+                        (draft_probs, "draft_probs", (B, N, V)), (uniforms, "uniforms", (B, N))):
+        if t is None and n == "draft_probs":
+            continue
+        if t.dtype != torch.float32:
+            raise TypeError(f"{n} must be a float32 CUDA tensor")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must have shape {shape}")
+        _check(t, n)
+    _int32(tokens, "tokens", (B, N))
+    _int32(parents, "parents", (B, N))
+    _here(target_probs, draft_probs, tokens, parents, uniforms)
+    dev = target_probs.device
+    with _allocating_on(stream):
+        path = torch.empty((B, N), dtype=torch.int32, device=dev)
+        count = torch.empty(B, dtype=torch.int32, device=dev)
+        nxt = torch.empty(B, dtype=torch.int32, device=dev)
+    st = fa_verify_tree(target_probs.data_ptr(),
+                        0 if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
+                        parents.data_ptr(), uniforms.data_ptr(), path.data_ptr(),
+                        count.data_ptr(), nxt.data_ptr(), B, N, V, _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_verify_tree")
+    return path, count, nxt
+
+
+def compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=None,
+                 stream=None):
+    """Keeps the accepted path of a drafted tree: in every layer of kpages and
+    vpages ([num_pages,page_size,Hkv,D], or [layers,...]), in place, row
+    path[b][i] of the tree's N slots moves to row i, for i < count[b].  seqlens
+    int32 [B] include the N nodes.  Returns the new lengths (seqlens_out, which
+    may be seqlens; a new tensor if None)."""
+    import torch
+    if kpages.dim() not in (4, 5) or tuple(vpages.shape) != tuple(kpages.shape):
+        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D] or [layers,...]")
+    if kpages.dtype != vpages.dtype:
+        raise TypeError("kpages and vpages must share a dtype")
+    _dtype_code(kpages)
+    layers = kpages.shape[0] if kpages.dim() == 5 else 1
+    num_pages, page_size, Hkv, D = kpages.shape[-4:]
+    if path.dim() != 2:
+        raise ValueError("path must be [B,N]")
+    B, N = path.shape
+    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
+        _check(t, n)
+    max_pages = page_table.shape[-1]
+    _int32(page_table, "page_table", (B, max_pages))
+    _int32(seqlens, "seqlens", (B,))
+    _int32(path, "path", (B, N))
+    _int32(count, "count", (B,))
+    _here(kpages, vpages, page_table, seqlens, path, count, seqlens_out)
+    if seqlens_out is None:
+        with _allocating_on(stream):
+            seqlens_out = torch.empty_like(seqlens)
+    _int32(seqlens_out, "seqlens_out", (B,))
+    st = fa_compact_tree(kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
+                         seqlens.data_ptr(), path.data_ptr(), count.data_ptr(),
+                         seqlens_out.data_ptr(), layers, B, N, Hkv, num_pages, page_size,
+                         max_pages, D, _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_compact_tree")
+    return seqlens_out

@@ -1,6 +1,6 @@
 """Build libfa_gb300.so in-tree with nvcc for sm_103a.
 
-The three translation units compile in parallel, then link into one shared
+The translation units compile in parallel, then link into one shared
 library next to this file.  No CMake, no torch extension machinery.
 """
 import os
@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_decode.cu", "fa_decode_noalloc.cu",
-           "fa_backward.cu", "fa_host.cu"]
+           "fa_backward.cu", "fa_host.cu", "fa_rope.cu", "fa_tree.cu", "fa_verify.cu"]
 HEADERS = ["fa_ptx.cuh", "fa_internal.h"]
 
 NVCC = os.environ.get("NVCC", "nvcc")

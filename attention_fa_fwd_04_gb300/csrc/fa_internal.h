@@ -73,6 +73,9 @@ int read_backward_error(unsigned int* out, int reset);
 // Device error words of the kernel translation units (read + optionally clear).
 int read_prefill_error(unsigned int* out, int reset);
 int read_decode_error(unsigned int* out, int reset);
+int read_rope_error(unsigned int* out, int reset);
+int read_tree_error(unsigned int* out, int reset);
+int read_verify_error(unsigned int* out, int reset);
 
 // Rows whose prefill lazy rescale fired since the last reset (read + optionally
 // clear).  Returns a cudaError_t.
@@ -83,6 +86,7 @@ int read_prefill_rescales(unsigned long long* out, int reset);
 int set_prefill_wait_limit(unsigned long long ns);
 int set_decode_wait_limit(unsigned long long ns);
 int set_backward_wait_limit(unsigned long long ns);
+int set_tree_wait_limit(unsigned long long ns);
 
 // Status of a CUDA call for the C ABI: FA_OK for 0, else FA_ERR_CUDA after
 // recording the raw error and the failing call (a static string) for

@@ -1,0 +1,995 @@
+// fa_tree.cu -- attention of a tree of drafted tokens over a paged KV cache.
+//
+// What it computes: sequence b has L valid tokens, the last N of them the
+// nodes of a tree (node s at position L - N + s, its parent a lower node).
+// Query row (s, h) attends to the keys before the tree and to the nodes on its
+// own way to the root, itself among them:
+//   O = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale <q, K_j> - max),
+//   j < L - N, or j = L - N + a for an ancestor-or-self a of s.
+//
+// Bound: each K/V byte is read once per row tile, and serves N * G query rows
+// (G = Hq / Hkv).  128 rows are 128 flops per byte, half of what the card
+// needs to be matrix-bound, so up to about 256 rows per kv head the cache
+// stream from HBM bounds it, and the matrix units above.
+//
+// Design: the rows (s, g) of one kv head are the M of tcgen05 MMAs against
+// 128-key tiles of the paged cache (S = Q K^T and O += P V, both accumulated in
+// tensor memory, P written back over S as PV's operand).
+//   CTA = MT warpgroups of softmax (one 128-row tile each), one TMA producer
+//   warp, one MMA warp.  MT = 1 (up to 128 rows per kv head): S is
+//   double-buffered, so S of the next tile runs under this tile's softmax.
+//   MT = 2: two row tiles share every K/V tile, one's MMAs under the other's
+//   softmax.
+// Split: lengths are device data.  All K/V tiles of all (sequence, kv head)
+// units form one list, cut into equal ranges, one per group of n_rt CTAs (one
+// CTA per row tile, side by side, so that they share K/V through L2).  A range
+// may end inside a unit; its part of that unit goes to fp32 partials (O, max,
+// sum) that a second kernel merges.  A unit inside one range is finished in
+// place.  So every SM streams the same number of tiles whatever the lengths,
+// and a CTA writes at most two partials.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "fa.h"
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_tree_err = 0;
+
+namespace tr {
+constexpr int BM = 128;    // query rows per tile
+constexpr int BN = 128;    // keys per K/V tile
+constexpr int MAX_N = 64;  // tree nodes: one 64-bit ancestor mask per row
+constexpr int HALF_BYTES = 128 * 128;  // 128 rows x 64 elements x 2 bytes
+constexpr int BAD_RING = 16;  // tiles whose page faults are remembered (> tiles in flight)
+
+template <int D, int MT>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
+  // MT = 2: three warpgroups, for the register split (setmaxnreg): launched with
+  // 168 registers a thread, the softmax warpgroups take 208, the third keeps 88
+  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).
+  static constexpr int THREADS = MT == 1 ? 192 : 384;
+  static constexpr int RT = MT * BM;  // rows per CTA
+  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 5) : 12;
+  static constexpr int SMEM_Q = MT * TILE_BYTES;
+  static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
+  static constexpr int SMEM_BAR = 512;
+  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV + SMEM_BAR;
+  static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
+  static_assert(NSTAGE / 2 + 2 < BAD_RING, "tiles in flight");
+  // Tensor memory: two S buffers (MT = 1: of alternate tiles; MT = 2: of the
+  // two row tiles), then O of each row tile.
+  static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
+};
+}  // namespace tr
+
+struct TreeParams {
+  const void* q;  // [B, N, Hq, D]
+  void* o;        // [B, N, Hq, D]
+  float* lse;     // [B, N, Hq] or null
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  const int32_t* parents;  // [B, N]
+  float* part_o;           // [CTAs][2][rt_rows][D] unnormalised partial outputs
+  float* part_ml;          // [CTAs][2][rt_rows][2] (max in log2 units, sum)
+  long long* start;        // [B + 1] first tile of each sequence in the list
+  int B, N, Hq, Hkv, G, rows, rt_rows, n_rt, groups;
+  int page_size, max_pages, num_pages, box;
+  float c;  // scale * log2(e)
+};
+
+// Length of sequence b as the tree takes it: 0 for padding (fewer than N
+// tokens) and for a length past the page table.
+__device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
+  const int L = p.seqlens[b];
+  return (L < p.N || (long long)L > (long long)p.max_pages * p.page_size) ? 0 : L;
+}
+__device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
+  return (tree_len(p, b) + tr::BN - 1) / tr::BN;
+}
+
+// A CTA's place in the tile list.
+struct TreeWalk {
+  long long x, hi;  // next and last tile of the range
+  long long first;  // first tile of sequence b
+  int b, T;         // sequence and its tiles per kv head
+};
+struct TreeSeg {
+  int b, hkv, t0, n, T, L;
+};
+
+// Whole warp: the range of group g and the sequence it starts in.
+__device__ TreeWalk tree_plan(const TreeParams& p, int g) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+#pragma unroll 4
+  for (int b = lane; b < p.B; b += 32) sum += tree_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const long long total = sum * p.Hkv;
+  TreeWalk w;
+  w.x = total * g / p.groups;
+  w.hi = total * (g + 1) / p.groups;
+  w.first = 0;
+  w.b = 0;
+  w.T = 0;
+  if (w.x >= w.hi) return w;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const long long T = b < p.B ? tree_tiles(p, b) : 0;
+    long long inc = T;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, w.x < (before + inc) * p.Hkv);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      w.b = b0 + l;
+      w.T = (int)__shfl_sync(0xffffffffu, T, l);
+      w.first = (before + __shfl_sync(0xffffffffu, inc, l) - w.T) * p.Hkv;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return w;
+}
+
+// The next stretch of one unit's tiles in the range.
+__device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, TreeSeg* s) {
+  if (w.x >= w.hi) return false;
+  while (w.x >= w.first + (long long)w.T * p.Hkv) {
+    w.first += (long long)w.T * p.Hkv;
+    if (++w.b >= p.B) return false;  // (the range ends at the list's end)
+    w.T = tree_tiles(p, w.b);
+  }
+  const long long off = w.x - w.first;
+  s->b = w.b;
+  s->hkv = (int)(off / w.T);
+  s->t0 = (int)(off - (long long)s->hkv * w.T);
+  s->T = w.T;
+  s->L = tree_len(p, w.b);
+  const long long left = w.hi - w.x;
+  s->n = w.T - s->t0 < left ? w.T - s->t0 : (int)left;
+  w.x += s->n;
+  return true;
+}
+
+// Bits [0, n) of a 128-bit mask held as two words (n may lie outside).
+struct Mask128 {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
+}
+// The keys [0, at) and the tree's nodes `bits` from key `at` on, both relative
+// to a tile.
+__device__ __forceinline__ Mask128 tile_mask(int at, uint64_t bits) {
+  Mask128 m{low_bits(at), low_bits(at - 64)};
+  if (at <= -64 || at >= 128) return m;
+  if (at < 0) {
+    m.lo |= bits >> -at;
+  } else if (at < 64) {
+    m.lo |= bits << at;
+    if (at > 0) m.hi |= bits >> (64 - at);
+  } else {
+    m.hi |= bits << (at - 64);
+  }
+  return m;
+}
+// Keys of a tile whose pages are sound (bad: one bit per box of `box` keys).
+__device__ __forceinline__ Mask128 sound_keys(uint32_t bad, int box) {
+  Mask128 m{~0ull, ~0ull};
+  if (bad == 0) return m;
+  for (int i = 0; i < 128 / box; ++i)
+    if (bad >> i & 1) {
+      const int a = i * box, e = a + box;
+      m.lo &= ~(low_bits(e) & ~low_bits(a));
+      m.hi &= ~(low_bits(e - 64) & ~low_bits(a - 64));
+    }
+  return m;
+}
+
+// Whole warp: ancestor masks of sequence b's nodes, lane l holding nodes l and
+// l + 32, by pointer doubling (six rounds reach depth 64).  A node is unused
+// when its parent entry is -2, is not a lower node (which also sets the bounds
+// bit), or when its way up meets an unused node.  *used: the usable nodes.
+__device__ __forceinline__ void tree_masks(const TreeParams& p, int b, uint64_t (&anc)[2],
+                                           uint64_t* used) {
+  const int lane = threadIdx.x & 31;
+  int up[2];
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int s = lane + 32 * e;
+    up[e] = -2;
+    if (s < p.N) {
+      const int v = p.parents[(size_t)b * p.N + s];
+      up[e] = v >= -1 && v < s ? v : -2;
+      odd |= v < -2 || v >= s;
+    }
+    anc[e] = 1ull << s;
+  }
+  if (odd) atomicOr(&g_tree_err, kErrBounds);
+#pragma unroll
+  for (int r = 0; r < 6; ++r) {
+    uint64_t na[2];
+    int nu[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = up[e] < 0 ? 0 : up[e];
+      const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], t & 31);
+      const uint64_t a1 = __shfl_sync(0xffffffffu, anc[1], t & 31);
+      const int u0 = __shfl_sync(0xffffffffu, up[0], t & 31);
+      const int u1 = __shfl_sync(0xffffffffu, up[1], t & 31);
+      na[e] = up[e] < 0 ? anc[e] : anc[e] | (t < 32 ? a0 : a1);
+      nu[e] = up[e] < 0 ? up[e] : (t < 32 ? u0 : u1);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      anc[e] = na[e];
+      up[e] = nu[e];
+    }
+  }
+  const uint64_t w0 = __ballot_sync(0xffffffffu, up[0] == -1);
+  const uint64_t w1 = __ballot_sync(0xffffffffu, up[1] == -1);
+  *used = w0 | w1 << 32;
+}
+
+template <typename T>
+struct TreeType {
+  static constexpr bool kBF16 = true;
+  // Largest row sum of unnormalised P that a tile may leave before the row's
+  // maximum is renewed: P fits the type and the sums fit fp32.
+  static constexpr float kBig = 1.152921504606846976e18f;  // 2^60
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+template <>
+struct TreeType<__half> {
+  static constexpr bool kBF16 = false;
+  static constexpr float kBig = 32768.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+
+template <int D, typename T, int MT>
+__global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
+    tree_split_kernel(const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ TreeParams p) {
+  using C = tr::Cfg<D, MT>;
+  constexpr int NSTAGE = C::NSTAGE;
+  constexpr int W_PROD = MT * 4, W_MMA = MT * 4 + 1;
+  constexpr bool kBF16 = TreeType<T>::kBF16;
+  constexpr float NEG_INF = -INFINITY;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + C::SMEM_Q;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sKV + C::SMEM_KV);
+  uint64_t* empty = full + NSTAGE;
+  uint64_t* q_full = empty + NSTAGE;
+  uint64_t* s_full = q_full + 1;  // [2] MT = 1: of alternate tiles; MT = 2: of the row tiles
+  uint64_t* p_full = s_full + 2;  // [MT]
+  uint64_t* pv_done = p_full + 2; // [MT] P V of each tile has completed
+  uint64_t* drain = pv_done + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);
+  volatile uint32_t* tile_bad = issued + 1;  // [BAD_RING]
+  static_assert(2 * C::NSTAGE * 8 + 8 * 8 + 12 + 4 * tr::BAD_RING <= C::SMEM_BAR, "barrier block");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x / p.n_rt, rt = blockIdx.x - group * p.n_rt;
+  // Row tiles of this CTA that hold rows (the last CTA of a unit may have one).
+  const int n_act = MT == 2 && p.rows - rt * C::RT > tr::BM ? 2 : 1;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == W_PROD * 32) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NSTAGE; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(q_full, tr::BM * n_act);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], tr::BM);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(tmem_holder, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait_primary();  // everything below reads or writes the caller's memory
+
+  TreeWalk w = tree_plan(p, group);
+  TreeSeg sg;
+  if (warp >= W_PROD) {
+   if constexpr (MT == 2) regs_decrease<88>();
+   if (warp == W_PROD) {
+    // ============================ TMA producer ============================
+    // Lane l < boxes * halves loads box l % boxes, half l / boxes of each tile.
+    const int boxes = tr::BN / p.box;
+    const int sub = lane % boxes, half = lane / boxes;
+    const bool loads = half < C::HALVES;
+    const uint64_t pol = p.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+    uint32_t tc = 0;  // tiles so far: K at ring position 2 tc, V at 2 tc + 1
+    bool ok = true;
+    while (ok && tree_next(p, w, &sg)) {
+      const int32_t* table = p.page_table + (size_t)sg.b * p.max_pages;
+      // Page of this lane's box in tile t (-1: past the sequence's end), one
+      // tile ahead of its use.
+      auto page_of = [&](int t, int* pos) {
+        const int row = t * tr::BN + sub * p.box;
+        if (!loads || row >= sg.L) return -1;
+        const int pg = row / p.page_size;
+        *pos = row - pg * p.page_size;
+        const int id = table[pg];
+        return id < 0 || id >= p.num_pages ? -2 : id;
+      };
+      int pos = 0, pos_n = 0;
+      int id_n = page_of(sg.t0, &pos_n);
+      for (int j = 0; j < sg.n && ok; ++j, ++tc) {
+        const int id = id_n;
+        pos = pos_n;
+        if (j + 1 < sg.n) id_n = page_of(sg.t0 + j + 1, &pos_n);
+        const uint32_t bad = __ballot_sync(0xffffffffu, id == -2 && half == 0);
+        const uint32_t bytes =
+            __popc(__ballot_sync(0xffffffffu, id >= 0)) * (uint32_t)p.box * 128u;
+        if (bad && lane == 0) atomicOr(&g_tree_err, kErrBounds);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t cnt = 2 * tc + v;
+          const int s = cnt % NSTAGE;
+          if (!(ok = mbar_wait<true>(&empty[s], ((cnt / NSTAGE) & 1) ^ 1, abort_flag,
+                                     &g_tree_err, 1)))
+            break;
+          if (lane == 0) {
+            if (v == 0) tile_bad[tc % tr::BAD_RING] = bad;
+            mbar_arrive_expect_tx(&full[s], bytes);
+          }
+          __syncwarp();
+          if (id >= 0)
+            tma_load_4d_hint(sKV + s * C::TILE_BYTES + half * tr::HALF_BYTES + sub * p.box * 128,
+                             v ? &tmV : &tmK, &full[s], half * 64, sg.hkv, pos, id, pol);
+          __syncwarp();
+          if (lane == 0) *issued = cnt + 1;
+        }
+      }
+    }
+    __syncwarp();
+   } else if (warp == W_MMA) {
+    // ============================ MMA issuer (lane 0) ============================
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = idesc_f16(tr::BM, tr::BN, kBF16, false);
+      constexpr uint32_t IDESC_O = idesc_f16(tr::BM, D, kBF16, true);
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sKV), tr::HALF_BYTES, 1024);
+      const uint32_t sd_hi = (uint32_t)(dq >> 32);
+      const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+      // S[buf] = Q[tile] K^T, over D / 16 steps.
+      auto issue_s = [&](int tile, int buf, uint32_t stage) {
+        const uint32_t a0 = q_lo + tile * (C::TILE_BYTES >> 4);
+        const uint32_t b0 = k_lo + stage * (C::TILE_BYTES >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * tr::HALF_BYTES + (k & 3) * 32) >> 4;
+          mma_ss_lh(tmem + C::COL_S + buf * 128, a0 + off, sd_hi, b0 + off, sd_hi, IDESC_S,
+                    k > 0 ? 1u : 0u);
+        }
+      };
+      // O[tile] (+)= P[buf] V, over 128 / 16 steps.
+      auto issue_pv = [&](int tile, int buf, uint32_t stage, bool add) {
+        const uint32_t b0 = v_lo + stage * (C::TILE_BYTES >> 4);
+#pragma unroll
+        for (int k = 0; k < tr::BN / 16; ++k)
+          mma_ts_lh(tmem + C::COL_O + tile * D, tmem + C::COL_S + buf * 128 + k * 8,
+                    b0 + (uint32_t)((k * 16 * 128) >> 4), sd_hi, IDESC_O, add || k > 0 ? 1u : 0u);
+      };
+      uint32_t tc = 0, sc = 0;
+      bool ok = true;
+      auto landed = [&](uint32_t cnt, unsigned site) {
+        const bool r = mbar_wait<true>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag,
+                                       &g_tree_err, site);
+        tc_fence_after();
+        return r;
+      };
+      while (ok && tree_next(p, w, &sg)) {
+        if (!(ok = mbar_wait<true>(q_full, sc & 1, abort_flag, &g_tree_err, 2))) break;
+        ++sc;
+        tc_fence_after();
+        if (!(ok = landed(2 * tc, 3))) break;
+        for (int i = 0; i < n_act; ++i) {
+          issue_s(i, MT == 1 ? tc & 1 : i, (2 * tc) % NSTAGE);
+          mma_commit(&s_full[MT == 1 ? tc & 1 : i]);
+        }
+        mma_commit(&empty[(2 * tc) % NSTAGE]);
+        for (int j = 0; j < sg.n; ++j, ++tc) {
+          const uint32_t ck = 2 * tc + 2, cv = 2 * tc + 1;
+          const bool more = j + 1 < sg.n;
+          if (MT == 1 && more) {
+            // S of the next tile goes ahead of this tile's P V, so that it is
+            // ready when the softmax warps get to it.  (Its buffer held P of
+            // the tile before this one, whose P V was issued earlier.)
+            if (!(ok = landed(ck, 4))) break;
+            issue_s(0, (tc + 1) & 1, ck % NSTAGE);
+            mma_commit(&s_full[(tc + 1) & 1]);
+            mma_commit(&empty[ck % NSTAGE]);
+          }
+          if (!(ok = landed(cv, 5))) break;
+          if (MT == 2 && more && !(ok = landed(ck, 4))) break;
+          for (int i = 0; i < n_act; ++i) {
+            if (!(ok = mbar_wait<true>(&p_full[i], tc & 1, abort_flag, &g_tree_err, 6 + i))) break;
+            tc_fence_after();
+            issue_pv(i, MT == 1 ? tc & 1 : i, cv % NSTAGE, j > 0);
+            mma_commit(&pv_done[i]);
+            if (i == n_act - 1) mma_commit(&empty[cv % NSTAGE]);
+            if (MT == 2 && more) {
+              issue_s(i, i, ck % NSTAGE);
+              mma_commit(&s_full[i]);
+              if (i == n_act - 1) mma_commit(&empty[ck % NSTAGE]);
+            }
+          }
+          if (!ok) break;
+        }
+      }
+      // Every MMA issued here has completed before tensor memory is freed.
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+    __syncwarp();
+   }
+  } else if ((warp >> 2) < n_act) {
+    if constexpr (MT == 2) regs_increase<208>();
+    // ======================= softmax and epilogue =======================
+    const int i = warp >> 2, wq = warp & 3;
+    const int tid = wq * 32 + lane;             // row within the tile, and V row it clears
+    const int rr = i * tr::BM + tid;            // row within the CTA
+    const int r = rt * C::RT + rr;              // row (s, g) of the kv head
+    const bool row_ok = r < p.rows;
+    const bool warp_ok = rt * C::RT + i * tr::BM + wq * 32 < p.rows;
+    const int s = row_ok ? r / p.G : 0, g = row_ok ? r - s * p.G : 0;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tO = t_lane + C::COL_O + i * D;
+    const float c = p.c;
+    const bool neg = c < 0.f;
+    const float hide = neg ? -NEG_INF : NEG_INF;
+    // The first CTA also lists where each sequence starts, for the merge.
+    if (blockIdx.x == 0 && warp == 0) {
+      long long before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const long long Tb = b0 + lane < p.B ? (long long)tree_tiles(p, b0 + lane) * p.Hkv : 0;
+        long long inc = Tb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (b0 + lane < p.B) {
+          p.start[b0 + lane + 1] = before + inc;
+          if ((long long)p.seqlens[b0 + lane] > (long long)p.max_pages * p.page_size)
+            atomicOr(&g_tree_err, kErrBounds);
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) p.start[0] = 0;
+    }
+    uint32_t tc = 0;
+    int cur_b = -1;
+    uint64_t anc = 0, used = 0;
+    bool ok = true;
+    while (ok && tree_next(p, w, &sg)) {
+      if (sg.b != cur_b) {
+        cur_b = sg.b;
+        uint64_t a[2];
+        tree_masks(p, cur_b, a, &used);
+        const uint64_t a0 = __shfl_sync(0xffffffffu, a[0], s & 31);
+        const uint64_t a1 = __shfl_sync(0xffffffffu, a[1], s & 31);
+        anc = s < 32 ? a0 : a1;
+      }
+      const size_t qrow = ((size_t)sg.b * p.N + s) * p.Hq + (size_t)sg.hkv * p.G + g;
+      {
+        // This row of Q, in the swizzled layout of a TMA load.  (Every MMA of
+        // the stretch before has completed: its last P V was waited for.)
+        uint4 v[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + qrow * D);
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) v[x] = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* dst = sQ + i * C::TILE_BYTES + tid * 128;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+          *reinterpret_cast<uint4*>(dst + (x >> 3) * tr::HALF_BYTES + (((x & 7) ^ (tid & 7)) << 4)) =
+              v[x];
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(q_full);
+      }
+      const int base = sg.L - p.N;  // keys before the tree
+      float m_used = NEG_INF, l = 0.f;
+      for (int j = 0; j < sg.n; ++j, ++tc) {
+        const int buf = MT == 1 ? tc & 1 : i;
+        const uint32_t tS = t_lane + C::COL_S + buf * 128;
+        const uint32_t par = MT == 1 ? (tc >> 1) & 1 : tc & 1;
+        if (!(ok = mbar_wait<true>(&s_full[buf], par, abort_flag, &g_tree_err, 8 + i))) break;
+        __syncwarp();
+        tc_fence_after();
+        const int kv0 = (sg.t0 + j) * tr::BN;
+        const uint32_t bad = tile_bad[tc % tr::BAD_RING];
+        const bool masked = kv0 + tr::BN > base || bad;
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {
+          const Mask128 fine = sound_keys(bad, p.box);
+          const Mask128 mine = tile_mask(base - kv0, anc);
+          see[0] = (uint32_t)(mine.lo & fine.lo);
+          see[1] = (uint32_t)((mine.lo & fine.lo) >> 32);
+          see[2] = (uint32_t)(mine.hi & fine.hi);
+          see[3] = (uint32_t)((mine.hi & fine.hi) >> 32);
+          // V rows that no query may see (unused nodes, slots past the end,
+          // bad pages) can hold anything: they are cleared, since 0 * NaN in
+          // P V would reach every row.
+          const Mask128 any = tile_mask(base - kv0, used);
+          const uint64_t keep = tid < 64 ? any.lo & fine.lo : any.hi & fine.hi;
+          const uint32_t cv = 2 * tc + 1;
+          if (!(ok = mbar_wait<true>(&full[cv % NSTAGE], (cv / NSTAGE) & 1, abort_flag,
+                                     &g_tree_err, 10)))
+            break;
+          if (!(keep >> (tid & 63) & 1)) {
+            uint8_t* vr = sKV + (cv % NSTAGE) * C::TILE_BYTES + tid * 128;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+              *reinterpret_cast<uint4*>(vr + (x >> 3) * tr::HALF_BYTES + (x & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        bool pv_waited = j == 0;  // (the stretch before waited for its last P V)
+        if (warp_ok) {
+          uint32_t sr[4][32];
+          float mx = hide;
+          float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+          auto find_max = [&](uint32_t (&reg)[32]) {
+            const float* v = reinterpret_cast<const float*>(reg);
+            if (!neg) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) mx = max3f(mx, v[x], v[x + 1]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) mx = min3f(mx, v[x], v[x + 1]);
+            }
+          };
+          auto exp_store = [&](uint32_t (&reg)[32], int q, float top) {
+            const float* v = reinterpret_cast<const float*>(reg);
+            const float2 c2 = make_float2(c, c), nb = make_float2(-top, -top);
+            uint32_t pk[16];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+              const float2 a = __ffma2_rn(make_float2(v[2 * t], v[2 * t + 1]), c2, nb);
+              const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+              if (t & 1)
+                lb = __fadd2_rn(lb, e);
+              else
+                la = __fadd2_rn(la, e);
+              pk[t] = TreeType<T>::pack(e.x, e.y);
+            }
+            tmem_st16(tS + q * 16, pk);
+          };
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_fence32(sr[q]);
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!(see[q] >> x & 1)) sr[q][x] = __float_as_uint(hide);
+          }
+          // The stretch's first tile takes its own maximum; later tiles are
+          // exponentiated against the running one, and a row takes the slow
+          // path only when its sum outgrows kBig or it had seen no key yet.
+          bool renew = j == 0;
+          if (!renew) {
+            const float top = m_used == NEG_INF ? 0.f : m_used;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) exp_store(sr[q], q, top);
+            const float lt = (la.x + la.y) + (lb.x + lb.y);
+            const bool mine = !(lt <= TreeType<T>::kBig) || m_used == NEG_INF;
+            renew = __any_sync(0xffffffffu, mine);
+          }
+          if (renew) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) find_max(sr[q]);
+            const float m_new = fmaxf(m_used, mx * c);
+            const float f = m_used == NEG_INF ? 0.f : fast_exp2(m_used - m_new);
+            const float top = m_new == NEG_INF ? 0.f : m_new;
+            if (j > 0) {
+              tmem_wait_st();
+              la = lb = make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) exp_store(sr[q], q, top);
+            l *= f;
+            m_used = m_new;
+            if (j > 0) {
+              // O of the tiles so far, once the last of their P V is done.
+              if (!(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag, &g_tree_err,
+                                         11 + i)))
+                break;
+              __syncwarp();
+              pv_waited = true;
+              tc_fence_after();
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tO + q * 32, o);
+                tmem_wait_ld();
+                reg_fence32(o);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st32(tO + q * 32, o);
+              }
+            }
+          }
+          l += (la.x + la.y) + (lb.x + lb.y);
+          tmem_wait_st();
+        }
+        // One phase of pv_done per tile, each waited for before the next P is
+        // handed over: the parity waits never fall two phases behind.
+        if (!pv_waited && !(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag,
+                                                 &g_tree_err, 13 + i)))
+          break;
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+      if (!(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag, &g_tree_err, 15))) break;
+      __syncwarp();
+      tc_fence_after();
+      if (warp_ok) {
+        // A row of an unused node gives O = 0 and log-sum-exp -inf.
+        const bool live = used >> s & 1;
+        if (!live) {
+          l = 0.f;
+          m_used = NEG_INF;
+        }
+        const bool whole = sg.t0 == 0 && sg.n == sg.T;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1)) * p.rt_rows + rr;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (row_ok) {
+          if (whole) {
+            if (p.lse) p.lse[qrow] = l > 0.f ? 0.6931471805599453f * (m_used + log2f(l)) : NEG_INF;
+          } else {
+            reinterpret_cast<float2*>(p.part_ml)[slot] = make_float2(m_used, l);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tO + q * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+          if (!row_ok) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + qrow * D + q * 32);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t k[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float e0 = __uint_as_float(o[8 * x + 2 * y]) * inv;
+                const float e1 = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
+                k[y] = live ? TreeType<T>::pack(e0, e1) : 0u;
+              }
+              dst[x] = make_uint4(k[0], k[1], k[2], k[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D + q * 32);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              dst[x] = live ? make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3])
+                            : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  // After an abort: every load that may still be in flight, before the CTA
+  // and its shared memory go.
+  if (warp == W_PROD && *abort_flag) {
+    const uint32_t n = *issued;
+    for (uint32_t u = n > (uint32_t)NSTAGE ? n - NSTAGE : 0u; u < n; ++u)
+      mbar_wait_drain(&full[u % NSTAGE], (u / NSTAGE) & 1);
+    __syncwarp();
+  }
+}
+
+// Merge of the units that several groups share, and zeros for padding
+// sequences: one warp per output row, lane l holding columns [l D/32, ...).
+// The partials are loaded four at a time and merged online.
+constexpr int kTreeRowWarps = 8;
+template <int D, typename T>
+__global__ void __launch_bounds__(kTreeRowWarps * 32)
+    tree_merge_kernel(const __grid_constant__ TreeParams p, int rt_size) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const size_t row = (size_t)blockIdx.x * kTreeRowWarps + (threadIdx.x >> 5);  // (b, s, hq)
+  const size_t per_b = (size_t)p.N * p.Hq;
+  if (row >= (size_t)p.B * per_b) return;
+  const int b = (int)(row / per_b), x = (int)(row - (size_t)b * per_b);
+  const int s = x / p.Hq, hq = x - s * p.Hq, hkv = hq / p.G;
+  const int r = s * p.G + (hq - hkv * p.G), rt = r / rt_size;
+  const long long first = p.start[b], total = p.start[p.B];
+  const long long T_b = (p.start[b + 1] - first) / p.Hkv;
+  float M = -INFINITY, den = 0.f, acc[CPL];
+#pragma unroll
+  for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+  if (T_b > 0) {
+    const long long u0 = first + hkv * T_b, u1 = u0 + T_b - 1;
+    // Group of tile t: the largest g with total * g / groups <= t.
+    const int g0 = (int)(((u0 + 1) * p.groups - 1) / total);
+    const int g1 = (int)(((u1 + 1) * p.groups - 1) / total);
+    if (g0 == g1) return;  // finished in place
+    for (int k0 = g0; k0 <= g1; k0 += 4) {
+      float2 ml[4];
+      float ov[4][CPL];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u;
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) ov[u][e] = 0.f;
+        if (k <= g1) {
+          const size_t slot = (((size_t)k * p.n_rt + rt) * 2 + (k == g0 ? 1 : 0)) * p.rt_rows +
+                              (r - rt * rt_size);
+          ml[u] = reinterpret_cast<const float2*>(p.part_ml)[slot];
+          const float* src = p.part_o + slot * D + lane * CPL;
+          if constexpr (CPL == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            ov[u][0] = v.x; ov[u][1] = v.y; ov[u][2] = v.z; ov[u][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            ov[u][0] = v.x; ov[u][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float m_u = ml[u].y > 0.f ? ml[u].x : -INFINITY;
+        if (m_u > M) {
+          const float f = M == -INFINITY ? 0.f : fast_exp2(M - m_u);
+          den *= f;
+#pragma unroll
+          for (int e = 0; e < CPL; ++e) acc[e] *= f;
+          M = m_u;
+        }
+        const float wt = m_u == -INFINITY ? 0.f : fast_exp2(m_u - M);
+        den += wt * ml[u].y;
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) acc[e] += wt * ov[u][e];
+      }
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  T* dst = static_cast<T*>(p.o) + row * D + lane * CPL;
+#pragma unroll
+  for (int e = 0; e < CPL; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = TreeType<T>::pack(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[row] = den > 0.f ? 0.6931471805599453f * (M + log2f(den)) : -INFINITY;
+}
+
+// Row tiles per CTA, row-tile CTAs per unit, tile groups.
+struct TreePlan {
+  int mt, n_rt, groups, rt_rows;
+  size_t o_floats, ml_floats, bytes;
+};
+static TreePlan tree_host_plan(int B, int N, int Hq, int Hkv, long long cap, int D) {
+  TreePlan t;
+  const int rows = N * (Hq / Hkv);
+  t.mt = rows <= tr::BM ? 1 : 2;
+  const int rt = t.mt * tr::BM;
+  t.n_rt = (rows + rt - 1) / rt;
+  t.rt_rows = rows < rt ? rows : rt;
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  long long g = sms / t.n_rt;
+  const long long most = (long long)B * Hkv * ((cap + tr::BN - 1) / tr::BN);
+  if (g > most) g = most;
+  if (g < 1) g = 1;
+  t.groups = (int)g;
+  const size_t slots = (size_t)t.groups * t.n_rt * 2 * t.rt_rows;
+  t.o_floats = slots * D;
+  t.ml_floats = slots * 2;
+  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 1) * sizeof(long long);
+  return t;
+}
+
+template <int D, typename T, int MT>
+static int launch_tree_t(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream) {
+  using C = tr::Cfg<D, MT>;
+  static int attr_set[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE)) {
+    e = cudaFuncSetAttribute(tree_split_kernel<D, T, MT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    // The split kernel's carveout, so that merge blocks become resident beside it.
+    e = cudaFuncSetAttribute(tree_merge_kernel<D, T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.groups * p.n_rt), 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_TOTAL;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, T, MT>, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  const size_t rows = (size_t)p.B * p.N * p.Hq;
+  cfg.gridDim = dim3((unsigned)((rows + kTreeRowWarps - 1) / kTreeRowWarps), 1, 1);
+  cfg.blockDim = dim3(kTreeRowWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T>, p, (int)C::RT);
+}
+
+template <int D, typename T>
+static int launch_tree_d(const TreeParams& p, int mt, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream) {
+  return mt == 1 ? launch_tree_t<D, T, 1>(p, tk, tv, stream)
+                 : launch_tree_t<D, T, 2>(p, tk, tv, stream);
+}
+
+// A cache without capacity: every row is a padding sequence's.
+__global__ void tree_zero_kernel(uint16_t* o, size_t n, float* lse, size_t nl) {
+  const size_t at = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+  const size_t step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = at; i < n; i += step) o[i] = 0;
+  if (lse)
+    for (size_t i = at; i < nl; i += step) lse[i] = -INFINITY;
+}
+
+int set_tree_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
+
+int read_tree_error(unsigned int* out, int reset) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_tree_err, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (reset && v) {
+    const unsigned int z = 0;
+    e = cudaMemcpyToSymbol(g_tree_err, &z, sizeof(z));
+    if (e != cudaSuccess) return e;
+  }
+  *out = v;
+  return cudaSuccess;
+}
+
+}  // namespace fa
+
+static bool al(const void* p, unsigned n) {
+  return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void* vpages,
+                                  const int32_t* page_table, const int32_t* seqlens,
+                                  const int32_t* parents, void* o, float* lse, int B, int N,
+                                  int Hq, int Hkv, int num_pages, int page_size, int max_pages,
+                                  int D, float scale, int dtype, cudaStream_t stream) {
+  if (B < 0 || N < 0 || Hq < 0 || Hkv < 0 || num_pages < 0 || max_pages < 0)
+    return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (page_size < 32 || page_size % 32 != 0) return FA_ERR_INVALID_ARG;
+  if (N > fa::tr::MAX_N) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0 || Hq == 0) return FA_OK;
+  if (Hkv == 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  // Row indexes and the merge's grid fit 31 bits with 8 rows per block.
+  if ((int64_t)B * N * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
+  if ((int64_t)max_pages * page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
+  if (!al(q, 16) || !al(o, 16)) return FA_ERR_INVALID_ARG;
+  if (lse && !al(lse, 4)) return FA_ERR_INVALID_ARG;
+  if (max_pages > 0 && (num_pages < 1 || !al(kpages, 16) || !al(vpages, 16) ||
+                        !al(page_table, 4) || !al(seqlens, 4) || !al(parents, 4)))
+    return FA_ERR_INVALID_ARG;
+  if ((int64_t)num_pages * page_size * Hkv * D * 2 >= (1ll << 40)) return FA_ERR_INVALID_ARG;
+  if (max_pages == 0) {
+    const size_t rows = (size_t)B * N * Hq, n = rows * D;
+    fa::tree_zero_kernel<<<(unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096), 256, 0,
+                           stream>>>(static_cast<uint16_t*>(o), n, lse, rows);
+    return fa::record_cuda_status(cudaGetLastError(), "tree decode zero-fill launch");
+  }
+  const fa::TreePlan t =
+      fa::tree_host_plan(B, N, Hq, Hkv, (long long)max_pages * page_size, D);
+  fa::TreeParams p = {};
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.page_table = page_table;
+  p.seqlens = seqlens;
+  p.parents = parents;
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.rows = N * p.G;
+  p.rt_rows = t.rt_rows;
+  p.n_rt = t.n_rt;
+  p.groups = t.groups;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  // Keys per TMA box: a tile's boxes must not straddle pages.
+  p.box = page_size % 128 == 0 ? 128 : (page_size % 64 == 0 ? 64 : 32);
+  p.c = scale * 1.4426950408889634f;
+  // scale == 0: every visible score is 0; a tiny c keeps hidden keys at -inf.
+  if (p.c == 0.f) p.c = 1e-30f;
+  CUtensorMap tk, tv;
+  if (fa::encode_tmap_rows(&tk, kpages, D, Hkv, page_size, num_pages, p.box) ||
+      fa::encode_tmap_rows(&tv, vpages, D, Hkv, page_size, num_pages, p.box))
+    return fa::record_cuda_status(cudaErrorInvalidValue, "tree decode tensor maps");
+  void* scratch = nullptr;
+  cudaError_t e = cudaMallocAsync(&scratch, t.bytes, stream);
+  if (e != cudaSuccess) return fa::record_cuda_status(e, "tree decode cudaMallocAsync");
+  p.start = static_cast<long long*>(scratch);
+  // (B + 1) 8-byte entries, then the partials 16-byte aligned.
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
+                                      (((size_t)B + 1) * 8 + 15) / 16 * 16);
+  p.part_ml = p.part_o + t.o_floats;
+  int r;
+  const bool bf16 = dtype == FA_BF16;
+  if (D == 64)
+    r = bf16 ? fa::launch_tree_d<64, __nv_bfloat16>(p, t.mt, tk, tv, stream)
+             : fa::launch_tree_d<64, __half>(p, t.mt, tk, tv, stream);
+  else
+    r = bf16 ? fa::launch_tree_d<128, __nv_bfloat16>(p, t.mt, tk, tv, stream)
+             : fa::launch_tree_d<128, __half>(p, t.mt, tk, tv, stream);
+  const cudaError_t ef = cudaFreeAsync(scratch, stream);
+  if (r != 0) return fa::record_cuda_status(r, "tree decode launch");
+  return fa::record_cuda_status(ef, "tree decode cudaFreeAsync");
+}

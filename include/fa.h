@@ -336,6 +336,189 @@ int fa_prefill_fwd_host(const void* q_host, const void* k_host, const void* v_ho
 int fa_prefill_host_pieces(int B, int Sq, int Sk, int causal, int n_pieces,
                            int* b, int* s0, int* s1, int* sk, int max_pieces);
 
+/*
+ * fa_qk_norm_rope -- RMS norm of every query and key head, then the rotation
+ * by position, in one pass: what prepares q and k for fa_prefill_fwd.
+ * (No counterpart in the source material: an operator next to attention that
+ * models with normed heads need.)
+ *
+ *   q      [T, Hq, D]    bf16 or fp16; token t's heads start at q + t * q_stride
+ *   k      [T, Hkv, D]   elements (so q and k may be views of one projection's
+ *                        output); strides are multiples of 8, at least H * D
+ *   q_out  [T, Hq, D], k_out [T, Hkv, D]   contiguous, written; may be q and k
+ *          themselves where those are contiguous
+ *   q_weight, k_weight   [D], the heads' dtype
+ *   inv_freq   [rot_dim / 2] fp32, device: radians per position of each pair
+ *   positions  [T] int32, device: any value
+ *   rot_dim    a multiple of 16, at most D: the rotated elements of a head
+ *   eps        > 0
+ *   interleaved  nonzero: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2)
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight; a pair (a, b) at position p turns by
+ *   p * inv_freq[i]: (a cos - b sin, b cos + a sin); elements at rot_dim and
+ *   past it pass through.
+ *
+ * fp32 arithmetic, one rounding.  Angles keep fp32 accuracy at every position
+ * (phases are 64-bit fixed point).  Hq or Hkv may be 0 (that side's pointers are
+ * then not used).
+ */
+int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                    const void* q_weight, const void* k_weight, const float* inv_freq,
+                    const int32_t* positions, long long T, int Hq, int Hkv, int D, int rot_dim,
+                    long long q_stride, long long k_stride, float eps, int interleaved,
+                    int dtype, cudaStream_t stream);
+
+/*
+ * fa_qk_norm_rope_append -- the serving form: the N new tokens of each of B
+ * sequences are normed and rotated, k and v written straight into the pages
+ * that fa_decode_paged_fwd and fa_decode_tree_fwd read.
+ *
+ *   q [B, N, Hq, D], k, v [B, N, Hkv, D]   token strides in elements as above
+ *   q_out            [B, N, Hq, D]         contiguous; may be q
+ *   kpages, vpages   [num_pages, page_size, Hkv, D]   same dtype
+ *   page_table       [B, max_pages] int32, device
+ *   seqlens          [B] int32, device: valid length L including the N tokens;
+ *                    token s is written to slot L - N + s
+ *   positions        [B, N] int32, device, or NULL: the slot.  (Nodes of a
+ *                    drafted tree sit at L - N + depth.)
+ *   page_size        a positive multiple of 32
+ *
+ * Tokens of a sequence with L < N (padding of the batch) write no cache row;
+ * neither do tokens whose length passes max_pages * page_size or whose page id
+ * lies outside [0, num_pages), which sets the bounds bit of fa_device_error().
+ * q_out is written for every token.  Two tokens must not share a slot.
+ */
+int fa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                           void* kpages, void* vpages, const void* q_weight,
+                           const void* k_weight, const float* inv_freq,
+                           const int32_t* positions, const int32_t* page_table,
+                           const int32_t* seqlens, int B, int N, int Hq, int Hkv, int num_pages,
+                           int page_size, int max_pages, int D, int rot_dim, long long q_stride,
+                           long long k_stride, long long v_stride, float eps, int interleaved,
+                           int dtype, cudaStream_t stream);
+
+/*
+ * fa_qk_norm_rope_backward -- gradient of fa_qk_norm_rope.
+ *
+ *   dq_out [T, Hq, D], dk_out [T, Hkv, D]   gradients of the outputs, contiguous
+ *   q, k, weights, inv_freq, positions ...  the forward's inputs
+ *   dq, dk                 contiguous, written; may be dq_out and dk_out
+ *   dq_weight, dk_weight   [D] fp32, written (summed over tokens and heads in
+ *                          a fixed order, so equal calls give equal bits)
+ *
+ * T == 0 writes zero weight gradients.  Block sums of the weight gradients live
+ * in stream-ordered scratch.
+ */
+int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
+                             const void* k, const void* q_weight, const void* k_weight,
+                             const float* inv_freq, const int32_t* positions, void* dq, void* dk,
+                             float* dq_weight, float* dk_weight, long long T, int Hq, int Hkv,
+                             int D, int rot_dim, long long q_stride, long long k_stride,
+                             float eps, int interleaved, int dtype, cudaStream_t stream);
+
+/*
+ * fa_decode_tree_fwd -- attention of a tree of drafted tokens over a paged
+ * cache: fa_decode_paged_fwd for several continuations at once (speculative
+ * decoding with a tree instead of a chain).
+ *
+ *   q, o             [B, N, Hq, D]   bf16 or fp16; N <= 64 tree nodes
+ *   kpages, vpages   [num_pages, page_size, Hkv, D]
+ *   page_table       [B, max_pages] int32, device
+ *   seqlens          [B] int32, device: valid length L including the N nodes;
+ *                    node s's K/V are in slot L - N + s
+ *   parents          [B, N] int32, device: node s's parent, a lower node, or -1
+ *                    (a root: its context is the cache alone), or -2 (unused)
+ *   lse              NULL, or [B, N, Hq] fp32: each row's log-sum-exp
+ *   page_size        a positive multiple of 32
+ *
+ * Node s attends to the keys [0, L - N), to its ancestors and to itself.  A
+ * chain (parents[s] = s - 1) gives fa_decode_paged_fwd's rows.
+ *
+ * Rows of unused nodes (and of nodes below an unused one) give O = 0 and lse
+ * = -inf; so do all rows of a sequence with L < N (padding of the batch).  A
+ * parent entry that is no lower node makes its node unused, a length past
+ * max_pages * page_size makes its sequence padding, and a page id outside [0,
+ * num_pages) masks that page's keys; each sets the bounds bit of
+ * fa_device_error().  Slots of unused nodes, slots at L and past it, and pages
+ * past a sequence's length may hold anything (NaN included).  The K/V of the
+ * used nodes and of the keys before them must be finite, as a non-finite V
+ * reaches the rows that do not see it too.
+ *
+ * Arithmetic as fa_prefill_fwd.  The K/V tiles of all sequences are cut into
+ * equal shares on the device, so lengths are never read on the host; shares
+ * that end inside a sequence meet in fp32 partials in stream-ordered scratch
+ * and are merged in a fixed order by a second kernel.  Equal calls give equal
+ * bits.  Returns FA_ERR_UNSUPPORTED for N > 64, else as fa_decode_paged_fwd.
+ */
+int fa_decode_tree_fwd(const void* q, const void* kpages, const void* vpages,
+                       const int32_t* page_table, const int32_t* seqlens,
+                       const int32_t* parents, void* o, float* lse, int B, int N, int Hq,
+                       int Hkv, int num_pages, int page_size, int max_pages, int D, float scale,
+                       int dtype, cudaStream_t stream);
+
+/*
+ * fa_verify_tree -- which path of a drafted tree the target accepts, and the
+ * token after it, from given random numbers.
+ *
+ *   target_probs  [B, N, V] fp32: the target's distribution after each node
+ *   draft_probs   [B, N, V] fp32: the distribution from which the children of
+ *                 each node were drawn (independently); or NULL: the drafts
+ *                 were chosen outright (greedily, or by top-k)
+ *   tokens        [B, N] int32: each node's token (node 0's is not looked at)
+ *   parents       [B, N] int32: as in fa_decode_tree_fwd; node 0 is the root
+ *                 (the last decided token) whatever its entry says, further
+ *                 nodes with -1 or -2 are never reached
+ *   uniforms      [B, N] fp32 in [0, 1): entry s >= 1 decides on node s, entry
+ *                 0 draws the next token
+ *   path          [B, N] int32, written: the accepted nodes, root first, then -1
+ *   count         [B] int32, written: how many (at least 1, the root)
+ *   next_token    [B] int32, written: the token drawn after the path's last node
+ *
+ * At a node with residual r = target_probs and mass Z = 1 the children are
+ * tried in index order.  Child c with token x is accepted if u_c q(x) Z < r(x);
+ * the walk goes on from it.  Else r becomes max(r - Z q, 0) and Z its sum; with
+ * draft_probs NULL, q(x) counts as 1, r(x) becomes 0 and Z becomes Z - r(x).
+ * When no child is left, the next token is the lowest whose cumulative r
+ * exceeds u_0 times the sum of r.  A residual without mass falls back to the
+ * node's target row; without mass there, the token is -1.  Probabilities that
+ * are not positive finite numbers count as 0.
+ *
+ * Tests, residuals and sums are carried to at least 46 bits, so that the
+ * answers are those of 64-bit arithmetic except where u lies within about
+ * 1e-13 of a border.  N <= 64 (else FA_ERR_UNSUPPORTED), V >= 1.  A token
+ * outside [0, V) or a parent that is no lower node (nor -1, -2) makes its node
+ * unreachable and sets the bounds bit of fa_device_error().
+ */
+int fa_verify_tree(const float* target_probs, const float* draft_probs, const int32_t* tokens,
+                   const int32_t* parents, const float* uniforms, int32_t* path,
+                   int32_t* count, int32_t* next_token, int B, int N, int V,
+                   cudaStream_t stream);
+
+/*
+ * fa_compact_tree -- keeps the accepted path of a drafted tree in the cache:
+ * node path[b][i] of sequence b (slot L - N + path[b][i]) moves to slot
+ * L - N + i, for i < count[b], in K and V of every layer, in place; the
+ * sequence's length becomes L - N + count[b].
+ *
+ *   kpages, vpages  [layers, num_pages, page_size, Hkv, D], 16-bit elements
+ *   page_table      [B, max_pages] int32, device
+ *   seqlens         [B] int32, device: lengths L including the N nodes
+ *   path            [B, N] int32, device: rising node numbers (fa_verify_tree's)
+ *   count           [B] int32, device: in [0, N]
+ *   seqlens_out     [B] int32, device, written; may be seqlens
+ *   N <= 64 (else FA_ERR_UNSUPPORTED); page_size a positive multiple of 32
+ *
+ * A sequence with L < N (padding) keeps its rows and its length.  So does one
+ * whose length, count, path or page ids are out of range or whose path does
+ * not rise; that sets the bounds bit of fa_device_error().  Slots behind the new
+ * length keep what they held.  The pages under a sequence's tree must not be
+ * shared with another sequence.
+ */
+int fa_compact_tree(void* kpages, void* vpages, const int32_t* page_table,
+                    const int32_t* seqlens, const int32_t* path, const int32_t* count,
+                    int32_t* seqlens_out, int layers, int B, int N, int Hkv, int num_pages,
+                    int page_size, int max_pages, int D, cudaStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* fa_status_string(int status);
 
@@ -347,7 +530,8 @@ const char* fa_status_string(int status);
  * offsets or page ids out of range, or an index self-check), FA_ERR_CUDA if
  * the read itself failed.
  * If detail != NULL it receives the raw bits: the prefill (and backward) word
- * in bits 0-15, the decode word in bits 16-31; in each, bit 0 = a wait timed out (bits 8-15:
+ * in bits 0-15, the decode word (also of the cache append, tree decode,
+ * verification and compaction) in bits 16-31; in each, bit 0 = a wait timed out (bits 8-15:
  * which wait), bit 1 = a bounds check fired.  Bounds bit with site 15: the
  * D = 128 backward dK/dV kernel found its dynamic shared memory too far from
  * a 1 KiB boundary to lay out its rings, and its CTAs left without work.
@@ -389,7 +573,7 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
 
 /*
  * fa_set_wait_limit_ns -- time limit of every device-side pipeline wait
- * (mbarrier waits of the prefill, decode and backward kernels) on the current
+ * (mbarrier waits of the prefill, decode, tree decode and backward kernels) on the current
  * device; ns == 0 restores the default of 2 s.
  *
  * A wait that runs past the limit makes its CTA abort: every warp leaves its
@@ -400,7 +584,7 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
  * default is far above any wait of a healthy call; a short limit serves as a
  * watchdog, or in tests to make the timeout path run.
  *
- * Below 1 ms the limit is a watchdog: the decode kernels, and the dense
+ * Below 1 ms the limit is a watchdog: the decode and tree decode kernels, and the dense
  * prefill (whose launches then use a polling instantiation of the kernel),
  * check it at every probe of every wait.  The packed-sequence prefill and the
  * backward kernels keep suspending probes of about 4 us each, so there a wait
