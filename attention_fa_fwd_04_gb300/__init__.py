@@ -543,92 +543,110 @@ def backward(q, k, v, o, dout, lse, scale, causal, stream=None):
     return dq, dk, dv
 
 
-def _here(*tensors):
-    """The tensors share the current device (kernels launch on it)."""
+# The helpers below run on every call of the small decode-step operators, where
+# the host's time per call is what a caller waits for: one comparison per
+# property, no containers, no generic loops on the usual layouts.
+def _device(*tensors):
+    """The current device's index, which every tensor must be on (kernels
+    launch there)."""
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"tensors must be on the current device (cuda:{dev})")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be CUDA tensors on the current device (cuda:{dev})")
+    return dev
 
 
-def _allocating_on(stream):
-    """Context in which new tensors belong to the call's stream: their memory
-    is then not still in use, nor reused too early, by another stream."""
-    import contextlib
+def _raw_stream(stream, dev):
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor that belongs to the call's stream: its memory is then
+    neither still in use nor reused too early by another stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _contiguous(t, name):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
 def _int32(t, name, shape):
     import torch
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be an int32 CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    _check(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
-def _heads(t, name):
-    """(leading shape, tokens, heads, D, token stride) of [..., H, D]: heads
-    contiguous, tokens at one stride (a slice of a packed projection is fine)."""
-    if t.dim() < 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [..., heads, D]")
-    lead, (H, D) = tuple(t.shape[:-2]), t.shape[-2:]
-    T = 1
-    for n in lead:
-        T *= n
-    want, ts = H * D, None  # stride of the innermost leading axis longer than 1
-    ok = T == 0 or H == 0 or ((D <= 1 or t.stride(-1) == 1) and (H <= 1 or t.stride(-2) == D))
-    if ok and T > 1 and H > 0:
-        step = None
-        for n, st in zip(reversed(lead), reversed(t.stride()[:-2])):
+def _token_stride(t, name):
+    """Stride between the tokens of [..., H, D]: heads contiguous, tokens at one
+    stride (a slice of a packed projection is fine)."""
+    shape, st = t.shape, t.stride()
+    H, D = shape[-2], shape[-1]
+    if t.numel() == 0:
+        return H * D
+    if (st[-1] == 1 or D == 1) and (st[-2] == D or H == 1):
+        if len(shape) == 3 or (len(shape) == 4 and st[0] == st[1] * shape[1]):
+            return st[-3] if shape[-3] > 1 or len(shape) == 4 else H * D
+        step = ts = None  # the stride that the next leading axis must have
+        for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
             if n == 1:
                 continue
             if ts is None:
-                ts = st
-            elif st != step:
-                ok = False
-            step = st * n
-    if not ok:
-        raise ValueError(f"{name}: heads must be contiguous and tokens at one stride")
-    return lead, T, H, D, want if ts is None else ts
+                ts = s
+            elif s != step:
+                break
+            step = s * n
+        else:
+            return H * D if ts is None else ts
+    raise ValueError(f"{name}: heads must be contiguous and tokens at one stride")
+
+
+def _out_like(t, out, name, dev, stream):
+    if out is None:
+        return _empty(t.shape, t.dtype, dev, stream)
+    if out.dtype is not t.dtype or out.shape != t.shape:
+        raise ValueError(f"{name} must have the input's shape and dtype")
+    _contiguous(out, name)
+    return out
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions):
+    """Checks shared by the norm and rotation's forms: (tokens, Hq, Hkv, D,
+    token strides, dtype code)."""
     import torch
-    lead, T, Hq, D, qs = _heads(q, "q")
-    lead_k, _, Hkv, Dk, ks = _heads(k, "k")
-    if lead_k != lead or Dk != D:
+    if q.dim() < 2 or q.dim() != k.dim():
+        raise ValueError("q and k must be [..., heads, D]")
+    lead, Hq, D = q.shape[:-2], q.shape[-2], q.shape[-1]
+    if k.shape[:-2] != lead or k.shape[-1] != D:
         raise ValueError("q and k must share their leading shape and head dimension")
-    _dtype_code(q)
-    for t, n in ((k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t.dtype != q.dtype:
-            raise TypeError(f"{n} must have q's dtype")
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if tuple(t.shape) != (D,):
-            raise ValueError(f"{n} must have shape ({D},)")
-        _check(t, n)
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+    code = _dtype_code(q)
+    dt = q.dtype
+    if k.dtype is not dt or q_weight.dtype is not dt or k_weight.dtype is not dt:
+        raise TypeError("q, k and the weights must share a dtype")
+    if q_weight.shape != (D,) or k_weight.shape != (D,):
+        raise ValueError(f"the weights must have shape ({D},)")
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a float32 CUDA tensor [rot_dim / 2]")
-    _check(inv_freq, "inv_freq")
+    _contiguous(q_weight, "q_weight")
+    _contiguous(k_weight, "k_weight")
+    _contiguous(inv_freq, "inv_freq")
     if positions is not None:
         _int32(positions, "positions", lead)
-    return lead, T, Hq, Hkv, D, qs, ks
-
-
-def _like(t, out, name):
-    import torch
-    if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    if out.dtype != t.dtype or tuple(out.shape) != tuple(t.shape):
-        raise ValueError(f"{name} must have the input's shape and dtype")
-    _check(out, name)
-    return out
+    return (lead.numel(), Hq, k.shape[-2], D, _token_stride(q, "q"), _token_stride(k, "k"), code)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved=False,
@@ -638,15 +656,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved
     position * inv_freq[i].  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
     interleaved, rot = 2 * len(inv_freq); further elements pass through.  q and
     k may be slices of one packed projection.  Returns contiguous (q_out, k_out)."""
-    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
-    _here(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)
-    with _allocating_on(stream):
-        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-    st = fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                         q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
-                         positions.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
-                         float(eps), int(bool(interleaved)), _dtype_code(q),
-                         _stream_handle(stream))
+    T, Hq, Hkv, D, qs, ks, code = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    dev = _device(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)
+    q_out = _out_like(q, q_out, "q_out", dev, stream)
+    k_out = _out_like(k, k_out, "k_out", dev, stream)
+    st = load().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                                q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
+                                positions.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
+                                eps, bool(interleaved), code, _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope")
     return q_out, k_out
@@ -657,22 +674,20 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, po
     """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope from those of
     its outputs (contiguous).  The weights' gradients are float32."""
     import torch
-    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    T, Hq, Hkv, D, qs, ks, code = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    dev = _device(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions)
     for t, like, n in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
+        if t.dtype is not like.dtype or t.shape != like.shape:
             raise ValueError(f"{n} must have the output's shape and dtype")
-        _check(t, n)
-    _here(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions)
-    with _allocating_on(stream):
-        dq, dk = _like(q, None, "dq"), _like(k, None, "dk")
-        dqw, dkw = (torch.empty(D, dtype=torch.float32, device=q.device) if H else
-                    torch.zeros(D, dtype=torch.float32, device=q.device) for H in (Hq, Hkv))
-    st = fa_qk_norm_rope_backward(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
-                                  k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-                                  inv_freq.data_ptr(), positions.data_ptr(), dq.data_ptr(),
-                                  dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), T, Hq, Hkv, D,
-                                  2 * inv_freq.numel(), qs, ks, float(eps),
-                                  int(bool(interleaved)), _dtype_code(q), _stream_handle(stream))
+        _contiguous(t, n)
+    dq, dk = _empty(q.shape, q.dtype, dev, stream), _empty(k.shape, k.dtype, dev, stream)
+    dqw = _empty((D,), torch.float32, dev, stream)
+    dkw = _empty((D,), torch.float32, dev, stream)
+    st = load().fa_qk_norm_rope_backward(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+        k_weight.data_ptr(), inv_freq.data_ptr(), positions.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
+        eps, bool(interleaved), code, _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
@@ -684,36 +699,33 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, p
     [B,N,Hkv,D]), k and v written into the paged cache: token s of sequence b
     goes to slot seqlens[b] - N + s (lengths include the new tokens).
     positions: int32 [B,N], or None for the slot.  Returns q_out."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [B,N,heads,D]")
-    lead, T, Hq, Hkv, D, qs, ks = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
-    B, N = lead
-    if tuple(v.shape) != tuple(k.shape):
-        raise ValueError("k and v shapes differ")
-    vs = _heads(v, "v")[4]
+    if q.dim() != 4:
+        raise ValueError("q must be [B,N,Hq,D]")
+    T, Hq, Hkv, D, qs, ks, code = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    B, N = q.shape[0], q.shape[1]
     num_pages, page_size, Hp, Dp = kpages.shape
-    if (Hp, Dp) != (Hkv, D) or tuple(vpages.shape) != tuple(kpages.shape):
+    if v.shape != k.shape:
+        raise ValueError("k and v shapes differ")
+    if Hp != Hkv or Dp != D or vpages.shape != kpages.shape:
         raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
-    for t, n in ((v, "v"), (kpages, "kpages"), (vpages, "vpages")):
-        if t.dtype != q.dtype:
-            raise TypeError(f"{n} must have q's dtype")
-    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
-        _check(t, n)
+    dt = q.dtype
+    if v.dtype is not dt or kpages.dtype is not dt or vpages.dtype is not dt:
+        raise TypeError("v, kpages and vpages must have q's dtype")
+    vs = _token_stride(v, "v")
+    _contiguous(kpages, "kpages")
+    _contiguous(vpages, "vpages")
     max_pages = page_table.shape[-1]
     _int32(page_table, "page_table", (B, max_pages))
     _int32(seqlens, "seqlens", (B,))
-    _here(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table, seqlens, positions,
-          q_out)
-    with _allocating_on(stream):
-        q_out = _like(q, q_out, "q_out")
-    st = fa_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                                kpages.data_ptr(), vpages.data_ptr(), q_weight.data_ptr(),
-                                k_weight.data_ptr(), inv_freq.data_ptr(),
-                                0 if positions is None else positions.data_ptr(),
-                                page_table.data_ptr(), seqlens.data_ptr(), B, N, Hq, Hkv,
-                                num_pages, page_size, max_pages, D, 2 * inv_freq.numel(), qs, ks,
-                                vs, float(eps), int(bool(interleaved)), _dtype_code(q),
-                                _stream_handle(stream))
+    dev = _device(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table, seqlens,
+                  positions, q_out)
+    q_out = _out_like(q, q_out, "q_out", dev, stream)
+    st = load().fa_qk_norm_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kpages.data_ptr(),
+        vpages.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
+        None if positions is None else positions.data_ptr(), page_table.data_ptr(),
+        seqlens.data_ptr(), B, N, Hq, Hkv, num_pages, page_size, max_pages, D,
+        2 * inv_freq.numel(), qs, ks, vs, eps, bool(interleaved), code, _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope_append")
     return q_out
@@ -729,33 +741,36 @@ def decode_tree(q, kpages, vpages, page_table, seqlens, parents, scale, out=None
     lower node, -1 for a root, -2 for an unused slot).  Node s sees the keys
     before the tree, its ancestors and itself.  Returns ``out`` like q, or (out,
     lse) with lse [B,N,Hq] fp32 when lse is True or a tensor."""
+    import torch
     if q.dim() != 4:
         raise ValueError("q must be [B,N,Hq,D]")
     B, N, Hq, D = q.shape
     num_pages, page_size, Hkv, Dp = kpages.shape
-    if Dp != D or tuple(vpages.shape) != tuple(kpages.shape):
+    if Dp != D or vpages.shape != kpages.shape:
         raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
     code = _dtype_code(q)
-    if kpages.dtype != q.dtype or vpages.dtype != q.dtype:
+    if kpages.dtype is not q.dtype or vpages.dtype is not q.dtype:
         raise TypeError("q, kpages, vpages must share a dtype")
-    for t, n in ((q, "q"), (kpages, "kpages"), (vpages, "vpages")):
-        _check(t, n)
+    _contiguous(q, "q")
+    _contiguous(kpages, "kpages")
+    _contiguous(vpages, "vpages")
     max_pages = page_table.shape[-1]
     _int32(page_table, "page_table", (B, max_pages))
     _int32(seqlens, "seqlens", (B,))
     _int32(parents, "parents", (B, N))
     want_lse = lse is not None and lse is not False
-    _here(q, kpages, vpages, page_table, seqlens, parents, out, lse if lse is not True and want_lse
-          else None)
-    with _allocating_on(stream):
-        out = _like(q, out, "out")
-        if want_lse:
-            lse = _lse_tensor(lse, (B, N, Hq), q)
-    st = fa_decode_tree_fwd(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
-                            page_table.data_ptr(), seqlens.data_ptr(), parents.data_ptr(),
-                            out.data_ptr(), lse.data_ptr() if want_lse else 0, B, N, Hq, Hkv,
-                            num_pages, page_size, max_pages, D, float(scale), code,
-                            _stream_handle(stream))
+    dev = _device(q, kpages, vpages, page_table, seqlens, parents, out,
+                  lse if want_lse and lse is not True else None)
+    out = _out_like(q, out, "out", dev, stream)
+    if lse is True:
+        lse = _empty((B, N, Hq), torch.float32, dev, stream)
+    elif want_lse:
+        lse = _lse_tensor(lse, (B, N, Hq), q)
+    st = load().fa_decode_tree_fwd(
+        q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
+        seqlens.data_ptr(), parents.data_ptr(), out.data_ptr(),
+        lse.data_ptr() if want_lse else None, B, N, Hq, Hkv, num_pages, page_size, max_pages, D,
+        scale, code, _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_decode_tree_fwd")
     return (out, lse) if want_lse else out
@@ -774,27 +789,29 @@ def verify_tree(target_probs, draft_probs, tokens, parents, uniforms, stream=Non
     if target_probs.dim() != 3:
         raise ValueError("target_probs must be [B,N,V]")
     B, N, V = target_probs.shape
-    for t, n, shape in ((target_probs, "target_probs", (B, N, V)),
-                        (draft_probs, "draft_probs", (B, N, V)), (uniforms, "uniforms", (B, N))):
-        if t is None and n == "draft_probs":
-            continue
-        if t.dtype != torch.float32:
-            raise TypeError(f"{n} must be a float32 CUDA tensor")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} must have shape {shape}")
-        _check(t, n)
+    f32 = torch.float32
+    if (target_probs.dtype is not f32 or uniforms.dtype is not f32 or
+            (draft_probs is not None and draft_probs.dtype is not f32)):
+        raise TypeError("target_probs, draft_probs and uniforms must be float32 CUDA tensors")
+    if draft_probs is not None:
+        if draft_probs.shape != target_probs.shape:
+            raise ValueError("draft_probs must have target_probs' shape")
+        _contiguous(draft_probs, "draft_probs")
+    if uniforms.shape != (B, N):
+        raise ValueError(f"uniforms must have shape {(B, N)}")
+    _contiguous(target_probs, "target_probs")
+    _contiguous(uniforms, "uniforms")
     _int32(tokens, "tokens", (B, N))
     _int32(parents, "parents", (B, N))
-    _here(target_probs, draft_probs, tokens, parents, uniforms)
-    dev = target_probs.device
-    with _allocating_on(stream):
-        path = torch.empty((B, N), dtype=torch.int32, device=dev)
-        count = torch.empty(B, dtype=torch.int32, device=dev)
-        nxt = torch.empty(B, dtype=torch.int32, device=dev)
-    st = fa_verify_tree(target_probs.data_ptr(),
-                        0 if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
-                        parents.data_ptr(), uniforms.data_ptr(), path.data_ptr(),
-                        count.data_ptr(), nxt.data_ptr(), B, N, V, _stream_handle(stream))
+    dev = _device(target_probs, draft_probs, tokens, parents, uniforms)
+    path = _empty((B, N), torch.int32, dev, stream)
+    count = _empty((B,), torch.int32, dev, stream)
+    nxt = _empty((B,), torch.int32, dev, stream)
+    st = load().fa_verify_tree(target_probs.data_ptr(),
+                               None if draft_probs is None else draft_probs.data_ptr(),
+                               tokens.data_ptr(), parents.data_ptr(), uniforms.data_ptr(),
+                               path.data_ptr(), count.data_ptr(), nxt.data_ptr(), B, N, V,
+                               _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_verify_tree")
     return path, count, nxt
@@ -808,32 +825,32 @@ def compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=N
     int32 [B] include the N nodes.  Returns the new lengths (seqlens_out, which
     may be seqlens; a new tensor if None)."""
     import torch
-    if kpages.dim() not in (4, 5) or tuple(vpages.shape) != tuple(kpages.shape):
+    shape = kpages.shape
+    if len(shape) not in (4, 5) or vpages.shape != shape:
         raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D] or [layers,...]")
-    if kpages.dtype != vpages.dtype:
+    if kpages.dtype is not vpages.dtype:
         raise TypeError("kpages and vpages must share a dtype")
     _dtype_code(kpages)
-    layers = kpages.shape[0] if kpages.dim() == 5 else 1
-    num_pages, page_size, Hkv, D = kpages.shape[-4:]
     if path.dim() != 2:
         raise ValueError("path must be [B,N]")
     B, N = path.shape
-    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
-        _check(t, n)
+    _contiguous(kpages, "kpages")
+    _contiguous(vpages, "vpages")
     max_pages = page_table.shape[-1]
     _int32(page_table, "page_table", (B, max_pages))
     _int32(seqlens, "seqlens", (B,))
     _int32(path, "path", (B, N))
     _int32(count, "count", (B,))
-    _here(kpages, vpages, page_table, seqlens, path, count, seqlens_out)
+    dev = _device(kpages, vpages, page_table, seqlens, path, count, seqlens_out)
     if seqlens_out is None:
-        with _allocating_on(stream):
-            seqlens_out = torch.empty_like(seqlens)
-    _int32(seqlens_out, "seqlens_out", (B,))
-    st = fa_compact_tree(kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
-                         seqlens.data_ptr(), path.data_ptr(), count.data_ptr(),
-                         seqlens_out.data_ptr(), layers, B, N, Hkv, num_pages, page_size,
-                         max_pages, D, _stream_handle(stream))
+        seqlens_out = _empty((B,), torch.int32, dev, stream)
+    else:
+        _int32(seqlens_out, "seqlens_out", (B,))
+    st = load().fa_compact_tree(kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
+                                seqlens.data_ptr(), path.data_ptr(), count.data_ptr(),
+                                seqlens_out.data_ptr(), shape[0] if len(shape) == 5 else 1, B, N,
+                                shape[-2], shape[-4], shape[-3], max_pages, shape[-1],
+                                _raw_stream(stream, dev))
     if st != FA_OK:
         raise FAError(st, "fa_compact_tree")
     return seqlens_out

@@ -60,6 +60,43 @@ int sm_count() {
   return n;
 }
 
+cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
+  static std::mutex mu;
+  static cudaMemPool_t pools[64];
+  static bool tried[64];
+  int dev = 0;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  // Under capture the graph owns the allocation, whatever the pool.
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 ||
+      cudaStreamIsCapturing(stream, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
+    cudaGetLastError();
+    return cudaMallocAsync(ptr, bytes, stream);
+  }
+  cudaMemPool_t pool = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!tried[dev]) {
+      tried[dev] = true;
+      cudaMemPoolProps props = {};
+      props.allocType = cudaMemAllocationTypePinned;
+      props.handleTypes = cudaMemHandleTypeNone;
+      props.location.type = cudaMemLocationTypeDevice;
+      props.location.id = dev;
+      unsigned long long keep = 256ull << 20;
+      if (cudaMemPoolCreate(&pools[dev], &props) != cudaSuccess) {
+        pools[dev] = nullptr;
+        cudaGetLastError();
+      } else if (cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &keep) !=
+                 cudaSuccess) {
+        cudaGetLastError();
+      }
+    }
+    pool = pools[dev];
+  }
+  return pool ? cudaMallocFromPoolAsync(ptr, bytes, pool, stream)
+              : cudaMallocAsync(ptr, bytes, stream);
+}
+
 }  // namespace fa
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -88,6 +88,12 @@ int set_decode_wait_limit(unsigned long long ns);
 int set_backward_wait_limit(unsigned long long ns);
 int set_tree_wait_limit(unsigned long long ns);
 
+// Stream-ordered scratch (free it with cudaFreeAsync on the stream) from a pool
+// of this library's that keeps up to 256 MiB of freed memory per device: the
+// device's default pool gives its memory back at every synchronisation, and a
+// call after one would wait for the driver to map it again.
+cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream);
+
 // Status of a CUDA call for the C ABI: FA_OK for 0, else FA_ERR_CUDA after
 // recording the raw error and the failing call (a static string) for
 // fa_last_cuda_error() in the calling thread.

@@ -43,8 +43,7 @@ __device__ unsigned int g_rope_err = 0;
 namespace rp {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int UNR = 4;           // head groups whose loads are in flight per warp
-constexpr int BWD_UNR = 2;
+constexpr int UNR = 2;  // head groups per step; a step's loads run ahead by one step
 constexpr int BLOCKS_PER_SM = 2;
 }  // namespace rp
 
@@ -87,17 +86,21 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack2<T>(f[6], f[7]));
 }
 
-// One of the tensors a launch walks (queries, keys, values), and the blocks
-// [b0, b0 + nb) of the grid that walk it.
+// One of the tensors a launch walks: queries, keys or values.
 struct RopePart {
-  const void* x;       // [tokens][H][D], token stride xs elements
-  const void* g;       // gradient: dL/dout, contiguous
-  void* y;             // contiguous output, or pages
-  const void* w;       // [D]; null: copy the heads as they are (values)
+  const void* x;  // [tokens][H][D], token stride xs elements
+  const void* g;  // gradient: dL/dout, contiguous
+  void* y;        // contiguous output, or pages
+  const void* w;  // [D]; null: copy the heads as they are (values)
   long long xs;
-  int H, units, upw, cpt;  // heads; head groups per token, per task; tasks per token
-  int b0, nb;
+  int H;
   int paged;
+  // Forward: the part's head groups are [first, first + units) of a token's.
+  int first, units;
+  // Gradient: blocks [b0, b0 + nb) of the grid walk the part.
+  int b0, nb;
+  // A task is up to upt head groups of one token, cpt tasks per token.
+  int upt, cpt;
 };
 
 struct RopeParams {
@@ -110,6 +113,7 @@ struct RopeParams {
   int N;  // new tokens per sequence (paged)
   int page_size, max_pages, num_pages;
   long long tokens;
+  int groups, upt, cpt;  // forward: head groups of a token, and its tasks
   int rot;
   float eps;
   float* partial;  // gradient: [blocks][D] sums of dw
@@ -199,12 +203,31 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// The part whose blocks include this one.
-__device__ __forceinline__ const RopePart& rope_part(const RopeParams& p) {
-  int i = 0;
-  while (i + 1 < p.n_parts && (int)blockIdx.x >= p.part[i + 1].b0) ++i;
-  return p.part[i];
-}
+// A warp's place in its tasks: warps take tasks in a grid stride, a step at a
+// time.  (The stride is added as whole tokens and tasks: no division per task.)
+struct RopeWalk {
+  long long t;  // token
+  int c;        // task of the token
+  int u;        // head group
+  __device__ __forceinline__ RopeWalk(long long w, int cpt, int upt) {
+    t = w / cpt;
+    c = (int)(w - t * cpt);
+    u = c * upt;
+  }
+  __device__ __forceinline__ int end(int upt, int groups) const {
+    const int e = (c + 1) * upt;
+    return e < groups ? e : groups;
+  }
+  __device__ __forceinline__ void next_task(int cpt, int upt, long long dt, int dc) {
+    t += dt;
+    c += dc;
+    if (c >= cpt) {
+      c -= cpt;
+      ++t;
+    }
+    u = c * upt;
+  }
+};
 
 // Cache row of token t (slot seqlens[b] - N + s), in rows of the pool, or -1
 // (a padding sequence, or a length or page id out of range, which sets the
@@ -227,8 +250,10 @@ __device__ __forceinline__ long long cache_row(const RopeParams& p, long long t,
   return (long long)pid * p.page_size + (*slot - pg * p.page_size);
 }
 
-// A task is upw head groups (HPW heads each) of one token; warps take tasks in
-// a grid stride.
+// HPW heads of one token make a head group; a token's groups are its query
+// heads', then its keys', then (paged) its values'.  Each warp keeps one step of
+// UNR groups in registers while the next step's loads are on their way, across
+// the ends of its tasks too.
 template <int D, typename T, bool IL, bool PAGED>
 __global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
     rope_kernel(const __grid_constant__ RopeParams p) {
@@ -236,88 +261,121 @@ __global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
   __shared__ unsigned long long sF[D / 2];
   pdl_launch_dependents();
   pdl_wait_primary();
-  load_fractions(p.inv_freq, p.rot / 2, sF);
-  const RopePart& pt = rope_part(p);
   const int lane = threadIdx.x & 31;
   const M m(lane, p.rot);
-  const T* x = static_cast<const T*>(pt.x);
-  T* y = static_cast<T*>(pt.y);
-  const bool norm = pt.w != nullptr;
-  float w0[8], w1[8];
-  if (norm) {
-    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8), w0);
-    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8), w1);
-  }
-  const long long n_tasks = p.tokens * pt.cpt;
-  const long long stride = (long long)pt.nb * rp::WARPS;
-  for (long long k = (long long)(blockIdx.x - pt.b0) * rp::WARPS + (threadIdx.x >> 5);
-       k < n_tasks; k += stride) {
-    const long long t = k / pt.cpt;
-    const int u0 = (int)(k - t * pt.cpt) * pt.upw;
-    const int u1 = u0 + pt.upw < pt.units ? u0 + pt.upw : pt.units;
-    long long row = t;
-    int pos = 0;
-    if constexpr (PAGED) {
-      int slot;
-      const long long cr = cache_row(p, t, &slot);
-      if (pt.paged) {
-        if (cr < 0) continue;  // warp-uniform
-        row = cr;
-      }
-      pos = p.positions ? p.positions[t] : slot;
-    } else {
-      pos = p.positions[t];
-    }
-    const T* xt = x + t * pt.xs;
-    T* yt = y + row * (long long)pt.H * D;
-    float cs[8], sn[8];
-    if (norm) cos_sin<D, IL>(m, p.rot, pos, sF, cs, sn);
-    for (int u = u0; u < u1; u += rp::UNR) {
-      uint4 r0[rp::UNR], r1[rp::UNR];
+  const long long warps = (long long)gridDim.x * rp::WARPS;
+  const long long w0 = (long long)blockIdx.x * rp::WARPS + (threadIdx.x >> 5);
+  const long long dt = warps / p.cpt;
+  const int dc = (int)(warps - dt * p.cpt);
+  RopeWalk at(w0, p.cpt, p.upt);
+
+  // The part of head group u.
+  auto part_of = [&](int u) {
+    int i = 0;
+    if (p.n_parts > 1 && u >= p.part[1].first) i = 1;
+    if (PAGED && p.n_parts > 2 && u >= p.part[2].first) i = 2;
+    return i;
+  };
+  auto load = [&](const RopeWalk& a, uint4 (&r)[rp::UNR][2], int* pos) {
+    if (a.t >= p.tokens) return;
+    const int end = a.end(p.upt, p.groups);
 #pragma unroll
-      for (int j = 0; j < rp::UNR; ++j) {
-        const int h = (u + j) * M::HPW + m.sub;
-        r0[j] = r1[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (u + j < u1 && h < pt.H) {
-          r0[j] = *reinterpret_cast<const uint4*>(xt + (size_t)h * D + m.c0 * 8);
-          r1[j] = *reinterpret_cast<const uint4*>(xt + (size_t)h * D + m.c1 * 8);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < rp::UNR; ++j) {
-        if (u + j >= u1) break;  // warp-uniform
-        const int h = (u + j) * M::HPW + m.sub;
-        if (norm) {
-          float a[8], b[8];
-          unpack8<T>(r0[j], a);
-          unpack8<T>(r1[j], b);
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-          ss = head_sum<M::LPH>(ss);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] *= r * w0[e];
-            b[e] *= r * w1[e];
-          }
-          turn<IL>(a, b, cs, sn, 1.f);
-          r0[j] = pack8<T>(a);
-          r1[j] = pack8<T>(b);
-        }
+    for (int j = 0; j < rp::UNR; ++j) {
+      const int u = a.u + j;
+      if (u < end) {
+        const RopePart& pt = p.part[part_of(u)];
+        const int h = (u - pt.first) * M::HPW + m.sub;
         if (h < pt.H) {
-          *reinterpret_cast<uint4*>(yt + (size_t)h * D + m.c0 * 8) = r0[j];
-          *reinterpret_cast<uint4*>(yt + (size_t)h * D + m.c1 * 8) = r1[j];
+          const T* x = static_cast<const T*>(pt.x) + a.t * pt.xs + (size_t)h * D;
+          r[j][0] = *reinterpret_cast<const uint4*>(x + m.c0 * 8);
+          r[j][1] = *reinterpret_cast<const uint4*>(x + m.c1 * 8);
         }
       }
+    }
+    if (!PAGED || p.positions) *pos = p.positions[a.t];
+  };
+
+  uint4 cur[rp::UNR][2], nxt[rp::UNR][2];
+#pragma unroll
+  for (int j = 0; j < rp::UNR; ++j)
+    cur[j][0] = cur[j][1] = nxt[j][0] = nxt[j][1] = make_uint4(0u, 0u, 0u, 0u);
+  int pos = 0, pos_n = 0;
+  load(at, cur, &pos);
+  load_fractions(p.inv_freq, p.rot / 2, sF);
+  long long token = -1, row = 0;
+  int kind = -1;
+  float cs[8], sn[8];
+  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+  while (at.t < p.tokens) {
+    RopeWalk nx = at;
+    nx.u += rp::UNR;
+    if (nx.u >= at.end(p.upt, p.groups)) nx.next_task(p.cpt, p.upt, dt, dc);
+    load(nx, nxt, &pos_n);
+    if (at.t != token) {  // warp-uniform, as is every branch on the walk
+      token = at.t;
+      if constexpr (PAGED) {
+        int slot;
+        row = cache_row(p, token, &slot);
+        if (!p.positions) pos = slot;
+      }
+      cos_sin<D, IL>(m, p.rot, pos, sF, cs, sn);
+    }
+    const int end = at.end(p.upt, p.groups);
+#pragma unroll
+    for (int j = 0; j < rp::UNR; ++j) {
+      const int u = at.u + j;
+      if (u >= end) break;
+      const int i = part_of(u);
+      const RopePart& pt = p.part[i];
+      const int h = (u - pt.first) * M::HPW + m.sub;
+      const bool norm = !PAGED || pt.w != nullptr;
+      if (i != kind) {
+        kind = i;
+        if (norm) {
+          wa = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8);
+          wb = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8);
+        }
+      }
+      if (norm) {
+        float a[8], b[8], w[8];
+        unpack8<T>(cur[j][0], a);
+        unpack8<T>(cur[j][1], b);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+        ss = head_sum<M::LPH>(ss);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        unpack8<T>(wa, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= r * w[e];
+        unpack8<T>(wb, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] *= r * w[e];
+        turn<IL>(a, b, cs, sn, 1.f);
+        cur[j][0] = pack8<T>(a);
+        cur[j][1] = pack8<T>(b);
+      }
+      const long long to = PAGED && pt.paged ? row : token;
+      if (h < pt.H && (!PAGED || to >= 0)) {
+        T* y = static_cast<T*>(pt.y) + (to * pt.H + h) * D;
+        *reinterpret_cast<uint4*>(y + m.c0 * 8) = cur[j][0];
+        *reinterpret_cast<uint4*>(y + m.c1 * 8) = cur[j][1];
+      }
+    }
+    at = nx;
+    pos = pos_n;
+#pragma unroll
+    for (int j = 0; j < rp::UNR; ++j) {
+      cur[j][0] = nxt[j][0];
+      cur[j][1] = nxt[j][1];
     }
   }
 }
 
-// Gradient of rope_kernel.  Each block walks the queries or the keys and ends
-// with one row of partial[] (its sum of gy x r per column); the sums of a
-// lane, a block and the blocks are taken in a fixed order, so equal calls give
-// equal bits.
+// Gradient of rope_kernel.  Each block walks the queries or the keys, a head
+// group per step with the next step's loads ahead, and ends with one row of
+// partial[] (its sum of gy x r per column); the sums of a lane, a block and the
+// blocks are taken in a fixed order, so equal calls give equal bits.
 template <int D, typename T, bool IL>
 __global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
     rope_bwd_kernel(const __grid_constant__ RopeParams p) {
@@ -326,76 +384,90 @@ __global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
   __shared__ float sW[rp::WARPS][D];
   pdl_launch_dependents();
   pdl_wait_primary();
-  load_fractions(p.inv_freq, p.rot / 2, sF);
-  const RopePart& pt = rope_part(p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const M m(lane, p.rot);
+  const RopePart& pt = p.part[p.n_parts > 1 && (int)blockIdx.x >= p.part[1].b0 ? 1 : 0];
   const T* x = static_cast<const T*>(pt.x);
   const T* g = static_cast<const T*>(pt.g);
   T* dx = static_cast<T*>(pt.y);
-  float w0[8], w1[8], acc0[8], acc1[8];
-  unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8), w0);
-  unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8), w1);
+  const long long warps = (long long)pt.nb * rp::WARPS;
+  const long long dt = warps / pt.cpt;
+  const int dc = (int)(warps - dt * pt.cpt);
+  RopeWalk at((long long)(blockIdx.x - pt.b0) * rp::WARPS + warp, pt.cpt, pt.upt);
+
+  auto load = [&](const RopeWalk& q, uint4 (&r)[4], int* pos) {
+    const int h = q.u * M::HPW + m.sub;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (q.t >= p.tokens) return;
+    if (h < pt.H) {
+      const T* xt = x + q.t * pt.xs + (size_t)h * D;
+      const T* gt = g + (q.t * pt.H + h) * D;
+      r[0] = *reinterpret_cast<const uint4*>(xt + m.c0 * 8);
+      r[1] = *reinterpret_cast<const uint4*>(xt + m.c1 * 8);
+      r[2] = *reinterpret_cast<const uint4*>(gt + m.c0 * 8);
+      r[3] = *reinterpret_cast<const uint4*>(gt + m.c1 * 8);
+    }
+    *pos = p.positions[q.t];
+  };
+  uint4 cur[4], nxt[4];
+  int pos = 0, pos_n = 0;
+  load(at, cur, &pos);
+  const uint4 wa = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8);
+  const uint4 wb = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8);
+  load_fractions(p.inv_freq, p.rot / 2, sF);
+  float acc0[8], acc1[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc0[e] = acc1[e] = 0.f;
-  const long long n_tasks = p.tokens * pt.cpt;
-  const long long stride = (long long)pt.nb * rp::WARPS;
-  for (long long k = (long long)(blockIdx.x - pt.b0) * rp::WARPS + warp; k < n_tasks;
-       k += stride) {
-    const long long t = k / pt.cpt;
-    const int u0 = (int)(k - t * pt.cpt) * pt.upw;
-    const int u1 = u0 + pt.upw < pt.units ? u0 + pt.upw : pt.units;
-    const T* xt = x + t * pt.xs;
-    const T* gt = g + t * (long long)pt.H * D;
-    T* dt = dx + t * (long long)pt.H * D;
-    float cs[8], sn[8];
-    cos_sin<D, IL>(m, p.rot, p.positions[t], sF, cs, sn);
-    for (int u = u0; u < u1; u += rp::BWD_UNR) {
-      uint4 x0[rp::BWD_UNR], x1[rp::BWD_UNR], g0[rp::BWD_UNR], g1[rp::BWD_UNR];
-#pragma unroll
-      for (int j = 0; j < rp::BWD_UNR; ++j) {
-        const int h = (u + j) * M::HPW + m.sub;
-        x0[j] = x1[j] = g0[j] = g1[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (u + j < u1 && h < pt.H) {
-          x0[j] = *reinterpret_cast<const uint4*>(xt + (size_t)h * D + m.c0 * 8);
-          x1[j] = *reinterpret_cast<const uint4*>(xt + (size_t)h * D + m.c1 * 8);
-          g0[j] = *reinterpret_cast<const uint4*>(gt + (size_t)h * D + m.c0 * 8);
-          g1[j] = *reinterpret_cast<const uint4*>(gt + (size_t)h * D + m.c1 * 8);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < rp::BWD_UNR; ++j) {
-        if (u + j >= u1) break;  // warp-uniform
-        const int h = (u + j) * M::HPW + m.sub;
-        float a[8], b[8], ga[8], gb[8];
-        unpack8<T>(x0[j], a);
-        unpack8<T>(x1[j], b);
-        unpack8<T>(g0[j], ga);
-        unpack8<T>(g1[j], gb);
-        turn<IL>(ga, gb, cs, sn, -1.f);
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss += a[e] * a[e] + b[e] * b[e];
-          dot += a[e] * (w0[e] * ga[e]) + b[e] * (w1[e] * gb[e]);
-        }
-        ss = head_sum<M::LPH>(ss);
-        dot = head_sum<M::LPH>(dot);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float f = dot * (1.f / D) * r * r;  // r^2 mean(x w gy)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          acc0[e] += ga[e] * (a[e] * r);
-          acc1[e] += gb[e] * (b[e] * r);
-          a[e] = r * (w0[e] * ga[e] - a[e] * f);
-          b[e] = r * (w1[e] * gb[e] - b[e] * f);
-        }
-        if (h < pt.H) {
-          *reinterpret_cast<uint4*>(dt + (size_t)h * D + m.c0 * 8) = pack8<T>(a);
-          *reinterpret_cast<uint4*>(dt + (size_t)h * D + m.c1 * 8) = pack8<T>(b);
-        }
-      }
+  long long token = -1;
+  float cs[8], sn[8];
+  while (at.t < p.tokens) {
+    RopeWalk nx = at;
+    if (++nx.u >= at.end(pt.upt, pt.units)) nx.next_task(pt.cpt, pt.upt, dt, dc);
+    load(nx, nxt, &pos_n);
+    const int h = at.u * M::HPW + m.sub;
+    float a[8], b[8], ga[8], gb[8], w[8];
+    if (at.t != token) {
+      token = at.t;
+      cos_sin<D, IL>(m, p.rot, pos, sF, cs, sn);
     }
+    unpack8<T>(cur[2], ga);
+    unpack8<T>(cur[3], gb);
+    turn<IL>(ga, gb, cs, sn, -1.f);
+    unpack8<T>(cur[0], a);
+    unpack8<T>(cur[1], b);
+    float ss = 0.f, dot = 0.f;
+    unpack8<T>(wa, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ss += a[e] * a[e] + b[e] * b[e];
+      dot += a[e] * (w[e] * ga[e]);
+    }
+    unpack8<T>(wb, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dot += b[e] * (w[e] * gb[e]);
+    ss = head_sum<M::LPH>(ss);
+    dot = head_sum<M::LPH>(dot);
+    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+    const float f = dot * (1.f / D) * r * r;  // r^2 mean(x w gy)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      acc0[e] += ga[e] * (a[e] * r);
+      acc1[e] += gb[e] * (b[e] * r);
+      b[e] = r * (w[e] * gb[e] - b[e] * f);
+    }
+    unpack8<T>(wa, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = r * (w[e] * ga[e] - a[e] * f);
+    if (h < pt.H) {
+      T* d = dx + (token * pt.H + h) * D;
+      *reinterpret_cast<uint4*>(d + m.c0 * 8) = pack8<T>(a);
+      *reinterpret_cast<uint4*>(d + m.c1 * 8) = pack8<T>(b);
+    }
+    at = nx;
+    pos = pos_n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cur[e] = nxt[e];
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -442,34 +514,58 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Blocks and head groups per task.  While the tokens alone do not give every
-// resident warp a task, a token's head groups are spread over several warps.
-static int plan_parts(RopeParams* p, int D) {
+// Head groups per task: the fewest rounds of the resident warps, a round
+// costing its groups and, once, the token's cosines and sines (about as much
+// as two groups).
+static void plan_tasks(long long tokens, int groups, long long warps, int* upt, int* cpt) {
+  long long best = 0;
+  for (int c = 1; c <= groups && c <= 64; ++c) {
+    const int u = (groups + c - 1) / c;
+    if ((groups + u - 1) / u != c) continue;
+    const long long cost = (tokens * c + warps - 1) / warps * (u + 2);
+    if (best == 0 || cost < best) {
+      best = cost;
+      *upt = u;
+      *cpt = c;
+    }
+  }
+}
+
+// Head groups, tasks and blocks.  Returns the grid size.
+static int plan_parts(RopeParams* p, int D, bool bwd) {
   const int hpw = 32 / (D / 16);
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  const long long slots = (long long)sms * rp::BLOCKS_PER_SM;
-  long long heads = 0;
-  for (int i = 0; i < p->n_parts; ++i) heads += p->part[i].H;
-  int b0 = 0;
+  const long long slots = (long long)sms * rp::BLOCKS_PER_SM;  // resident blocks
+  long long groups = 0;
   for (int i = 0; i < p->n_parts; ++i) {
     RopePart& t = p->part[i];
     t.units = (t.H + hpw - 1) / hpw;
-    const long long all = p->tokens * t.units;
-    // This part's share of the resident blocks.
-    long long nb = (slots * t.H + heads - 1) / heads;
-    long long upw = (all + nb * rp::WARPS - 1) / (nb * rp::WARPS);
-    if (upw > t.units) upw = t.units;
-    if (upw < 1) upw = 1;
-    t.upw = (int)upw;
-    t.cpt = (t.units + t.upw - 1) / t.upw;
-    const long long need = (p->tokens * t.cpt + rp::WARPS - 1) / rp::WARPS;
-    if (nb > need) nb = need;
-    if (nb < 1) nb = 1;
-    t.b0 = b0;
-    t.nb = (int)nb;
-    b0 += t.nb;
+    t.first = (int)groups;
+    groups += t.units;
   }
-  return b0;
+  if (bwd) {
+    // Blocks in proportion to the parts' head groups, all resident at once.
+    long long left = slots;
+    int b0 = 0;
+    for (int i = 0; i < p->n_parts; ++i) {
+      RopePart& t = p->part[i];
+      long long nb = i + 1 < p->n_parts ? (slots * t.units + groups / 2) / groups : left;
+      if (nb > left - (p->n_parts - 1 - i)) nb = left - (p->n_parts - 1 - i);
+      if (nb < 1) nb = 1;
+      left -= nb;
+      plan_tasks(p->tokens, t.units, nb * rp::WARPS, &t.upt, &t.cpt);
+      const long long need = (p->tokens * t.cpt + rp::WARPS - 1) / rp::WARPS;
+      if (nb > need) nb = need;
+      t.b0 = b0;
+      t.nb = (int)nb;
+      b0 += t.nb;
+    }
+    return b0;
+  }
+  p->groups = (int)groups;
+  plan_tasks(p->tokens, p->groups, slots * rp::WARPS, &p->upt, &p->cpt);
+  const long long need = (p->tokens * p->cpt + rp::WARPS - 1) / rp::WARPS;
+  return (int)(need < slots ? need : slots);
 }
 
 template <typename... Args>
@@ -580,7 +676,7 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
   p.tokens = T;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D);
+  const int blocks = fa::plan_parts(&p, D, false);
   return fa::record_cuda_status(
       fa::launch_rope(p, blocks, D, dtype == FA_BF16, false, false, interleaved != 0, stream),
       "norm and rotation launch");
@@ -627,7 +723,7 @@ extern "C" int fa_qk_norm_rope_append(const void* q, const void* k, const void* 
   p.tokens = (long long)B * N;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D);
+  const int blocks = fa::plan_parts(&p, D, false);
   return fa::record_cuda_status(
       fa::launch_rope(p, blocks, D, dtype == FA_BF16, true, false, interleaved != 0, stream),
       "norm, rotation and append launch");
@@ -641,20 +737,21 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
                                         long long k_stride, float eps, int interleaved, int dtype,
                                         cudaStream_t stream) {
   if (!rope_sizes_ok(T, Hq, Hkv, D, rot_dim, eps, dtype)) return FA_ERR_INVALID_ARG;
-  if (Hq == 0 && Hkv == 0) return FA_OK;
-  if ((Hq && !al(dq_weight, 4)) || (Hkv && !al(dk_weight, 4))) return FA_ERR_INVALID_ARG;
-  if (T == 0) {  // no row: the weights' gradients are zero
-    cudaError_t e = cudaSuccess;
-    if (Hq) e = cudaMemsetAsync(dq_weight, 0, D * sizeof(float), stream);
-    if (Hkv && e == cudaSuccess) e = cudaMemsetAsync(dk_weight, 0, D * sizeof(float), stream);
-    return fa::record_cuda_status(e, "norm and rotation gradient zero-fill");
-  }
-  if (!al(inv_freq, 4) || !al(positions, 4)) return FA_ERR_INVALID_ARG;
-  if (Hq && (!heads_ok(q, q_stride, Hq, D) || !al(dq_out, 16) || !al(dq, 16) || !al(q_weight, 16)))
+  if (!al(dq_weight, 4) || !al(dk_weight, 4)) return FA_ERR_INVALID_ARG;
+  if (T > 0 && (Hq || Hkv) && (!al(inv_freq, 4) || !al(positions, 4))) return FA_ERR_INVALID_ARG;
+  if (T > 0 && Hq &&
+      (!heads_ok(q, q_stride, Hq, D) || !al(dq_out, 16) || !al(dq, 16) || !al(q_weight, 16)))
     return FA_ERR_INVALID_ARG;
-  if (Hkv &&
+  if (T > 0 && Hkv &&
       (!heads_ok(k, k_stride, Hkv, D) || !al(dk_out, 16) || !al(dk, 16) || !al(k_weight, 16)))
     return FA_ERR_INVALID_ARG;
+  // A side without rows has a zero weight gradient.
+  cudaError_t e = cudaSuccess;
+  if (T == 0 || Hq == 0) e = cudaMemsetAsync(dq_weight, 0, D * sizeof(float), stream);
+  if (e == cudaSuccess && (T == 0 || Hkv == 0))
+    e = cudaMemsetAsync(dk_weight, 0, D * sizeof(float), stream);
+  if (e != cudaSuccess || T == 0 || (Hq == 0 && Hkv == 0))
+    return fa::record_cuda_status(e, "norm and rotation gradient zero-fill");
   fa::RopeParams p = {};
   int iq = -1, ik = -1;
   if (Hq) {
@@ -670,11 +767,10 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
   p.tokens = T;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D);
+  const int blocks = fa::plan_parts(&p, D, true);
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocAsync(&scratch, (size_t)blocks * D * sizeof(float), stream);
-  if (e != cudaSuccess)
-    return fa::record_cuda_status(e, "norm and rotation gradient cudaMallocAsync");
+  e = fa::scratch_alloc(&scratch, (size_t)blocks * D * sizeof(float), stream);
+  if (e != cudaSuccess) return fa::record_cuda_status(e, "norm and rotation gradient scratch");
   p.partial = static_cast<float*>(scratch);
   int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, false, true, interleaved != 0, stream);
   if (r == 0)

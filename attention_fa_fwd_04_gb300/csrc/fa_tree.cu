@@ -103,6 +103,12 @@ struct TreeSeg {
   int b, hkv, t0, n, T, L;
 };
 
+// Groups in use: every one of them has a tile (a group without one between two
+// of a unit's would leave the merge a partial that nobody wrote).
+__device__ __forceinline__ long long tree_groups(const TreeParams& p, long long total) {
+  return total < p.groups ? total : p.groups;
+}
+
 // Whole warp: the range of group g and the sequence it starts in.
 __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
   const int lane = threadIdx.x & 31;
@@ -112,9 +118,10 @@ __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const long long total = sum * p.Hkv;
+  const long long G = tree_groups(p, total);
   TreeWalk w;
-  w.x = total * g / p.groups;
-  w.hi = total * (g + 1) / p.groups;
+  w.x = g < G ? total * g / G : 0;
+  w.hi = g < G ? total * (g + 1) / G : 0;
   w.first = 0;
   w.b = 0;
   w.T = 0;
@@ -762,9 +769,10 @@ __global__ void __launch_bounds__(kTreeRowWarps * 32)
   for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
   if (T_b > 0) {
     const long long u0 = first + hkv * T_b, u1 = u0 + T_b - 1;
-    // Group of tile t: the largest g with total * g / groups <= t.
-    const int g0 = (int)(((u0 + 1) * p.groups - 1) / total);
-    const int g1 = (int)(((u1 + 1) * p.groups - 1) / total);
+    // Group of tile t: the largest g with total * g / G <= t.
+    const long long G = tree_groups(p, total);
+    const int g0 = (int)(((u0 + 1) * G - 1) / total);
+    const int g1 = (int)(((u1 + 1) * G - 1) / total);
     if (g0 == g1) return;  // finished in place
     for (int k0 = g0; k0 <= g1; k0 += 4) {
       float2 ml[4];
@@ -836,7 +844,7 @@ static TreePlan tree_host_plan(int B, int N, int Hq, int Hkv, long long cap, int
   const size_t slots = (size_t)t.groups * t.n_rt * 2 * t.rt_rows;
   t.o_floats = slots * D;
   t.ml_floats = slots * 2;
-  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 1) * sizeof(long long);
+  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 3) * sizeof(long long);
   return t;
 }
 
@@ -974,8 +982,8 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
       fa::encode_tmap_rows(&tv, vpages, D, Hkv, page_size, num_pages, p.box))
     return fa::record_cuda_status(cudaErrorInvalidValue, "tree decode tensor maps");
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocAsync(&scratch, t.bytes, stream);
-  if (e != cudaSuccess) return fa::record_cuda_status(e, "tree decode cudaMallocAsync");
+  cudaError_t e = fa::scratch_alloc(&scratch, t.bytes, stream);
+  if (e != cudaSuccess) return fa::record_cuda_status(e, "tree decode scratch");
   p.start = static_cast<long long*>(scratch);
   // (B + 1) 8-byte entries, then the partials 16-byte aligned.
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +

@@ -19,12 +19,13 @@
 // bits, by error-free sums and products), which costs a dozen fp32 operations
 // per element where fp64 would be bound by the few fp64 units.
 //
-// Bound: two rows of V floats per sequence (the node where its walk stops),
-// once from HBM and for further rejected siblings from L2; for few sequences,
-// latency.  The tests themselves read single elements: those of all nodes are
-// fetched at once, and the walk itself runs on shared memory.  A cluster of 8
-// CTAs takes one sequence: every CTA walks (the same way), and for a mass each
-// sums an eighth of the row and pushes its sum to the other seven.
+// Bound: two rows of V floats per sequence (the node where its walk stops, and
+// nodes where more than one child is tried), once from HBM and for further
+// rejected siblings from L2; for few sequences, latency.  The tests themselves
+// read single elements: those of all nodes are fetched at once, and the walk
+// runs on shared memory, in one warp of each CTA.  A cluster of up to 8 CTAs
+// takes one sequence: every CTA walks (the same way), and for a mass each sums
+// its part of the row and pushes its sum to the others.
 #include <math.h>
 
 #include "fa.h"
@@ -36,9 +37,10 @@ namespace fa {
 __device__ unsigned int g_verify_err = 0;
 
 namespace vf {
-constexpr int CLUSTER = 8;
+constexpr int CLUSTER = 8;  // CTAs per sequence, at most
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
+constexpr int BLOCKS_PER_SM = 2;
 constexpr int MAX_N = 64;
 }  // namespace vf
 
@@ -52,7 +54,8 @@ struct VerifyParams {
   int32_t* count;
   int32_t* next;
   int N, V;
-  int part;  // tokens per warp, a multiple of 128
+  int cluster;  // CTAs per sequence
+  int part;     // tokens per warp, a multiple of 128
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -70,73 +73,162 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_remote(double* local, uint32_t rank, double v) {
+
+// A probability as it counts: anything but a positive finite number is 0.
+__device__ __forceinline__ float clean(float x) {
+  return __float_as_uint(x) < 0x7f800000u ? x : 0.f;
+}
+
+// Unevaluated sum of two floats, |lo| at most half a step of hi.
+struct __align__(8) Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ void store_remote(Pair* local, uint32_t rank, Pair v) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f64 [a], %2;\n\t}" ::"r"(smem_u32(local)),
-      "r"(rank), "d"(v)
+      "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(smem_u32(local)),
+      "r"(rank), "f"(v.hi), "f"(v.lo)
       : "memory");
 }
-
-// A probability as it counts: anything but a positive finite number is 0.
-__device__ __forceinline__ float clean(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
-
-// Unevaluated sum of two floats, |lo| at most half a step of hi.
-struct Pair {
-  float hi, lo;
-};
 __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+// |a| >= |b|.
+__device__ __forceinline__ Pair fast_two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return fast_two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float h = __fmul_rn(a.hi, b.hi);
+  float l = __fmaf_rn(a.hi, b.hi, -h);
+  l = __fmaf_rn(a.hi, b.lo, l);
+  return fast_two_sum(h, __fmaf_rn(a.lo, b.hi, l));
+}
+__device__ __forceinline__ bool above(Pair a, Pair b) {
+  const Pair d = two_sum(a.hi, -b.hi);
+  return __fadd_rn(d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo))) > 0.f;
+}
+__device__ __forceinline__ Pair shfl_up(Pair a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+}
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
+  return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+}
+__device__ __forceinline__ Pair shfl(Pair a, int l) {
+  return {__shfl_sync(0xffffffffu, a.hi, l), __shfl_sync(0xffffffffu, a.lo, l)};
 }
 // max(r - Z q, 0).
 __device__ __forceinline__ Pair residual(Pair r, Pair Z, float q) {
   const float h = __fmul_rn(Z.hi, q);
   const float l = __fmaf_rn(Z.lo, q, __fmaf_rn(Z.hi, q, -h));
   Pair d = two_sum(r.hi, -h);
-  d.lo = __fadd_rn(d.lo, __fsub_rn(r.lo, l));
-  const float s = __fadd_rn(d.hi, d.lo);
-  const float e = __fsub_rn(d.lo, __fsub_rn(s, d.hi));
-  return s > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
+  d = fast_two_sum(d.hi, __fadd_rn(d.lo, __fsub_rn(r.lo, l)));
+  return d.hi > 0.f ? d : Pair{0.f, 0.f};
 }
 
-// What a node's rejected children left: the masses before each rejection
-// (drafted from q), or the rejected tokens (no q).
+// What a node's rejected children left of its row: the masses before each
+// rejection (drafted from q), or the rejected tokens (no q).
 struct Rejected {
   int n;
   const Pair* mass;
   const int* token;
 };
 
-template <bool DRAFT>
+// Element v of what is left.  LEVEL: rj.n where it is 0 or 1, else 2.  (After
+// one rejection, with Z = 1, a positive p - q is a difference of p >= q >= 0,
+// whose error is one more subtraction.)
+template <bool DRAFT, int LEVEL>
 __device__ __forceinline__ Pair left_of(float p, float q, int v, const Rejected& rj) {
   Pair r{clean(p), 0.f};
-  if constexpr (DRAFT) {
-    const float qc = clean(q);
-    for (int i = 0; i < rj.n; ++i) r = residual(r, rj.mass[i], qc);
-  } else {
+  if constexpr (LEVEL == 0) {
+  } else if constexpr (!DRAFT) {
     for (int i = 0; i < rj.n; ++i)
       if (rj.token[i] == v) r.hi = 0.f;
+  } else {
+    const float c = clean(q);
+    const float d = __fsub_rn(r.hi, c);
+    r = d > 0.f ? Pair{d, __fsub_rn(__fsub_rn(r.hi, d), c)} : Pair{0.f, 0.f};
+    if constexpr (LEVEL == 2)
+      for (int i = 1; i < rj.n; ++i) r = residual(r, rj.mass[i], c);
   }
   return r;
 }
 
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* row, int v, int end) {
+  if constexpr (VEC) {
+    return v < end ? *reinterpret_cast<const float4*>(row + v) : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    return make_float4(v < end ? row[v] : 0.f, v + 1 < end ? row[v + 1] : 0.f,
+                       v + 2 < end ? row[v + 2] : 0.f, v + 3 < end ? row[v + 3] : 0.f);
+  }
+}
+
+// Sum of what is left in [va, vb) of a row, over the warp.
+template <bool DRAFT, bool VEC, int LEVEL>
+__device__ __forceinline__ Pair sum_left(const float* pr, const float* qr, int va, int vb,
+                                         const Rejected& rj) {
+  const int lane = threadIdx.x & 31;
+  Pair acc{0.f, 0.f};
+  auto take = [&](float a, float d, int v) {
+    const Pair r = left_of<DRAFT, LEVEL>(a, d, v, rj);
+    const Pair s = two_sum(acc.hi, r.hi);
+    acc = {s.hi, __fadd_rn(acc.lo, __fadd_rn(s.lo, r.lo))};
+  };
+  if constexpr (VEC) {
+    constexpr int AHEAD = 4;
+    for (int v0 = va + lane * 4; v0 < vb; v0 += 128 * AHEAD) {
+      float4 a[AHEAD], d[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        a[i] = load4<true>(pr, v0 + i * 128, vb);
+        if constexpr (DRAFT && LEVEL > 0) d[i] = load4<true>(qr, v0 + i * 128, vb);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int v = v0 + i * 128;
+        if constexpr (!(DRAFT && LEVEL > 0)) d[i] = a[i];
+        take(a[i].x, d[i].x, v);
+        take(a[i].y, d[i].y, v + 1);
+        take(a[i].z, d[i].z, v + 2);
+        take(a[i].w, d[i].w, v + 3);
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (int v = va + lane; v < vb; v += 32)
+      take(pr[v], DRAFT && LEVEL > 0 ? qr[v] : 0.f, v);
+  }
+  acc = fast_two_sum(acc.hi, acc.lo);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc = add(acc, shfl_xor(acc, o));
+  return acc;
+}
+
 // VEC: rows are 16-byte aligned (V a multiple of 4).
 template <bool DRAFT, bool VEC>
-__global__ void __cluster_dims__(vf::CLUSTER, 1, 1) __launch_bounds__(vf::THREADS, 2)
+__global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int s_parent[vf::MAX_N], s_token[vf::MAX_N], s_rej[vf::MAX_N];
   __shared__ float s_u[vf::MAX_N], s_px[vf::MAX_N], s_qx[vf::MAX_N];
   __shared__ Pair s_mass[vf::MAX_N];
-  __shared__ double s_warp[vf::WARPS];
-  __shared__ double s_cta[2][vf::CLUSTER];
+  __shared__ Pair s_warp[vf::WARPS];
+  __shared__ Pair s_cta[2][vf::CLUSTER];
+  __shared__ int s_cur, s_nrej;
+  __shared__ bool s_last, s_known;
+  __shared__ uint64_t s_path;
   pdl_launch_dependents();
   cluster_arrive();  // (waited for below: no CTA is written to before it runs)
   pdl_wait_primary();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank();
-  const int b = blockIdx.x / vf::CLUSTER;
+  const int rank = (int)cluster_rank(), CL = p.cluster;
+  const int b = blockIdx.x / CL;
   const int N = p.N, V = p.V;
   const size_t node0 = (size_t)b * N;
 
@@ -148,183 +240,223 @@ __global__ void __cluster_dims__(vf::CLUSTER, 1, 1) __launch_bounds__(vf::THREAD
       par = -2;
       if (rank == 0) atomicOr(&g_verify_err, kErrBounds);
     }
-    s_parent[tid] = tid == 0 ? -1 : (par < 0 ? -2 : par);
+    const bool edge = tid > 0 && par >= 0;
+    s_parent[tid] = edge ? par : -2;
     s_token[tid] = x;
     s_u[tid] = p.u[node0 + tid];
-    s_px[tid] = par >= 0 && tid > 0 ? clean(p.p[(node0 + par) * V + x]) : 0.f;
-    s_qx[tid] = DRAFT && par >= 0 && tid > 0 ? clean(p.q[(node0 + par) * V + x]) : 1.f;
+    s_px[tid] = edge ? clean(p.p[(node0 + par) * V + x]) : 0.f;
+    s_qx[tid] = DRAFT ? (edge ? clean(p.q[(node0 + par) * V + x]) : 0.f) : 1.f;
   }
   __syncthreads();
   cluster_wait();
 
-  // The walk.  Every warp of every CTA takes the same steps.
-  const int par0 = lane < N ? s_parent[lane] : -2, par1 = lane + 32 < N ? s_parent[lane + 32] : -2;
-  int cur = 0, n_path = 1;
-  uint64_t on_path = 1;
-  int n_rej = 0, n_sum = -1;  // rejections at cur; rejections that s_warp, s_cta stand for
-  int pass = 0;
   const long long v0 = ((long long)rank * vf::WARPS + warp) * p.part;
   const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
-
-  // Sum of what is left at cur after n rejections, over all of the row.
-  auto mass_of = [&](int n) {
+  int pass = 0;
+  // Sum of what is left of node cur's row after n rejections: s_warp and
+  // s_cta[pass & 1], and their total.  All threads of the cluster.
+  auto mass_of = [&](int cur, int n) {
     const Rejected rj{n, s_mass, s_rej};
     const float* pr = p.p + (node0 + cur) * V;
     const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-    Pair acc{0.f, 0.f};
-    auto add = [&](float a, float d, int v) {
-      const Pair r = left_of<DRAFT>(a, d, v, rj);
-      const Pair s = two_sum(acc.hi, r.hi);
-      acc = {s.hi, __fadd_rn(acc.lo, __fadd_rn(s.lo, r.lo))};
-    };
-    if constexpr (VEC) {
-#pragma unroll 4
-      for (int v = va + lane * 4; v < vb; v += 128) {
-        const float4 a = *reinterpret_cast<const float4*>(pr + v);
-        const float4 d = DRAFT ? *reinterpret_cast<const float4*>(qr + v) : a;
-        add(a.x, d.x, v);
-        add(a.y, d.y, v + 1);
-        add(a.z, d.z, v + 2);
-        add(a.w, d.w, v + 3);
-      }
-    } else {
-#pragma unroll 8
-      for (int v = va + lane; v < vb; v += 32) add(pr[v], DRAFT ? qr[v] : 0.f, v);
-    }
-    double s = (double)acc.hi + (double)acc.lo;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();  // (s_warp of an earlier pass has been read)
+    const Pair s = n == 0   ? sum_left<DRAFT, VEC, 0>(pr, qr, va, vb, rj)
+                   : n == 1 ? sum_left<DRAFT, VEC, 1>(pr, qr, va, vb, rj)
+                            : sum_left<DRAFT, VEC, 2>(pr, qr, va, vb, rj);
     if (lane == 0) s_warp[warp] = s;
     __syncthreads();
-    if (warp == 0 && lane < vf::CLUSTER) {
-      double t = 0.0;
+    ++pass;
+    if (warp == 0) {
+      Pair t = lane < vf::WARPS ? s_warp[lane] : Pair{0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < vf::WARPS; ++i) t += s_warp[i];
-      store_remote(&s_cta[pass & 1][rank], lane, t);
+      for (int o = vf::WARPS / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
+      if (lane < CL) store_remote(&s_cta[pass & 1][rank], lane, t);
     }
     cluster_sync();
-    double t = 0.0;
-#pragma unroll
-    for (int i = 0; i < vf::CLUSTER; ++i) t += s_cta[pass & 1][i];
-    ++pass;
-    n_sum = n;
+  };
+  auto total_of = [&]() {
+    Pair t{0.f, 0.f};
+    for (int i = 0; i < CL; ++i) t = add(t, s_cta[pass & 1][i]);
     return t;
   };
 
+  // The walk, by warp 0; the others join for masses.
+  const int par0 = lane < N ? s_parent[lane] : -2, par1 = lane + 32 < N ? s_parent[lane + 32] : -2;
+  auto children = [&](int node) {
+    return (uint64_t)__ballot_sync(0xffffffffu, par0 == node) |
+           (uint64_t)__ballot_sync(0xffffffffu, par1 == node) << 32;
+  };
+  int cur = 0, n_rej = 0, n_sum = -1;  // n_sum: rejections that the sums stand for
+  uint64_t path = 1, kids = warp == 0 ? children(0) : 0;
+  Pair Z{1.f, 0.f};
   for (;;) {
-    uint64_t kids = (uint64_t)__ballot_sync(0xffffffffu, par0 == cur) |
-                    (uint64_t)__ballot_sync(0xffffffffu, par1 == cur) << 32;
-    n_rej = 0;
-    n_sum = -1;
-    double Z = 1.0;
-    int down = -1;
-    while (kids) {
-      const int c = __ffsll((long long)kids) - 1;
-      kids &= kids - 1;
-      const int x = s_token[c];
-      double r = (double)s_px[c], qx = (double)s_qx[c];
-      if constexpr (DRAFT) {
-        if (n_rej > 0) {
-          if (n_sum != n_rej) Z = mass_of(n_rej);
-          for (int i = 0; i < n_rej; ++i) {
-            const double z = (double)s_mass[i].hi + (double)s_mass[i].lo;
-            r = fmax(r - z * qx, 0.0);
-          }
+    if (warp == 0) {
+      while (kids) {
+        if (DRAFT && n_rej > 0) {
+          if (n_sum != n_rej) break;
+          Z = total_of();
         }
-      } else {
-        for (int i = 0; i < n_rej; ++i)
-          if (s_rej[i] == x) r = 0.0;
+        const int c = __ffsll((long long)kids) - 1;
+        kids &= kids - 1;
+        const int x = s_token[c];
+        Pair r{s_px[c], 0.f};
+        if constexpr (DRAFT) {
+          for (int i = 0; i < n_rej; ++i) r = residual(r, s_mass[i], s_qx[c]);
+        } else {
+          for (int i = 0; i < n_rej; ++i)
+            if (s_rej[i] == x) r.hi = 0.f;
+        }
+        const Pair bar = mul(mul(Pair{s_u[c], 0.f}, Pair{s_qx[c], 0.f}), Z);
+        if (above(r, bar)) {
+          cur = c;
+          path |= 1ull << c;
+          kids = children(c);
+          n_rej = 0;
+          n_sum = -1;
+          Z = {1.f, 0.f};
+        } else {
+          if (lane == 0) {
+            s_mass[n_rej] = Z;
+            s_rej[n_rej] = x;
+          }
+          __syncwarp();
+          ++n_rej;
+          if constexpr (!DRAFT) Z = add(Z, Pair{-r.hi, 0.f});
+        }
       }
-      if ((double)s_u[c] * qx * Z < r) {
-        down = c;
-        break;
+      if (lane == 0) {
+        s_cur = cur;
+        s_nrej = n_rej;
+        s_last = kids == 0;
+        s_known = n_sum == n_rej;
+        s_path = path;
       }
-      __syncthreads();  // (the lists are still being read)
-      if (tid == 0) {
-        s_mass[n_rej] = {(float)Z, (float)(Z - (double)(float)Z)};
-        s_rej[n_rej] = x;
-      }
-      __syncthreads();
-      ++n_rej;
-      if constexpr (!DRAFT) Z -= r;
     }
-    if (down < 0) break;
-    cur = down;
-    on_path |= 1ull << cur;
-    ++n_path;
+    __syncthreads();
+    const bool last = s_last, known = s_known;
+    cur = s_cur;
+    n_rej = s_nrej;
+    if (!known) mass_of(cur, n_rej);
+    n_sum = n_rej;
+    if (last) break;
   }
 
   if (rank == 0 && tid < N) {
     // Node k of the path: the k-th set bit.
-    uint64_t m = on_path;
+    uint64_t m = s_path;
+    const int n = __popcll(m);
     for (int i = 0; i < tid && m; ++i) m &= m - 1;
     p.path[node0 + tid] = m ? __ffsll((long long)m) - 1 : -1;
-    if (tid == 0) p.count[b] = n_path;
+    if (tid == 0) p.count[b] = n;
   }
 
   // The next token.
-  if (n_sum != n_rej) mass_of(n_rej);
-  double total = 0.0;
-#pragma unroll
-  for (int i = 0; i < vf::CLUSTER; ++i) total += s_cta[(pass - 1) & 1][i];
-  if (!(total > 0.0) && n_rej > 0) {  // nothing left: the target's own row
+  Pair total = total_of();
+  if (!(total.hi > 0.f) && n_rej > 0) {  // nothing left: the target's own row
     n_rej = 0;
-    total = mass_of(0);
+    __syncthreads();  // (s_warp is still being read)
+    mass_of(cur, 0);
+    total = total_of();
   }
-  if (!(total > 0.0)) {
+  if (!(total.hi > 0.f)) {
     if (rank == 0 && tid == 0) p.next[b] = -1;
     return;
   }
-  const double aim = (double)s_u[0] * total;
+  const Pair aim = mul(Pair{s_u[0], 0.f}, total);
   // The CTA and warp whose part of the row the aim falls in: the first whose
   // cumulative sum exceeds it, else (u of 1, or the last rounding) the last
   // that holds anything.
-  double before = 0.0, run = 0.0;
+  Pair before{0.f, 0.f}, run{0.f, 0.f};
   int at = -1;
-#pragma unroll
-  for (int i = 0; i < vf::CLUSTER; ++i) {
-    const double s = s_cta[(pass - 1) & 1][i];
-    if (s > 0.0 && (at < 0 || !(run > aim))) {
+  for (int i = 0; i < CL; ++i) {
+    const Pair s = s_cta[pass & 1][i];
+    if (s.hi > 0.f && (at < 0 || !above(run, aim))) {
       at = i;
       before = run;
     }
-    run += s;
+    run = add(run, s);
   }
   if (at != rank) return;
   run = before;
   at = -1;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < vf::WARPS; ++i) {
-    const double s = s_warp[i];
-    if (s > 0.0 && (at < 0 || !(run > aim))) {
+    const Pair s = s_warp[i];
+    if (s.hi > 0.f && (at < 0 || !above(run, aim))) {
       at = i;
       before = run;
     }
-    run += s;
+    run = add(run, s);
   }
   if (at != warp) return;
+  // Blocks of 128 tokens, four per lane, several at once.
   const Rejected rj{n_rej, s_mass, s_rej};
   const float* pr = p.p + (node0 + cur) * V;
   const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-  int found = -1, last = -1;
-  for (int v = va; v < vb && found < 0; v += 32) {
-    const int x = v + lane;
-    Pair r{0.f, 0.f};
-    if (x < vb) r = left_of<DRAFT>(pr[x], DRAFT ? qr[x] : 0.f, x, rj);
-    double inc = (double)r.hi + (double)r.lo;
+  auto four = [&](float4 a, float4 d, int v, Pair (&r)[4]) {
+    const float x[4] = {a.x, a.y, a.z, a.w}, y[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+    for (int e = 0; e < 4; ++e)
+      r[e] = n_rej == 0 ? left_of<DRAFT, 0>(x[e], y[e], v + e, rj)
+                        : left_of<DRAFT, 2>(x[e], y[e], v + e, rj);
+  };
+  constexpr int BLK = 4;
+  int found = -1, last_v = -1;  // first token of the lane's four
+  for (int w0 = va; w0 < vb && found < 0; w0 += 128 * BLK) {
+    float4 a[BLK], d[BLK];
+    Pair inc[BLK];
+    bool some[BLK];
+#pragma unroll
+    for (int i = 0; i < BLK; ++i) {
+      const int v = w0 + i * 128 + lane * 4;
+      a[i] = load4<VEC>(pr, v, vb);
+      d[i] = DRAFT && n_rej > 0 ? load4<VEC>(qr, v, vb) : a[i];
     }
-    const uint32_t some = __ballot_sync(0xffffffffu, r.hi > 0.f);
-    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > aim) & some;
-    if (past) found = v + __ffs(past) - 1;
-    if (some) last = v + 31 - __clz(some);
-    before += __shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll
+    for (int i = 0; i < BLK; ++i) {
+      Pair r[4];
+      four(a[i], d[i], w0 + i * 128 + lane * 4, r);
+      inc[i] = add(add(r[0], r[1]), add(r[2], r[3]));
+      some[i] = inc[i].hi > 0.f;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < BLK; ++i) {
+        const Pair y = shfl_up(inc[i], o);
+        if (lane >= o) inc[i] = add(y, inc[i]);
+      }
+#pragma unroll
+    for (int i = 0; i < BLK; ++i) {
+      const uint32_t any = __ballot_sync(0xffffffffu, some[i]);
+      const uint32_t past = __ballot_sync(0xffffffffu, above(add(before, inc[i]), aim)) & any;
+      if (any) last_v = w0 + i * 128 + (31 - __clz(any)) * 4;
+      if (past && found < 0) {
+        const int l = __ffs(past) - 1;
+        found = w0 + i * 128 + l * 4;
+        // What comes before that lane's four.
+        const Pair up = shfl(inc[i], l > 0 ? l - 1 : 0);
+        if (l > 0) before = add(before, up);
+      }
+      const Pair tot = shfl(inc[i], 31);
+      if (found < 0) before = add(before, tot);
+    }
   }
-  if (lane == 0) p.next[b] = found >= 0 ? found : last;
+  if (lane == 0) {
+    const int v = found >= 0 ? found : last_v;
+    Pair r[4];
+    four(load4<VEC>(pr, v, vb), DRAFT ? load4<VEC>(qr, v, vb) : make_float4(0.f, 0.f, 0.f, 0.f), v,
+         r);
+    int pick = v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // The first that passes the aim; the last with mass where rounding (or a
+      // missing aim) leaves none.
+      const bool open = found < 0 || !above(before, aim);
+      if (r[e].hi > 0.f && open) pick = v + e;
+      before = add(before, r[e]);
+    }
+    p.next[b] = pick;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -413,16 +545,20 @@ __global__ void __launch_bounds__(cp::THREADS)
 
 template <typename P>
 static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, cudaStream_t stream,
-                                    const P& p) {
-  cudaLaunchAttribute attr[1];
+                                    const P& p, int cluster = 0) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -467,17 +603,20 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   p.next = next_token;
   p.N = N;
   p.V = V;
-  const int parts = fa::vf::CLUSTER * fa::vf::WARPS;
+  // As many CTAs per sequence as leave all of them resident at once.
+  const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
+  p.cluster = fa::vf::CLUSTER;
+  while (p.cluster > 1 && (long long)B * p.cluster > (long long)sms * fa::vf::BLOCKS_PER_SM)
+    p.cluster /= 2;
+  const int parts = p.cluster * fa::vf::WARPS;
   p.part = ((V + parts - 1) / parts + 127) / 128 * 128;
   const bool vec = V % 4 == 0 && al(target_probs, 16) && (!draft_probs || al(draft_probs, 16));
-  const dim3 grid((unsigned)B * fa::vf::CLUSTER);
-  cudaError_t e;
-  if (draft_probs)
-    e = vec ? fa::launch_dependent(fa::verify_kernel<true, true>, grid, fa::vf::THREADS, stream, p)
-            : fa::launch_dependent(fa::verify_kernel<true, false>, grid, fa::vf::THREADS, stream, p);
-  else
-    e = vec ? fa::launch_dependent(fa::verify_kernel<false, true>, grid, fa::vf::THREADS, stream, p)
-            : fa::launch_dependent(fa::verify_kernel<false, false>, grid, fa::vf::THREADS, stream, p);
+  const dim3 grid((unsigned)B * p.cluster);
+  void (*kernel)(fa::VerifyParams) =
+      draft_probs ? (vec ? fa::verify_kernel<true, true> : fa::verify_kernel<true, false>)
+                  : (vec ? fa::verify_kernel<false, true> : fa::verify_kernel<false, false>);
+  const cudaError_t e =
+      fa::launch_dependent(kernel, grid, fa::vf::THREADS, stream, p, p.cluster);
   return fa::record_cuda_status(e, "tree verification launch");
 }
 
