@@ -19,13 +19,19 @@
 // Layout: a head is D/16 lanes with two 16-byte chunks each, so that both
 // elements of every pair sit in one lane (no exchange for the rotation; the
 // mean takes log2(D/16) shuffles), and a warp holds 4 (D = 128) or 8 heads of
-// one token.  A warp keeps one token's cosines and sines in registers over
-// all of that token's heads that it takes.
+// one token.  A warp keeps one token's rotation in registers, as factors with
+// the norm's weights in them, over all of that token's heads that it takes.
+//
+// Loads: a token's heads are contiguous, so each warp fetches steps of up to 16
+// (D = 128) or 32 heads by one bulk copy into a ring of its own in shared
+// memory, two steps ahead of its arithmetic: 128 to 192 KiB in flight per SM
+// whatever the arithmetic's latency.  (Loads into registers, two head groups
+// ahead, held 64 KiB: 4.6 TB/s, half of the issue slots waiting for memory.)
 //
 // Angles: positions reach 2^31, where an fp32 product p * inv_freq has no
 // correct bit left.  Each block turns inv_freq once into a 64-bit fixed-point
 // fraction of a turn; the phase p * fraction is then an integer product
-// modulo 2^64 (whole turns drop out by overflow), good to about 2^-25 turns at
+// modulo 2^64 (whole turns drop out by overflow), good to about 2^-23 turns at
 // |p| = 2^31 and to fp32 rounding below 2^28, without any 64-bit
 // floating-point work per token.
 #include <cuda_bf16.h>
@@ -43,8 +49,22 @@ __device__ unsigned int g_rope_err = 0;
 namespace rp {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int UNR = 2;  // head groups per step; a step's loads run ahead by one step
-constexpr int BLOCKS_PER_SM = 2;
+constexpr int STAGE_BYTES = 4096;
+template <int D, bool BWD>
+struct Cfg {
+  static constexpr int STAGES = BWD ? 2 : 3;  // steps in a warp's ring
+  static constexpr int BLOCKS_PER_SM = BWD ? 3 : 2;
+  // Heads of a head group (one warp's registers): lanes hold two chunks of 8
+  // elements of a head, in the gradient one.
+  static constexpr int HPW = (BWD ? 256 : 512) / D;
+  // A step fills a stage with heads (the gradient: with x and g of half as many).
+  static constexpr int UNITS = 4;  // head groups per step
+  static constexpr int HEADS = UNITS * HPW;
+  // Rings, cosines and sines of a warp's token, turn fractions, barriers.
+  static constexpr int SMEM_CS = WARPS * D * 4;
+  static constexpr int SMEM_TOTAL =
+      WARPS * STAGES * STAGE_BYTES + SMEM_CS + (D / 2) * 8 + WARPS * STAGES * 8 + 16;
+};
 }  // namespace rp
 
 template <typename T>
@@ -70,21 +90,21 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Eight elements as four pairs for the packed fp32 operations.
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 v = unpack2<T>(w[j]);
-    f[2 * j] = v.x;
-    f[2 * j + 1] = v.y;
-  }
+__device__ __forceinline__ void unpack8(const uint4& u, float2 (&f)[4]) {
+  f[0] = unpack2<T>(u.x);
+  f[1] = unpack2<T>(u.y);
+  f[2] = unpack2<T>(u.z);
+  f[3] = unpack2<T>(u.w);
 }
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                    pack2<T>(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y),
+                    pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 swap2(float2 v) { return make_float2(v.y, v.x); }
 
 // One of the tensors a launch walks: queries, keys or values.
 struct RopePart {
@@ -95,12 +115,11 @@ struct RopePart {
   long long xs;
   int H;
   int paged;
-  // Forward: the part's head groups are [first, first + units) of a token's.
-  int first, units;
-  // Gradient: blocks [b0, b0 + nb) of the grid walk the part.
+  // Forward: the part's steps are [first, first + steps) of a token's.
+  int first, steps;
+  // Gradient: blocks [b0, b0 + nb) of the grid walk the part, by tasks of its own.
   int b0, nb;
-  // A task is up to upt head groups of one token, cpt tasks per token.
-  int upt, cpt;
+  int spt, cpt;
 };
 
 struct RopeParams {
@@ -112,8 +131,9 @@ struct RopeParams {
   const int32_t* seqlens;
   int N;  // new tokens per sequence (paged)
   int page_size, max_pages, num_pages;
-  long long tokens;
-  int groups, upt, cpt;  // forward: head groups of a token, and its tasks
+  int tokens;
+  // A task is up to spt steps of one token, cpt tasks per token.
+  int steps, spt, cpt;
   int rot;
   float eps;
   float* partial;  // gradient: [blocks][D] sums of dw
@@ -158,43 +178,116 @@ __device__ __forceinline__ void load_fractions(const float* inv_freq, int n,
   __syncthreads();
 }
 
-template <int D, bool IL>
-__device__ __forceinline__ void cos_sin(const LaneMap<D, IL>& m, int rot, int pos,
-                                        const unsigned long long* sF, float (&cs)[8],
-                                        float (&sn)[8]) {
+// Whole warp: cosines and sines of a position into the warp's table (frequency
+// i's computed by one lane).
+template <int D>
+__device__ __forceinline__ void cos_sin(int rot, int pos, const unsigned long long* sF,
+                                        float2* table) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // (the table's last values have been read)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int f = m.freq(e, rot);
-    cs[e] = 1.f;
-    sn[e] = 0.f;
-    if (f >= 0) {
+  for (int i = 0; i < D / 64; ++i) {
+    const int f = lane + 32 * i;
+    if (f < rot / 2) {
       const unsigned long long ph = sF[f] * (unsigned long long)(long long)pos;
       // Signed fraction of a turn in [-1/2, 1/2), times two: half turns.
-      sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &sn[e], &cs[e]);
+      float2 v;
+      sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &v.y, &v.x);
+      table[f] = v;
     }
   }
+  __syncwarp();
+}
+// Frequency f's, or 1 and 0 for elements that pass through (f < 0).
+__device__ __forceinline__ float2 cos_sin_of(const float2* table, int f) {
+  return f >= 0 ? table[f] : make_float2(1.f, 0.f);
 }
 
-// Pair e of a lane's 16 elements, as (first, second).
+// The rotation as two products per output, o0 = x0 c0 + y0 s0 and o1 = x1 c1 +
+// y1 s1, y the other element of each pair: for pairs across the chunks y0 = x1
+// and y1 = x0, for neighbours the swapped x0 and x1.  The norm's weights go
+// into the factors once per token.
 template <bool IL>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
-                                     const float (&sn)[8], float sign) {
+struct Turn {
+  float2 c0[4], s0[4], c1[4], s1[4];
+  __device__ __forceinline__ void set(const float (&cs)[8], const float (&sn)[8],
+                                      const float2 (&wa)[4], const float2 (&wb)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float s = sign * sn[e];
-    if constexpr (IL) {
-      float(&v)[8] = e < 4 ? a : b;
-      const int k = 2 * (e & 3);
-      const float p = v[k], q = v[k + 1];
-      v[k] = p * cs[e] - q * s;
-      v[k + 1] = q * cs[e] + p * s;
-    } else {
-      const float p = a[e], q = b[e];
-      a[e] = p * cs[e] - q * s;
-      b[e] = q * cs[e] + p * s;
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (IL) {
+        c0[e] = make_float2(wa[e].x * cs[e], wa[e].y * cs[e]);
+        s0[e] = make_float2(-wa[e].y * sn[e], wa[e].x * sn[e]);
+        c1[e] = make_float2(wb[e].x * cs[e + 4], wb[e].y * cs[e + 4]);
+        s1[e] = make_float2(-wb[e].y * sn[e + 4], wb[e].x * sn[e + 4]);
+      } else {
+        const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]);
+        const float2 n = make_float2(sn[2 * e], sn[2 * e + 1]);
+        c0[e] = __fmul2_rn(wa[e], c);
+        s0[e] = make_float2(-wb[e].x * n.x, -wb[e].y * n.y);
+        c1[e] = __fmul2_rn(wb[e], c);
+        s1[e] = __fmul2_rn(wa[e], n);
+      }
     }
   }
-}
+  // a, b: the lane's chunks, turned and scaled by r.
+  __device__ __forceinline__ void apply(float2 (&a)[4], float2 (&b)[4], float r) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 y0 = IL ? swap2(a[e]) : b[e], y1 = IL ? swap2(b[e]) : a[e];
+      a[e] = __fmul2_rn(__ffma2_rn(a[e], c0[e], __fmul2_rn(y0, s0[e])), both(r));
+      b[e] = __fmul2_rn(__ffma2_rn(b[e], c1[e], __fmul2_rn(y1, s1[e])), both(r));
+    }
+  }
+};
+
+// The gradient's lanes hold one chunk each, so its rotation (back, by the
+// negative angle) is o = x c + y s with y the chunk that holds the pairs' other
+// elements (neighbours: x swapped), read from the ring as well: half the
+// registers, twice the warps, for one more load.
+template <int D, bool IL>
+struct BackMap {
+  static constexpr int LPH = D / 8;
+  int sub, c, other;  // head of the group, chunk, the other elements' chunk
+  float sign;
+  int f0;  // first frequency, or -1
+  __device__ __forceinline__ BackMap(int lane, int rot) {
+    sub = lane / LPH;
+    c = lane % LPH;
+    other = c;
+    sign = 1.f;
+    f0 = -1;
+    if (c * 8 >= rot) return;
+    if constexpr (IL) {
+      f0 = c * 4;
+    } else {
+      const int rc = rot / 16;
+      const bool second = c >= rc;
+      other = second ? c - rc : c + rc;
+      sign = second ? -1.f : 1.f;
+      f0 = (second ? other : c) * 8;
+    }
+  }
+};
+template <bool IL>
+struct TurnBack {
+  float2 c[4], s[4];
+  template <typename MAP>
+  __device__ __forceinline__ void set(const float2* table, const MAP& m) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (IL) {
+        const float2 v = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + e);
+        c[e] = both(v.x);
+        s[e] = make_float2(v.y, -v.y);
+      } else {
+        const float2 v = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + 2 * e);
+        const float2 w = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + 2 * e + 1);
+        c[e] = make_float2(v.x, w.x);
+        s[e] = make_float2(m.sign * v.y, m.sign * w.y);
+      }
+    }
+  }
+};
 
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
@@ -206,34 +299,75 @@ __device__ __forceinline__ float head_sum(float v) {
 // A warp's place in its tasks: warps take tasks in a grid stride, a step at a
 // time.  (The stride is added as whole tokens and tasks: no division per task.)
 struct RopeWalk {
-  long long t;  // token
+  int t;        // token
   int c;        // task of the token
-  int u;        // head group
-  __device__ __forceinline__ RopeWalk(long long w, int cpt, int upt) {
+  int s;        // step of the token
+  __device__ __forceinline__ RopeWalk(int w, int cpt, int spt) {
     t = w / cpt;
-    c = (int)(w - t * cpt);
-    u = c * upt;
+    c = w - t * cpt;
+    s = c * spt;
   }
-  __device__ __forceinline__ int end(int upt, int groups) const {
-    const int e = (c + 1) * upt;
-    return e < groups ? e : groups;
-  }
-  __device__ __forceinline__ void next_task(int cpt, int upt, long long dt, int dc) {
+  __device__ __forceinline__ void next(int cpt, int spt, int steps, int dt, int dc) {
+    ++s;
+    if (s < steps && s < (c + 1) * spt) return;
     t += dt;
     c += dc;
     if (c >= cpt) {
       c -= cpt;
       ++t;
     }
-    u = c * upt;
+    s = c * spt;
   }
 };
+
+// Untiled bulk copy into shared memory; addresses and size are multiples of 16.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// A lane's 16 bytes of a head in its ring.
+__device__ __forceinline__ uint4 ring_load(const uint8_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+// Shared memory of a block and of one of its warps.
+template <int D, bool BWD>
+struct RopeSmem {
+  uint8_t* ring;
+  float2* table;
+  unsigned long long* frac;
+  uint64_t* full;
+  volatile int* abort_flag;
+  using C = rp::Cfg<D, BWD>;
+  __device__ __forceinline__ RopeSmem(uint8_t* smem, int warp) {
+    ring = smem + warp * C::STAGES * rp::STAGE_BYTES;
+    uint8_t* q = smem + rp::WARPS * C::STAGES * rp::STAGE_BYTES;
+    table = reinterpret_cast<float2*>(q) + warp * (D / 2);
+    q += C::SMEM_CS;
+    frac = reinterpret_cast<unsigned long long*>(q);
+    q += (D / 2) * 8;
+    full = reinterpret_cast<uint64_t*>(q) + warp * C::STAGES;
+    q += rp::WARPS * C::STAGES * 8;
+    abort_flag = reinterpret_cast<volatile int*>(q);
+  }
+};
+
+// After an abort: the warp's loads in flight land before its block goes.
+template <int STAGES>
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t done, uint32_t issued) {
+  for (uint32_t k = done; k < issued; ++k) mbar_wait_drain(&full[k % STAGES], (k / STAGES) & 1);
+  __syncwarp();
+}
 
 // Cache row of token t (slot seqlens[b] - N + s), in rows of the pool, or -1
 // (a padding sequence, or a length or page id out of range, which sets the
 // bounds bit); *slot receives the position in the sequence.
-__device__ __forceinline__ long long cache_row(const RopeParams& p, long long t, int* slot) {
-  const int b = (int)(t / p.N), s = (int)(t - (long long)b * p.N);
+__device__ __forceinline__ long long cache_row(const RopeParams& p, int t, int* slot) {
+  const int b = t / p.N, s = t - b * p.N;
   const int L = p.seqlens[b];
   *slot = L - p.N + s;
   if (L < p.N) return -1;
@@ -250,242 +384,263 @@ __device__ __forceinline__ long long cache_row(const RopeParams& p, long long t,
   return (long long)pid * p.page_size + (*slot - pg * p.page_size);
 }
 
-// HPW heads of one token make a head group; a token's groups are its query
-// heads', then its keys', then (paged) its values'.  Each warp keeps one step of
-// UNR groups in registers while the next step's loads are on their way, across
-// the ends of its tasks too.
+// A token's steps are its query heads', then its keys', then (paged) its
+// values'.
 template <int D, typename T, bool IL, bool PAGED>
-__global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
+__global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, false>::BLOCKS_PER_SM)
     rope_kernel(const __grid_constant__ RopeParams p) {
+  using C = rp::Cfg<D, false>;
   using M = LaneMap<D, IL>;
-  __shared__ unsigned long long sF[D / 2];
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RopeSmem<D, false> sm(smem, warp);
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&sm.full[i], 1);
+    if (warp == 0) *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31;
   const M m(lane, p.rot);
-  const long long warps = (long long)gridDim.x * rp::WARPS;
-  const long long w0 = (long long)blockIdx.x * rp::WARPS + (threadIdx.x >> 5);
-  const long long dt = warps / p.cpt;
-  const int dc = (int)(warps - dt * p.cpt);
-  RopeWalk at(w0, p.cpt, p.upt);
+  const int warps = gridDim.x * rp::WARPS;
+  const int dt = warps / p.cpt, dc = warps - dt * p.cpt;
+  RopeWalk at(blockIdx.x * rp::WARPS + warp, p.cpt, p.spt), ahead = at;
 
-  // The part of head group u.
-  auto part_of = [&](int u) {
+  auto part_of = [&](int s) {
     int i = 0;
-    if (p.n_parts > 1 && u >= p.part[1].first) i = 1;
-    if (PAGED && p.n_parts > 2 && u >= p.part[2].first) i = 2;
+    if (p.n_parts > 1 && s >= p.part[1].first) i = 1;
+    if (PAGED && p.n_parts > 2 && s >= p.part[2].first) i = 2;
     return i;
   };
-  auto load = [&](const RopeWalk& a, uint4 (&r)[rp::UNR][2], int* pos) {
-    if (a.t >= p.tokens) return;
-    const int end = a.end(p.upt, p.groups);
-#pragma unroll
-    for (int j = 0; j < rp::UNR; ++j) {
-      const int u = a.u + j;
-      if (u < end) {
-        const RopePart& pt = p.part[part_of(u)];
-        const int h = (u - pt.first) * M::HPW + m.sub;
-        if (h < pt.H) {
-          const T* x = static_cast<const T*>(pt.x) + a.t * pt.xs + (size_t)h * D;
-          r[j][0] = *reinterpret_cast<const uint4*>(x + m.c0 * 8);
-          r[j][1] = *reinterpret_cast<const uint4*>(x + m.c1 * 8);
-        }
-      }
+  // The load of step `ahead` into its stage (k: the warp's step number).
+  uint32_t issued = 0;
+  auto fetch = [&]() {
+    if (ahead.t >= p.tokens) return;
+    if (lane == 0) {
+      const RopePart& pt = p.part[part_of(ahead.s)];
+      const int h0 = (ahead.s - pt.first) * C::HEADS;
+      const uint32_t bytes = (uint32_t)(pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS) * D * 2;
+      const int st = issued % C::STAGES;
+      mbar_arrive_expect_tx(&sm.full[st], bytes);
+      bulk_load(sm.ring + st * rp::STAGE_BYTES,
+                static_cast<const T*>(pt.x) + ahead.t * pt.xs + (size_t)h0 * D, bytes,
+                &sm.full[st]);
     }
-    if (!PAGED || p.positions) *pos = p.positions[a.t];
+    ++issued;
+    ahead.next(p.cpt, p.spt, p.steps, dt, dc);
   };
+  __syncwarp();
+  for (int i = 0; i < C::STAGES; ++i) fetch();
+  int pos_n = 0;
+  if ((!PAGED || p.positions) && at.t < p.tokens) pos_n = p.positions[at.t];
+  load_fractions(p.inv_freq, p.rot / 2, sm.frac);  // (ends with the block's barrier)
 
-  uint4 cur[rp::UNR][2], nxt[rp::UNR][2];
-#pragma unroll
-  for (int j = 0; j < rp::UNR; ++j)
-    cur[j][0] = cur[j][1] = nxt[j][0] = nxt[j][1] = make_uint4(0u, 0u, 0u, 0u);
-  int pos = 0, pos_n = 0;
-  load(at, cur, &pos);
-  load_fractions(p.inv_freq, p.rot / 2, sF);
-  long long token = -1, row = 0;
-  int kind = -1;
+  int token = -1;
+  long long row = 0;
+  int kind = -1;  // the part that `turn` holds the weights of
   float cs[8], sn[8];
-  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
-  while (at.t < p.tokens) {
+  Turn<IL> turn;
+  uint32_t k = 0;
+  for (; at.t < p.tokens; ++k) {
+    const int pos = pos_n;
     RopeWalk nx = at;
-    nx.u += rp::UNR;
-    if (nx.u >= at.end(p.upt, p.groups)) nx.next_task(p.cpt, p.upt, dt, dc);
-    load(nx, nxt, &pos_n);
+    nx.next(p.cpt, p.spt, p.steps, dt, dc);
+    if ((!PAGED || p.positions) && nx.t < p.tokens) pos_n = p.positions[nx.t];
+    const int i = part_of(at.s);
+    const RopePart& pt = p.part[i];
     if (at.t != token) {  // warp-uniform, as is every branch on the walk
       token = at.t;
-      if constexpr (PAGED) {
-        int slot;
-        row = cache_row(p, token, &slot);
-        if (!p.positions) pos = slot;
-      }
-      cos_sin<D, IL>(m, p.rot, pos, sF, cs, sn);
-    }
-    const int end = at.end(p.upt, p.groups);
+      kind = -1;
+      int slot = 0;
+      if constexpr (PAGED) row = cache_row(p, token, &slot);
+      if (pt.w) {
+        cos_sin<D>(p.rot, PAGED && !p.positions ? slot : pos, sm.frac, sm.table);
 #pragma unroll
-    for (int j = 0; j < rp::UNR; ++j) {
-      const int u = at.u + j;
-      if (u >= end) break;
-      const int i = part_of(u);
-      const RopePart& pt = p.part[i];
-      const int h = (u - pt.first) * M::HPW + m.sub;
-      const bool norm = !PAGED || pt.w != nullptr;
-      if (i != kind) {
-        kind = i;
-        if (norm) {
-          wa = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8);
-          wb = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8);
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = cos_sin_of(sm.table, m.freq(e, p.rot));
+          cs[e] = v.x;
+          sn[e] = v.y;
         }
       }
-      if (norm) {
-        float a[8], b[8], w[8];
-        unpack8<T>(cur[j][0], a);
-        unpack8<T>(cur[j][1], b);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-        ss = head_sum<M::LPH>(ss);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        unpack8<T>(wa, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= r * w[e];
-        unpack8<T>(wb, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] *= r * w[e];
-        turn<IL>(a, b, cs, sn, 1.f);
-        cur[j][0] = pack8<T>(a);
-        cur[j][1] = pack8<T>(b);
-      }
-      const long long to = PAGED && pt.paged ? row : token;
-      if (h < pt.H && (!PAGED || to >= 0)) {
-        T* y = static_cast<T*>(pt.y) + (to * pt.H + h) * D;
-        *reinterpret_cast<uint4*>(y + m.c0 * 8) = cur[j][0];
-        *reinterpret_cast<uint4*>(y + m.c1 * 8) = cur[j][1];
+    }
+    float2 a[4], b[4];
+    if (i != kind) {
+      kind = i;
+      if (!PAGED || pt.w) {
+        unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8), a);
+        unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8), b);
+        turn.set(cs, sn, a, b);
       }
     }
+    const int h0 = (at.s - pt.first) * C::HEADS;
+    const int nh = pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS;
+    const long long to = PAGED && pt.paged ? row : token;
+    T* y = static_cast<T*>(pt.y) + (to * pt.H + h0 + m.sub) * D;
+    const uint8_t* x = sm.ring + (k % C::STAGES) * rp::STAGE_BYTES + m.sub * D * 2;
+    if (!mbar_wait<true>(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, sm.abort_flag,
+                         &g_rope_err, 20))
+      break;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < C::UNITS; ++u) {
+      if (u * C::HPW >= nh) break;  // warp-uniform
+      uint4 r0 = ring_load(x + u * C::HPW * D * 2 + m.c0 * 16);
+      uint4 r1 = ring_load(x + u * C::HPW * D * 2 + m.c1 * 16);
+      if (!PAGED || pt.w) {
+        unpack8<T>(r0, a);
+        unpack8<T>(r1, b);
+        float2 s2 = both(0.f), t2 = both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s2 = __ffma2_rn(a[e], a[e], s2);
+          t2 = __ffma2_rn(b[e], b[e], t2);
+        }
+        const float ss = head_sum<M::LPH>((s2.x + s2.y) + (t2.x + t2.y));
+        turn.apply(a, b, rsqrtf(ss * (1.f / D) + p.eps));
+        r0 = pack8<T>(a);
+        r1 = pack8<T>(b);
+      }
+      if (u * C::HPW + m.sub < nh && (!PAGED || to >= 0)) {
+        *reinterpret_cast<uint4*>(y + u * C::HPW * D + m.c0 * 8) = r0;
+        *reinterpret_cast<uint4*>(y + u * C::HPW * D + m.c1 * 8) = r1;
+      }
+    }
+    __syncwarp();  // the stage has been read
+    fetch();
     at = nx;
-    pos = pos_n;
-#pragma unroll
-    for (int j = 0; j < rp::UNR; ++j) {
-      cur[j][0] = nxt[j][0];
-      cur[j][1] = nxt[j][1];
-    }
   }
+  if (*sm.abort_flag) drain_ring<C::STAGES>(sm.full, k, issued);
 }
 
-// Gradient of rope_kernel.  Each block walks the queries or the keys, a head
-// group per step with the next step's loads ahead, and ends with one row of
-// partial[] (its sum of gy x r per column); the sums of a lane, a block and the
-// blocks are taken in a fixed order, so equal calls give equal bits.
+// Gradient of rope_kernel.  Each block walks the queries or the keys, and ends
+// with one row of partial[] (its sum of gy x r per column); the sums of a
+// lane, a block and the blocks are taken in a fixed order, so equal calls give
+// equal bits.
 template <int D, typename T, bool IL>
-__global__ void __launch_bounds__(rp::THREADS, rp::BLOCKS_PER_SM)
+__global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
     rope_bwd_kernel(const __grid_constant__ RopeParams p) {
-  using M = LaneMap<D, IL>;
-  __shared__ unsigned long long sF[D / 2];
-  __shared__ float sW[rp::WARPS][D];
+  using C = rp::Cfg<D, true>;
+  using M = BackMap<D, IL>;
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
-  pdl_wait_primary();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RopeSmem<D, true> sm(smem, warp);
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&sm.full[i], 1);
+    if (warp == 0) *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait_primary();
   const M m(lane, p.rot);
   const RopePart& pt = p.part[p.n_parts > 1 && (int)blockIdx.x >= p.part[1].b0 ? 1 : 0];
-  const T* x = static_cast<const T*>(pt.x);
-  const T* g = static_cast<const T*>(pt.g);
-  T* dx = static_cast<T*>(pt.y);
-  const long long warps = (long long)pt.nb * rp::WARPS;
-  const long long dt = warps / pt.cpt;
-  const int dc = (int)(warps - dt * pt.cpt);
-  RopeWalk at((long long)(blockIdx.x - pt.b0) * rp::WARPS + warp, pt.cpt, pt.upt);
-
-  auto load = [&](const RopeWalk& q, uint4 (&r)[4], int* pos) {
-    const int h = q.u * M::HPW + m.sub;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = make_uint4(0u, 0u, 0u, 0u);
-    if (q.t >= p.tokens) return;
-    if (h < pt.H) {
-      const T* xt = x + q.t * pt.xs + (size_t)h * D;
-      const T* gt = g + (q.t * pt.H + h) * D;
-      r[0] = *reinterpret_cast<const uint4*>(xt + m.c0 * 8);
-      r[1] = *reinterpret_cast<const uint4*>(xt + m.c1 * 8);
-      r[2] = *reinterpret_cast<const uint4*>(gt + m.c0 * 8);
-      r[3] = *reinterpret_cast<const uint4*>(gt + m.c1 * 8);
+  const int warps = pt.nb * rp::WARPS;
+  const int dt = warps / pt.cpt, dc = warps - dt * pt.cpt;
+  RopeWalk at((blockIdx.x - pt.b0) * rp::WARPS + warp, pt.cpt, pt.spt), ahead = at;
+  uint32_t issued = 0;
+  // x in the first half of the stage, g in the second.
+  auto fetch = [&]() {
+    if (ahead.t >= p.tokens) return;
+    if (lane == 0) {
+      const int h0 = ahead.s * C::HEADS;
+      const uint32_t bytes = (uint32_t)(pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS) * D * 2;
+      const int st = issued % C::STAGES;
+      uint8_t* to = sm.ring + st * rp::STAGE_BYTES;
+      mbar_arrive_expect_tx(&sm.full[st], 2 * bytes);
+      bulk_load(to, static_cast<const T*>(pt.x) + ahead.t * pt.xs + (size_t)h0 * D, bytes,
+                &sm.full[st]);
+      bulk_load(to + rp::STAGE_BYTES / 2,
+                static_cast<const T*>(pt.g) + ((long long)ahead.t * pt.H + h0) * D, bytes, &sm.full[st]);
     }
-    *pos = p.positions[q.t];
+    ++issued;
+    ahead.next(pt.cpt, pt.spt, pt.steps, dt, dc);
   };
-  uint4 cur[4], nxt[4];
-  int pos = 0, pos_n = 0;
-  load(at, cur, &pos);
-  const uint4 wa = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8);
-  const uint4 wb = *reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8);
-  load_fractions(p.inv_freq, p.rot / 2, sF);
-  float acc0[8], acc1[8];
+  __syncwarp();
+  for (int i = 0; i < C::STAGES; ++i) fetch();
+  int pos_n = at.t < p.tokens ? p.positions[at.t] : 0;
+  float2 w[4];
+  unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c * 8), w);
+  load_fractions(p.inv_freq, p.rot / 2, sm.frac);
+  float2 acc[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc0[e] = acc1[e] = 0.f;
-  long long token = -1;
-  float cs[8], sn[8];
-  while (at.t < p.tokens) {
+  for (int e = 0; e < 4; ++e) acc[e] = both(0.f);
+  int token = -1;
+  TurnBack<IL> back;
+  uint32_t k = 0;
+  for (; at.t < p.tokens; ++k) {
+    const int pos = pos_n;
     RopeWalk nx = at;
-    if (++nx.u >= at.end(pt.upt, pt.units)) nx.next_task(pt.cpt, pt.upt, dt, dc);
-    load(nx, nxt, &pos_n);
-    const int h = at.u * M::HPW + m.sub;
-    float a[8], b[8], ga[8], gb[8], w[8];
+    nx.next(pt.cpt, pt.spt, pt.steps, dt, dc);
+    if (nx.t < p.tokens) pos_n = p.positions[nx.t];
     if (at.t != token) {
       token = at.t;
-      cos_sin<D, IL>(m, p.rot, pos, sF, cs, sn);
+      cos_sin<D>(p.rot, pos, sm.frac, sm.table);
+      back.set(sm.table, m);
     }
-    unpack8<T>(cur[2], ga);
-    unpack8<T>(cur[3], gb);
-    turn<IL>(ga, gb, cs, sn, -1.f);
-    unpack8<T>(cur[0], a);
-    unpack8<T>(cur[1], b);
-    float ss = 0.f, dot = 0.f;
-    unpack8<T>(wa, w);
+    const int h0 = at.s * C::HEADS;
+    const int nh = pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS;
+    T* dst = static_cast<T*>(pt.y) + ((long long)token * pt.H + h0 + m.sub) * D;
+    const uint8_t* x = sm.ring + (k % C::STAGES) * rp::STAGE_BYTES + m.sub * D * 2;
+    if (!mbar_wait<true>(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, sm.abort_flag,
+                         &g_rope_err, 21))
+      break;
+    __syncwarp();
+#pragma unroll 1
+    for (int u = 0; u < C::UNITS; ++u) {
+      if (u * C::HPW >= nh) break;  // warp-uniform
+      // (A lane past the last head works on what its ring holds, and its
+      // terms are left out of the weights' sums.)
+      const bool real = u * C::HPW + m.sub < nh;
+      const uint8_t* xu = x + u * C::HPW * D * 2;
+      const uint8_t* gu = xu + rp::STAGE_BYTES / 2;
+      float2 a[4], g[4], y[4];
+      unpack8<T>(ring_load(xu + m.c * 16), a);
+      unpack8<T>(ring_load(gu + m.c * 16), g);
+      if constexpr (!IL) unpack8<T>(ring_load(gu + m.other * 16), y);
+      float2 s2 = both(0.f), d2 = both(0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ss += a[e] * a[e] + b[e] * b[e];
-      dot += a[e] * (w[e] * ga[e]);
+      for (int e = 0; e < 4; ++e) {
+        g[e] = __ffma2_rn(g[e], back.c[e], __fmul2_rn(IL ? swap2(g[e]) : y[e], back.s[e]));
+        y[e] = __fmul2_rn(g[e], a[e]);
+        s2 = __ffma2_rn(a[e], a[e], s2);
+        d2 = __ffma2_rn(y[e], w[e], d2);
+      }
+      float ss = s2.x + s2.y, dot = d2.x + d2.y;
+#pragma unroll
+      for (int o = M::LPH / 2; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      }
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+      const float nf = -dot * (1.f / D) * r * r;  // -r^2 mean(x w gy)
+      if (real) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[e] = __ffma2_rn(y[e], both(r), acc[e]);
+          a[e] = __fmul2_rn(__ffma2_rn(a[e], both(nf), __fmul2_rn(w[e], g[e])), both(r));
+        }
+        *reinterpret_cast<uint4*>(dst + u * C::HPW * D + m.c * 8) = pack8<T>(a);
+      }
     }
-    unpack8<T>(wb, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dot += b[e] * (w[e] * gb[e]);
-    ss = head_sum<M::LPH>(ss);
-    dot = head_sum<M::LPH>(dot);
-    const float r = rsqrtf(ss * (1.f / D) + p.eps);
-    const float f = dot * (1.f / D) * r * r;  // r^2 mean(x w gy)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      acc0[e] += ga[e] * (a[e] * r);
-      acc1[e] += gb[e] * (b[e] * r);
-      b[e] = r * (w[e] * gb[e] - b[e] * f);
-    }
-    unpack8<T>(wa, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = r * (w[e] * ga[e] - a[e] * f);
-    if (h < pt.H) {
-      T* d = dx + (token * pt.H + h) * D;
-      *reinterpret_cast<uint4*>(d + m.c0 * 8) = pack8<T>(a);
-      *reinterpret_cast<uint4*>(d + m.c1 * 8) = pack8<T>(b);
-    }
+    __syncwarp();  // the stage has been read
+    fetch();
     at = nx;
-    pos = pos_n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cur[e] = nxt[e];
   }
+  if (*sm.abort_flag) drain_ring<C::STAGES>(sm.full, k, issued);
+  __syncthreads();  // the rings have been read: they take the block's sums
+  float* sW = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    float v = e & 1 ? acc[e >> 1].y : acc[e >> 1].x;
 #pragma unroll
-    for (int o = M::LPH; o < 32; o <<= 1) {  // the lanes of the warp's other heads
-      acc0[e] += __shfl_xor_sync(0xffffffffu, acc0[e], o);
-      acc1[e] += __shfl_xor_sync(0xffffffffu, acc1[e], o);
-    }
-    if (m.sub == 0) {
-      sW[warp][m.c0 * 8 + e] = acc0[e];
-      sW[warp][m.c1 * 8 + e] = acc1[e];
-    }
+    for (int o = M::LPH; o < 32; o <<= 1)  // the lanes of the warp's other heads
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (m.sub == 0) sW[warp * D + m.c * 8 + e] = v;
   }
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < rp::WARPS; ++i) s += sW[i][threadIdx.x];
+    for (int i = 0; i < rp::WARPS; ++i) s += sW[i * D + threadIdx.x];
     p.partial[(size_t)blockIdx.x * D + threadIdx.x] = s;
   }
 }
@@ -514,47 +669,49 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Head groups per task: the fewest rounds of the resident warps, a round
-// costing its groups and, once, the token's cosines and sines (about as much
-// as two groups).
-static void plan_tasks(long long tokens, int groups, long long warps, int* upt, int* cpt) {
+// Steps per task: the fewest rounds of the resident warps, a round costing its
+// steps and, once, the token's cosines, sines and factors (about as much as
+// half a step).
+static void plan_tasks(int tokens, int steps, long long warps, int* spt, int* cpt) {
   long long best = 0;
-  for (int c = 1; c <= groups && c <= 64; ++c) {
-    const int u = (groups + c - 1) / c;
-    if ((groups + u - 1) / u != c) continue;
-    const long long cost = (tokens * c + warps - 1) / warps * (u + 2);
+  for (int c = 1; c <= steps && c <= 64; ++c) {
+    const int u = (steps + c - 1) / c;
+    if ((steps + u - 1) / u != c) continue;
+    const long long cost = ((long long)tokens * c + warps - 1) / warps * (2 * u + 1);
     if (best == 0 || cost < best) {
       best = cost;
-      *upt = u;
+      *spt = u;
       *cpt = c;
     }
   }
 }
 
-// Head groups, tasks and blocks.  Returns the grid size.
+// Steps, tasks and blocks.  Returns the grid size.
 static int plan_parts(RopeParams* p, int D, bool bwd) {
-  const int hpw = 32 / (D / 16);
+  const int heads = bwd ? rp::Cfg<128, true>::HEADS * 128 / D : rp::Cfg<128, false>::HEADS * 128 / D;
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  const long long slots = (long long)sms * rp::BLOCKS_PER_SM;  // resident blocks
-  long long groups = 0;
+  const long long slots =  // resident blocks
+      (long long)sms * (bwd ? rp::Cfg<128, true>::BLOCKS_PER_SM : rp::Cfg<128, false>::BLOCKS_PER_SM);
+  long long steps = 0, all_heads = 0;
   for (int i = 0; i < p->n_parts; ++i) {
     RopePart& t = p->part[i];
-    t.units = (t.H + hpw - 1) / hpw;
-    t.first = (int)groups;
-    groups += t.units;
+    t.steps = (t.H + heads - 1) / heads;
+    t.first = (int)steps;
+    steps += t.steps;
+    all_heads += t.H;
   }
   if (bwd) {
-    // Blocks in proportion to the parts' head groups, all resident at once.
+    // Blocks in proportion to the parts' heads, all resident at once.
     long long left = slots;
     int b0 = 0;
     for (int i = 0; i < p->n_parts; ++i) {
       RopePart& t = p->part[i];
-      long long nb = i + 1 < p->n_parts ? (slots * t.units + groups / 2) / groups : left;
+      long long nb = i + 1 < p->n_parts ? (slots * t.H + all_heads / 2) / all_heads : left;
       if (nb > left - (p->n_parts - 1 - i)) nb = left - (p->n_parts - 1 - i);
       if (nb < 1) nb = 1;
       left -= nb;
-      plan_tasks(p->tokens, t.units, nb * rp::WARPS, &t.upt, &t.cpt);
-      const long long need = (p->tokens * t.cpt + rp::WARPS - 1) / rp::WARPS;
+      plan_tasks(p->tokens, t.steps, nb * rp::WARPS, &t.spt, &t.cpt);
+      const long long need = ((long long)p->tokens * t.cpt + rp::WARPS - 1) / rp::WARPS;
       if (nb > need) nb = need;
       t.b0 = b0;
       t.nb = (int)nb;
@@ -562,14 +719,14 @@ static int plan_parts(RopeParams* p, int D, bool bwd) {
     }
     return b0;
   }
-  p->groups = (int)groups;
-  plan_tasks(p->tokens, p->groups, slots * rp::WARPS, &p->upt, &p->cpt);
-  const long long need = (p->tokens * p->cpt + rp::WARPS - 1) / rp::WARPS;
+  p->steps = (int)steps;
+  plan_tasks(p->tokens, p->steps, slots * rp::WARPS, &p->spt, &p->cpt);
+  const long long need = ((long long)p->tokens * p->cpt + rp::WARPS - 1) / rp::WARPS;
   return (int)(need < slots ? need : slots);
 }
 
 template <typename... Args>
-static cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads,
+static cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, int smem,
                               cudaStream_t stream, Args... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -577,33 +734,48 @@ static cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// kind: 0 contiguous outputs, 1 pages, 2 gradient.
 template <int D, typename T>
-static int launch_rope_t(const RopeParams& p, int blocks, bool paged, bool bwd, bool il,
-                         cudaStream_t s) {
-  if (bwd)
-    return il ? launch_pdl(rope_bwd_kernel<D, T, true>, dim3(blocks), rp::THREADS, s, p)
-              : launch_pdl(rope_bwd_kernel<D, T, false>, dim3(blocks), rp::THREADS, s, p);
-  if (paged)
-    return il ? launch_pdl(rope_kernel<D, T, true, true>, dim3(blocks), rp::THREADS, s, p)
-              : launch_pdl(rope_kernel<D, T, false, true>, dim3(blocks), rp::THREADS, s, p);
-  return il ? launch_pdl(rope_kernel<D, T, true, false>, dim3(blocks), rp::THREADS, s, p)
-            : launch_pdl(rope_kernel<D, T, false, false>, dim3(blocks), rp::THREADS, s, p);
+static int launch_rope_t(const RopeParams& p, int blocks, int kind, bool il, cudaStream_t s) {
+  void (*const kernels[6])(RopeParams) = {
+      rope_kernel<D, T, false, false>, rope_kernel<D, T, true, false>,
+      rope_kernel<D, T, false, true>,  rope_kernel<D, T, true, true>,
+      rope_bwd_kernel<D, T, false>,    rope_bwd_kernel<D, T, true>};
+  auto smem = [](int k) {
+    return k < 4 ? rp::Cfg<D, false>::SMEM_TOTAL : rp::Cfg<D, true>::SMEM_TOTAL;
+  };
+  static int attr_set[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE)) {
+    for (int k = 0; k < 6; ++k) {
+      e = cudaFuncSetAttribute(kernels[k], cudaFuncAttributeMaxDynamicSharedMemorySize, smem(k));
+      if (e != cudaSuccess) return e;
+    }
+    if (dev >= 0 && dev < 64) __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
+  }
+  const int k = 2 * kind + (il ? 1 : 0);
+  return launch_pdl(kernels[k], dim3(blocks), rp::THREADS, smem(k), s, p);
 }
 
-static int launch_rope(const RopeParams& p, int blocks, int D, bool bf16, bool paged, bool bwd,
-                       bool il, cudaStream_t s) {
+static int launch_rope(const RopeParams& p, int blocks, int D, bool bf16, int kind, bool il,
+                       cudaStream_t s) {
   if (D == 64)
-    return bf16 ? launch_rope_t<64, __nv_bfloat16>(p, blocks, paged, bwd, il, s)
-                : launch_rope_t<64, __half>(p, blocks, paged, bwd, il, s);
-  return bf16 ? launch_rope_t<128, __nv_bfloat16>(p, blocks, paged, bwd, il, s)
-              : launch_rope_t<128, __half>(p, blocks, paged, bwd, il, s);
+    return bf16 ? launch_rope_t<64, __nv_bfloat16>(p, blocks, kind, il, s)
+                : launch_rope_t<64, __half>(p, blocks, kind, il, s);
+  return bf16 ? launch_rope_t<128, __nv_bfloat16>(p, blocks, kind, il, s)
+              : launch_rope_t<128, __half>(p, blocks, kind, il, s);
 }
+
+int set_rope_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
 
 int read_rope_error(unsigned int* out, int reset) {
   unsigned int v = 0;
@@ -631,8 +803,8 @@ bool rope_sizes_ok(long long T, int Hq, int Hkv, int D, int rot, float eps, int 
   if (rot < 16 || rot > D || rot % 16 != 0) return false;
   if (!isfinite(eps) || !(eps > 0.f)) return false;
   if (dtype != FA_BF16 && dtype != FA_FP16) return false;
-  // Work indexes (tasks) and element offsets stay far inside 63 bits.
-  if (T > (1ll << 40) || Hq > (1 << 20) || Hkv > (1 << 20)) return false;
+  // Token indexes fit 31 bits with room for the warps' stride.
+  if (T > INT32_MAX - (1 << 20) || Hq > (1 << 20) || Hkv > (1 << 20)) return false;
   return true;
 }
 
@@ -673,12 +845,12 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
   if (Hkv) p.part[p.n_parts++] = part(k, k_stride, Hkv, k_weight, k_out, nullptr, false);
   p.inv_freq = inv_freq;
   p.positions = positions;
-  p.tokens = T;
+  p.tokens = (int)T;
   p.rot = rot_dim;
   p.eps = eps;
   const int blocks = fa::plan_parts(&p, D, false);
   return fa::record_cuda_status(
-      fa::launch_rope(p, blocks, D, dtype == FA_BF16, false, false, interleaved != 0, stream),
+      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 0, interleaved != 0, stream),
       "norm and rotation launch");
 }
 
@@ -720,12 +892,12 @@ extern "C" int fa_qk_norm_rope_append(const void* q, const void* k, const void* 
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
-  p.tokens = (long long)B * N;
+  p.tokens = B * N;
   p.rot = rot_dim;
   p.eps = eps;
   const int blocks = fa::plan_parts(&p, D, false);
   return fa::record_cuda_status(
-      fa::launch_rope(p, blocks, D, dtype == FA_BF16, true, false, interleaved != 0, stream),
+      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 1, interleaved != 0, stream),
       "norm, rotation and append launch");
 }
 
@@ -764,7 +936,7 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
   }
   p.inv_freq = inv_freq;
   p.positions = positions;
-  p.tokens = T;
+  p.tokens = (int)T;
   p.rot = rot_dim;
   p.eps = eps;
   const int blocks = fa::plan_parts(&p, D, true);
@@ -772,9 +944,9 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
   e = fa::scratch_alloc(&scratch, (size_t)blocks * D * sizeof(float), stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "norm and rotation gradient scratch");
   p.partial = static_cast<float*>(scratch);
-  int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, false, true, interleaved != 0, stream);
+  int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, 2, interleaved != 0, stream);
   if (r == 0)
-    r = fa::launch_pdl(fa::rope_dw_kernel, dim3(D / 32, 2), 256, stream,
+    r = fa::launch_pdl(fa::rope_dw_kernel, dim3(D / 32, 2), 256, 0, stream,
                        (const float*)p.partial, D, iq >= 0 ? p.part[iq].b0 : 0,
                        iq >= 0 ? p.part[iq].nb : 0, iq >= 0 ? dq_weight : (float*)nullptr,
                        ik >= 0 ? p.part[ik].b0 : 0, ik >= 0 ? p.part[ik].nb : 0,

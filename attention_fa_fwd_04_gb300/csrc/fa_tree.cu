@@ -55,7 +55,14 @@ struct Cfg {
   // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).
   static constexpr int THREADS = MT == 1 ? 192 : 384;
   static constexpr int RT = MT * BM;  // rows per CTA
-  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 5) : 12;
+  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 4) : 12;
+  // MT = 2 (matrix-bound): ring positions 2g - 1 (a V) and 2g (the K after it)
+  // share a pair of slots, released by one commit, and land on one barrier: the
+  // MMA warp's instruction stream paces the kernel, and a commit or a wait
+  // less per tile shows.  MT = 1 (bound by memory) releases slots one by one.
+  static constexpr bool PAIRED = MT == 2;
+  static constexpr int NPAIR = NSTAGE / 2;
+  static_assert(NSTAGE % 2 == 0, "pairs");
   static constexpr int SMEM_Q = MT * TILE_BYTES;
   static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
   static constexpr int SMEM_BAR = 512;
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
   uint64_t* q_full = empty + NSTAGE;
   uint64_t* s_full = q_full + 1;  // [2] MT = 1: of alternate tiles; MT = 2: of the row tiles
   uint64_t* p_full = s_full + 2;  // [MT]
-  uint64_t* pv_done = p_full + 2; // [MT] P V of each tile has completed
+  uint64_t* pv_done = p_full + 2;  // [2] P V completed: MT = 1 of every tile, 2 of a stretch's last
   uint64_t* drain = pv_done + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -347,10 +354,31 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
     const uint64_t pol = p.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
     uint32_t tc = 0;  // tiles so far: K at ring position 2 tc, V at 2 tc + 1
     bool ok = true;
+    // Whole warp: ring position cnt may be overwritten.
+    auto slot_free = [&](uint32_t cnt) {
+      const uint32_t g = C::PAIRED ? (cnt + 1) >> 1 : cnt, n = C::PAIRED ? C::NPAIR : NSTAGE;
+      return mbar_wait<true>(&empty[g % n], ((g / n) & 1) ^ 1, abort_flag, &g_tree_err, 1);
+    };
+    auto load = [&](uint32_t cnt, const CUtensorMap* m, uint64_t* bar, int id, int pos) {
+      if (id >= 0)
+        tma_load_4d_hint(
+            sKV + (cnt % NSTAGE) * C::TILE_BYTES + half * tr::HALF_BYTES + sub * p.box * 128, m,
+            bar, half * 64, sg.hkv, pos, id, pol);
+    };
+    auto tile_bytes = [&](int id) {
+      return __popc(__ballot_sync(0xffffffffu, id >= 0)) * (uint32_t)p.box * 128u;
+    };
+    auto note_bad = [&](uint32_t t, int id) {
+      const uint32_t bad = __ballot_sync(0xffffffffu, id == -2 && half == 0);
+      if (lane == 0) {
+        if (bad) atomicOr(&g_tree_err, kErrBounds);
+        tile_bad[t % tr::BAD_RING] = bad;
+      }
+    };
     while (ok && tree_next(p, w, &sg)) {
       const int32_t* table = p.page_table + (size_t)sg.b * p.max_pages;
-      // Page of this lane's box in tile t (-1: past the sequence's end), one
-      // tile ahead of its use.
+      // Page of this lane's box in tile t (-1: nothing to load, -2: no such
+      // page) and the row in it.
       auto page_of = [&](int t, int* pos) {
         const int row = t * tr::BN + sub * p.box;
         if (!loads || row >= sg.L) return -1;
@@ -359,34 +387,54 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         const int id = table[pg];
         return id < 0 || id >= p.num_pages ? -2 : id;
       };
-      int pos = 0, pos_n = 0;
-      int id_n = page_of(sg.t0, &pos_n);
+      // Ring order K_0, V_0, K_1, V_1, ...; pages are looked up two tiles ahead.
+      int pos = 0, pos_n = 0, pos_nn = 0;
+      int id = page_of(sg.t0, &pos), id_n = sg.n > 1 ? page_of(sg.t0 + 1, &pos_n) : -1;
+      if (!(ok = slot_free(2 * tc))) break;
+      {
+        const uint32_t s = (2 * tc) % NSTAGE, bytes = tile_bytes(id);
+        note_bad(tc, id);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        __syncwarp();
+        load(2 * tc, &tmK, &full[s], id, pos);
+        if (lane == 0) *issued = 2 * tc + 1;
+      }
       for (int j = 0; j < sg.n && ok; ++j, ++tc) {
-        const int id = id_n;
-        pos = pos_n;
-        if (j + 1 < sg.n) id_n = page_of(sg.t0 + j + 1, &pos_n);
-        const uint32_t bad = __ballot_sync(0xffffffffu, id == -2 && half == 0);
-        const uint32_t bytes =
-            __popc(__ballot_sync(0xffffffffu, id >= 0)) * (uint32_t)p.box * 128u;
-        if (bad && lane == 0) atomicOr(&g_tree_err, kErrBounds);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t cnt = 2 * tc + v;
-          const int s = cnt % NSTAGE;
-          if (!(ok = mbar_wait<true>(&empty[s], ((cnt / NSTAGE) & 1) ^ 1, abort_flag,
-                                     &g_tree_err, 1)))
-            break;
+        const uint32_t cv = 2 * tc + 1, ck = cv + 1;
+        const bool more = j + 1 < sg.n;
+        const int id_nn = j + 2 < sg.n ? page_of(sg.t0 + j + 2, &pos_nn) : -1;
+        const uint32_t vb = tile_bytes(id), kb = tile_bytes(id_n);
+        if (!(ok = slot_free(cv))) break;
+        if (C::PAIRED && more) {
+          // V_j completes on K_{j+1}'s barrier; its own gets a plain arrival
+          // that keeps its phases in step.
+          note_bad(tc + 1, id_n);
+          uint64_t* bar = &full[ck % NSTAGE];
           if (lane == 0) {
-            if (v == 0) tile_bad[tc % tr::BAD_RING] = bad;
-            mbar_arrive_expect_tx(&full[s], bytes);
+            mbar_arrive_expect_tx(bar, vb + kb);
+            mbar_arrive(&full[cv % NSTAGE]);
           }
           __syncwarp();
-          if (id >= 0)
-            tma_load_4d_hint(sKV + s * C::TILE_BYTES + half * tr::HALF_BYTES + sub * p.box * 128,
-                             v ? &tmV : &tmK, &full[s], half * 64, sg.hkv, pos, id, pol);
+          load(cv, &tmV, bar, id, pos);
+          load(ck, &tmK, bar, id_n, pos_n);
+        } else {
+          if (lane == 0) mbar_arrive_expect_tx(&full[cv % NSTAGE], vb);
           __syncwarp();
-          if (lane == 0) *issued = cnt + 1;
+          load(cv, &tmV, &full[cv % NSTAGE], id, pos);
+          if (more) {
+            if (lane == 0) *issued = cv + 1;
+            if (!(ok = slot_free(ck))) break;
+            note_bad(tc + 1, id_n);
+            if (lane == 0) mbar_arrive_expect_tx(&full[ck % NSTAGE], kb);
+            __syncwarp();
+            load(ck, &tmK, &full[ck % NSTAGE], id_n, pos_n);
+          }
         }
+        if (lane == 0) *issued = more ? ck + 1 : cv + 1;
+        id = id_n;
+        pos = pos_n;
+        id_n = id_nn;
+        pos_n = pos_nn;
       }
     }
     __syncwarp();
@@ -422,48 +470,73 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
       uint32_t tc = 0, sc = 0;
       bool ok = true;
       auto landed = [&](uint32_t cnt, unsigned site) {
-        const bool r = mbar_wait<true>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag,
+        const bool r = mbar_wait<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag,
                                        &g_tree_err, site);
         tc_fence_after();
         return r;
       };
       while (ok && tree_next(p, w, &sg)) {
-        if (!(ok = mbar_wait<true>(q_full, sc & 1, abort_flag, &g_tree_err, 2))) break;
+        if (!(ok = mbar_wait<false>(q_full, sc & 1, abort_flag, &g_tree_err, 2))) break;
         ++sc;
         tc_fence_after();
         if (!(ok = landed(2 * tc, 3))) break;
-        for (int i = 0; i < n_act; ++i) {
-          issue_s(i, MT == 1 ? tc & 1 : i, (2 * tc) % NSTAGE);
-          mma_commit(&s_full[MT == 1 ? tc & 1 : i]);
-        }
-        mma_commit(&empty[(2 * tc) % NSTAGE]);
-        for (int j = 0; j < sg.n; ++j, ++tc) {
-          const uint32_t ck = 2 * tc + 2, cv = 2 * tc + 1;
-          const bool more = j + 1 < sg.n;
-          if (MT == 1 && more) {
-            // S of the next tile goes ahead of this tile's P V, so that it is
-            // ready when the softmax warps get to it.  (Its buffer held P of
-            // the tile before this one, whose P V was issued earlier.)
-            if (!(ok = landed(ck, 4))) break;
-            issue_s(0, (tc + 1) & 1, ck % NSTAGE);
-            mma_commit(&s_full[(tc + 1) & 1]);
-            mma_commit(&empty[ck % NSTAGE]);
-          }
-          if (!(ok = landed(cv, 5))) break;
-          if (MT == 2 && more && !(ok = landed(ck, 4))) break;
-          for (int i = 0; i < n_act; ++i) {
-            if (!(ok = mbar_wait<true>(&p_full[i], tc & 1, abort_flag, &g_tree_err, 6 + i))) break;
-            tc_fence_after();
-            issue_pv(i, MT == 1 ? tc & 1 : i, cv % NSTAGE, j > 0);
-            mma_commit(&pv_done[i]);
-            if (i == n_act - 1) mma_commit(&empty[cv % NSTAGE]);
-            if (MT == 2 && more) {
-              issue_s(i, i, ck % NSTAGE);
-              mma_commit(&s_full[i]);
-              if (i == n_act - 1) mma_commit(&empty[ck % NSTAGE]);
+        if constexpr (MT == 1) {
+          issue_s(0, tc & 1, (2 * tc) % NSTAGE);
+          mma_commit(&s_full[tc & 1]);
+          mma_commit(&empty[(2 * tc) % NSTAGE]);
+          for (int j = 0; j < sg.n; ++j, ++tc) {
+            const uint32_t ck = 2 * tc + 2, cv = 2 * tc + 1;
+            if (j + 1 < sg.n) {
+              // S of the next tile goes ahead of this tile's P V, so that it is
+              // ready when the softmax warps get to it.  (Its buffer held P of
+              // the tile before this one, whose P V was issued earlier.)
+              if (!(ok = landed(ck, 4))) break;
+              issue_s(0, (tc + 1) & 1, ck % NSTAGE);
+              mma_commit(&s_full[(tc + 1) & 1]);
+              mma_commit(&empty[ck % NSTAGE]);
             }
+            if (!(ok = landed(cv, 5))) break;
+            if (!(ok = mbar_wait<false>(&p_full[0], tc & 1, abort_flag, &g_tree_err, 6))) break;
+            tc_fence_after();
+            issue_pv(0, tc & 1, cv % NSTAGE, j > 0);
+            mma_commit(&pv_done[0]);
+            mma_commit(&empty[cv % NSTAGE]);
           }
-          if (!ok) break;
+        } else {
+          issue_s(0, 0, (2 * tc) % NSTAGE);
+          mma_commit(&s_full[0]);
+          if (n_act == 2) {
+            issue_s(1, 1, (2 * tc) % NSTAGE);
+            mma_commit(&s_full[1]);
+          }
+          // K_0 completes its pair with the stretch before's last V.
+          mma_commit(&empty[tc % C::NPAIR]);
+          for (int j = 0; j < sg.n; ++j, ++tc) {
+            const uint32_t ck = 2 * tc + 2, cv = 2 * tc + 1;
+            const bool more = j + 1 < sg.n;
+            if (!(ok = landed(more ? ck : cv, 5))) break;
+            if (!(ok = mbar_wait<false>(&p_full[0], tc & 1, abort_flag, &g_tree_err, 6))) break;
+            tc_fence_after();
+            issue_pv(0, 0, cv % NSTAGE, j > 0);
+            if (more) {
+              issue_s(0, 0, ck % NSTAGE);
+              mma_commit(&s_full[0]);
+            } else {
+              mma_commit(&pv_done[0]);
+            }
+            if (n_act == 2) {
+              if (!(ok = mbar_wait<false>(&p_full[1], tc & 1, abort_flag, &g_tree_err, 7))) break;
+              tc_fence_after();
+              issue_pv(1, 1, cv % NSTAGE, j > 0);
+              if (more) {
+                issue_s(1, 1, ck % NSTAGE);
+                mma_commit(&s_full[1]);
+              } else {
+                mma_commit(&pv_done[1]);
+              }
+            }
+            if (more) mma_commit(&empty[(tc + 1) % C::NPAIR]);
+          }
         }
       }
       // Every MMA issued here has completed before tensor memory is freed.
@@ -507,7 +580,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
       }
       if (lane == 0) p.start[0] = 0;
     }
-    uint32_t tc = 0;
+    uint32_t tc = 0, seg = 0;
     int cur_b = -1;
     uint64_t anc = 0, used = 0;
     bool ok = true;
@@ -542,28 +615,22 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         const int buf = MT == 1 ? tc & 1 : i;
         const uint32_t tS = t_lane + C::COL_S + buf * 128;
         const uint32_t par = MT == 1 ? (tc >> 1) & 1 : tc & 1;
-        if (!(ok = mbar_wait<true>(&s_full[buf], par, abort_flag, &g_tree_err, 8 + i))) break;
+        if (!(ok = mbar_wait<false>(&s_full[buf], par, abort_flag, &g_tree_err, 8 + i))) break;
         __syncwarp();
         tc_fence_after();
         const int kv0 = (sg.t0 + j) * tr::BN;
         const uint32_t bad = tile_bad[tc % tr::BAD_RING];
         const bool masked = kv0 + tr::BN > base || bad;
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked) {
-          const Mask128 fine = sound_keys(bad, p.box);
-          const Mask128 mine = tile_mask(base - kv0, anc);
-          see[0] = (uint32_t)(mine.lo & fine.lo);
-          see[1] = (uint32_t)((mine.lo & fine.lo) >> 32);
-          see[2] = (uint32_t)(mine.hi & fine.hi);
-          see[3] = (uint32_t)((mine.hi & fine.hi) >> 32);
           // V rows that no query may see (unused nodes, slots past the end,
           // bad pages) can hold anything: they are cleared, since 0 * NaN in
           // P V would reach every row.
-          const Mask128 any = tile_mask(base - kv0, used);
+          const Mask128 any = tile_mask(base - kv0, used), fine = sound_keys(bad, p.box);
           const uint64_t keep = tid < 64 ? any.lo & fine.lo : any.hi & fine.hi;
           const uint32_t cv = 2 * tc + 1;
-          if (!(ok = mbar_wait<true>(&full[cv % NSTAGE], (cv / NSTAGE) & 1, abort_flag,
-                                     &g_tree_err, 10)))
+          const uint32_t on = C::PAIRED && j + 1 < sg.n ? cv + 1 : cv;  // V's barrier
+          if (!(ok = mbar_wait<false>(&full[on % NSTAGE], (on / NSTAGE) & 1, abort_flag,
+                                      &g_tree_err, 10)))
             break;
           if (!(keep >> (tid & 63) & 1)) {
             uint8_t* vr = sKV + (cv % NSTAGE) * C::TILE_BYTES + tid * 128;
@@ -575,7 +642,9 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        bool pv_waited = j == 0;  // (the stretch before waited for its last P V)
+        // MT = 1: (the stretch before waited for its last P V.)  MT = 2: S of
+        // this tile was issued after P V of the last, and both are done.
+        bool pv_waited = MT == 2 || j == 0;
         if (warp_ok) {
           uint32_t sr[4][32];
           float mx = hide;
@@ -612,11 +681,15 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) reg_fence32(sr[q]);
           if (masked) {
+            const Mask128 fine = sound_keys(bad, p.box), mine = tile_mask(base - kv0, anc);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t m64 = q < 2 ? mine.lo & fine.lo : mine.hi & fine.hi;
+              const uint32_t see = (uint32_t)(q & 1 ? m64 >> 32 : m64);
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (!(see[q] >> x & 1)) sr[q][x] = __float_as_uint(hide);
+                if (!(see >> x & 1)) sr[q][x] = __float_as_uint(hide);
+            }
           }
           // The stretch's first tile takes its own maximum; later tiles are
           // exponentiated against the running one, and a row takes the slow
@@ -646,8 +719,8 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
             m_used = m_new;
             if (j > 0) {
               // O of the tiles so far, once the last of their P V is done.
-              if (!(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag, &g_tree_err,
-                                         11 + i)))
+              if (!pv_waited && !(ok = mbar_wait<false>(&pv_done[i], (tc - 1) & 1, abort_flag,
+                                                        &g_tree_err, 11)))
                 break;
               __syncwarp();
               pv_waited = true;
@@ -667,16 +740,19 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           l += (la.x + la.y) + (lb.x + lb.y);
           tmem_wait_st();
         }
-        // One phase of pv_done per tile, each waited for before the next P is
-        // handed over: the parity waits never fall two phases behind.
-        if (!pv_waited && !(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag,
-                                                 &g_tree_err, 13 + i)))
+        // MT = 1: one phase of pv_done per tile, each waited for before the next P
+        // is handed over: the parity waits never fall two phases behind.
+        if (!pv_waited && !(ok = mbar_wait<false>(&pv_done[i], (tc - 1) & 1, abort_flag,
+                                                  &g_tree_err, 13)))
           break;
         tc_fence_before();
         mbar_arrive(&p_full[i]);
       }
       if (!ok) break;
-      if (!(ok = mbar_wait<true>(&pv_done[i], (tc - 1) & 1, abort_flag, &g_tree_err, 15))) break;
+      if (!(ok = mbar_wait<false>(&pv_done[i], (MT == 1 ? tc - 1 : seg) & 1, abort_flag,
+                                  &g_tree_err, 15)))
+        break;
+      ++seg;
       __syncwarp();
       tc_fence_after();
       if (warp_ok) {

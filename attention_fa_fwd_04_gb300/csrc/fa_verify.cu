@@ -123,92 +123,151 @@ __device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
 __device__ __forceinline__ Pair shfl(Pair a, int l) {
   return {__shfl_sync(0xffffffffu, a.hi, l), __shfl_sync(0xffffffffu, a.lo, l)};
 }
-// max(r - Z q, 0).
-__device__ __forceinline__ Pair residual(Pair r, Pair Z, float q) {
-  const float h = __fmul_rn(Z.hi, q);
-  const float l = __fmaf_rn(Z.lo, q, __fmaf_rn(Z.hi, q, -h));
-  Pair d = two_sum(r.hi, -h);
-  d = fast_two_sum(d.hi, __fadd_rn(d.lo, __fsub_rn(r.lo, l)));
+// max(p - c q, 0).
+__device__ __forceinline__ Pair residual(float p, Pair c, float q) {
+  const float h = __fmul_rn(c.hi, q);
+  const float l = __fmaf_rn(c.lo, q, __fmaf_rn(c.hi, q, -h));
+  Pair d = two_sum(p, -h);
+  d = fast_two_sum(d.hi, __fsub_rn(d.lo, l));
   return d.hi > 0.f ? d : Pair{0.f, 0.f};
 }
 
-// What a node's rejected children left of its row: the masses before each
-// rejection (drafted from q), or the rejected tokens (no q).
-struct Rejected {
-  int n;
-  const Pair* mass;
-  const int* token;
+// The same on two elements at once (packed fp32 operations).
+struct Pair2 {
+  float2 hi, lo;
 };
-
-// Element v of what is left.  LEVEL: rj.n where it is 0 or 1, else 2.  (After
-// one rejection, with Z = 1, a positive p - q is a difference of p >= q >= 0,
-// whose error is one more subtraction.)
-template <bool DRAFT, int LEVEL>
-__device__ __forceinline__ Pair left_of(float p, float q, int v, const Rejected& rj) {
-  Pair r{clean(p), 0.f};
-  if constexpr (LEVEL == 0) {
-  } else if constexpr (!DRAFT) {
-    for (int i = 0; i < rj.n; ++i)
-      if (rj.token[i] == v) r.hi = 0.f;
-  } else {
-    const float c = clean(q);
-    const float d = __fsub_rn(r.hi, c);
-    r = d > 0.f ? Pair{d, __fsub_rn(__fsub_rn(r.hi, d), c)} : Pair{0.f, 0.f};
-    if constexpr (LEVEL == 2)
-      for (int i = 1; i < rj.n; ++i) r = residual(r, rj.mass[i], c);
-  }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return __ffma2_rn(b, both(-1.f), a);
+}
+__device__ __forceinline__ Pair2 two_sum2(float2 a, float2 b) {
+  const float2 s = __fadd2_rn(a, b), t = sub2(s, a);
+  return {s, __fadd2_rn(sub2(a, sub2(s, t)), sub2(b, t))};
+}
+__device__ __forceinline__ Pair2 residual2(float2 p, Pair c, float2 q) {
+  const float2 nh = __fmul2_rn(both(-c.hi), q);
+  const float2 l = __ffma2_rn(both(c.lo), q, __ffma2_rn(both(c.hi), q, nh));
+  const Pair2 d = two_sum2(p, nh);
+  const float2 lo = sub2(d.lo, l);
+  Pair2 r;
+  r.hi = __fadd2_rn(d.hi, lo);
+  r.lo = sub2(lo, sub2(r.hi, d.hi));
+  if (!(r.hi.x > 0.f)) r.hi.x = r.lo.x = 0.f;
+  if (!(r.hi.y > 0.f)) r.hi.y = r.lo.y = 0.f;
   return r;
 }
 
-template <bool VEC>
+// What a node's n rejected children left of its row: with q, max(p - c q, 0),
+// c = 1 + Z_1 + ... + Z_{n-1} the sum of the masses so far (taking Z q off an
+// earlier residual again only lowers the same difference); without, p with the
+// rejected tokens' entries 0.
+struct Rejected {
+  int n;
+  Pair c;
+  const int* token;
+};
+
+// Four elements of a row from v on: v, v + ST, v + 2 ST, v + 3 ST.  (ST = 1 by
+// one 16-byte load where rows are aligned, else scalar loads, for a whole
+// warp's group of 128 with ST = 32.)
+template <bool VEC, int ST>
 __device__ __forceinline__ float4 load4(const float* row, int v, int end) {
   if constexpr (VEC) {
     return v < end ? *reinterpret_cast<const float4*>(row + v) : make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
-    return make_float4(v < end ? row[v] : 0.f, v + 1 < end ? row[v + 1] : 0.f,
-                       v + 2 < end ? row[v + 2] : 0.f, v + 3 < end ? row[v + 3] : 0.f);
+    return make_float4(v < end ? row[v] : 0.f, v + ST < end ? row[v + ST] : 0.f,
+                       v + 2 * ST < end ? row[v + 2 * ST] : 0.f,
+                       v + 3 * ST < end ? row[v + 3 * ST] : 0.f);
+  }
+}
+template <bool DRAFT, int ST>
+__device__ __forceinline__ void left4(float4 a, float4 d, int v, const Rejected& rj,
+                                      Pair2 (&r)[2]) {
+  r[0] = {make_float2(clean(a.x), clean(a.y)), both(0.f)};
+  r[1] = {make_float2(clean(a.z), clean(a.w)), both(0.f)};
+  if (rj.n == 0) return;
+  if constexpr (DRAFT) {
+    r[0] = residual2(r[0].hi, rj.c, make_float2(clean(d.x), clean(d.y)));
+    r[1] = residual2(r[1].hi, rj.c, make_float2(clean(d.z), clean(d.w)));
+  } else {
+    for (int k = 0; k < rj.n; ++k) {
+      const int o = rj.token[k] - v;
+      if (o == 0) r[0].hi.x = 0.f;
+      if (o == ST) r[0].hi.y = 0.f;
+      if (o == 2 * ST) r[1].hi.x = 0.f;
+      if (o == 3 * ST) r[1].hi.y = 0.f;
+    }
   }
 }
 
-// Sum of what is left in [va, vb) of a row, over the warp.
-template <bool DRAFT, bool VEC, int LEVEL>
+// Sum of what is left in [va, vb) of a row, over the warp: groups of 128
+// elements, four at a time, each four's loads ahead of the last four's sums.
+template <bool DRAFT, bool VEC>
 __device__ __forceinline__ Pair sum_left(const float* pr, const float* qr, int va, int vb,
                                          const Rejected& rj) {
+  constexpr int G = DRAFT ? 2 : 4, ST = VEC ? 1 : 32;
   const int lane = threadIdx.x & 31;
-  Pair acc{0.f, 0.f};
-  auto take = [&](float a, float d, int v) {
-    const Pair r = left_of<DRAFT, LEVEL>(a, d, v, rj);
-    const Pair s = two_sum(acc.hi, r.hi);
-    acc = {s.hi, __fadd_rn(acc.lo, __fadd_rn(s.lo, r.lo))};
+  const bool use_q = DRAFT && rj.n > 0;
+  int v = va + (VEC ? lane * 4 : lane);
+  Pair2 acc{both(0.f), both(0.f)};
+  float4 a[G], d[G], an[G], dn[G];
+  auto fetch = [&](int at, float4 (&x)[G], float4 (&y)[G]) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      x[i] = load4<VEC, ST>(pr, at + i * 128, vb);
+      if constexpr (DRAFT)
+        if (use_q) y[i] = load4<VEC, ST>(qr, at + i * 128, vb);
+    }
   };
-  if constexpr (VEC) {
-    constexpr int AHEAD = 4;
-    for (int v0 = va + lane * 4; v0 < vb; v0 += 128 * AHEAD) {
-      float4 a[AHEAD], d[AHEAD];
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        a[i] = load4<true>(pr, v0 + i * 128, vb);
-        if constexpr (DRAFT && LEVEL > 0) d[i] = load4<true>(qr, v0 + i * 128, vb);
-      }
+  for (int i = 0; i < G; ++i) d[i] = dn[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  fetch(v, a, d);
+  for (int w0 = va; w0 < vb; w0 += 128 * G, v += 128 * G) {
+    fetch(v + 128 * G, an, dn);
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const int v = v0 + i * 128;
-        if constexpr (!(DRAFT && LEVEL > 0)) d[i] = a[i];
-        take(a[i].x, d[i].x, v);
-        take(a[i].y, d[i].y, v + 1);
-        take(a[i].z, d[i].z, v + 2);
-        take(a[i].w, d[i].w, v + 3);
+    for (int i = 0; i < G; ++i) {
+      Pair2 r[2];
+      left4<DRAFT, ST>(a[i], d[i], v + i * 128, rj, r);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const Pair2 s = two_sum2(acc.hi, r[e].hi);
+        acc = {s.hi, __fadd2_rn(acc.lo, __fadd2_rn(s.lo, r[e].lo))};
       }
     }
-  } else {
-#pragma unroll 8
-    for (int v = va + lane; v < vb; v += 32)
-      take(pr[v], DRAFT && LEVEL > 0 ? qr[v] : 0.f, v);
-  }
-  acc = fast_two_sum(acc.hi, acc.lo);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc = add(acc, shfl_xor(acc, o));
-  return acc;
+    for (int i = 0; i < G; ++i) {
+      a[i] = an[i];
+      d[i] = dn[i];
+    }
+  }
+  Pair t = add(fast_two_sum(acc.hi.x, acc.lo.x), fast_two_sum(acc.hi.y, acc.lo.y));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
+  return t;
+}
+
+// Whole warp: inclusive sums of n <= 32 values, one per lane.
+__device__ __forceinline__ Pair scan(Pair x, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int o = 1; o < n; o <<= 1) {
+    const Pair y = shfl_up(x, o);
+    if (lane >= o) x = add(y, x);
+  }
+  return x;
+}
+// Whole warp: which of n sums (in shared memory) the aim falls in: the first
+// whose cumulative sum, on top of *before, exceeds it; else (u of 1, or the
+// last rounding) the last that holds anything.  *before moves up to its start.
+__device__ __forceinline__ int pick_part(const Pair* sums, int n, Pair aim, Pair* before) {
+  const int lane = threadIdx.x & 31;
+  const Pair s = lane < n ? sums[lane] : Pair{0.f, 0.f};
+  const Pair inc = scan(s, n);
+  const uint32_t some = __ballot_sync(0xffffffffu, s.hi > 0.f);
+  const uint32_t past = __ballot_sync(0xffffffffu, above(add(*before, inc), aim)) & some;
+  const int at = past ? __ffs(past) - 1 : 31 - __clz(some);
+  const Pair up = shfl(inc, at > 0 ? at - 1 : 0);
+  if (at > 0) *before = add(*before, up);
+  return at;
 }
 
 // VEC: rows are 16-byte aligned (V a multiple of 4).
@@ -217,12 +276,13 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int s_parent[vf::MAX_N], s_token[vf::MAX_N], s_rej[vf::MAX_N];
   __shared__ float s_u[vf::MAX_N], s_px[vf::MAX_N], s_qx[vf::MAX_N];
-  __shared__ Pair s_mass[vf::MAX_N];
   __shared__ Pair s_warp[vf::WARPS];
   __shared__ Pair s_cta[2][vf::CLUSTER];
+  __shared__ int s_pick[2][vf::WARPS];
   __shared__ int s_cur, s_nrej;
   __shared__ bool s_last, s_known;
   __shared__ uint64_t s_path;
+  __shared__ Pair s_c;
   pdl_launch_dependents();
   cluster_arrive();  // (waited for below: no CTA is written to before it runs)
   pdl_wait_primary();
@@ -236,6 +296,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     // Node tid: an edge that the walk may take, or parent -2.
     int par = tid == 0 ? -1 : p.parents[node0 + tid];
     const int x = p.tokens[node0 + tid];
+    s_u[tid] = p.u[node0 + tid];
     if (tid > 0 && (par < -2 || par >= tid || (par >= 0 && (x < 0 || x >= V)))) {
       par = -2;
       if (rank == 0) atomicOr(&g_verify_err, kErrBounds);
@@ -243,40 +304,38 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     const bool edge = tid > 0 && par >= 0;
     s_parent[tid] = edge ? par : -2;
     s_token[tid] = x;
-    s_u[tid] = p.u[node0 + tid];
     s_px[tid] = edge ? clean(p.p[(node0 + par) * V + x]) : 0.f;
     s_qx[tid] = DRAFT ? (edge ? clean(p.q[(node0 + par) * V + x]) : 0.f) : 1.f;
   }
   __syncthreads();
   cluster_wait();
 
-  const long long v0 = ((long long)rank * vf::WARPS + warp) * p.part;
-  const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
   int pass = 0;
-  // Sum of what is left of node cur's row after n rejections: s_warp and
-  // s_cta[pass & 1], and their total.  All threads of the cluster.
-  auto mass_of = [&](int cur, int n) {
-    const Rejected rj{n, s_mass, s_rej};
+  // Sum of what is left of node cur's row: s_warp, and s_cta[pass & 1].  All
+  // threads of the cluster.
+  auto mass_of = [&](int cur, const Rejected& rj) {
+    const long long v0 = ((long long)rank * vf::WARPS + warp) * p.part;
+    const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
     const float* pr = p.p + (node0 + cur) * V;
     const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-    const Pair s = n == 0   ? sum_left<DRAFT, VEC, 0>(pr, qr, va, vb, rj)
-                   : n == 1 ? sum_left<DRAFT, VEC, 1>(pr, qr, va, vb, rj)
-                            : sum_left<DRAFT, VEC, 2>(pr, qr, va, vb, rj);
+    const Pair s = sum_left<DRAFT, VEC>(pr, qr, va, vb, rj);
     if (lane == 0) s_warp[warp] = s;
     __syncthreads();
     ++pass;
     if (warp == 0) {
       Pair t = lane < vf::WARPS ? s_warp[lane] : Pair{0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
       for (int o = vf::WARPS / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
       if (lane < CL) store_remote(&s_cta[pass & 1][rank], lane, t);
     }
     cluster_sync();
   };
+  // (The same bits in every warp of every CTA.)
   auto total_of = [&]() {
-    Pair t{0.f, 0.f};
-    for (int i = 0; i < CL; ++i) t = add(t, s_cta[pass & 1][i]);
-    return t;
+    Pair t = lane < CL ? s_cta[pass & 1][lane] : Pair{0.f, 0.f};
+#pragma unroll 1
+    for (int o = vf::CLUSTER / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
+    return shfl(t, 0);
   };
 
   // The walk, by warp 0; the others join for masses.
@@ -285,14 +344,15 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     return (uint64_t)__ballot_sync(0xffffffffu, par0 == node) |
            (uint64_t)__ballot_sync(0xffffffffu, par1 == node) << 32;
   };
-  int cur = 0, n_rej = 0, n_sum = -1;  // n_sum: rejections that the sums stand for
+  int cur = 0, n_sum = -1;  // n_sum: rejections that the sums stand for
+  Rejected rj{0, {0.f, 0.f}, s_rej};
   uint64_t path = 1, kids = warp == 0 ? children(0) : 0;
   Pair Z{1.f, 0.f};
   for (;;) {
     if (warp == 0) {
       while (kids) {
-        if (DRAFT && n_rej > 0) {
-          if (n_sum != n_rej) break;
+        if (DRAFT && rj.n > 0) {
+          if (n_sum != rj.n) break;
           Z = total_of();
         }
         const int c = __ffsll((long long)kids) - 1;
@@ -300,9 +360,9 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
         const int x = s_token[c];
         Pair r{s_px[c], 0.f};
         if constexpr (DRAFT) {
-          for (int i = 0; i < n_rej; ++i) r = residual(r, s_mass[i], s_qx[c]);
+          if (rj.n > 0) r = residual(r.hi, rj.c, s_qx[c]);
         } else {
-          for (int i = 0; i < n_rej; ++i)
+          for (int i = 0; i < rj.n; ++i)
             if (s_rej[i] == x) r.hi = 0.f;
         }
         const Pair bar = mul(mul(Pair{s_u[c], 0.f}, Pair{s_qx[c], 0.f}), Z);
@@ -310,33 +370,37 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
           cur = c;
           path |= 1ull << c;
           kids = children(c);
-          n_rej = 0;
+          rj.n = 0;
+          rj.c = {0.f, 0.f};
           n_sum = -1;
           Z = {1.f, 0.f};
         } else {
-          if (lane == 0) {
-            s_mass[n_rej] = Z;
-            s_rej[n_rej] = x;
+          if constexpr (DRAFT) {
+            rj.c = add(rj.c, Z);
+          } else {
+            if (lane == 0) s_rej[rj.n] = x;
+            __syncwarp();
+            Z = add(Z, Pair{-r.hi, 0.f});
           }
-          __syncwarp();
-          ++n_rej;
-          if constexpr (!DRAFT) Z = add(Z, Pair{-r.hi, 0.f});
+          ++rj.n;
         }
       }
       if (lane == 0) {
         s_cur = cur;
-        s_nrej = n_rej;
+        s_nrej = rj.n;
+        s_c = rj.c;
         s_last = kids == 0;
-        s_known = n_sum == n_rej;
+        s_known = n_sum == rj.n;
         s_path = path;
       }
     }
     __syncthreads();
     const bool last = s_last, known = s_known;
     cur = s_cur;
-    n_rej = s_nrej;
-    if (!known) mass_of(cur, n_rej);
-    n_sum = n_rej;
+    rj.n = s_nrej;
+    rj.c = s_c;
+    if (!known) mass_of(cur, rj);
+    n_sum = rj.n;
     if (last) break;
   }
 
@@ -351,10 +415,9 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
 
   // The next token.
   Pair total = total_of();
-  if (!(total.hi > 0.f) && n_rej > 0) {  // nothing left: the target's own row
-    n_rej = 0;
-    __syncthreads();  // (s_warp is still being read)
-    mass_of(cur, 0);
+  if (!(total.hi > 0.f) && rj.n > 0) {  // nothing left: the target's own row
+    rj.n = 0;
+    mass_of(cur, rj);
     total = total_of();
   }
   if (!(total.hi > 0.f)) {
@@ -362,101 +425,56 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     return;
   }
   const Pair aim = mul(Pair{s_u[0], 0.f}, total);
-  // The CTA and warp whose part of the row the aim falls in: the first whose
-  // cumulative sum exceeds it, else (u of 1, or the last rounding) the last
-  // that holds anything.
-  Pair before{0.f, 0.f}, run{0.f, 0.f};
-  int at = -1;
-  for (int i = 0; i < CL; ++i) {
-    const Pair s = s_cta[pass & 1][i];
-    if (s.hi > 0.f && (at < 0 || !above(run, aim))) {
-      at = i;
-      before = run;
-    }
-    run = add(run, s);
-  }
-  if (at != rank) return;
-  run = before;
-  at = -1;
-#pragma unroll 4
-  for (int i = 0; i < vf::WARPS; ++i) {
-    const Pair s = s_warp[i];
-    if (s.hi > 0.f && (at < 0 || !above(run, aim))) {
-      at = i;
-      before = run;
-    }
-    run = add(run, s);
-  }
-  if (at != warp) return;
-  // Blocks of 128 tokens, four per lane, several at once.
-  const Rejected rj{n_rej, s_mass, s_rej};
+  Pair before{0.f, 0.f};
+  if (pick_part(s_cta[pass & 1], CL, aim, &before) != rank) return;
+  const int at = pick_part(s_warp, vf::WARPS, aim, &before);
+  // That part of the row, a group of 128 tokens per warp, four per lane.
+  const long long v0 = ((long long)rank * vf::WARPS + at) * p.part;
+  const int vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
   const float* pr = p.p + (node0 + cur) * V;
   const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-  auto four = [&](float4 a, float4 d, int v, Pair (&r)[4]) {
-    const float x[4] = {a.x, a.y, a.z, a.w}, y[4] = {d.x, d.y, d.z, d.w};
+  int found = INT32_MAX, last_v = -1;
+  for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * vf::WARPS) {
+    const int v = w0 + warp * 128 + lane * 4;
+    const float4 a = load4<VEC, 1>(pr, v, vb);
+    const float4 d = DRAFT && rj.n > 0 ? load4<VEC, 1>(qr, v, vb) : a;
+    Pair2 r2[2];
+    left4<DRAFT, 1>(a, d, v, rj, r2);
+    const Pair r[4] = {{r2[0].hi.x, r2[0].lo.x}, {r2[0].hi.y, r2[0].lo.y},
+                       {r2[1].hi.x, r2[1].lo.x}, {r2[1].hi.y, r2[1].lo.y}};
+    const Pair own = add(add(r[0], r[1]), add(r[2], r[3]));
+    const Pair inc = scan(own, 32);
+    __syncthreads();  // (s_warp and s_pick have been read)
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    const Pair upto = scan(lane < vf::WARPS ? s_warp[lane] : Pair{0.f, 0.f}, vf::WARPS);
+    Pair start = shfl(upto, warp > 0 ? warp - 1 : 0);
+    start = warp > 0 ? add(before, start) : before;
+    const uint32_t some = __ballot_sync(0xffffffffu, own.hi > 0.f);
+    const uint32_t past = __ballot_sync(0xffffffffu, above(add(start, inc), aim)) & some;
+    const int l = past ? __ffs(past) - 1 : (some ? 31 - __clz(some) : 0);
+    const Pair up = shfl(inc, l > 0 ? l - 1 : 0);
+    if (lane == l) {
+      // The lane's first that passes the aim; its last with mass where
+      // rounding (or a missing aim) leaves none.
+      Pair run = l > 0 ? add(start, up) : start;
+      int pick = -1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      r[e] = n_rej == 0 ? left_of<DRAFT, 0>(x[e], y[e], v + e, rj)
-                        : left_of<DRAFT, 2>(x[e], y[e], v + e, rj);
-  };
-  constexpr int BLK = 4;
-  int found = -1, last_v = -1;  // first token of the lane's four
-  for (int w0 = va; w0 < vb && found < 0; w0 += 128 * BLK) {
-    float4 a[BLK], d[BLK];
-    Pair inc[BLK];
-    bool some[BLK];
-#pragma unroll
-    for (int i = 0; i < BLK; ++i) {
-      const int v = w0 + i * 128 + lane * 4;
-      a[i] = load4<VEC>(pr, v, vb);
-      d[i] = DRAFT && n_rej > 0 ? load4<VEC>(qr, v, vb) : a[i];
-    }
-#pragma unroll
-    for (int i = 0; i < BLK; ++i) {
-      Pair r[4];
-      four(a[i], d[i], w0 + i * 128 + lane * 4, r);
-      inc[i] = add(add(r[0], r[1]), add(r[2], r[3]));
-      some[i] = inc[i].hi > 0.f;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < BLK; ++i) {
-        const Pair y = shfl_up(inc[i], o);
-        if (lane >= o) inc[i] = add(y, inc[i]);
+      for (int e = 0; e < 4; ++e) {
+        if (r[e].hi > 0.f && (!past || pick < 0 || !above(run, aim))) pick = v + e;
+        run = add(run, r[e]);
       }
-#pragma unroll
-    for (int i = 0; i < BLK; ++i) {
-      const uint32_t any = __ballot_sync(0xffffffffu, some[i]);
-      const uint32_t past = __ballot_sync(0xffffffffu, above(add(before, inc[i]), aim)) & any;
-      if (any) last_v = w0 + i * 128 + (31 - __clz(any)) * 4;
-      if (past && found < 0) {
-        const int l = __ffs(past) - 1;
-        found = w0 + i * 128 + l * 4;
-        // What comes before that lane's four.
-        const Pair up = shfl(inc[i], l > 0 ? l - 1 : 0);
-        if (l > 0) before = add(before, up);
-      }
-      const Pair tot = shfl(inc[i], 31);
-      if (found < 0) before = add(before, tot);
+      s_pick[0][warp] = past ? pick : INT32_MAX;
+      s_pick[1][warp] = some ? pick : -1;
     }
-  }
-  if (lane == 0) {
-    const int v = found >= 0 ? found : last_v;
-    Pair r[4];
-    four(load4<VEC>(pr, v, vb), DRAFT ? load4<VEC>(qr, v, vb) : make_float4(0.f, 0.f, 0.f, 0.f), v,
-         r);
-    int pick = v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // The first that passes the aim; the last with mass where rounding (or a
-      // missing aim) leaves none.
-      const bool open = found < 0 || !above(before, aim);
-      if (r[e].hi > 0.f && open) pick = v + e;
-      before = add(before, r[e]);
+    __syncthreads();
+    for (int i = 0; i < vf::WARPS; ++i) {
+      found = s_pick[0][i] < found ? s_pick[0][i] : found;
+      last_v = s_pick[1][i] > last_v ? s_pick[1][i] : last_v;
     }
-    p.next[b] = pick;
+    before = add(before, shfl(upto, vf::WARPS - 1));
   }
+  if (tid == 0) p.next[b] = found != INT32_MAX ? found : last_v;
 }
 
 // ---------------------------------------------------------------------------
