@@ -320,15 +320,6 @@ struct RopeWalk {
   }
 };
 
-// Untiled bulk copy into shared memory; addresses and size are multiples of 16.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 // A lane's 16 bytes of a head in its ring.
 __device__ __forceinline__ uint4 ring_load(const uint8_t* p) {
   return *reinterpret_cast<const uint4*>(p);

@@ -31,6 +31,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -82,7 +84,7 @@ struct TreeParams {
   const int32_t* page_table;
   const int32_t* seqlens;
   const int32_t* parents;  // [B, N]
-  float* part_o;           // [CTAs][2][rt_rows][D] unnormalised partial outputs
+  float* part_o;           // [CTAs][2][D / 4][rt_rows][4] unnormalised partial outputs
   float* part_ml;          // [CTAs][2][rt_rows][2] (max in log2 units, sum)
   long long* start;        // [B + 1] first tile of each sequence in the list
   int B, N, Hq, Hkv, G, rows, rt_rows, n_rt, groups;
@@ -98,6 +100,16 @@ __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
 }
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
   return (tree_len(p, b) + tr::BN - 1) / tr::BN;
+}
+
+// a * b / c and a / c in 32 bits where they fit: a 64-bit division is a few
+// hundred instructions, and a short call makes several one after another.
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  return a <= (0xffffffffll / (b + 1)) ? (long long)((uint32_t)a * (uint32_t)b / (uint32_t)c)
+                                       : a * b / c;
+}
+__device__ __forceinline__ int div_small(long long a, int c) {
+  return a >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)c) : (int)(a / c);
 }
 
 // A CTA's place in the tile list.
@@ -127,8 +139,8 @@ __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
   const long long total = sum * p.Hkv;
   const long long G = tree_groups(p, total);
   TreeWalk w;
-  w.x = g < G ? total * g / G : 0;
-  w.hi = g < G ? total * (g + 1) / G : 0;
+  w.x = g < G ? mul_div(total, g, G) : 0;
+  w.hi = g < G ? mul_div(total, g + 1, G) : 0;
   w.first = 0;
   w.b = 0;
   w.T = 0;
@@ -166,7 +178,7 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, Tree
   }
   const long long off = w.x - w.first;
   s->b = w.b;
-  s->hkv = (int)(off / w.T);
+  s->hkv = div_small(off, w.T);
   s->t0 = (int)(off - (long long)s->hkv * w.T);
   s->T = w.T;
   s->L = tree_len(p, w.b);
@@ -438,6 +450,27 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
       }
     }
     __syncwarp();
+    // The first CTA's producer, done early, lists where each sequence starts for
+    // the merge.
+    if (blockIdx.x == 0) {
+      long long before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const long long Tb = b0 + lane < p.B ? (long long)tree_tiles(p, b0 + lane) * p.Hkv : 0;
+        long long inc = Tb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (b0 + lane < p.B) {
+          p.start[b0 + lane + 1] = before + inc;
+          if ((long long)p.seqlens[b0 + lane] > (long long)p.max_pages * p.page_size)
+            atomicOr(&g_tree_err, kErrBounds);
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) p.start[0] = 0;
+    }
    } else if (warp == W_MMA) {
     // ============================ MMA issuer (lane 0) ============================
     if (lane == 0) {
@@ -560,31 +593,31 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
     const float c = p.c;
     const bool neg = c < 0.f;
     const float hide = neg ? -NEG_INF : NEG_INF;
-    // The first CTA also lists where each sequence starts, for the merge.
-    if (blockIdx.x == 0 && warp == 0) {
-      long long before = 0;
-      for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long Tb = b0 + lane < p.B ? (long long)tree_tiles(p, b0 + lane) * p.Hkv : 0;
-        long long inc = Tb;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        if (b0 + lane < p.B) {
-          p.start[b0 + lane + 1] = before + inc;
-          if ((long long)p.seqlens[b0 + lane] > (long long)p.max_pages * p.page_size)
-            atomicOr(&g_tree_err, kErrBounds);
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-      }
-      if (lane == 0) p.start[0] = 0;
-    }
     uint32_t tc = 0, seg = 0;
     int cur_b = -1;
     uint64_t anc = 0, used = 0;
     bool ok = true;
-    while (ok && tree_next(p, w, &sg)) {
+    // This row of Q for a stretch, in the swizzled layout of a TMA load.  Done
+    // as soon as S of the stretch before's last tile is there (no MMA reads Q
+    // any more), so that the next stretch's S runs under the epilogue.
+    auto load_q = [&](const TreeSeg& t) {
+      uint4 v[D / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const T*>(p.q) +
+          (((size_t)t.b * p.N + s) * p.Hq + (size_t)t.hkv * p.G + g) * D);
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) v[x] = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
+      uint8_t* dst = sQ + i * C::TILE_BYTES + tid * 128;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+        *reinterpret_cast<uint4*>(dst + (x >> 3) * tr::HALF_BYTES + (((x & 7) ^ (tid & 7)) << 4)) =
+            v[x];
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(q_full);
+    };
+    bool have = tree_next(p, w, &sg);
+    if (have) load_q(sg);
+    while (have) {
       if (sg.b != cur_b) {
         cur_b = sg.b;
         uint64_t a[2];
@@ -594,21 +627,6 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         anc = s < 32 ? a0 : a1;
       }
       const size_t qrow = ((size_t)sg.b * p.N + s) * p.Hq + (size_t)sg.hkv * p.G + g;
-      {
-        // This row of Q, in the swizzled layout of a TMA load.  (Every MMA of
-        // the stretch before has completed: its last P V was waited for.)
-        uint4 v[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + qrow * D);
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) v[x] = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-        uint8_t* dst = sQ + i * C::TILE_BYTES + tid * 128;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-          *reinterpret_cast<uint4*>(dst + (x >> 3) * tr::HALF_BYTES + (((x & 7) ^ (tid & 7)) << 4)) =
-              v[x];
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(q_full);
-      }
       const int base = sg.L - p.N;  // keys before the tree
       float m_used = NEG_INF, l = 0.f;
       for (int j = 0; j < sg.n; ++j, ++tc) {
@@ -626,18 +644,24 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           // bad pages) can hold anything: they are cleared, since 0 * NaN in
           // P V would reach every row.
           const Mask128 any = tile_mask(base - kv0, used), fine = sound_keys(bad, p.box);
-          const uint64_t keep = tid < 64 ? any.lo & fine.lo : any.hi & fine.hi;
+          // This warp's 32 rows, two at a time, a row by D/8 lanes.
+          const uint64_t keep64 = wq < 2 ? any.lo & fine.lo : any.hi & fine.hi;
+          uint32_t clear = ~(uint32_t)(wq & 1 ? keep64 >> 32 : keep64);
           const uint32_t cv = 2 * tc + 1;
           const uint32_t on = C::PAIRED && j + 1 < sg.n ? cv + 1 : cv;  // V's barrier
           if (!(ok = mbar_wait<false>(&full[on % NSTAGE], (on / NSTAGE) & 1, abort_flag,
                                       &g_tree_err, 10)))
             break;
-          if (!(keep >> (tid & 63) & 1)) {
-            uint8_t* vr = sKV + (cv % NSTAGE) * C::TILE_BYTES + tid * 128;
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x)
-              *reinterpret_cast<uint4*>(vr + (x >> 3) * tr::HALF_BYTES + (x & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+          const int x = lane % (D / 8);
+          uint8_t* const vt = sKV + (cv % NSTAGE) * C::TILE_BYTES + (x >> 3) * tr::HALF_BYTES +
+                              wq * 32 * 128 + (x & 7) * 16;
+          while (clear) {
+            const int ra = __ffs(clear) - 1;
+            clear &= clear - 1;
+            const int rb = clear ? __ffs(clear) - 1 : ra;
+            clear &= clear - 1;
+            *reinterpret_cast<uint4*>(vt + (lane / (D / 8) & 1 ? rb : ra) * 128) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -749,6 +773,9 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         mbar_arrive(&p_full[i]);
       }
       if (!ok) break;
+      TreeSeg next;
+      have = tree_next(p, w, &next);
+      if (have) load_q(next);
       if (!(ok = mbar_wait<false>(&pv_done[i], (MT == 1 ? tc - 1 : seg) & 1, abort_flag,
                                   &g_tree_err, 15)))
         break;
@@ -763,13 +790,14 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           m_used = NEG_INF;
         }
         const bool whole = sg.t0 == 0 && sg.n == sg.T;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1)) * p.rt_rows + rr;
+        const size_t part = (size_t)blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
+        const size_t tile0 = part * (D / 4) * p.rt_rows + rr;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (row_ok) {
           if (whole) {
             if (p.lse) p.lse[qrow] = l > 0.f ? 0.6931471805599453f * (m_used + log2f(l)) : NEG_INF;
           } else {
-            reinterpret_cast<float2*>(p.part_ml)[slot] = make_float2(m_used, l);
+            reinterpret_cast<float2*>(p.part_ml)[part * p.rt_rows + rr] = make_float2(m_used, l);
           }
         }
 #pragma unroll
@@ -793,15 +821,19 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
               dst[x] = make_uint4(k[0], k[1], k[2], k[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D + q * 32);
+            // [column / 4][row] of 16 bytes: the lanes' rows side by side.
+            float4* dst = reinterpret_cast<float4*>(p.part_o) + tile0 + (size_t)q * 8 * p.rt_rows;
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              dst[x] = live ? make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3])
-                            : make_uint4(0u, 0u, 0u, 0u);
+              dst[(size_t)x * p.rt_rows] =
+                  live ? make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                     __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
       }
       tc_fence_before();
+      sg = next;
     }
   }
   __syncwarp();
@@ -822,80 +854,129 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
 }
 
 // Merge of the units that several groups share, and zeros for padding
-// sequences: one warp per output row, lane l holding columns [l D/32, ...).
-// The partials are loaded four at a time and merged online.
-constexpr int kTreeRowWarps = 8;
-template <int D, typename T>
-__global__ void __launch_bounds__(kTreeRowWarps * 32)
+// sequences.  A thread takes 16 columns of a row, the lanes of a warp 32 rows of
+// one (sequence, kv head), so that loads are as wide as the split kernel's
+// stores; the partials' loads run kMergeAhead partials ahead, merged online
+// (running max M, output and sum rescaled when it grows).
+// KS = 1: a thread walks all of its row's partials.  KS = 8: the block's 8 warps
+// share one set of 32 rows x 16 columns, each every 8th partial: with few rows
+// a long cache leaves each of them up to one partial per SM.
+constexpr int kMergeWarps = 8;
+template <int D, typename T, int KS>
+__global__ void __launch_bounds__(kMergeWarps * 32)
     tree_merge_kernel(const __grid_constant__ TreeParams p, int rt_size) {
   pdl_launch_dependents();
   pdl_wait_primary();
-  constexpr int CPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const size_t row = (size_t)blockIdx.x * kTreeRowWarps + (threadIdx.x >> 5);  // (b, s, hq)
-  const size_t per_b = (size_t)p.N * p.Hq;
-  if (row >= (size_t)p.B * per_b) return;
-  const int b = (int)(row / per_b), x = (int)(row - (size_t)b * per_b);
-  const int s = x / p.Hq, hq = x - s * p.Hq, hkv = hq / p.G;
-  const int r = s * p.G + (hq - hkv * p.G), rt = r / rt_size;
-  const long long first = p.start[b], total = p.start[p.B];
-  const long long T_b = (p.start[b + 1] - first) / p.Hkv;
-  float M = -INFINITY, den = 0.f, acc[CPL];
-#pragma unroll
-  for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+  constexpr int NC = D / 16;  // column chunks of a row
+  constexpr int kMergeAhead = KS > 1 ? 4 : 2;
+  __shared__ float sM[KS > 1 ? KS : 1][32], sDen[KS > 1 ? KS : 1][32];
+  __shared__ float sAcc[KS > 1 ? KS : 1][16][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Blocks of 32-row sets: KS = 1 takes 8 / NC sets, KS = 8 a chunk of one.
+  const int sets = (p.rows + 31) / 32;
+  int unit, set, chunk;
+  if constexpr (KS == 1) {
+    const int x = blockIdx.x * (kMergeWarps / NC) + warp / NC;
+    unit = x / sets;
+    set = x - unit * sets;
+    chunk = warp % NC;
+    if (unit >= p.B * p.Hkv) return;
+  } else {
+    const int x = blockIdx.x / NC;
+    unit = x / sets;
+    set = x - unit * sets;
+    chunk = blockIdx.x - x * NC;
+  }
+  const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
+  const long long first = p.start[b], after = p.start[b + 1], total = p.start[p.B];
+  const int T_b = div_small(after - first, p.Hkv);
+  int g0 = 0, g1 = -1;  // groups of the unit's tiles
   if (T_b > 0) {
-    const long long u0 = first + hkv * T_b, u1 = u0 + T_b - 1;
+    const long long u0 = first + (long long)hkv * T_b, u1 = u0 + T_b - 1;
     // Group of tile t: the largest g with total * g / G <= t.
     const long long G = tree_groups(p, total);
-    const int g0 = (int)(((u0 + 1) * G - 1) / total);
-    const int g1 = (int)(((u1 + 1) * G - 1) / total);
+    g0 = (int)((u0 + 1) * G > 0xffffffffll ? ((u0 + 1) * G - 1) / total
+                                           : (uint32_t)((u0 + 1) * G - 1) / (uint32_t)total);
+    g1 = (int)((u1 + 1) * G > 0xffffffffll ? ((u1 + 1) * G - 1) / total
+                                           : (uint32_t)((u1 + 1) * G - 1) / (uint32_t)total);
     if (g0 == g1) return;  // finished in place
-    for (int k0 = g0; k0 <= g1; k0 += 4) {
-      float2 ml[4];
-      float ov[4][CPL];
+  }
+  const int r = set * 32 + lane;
+  const bool real = r < p.rows;
+  const int rt = real ? r / rt_size : 0, rr = real ? r - rt * rt_size : 0;
+  float M = -INFINITY, den = 0.f, acc[16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = k0 + u;
-        ml[u] = make_float2(-INFINITY, 0.f);
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  auto scale = [&](float m) {  // the weight of values against max m
+    if (m > M) {
+      const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+      den *= f;
 #pragma unroll
-        for (int e = 0; e < CPL; ++e) ov[u][e] = 0.f;
-        if (k <= g1) {
-          const size_t slot = (((size_t)k * p.n_rt + rt) * 2 + (k == g0 ? 1 : 0)) * p.rt_rows +
-                              (r - rt * rt_size);
-          ml[u] = reinterpret_cast<const float2*>(p.part_ml)[slot];
-          const float* src = p.part_o + slot * D + lane * CPL;
-          if constexpr (CPL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            ov[u][0] = v.x; ov[u][1] = v.y; ov[u][2] = v.z; ov[u][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            ov[u][0] = v.x; ov[u][1] = v.y;
-          }
-        }
+      for (int e = 0; e < 16; ++e) acc[e] *= f;
+      M = m;
+    }
+    return m == -INFINITY ? 0.f : fast_exp2(m - M);
+  };
+  float2 ml[kMergeAhead];
+  float4 ov[kMergeAhead][4];
+  auto load = [&](int k, int u) {
+    ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ov[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k <= g1 && real) {
+      const size_t part = ((size_t)k * p.n_rt + rt) * 2 + (k == g0 ? 1 : 0);
+      ml[u] = reinterpret_cast<const float2*>(p.part_ml)[part * p.rt_rows + rr];
+      const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                          (part * (D / 4) + chunk * 4) * p.rt_rows + rr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ov[u][e] = src[(size_t)e * p.rt_rows];
+    }
+  };
+  const int k0 = g0 + (KS > 1 ? warp : 0);
+#pragma unroll
+  for (int u = 0; u < kMergeAhead; ++u) load(k0 + u * KS, u);
+  for (int k = k0; k <= g1; k += kMergeAhead * KS) {
+#pragma unroll
+    for (int u = 0; u < kMergeAhead; ++u) {
+      const float wt = scale(ml[u].y > 0.f ? ml[u].x : -INFINITY);
+      den += wt * ml[u].y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[4 * e] += wt * ov[u][e].x;
+        acc[4 * e + 1] += wt * ov[u][e].y;
+        acc[4 * e + 2] += wt * ov[u][e].z;
+        acc[4 * e + 3] += wt * ov[u][e].w;
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float m_u = ml[u].y > 0.f ? ml[u].x : -INFINITY;
-        if (m_u > M) {
-          const float f = M == -INFINITY ? 0.f : fast_exp2(M - m_u);
-          den *= f;
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) acc[e] *= f;
-          M = m_u;
-        }
-        const float wt = m_u == -INFINITY ? 0.f : fast_exp2(m_u - M);
-        den += wt * ml[u].y;
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) acc[e] += wt * ov[u][e];
-      }
+      load(k + (kMergeAhead + u) * KS, u);
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  T* dst = static_cast<T*>(p.o) + row * D + lane * CPL;
+  if constexpr (KS > 1) {
+    sM[warp][lane] = M;
+    sDen[warp][lane] = den;
 #pragma unroll
-  for (int e = 0; e < CPL; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = TreeType<T>::pack(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0)
+    for (int e = 0; e < 16; ++e) sAcc[warp][e][lane] = acc[e];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll 1
+    for (int i = 1; i < KS; ++i) {
+      const float wt = scale(sM[i][lane]);
+      den += wt * sDen[i][lane];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] += wt * sAcc[i][e][lane];
+    }
+  }
+  if (!real) return;
+  const int s = r / p.G;
+  const size_t row = ((size_t)b * p.N + s) * p.Hq + (size_t)hkv * p.G + (r - s * p.G);
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + chunk * 16);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    dst[e] = make_uint4(TreeType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
+                        TreeType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
+                        TreeType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
+                        TreeType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+  if (p.lse && chunk == 0)
     p.lse[row] = den > 0.f ? 0.6931471805599453f * (M + log2f(den)) : -INFINITY;
 }
 
@@ -920,7 +1001,7 @@ static TreePlan tree_host_plan(int B, int N, int Hq, int Hkv, long long cap, int
   const size_t slots = (size_t)t.groups * t.n_rt * 2 * t.rt_rows;
   t.o_floats = slots * D;
   t.ml_floats = slots * 2;
-  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 3) * sizeof(long long);
+  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 5) * sizeof(long long);
   return t;
 }
 
@@ -937,9 +1018,11 @@ static int launch_tree_t(const TreeParams& p, const CUtensorMap& tk, const CUten
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     // The split kernel's carveout, so that merge blocks become resident beside it.
-    e = cudaFuncSetAttribute(tree_merge_kernel<D, T>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             (int)cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
+    for (auto k : {tree_merge_kernel<D, T, 1>, tree_merge_kernel<D, T, kMergeWarps>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               (int)cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 64) __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
   }
   cudaLaunchAttribute attr[1];
@@ -954,11 +1037,17 @@ static int launch_tree_t(const TreeParams& p, const CUtensorMap& tk, const CUten
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, T, MT>, tk, tv, p);
   if (e != cudaSuccess) return e;
-  const size_t rows = (size_t)p.B * p.N * p.Hq;
-  cfg.gridDim = dim3((unsigned)((rows + kTreeRowWarps - 1) / kTreeRowWarps), 1, 1);
-  cfg.blockDim = dim3(kTreeRowWarps * 32, 1, 1);
+  constexpr int NC = D / 16;
+  const int sets = p.B * p.Hkv * ((p.rows + 31) / 32);
+  // Both kernels together, KS = 1 / 8: 64 rows of 22 partials 16.6 / 11.8 us, 512
+  // rows of 5 partials 38.3 / 36.8 us, 2048 rows of 19 partials 68.4 / 64.1 us;
+  // 8192 rows of 5 partials 189.6 / 198.7 us, 32768 rows of 2 140.9 / 174.7 us.
+  const bool split = sets * NC <= 4 * (sm_count() > 0 ? sm_count() : 148);
+  cfg.gridDim = dim3((unsigned)(split ? sets * NC : (sets * NC + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T>, p, (int)C::RT);
+  return split ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T, kMergeWarps>, p, (int)C::RT)
+               : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T, 1>, p, (int)C::RT);
 }
 
 template <int D, typename T>
@@ -1012,8 +1101,8 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   if (N > fa::tr::MAX_N) return FA_ERR_UNSUPPORTED;
   if (B == 0 || N == 0 || Hq == 0) return FA_OK;
   if (Hkv == 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-  // Row indexes and the merge's grid fit 31 bits with 8 rows per block.
-  if ((int64_t)B * N * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
+  // Row indexes and the merge's grid (up to D / 16 blocks per row) fit 31 bits.
+  if ((int64_t)B * N * Hq > INT32_MAX / 8) return FA_ERR_INVALID_ARG;
   if ((int64_t)max_pages * page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
   if (!al(q, 16) || !al(o, 16)) return FA_ERR_INVALID_ARG;
   if (lse && !al(lse, 4)) return FA_ERR_INVALID_ARG;
@@ -1061,9 +1150,9 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   cudaError_t e = fa::scratch_alloc(&scratch, t.bytes, stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "tree decode scratch");
   p.start = static_cast<long long*>(scratch);
-  // (B + 1) 8-byte entries, then the partials 16-byte aligned.
+  // (B + 1) 8-byte entries, then the partials 32-byte aligned.
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
-                                      (((size_t)B + 1) * 8 + 15) / 16 * 16);
+                                      (((size_t)B + 1) * 8 + 31) / 32 * 32);
   p.part_ml = p.part_o + t.o_floats;
   int r;
   const bool bf16 = dtype == FA_BF16;

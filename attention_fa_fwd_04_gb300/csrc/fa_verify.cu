@@ -21,7 +21,11 @@
 //
 // Bound: two rows of V floats per sequence (the node where its walk stops, and
 // nodes where more than one child is tried), once from HBM and for further
-// rejected siblings from L2; for few sequences, latency.  The tests themselves
+// rejected siblings from L2; in fact the latency of the passes over a row that
+// the sequence with the most rejections needs one after another: 64 trees of 32
+// nodes over 128000 tokens take 43 us (1.5 TB/s of the rows where they stop;
+// about 12000 clocks per pass, at most five passes), one chain of 5 over 32000
+// tokens 6.5 us.  The tests themselves
 // read single elements: those of all nodes are fetched at once, and the walk
 // runs on shared memory, in one warp of each CTA.  A cluster of up to 8 CTAs
 // takes one sequence: every CTA walks (the same way), and for a mass each sums
@@ -42,6 +46,12 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BLOCKS_PER_SM = 2;
 constexpr int MAX_N = 64;
+// Each warp streams its part of a row through a ring of its own: 256 elements
+// of p and of q per stage.
+constexpr int STAGES = 3;
+constexpr int STAGE_ELEMS = 256;
+constexpr int RING_BYTES = STAGES * 2 * STAGE_ELEMS * 4;
+constexpr int SMEM = WARPS * RING_BYTES + WARPS * STAGES * 8;
 }  // namespace vf
 
 struct VerifyParams {
@@ -144,16 +154,26 @@ __device__ __forceinline__ Pair2 two_sum2(float2 a, float2 b) {
   const float2 s = __fadd2_rn(a, b), t = sub2(s, a);
   return {s, __fadd2_rn(sub2(a, sub2(s, t)), sub2(b, t))};
 }
+// max(p - c q, 0), as a pair whose lower part need not be below half a step.
+// Where the difference counts, p is at least the rounded product, and its
+// rounding error takes two more subtractions.  ONE: c = 1.
+template <bool ONE>
 __device__ __forceinline__ Pair2 residual2(float2 p, Pair c, float2 q) {
-  const float2 nh = __fmul2_rn(both(-c.hi), q);
-  const float2 l = __ffma2_rn(both(c.lo), q, __ffma2_rn(both(c.hi), q, nh));
-  const Pair2 d = two_sum2(p, nh);
-  const float2 lo = sub2(d.lo, l);
   Pair2 r;
-  r.hi = __fadd2_rn(d.hi, lo);
-  r.lo = sub2(lo, sub2(r.hi, d.hi));
-  if (!(r.hi.x > 0.f)) r.hi.x = r.lo.x = 0.f;
-  if (!(r.hi.y > 0.f)) r.hi.y = r.lo.y = 0.f;
+  float2 sum;
+  if constexpr (ONE) {
+    r.hi = sub2(p, q);
+    r.lo = sub2(sub2(p, r.hi), q);
+    sum = r.hi;
+  } else {
+    const float2 nh = __fmul2_rn(both(-c.hi), q);
+    const float2 l = __ffma2_rn(both(c.lo), q, __ffma2_rn(both(c.hi), q, nh));
+    r.hi = __fadd2_rn(p, nh);
+    r.lo = sub2(sub2(nh, sub2(r.hi, p)), l);
+    sum = __fadd2_rn(r.hi, r.lo);
+  }
+  if (!(sum.x > 0.f)) r.hi.x = r.lo.x = 0.f;
+  if (!(sum.y > 0.f)) r.hi.y = r.lo.y = 0.f;
   return r;
 }
 
@@ -180,15 +200,25 @@ __device__ __forceinline__ float4 load4(const float* row, int v, int end) {
                        v + 3 * ST < end ? row[v + 3 * ST] : 0.f);
   }
 }
-template <bool DRAFT, int ST>
+__device__ __forceinline__ float4 clean4(float4 a) {
+  return make_float4(clean(a.x), clean(a.y), clean(a.z), clean(a.w));
+}
+// The largest of the four's bits: below those of infinity if all of them are
+// probabilities as they stand.
+__device__ __forceinline__ uint32_t bits4(float4 a) {
+  return max(max(__float_as_uint(a.x), __float_as_uint(a.y)),
+             max(__float_as_uint(a.z), __float_as_uint(a.w)));
+}
+// What is left of four clean elements.  LEVEL: rj.n where it is 0 or 1, else 2.
+template <bool DRAFT, int ST, int LEVEL>
 __device__ __forceinline__ void left4(float4 a, float4 d, int v, const Rejected& rj,
                                       Pair2 (&r)[2]) {
-  r[0] = {make_float2(clean(a.x), clean(a.y)), both(0.f)};
-  r[1] = {make_float2(clean(a.z), clean(a.w)), both(0.f)};
-  if (rj.n == 0) return;
-  if constexpr (DRAFT) {
-    r[0] = residual2(r[0].hi, rj.c, make_float2(clean(d.x), clean(d.y)));
-    r[1] = residual2(r[1].hi, rj.c, make_float2(clean(d.z), clean(d.w)));
+  r[0] = {make_float2(a.x, a.y), both(0.f)};
+  r[1] = {make_float2(a.z, a.w), both(0.f)};
+  if constexpr (LEVEL == 0) {
+  } else if constexpr (DRAFT) {
+    r[0] = residual2<LEVEL == 1>(r[0].hi, rj.c, make_float2(d.x, d.y));
+    r[1] = residual2<LEVEL == 1>(r[1].hi, rj.c, make_float2(d.z, d.w));
   } else {
     for (int k = 0; k < rj.n; ++k) {
       const int o = rj.token[k] - v;
@@ -200,50 +230,115 @@ __device__ __forceinline__ void left4(float4 a, float4 d, int v, const Rejected&
   }
 }
 
-// Sum of what is left in [va, vb) of a row, over the warp: groups of 128
-// elements, four at a time, each four's loads ahead of the last four's sums.
-template <bool DRAFT, bool VEC>
-__device__ __forceinline__ Pair sum_left(const float* pr, const float* qr, int va, int vb,
-                                         const Rejected& rj) {
-  constexpr int G = DRAFT ? 2 : 4, ST = VEC ? 1 : 32;
-  const int lane = threadIdx.x & 31;
-  const bool use_q = DRAFT && rj.n > 0;
-  int v = va + (VEC ? lane * 4 : lane);
-  Pair2 acc{both(0.f), both(0.f)};
-  float4 a[G], d[G], an[G], dn[G];
-  auto fetch = [&](int at, float4 (&x)[G], float4 (&y)[G]) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      x[i] = load4<VEC, ST>(pr, at + i * 128, vb);
-      if constexpr (DRAFT)
-        if (use_q) y[i] = load4<VEC, ST>(qr, at + i * 128, vb);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < G; ++i) d[i] = dn[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  fetch(v, a, d);
-  for (int w0 = va; w0 < vb; w0 += 128 * G, v += 128 * G) {
-    fetch(v + 128 * G, an, dn);
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      Pair2 r[2];
-      left4<DRAFT, ST>(a[i], d[i], v + i * 128, rj, r);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const Pair2 s = two_sum2(acc.hi, r[e].hi);
-        acc = {s.hi, __fadd2_rn(acc.lo, __fadd2_rn(s.lo, r[e].lo))};
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      a[i] = an[i];
-      d[i] = dn[i];
-    }
-  }
-  Pair t = add(fast_two_sum(acc.hi.x, acc.lo.x), fast_two_sum(acc.hi.y, acc.lo.y));
+__device__ __forceinline__ Pair lane_sum(const Pair2& a) {
+  return add(fast_two_sum(a.hi.x, a.lo.x), fast_two_sum(a.hi.y, a.lo.y));
+}
+__device__ __forceinline__ Pair warp_sum(Pair t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
   return t;
+}
+__device__ __forceinline__ void gather(Pair2& acc, const Pair2 (&r)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const Pair2 s = two_sum2(acc.hi, r[e].hi);
+    acc = {s.hi, __fadd2_rn(acc.lo, __fadd2_rn(s.lo, r[e].lo))};
+  }
+}
+
+// Sum of what is left in [va, vb) of a row, over the warp.  Rows that are not
+// aligned: plain loads, four per lane and 128 elements.
+template <bool DRAFT>
+__device__ __forceinline__ Pair sum_plain(const float* pr, const float* qr, int va, int vb,
+                                          const Rejected& rj) {
+  const bool use_q = DRAFT && rj.n > 0;
+  Pair2 acc{both(0.f), both(0.f)};
+#pragma unroll 2
+  for (int v = va + (threadIdx.x & 31); v < vb; v += 128) {
+    const float4 a = clean4(load4<false, 32>(pr, v, vb));
+    const float4 d = use_q ? clean4(load4<false, 32>(qr, v, vb)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    Pair2 r[2];
+    left4<DRAFT, 32, 2>(a, d, v, rj, r);
+    gather(acc, r);
+  }
+  return warp_sum(lane_sum(acc));
+}
+// Aligned rows: bulk copies into the warp's ring, STAGES ahead of the sums.
+struct Ring {
+  uint8_t* data;
+  uint64_t* full;
+  uint32_t n;  // stages used so far
+  volatile int* abort_flag;
+};
+template <bool DRAFT, int LEVEL>
+__device__ __forceinline__ Pair sum_ring(const float* pr, const float* qr, int va, int vb,
+                                         const Rejected& rj, Ring& ring) {
+  constexpr int E = vf::STAGE_ELEMS;
+  const int lane = threadIdx.x & 31;
+  constexpr bool use_q = DRAFT && LEVEL > 0;
+  const int n = (vb - va + E - 1) / E;
+  auto fetch = [&](int i) {
+    if (i >= n || lane != 0) return;
+    const int v = va + i * E, st = (ring.n + i) % vf::STAGES;
+    const uint32_t bytes = (uint32_t)(vb - v < E ? vb - v : E) * 4;
+    uint8_t* to = ring.data + st * 2 * E * 4;
+    mbar_arrive_expect_tx(&ring.full[st], use_q ? 2 * bytes : bytes);
+    bulk_load(to, pr + v, bytes, &ring.full[st]);
+    if (use_q) bulk_load(to + E * 4, qr + v, bytes, &ring.full[st]);
+  };
+  // An accumulator per 128 elements of a stage: independent chains.
+  Pair2 acc[E / 128];
+#pragma unroll
+  for (int g = 0; g < E / 128; ++g) acc[g] = {both(0.f), both(0.f)};
+  for (int i = 0; i < vf::STAGES; ++i) fetch(i);
+  int i = 0;
+  for (; i < n; ++i) {
+    const uint32_t k = ring.n + i;
+    if (!mbar_wait<true>(&ring.full[k % vf::STAGES], (k / vf::STAGES) & 1, ring.abort_flag,
+                         &g_verify_err, 22))
+      break;
+    __syncwarp();
+    const float* at = reinterpret_cast<const float*>(ring.data + (k % vf::STAGES) * 2 * E * 4);
+    const int v = va + i * E + lane * 4;
+    float4 a[E / 128], d[E / 128];
+    uint32_t top = 0;
+#pragma unroll
+    for (int g = 0; g < E / 128; ++g) {
+      a[g] = *reinterpret_cast<const float4*>(at + g * 128 + lane * 4);
+      // (Past the row's end the stage holds an earlier one's values.)
+      if (v + g * 128 >= vb) a[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+      top = max(top, bits4(a[g]));
+      d[g] = a[g];
+      if constexpr (use_q) {
+        d[g] = *reinterpret_cast<const float4*>(at + E + g * 128 + lane * 4);
+        if (v + g * 128 >= vb) d[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        top = max(top, bits4(d[g]));
+      }
+    }
+    if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+#pragma unroll
+      for (int g = 0; g < E / 128; ++g) {
+        a[g] = clean4(a[g]);
+        d[g] = clean4(d[g]);
+      }
+    }
+    Pair2 r[E / 128][2];
+#pragma unroll
+    for (int g = 0; g < E / 128; ++g) left4<DRAFT, 1, LEVEL>(a[g], d[g], v + g * 128, rj, r[g]);
+#pragma unroll
+    for (int g = 0; g < E / 128; ++g) gather(acc[g], r[g]);
+    __syncwarp();  // the stage has been read
+    fetch(i + vf::STAGES);
+  }
+  // A wait that gave up: the loads in flight land before anything else.
+  for (int j = i; j < n && j < i + vf::STAGES; ++j)
+    mbar_wait_drain(&ring.full[(ring.n + j) % vf::STAGES], ((ring.n + j) / vf::STAGES) & 1);
+  __syncwarp();
+  ring.n += i < n ? (i + vf::STAGES < n ? i + vf::STAGES : n) : n;
+  Pair t = lane_sum(acc[0]);
+#pragma unroll
+  for (int g = 1; g < E / 128; ++g) t = add(t, lane_sum(acc[g]));
+  return warp_sum(t);
 }
 
 // Whole warp: inclusive sums of n <= 32 values, one per lane.
@@ -282,7 +377,10 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   __shared__ int s_cur, s_nrej;
   __shared__ bool s_last, s_known;
   __shared__ uint64_t s_path;
+  __shared__ uint32_t s_first[2];
   __shared__ Pair s_c;
+  __shared__ int s_abort;
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
   cluster_arrive();  // (waited for below: no CTA is written to before it runs)
   pdl_wait_primary();
@@ -291,6 +389,16 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   const int b = blockIdx.x / CL;
   const int N = p.N, V = p.V;
   const size_t node0 = (size_t)b * N;
+  Ring ring{smem + warp * vf::RING_BYTES,
+            reinterpret_cast<uint64_t*>(smem + vf::WARPS * vf::RING_BYTES) + warp * vf::STAGES, 0,
+            &s_abort};
+  if constexpr (VEC) {
+    if (lane == 0) {
+      for (int i = 0; i < vf::STAGES; ++i) mbar_init(&ring.full[i], 1);
+      fence_mbar_init();
+    }
+    if (tid == 0) s_abort = 0;
+  }
 
   if (tid < N) {
     // Node tid: an edge that the walk may take, or parent -2.
@@ -304,8 +412,18 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     const bool edge = tid > 0 && par >= 0;
     s_parent[tid] = edge ? par : -2;
     s_token[tid] = x;
-    s_px[tid] = edge ? clean(p.p[(node0 + par) * V + x]) : 0.f;
-    s_qx[tid] = DRAFT ? (edge ? clean(p.q[(node0 + par) * V + x]) : 0.f) : 1.f;
+    const float px = edge ? clean(p.p[(node0 + par) * V + x]) : 0.f;
+    const float qx = DRAFT ? (edge ? clean(p.q[(node0 + par) * V + x]) : 0.f) : 1.f;
+    s_px[tid] = px;
+    s_qx[tid] = qx;
+  }
+  __syncthreads();
+  if (tid < vf::MAX_N) {
+    // Every node's test as a first child (Z = 1).
+    const bool yes =
+        tid < N && above(Pair{s_px[tid], 0.f}, mul(Pair{s_u[tid], 0.f}, Pair{s_qx[tid], 0.f}));
+    const uint32_t w = __ballot_sync(0xffffffffu, yes);
+    if (lane == 0) s_first[warp] = w;
   }
   __syncthreads();
   cluster_wait();
@@ -318,7 +436,13 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
     const float* pr = p.p + (node0 + cur) * V;
     const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-    const Pair s = sum_left<DRAFT, VEC>(pr, qr, va, vb, rj);
+    Pair s;
+    if constexpr (VEC)
+      s = rj.n == 0   ? sum_ring<DRAFT, 0>(pr, qr, va, vb, rj, ring)
+          : rj.n == 1 ? sum_ring<DRAFT, 1>(pr, qr, va, vb, rj, ring)
+                      : sum_ring<DRAFT, 2>(pr, qr, va, vb, rj, ring);
+    else
+      s = sum_plain<DRAFT>(pr, qr, va, vb, rj);
     if (lane == 0) s_warp[warp] = s;
     __syncthreads();
     ++pass;
@@ -348,6 +472,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   Rejected rj{0, {0.f, 0.f}, s_rej};
   uint64_t path = 1, kids = warp == 0 ? children(0) : 0;
   Pair Z{1.f, 0.f};
+  const uint64_t first_yes = s_first[0] | (uint64_t)s_first[1] << 32;
   for (;;) {
     if (warp == 0) {
       while (kids) {
@@ -357,16 +482,20 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
         }
         const int c = __ffsll((long long)kids) - 1;
         kids &= kids - 1;
-        const int x = s_token[c];
         Pair r{s_px[c], 0.f};
-        if constexpr (DRAFT) {
-          if (rj.n > 0) r = residual(r.hi, rj.c, s_qx[c]);
+        bool yes;
+        if (rj.n == 0) {
+          yes = first_yes >> c & 1;
         } else {
-          for (int i = 0; i < rj.n; ++i)
-            if (s_rej[i] == x) r.hi = 0.f;
+          if constexpr (DRAFT) {
+            r = residual(r.hi, rj.c, s_qx[c]);
+          } else {
+            for (int i = 0; i < rj.n; ++i)
+              if (s_rej[i] == s_token[c]) r.hi = 0.f;
+          }
+          yes = above(r, mul(mul(Pair{s_u[c], 0.f}, Pair{s_qx[c], 0.f}), Z));
         }
-        const Pair bar = mul(mul(Pair{s_u[c], 0.f}, Pair{s_qx[c], 0.f}), Z);
-        if (above(r, bar)) {
+        if (yes) {
           cur = c;
           path |= 1ull << c;
           kids = children(c);
@@ -378,7 +507,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
           if constexpr (DRAFT) {
             rj.c = add(rj.c, Z);
           } else {
-            if (lane == 0) s_rej[rj.n] = x;
+            if (lane == 0) s_rej[rj.n] = s_token[c];
             __syncwarp();
             Z = add(Z, Pair{-r.hi, 0.f});
           }
@@ -436,12 +565,13 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   int found = INT32_MAX, last_v = -1;
   for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * vf::WARPS) {
     const int v = w0 + warp * 128 + lane * 4;
-    const float4 a = load4<VEC, 1>(pr, v, vb);
-    const float4 d = DRAFT && rj.n > 0 ? load4<VEC, 1>(qr, v, vb) : a;
+    const float4 a = clean4(load4<VEC, 1>(pr, v, vb));
+    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (DRAFT && rj.n > 0) d = clean4(load4<VEC, 1>(qr, v, vb));
     Pair2 r2[2];
-    left4<DRAFT, 1>(a, d, v, rj, r2);
-    const Pair r[4] = {{r2[0].hi.x, r2[0].lo.x}, {r2[0].hi.y, r2[0].lo.y},
-                       {r2[1].hi.x, r2[1].lo.x}, {r2[1].hi.y, r2[1].lo.y}};
+    left4<DRAFT, 1, 2>(a, d, v, rj, r2);
+    const Pair r[4] = {fast_two_sum(r2[0].hi.x, r2[0].lo.x), fast_two_sum(r2[0].hi.y, r2[0].lo.y),
+                       fast_two_sum(r2[1].hi.x, r2[1].lo.x), fast_two_sum(r2[1].hi.y, r2[1].lo.y)};
     const Pair own = add(add(r[0], r[1]), add(r[2], r[3]));
     const Pair inc = scan(own, 32);
     __syncthreads();  // (s_warp and s_pick have been read)
@@ -563,7 +693,7 @@ __global__ void __launch_bounds__(cp::THREADS)
 
 template <typename P>
 static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, cudaStream_t stream,
-                                    const P& p, int cluster = 0) {
+                                    const P& p, int cluster = 0, int smem = 0) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -574,11 +704,14 @@ static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
+
+int set_verify_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
 
 int read_verify_error(unsigned int* out, int reset) {
   unsigned int v = 0;
@@ -621,20 +754,44 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   p.next = next_token;
   p.N = N;
   p.V = V;
-  // As many CTAs per sequence as leave all of them resident at once.
+  // CTAs per sequence: no more than have a stage for each of their warps (64
+  // sequences of 5000 tokens: 2 CTAs 15.7 us, 8 22.6 us), and all resident at
+  // once (128 of 32000: 4 CTAs 29.5 us, 8 41.4 us), or twice that where a warp's
+  // part would pass 1024 tokens (64 of 128000: 8 CTAs 43.0 us, 4 52.5 us).
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
+  const long long slots = (long long)sms * fa::vf::BLOCKS_PER_SM;
+  auto part_of = [&](int cluster) {
+    const int n = cluster * fa::vf::WARPS;
+    return ((V + n - 1) / n + 127) / 128 * 128;
+  };
   p.cluster = fa::vf::CLUSTER;
-  while (p.cluster > 1 && (long long)B * p.cluster > (long long)sms * fa::vf::BLOCKS_PER_SM)
+  while (p.cluster > 1 &&
+         (part_of(p.cluster / 2) <= fa::vf::STAGE_ELEMS || B * p.cluster > 2 * slots ||
+          (B * p.cluster > slots && part_of(p.cluster / 2) <= 1024)))
     p.cluster /= 2;
-  const int parts = p.cluster * fa::vf::WARPS;
-  p.part = ((V + parts - 1) / parts + 127) / 128 * 128;
+  p.part = part_of(p.cluster);
   const bool vec = V % 4 == 0 && al(target_probs, 16) && (!draft_probs || al(draft_probs, 16));
   const dim3 grid((unsigned)B * p.cluster);
   void (*kernel)(fa::VerifyParams) =
       draft_probs ? (vec ? fa::verify_kernel<true, true> : fa::verify_kernel<true, false>)
                   : (vec ? fa::verify_kernel<false, true> : fa::verify_kernel<false, false>);
-  const cudaError_t e =
-      fa::launch_dependent(kernel, grid, fa::vf::THREADS, stream, p, p.cluster);
+  cudaError_t e = cudaSuccess;
+  if (vec) {
+    static int attr_set[64] = {0};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess &&
+        (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE))) {
+      for (auto k : {fa::verify_kernel<true, true>, fa::verify_kernel<false, true>})
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::vf::SMEM);
+      if (e == cudaSuccess && dev >= 0 && dev < 64)
+        __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
+    }
+  }
+  if (e == cudaSuccess)
+    e = fa::launch_dependent(kernel, grid, fa::vf::THREADS, stream, p, p.cluster,
+                             vec ? fa::vf::SMEM : 0);
   return fa::record_cuda_status(e, "tree verification launch");
 }
 

@@ -406,8 +406,9 @@ int fa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_
  *   dq_weight, dk_weight   [D] fp32, written (summed over tokens and heads in
  *                          a fixed order, so equal calls give equal bits)
  *
- * T == 0 writes zero weight gradients.  Block sums of the weight gradients live
- * in stream-ordered scratch.
+ * Both weight gradients are always written: a side without rows (T == 0, or no
+ * heads) gets zeros.  Block sums of the weight gradients live in stream-ordered
+ * scratch.
  */
 int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
                              const void* k, const void* q_weight, const void* k_weight,
@@ -573,7 +574,8 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
 
 /*
  * fa_set_wait_limit_ns -- time limit of every device-side pipeline wait
- * (mbarrier waits of the prefill, decode, tree decode and backward kernels) on the current
+ * (mbarrier waits of the prefill, decode, backward, norm and rotation, tree decode and
+ * verification kernels) on the current
  * device; ns == 0 restores the default of 2 s.
  *
  * A wait that runs past the limit makes its CTA abort: every warp leaves its
@@ -584,11 +586,13 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
  * default is far above any wait of a healthy call; a short limit serves as a
  * watchdog, or in tests to make the timeout path run.
  *
- * Below 1 ms the limit is a watchdog: the decode and tree decode kernels, and the dense
+ * Below 1 ms the limit is a watchdog: the decode, norm and rotation and verification
+ * kernels, the tree decode's loads, and the dense
  * prefill (whose launches then use a polling instantiation of the kernel),
  * check it at every probe of every wait.  The packed-sequence prefill and the
  * backward kernels keep suspending probes of about 4 us each, so there a wait
- * trips the watchdog only once it has lasted about two of them.
+ * trips the watchdog only once it has lasted about two of them (so too in the
+ * tree decode's arithmetic).
  *
  * Synchronises the current device and applies to calls enqueued afterwards.
  * Returns FA_OK or FA_ERR_CUDA.
