@@ -25,8 +25,9 @@
 // Loads: a token's heads are contiguous, so each warp fetches steps of up to 16
 // (D = 128) or 32 heads by one bulk copy into a ring of its own in shared
 // memory, two steps ahead of its arithmetic: 128 to 192 KiB in flight per SM
-// whatever the arithmetic's latency.  (Loads into registers, two head groups
-// ahead, held 64 KiB: 4.6 TB/s, half of the issue slots waiting for memory.)
+// whatever the arithmetic's latency.  8192 tokens of 128 + 8 heads, D = 128: 97 us,
+// 5.9 TB/s (84 us at the copy bandwidth); loads into registers, two head groups
+// ahead, held 64 KiB in flight and took 117 us.
 //
 // Angles: positions reach 2^31, where an fp32 product p * inv_freq has no
 // correct bit left.  Each block turns inv_freq once into a 64-bit fixed-point
@@ -52,8 +53,8 @@ constexpr int WARPS = THREADS / 32;
 constexpr int STAGE_BYTES = 4096;
 template <int D, bool BWD>
 struct Cfg {
-  static constexpr int STAGES = BWD ? 2 : 3;  // steps in a warp's ring
-  static constexpr int BLOCKS_PER_SM = BWD ? 3 : 2;
+  static constexpr int STAGES = 3;  // steps in a warp's ring
+  static constexpr int BLOCKS_PER_SM = 2;
   // Heads of a head group (one warp's registers): lanes hold two chunks of 8
   // elements of a head, in the gradient one.
   static constexpr int HPW = (BWD ? 256 : 512) / D;
@@ -242,8 +243,10 @@ struct Turn {
 
 // The gradient's lanes hold one chunk each, so its rotation (back, by the
 // negative angle) is o = x c + y s with y the chunk that holds the pairs' other
-// elements (neighbours: x swapped), read from the ring as well: half the
-// registers, twice the warps, for one more load.
+// elements (neighbours: x swapped), read from the ring as well.  With half the
+// registers per head, two head groups' chains run side by side within 128
+// registers (16384 tokens of 16 + 16 heads: 67.7 us; one after another at 80
+// registers and three blocks per SM 82 us; both chunks in a lane 89 us).
 template <int D, bool IL>
 struct BackMap {
   static constexpr int LPH = D / 8;
@@ -575,9 +578,7 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
                          &g_rope_err, 21))
       break;
     __syncwarp();
-#pragma unroll 1
-    for (int u = 0; u < C::UNITS; ++u) {
-      if (u * C::HPW >= nh) break;  // warp-uniform
+    auto unit = [&](int u) {
       // (A lane past the last head works on what its ring holds, and its
       // terms are left out of the weights' sums.)
       const bool real = u * C::HPW + m.sub < nh;
@@ -611,6 +612,13 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
         }
         *reinterpret_cast<uint4*>(dst + u * C::HPW * D + m.c * 8) = pack8<T>(a);
       }
+    };
+    if (nh == C::HEADS) {
+#pragma unroll 2
+      for (int u = 0; u < C::UNITS; ++u) unit(u);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u * C::HPW < nh; ++u) unit(u);
     }
     __syncwarp();  // the stage has been read
     fetch();
@@ -661,14 +669,15 @@ __global__ void __launch_bounds__(256)
 }
 
 // Steps per task: the fewest rounds of the resident warps, a round costing its
-// steps and, once, the token's cosines, sines and factors (about as much as
-// half a step).
+// steps and, once, the token's cosines, sines and factors.  These count as a
+// quarter of a step: 4096 tokens of 128 + 8 + 8 heads into pages take 52 us so,
+// 55 us when they count as a half or as a sixteenth.
 static void plan_tasks(int tokens, int steps, long long warps, int* spt, int* cpt) {
   long long best = 0;
   for (int c = 1; c <= steps && c <= 64; ++c) {
     const int u = (steps + c - 1) / c;
     if ((steps + u - 1) / u != c) continue;
-    const long long cost = ((long long)tokens * c + warps - 1) / warps * (2 * u + 1);
+    const long long cost = ((long long)tokens * c + warps - 1) / warps * (4 * u + 1);
     if (best == 0 || cost < best) {
       best = cost;
       *spt = u;

@@ -194,7 +194,7 @@ def test_tensor_helpers_refuse(fa):
 ])
 def test_token_strides(fa, shape, stride, ok):
     import torch
-    t = torch.empty(8192, dtype=torch.float16).as_strided(shape, stride)
+    t = torch.empty(32768, dtype=torch.float16).as_strided(shape, stride)
     if ok is None:
         with pytest.raises(ValueError):
             fa._token_stride(t, "x")
