@@ -1038,7 +1038,7 @@ static int launch_tree_t(const TreeParams& p, const CUtensorMap& tk, const CUten
   e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, T, MT>, tk, tv, p);
   if (e != cudaSuccess) return e;
   constexpr int NC = D / 16;
-  const int sets = p.B * p.Hkv * ((p.rows + 31) / 32);
+  const long long sets = (long long)p.B * p.Hkv * ((p.rows + 31) / 32);
   // Both kernels together, KS = 1 / 8: 64 rows of 22 partials 16.6 / 11.8 us, 512
   // rows of 5 partials 38.3 / 36.8 us, 2048 rows of 19 partials 68.4 / 64.1 us;
   // 8192 rows of 5 partials 189.6 / 198.7 us, 32768 rows of 2 140.9 / 174.7 us.
@@ -1101,8 +1101,8 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   if (N > fa::tr::MAX_N) return FA_ERR_UNSUPPORTED;
   if (B == 0 || N == 0 || Hq == 0) return FA_OK;
   if (Hkv == 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-  // Row indexes and the merge's grid (up to D / 16 blocks per row) fit 31 bits.
-  if ((int64_t)B * N * Hq > INT32_MAX / 8) return FA_ERR_INVALID_ARG;
+  // Row indexes and the merge's grid (at most one block per row) fit 31 bits.
+  if ((int64_t)B * N * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
   if ((int64_t)max_pages * page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
   if (!al(q, 16) || !al(o, 16)) return FA_ERR_INVALID_ARG;
   if (lse && !al(lse, 4)) return FA_ERR_INVALID_ARG;

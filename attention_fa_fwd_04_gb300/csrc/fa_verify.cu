@@ -23,9 +23,9 @@
 // nodes where more than one child is tried), once from HBM and for further
 // rejected siblings from L2; in fact the latency of the passes over a row that
 // the sequence with the most rejections needs one after another: 64 trees of 32
-// nodes over 128000 tokens take 43 us (1.5 TB/s of the rows where they stop;
+// nodes over 128000 tokens take 44 us (1.5 TB/s of the rows where they stop;
 // about 12000 clocks per pass, at most five passes), one chain of 5 over 32000
-// tokens 6.5 us.  The tests themselves
+// tokens 5.9 us.  The tests themselves
 // read single elements: those of all nodes are fetched at once, and the walk
 // runs on shared memory, in one warp of each CTA.  A cluster of up to 8 CTAs
 // takes one sequence: every CTA walks (the same way), and for a mass each sums
@@ -42,16 +42,14 @@ __device__ unsigned int g_verify_err = 0;
 
 namespace vf {
 constexpr int CLUSTER = 8;  // CTAs per sequence, at most
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
-constexpr int BLOCKS_PER_SM = 2;
+constexpr int SM_WARPS = 32;  // resident per SM, as two blocks of 16 warps or four of 8
 constexpr int MAX_N = 64;
 // Each warp streams its part of a row through a ring of its own: 256 elements
 // of p and of q per stage.
 constexpr int STAGES = 3;
 constexpr int STAGE_ELEMS = 256;
 constexpr int RING_BYTES = STAGES * 2 * STAGE_ELEMS * 4;
-constexpr int SMEM = WARPS * RING_BYTES + WARPS * STAGES * 8;
+constexpr int smem(int warps) { return warps * (RING_BYTES + STAGES * 8); }
 }  // namespace vf
 
 struct VerifyParams {
@@ -365,15 +363,15 @@ __device__ __forceinline__ int pick_part(const Pair* sums, int n, Pair aim, Pair
   return at;
 }
 
-// VEC: rows are 16-byte aligned (V a multiple of 4).
-template <bool DRAFT, bool VEC>
-__global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
+// VEC: rows are 16-byte aligned (V a multiple of 4).  W: warps per CTA.
+template <bool DRAFT, bool VEC, int W>
+__global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
     verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int s_parent[vf::MAX_N], s_token[vf::MAX_N], s_rej[vf::MAX_N];
   __shared__ float s_u[vf::MAX_N], s_px[vf::MAX_N], s_qx[vf::MAX_N];
-  __shared__ Pair s_warp[vf::WARPS];
+  __shared__ Pair s_warp[W];
   __shared__ Pair s_cta[2][vf::CLUSTER];
-  __shared__ int s_pick[2][vf::WARPS];
+  __shared__ int s_pick[2][W];
   __shared__ int s_cur, s_nrej;
   __shared__ bool s_last, s_known;
   __shared__ uint64_t s_path;
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   const int N = p.N, V = p.V;
   const size_t node0 = (size_t)b * N;
   Ring ring{smem + warp * vf::RING_BYTES,
-            reinterpret_cast<uint64_t*>(smem + vf::WARPS * vf::RING_BYTES) + warp * vf::STAGES, 0,
+            reinterpret_cast<uint64_t*>(smem + W * vf::RING_BYTES) + warp * vf::STAGES, 0,
             &s_abort};
   if constexpr (VEC) {
     if (lane == 0) {
@@ -432,7 +430,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   // Sum of what is left of node cur's row: s_warp, and s_cta[pass & 1].  All
   // threads of the cluster.
   auto mass_of = [&](int cur, const Rejected& rj) {
-    const long long v0 = ((long long)rank * vf::WARPS + warp) * p.part;
+    const long long v0 = ((long long)rank * W + warp) * p.part;
     const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
     const float* pr = p.p + (node0 + cur) * V;
     const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
@@ -447,9 +445,9 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     __syncthreads();
     ++pass;
     if (warp == 0) {
-      Pair t = lane < vf::WARPS ? s_warp[lane] : Pair{0.f, 0.f};
+      Pair t = lane < W ? s_warp[lane] : Pair{0.f, 0.f};
 #pragma unroll 1
-      for (int o = vf::WARPS / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
+      for (int o = W / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
       if (lane < CL) store_remote(&s_cta[pass & 1][rank], lane, t);
     }
     cluster_sync();
@@ -556,14 +554,14 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
   const Pair aim = mul(Pair{s_u[0], 0.f}, total);
   Pair before{0.f, 0.f};
   if (pick_part(s_cta[pass & 1], CL, aim, &before) != rank) return;
-  const int at = pick_part(s_warp, vf::WARPS, aim, &before);
+  const int at = pick_part(s_warp, W, aim, &before);
   // That part of the row, a group of 128 tokens per warp, four per lane.
-  const long long v0 = ((long long)rank * vf::WARPS + at) * p.part;
+  const long long v0 = ((long long)rank * W + at) * p.part;
   const int vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
   const float* pr = p.p + (node0 + cur) * V;
   const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
   int found = INT32_MAX, last_v = -1;
-  for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * vf::WARPS) {
+  for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * W) {
     const int v = w0 + warp * 128 + lane * 4;
     const float4 a = clean4(load4<VEC, 1>(pr, v, vb));
     float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -577,7 +575,7 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
     __syncthreads();  // (s_warp and s_pick have been read)
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    const Pair upto = scan(lane < vf::WARPS ? s_warp[lane] : Pair{0.f, 0.f}, vf::WARPS);
+    const Pair upto = scan(lane < W ? s_warp[lane] : Pair{0.f, 0.f}, W);
     Pair start = shfl(upto, warp > 0 ? warp - 1 : 0);
     start = warp > 0 ? add(before, start) : before;
     const uint32_t some = __ballot_sync(0xffffffffu, own.hi > 0.f);
@@ -598,11 +596,11 @@ __global__ void __launch_bounds__(vf::THREADS, vf::BLOCKS_PER_SM)
       s_pick[1][warp] = some ? pick : -1;
     }
     __syncthreads();
-    for (int i = 0; i < vf::WARPS; ++i) {
+    for (int i = 0; i < W; ++i) {
       found = s_pick[0][i] < found ? s_pick[0][i] : found;
       last_v = s_pick[1][i] > last_v ? s_pick[1][i] : last_v;
     }
-    before = add(before, shfl(upto, vf::WARPS - 1));
+    before = add(before, shfl(upto, W - 1));
   }
   if (tid == 0) p.next[b] = found != INT32_MAX ? found : last_v;
 }
@@ -754,27 +752,34 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   p.next = next_token;
   p.N = N;
   p.V = V;
-  // CTAs per sequence: no more than have a stage for each of their warps (64
-  // sequences of 5000 tokens: 2 CTAs 15.7 us, 8 22.6 us), and all resident at
-  // once (128 of 32000: 4 CTAs 29.5 us, 8 41.4 us), or twice that where a warp's
-  // part would pass 1024 tokens (64 of 128000: 8 CTAs 43.0 us, 4 52.5 us).
+  // CTAs per sequence: 8, or as few of 8 warps as leave all of them resident at
+  // once (64 sequences of 128000 tokens: 8 CTAs 43.6 us, 4 51.2 us), or twice
+  // that where a warp's part would pass 1024 tokens (200 of 32000: 4 CTAs 22.2 us,
+  // 2 25.6 us); and no more than give each warp a stage of tokens.
+  // 16 warps where the SMs are not filled and a warp's part stays above 256
+  // tokens (16 sequences of 128000: 16 warps 22.7 us, 8 25.4 us, 32 24.0 us; one of
+  // 32000: 16 warps 6.5 us, 8 5.9 us).
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
-  const long long slots = (long long)sms * fa::vf::BLOCKS_PER_SM;
-  auto part_of = [&](int cluster) {
-    const int n = cluster * fa::vf::WARPS;
+  auto part_of = [&](int cluster, int warps) {
+    const int n = cluster * warps;
     return ((V + n - 1) / n + 127) / 128 * 128;
   };
   p.cluster = fa::vf::CLUSTER;
   while (p.cluster > 1 &&
-         (part_of(p.cluster / 2) <= fa::vf::STAGE_ELEMS || B * p.cluster > 2 * slots ||
-          (B * p.cluster > slots && part_of(p.cluster / 2) <= 1024)))
+         (part_of(p.cluster / 2, 8) <= fa::vf::STAGE_ELEMS ||
+          (long long)B * p.cluster > 8ll * sms ||
+          ((long long)B * p.cluster > 4ll * sms && part_of(p.cluster / 2, 8) <= 1024)))
     p.cluster /= 2;
-  p.part = part_of(p.cluster);
+  const int warps =
+      (long long)B * p.cluster <= sms && part_of(p.cluster, 16) > fa::vf::STAGE_ELEMS ? 16 : 8;
+  p.part = part_of(p.cluster, warps);
   const bool vec = V % 4 == 0 && al(target_probs, 16) && (!draft_probs || al(draft_probs, 16));
   const dim3 grid((unsigned)B * p.cluster);
-  void (*kernel)(fa::VerifyParams) =
-      draft_probs ? (vec ? fa::verify_kernel<true, true> : fa::verify_kernel<true, false>)
-                  : (vec ? fa::verify_kernel<false, true> : fa::verify_kernel<false, false>);
+  void (*const kernels[2][4])(fa::VerifyParams) = {
+      {fa::verify_kernel<false, false, 8>, fa::verify_kernel<false, true, 8>,
+       fa::verify_kernel<true, false, 8>, fa::verify_kernel<true, true, 8>},
+      {fa::verify_kernel<false, false, 16>, fa::verify_kernel<false, true, 16>,
+       fa::verify_kernel<true, false, 16>, fa::verify_kernel<true, true, 16>}};
   cudaError_t e = cudaSuccess;
   if (vec) {
     static int attr_set[64] = {0};
@@ -782,16 +787,18 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
     e = cudaGetDevice(&dev);
     if (e == cudaSuccess &&
         (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE))) {
-      for (auto k : {fa::verify_kernel<true, true>, fa::verify_kernel<false, true>})
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::vf::SMEM);
+      for (int i = 0; i < 2; ++i)
+        for (int k = 1; k < 4; k += 2)
+          if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernels[i][k], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     fa::vf::smem(8 << i));
       if (e == cudaSuccess && dev >= 0 && dev < 64)
         __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
     }
   }
   if (e == cudaSuccess)
-    e = fa::launch_dependent(kernel, grid, fa::vf::THREADS, stream, p, p.cluster,
-                             vec ? fa::vf::SMEM : 0);
+    e = fa::launch_dependent(kernels[warps == 16][(draft_probs ? 2 : 0) + (vec ? 1 : 0)], grid, warps * 32,
+                             stream, p, p.cluster, vec ? fa::vf::smem(warps) : 0);
   return fa::record_cuda_status(e, "tree verification launch");
 }
 
