@@ -543,118 +543,33 @@ def backward(q, k, v, o, dout, lse, scale, causal, stream=None):
     return dq, dk, dv
 
 
-# The functions below serve decoding steps, where the host's time per call is
-# what a caller waits for.  Each tests all of its conditions in one expression;
-# only when that fails does a `_refuse` function look for the condition to name.
-def _raw_stream(stream, dev):
-    import torch
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+# ----------------------------------------------------------------------------
+# Norm with rotary positions, and draft-tree decoding.  Checks, outputs and
+# pointers are marshalled natively (csrc/fa_bind.cpp): these calls are short, and
+# the host's time per call is what a decoding step waits for.
+# ----------------------------------------------------------------------------
+_native = None
 
 
-def _empty(shape, dtype, dev, stream):
-    """A new tensor that belongs to the call's stream: its memory is then
-    neither still in use nor reused too early by another stream."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _load_native():
+    global _native
+    lib = load()
+    import torch  # noqa: F401  (its libraries must be loaded first)
+    try:
+        from . import _fa_bind
+    except ImportError as e:
+        raise ImportError(
+            f"{e}: build the binding with `python -c \"import __graft_entry__ as g; g.build()\"`"
+        ) from e
+    _fa_bind.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_append, lib.fa_qk_norm_rope_backward,
+        lib.fa_decode_tree_fwd, lib.fa_verify_tree, lib.fa_compact_tree)))
+    _native = _fa_bind
+    return _fa_bind
 
 
-def _out_like(t, out, name, dev, stream):
-    if out is None:
-        return _empty(t.shape, t.dtype, dev, stream)
-    if out.dtype is not t.dtype or out.shape != t.shape:
-        raise ValueError(f"{name} must have the input's shape and dtype")
-    if out.get_device() != dev or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on the current device")
-    return out
-
-
-def _refuse(what, dtype=(), int32=(), contiguous=(), tensors=()):
-    """Raises for the first condition that fails.  dtype: (tensor, name, wanted
-    types); int32: (tensor, name, shape); then contiguity and the device."""
-    import torch
-    for t, name, want in dtype:
-        if t.dtype not in want:
-            raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(map(str, want))}")
-    for t, name, shape in int32:
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be an int32 CUDA tensor")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}")
-    for t, name in [*contiguous, *((t, name) for t, name, _ in int32)]:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be CUDA tensors on the current device (cuda:{dev})")
-    raise ValueError(f"{what}: invalid arguments")
-
-
-def _token_stride(t, name):
-    """Stride between the tokens of [..., H, D]: heads contiguous, tokens at one
-    stride (a slice of a packed projection is fine)."""
-    shape, st = t.shape, t.stride()
-    H, D = shape[-2], shape[-1]
-    if t.numel() == 0:
-        return H * D
-    if (st[-1] == 1 or D == 1) and (st[-2] == D or H == 1):
-        if len(shape) == 3 or (len(shape) == 4 and st[0] == st[1] * shape[1]):
-            return st[-3] if shape[-3] > 1 or len(shape) == 4 else H * D
-        step = ts = None  # the stride that the next leading axis must have
-        for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
-            if n == 1:
-                continue
-            if ts is None:
-                ts = s
-            elif s != step:
-                break
-            step = s * n
-        else:
-            return H * D if ts is None else ts
-    raise ValueError(f"{name}: heads must be contiguous and tokens at one stride")
-
-
-def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions):
-    """Checks shared by the norm and rotation's forms: (shape, tokens, Hq, Hkv,
-    D, token strides, dtype code, device)."""
-    import torch
-    shape, kshape, dt, dev = q.shape, k.shape, q.dtype, q.get_device()
-    n = len(shape)
-    if n < 2 or len(kshape) != n:
-        raise ValueError("q and k must be [..., heads, D]")
-    D = shape[-1]
-    lead = shape[:-2]
-    if kshape[:-2] != lead or kshape[-1] != D:
-        raise ValueError("q and k must share their leading shape and head dimension")
-    if q_weight.shape != (D,) or k_weight.shape != (D,):
-        raise ValueError(f"the weights must have shape ({D},)")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot_dim / 2]")
-    if not ((dt is torch.bfloat16 or dt is torch.float16) and k.dtype is dt and
-            q_weight.dtype is dt and k_weight.dtype is dt and
-            inv_freq.dtype is torch.float32 and q_weight.is_contiguous() and
-            k_weight.is_contiguous() and inv_freq.is_contiguous() and
-            k.get_device() == q_weight.get_device() == k_weight.get_device() ==
-            inv_freq.get_device() == dev and dev >= 0 and dev == torch.cuda.current_device() and
-            (positions is None or
-             (positions.dtype is torch.int32 and positions.shape == lead and
-              positions.is_contiguous() and positions.get_device() == dev))):
-        _refuse("norm and rotation",
-                [(q, "q", (torch.bfloat16, torch.float16)), (k, "k", (dt,)),
-                 (q_weight, "q_weight", (dt,)), (k_weight, "k_weight", (dt,)),
-                 (inv_freq, "inv_freq", (torch.float32,))],
-                [] if positions is None else [(positions, "positions", lead)],
-                [(q_weight, "q_weight"), (k_weight, "k_weight"), (inv_freq, "inv_freq")],
-                (q, k, q_weight, k_weight, inv_freq, positions))
-    return (shape, lead.numel(), shape[-2], kshape[-2], D, _token_stride(q, "q"),
-            _token_stride(k, "k"), FA_BF16 if dt is torch.bfloat16 else FA_FP16, dev)
+def _token_stride(t):
+    return (_native or _load_native()).token_stride(t)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved=False,
@@ -664,43 +579,22 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved
     position * inv_freq[i].  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
     interleaved, rot = 2 * len(inv_freq); further elements pass through.  q and
     k may be slices of one packed projection.  Returns contiguous (q_out, k_out)."""
-    _, T, Hq, Hkv, D, qs, ks, code, dev = _norm_rope_args(q, k, q_weight, k_weight, inv_freq,
-                                                          positions)
-    q_out = _out_like(q, q_out, "q_out", dev, stream)
-    k_out = _out_like(k, k_out, "k_out", dev, stream)
-    st = load().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
-                                positions.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
-                                eps, bool(interleaved), code, _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_qk_norm_rope")
-    return q_out, k_out
+    r = (_native or _load_native()).qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions,
+                                                 eps, interleaved, q_out, k_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_qk_norm_rope")
+    return r
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, eps,
                           interleaved=False, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope from those of
     its outputs (contiguous).  The weights' gradients are float32."""
-    import torch
-    shape, T, Hq, Hkv, D, qs, ks, code, dev = _norm_rope_args(q, k, q_weight, k_weight, inv_freq,
-                                                              positions)
-    if dq_out.shape != shape or dk_out.shape != k.shape:
-        raise ValueError("dq_out and dk_out must have the outputs' shapes")
-    dt = q.dtype
-    if not (dq_out.dtype is dt and dk_out.dtype is dt and dq_out.is_contiguous() and
-            dk_out.is_contiguous() and dq_out.get_device() == dk_out.get_device() == dev):
-        _refuse("norm and rotation", [(dq_out, "dq_out", (dt,)), (dk_out, "dk_out", (dt,))], (),
-                [(dq_out, "dq_out"), (dk_out, "dk_out")], (dq_out, dk_out))
-    dq, dk = _empty(shape, dt, dev, stream), _empty(k.shape, dt, dev, stream)
-    dqw, dkw = _empty((D,), torch.float32, dev, stream), _empty((D,), torch.float32, dev, stream)
-    st = load().fa_qk_norm_rope_backward(
-        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-        k_weight.data_ptr(), inv_freq.data_ptr(), positions.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), T, Hq, Hkv, D, 2 * inv_freq.numel(), qs, ks,
-        eps, bool(interleaved), code, _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_qk_norm_rope_backward")
-    return dq, dk, dqw, dkw
+    r = (_native or _load_native()).qk_norm_rope_backward(
+        q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dq_out, dk_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_qk_norm_rope_backward")
+    return r
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, page_table,
@@ -709,39 +603,12 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, kpages, vpages, p
     [B,N,Hkv,D]), k and v written into the paged cache: token s of sequence b
     goes to slot seqlens[b] - N + s (lengths include the new tokens).
     positions: int32 [B,N], or None for the slot.  Returns q_out."""
-    import torch
-    shape, T, Hq, Hkv, D, qs, ks, code, dev = _norm_rope_args(q, k, q_weight, k_weight, inv_freq,
-                                                              positions)
-    if len(shape) != 4 or v.shape != k.shape:
-        raise ValueError("q must be [B,N,Hq,D], k and v [B,N,Hkv,D]")
-    B, N = shape[0], shape[1]
-    pshape = kpages.shape
-    num_pages, page_size, Hp, Dp = pshape
-    if Hp != Hkv or Dp != D or vpages.shape != pshape:
-        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
-    dt, i32 = q.dtype, torch.int32
-    tshape = page_table.shape
-    if not (v.dtype is dt and kpages.dtype is dt and vpages.dtype is dt and
-            page_table.dtype is i32 and seqlens.dtype is i32 and len(tshape) == 2 and
-            tshape[0] == B and seqlens.shape == (B,) and kpages.is_contiguous() and
-            vpages.is_contiguous() and page_table.is_contiguous() and seqlens.is_contiguous() and
-            v.get_device() == kpages.get_device() == vpages.get_device() ==
-            page_table.get_device() == seqlens.get_device() == dev):
-        _refuse("norm, rotation and append",
-                [(v, "v", (dt,)), (kpages, "kpages", (dt,)), (vpages, "vpages", (dt,))],
-                [(page_table, "page_table", (B, tshape[-1])), (seqlens, "seqlens", (B,))],
-                [(kpages, "kpages"), (vpages, "vpages")], (v, kpages, vpages, page_table, seqlens))
-    vs = _token_stride(v, "v")
-    q_out = _out_like(q, q_out, "q_out", dev, stream)
-    st = load().fa_qk_norm_rope_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kpages.data_ptr(),
-        vpages.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr(),
-        None if positions is None else positions.data_ptr(), page_table.data_ptr(),
-        seqlens.data_ptr(), B, N, Hq, Hkv, num_pages, page_size, tshape[1], D,
-        2 * inv_freq.numel(), qs, ks, vs, eps, bool(interleaved), code, _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_qk_norm_rope_append")
-    return q_out
+    r = (_native or _load_native()).qk_norm_rope_append(
+        q, k, q_weight, k_weight, inv_freq, v, kpages, vpages, page_table, seqlens, eps, positions,
+        interleaved, q_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_qk_norm_rope_append")
+    return r
 
 
 def decode_tree(q, kpages, vpages, page_table, seqlens, parents, scale, out=None, stream=None,
@@ -754,44 +621,11 @@ def decode_tree(q, kpages, vpages, page_table, seqlens, parents, scale, out=None
     lower node, -1 for a root, -2 for an unused slot).  Node s sees the keys
     before the tree, its ancestors and itself.  Returns ``out`` like q, or (out,
     lse) with lse [B,N,Hq] fp32 when lse is True or a tensor."""
-    import torch
-    B, N, Hq, D = q.shape
-    pshape, tshape = kpages.shape, page_table.shape
-    num_pages, page_size, Hkv, Dp = pshape
-    if Dp != D or vpages.shape != pshape:
-        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D]")
-    dt, i32, dev = q.dtype, torch.int32, q.get_device()
-    if not ((dt is torch.bfloat16 or dt is torch.float16) and kpages.dtype is dt and
-            vpages.dtype is dt and page_table.dtype is i32 and seqlens.dtype is i32 and
-            parents.dtype is i32 and len(tshape) == 2 and tshape[0] == B and
-            seqlens.shape == (B,) and parents.shape == (B, N) and q.is_contiguous() and
-            kpages.is_contiguous() and vpages.is_contiguous() and page_table.is_contiguous() and
-            seqlens.is_contiguous() and parents.is_contiguous() and
-            kpages.get_device() == vpages.get_device() == page_table.get_device() ==
-            seqlens.get_device() == parents.get_device() == dev and dev >= 0 and
-            dev == torch.cuda.current_device()):
-        _refuse("decode_tree",
-                [(q, "q", (torch.bfloat16, torch.float16)), (kpages, "kpages", (dt,)),
-                 (vpages, "vpages", (dt,))],
-                [(page_table, "page_table", (B, tshape[-1])), (seqlens, "seqlens", (B,)),
-                 (parents, "parents", (B, N))],
-                [(q, "q"), (kpages, "kpages"), (vpages, "vpages")],
-                (q, kpages, vpages, page_table, seqlens, parents))
-    out = _out_like(q, out, "out", dev, stream)
-    lse_ptr = None
-    if lse is True:
-        lse = _empty((B, N, Hq), torch.float32, dev, stream)
-        lse_ptr = lse.data_ptr()
-    elif lse is not None and lse is not False:
-        lse_ptr = _lse_tensor(lse, (B, N, Hq), q).data_ptr()
-    st = load().fa_decode_tree_fwd(
-        q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
-        seqlens.data_ptr(), parents.data_ptr(), out.data_ptr(), lse_ptr, B, N, Hq, Hkv, num_pages,
-        page_size, tshape[1], D, scale, FA_BF16 if dt is torch.bfloat16 else FA_FP16,
-        _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_decode_tree_fwd")
-    return out if lse_ptr is None else (out, lse)
+    r = (_native or _load_native()).decode_tree(q, kpages, vpages, page_table, seqlens, parents,
+                                                scale, out, stream, lse)
+    if type(r) is int:
+        raise FAError(r, "fa_decode_tree_fwd")
+    return r
 
 
 def verify_tree(target_probs, draft_probs, tokens, parents, uniforms, stream=None):
@@ -803,37 +637,11 @@ def verify_tree(target_probs, draft_probs, tokens, parents, uniforms, stream=Non
     the root); uniforms float32 [B,N] in [0,1) (entry 0 draws the next token).
     Returns int32 (path [B,N], count [B], next_token [B]): the accepted nodes,
     root first, padded with -1."""
-    import torch
-    shape = target_probs.shape
-    B, N, V = shape
-    bn, f32, i32, dev = (B, N), torch.float32, torch.int32, target_probs.get_device()
-    if uniforms.shape != bn or (draft_probs is not None and draft_probs.shape != shape):
-        raise ValueError("draft_probs must have target_probs' shape, uniforms [B,N]")
-    if not (target_probs.dtype is f32 and uniforms.dtype is f32 and tokens.dtype is i32 and
-            parents.dtype is i32 and tokens.shape == bn and parents.shape == bn and
-            target_probs.is_contiguous() and uniforms.is_contiguous() and
-            tokens.is_contiguous() and parents.is_contiguous() and
-            tokens.get_device() == parents.get_device() == uniforms.get_device() == dev and
-            dev >= 0 and dev == torch.cuda.current_device() and
-            (draft_probs is None or (draft_probs.dtype is f32 and draft_probs.is_contiguous() and
-                                     draft_probs.get_device() == dev))):
-        d = [] if draft_probs is None else [(draft_probs, "draft_probs")]
-        _refuse("verify_tree",
-                [(t, n, (f32,)) for t, n in [(target_probs, "target_probs"), *d,
-                                             (uniforms, "uniforms")]],
-                [(tokens, "tokens", bn), (parents, "parents", bn)],
-                [(target_probs, "target_probs"), *d, (uniforms, "uniforms")],
-                (target_probs, draft_probs, tokens, parents, uniforms))
-    path = _empty(bn, i32, dev, stream)
-    count, nxt = _empty((B,), i32, dev, stream), _empty((B,), i32, dev, stream)
-    st = load().fa_verify_tree(target_probs.data_ptr(),
-                               None if draft_probs is None else draft_probs.data_ptr(),
-                               tokens.data_ptr(), parents.data_ptr(), uniforms.data_ptr(),
-                               path.data_ptr(), count.data_ptr(), nxt.data_ptr(), B, N, V,
-                               _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_verify_tree")
-    return path, count, nxt
+    r = (_native or _load_native()).verify_tree(target_probs, draft_probs, tokens, parents,
+                                                uniforms, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_verify_tree")
+    return r
 
 
 def compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=None,
@@ -843,34 +651,8 @@ def compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=N
     path[b][i] of the tree's N slots moves to row i, for i < count[b].  seqlens
     int32 [B] include the N nodes.  Returns the new lengths (seqlens_out, which
     may be seqlens; a new tensor if None)."""
-    import torch
-    shape, tshape = kpages.shape, page_table.shape
-    n = len(shape)
-    if (n != 4 and n != 5) or vpages.shape != shape:
-        raise ValueError("kpages and vpages must be [num_pages,page_size,Hkv,D] or [layers,...]")
-    B, N = path.shape
-    dt, i32, dev = kpages.dtype, torch.int32, kpages.get_device()
-    if not ((dt is torch.bfloat16 or dt is torch.float16) and vpages.dtype is dt and
-            page_table.dtype is i32 and seqlens.dtype is i32 and path.dtype is i32 and
-            count.dtype is i32 and len(tshape) == 2 and tshape[0] == B and
-            seqlens.shape == (B,) and count.shape == (B,) and kpages.is_contiguous() and
-            vpages.is_contiguous() and page_table.is_contiguous() and seqlens.is_contiguous() and
-            path.is_contiguous() and count.is_contiguous() and
-            vpages.get_device() == page_table.get_device() == seqlens.get_device() ==
-            path.get_device() == count.get_device() == dev and dev >= 0 and
-            dev == torch.cuda.current_device()):
-        _refuse("compact_tree",
-                [(kpages, "kpages", (torch.bfloat16, torch.float16)), (vpages, "vpages", (dt,))],
-                [(page_table, "page_table", (B, tshape[-1])), (seqlens, "seqlens", (B,)),
-                 (path, "path", None), (count, "count", (B,))],
-                [(kpages, "kpages"), (vpages, "vpages")],
-                (kpages, vpages, page_table, seqlens, path, count))
-    seqlens_out = _out_like(seqlens, seqlens_out, "seqlens_out", dev, stream)
-    st = load().fa_compact_tree(kpages.data_ptr(), vpages.data_ptr(), page_table.data_ptr(),
-                                seqlens.data_ptr(), path.data_ptr(), count.data_ptr(),
-                                seqlens_out.data_ptr(), shape[0] if n == 5 else 1, B, N, shape[-2],
-                                shape[-4], shape[-3], tshape[1], shape[-1],
-                                _raw_stream(stream, dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_compact_tree")
-    return seqlens_out
+    r = (_native or _load_native()).compact_tree(kpages, vpages, page_table, seqlens, path, count,
+                                                 seqlens_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_compact_tree")
+    return r

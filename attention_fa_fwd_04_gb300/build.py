@@ -1,11 +1,14 @@
-"""Build libfa_gb300.so in-tree with nvcc for sm_103a.
+"""Build libfa_gb300.so in-tree with nvcc for sm_103a, and _fa_bind.so, the
+native part of the Python binding, with the host compiler.
 
-The translation units compile in parallel, then link into one shared
+The translation units compile in parallel; the CUDA ones link into one shared
 library next to this file.  No CMake, no torch extension machinery.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +19,8 @@ LIB = os.path.join(HERE, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_decode.cu", "fa_decode_noalloc.cu",
            "fa_backward.cu", "fa_host.cu", "fa_rope.cu", "fa_tree.cu", "fa_verify.cu"]
 HEADERS = ["fa_ptx.cuh", "fa_internal.h"]
+BIND = os.path.join(HERE, "_fa_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "fa_bind.cpp")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -30,10 +35,23 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    return all(os.path.getmtime(f) <= t for f in _inputs() + [BIND_SOURCE])
+
+
+def _bind_command(out):
+    """The host compiler's command for the native binding: against the
+    installed torch's headers and libraries, and the CUDA headers beside nvcc."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    lib = os.path.join(torch_dir, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), BIND_SOURCE, "-o", out, "-L", lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -50,6 +68,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             procs.append((s, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                               stderr=subprocess.STDOUT, text=True)))
             objs.append(obj)
+        tmp_bind = os.path.join(tmp, "_fa_bind.so")
+        cmd = _bind_command(tmp_bind)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        procs.append(("fa_bind.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                                      stderr=subprocess.STDOUT, text=True)))
         failed = []
         for s, pr in procs:
             out, _ = pr.communicate()
@@ -58,11 +82,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if pr.returncode:
                 failed.append(s)
         if failed:
-            raise RuntimeError(f"nvcc failed for {failed}")
+            raise RuntimeError(f"compilation failed for {failed}")
         tmp_lib = os.path.join(tmp, "libfa_gb300.so")
         cmd = [NVCC] + ARCH + ["-shared", "-o", tmp_lib] + objs
         subprocess.check_call(cmd)
         os.replace(tmp_lib, LIB)
+        os.replace(tmp_bind, BIND)
     return LIB
 
 

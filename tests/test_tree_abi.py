@@ -197,6 +197,6 @@ def test_token_strides(fa, shape, stride, ok):
     t = torch.empty(32768, dtype=torch.float16).as_strided(shape, stride)
     if ok is None:
         with pytest.raises(ValueError):
-            fa._token_stride(t, "x")
+            fa._token_stride(t)
     else:
-        assert fa._token_stride(t, "x") == ok
+        assert fa._token_stride(t) == ok
