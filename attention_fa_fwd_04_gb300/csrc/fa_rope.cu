@@ -645,27 +645,28 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
 }
 
 // dw of part blockIdx.y: the sum of its blocks' partial rows, 32 columns per
-// block, 8 interleaved row sums each.
-__global__ void __launch_bounds__(256)
+// block; each of the 32 warps sums every 32nd row, then one column.
+constexpr int kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads)
     rope_dw_kernel(const float* partial, int D, int b0q, int nbq, float* dqw, int b0k, int nbk,
                    float* dkw) {
-  __shared__ float sS[8][32];
+  __shared__ float sS[32][33];
   pdl_launch_dependents();
   pdl_wait_primary();
   const int b0 = blockIdx.y ? b0k : b0q, nb = blockIdx.y ? nbk : nbq;
   float* dw = blockIdx.y ? dkw : dqw;
   if (!dw) return;
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const float* col = partial + (size_t)b0 * D + blockIdx.x * 32 + lane;
   float s = 0.f;
-#pragma unroll 4
-  for (int i = r; i < nb; i += 8) s += partial[(size_t)(b0 + i) * D + col];
-  sS[r][c] = s;
+#pragma unroll 8
+  for (int i = r; i < nb; i += 32) s += col[(size_t)i * D];
+  sS[r][lane] = s;
   __syncthreads();
-  if (r == 0) {
+  s = sS[lane][r];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sS[i][c];
-    dw[col] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) dw[blockIdx.x * 32 + r] = s;
 }
 
 // Steps per task: the fewest rounds of the resident warps, a round costing its
@@ -946,7 +947,7 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
   p.partial = static_cast<float*>(scratch);
   int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, 2, interleaved != 0, stream);
   if (r == 0)
-    r = fa::launch_pdl(fa::rope_dw_kernel, dim3(D / 32, 2), 256, 0, stream,
+    r = fa::launch_pdl(fa::rope_dw_kernel, dim3(D / 32, 2), fa::kDwThreads, 0, stream,
                        (const float*)p.partial, D, iq >= 0 ? p.part[iq].b0 : 0,
                        iq >= 0 ? p.part[iq].nb : 0, iq >= 0 ? dq_weight : (float*)nullptr,
                        ik >= 0 ? p.part[ik].b0 : 0, ik >= 0 ? p.part[ik].nb : 0,

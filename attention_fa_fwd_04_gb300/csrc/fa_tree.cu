@@ -131,38 +131,54 @@ __device__ __forceinline__ long long tree_groups(const TreeParams& p, long long 
 // Whole warp: the range of group g and the sequence it starts in.
 __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
   const int lane = threadIdx.x & 31;
+  TreeWalk w;
+  w.first = 0;
+  w.b = 0;
+  w.T = 0;
+  auto range = [&](long long total) {
+    const long long G = tree_groups(p, total);
+    w.x = g < G ? mul_div(total, g, G) : 0;
+    w.hi = g < G ? mul_div(total, g + 1, G) : 0;
+    return w.x < w.hi;
+  };
+  // The sequence of lane l (tiles T, inclusive sum inc on top of `before`) is
+  // the first that ends past the range's start.
+  auto find = [&](int b0, int T, long long inc, long long before) {
+    const uint32_t past = __ballot_sync(0xffffffffu, w.x < (before + inc) * p.Hkv);
+    if (!past) return false;
+    const int l = __ffs(past) - 1;
+    w.b = b0 + l;
+    w.T = __shfl_sync(0xffffffffu, T, l);
+    w.first = (before + __shfl_sync(0xffffffffu, inc, l) - w.T) * p.Hkv;
+    return true;
+  };
+  if (p.B <= 32) {  // one load, 32-bit sums (a sequence has at most 2^24 tiles)
+    const int T = lane < p.B ? tree_tiles(p, lane) : 0;
+    int inc = T;
+    for (int o = 1; o < p.B; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (range((long long)__shfl_sync(0xffffffffu, inc, p.B - 1) * p.Hkv)) find(0, T, inc, 0);
+    return w;
+  }
   long long sum = 0;
 #pragma unroll 4
   for (int b = lane; b < p.B; b += 32) sum += tree_tiles(p, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const long long total = sum * p.Hkv;
-  const long long G = tree_groups(p, total);
-  TreeWalk w;
-  w.x = g < G ? mul_div(total, g, G) : 0;
-  w.hi = g < G ? mul_div(total, g + 1, G) : 0;
-  w.first = 0;
-  w.b = 0;
-  w.T = 0;
-  if (w.x >= w.hi) return w;
+  if (!range(sum * p.Hkv)) return w;
   long long before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    const long long T = b < p.B ? tree_tiles(p, b) : 0;
+    const int T = b < p.B ? tree_tiles(p, b) : 0;
     long long inc = T;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, w.x < (before + inc) * p.Hkv);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      w.b = b0 + l;
-      w.T = (int)__shfl_sync(0xffffffffu, T, l);
-      w.first = (before + __shfl_sync(0xffffffffu, inc, l) - w.T) * p.Hkv;
-      break;
-    }
+    if (find(b0, T, inc, before)) break;
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
   return w;
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
   pdl_wait_primary();  // everything below reads or writes the caller's memory
 
   TreeWalk w = tree_plan(p, group);
-  TreeSeg sg;
+  TreeSeg sg = {};
   if (warp >= W_PROD) {
    if constexpr (MT == 2) regs_decrease<88>();
    if (warp == W_PROD) {
@@ -773,7 +789,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         mbar_arrive(&p_full[i]);
       }
       if (!ok) break;
-      TreeSeg next;
+      TreeSeg next = {};
       have = tree_next(p, w, &next);
       if (have) load_q(next);
       if (!(ok = mbar_wait<false>(&pv_done[i], (MT == 1 ? tc - 1 : seg) & 1, abort_flag,
@@ -950,32 +966,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       load(k + (kMergeAhead + u) * KS, u);
     }
   }
+  const int s = real ? r / p.G : 0;
+  const size_t row = ((size_t)b * p.N + s) * p.Hq + (size_t)hkv * p.G + (r - s * p.G);
+  T* const dst = static_cast<T*>(p.o) + row * D + chunk * 16;
   if constexpr (KS > 1) {
+    // The warps' results meet in shared memory; then each warp finishes two of
+    // the 16 columns.
     sM[warp][lane] = M;
     sDen[warp][lane] = den;
 #pragma unroll
     for (int e = 0; e < 16; ++e) sAcc[warp][e][lane] = acc[e];
     __syncthreads();
-    if (warp != 0) return;
-#pragma unroll 1
-    for (int i = 1; i < KS; ++i) {
-      const float wt = scale(sM[i][lane]);
-      den += wt * sDen[i][lane];
+    static_assert(KS == kMergeWarps && 2 * KS == 16, "two columns per warp");
+    float m[KS];
+    M = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] += wt * sAcc[i][e][lane];
+    for (int i = 0; i < KS; ++i) {
+      m[i] = sM[i][lane];
+      M = fmaxf(M, m[i]);
     }
-  }
-  if (!real) return;
-  const int s = r / p.G;
-  const size_t row = ((size_t)b * p.N + s) * p.Hq + (size_t)hkv * p.G + (r - s * p.G);
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + chunk * 16);
+    float a0 = 0.f, a1 = 0.f;
+    den = 0.f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    dst[e] = make_uint4(TreeType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
-                        TreeType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-                        TreeType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-                        TreeType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+    for (int i = 0; i < KS; ++i) {
+      const float wt = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - M);
+      den += wt * sDen[i][lane];
+      a0 += wt * sAcc[i][2 * warp][lane];
+      a1 += wt * sAcc[i][2 * warp + 1][lane];
+    }
+    if (!real) return;
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    reinterpret_cast<uint32_t*>(dst)[warp] = TreeType<T>::pack(a0 * inv, a1 * inv);
+    if (warp != 0) return;
+  } else {
+    if (!real) return;
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      reinterpret_cast<uint4*>(dst)[e] =
+          make_uint4(TreeType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
+                     TreeType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
+                     TreeType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
+                     TreeType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+  }
   if (p.lse && chunk == 0)
     p.lse[row] = den > 0.f ? 0.6931471805599453f * (M + log2f(den)) : -INFINITY;
 }
