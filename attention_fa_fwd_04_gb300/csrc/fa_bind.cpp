@@ -108,7 +108,9 @@ struct Stream {
     handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
     Py_DECREF(v);
     if (PyErr_Occurred()) throw python_error();
-    guard.emplace(c10::cuda::getStreamFromExternal(handle, device));
+    // (The legacy stream's handle is another name of the null stream.)
+    const cudaStream_t own = handle == cudaStreamLegacy ? nullptr : handle;
+    guard.emplace(c10::cuda::getStreamFromExternal(own, device));
   }
 };
 
@@ -154,6 +156,19 @@ bool truth(PyObject* o) {
 }
 int narrow(int64_t v) {  // a size that the C ABI takes as an int
   return v > INT32_MAX ? INT32_MAX : static_cast<int>(v);
+}
+
+// The library's calls run without the interpreter's lock: a launch may wait for
+// room in the stream's queue, and what makes room can need the lock (a host
+// function in Python).
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... Args>
+int unlocked(F* f, Args... args) {
+  const Unlocked u;
+  return f(args...);
 }
 
 PyObject* wrapped(std::initializer_list<at::Tensor> ts) {
@@ -205,7 +220,7 @@ struct Heads {
     for (const at::Tensor* t : {&k, &qw, &kw, &freq}) d.has(*t);
     if (pos) d.has(*pos);
   }
-  int rot() const { return 2 * narrow(freq.size(0)); }
+  int rot() const { return narrow(2 * freq.size(0)); }
 };
 
 // A paged cache [num_pages, page_size, Hkv, D], page table [B, max_pages] and
@@ -250,10 +265,10 @@ PyObject* norm_rope(PyObject* const* a) {
   h.on(dev);
   Stream s(a[10], dev.index);
   const at::Tensor qo = output(a[8], "q_out", h.q, dev), ko = output(a[9], "k_out", h.k, dev);
-  const int st = p_rope(h.q.const_data_ptr(), h.k.const_data_ptr(), qo.data_ptr(), ko.data_ptr(),
-                        h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq), i32(*h.pos), h.T,
-                        h.Hq, h.Hkv, h.D, h.rot(), h.qs, h.ks, (float)number(a[6]), truth(a[7]),
-                        h.code, s.handle);
+  const int st = unlocked(
+      p_rope, h.q.const_data_ptr(), h.k.const_data_ptr(), qo.data_ptr(), ko.data_ptr(),
+      h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq), i32(*h.pos), h.T, h.Hq, h.Hkv, h.D,
+      h.rot(), h.qs, h.ks, (float)number(a[6]), truth(a[7]), h.code, s.handle);
   return st ? PyLong_FromLong(st) : wrapped({qo, ko});
 }
 
@@ -277,11 +292,12 @@ PyObject* norm_rope_backward(PyObject* const* a) {
   const at::Tensor dk = at::empty(h.k.sizes(), h.k.options());
   const at::Tensor dqw = at::empty({h.D}, h.q.options().dtype(at::kFloat));
   const at::Tensor dkw = at::empty({h.D}, h.q.options().dtype(at::kFloat));
-  const int st = p_rope_backward(
-      gq.const_data_ptr(), gk.const_data_ptr(), h.q.const_data_ptr(), h.k.const_data_ptr(),
-      h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq), i32(*h.pos), dq.data_ptr(),
-      dk.data_ptr(), static_cast<float*>(dqw.data_ptr()), static_cast<float*>(dkw.data_ptr()), h.T,
-      h.Hq, h.Hkv, h.D, h.rot(), h.qs, h.ks, (float)number(a[6]), truth(a[7]), h.code, s.handle);
+  const int st = unlocked(
+      p_rope_backward, gq.const_data_ptr(), gk.const_data_ptr(), h.q.const_data_ptr(),
+      h.k.const_data_ptr(), h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq), i32(*h.pos),
+      dq.data_ptr(), dk.data_ptr(), static_cast<float*>(dqw.data_ptr()),
+      static_cast<float*>(dkw.data_ptr()), h.T, h.Hq, h.Hkv, h.D, h.rot(), h.qs, h.ks,
+      (float)number(a[6]), truth(a[7]), h.code, s.handle);
   return st ? PyLong_FromLong(st) : wrapped({dq, dk, dqw, dkw});
 }
 
@@ -304,8 +320,8 @@ PyObject* append(PyObject* const* a) {
   p.on(dev);
   Stream s(a[14], dev.index);
   const at::Tensor qo = output(a[13], "q_out", h.q, dev);
-  const int st = p_append(
-      h.q.const_data_ptr(), h.k.const_data_ptr(), v.const_data_ptr(), qo.data_ptr(),
+  const int st = unlocked(
+      p_append, h.q.const_data_ptr(), h.k.const_data_ptr(), v.const_data_ptr(), qo.data_ptr(),
       p.k.data_ptr(), p.v.data_ptr(), h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq),
       h.pos ? i32(*h.pos) : nullptr, i32(p.table), i32(p.lens), narrow(h.q.size(0)),
       narrow(h.q.size(1)), h.Hq, h.Hkv, p.num_pages, p.page_size, p.max_pages, h.D, h.rot(), h.qs,
@@ -342,11 +358,11 @@ PyObject* tree(PyObject* const* a) {
     contiguous(lse, "lse");
     dev.has(lse);
   }
-  const int st = p_tree(q.const_data_ptr(), p.k.const_data_ptr(), p.v.const_data_ptr(),
-                        i32(p.table), i32(p.lens), i32(parents), out.data_ptr(),
-                        want ? static_cast<float*>(lse.data_ptr()) : nullptr, narrow(B), narrow(N),
-                        narrow(Hq), p.Hkv, p.num_pages, p.page_size, p.max_pages, p.D,
-                        (float)number(a[6]), code, s.handle);
+  const int st = unlocked(
+      p_tree, q.const_data_ptr(), p.k.const_data_ptr(), p.v.const_data_ptr(), i32(p.table),
+      i32(p.lens), i32(parents), out.data_ptr(),
+      want ? static_cast<float*>(lse.data_ptr()) : nullptr, narrow(B), narrow(N), narrow(Hq), p.Hkv,
+      p.num_pages, p.page_size, p.max_pages, p.D, (float)number(a[6]), code, s.handle);
   if (st) return PyLong_FromLong(st);
   return want ? wrapped({out, lse}) : wrapped({out});
 }
@@ -380,7 +396,7 @@ PyObject* verify(PyObject* const* a) {
   const auto opt = tokens.options();
   const at::Tensor path = at::empty(bn, opt), count = at::empty(b1, opt), next = at::empty(b1, opt);
   const int st =
-      p_verify(f32(p), q ? f32(*q) : nullptr, i32(tokens), i32(parents), f32(u),
+      unlocked(p_verify, f32(p), q ? f32(*q) : nullptr, i32(tokens), i32(parents), f32(u),
                static_cast<int32_t*>(path.data_ptr()), static_cast<int32_t*>(count.data_ptr()),
                static_cast<int32_t*>(next.data_ptr()), narrow(bn[0]), narrow(bn[1]),
                narrow(p.size(2)), s.handle);
@@ -402,11 +418,10 @@ PyObject* compact(PyObject* const* a) {
   dev.has(count);
   Stream s(a[7], dev.index);
   const at::Tensor out = output(a[6], "seqlens_out", p.lens, dev);
-  const int st = p_compact(p.k.data_ptr(), p.v.data_ptr(), i32(p.table), i32(p.lens), i32(path),
-                           i32(count), static_cast<int32_t*>(out.data_ptr()),
-                           p.k.dim() == 5 ? narrow(p.k.size(0)) : 1, narrow(B),
-                           narrow(path.size(1)), p.Hkv, p.num_pages, p.page_size, p.max_pages, p.D,
-                           s.handle);
+  const int st = unlocked(
+      p_compact, p.k.data_ptr(), p.v.data_ptr(), i32(p.table), i32(p.lens), i32(path), i32(count),
+      static_cast<int32_t*>(out.data_ptr()), p.k.dim() == 5 ? narrow(p.k.size(0)) : 1, narrow(B),
+      narrow(path.size(1)), p.Hkv, p.num_pages, p.page_size, p.max_pages, p.D, s.handle);
   return st ? PyLong_FromLong(st) : wrapped({out});
 }
 

@@ -96,6 +96,24 @@ int set_verify_wait_limit(unsigned long long ns);
 // call after one would wait for the driver to map it again.
 cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 
+// While it lives, what this thread does to set itself up (a kernel's attributes,
+// its module's loading, the scratch pool) does not end a capture that forbids
+// such calls on every thread, another thread's included: none of it waits for
+// the GPU or is left out of a graph.
+class SetupDuringCapture {
+ public:
+  SetupDuringCapture() { ok_ = cudaThreadExchangeStreamCaptureMode(&mode_) == cudaSuccess; }
+  ~SetupDuringCapture() {
+    if (ok_) cudaThreadExchangeStreamCaptureMode(&mode_);
+  }
+  SetupDuringCapture(const SetupDuringCapture&) = delete;
+  SetupDuringCapture& operator=(const SetupDuringCapture&) = delete;
+
+ private:
+  cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+  bool ok_;
+};
+
 // Status of a CUDA call for the C ABI: FA_OK for 0, else FA_ERR_CUDA after
 // recording the raw error and the failing call (a static string) for
 // fa_last_cuda_error() in the calling thread.

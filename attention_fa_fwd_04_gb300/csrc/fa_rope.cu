@@ -841,6 +841,7 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
     return FA_ERR_INVALID_ARG;
   if (Hkv && (!heads_ok(k, k_stride, Hkv, D) || !al(k_out, 16) || !al(k_weight, 16)))
     return FA_ERR_INVALID_ARG;
+  const fa::SetupDuringCapture setup;
   fa::RopeParams p = {};
   if (Hq) p.part[p.n_parts++] = part(q, q_stride, Hq, q_weight, q_out, nullptr, false);
   if (Hkv) p.part[p.n_parts++] = part(k, k_stride, Hkv, k_weight, k_out, nullptr, false);
@@ -879,6 +880,7 @@ extern "C" int fa_qk_norm_rope_append(const void* q, const void* k, const void* 
     return FA_ERR_INVALID_ARG;
   if ((int64_t)num_pages * page_size > (1ll << 40) / (2 * D) / (Hkv ? Hkv : 1))
     return FA_ERR_INVALID_ARG;
+  const fa::SetupDuringCapture setup;
   fa::RopeParams p = {};
   if (Hq) p.part[p.n_parts++] = part(q, q_stride, Hq, q_weight, q_out, nullptr, false);
   if (Hkv) {
@@ -925,6 +927,7 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
     e = cudaMemsetAsync(dk_weight, 0, D * sizeof(float), stream);
   if (e != cudaSuccess || T == 0 || (Hq == 0 && Hkv == 0))
     return fa::record_cuda_status(e, "norm and rotation gradient zero-fill");
+  const fa::SetupDuringCapture setup;
   fa::RopeParams p = {};
   int iq = -1, ik = -1;
   if (Hq) {

@@ -1142,7 +1142,8 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   if (max_pages > 0 && (num_pages < 1 || !al(kpages, 16) || !al(vpages, 16) ||
                         !al(page_table, 4) || !al(seqlens, 4) || !al(parents, 4)))
     return FA_ERR_INVALID_ARG;
-  if ((int64_t)num_pages * page_size * Hkv * D * 2 >= (1ll << 40)) return FA_ERR_INVALID_ARG;
+  if ((int64_t)num_pages * page_size > (1ll << 40) / (2 * D) / Hkv) return FA_ERR_INVALID_ARG;
+  const fa::SetupDuringCapture setup;
   if (max_pages == 0) {
     const size_t rows = (size_t)B * N * Hq, n = rows * D;
     fa::tree_zero_kernel<<<(unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096), 256, 0,

@@ -741,6 +741,7 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   if (!al(target_probs, 4) || (draft_probs && !al(draft_probs, 4)) || !al(tokens, 4) ||
       !al(parents, 4) || !al(uniforms, 4) || !al(path, 4) || !al(count, 4) || !al(next_token, 4))
     return FA_ERR_INVALID_ARG;
+  const fa::SetupDuringCapture setup;
   fa::VerifyParams p = {};
   p.p = target_probs;
   p.q = draft_probs;
@@ -822,6 +823,7 @@ extern "C" int fa_compact_tree(void* kpages, void* vpages, const int32_t* page_t
   if (rows && (!al(kpages, 16) || !al(vpages, 16))) return FA_ERR_INVALID_ARG;
   if ((int64_t)num_pages * page_size > (1ll << 40) / (2 * D) / (Hkv ? Hkv : 1))
     return FA_ERR_INVALID_ARG;
+  const fa::SetupDuringCapture setup;
   fa::CompactParams p = {};
   p.k = static_cast<uint4*>(kpages);
   p.v = static_cast<uint4*>(vpages);

@@ -486,7 +486,7 @@ int fa_decode_tree_fwd(const void* q, const void* kpages, const void* vpages,
  *
  * Tests, residuals and sums are carried to at least 46 bits, so that the
  * answers are those of 64-bit arithmetic except where u lies within about
- * 1e-13 of a border.  N <= 64 (else FA_ERR_UNSUPPORTED), V >= 1.  A token
+ * 1e-13 of a border.  N <= 64 (else FA_ERR_UNSUPPORTED), 1 <= V < 2^30.  A token
  * outside [0, V) or a parent that is no lower node (nor -1, -2) makes its node
  * unreachable and sets the bounds bit of fa_device_error().
  */
@@ -507,7 +507,8 @@ int fa_verify_tree(const float* target_probs, const float* draft_probs, const in
  *   path            [B, N] int32, device: rising node numbers (fa_verify_tree's)
  *   count           [B] int32, device: in [0, N]
  *   seqlens_out     [B] int32, device, written; may be seqlens
- *   N <= 64 (else FA_ERR_UNSUPPORTED); page_size a positive multiple of 32
+ *   N <= 64 (else FA_ERR_UNSUPPORTED); page_size a positive multiple of 32;
+ *   layers and B at most 65535
  *
  * A sequence with L < N (padding) keeps its rows and its length.  So does one
  * whose length, count, path or page ids are out of range or whose path does

@@ -89,6 +89,7 @@ def tree(fa, **kw):
     dict(pages=-1), dict(maxp=-1), dict(q=0), dict(q=FAKE + 2), dict(o=FAKE + 8), dict(lse=FAKE + 1),
     dict(par=0), dict(par=FAKE + 2), dict(table=0), dict(lens=FAKE + 2), dict(kp=FAKE + 4), dict(vp=0),
     dict(maxp=1 << 26), dict(B=1 << 20, N=64, Hq=64), dict(pages=1 << 30),
+    dict(pages=1 << 30, page=1 << 30, maxp=1, Hkv=8),  # (2^71 bytes: a product would wrap to 0)
 ])
 def test_tree_rejects(fa, kw):
     assert tree(fa, **kw) == fa.FA_ERR_INVALID_ARG

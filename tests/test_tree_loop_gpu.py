@@ -238,6 +238,134 @@ def test_eager_streams_do_not_share_scratch(fa):
             assert torch.equal(a, b)
 
 
+def test_threads_call_at_once(fa):
+    """Four threads, a stream each, with calls of every operator in flight: each
+    gives the bits it gives alone."""
+    import threading
+    steps, refs = [], []
+    for seed in range(4):
+        st = Step(B=2, N=12, Hq=16, Hkv=2, D=64, V=3000, page=64, max_pages=12, seed=20 + seed)
+        st.kp.normal_()
+        st.vp.normal_()
+        st.draw([700 - 50 * seed, 300])
+        st.keep = st.kp.clone(), st.vp.clone()
+        refs.append(st.run(fa))
+        steps.append(st)
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        st, mine = steps[i], []
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                st.kp.copy_(st.keep[0])
+                st.vp.copy_(st.keep[1])
+                mine.append(st.run(fa))
+        got[i] = mine
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert fa.fa_device_error()[0] == fa.FA_OK
+    for ref, mine in zip(refs, got):
+        for out in mine:
+            for a, b in zip(ref[0], out[0]):
+                for x, y in zip(a, b):
+                    assert torch.equal(x, y)
+            for x, y in zip(ref[1:], out[1:]):
+                assert torch.equal(x, y)
+
+
+def test_streams_given_as_handles(fa):
+    """A stream as torch's object, as its handle, and as the handles of the null
+    and the legacy stream."""
+    st = Step(B=1, N=5, Hq=4, Hkv=2, D=64, V=50, page=32, max_pages=2, seed=30)
+    st.kp.normal_()
+    st.vp.normal_()
+    st.draw([40])
+    q = torch.randn(1, 5, 4, 64, device="cuda").to(st.dtype)
+    args = (q, st.kp[0], st.vp[0], st.table, st.lens, st.parents, 0.125)
+    ref = fa.decode_tree(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream, 0, 1, 2):  # (1: the legacy stream, 2: the thread's own)
+        out = fa.decode_tree(*args, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), s
+
+
+def test_call_from_a_new_thread(fa):
+    """A thread that has made no CUDA call yet, with outputs that are there."""
+    import threading
+    st = Step(B=1, N=5, Hq=4, Hkv=2, D=64, V=50, page=32, max_pages=2, seed=31)
+    st.kp.normal_()
+    st.vp.normal_()
+    st.draw([40])
+    q = torch.randn(1, 5, 4, 64, device="cuda").to(st.dtype)
+    args = (q, st.kp[0], st.vp[0], st.table, st.lens, st.parents, 0.125)
+    ref, out, side, errors = fa.decode_tree(*args), torch.empty_like(q), torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+
+    def call():
+        try:
+            fa.decode_tree(*args, out=out, stream=side)
+        except Exception as e:
+            errors.append(e)
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert torch.equal(out, ref)
+
+
+def test_first_call_while_another_thread_captures():
+    """What the first call sets up (the kernels' module and attributes, the
+    scratch pool), here while a capture that forbids such calls on every thread
+    is under way: the capture goes on, and both results are right.  (A process
+    of its own: it is set up once.)"""
+    import subprocess
+    import sys
+    code = """
+import threading, torch
+import attention_fa_fwd_04_gb300 as fa
+bf, i32 = torch.bfloat16, torch.int32
+g = torch.Generator().manual_seed(1)
+q = torch.randn(1, 4, 4, 64, generator=g).to(bf).cuda()
+kp, vp = (torch.randn(9, 32, 2, 64, generator=g).to(bf).cuda() for _ in range(2))
+table = torch.arange(9, dtype=i32, device="cuda")[None]
+lens = torch.tensor([280], dtype=i32, device="cuda")
+parents = torch.tensor([[-1, 0, 0, 2]], dtype=i32, device="cuda")
+out, x = torch.empty_like(q), torch.ones(8, device="cuda")
+side, errors = torch.cuda.Stream(), []
+torch.cuda.synchronize()
+def other():
+    try:
+        fa.decode_tree(q, kp, vp, table, lens, parents, 0.125, out=out, stream=side)
+    except Exception as e:
+        errors.append(e)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, capture_error_mode="global"):
+    x.mul_(2)
+    t = threading.Thread(target=other)
+    t.start()
+    t.join()
+    x.add_(1)
+graph.replay()
+torch.cuda.synchronize()
+assert not errors, errors
+assert x.tolist() == [3.0] * 8
+assert torch.equal(out, fa.decode_tree(q, kp, vp, table, lens, parents, 0.125))
+assert fa.fa_device_error()[0] == fa.FA_OK
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_waits_that_run_out_report_and_the_next_calls_are_correct(fa):
     """A limit of 1 ns: the norm and rotation, the tree decode (its loader polls
     for ring slots) and the verification (aligned rows) give up, report
