@@ -23,13 +23,20 @@
 // nodes where more than one child is tried), once from HBM and for further
 // rejected siblings from L2; in fact the latency of the passes over a row that
 // the sequence with the most rejections needs one after another: 64 trees of 32
-// nodes over 128000 tokens take 44 us (1.5 TB/s of the rows where they stop;
-// about 12000 clocks per pass, at most five passes), one chain of 5 over 32000
-// tokens 5.9 us.  The tests themselves
+// nodes over 128000 tokens take 41.3 us (1.6 TB/s of the rows where they stop;
+// at most five passes of about 10000 clocks: the loads' latency 1400, 7 further
+// stages 1000 or less each, the sums 1300, the walk 800 to 1900), one chain of 5
+// over 32000 tokens 5.9 us.  The tests themselves
 // read single elements: those of all nodes are fetched at once, and the walk
 // runs on shared memory, in one warp of each CTA.  A cluster of up to 8 CTAs
 // takes one sequence: every CTA walks (the same way), and for a mass each sums
-// its part of the row and pushes its sum to the others.
+// its part of the row and pushes its sum to the others, onto a barrier that
+// counts the sums (43.5 us with a cluster barrier after each pass, 1150 clocks).
+//
+// Tried without gain: 16-byte asynchronous copies by every lane in place of bulk
+// copies (43.2 against 43.4 us, without q 24.4 against 19.9), the row's first
+// stages fetched again before the sums meet (44.6 against 43.4: the next child is
+// often accepted, and its row is another).
 #include <math.h>
 
 #include "fa.h"
@@ -71,10 +78,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
@@ -91,13 +94,24 @@ __device__ __forceinline__ float clean(float x) {
 struct __align__(8) Pair {
   float hi, lo;
 };
-__device__ __forceinline__ void store_remote(Pair* local, uint32_t rank, Pair v) {
+// A store into CTA `rank` of the cluster that counts on that CTA's barrier, both
+// given by this CTA's addresses.
+__device__ __forceinline__ void store_remote(Pair* local, uint64_t* bar, uint32_t rank, Pair v) {
   asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(smem_u32(local)),
-      "r"(rank), "f"(v.hi), "f"(v.lo)
+      "{\n\t.reg .b32 a, m;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 m, %1, %2;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [a], {%3, %4}, [m];\n\t}" ::"r"(
+          smem_u32(local)),
+      "r"(smem_u32(bar)), "r"(rank), "f"(v.hi), "f"(v.lo)
       : "memory");
+}
+// Until a barrier's phase is complete: polls, which a sum from another SM ends
+// within about a microsecond, then suspends, within the teardown limit.
+__device__ __forceinline__ void peers_wait(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_test_wait(smem_u32(bar), parity)) return;
+  if (!mbar_wait_drain(bar, parity)) atomicOr(&g_verify_err, kErrTimeout | (23u << 8));
 }
 __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
@@ -228,13 +242,21 @@ __device__ __forceinline__ void left4(float4 a, float4 d, int v, const Rejected&
   }
 }
 
+// A sum whose lower part may pass half a step of the upper one: a few of them
+// may be added up so, and tidy() ends such a run.  (A third fewer operations in a
+// row; 64 trees over 128000 tokens without q 20.6 -> 19.9 us.)
+__device__ __forceinline__ Pair add_loose(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return {s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
+}
+__device__ __forceinline__ Pair tidy(Pair a) { return fast_two_sum(a.hi, a.lo); }
 __device__ __forceinline__ Pair lane_sum(const Pair2& a) {
-  return add(fast_two_sum(a.hi.x, a.lo.x), fast_two_sum(a.hi.y, a.lo.y));
+  return add_loose({a.hi.x, a.lo.x}, {a.hi.y, a.lo.y});
 }
 __device__ __forceinline__ Pair warp_sum(Pair t) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
-  return t;
+  for (int o = 16; o > 0; o >>= 1) t = add_loose(t, shfl_xor(t, o));
+  return tidy(t);
 }
 __device__ __forceinline__ void gather(Pair2& acc, const Pair2 (&r)[2]) {
 #pragma unroll
@@ -335,7 +357,7 @@ __device__ __forceinline__ Pair sum_ring(const float* pr, const float* qr, int v
   ring.n += i < n ? (i + vf::STAGES < n ? i + vf::STAGES : n) : n;
   Pair t = lane_sum(acc[0]);
 #pragma unroll
-  for (int g = 1; g < E / 128; ++g) t = add(t, lane_sum(acc[g]));
+  for (int g = 1; g < E / 128; ++g) t = add_loose(t, lane_sum(acc[g]));
   return warp_sum(t);
 }
 
@@ -378,12 +400,19 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
   __shared__ uint32_t s_first[2];
   __shared__ Pair s_c;
   __shared__ int s_abort;
+  __shared__ uint64_t s_sums[2];  // counts the sums that arrive in s_cta
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
-  cluster_arrive();  // (waited for below: no CTA is written to before it runs)
-  pdl_wait_primary();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), CL = p.cluster;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&s_sums[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&s_sums[i], CL * sizeof(Pair));
+  }
+  __syncwarp();
+  cluster_arrive();  // (waited for below: no CTA is written to before it runs)
+  pdl_wait_primary();
   const int b = blockIdx.x / CL;
   const int N = p.N, V = p.V;
   const size_t node0 = (size_t)b * N;
@@ -447,17 +476,22 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
     if (warp == 0) {
       Pair t = lane < W ? s_warp[lane] : Pair{0.f, 0.f};
 #pragma unroll 1
-      for (int o = W / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
-      if (lane < CL) store_remote(&s_cta[pass & 1][rank], lane, t);
+      for (int o = W / 2; o > 0; o >>= 1) t = add_loose(t, shfl_xor(t, o));
+      t = tidy(t);
+      if (lane < CL) store_remote(&s_cta[pass & 1][rank], &s_sums[pass & 1], lane, t);
     }
-    cluster_sync();
+    // The other CTAs' sums.  (All of them come: what a CTA waits for before it
+    // sends is bounded, and all walk by the same sums.)  A CTA sends its next one
+    // after this one has been read here, so two buffers are enough.
+    peers_wait(&s_sums[pass & 1], ((pass - 1) >> 1) & 1);
+    if (tid == 0) mbar_arrive_expect_tx(&s_sums[pass & 1], CL * sizeof(Pair));
   };
   // (The same bits in every warp of every CTA.)
   auto total_of = [&]() {
     Pair t = lane < CL ? s_cta[pass & 1][lane] : Pair{0.f, 0.f};
 #pragma unroll 1
-    for (int o = vf::CLUSTER / 2; o > 0; o >>= 1) t = add(t, shfl_xor(t, o));
-    return shfl(t, 0);
+    for (int o = vf::CLUSTER / 2; o > 0; o >>= 1) t = add_loose(t, shfl_xor(t, o));
+    return shfl(tidy(t), 0);
   };
 
   // The walk, by warp 0; the others join for masses.
@@ -547,62 +581,71 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
     mass_of(cur, rj);
     total = total_of();
   }
-  if (!(total.hi > 0.f)) {
-    if (rank == 0 && tid == 0) p.next[b] = -1;
-    return;
-  }
-  const Pair aim = mul(Pair{s_u[0], 0.f}, total);
-  Pair before{0.f, 0.f};
-  if (pick_part(s_cta[pass & 1], CL, aim, &before) != rank) return;
-  const int at = pick_part(s_warp, W, aim, &before);
-  // That part of the row, a group of 128 tokens per warp, four per lane.
-  const long long v0 = ((long long)rank * W + at) * p.part;
-  const int vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
-  const float* pr = p.p + (node0 + cur) * V;
-  const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-  int found = INT32_MAX, last_v = -1;
-  for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * W) {
-    const int v = w0 + warp * 128 + lane * 4;
-    const float4 a = clean4(load4<VEC, 1>(pr, v, vb));
-    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (DRAFT && rj.n > 0) d = clean4(load4<VEC, 1>(qr, v, vb));
-    Pair2 r2[2];
-    left4<DRAFT, 1, 2>(a, d, v, rj, r2);
-    const Pair r[4] = {fast_two_sum(r2[0].hi.x, r2[0].lo.x), fast_two_sum(r2[0].hi.y, r2[0].lo.y),
-                       fast_two_sum(r2[1].hi.x, r2[1].lo.x), fast_two_sum(r2[1].hi.y, r2[1].lo.y)};
-    const Pair own = add(add(r[0], r[1]), add(r[2], r[3]));
-    const Pair inc = scan(own, 32);
-    __syncthreads();  // (s_warp and s_pick have been read)
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    const Pair upto = scan(lane < W ? s_warp[lane] : Pair{0.f, 0.f}, W);
-    Pair start = shfl(upto, warp > 0 ? warp - 1 : 0);
-    start = warp > 0 ? add(before, start) : before;
-    const uint32_t some = __ballot_sync(0xffffffffu, own.hi > 0.f);
-    const uint32_t past = __ballot_sync(0xffffffffu, above(add(start, inc), aim)) & some;
-    const int l = past ? __ffs(past) - 1 : (some ? 31 - __clz(some) : 0);
-    const Pair up = shfl(inc, l > 0 ? l - 1 : 0);
-    if (lane == l) {
-      // The lane's first that passes the aim; its last with mass where
-      // rounding (or a missing aim) leaves none.
-      Pair run = l > 0 ? add(start, up) : start;
-      int pick = -1;
+  auto draw = [&]() {
+    if (!(total.hi > 0.f)) {
+      if (rank == 0 && tid == 0) p.next[b] = -1;
+      return;
+    }
+    const Pair aim = mul(Pair{s_u[0], 0.f}, total);
+    Pair before{0.f, 0.f};
+    if (pick_part(s_cta[pass & 1], CL, aim, &before) != rank) return;
+    const int at = pick_part(s_warp, W, aim, &before);
+    // That part of the row, a group of 128 tokens per warp, four per lane.
+    const long long v0 = ((long long)rank * W + at) * p.part;
+    const int vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
+    const float* pr = p.p + (node0 + cur) * V;
+    const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
+    int found = INT32_MAX, last_v = -1;
+    for (int w0 = (int)v0; w0 < vb && found == INT32_MAX; w0 += 128 * W) {
+      const int v = w0 + warp * 128 + lane * 4;
+      const float4 a = clean4(load4<VEC, 1>(pr, v, vb));
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (DRAFT && rj.n > 0) d = clean4(load4<VEC, 1>(qr, v, vb));
+      Pair2 r2[2];
+      left4<DRAFT, 1, 2>(a, d, v, rj, r2);
+      const Pair r[4] = {fast_two_sum(r2[0].hi.x, r2[0].lo.x), fast_two_sum(r2[0].hi.y, r2[0].lo.y),
+                         fast_two_sum(r2[1].hi.x, r2[1].lo.x), fast_two_sum(r2[1].hi.y, r2[1].lo.y)};
+      const Pair own = add(add(r[0], r[1]), add(r[2], r[3]));
+      const Pair inc = scan(own, 32);
+      __syncthreads();  // (s_warp and s_pick have been read)
+      if (lane == 31) s_warp[warp] = inc;
+      __syncthreads();
+      const Pair upto = scan(lane < W ? s_warp[lane] : Pair{0.f, 0.f}, W);
+      Pair start = shfl(upto, warp > 0 ? warp - 1 : 0);
+      start = warp > 0 ? add(before, start) : before;
+      const uint32_t some = __ballot_sync(0xffffffffu, own.hi > 0.f);
+      const uint32_t past = __ballot_sync(0xffffffffu, above(add(start, inc), aim)) & some;
+      const int l = past ? __ffs(past) - 1 : (some ? 31 - __clz(some) : 0);
+      const Pair up = shfl(inc, l > 0 ? l - 1 : 0);
+      if (lane == l) {
+        // The lane's first that passes the aim; its last with mass where
+        // rounding (or a missing aim) leaves none.
+        Pair run = l > 0 ? add(start, up) : start;
+        int pick = -1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (r[e].hi > 0.f && (!past || pick < 0 || !above(run, aim))) pick = v + e;
-        run = add(run, r[e]);
+        for (int e = 0; e < 4; ++e) {
+          if (r[e].hi > 0.f && (!past || pick < 0 || !above(run, aim))) pick = v + e;
+          run = add(run, r[e]);
+        }
+        s_pick[0][warp] = past ? pick : INT32_MAX;
+        s_pick[1][warp] = some ? pick : -1;
       }
-      s_pick[0][warp] = past ? pick : INT32_MAX;
-      s_pick[1][warp] = some ? pick : -1;
+      __syncthreads();
+      for (int i = 0; i < W; ++i) {
+        found = s_pick[0][i] < found ? s_pick[0][i] : found;
+        last_v = s_pick[1][i] > last_v ? s_pick[1][i] : last_v;
+      }
+      before = add(before, shfl(upto, W - 1));
     }
-    __syncthreads();
-    for (int i = 0; i < W; ++i) {
-      found = s_pick[0][i] < found ? s_pick[0][i] : found;
-      last_v = s_pick[1][i] > last_v ? s_pick[1][i] : last_v;
-    }
-    before = add(before, shfl(upto, W - 1));
-  }
-  if (tid == 0) p.next[b] = found != INT32_MAX ? found : last_v;
+    if (tid == 0) p.next[b] = found != INT32_MAX ? found : last_v;
+  };
+  // The other CTAs may leave from here on, and this one once they are here: none
+  // is written to after it has gone, even if a call's inputs change under it and
+  // its CTAs disagree on the walk.
+  cluster_arrive();
+  draw();
+  __syncwarp();
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -754,12 +797,12 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   p.N = N;
   p.V = V;
   // CTAs per sequence: 8, or as few of 8 warps as leave all of them resident at
-  // once (64 sequences of 128000 tokens: 8 CTAs 43.6 us, 4 51.2 us), or twice
-  // that where a warp's part would pass 1024 tokens (200 of 32000: 4 CTAs 22.2 us,
-  // 2 25.6 us); and no more than give each warp a stage of tokens.
+  // once (64 sequences of 128000 tokens: 8 CTAs 41.1 us, 4 61.2 us), or twice
+  // that where a warp's part would pass 1024 tokens (200 of 32000: 4 CTAs 21.2 us,
+  // 2 23.8 us); and no more than give each warp a stage of tokens.
   // 16 warps where the SMs are not filled and a warp's part stays above 256
-  // tokens (16 sequences of 128000: 16 warps 22.7 us, 8 25.4 us, 32 24.0 us; one of
-  // 32000: 16 warps 6.5 us, 8 5.9 us).
+  // tokens (16 sequences of 128000: 16 warps 21.2 us, 8 23.2 us; one of 32000: 16
+  // warps 6.3 us, 8 5.8 us).
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
   auto part_of = [&](int cluster, int warps) {
     const int n = cluster * warps;
