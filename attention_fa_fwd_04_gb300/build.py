@@ -51,7 +51,7 @@ def _bind_command(out):
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
             "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
             "-I", os.path.join(cuda, "include"), BIND_SOURCE, "-o", out, "-L", lib,
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -12,7 +12,7 @@
 // module and the ctypes binding use the one loaded copy.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -114,8 +114,12 @@ struct Stream {
   }
 };
 
+// A new tensor on the current device: at::empty without its dispatch.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const Device& dev) {
+  return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, dev.index), std::nullopt);
+}
 at::Tensor output(PyObject* given, const char* name, const at::Tensor& like, const Device& dev) {
-  if (given == Py_None) return at::empty(like.sizes(), like.options());
+  if (given == Py_None) return fresh(like.sizes(), like.scalar_type(), dev);
   const at::Tensor& t = tensor(given, name);
   if (t.scalar_type() != like.scalar_type() || t.sizes() != like.sizes())
     bad_value(std::string(name) + " must have the input's shape and dtype");
@@ -288,10 +292,9 @@ PyObject* norm_rope_backward(PyObject* const* a) {
   dev.has(gq);
   dev.has(gk);
   Stream s(a[10], dev.index);
-  const at::Tensor dq = at::empty(h.q.sizes(), h.q.options());
-  const at::Tensor dk = at::empty(h.k.sizes(), h.k.options());
-  const at::Tensor dqw = at::empty({h.D}, h.q.options().dtype(at::kFloat));
-  const at::Tensor dkw = at::empty({h.D}, h.q.options().dtype(at::kFloat));
+  const at::Tensor dq = fresh(h.q.sizes(), h.q.scalar_type(), dev);
+  const at::Tensor dk = fresh(h.k.sizes(), h.k.scalar_type(), dev);
+  const at::Tensor dqw = fresh({h.D}, at::kFloat, dev), dkw = fresh({h.D}, at::kFloat, dev);
   const int st = unlocked(
       p_rope_backward, gq.const_data_ptr(), gk.const_data_ptr(), h.q.const_data_ptr(),
       h.k.const_data_ptr(), h.qw.const_data_ptr(), h.kw.const_data_ptr(), f32(h.freq), i32(*h.pos),
@@ -350,7 +353,7 @@ PyObject* tree(PyObject* const* a) {
   at::Tensor lse;
   const bool want = a[9] != Py_None && a[9] != Py_False;
   if (a[9] == Py_True) {
-    lse = at::empty(rows, q.options().dtype(at::kFloat));
+    lse = fresh(rows, at::kFloat, dev);
   } else if (want) {
     lse = tensor(a[9], "lse");
     if (lse.scalar_type() != at::kFloat) bad_value("lse must be a float32 tensor [B,N,Hq]");
@@ -393,8 +396,8 @@ PyObject* verify(PyObject* const* a) {
   dev.has(parents);
   dev.has(u);
   Stream s(a[5], dev.index);
-  const auto opt = tokens.options();
-  const at::Tensor path = at::empty(bn, opt), count = at::empty(b1, opt), next = at::empty(b1, opt);
+  const at::Tensor path = fresh(bn, at::kInt, dev), count = fresh(b1, at::kInt, dev),
+                   next = fresh(b1, at::kInt, dev);
   const int st =
       unlocked(p_verify, f32(p), q ? f32(*q) : nullptr, i32(tokens), i32(parents), f32(u),
                static_cast<int32_t*>(path.data_ptr()), static_cast<int32_t*>(count.data_ptr()),
