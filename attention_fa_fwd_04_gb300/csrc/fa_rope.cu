@@ -25,8 +25,8 @@
 // Loads: a token's heads are contiguous, so each warp fetches steps of up to 16
 // (D = 128) or 32 heads by one bulk copy into a ring of its own in shared
 // memory, two steps ahead of its arithmetic: 128 to 192 KiB in flight per SM
-// whatever the arithmetic's latency.  8192 tokens of 128 + 8 heads, D = 128: 97 us,
-// 5.9 TB/s (84 us at the copy bandwidth); loads into registers, two head groups
+// whatever the arithmetic's latency.  8192 tokens of 128 + 8 heads, D = 128: 98 us,
+// 5.8 TB/s (84 us at the copy bandwidth); loads into registers, two head groups
 // ahead, held 64 KiB in flight and took 117 us.
 //
 // Angles: positions reach 2^31, where an fp32 product p * inv_freq has no
@@ -51,7 +51,8 @@ namespace rp {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int STAGE_BYTES = 4096;
-template <int D, bool BWD>
+// FEW: several tokens per step (see rope_few_kernel).
+template <int D, bool BWD, bool FEW = false>
 struct Cfg {
   static constexpr int STAGES = 3;  // steps in a warp's ring
   static constexpr int BLOCKS_PER_SM = 2;
@@ -61,8 +62,11 @@ struct Cfg {
   // A step fills a stage with heads (the gradient: with x and g of half as many).
   static constexpr int UNITS = 4;  // head groups per step
   static constexpr int HEADS = UNITS * HPW;
-  // Rings, cosines and sines of a warp's token, turn fractions, barriers.
-  static constexpr int SMEM_CS = WARPS * D * 4;
+  // Tokens of a step, at most (FEW).
+  static constexpr int TOKENS = FEW ? 384 / D : 1;
+  // Rings, cosines and sines of a warp's tokens, turn fractions, barriers.
+  static constexpr int TABLE = TOKENS * D;
+  static constexpr int SMEM_CS = WARPS * TABLE * 4;
   static constexpr int SMEM_TOTAL =
       WARPS * STAGES * STAGE_BYTES + SMEM_CS + (D / 2) * 8 + WARPS * STAGES * 8 + 16;
 };
@@ -118,9 +122,12 @@ struct RopePart {
   int paged;
   // Forward: the part's steps are [first, first + steps) of a token's.
   int first, steps;
-  // Gradient: blocks [b0, b0 + nb) of the grid walk the part, by tasks of its own.
+  // Gradient, and few heads: blocks [b0, b0 + nb) of the grid walk the part, by
+  // tasks of its own.
   int b0, nb;
   int spt, cpt;
+  // Few heads: tokens per step; r * inv_h >> 16 = r / H for the rows of a step.
+  int tg, inv_h;
 };
 
 struct RopeParams {
@@ -136,6 +143,7 @@ struct RopeParams {
   // A task is up to spt steps of one token, cpt tasks per token.
   int steps, spt, cpt;
   int rot;
+  int inv_half;  // j * inv_half >> 16 = j / (rot / 2) for a step's table
   float eps;
   float* partial;  // gradient: [blocks][D] sums of dw
 };
@@ -179,29 +187,75 @@ __device__ __forceinline__ void load_fractions(const float* inv_freq, int n,
   __syncthreads();
 }
 
-// Whole warp: cosines and sines of a position into the warp's table (frequency
-// i's computed by one lane).
+// Cosine and sine of a position's angle.  The phase's upper 32 bits are enough:
+// 2^-32 turns are 2^-29 radians.  The nearest quarter turn is taken off exactly,
+// and the Taylor series of what is left (at most pi / 4) end where their next
+// term, r^11 / 11! and r^12 / 12!, is below 2^-28.  Within 1.7 * 2^-24 of the
+// cosine and sine.  (sincospif reduces its argument itself: 32768 tokens of 8 + 2
+// heads, D = 128, several tokens per step: 49.5 us with it, 48.4 so.)
+__device__ __forceinline__ float2 cos_sin_at(unsigned long long fraction, int pos) {
+  const uint32_t ph = (uint32_t)(fraction * (unsigned long long)(long long)pos >> 32);
+  const uint32_t quarter = (ph + 0x20000000u) >> 30;
+  const float r = (float)(int)(ph - (quarter << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float z = r * r;
+  float s = fmaf(z, 1.f / 362880, -1.f / 5040), c = fmaf(z, -1.f / 3628800, 1.f / 40320);
+  s = fmaf(z, s, 1.f / 120);
+  c = fmaf(z, c, -1.f / 720);
+  s = fmaf(z, s, -1.f / 6);
+  c = fmaf(z, c, 1.f / 24);
+  s = fmaf(z * s, r, r);
+  c = fmaf(z, fmaf(z, c, -0.5f), 1.f);
+  float2 v = quarter & 1 ? make_float2(s, c) : make_float2(c, s);
+  if ((quarter + 1) & 2) v.x = -v.x;
+  if (quarter & 2) v.y = -v.y;
+  return v;
+}
+// Whole warp: cosines and then sines of a position's rot / 2 angles into the warp's
+// table (each computed by one lane).
 template <int D>
 __device__ __forceinline__ void cos_sin(int rot, int pos, const unsigned long long* sF,
-                                        float2* table) {
+                                        float* table) {
   const int lane = threadIdx.x & 31;
   __syncwarp();  // (the table's last values have been read)
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
     const int f = lane + 32 * i;
     if (f < rot / 2) {
-      const unsigned long long ph = sF[f] * (unsigned long long)(long long)pos;
-      // Signed fraction of a turn in [-1/2, 1/2), times two: half turns.
-      float2 v;
-      sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &v.y, &v.x);
-      table[f] = v;
+      const float2 v = cos_sin_at(sF[f], pos);
+      table[f] = v.x;
+      table[rot / 2 + f] = v.y;
     }
   }
   __syncwarp();
 }
-// Frequency f's, or 1 and 0 for elements that pass through (f < 0).
-__device__ __forceinline__ float2 cos_sin_of(const float2* table, int f) {
-  return f >= 0 ? table[f] : make_float2(1.f, 0.f);
+// The same for n tokens, lane l holding the l-th one's position: [token][rot].
+__device__ __forceinline__ void cos_sin_group(const RopeParams& p, int n, int pos,
+                                              const unsigned long long* sF, float* table) {
+  const int lane = threadIdx.x & 31, half = p.rot / 2;
+  __syncwarp();  // (the table's last values have been read)
+#pragma unroll 2
+  for (int j0 = 0; j0 < n * half; j0 += 32) {
+    const int j = j0 + lane, t = j * p.inv_half >> 16;
+    const int at = __shfl_sync(0xffffffffu, pos, t);
+    if (j < n * half) {
+      const float2 v = cos_sin_at(sF[j - t * half], at);
+      table[t * half + j] = v.x;
+      table[t * half + j + half] = v.y;
+    }
+  }
+  __syncwarp();
+}
+// Four of a token's angles from the f-th on (f a multiple of 4), or 1 and 0 for
+// elements that pass through (f < 0).
+__device__ __forceinline__ void cos_sin_of(const float* table, int half, int f, float* cs,
+                                           float* sn) {
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (f >= 0) {
+    c = *reinterpret_cast<const float4*>(table + f);
+    s = *reinterpret_cast<const float4*>(table + half + f);
+  }
+  cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+  sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
 }
 
 // The rotation as two products per output, o0 = x0 c0 + y0 s0 and o1 = x1 c1 +
@@ -245,8 +299,9 @@ struct Turn {
 // negative angle) is o = x c + y s with y the chunk that holds the pairs' other
 // elements (neighbours: x swapped), read from the ring as well.  With half the
 // registers per head, two head groups' chains run side by side within 128
-// registers (16384 tokens of 16 + 16 heads: 67.7 us; one after another at 80
-// registers and three blocks per SM 82 us; both chunks in a lane 89 us).
+// registers (16384 tokens of 16 + 16 heads, before later steps: 67.7 us; one after
+// another at 80 registers and three blocks per SM 82 us; both chunks in a lane 89 us).
+// Now 65.5 us, 6.1 TB/s.
 template <int D, bool IL>
 struct BackMap {
   static constexpr int LPH = D / 8;
@@ -274,20 +329,35 @@ struct BackMap {
 template <bool IL>
 struct TurnBack {
   float2 c[4], s[4];
-  template <typename MAP>
-  __device__ __forceinline__ void set(const float2* table, const MAP& m) {
+  __device__ __forceinline__ TurnBack() {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if constexpr (IL) {
-        const float2 v = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + e);
-        c[e] = both(v.x);
-        s[e] = make_float2(v.y, -v.y);
-      } else {
-        const float2 v = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + 2 * e);
-        const float2 w = cos_sin_of(table, m.f0 < 0 ? -1 : m.f0 + 2 * e + 1);
-        c[e] = make_float2(v.x, w.x);
-        s[e] = make_float2(m.sign * v.y, m.sign * w.y);
-      }
+      c[e] = both(1.f);
+      s[e] = both(0.f);
+    }
+  }
+  template <typename MAP>
+  __device__ __forceinline__ void set(const float* table, int half, const MAP& m) {
+    if (m.f0 < 0) return;  // (elements that pass through keep 1 and 0)
+    const float4 c0 = *reinterpret_cast<const float4*>(table + m.f0);
+    const float4 s0 = *reinterpret_cast<const float4*>(table + half + m.f0);
+    if constexpr (IL) {
+      c[0] = both(c0.x), c[1] = both(c0.y), c[2] = both(c0.z), c[3] = both(c0.w);
+      s[0] = make_float2(s0.x, -s0.x);
+      s[1] = make_float2(s0.y, -s0.y);
+      s[2] = make_float2(s0.z, -s0.z);
+      s[3] = make_float2(s0.w, -s0.w);
+    } else {
+      const float4 c1 = *reinterpret_cast<const float4*>(table + m.f0 + 4);
+      const float4 s1 = *reinterpret_cast<const float4*>(table + half + m.f0 + 4);
+      c[0] = make_float2(c0.x, c0.y);
+      c[1] = make_float2(c0.z, c0.w);
+      c[2] = make_float2(c1.x, c1.y);
+      c[3] = make_float2(c1.z, c1.w);
+      s[0] = __fmul2_rn(both(m.sign), make_float2(s0.x, s0.y));
+      s[1] = __fmul2_rn(both(m.sign), make_float2(s0.z, s0.w));
+      s[2] = __fmul2_rn(both(m.sign), make_float2(s1.x, s1.y));
+      s[3] = __fmul2_rn(both(m.sign), make_float2(s1.z, s1.w));
     }
   }
 };
@@ -329,18 +399,18 @@ __device__ __forceinline__ uint4 ring_load(const uint8_t* p) {
 }
 
 // Shared memory of a block and of one of its warps.
-template <int D, bool BWD>
+template <int D, bool BWD, bool FEW = false>
 struct RopeSmem {
   uint8_t* ring;
-  float2* table;
+  float* table;
   unsigned long long* frac;
   uint64_t* full;
   volatile int* abort_flag;
-  using C = rp::Cfg<D, BWD>;
+  using C = rp::Cfg<D, BWD, FEW>;
   __device__ __forceinline__ RopeSmem(uint8_t* smem, int warp) {
     ring = smem + warp * C::STAGES * rp::STAGE_BYTES;
     uint8_t* q = smem + rp::WARPS * C::STAGES * rp::STAGE_BYTES;
-    table = reinterpret_cast<float2*>(q) + warp * (D / 2);
+    table = reinterpret_cast<float*>(q) + warp * C::TABLE;
     q += C::SMEM_CS;
     frac = reinterpret_cast<unsigned long long*>(q);
     q += (D / 2) * 8;
@@ -449,12 +519,8 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, false>::BLOCKS_PER_SM)
       if constexpr (PAGED) row = cache_row(p, token, &slot);
       if (pt.w) {
         cos_sin<D>(p.rot, PAGED && !p.positions ? slot : pos, sm.frac, sm.table);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 v = cos_sin_of(sm.table, m.freq(e, p.rot));
-          cs[e] = v.x;
-          sn[e] = v.y;
-        }
+        cos_sin_of(sm.table, p.rot / 2, m.freq(0, p.rot), cs, sn);
+        cos_sin_of(sm.table, p.rot / 2, m.freq(4, p.rot), cs + 4, sn + 4);
       }
     }
     float2 a[4], b[4];
@@ -506,19 +572,162 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, false>::BLOCKS_PER_SM)
   if (*sm.abort_flag) drain_ring<C::STAGES>(sm.full, k, issued);
 }
 
+// Few heads per token: a step takes several tokens, so that it still fills the
+// lanes and moves a few KB.  Blocks walk one part each, as in the gradient; a
+// step's rows are its tokens' heads one after another, the table holds the
+// cosines and sines of its tokens, and each lane makes the factors of its own
+// row's token.  50640 tokens of 4 + 2 heads, D = 64: 19.8 us, 3.9 TB/s (11.5 us at
+// the copy bandwidth); bound by the instructions per row, half of the issue slots.
+
+// Copies of a step's heads of the tokens [t0, t0 + n) into `to`; whole warp.
+template <int D, typename T>
+__device__ __forceinline__ void fetch_group(const void* x, long long xs, int H, long long t0, int n,
+                                            uint8_t* to, uint64_t* bar) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t bytes = (uint32_t)H * D * 2;
+  const T* src = static_cast<const T*>(x) + t0 * xs;
+  if (xs == (long long)H * D) {
+    if (lane == 0) bulk_load(to, src, n * bytes, bar);
+  } else if (lane < n) {
+    bulk_load(to + lane * bytes, src + lane * xs, bytes, bar);
+  }
+}
+
+template <int D, typename T, bool IL, bool PAGED>
+__global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, false, true>::BLOCKS_PER_SM)
+    rope_few_kernel(const __grid_constant__ RopeParams p) {
+  using C = rp::Cfg<D, false, true>;
+  using M = LaneMap<D, IL>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RopeSmem<D, false, true> sm(smem, warp);
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&sm.full[i], 1);
+    if (warp == 0) *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait_primary();
+  const M m(lane, p.rot);
+  int part = 0;
+  if (p.n_parts > 1 && (int)blockIdx.x >= p.part[1].b0) part = 1;
+  if (PAGED && p.n_parts > 2 && (int)blockIdx.x >= p.part[2].b0) part = 2;
+  const RopePart& pt = p.part[part];
+  const int H = pt.H, tg = pt.tg, half = p.rot / 2;
+  const int groups = (p.tokens + tg - 1) / tg, warps = pt.nb * rp::WARPS;
+  int at = (blockIdx.x - pt.b0) * rp::WARPS + warp, ahead = at;
+  uint32_t issued = 0;
+  auto tokens_of = [&](int g) { return p.tokens - g * tg < tg ? p.tokens - g * tg : tg; };
+  auto fetch = [&]() {
+    if (ahead >= groups) return;
+    const int n = tokens_of(ahead), st = issued % C::STAGES;
+    if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)n * H * D * 2);
+    __syncwarp();
+    fetch_group<D, T>(pt.x, pt.xs, H, (long long)ahead * tg, n, sm.ring + st * rp::STAGE_BYTES,
+                      &sm.full[st]);
+    ++issued;
+    ahead += warps;
+  };
+  __syncwarp();
+  for (int i = 0; i < C::STAGES; ++i) fetch();
+  const bool own_pos = !PAGED || p.positions, normed = !PAGED || pt.w;
+  auto position = [&](int g) {
+    return own_pos && normed && g < groups && lane < tokens_of(g) ? p.positions[g * tg + lane] : 0;
+  };
+  int pos_n = position(at);
+  float2 wa[4], wb[4];
+  if (normed) {
+    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c0 * 8), wa);
+    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c1 * 8), wb);
+  }
+  load_fractions(p.inv_freq, half, sm.frac);  // (ends with the block's barrier)
+
+  uint32_t k = 0;
+  for (; at < groups; at += warps, ++k) {
+    const int n = tokens_of(at), rows = n * H;
+    int pos = pos_n;
+    pos_n = position(at + warps);
+    long long row = 0;
+    if constexpr (PAGED) {
+      if (lane < n && (pt.paged || !own_pos)) {
+        int slot;
+        row = cache_row(p, at * tg + lane, &slot);
+        if (!own_pos) pos = slot;
+      }
+    }
+    if (normed) cos_sin_group(p, n, pos, sm.frac, sm.table);
+    T* const y = static_cast<T*>(pt.y) + (long long)at * tg * H * D;
+    const uint8_t* x = sm.ring + (k % C::STAGES) * rp::STAGE_BYTES + m.sub * D * 2;
+    if (!mbar_wait<true>(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, sm.abort_flag,
+                         &g_rope_err, 20))
+      break;
+    __syncwarp();
+    Turn<IL> turn;
+    int turned = -1;  // the token whose factors `turn` holds
+    for (int u = 0; u * C::HPW < rows; ++u) {
+      // (A lane past the last row works on what its ring holds.)
+      const int r = u * C::HPW + m.sub;
+      int t = r * pt.inv_h >> 16;
+      t = t < n ? t : n - 1;
+      uint4 r0 = ring_load(x + u * C::HPW * D * 2 + m.c0 * 16);
+      uint4 r1 = ring_load(x + u * C::HPW * D * 2 + m.c1 * 16);
+      if (normed) {
+        float2 a[4], b[4];
+        unpack8<T>(r0, a);
+        unpack8<T>(r1, b);
+        float2 s2 = both(0.f), t2 = both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s2 = __ffma2_rn(a[e], a[e], s2);
+          t2 = __ffma2_rn(b[e], b[e], t2);
+        }
+        if (t != turned) {
+          turned = t;
+          float cs[8], sn[8];
+          cos_sin_of(sm.table + t * p.rot, half, m.freq(0, p.rot), cs, sn);
+          cos_sin_of(sm.table + t * p.rot, half, m.freq(4, p.rot), cs + 4, sn + 4);
+          turn.set(cs, sn, wa, wb);
+        }
+        const float ss = head_sum<M::LPH>((s2.x + s2.y) + (t2.x + t2.y));
+        turn.apply(a, b, rsqrtf(ss * (1.f / D) + p.eps));
+        r0 = pack8<T>(a);
+        r1 = pack8<T>(b);
+      }
+      T* dst = y + r * D;
+      bool real = r < rows;
+      if constexpr (PAGED) {
+        const long long to = __shfl_sync(0xffffffffu, row, t);
+        if (pt.paged) {
+          dst = static_cast<T*>(pt.y) + (to * H + (r - t * H)) * D;
+          real = real && to >= 0;
+        }
+      }
+      if (real) {
+        *reinterpret_cast<uint4*>(dst + m.c0 * 8) = r0;
+        *reinterpret_cast<uint4*>(dst + m.c1 * 8) = r1;
+      }
+    }
+    __syncwarp();  // the stage has been read
+    fetch();
+  }
+  if (*sm.abort_flag) drain_ring<C::STAGES>(sm.full, k, issued);
+}
+
 // Gradient of rope_kernel.  Each block walks the queries or the keys, and ends
 // with one row of partial[] (its sum of gy x r per column); the sums of a
 // lane, a block and the blocks are taken in a fixed order, so equal calls give
 // equal bits.
-template <int D, typename T, bool IL>
-__global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
+// FEW: steps of several tokens, as in rope_few_kernel (walked as groups of one
+// step each).
+template <int D, typename T, bool IL, bool FEW>
+__global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true, FEW>::BLOCKS_PER_SM)
     rope_bwd_kernel(const __grid_constant__ RopeParams p) {
-  using C = rp::Cfg<D, true>;
+  using C = rp::Cfg<D, true, FEW>;
   using M = BackMap<D, IL>;
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const RopeSmem<D, true> sm(smem, warp);
+  const RopeSmem<D, true, FEW> sm(smem, warp);
   if (lane == 0) {
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&sm.full[i], 1);
     if (warp == 0) *sm.abort_flag = 0;
@@ -529,12 +738,23 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
   const RopePart& pt = p.part[p.n_parts > 1 && (int)blockIdx.x >= p.part[1].b0 ? 1 : 0];
   const int warps = pt.nb * rp::WARPS;
   const int dt = warps / pt.cpt, dc = warps - dt * pt.cpt;
+  const int tg = FEW ? pt.tg : 1, items = FEW ? (p.tokens + tg - 1) / tg : p.tokens;
+  auto tokens_of = [&](int g) { return p.tokens - g * tg < tg ? p.tokens - g * tg : tg; };
   RopeWalk at((blockIdx.x - pt.b0) * rp::WARPS + warp, pt.cpt, pt.spt), ahead = at;
   uint32_t issued = 0;
   // x in the first half of the stage, g in the second.
   auto fetch = [&]() {
-    if (ahead.t >= p.tokens) return;
-    if (lane == 0) {
+    if (ahead.t >= items) return;
+    if constexpr (FEW) {
+      const int n = tokens_of(ahead.t), st = issued % C::STAGES;
+      const long long t0 = (long long)ahead.t * tg;
+      uint8_t* to = sm.ring + st * rp::STAGE_BYTES;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)n * pt.H * D * 4);
+      __syncwarp();
+      fetch_group<D, T>(pt.x, pt.xs, pt.H, t0, n, to, &sm.full[st]);
+      fetch_group<D, T>(pt.g, (long long)pt.H * D, pt.H, t0, n, to + rp::STAGE_BYTES / 2,
+                        &sm.full[st]);
+    } else if (lane == 0) {
       const int h0 = ahead.s * C::HEADS;
       const uint32_t bytes = (uint32_t)(pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS) * D * 2;
       const int st = issued % C::STAGES;
@@ -543,14 +763,20 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
       bulk_load(to, static_cast<const T*>(pt.x) + ahead.t * pt.xs + (size_t)h0 * D, bytes,
                 &sm.full[st]);
       bulk_load(to + rp::STAGE_BYTES / 2,
-                static_cast<const T*>(pt.g) + ((long long)ahead.t * pt.H + h0) * D, bytes, &sm.full[st]);
+                static_cast<const T*>(pt.g) + ((long long)ahead.t * pt.H + h0) * D, bytes,
+                &sm.full[st]);
     }
     ++issued;
     ahead.next(pt.cpt, pt.spt, pt.steps, dt, dc);
   };
   __syncwarp();
   for (int i = 0; i < C::STAGES; ++i) fetch();
-  int pos_n = at.t < p.tokens ? p.positions[at.t] : 0;
+  // FEW: lane l holds the l-th token's.
+  auto position = [&](int g) {
+    if constexpr (FEW) return g < items && lane < tokens_of(g) ? p.positions[g * tg + lane] : 0;
+    return g < items ? p.positions[g] : 0;
+  };
+  int pos_n = position(at.t);
   float2 w[4];
   unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(pt.w) + m.c * 8), w);
   load_fractions(p.inv_freq, p.rot / 2, sm.frac);
@@ -560,18 +786,25 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
   int token = -1;
   TurnBack<IL> back;
   uint32_t k = 0;
-  for (; at.t < p.tokens; ++k) {
+  for (; at.t < items; ++k) {
     const int pos = pos_n;
     RopeWalk nx = at;
     nx.next(pt.cpt, pt.spt, pt.steps, dt, dc);
-    if (nx.t < p.tokens) pos_n = p.positions[nx.t];
-    if (at.t != token) {
-      token = at.t;
-      cos_sin<D>(p.rot, pos, sm.frac, sm.table);
-      back.set(sm.table, m);
+    if (FEW || nx.t < items) pos_n = position(nx.t);
+    int h0 = 0, nh;  // first head and number of rows
+    if constexpr (FEW) {
+      token = at.t * tg;
+      nh = tokens_of(at.t) * pt.H;
+      cos_sin_group(p, tokens_of(at.t), pos, sm.frac, sm.table);
+    } else {
+      if (at.t != token) {
+        token = at.t;
+        cos_sin<D>(p.rot, pos, sm.frac, sm.table);
+        back.set(sm.table, p.rot / 2, m);
+      }
+      h0 = at.s * C::HEADS;
+      nh = pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS;
     }
-    const int h0 = at.s * C::HEADS;
-    const int nh = pt.H - h0 < C::HEADS ? pt.H - h0 : C::HEADS;
     T* dst = static_cast<T*>(pt.y) + ((long long)token * pt.H + h0 + m.sub) * D;
     const uint8_t* x = sm.ring + (k % C::STAGES) * rp::STAGE_BYTES + m.sub * D * 2;
     if (!mbar_wait<true>(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, sm.abort_flag,
@@ -582,6 +815,13 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
       // (A lane past the last head works on what its ring holds, and its
       // terms are left out of the weights' sums.)
       const bool real = u * C::HPW + m.sub < nh;
+      TurnBack<IL> own;
+      if constexpr (FEW) {
+        int t = (u * C::HPW + m.sub) * pt.inv_h >> 16;
+        t = t < C::TOKENS ? t : 0;  // (of a lane past the last head: any)
+        own.set(sm.table + t * p.rot, p.rot / 2, m);
+      }
+      const TurnBack<IL>& by = FEW ? own : back;
       const uint8_t* xu = x + u * C::HPW * D * 2;
       const uint8_t* gu = xu + rp::STAGE_BYTES / 2;
       float2 a[4], g[4], y[4];
@@ -591,7 +831,7 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, true>::BLOCKS_PER_SM)
       float2 s2 = both(0.f), d2 = both(0.f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g[e] = __ffma2_rn(g[e], back.c[e], __fmul2_rn(IL ? swap2(g[e]) : y[e], back.s[e]));
+        g[e] = __ffma2_rn(g[e], by.c[e], __fmul2_rn(IL ? swap2(g[e]) : y[e], by.s[e]));
         y[e] = __fmul2_rn(g[e], a[e]);
         s2 = __ffma2_rn(a[e], a[e], s2);
         d2 = __ffma2_rn(y[e], w[e], d2);
@@ -670,15 +910,16 @@ __global__ void __launch_bounds__(kDwThreads)
 }
 
 // Steps per task: the fewest rounds of the resident warps, a round costing its
-// steps and, once, the token's cosines, sines and factors.  These count as a
-// quarter of a step: 4096 tokens of 128 + 8 + 8 heads into pages take 52 us so,
-// 55 us when they count as a half or as a sixteenth.
-static void plan_tasks(int tokens, int steps, long long warps, int* spt, int* cpt) {
+// steps and, once, the token's cosines, sines and factors.  These count as an
+// eighth of a step (forward: 8192 tokens of 32 + 8 heads 30.5 us so, 31.5 us as a
+// quarter; 8192 of 128 + 8 heads 97.9 us, 100.9 us as a sixteenth) or a sixteenth
+// (gradient: 16384 tokens of 16 + 16 heads 65.5 us so, 69.0 us as an eighth).
+static void plan_tasks(int tokens, int steps, long long warps, int weight, int* spt, int* cpt) {
   long long best = 0;
   for (int c = 1; c <= steps && c <= 64; ++c) {
     const int u = (steps + c - 1) / c;
     if ((steps + u - 1) / u != c) continue;
-    const long long cost = ((long long)tokens * c + warps - 1) / warps * (4 * u + 1);
+    const long long cost = ((long long)tokens * c + warps - 1) / warps * (weight * u + 1);
     if (best == 0 || cost < best) {
       best = cost;
       *spt = u;
@@ -687,31 +928,94 @@ static void plan_tasks(int tokens, int steps, long long warps, int* spt, int* cp
   }
 }
 
+// Blocks of the parts, in proportion to what a token of each costs, all of them
+// resident at once (left: what the parts before this one did not take).
+static int part_blocks(const RopeParams& p, int i, long long slots, const long long* cost,
+                       long long left) {
+  long long all = 0;
+  for (int k = 0; k < p.n_parts; ++k) all += cost[k];
+  long long nb = i + 1 < p.n_parts ? (slots * cost[i] + all / 2) / all : left;
+  if (nb > left - (p.n_parts - 1 - i)) nb = left - (p.n_parts - 1 - i);
+  return (int)(nb < 1 ? 1 : nb);
+}
+
+// Steps of several tokens, where each part's step has room for a second token and
+// there are tokens enough for more than one.  A part's step holds as many tokens
+// as take the fewest rounds of its warps, a round costing its head groups and
+// about two more.  Returns the grid size, or 0.
+// (D = 64, 50640 tokens of 4 + 2 heads: 19.8 us, a token per step 50.5; 16384 of
+// 16 + 16: 24.8 and 28.5; without room, 16384 of 32 + 4: 32.7 and 31.8, and D = 128,
+// 16384 of 16 + 4: 35.5 and 32.2.  Into pages, 4096 of 8 + 2 + 2: D = 64 7.0 and
+// 9.5, D = 128 11.7 and 10.9.  Gradient: 33841 of 8 + 4 heads 35.0 and 40.9;
+// without room, D = 128, 32768 of 8 + 2: 73.3 and 60.4.)
+static int plan_few(RopeParams* p, int D, bool bwd, long long slots) {
+  const int heads = (bwd ? rp::Cfg<128, true>::HEADS : rp::Cfg<128, false>::HEADS) * 128 / D;
+  const int hpw = heads / rp::Cfg<128, false>::UNITS, most = 384 / D;
+  long long cost[3] = {0, 0, 0};
+  for (int i = 0; i < p->n_parts; ++i) {
+    const int H = p->part[i].H;
+    if (2 * H > heads) return 0;
+    const int tg = heads / H < most ? heads / H : most;
+    const int unit = p->part[i].w ? 5 : 2;  // (values are only copied)
+    cost[i] = 1024ll * (unit * ((tg * H + hpw - 1) / hpw) + 10) / tg;
+  }
+  long long left = slots;
+  int b0 = 0;
+  bool several = false;
+  for (int i = 0; i < p->n_parts; ++i) {
+    RopePart& t = p->part[i];
+    long long nb = part_blocks(*p, i, slots, cost, left);
+    left -= nb;
+    long long best = 0;
+    for (int tg = 1; tg <= most && tg * t.H <= heads; ++tg) {
+      const long long groups = ((long long)p->tokens + tg - 1) / tg, warps = nb * rp::WARPS;
+      const long long c = (groups + warps - 1) / warps * ((tg * t.H + hpw - 1) / hpw + 2);
+      if (best == 0 || c < best) {
+        best = c;
+        t.tg = tg;
+      }
+    }
+    several |= t.tg > 1;
+    const long long need =
+        (((long long)p->tokens + t.tg - 1) / t.tg + rp::WARPS - 1) / rp::WARPS;
+    if (nb > need) nb = need;
+    t.inv_h = 65536 / t.H + 1;
+    t.steps = t.spt = t.cpt = 1;
+    t.b0 = b0;
+    t.nb = (int)nb;
+    b0 += t.nb;
+  }
+  p->inv_half = 65536 / (p->rot / 2) + 1;
+  return several ? b0 : 0;
+}
+
 // Steps, tasks and blocks.  Returns the grid size.
-static int plan_parts(RopeParams* p, int D, bool bwd) {
-  const int heads = bwd ? rp::Cfg<128, true>::HEADS * 128 / D : rp::Cfg<128, false>::HEADS * 128 / D;
+static int plan_parts(RopeParams* p, int D, bool bwd, bool* few) {
+  const int heads = (bwd ? rp::Cfg<128, true>::HEADS : rp::Cfg<128, false>::HEADS) * 128 / D;
+  const int hpw = heads / rp::Cfg<128, false>::UNITS;
   const int sms = sm_count() > 0 ? sm_count() : 148;
   const long long slots =  // resident blocks
-      (long long)sms * (bwd ? rp::Cfg<128, true>::BLOCKS_PER_SM : rp::Cfg<128, false>::BLOCKS_PER_SM);
-  long long steps = 0, all_heads = 0;
+      (long long)sms *
+      (bwd ? rp::Cfg<128, true>::BLOCKS_PER_SM : rp::Cfg<128, false>::BLOCKS_PER_SM);
+  const int blocks = plan_few(p, D, bwd, slots);
+  *few = blocks > 0;
+  if (*few) return blocks;
+  long long steps = 0, cost[3];
   for (int i = 0; i < p->n_parts; ++i) {
     RopePart& t = p->part[i];
     t.steps = (t.H + heads - 1) / heads;
     t.first = (int)steps;
     steps += t.steps;
-    all_heads += t.H;
+    cost[i] = 3 * ((t.H + hpw - 1) / hpw) + 4 * t.steps;  // head groups, and each step's start
   }
   if (bwd) {
-    // Blocks in proportion to the parts' heads, all resident at once.
     long long left = slots;
     int b0 = 0;
     for (int i = 0; i < p->n_parts; ++i) {
       RopePart& t = p->part[i];
-      long long nb = i + 1 < p->n_parts ? (slots * t.H + all_heads / 2) / all_heads : left;
-      if (nb > left - (p->n_parts - 1 - i)) nb = left - (p->n_parts - 1 - i);
-      if (nb < 1) nb = 1;
+      long long nb = part_blocks(*p, i, slots, cost, left);
       left -= nb;
-      plan_tasks(p->tokens, t.steps, nb * rp::WARPS, &t.spt, &t.cpt);
+      plan_tasks(p->tokens, t.steps, nb * rp::WARPS, 16, &t.spt, &t.cpt);
       const long long need = ((long long)p->tokens * t.cpt + rp::WARPS - 1) / rp::WARPS;
       if (nb > need) nb = need;
       t.b0 = b0;
@@ -721,7 +1025,7 @@ static int plan_parts(RopeParams* p, int D, bool bwd) {
     return b0;
   }
   p->steps = (int)steps;
-  plan_tasks(p->tokens, p->steps, slots * rp::WARPS, &p->spt, &p->cpt);
+  plan_tasks(p->tokens, p->steps, slots * rp::WARPS, 8, &p->spt, &p->cpt);
   const long long need = ((long long)p->tokens * p->cpt + rp::WARPS - 1) / rp::WARPS;
   return (int)(need < slots ? need : slots);
 }
@@ -744,36 +1048,42 @@ static cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, i
 
 // kind: 0 contiguous outputs, 1 pages, 2 gradient.
 template <int D, typename T>
-static int launch_rope_t(const RopeParams& p, int blocks, int kind, bool il, cudaStream_t s) {
-  void (*const kernels[6])(RopeParams) = {
-      rope_kernel<D, T, false, false>, rope_kernel<D, T, true, false>,
-      rope_kernel<D, T, false, true>,  rope_kernel<D, T, true, true>,
-      rope_bwd_kernel<D, T, false>,    rope_bwd_kernel<D, T, true>};
+static int launch_rope_t(const RopeParams& p, int blocks, int kind, bool il, bool few,
+                         cudaStream_t s) {
+  void (*const kernels[12])(RopeParams) = {
+      rope_kernel<D, T, false, false>,     rope_kernel<D, T, true, false>,
+      rope_kernel<D, T, false, true>,      rope_kernel<D, T, true, true>,
+      rope_bwd_kernel<D, T, false, false>, rope_bwd_kernel<D, T, true, false>,
+      rope_few_kernel<D, T, false, false>, rope_few_kernel<D, T, true, false>,
+      rope_few_kernel<D, T, false, true>,  rope_few_kernel<D, T, true, true>,
+      rope_bwd_kernel<D, T, false, true>,  rope_bwd_kernel<D, T, true, true>};
   auto smem = [](int k) {
-    return k < 4 ? rp::Cfg<D, false>::SMEM_TOTAL : rp::Cfg<D, true>::SMEM_TOTAL;
+    return k < 4 ? rp::Cfg<D, false>::SMEM_TOTAL
+           : k < 6 ? rp::Cfg<D, true>::SMEM_TOTAL
+           : k < 10 ? rp::Cfg<D, false, true>::SMEM_TOTAL : rp::Cfg<D, true, true>::SMEM_TOTAL;
   };
   static int attr_set[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE)) {
-    for (int k = 0; k < 6; ++k) {
+    for (int k = 0; k < 12; ++k) {
       e = cudaFuncSetAttribute(kernels[k], cudaFuncAttributeMaxDynamicSharedMemorySize, smem(k));
       if (e != cudaSuccess) return e;
     }
     if (dev >= 0 && dev < 64) __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
   }
-  const int k = 2 * kind + (il ? 1 : 0);
+  const int k = 6 * (few ? 1 : 0) + 2 * kind + (il ? 1 : 0);
   return launch_pdl(kernels[k], dim3(blocks), rp::THREADS, smem(k), s, p);
 }
 
 static int launch_rope(const RopeParams& p, int blocks, int D, bool bf16, int kind, bool il,
-                       cudaStream_t s) {
+                       bool few, cudaStream_t s) {
   if (D == 64)
-    return bf16 ? launch_rope_t<64, __nv_bfloat16>(p, blocks, kind, il, s)
-                : launch_rope_t<64, __half>(p, blocks, kind, il, s);
-  return bf16 ? launch_rope_t<128, __nv_bfloat16>(p, blocks, kind, il, s)
-              : launch_rope_t<128, __half>(p, blocks, kind, il, s);
+    return bf16 ? launch_rope_t<64, __nv_bfloat16>(p, blocks, kind, il, few, s)
+                : launch_rope_t<64, __half>(p, blocks, kind, il, few, s);
+  return bf16 ? launch_rope_t<128, __nv_bfloat16>(p, blocks, kind, il, few, s)
+              : launch_rope_t<128, __half>(p, blocks, kind, il, few, s);
 }
 
 int set_rope_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
@@ -850,9 +1160,10 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
   p.tokens = (int)T;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D, false);
+  bool few;
+  const int blocks = fa::plan_parts(&p, D, false, &few);
   return fa::record_cuda_status(
-      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 0, interleaved != 0, stream),
+      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 0, interleaved != 0, few, stream),
       "norm and rotation launch");
 }
 
@@ -898,9 +1209,10 @@ extern "C" int fa_qk_norm_rope_append(const void* q, const void* k, const void* 
   p.tokens = B * N;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D, false);
+  bool few;
+  const int blocks = fa::plan_parts(&p, D, false, &few);
   return fa::record_cuda_status(
-      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 1, interleaved != 0, stream),
+      fa::launch_rope(p, blocks, D, dtype == FA_BF16, 1, interleaved != 0, few, stream),
       "norm, rotation and append launch");
 }
 
@@ -943,12 +1255,13 @@ extern "C" int fa_qk_norm_rope_backward(const void* dq_out, const void* dk_out, 
   p.tokens = (int)T;
   p.rot = rot_dim;
   p.eps = eps;
-  const int blocks = fa::plan_parts(&p, D, true);
+  bool few;
+  const int blocks = fa::plan_parts(&p, D, true, &few);
   void* scratch = nullptr;
   e = fa::scratch_alloc(&scratch, (size_t)blocks * D * sizeof(float), stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "norm and rotation gradient scratch");
   p.partial = static_cast<float*>(scratch);
-  int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, 2, interleaved != 0, stream);
+  int r = fa::launch_rope(p, blocks, D, dtype == FA_BF16, 2, interleaved != 0, few, stream);
   if (r == 0)
     r = fa::launch_pdl(fa::rope_dw_kernel, dim3(D / 32, 2), fa::kDwThreads, 0, stream,
                        (const float*)p.partial, D, iq >= 0 ? p.part[iq].b0 : 0,

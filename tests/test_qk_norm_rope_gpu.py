@@ -40,6 +40,14 @@ SHAPES = [
     (513, 3, 1, 64, 48, torch.bfloat16, True, True),
     (64, 9, 3, 128, 112, torch.float16, False, False),
     (5000, 2, 1, 128, 128, torch.bfloat16, True, False),
+    # Several tokens per step: more tokens than resident warps, few heads.
+    (9001, 4, 2, 64, 16, torch.float16, False, False),
+    (7003, 8, 3, 64, 64, torch.bfloat16, True, True),
+    (6001, 16, 1, 64, 48, torch.float16, False, True),
+    (5999, 1, 1, 64, 64, torch.bfloat16, False, True),
+    (4003, 8, 2, 128, 112, torch.bfloat16, False, True),
+    (5003, 5, 3, 128, 64, torch.float16, True, False),
+    (20011, 0, 2, 64, 32, torch.bfloat16, False, False),
 ]
 
 
@@ -169,6 +177,9 @@ def test_no_tokens(fa):
     (4, 5, 6, 3, 64, 32, [5, 0, 100, 4], torch.float16, True, True),
     (3, 64, 16, 1, 128, 96, [64, 300, 97], torch.bfloat16, False, True),
     (20, 2, 4, 4, 64, 32, [2 + 31 * i for i in range(20)], torch.bfloat16, False, False),
+    # Several tokens per step, some of one sequence and some of the next.
+    (71, 43, 6, 3, 64, 32, [43 + 5 * i if i % 7 else i for i in range(71)], torch.float16, True, False),
+    (70, 37, 8, 1, 128, 64, [37 + 3 * i if i % 9 else 0 for i in range(70)], torch.bfloat16, False, True),
 ])
 def test_append(fa, B, N, Hq, Hkv, D, page, lens, dtype, il, own_pos):
     g = torch.Generator().manual_seed(B + N)
@@ -203,6 +214,22 @@ def test_append(fa, B, N, Hq, Hkv, D, page, lens, dtype, il, own_pos):
             assert torch.equal(vp[pid, t % page], v[b, s].cpu())
             kp[pid, t % page], vp[pid, t % page] = kp0[pid, t % page], vp0[pid, t % page]
     assert torch.equal(kp, kp0) and torch.equal(vp, vp0)  # nothing else was written
+
+
+@pytest.mark.parametrize("H,T", [(4, 9000), (16, 30000)])
+def test_rows_at_the_ends_of_their_memory(fa, H, T):
+    """Loads of several tokens per step stay in the rows: q is the end of a tensor
+    whose other rows are NaN, and the outputs are the same as alone."""
+    g = torch.Generator().manual_seed(T)
+    q, k = heads(T, H, 1, 64, torch.bfloat16, g, False)
+    qw, kw = (w.cuda() for w in weights(64, torch.bfloat16, g))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f = freqs(64).cuda()
+    ref = fa.qk_norm_rope(q, k, qw, kw, f, pos, EPS)
+    big = torch.full((T + 7, H + 3, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    big[7:, 3:] = q
+    got = fa.qk_norm_rope(big[7:, 3:], k, qw, kw, f, pos, EPS)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
 def test_append_with_bad_pages_and_lengths(fa):
