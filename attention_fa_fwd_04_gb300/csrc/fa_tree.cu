@@ -660,9 +660,9 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           // bad pages) can hold anything: they are cleared, since 0 * NaN in
           // P V would reach every row.
           const Mask128 any = tile_mask(base - kv0, used), fine = sound_keys(bad, p.box);
-          // This warp's 32 rows, two at a time, a row by D/8 lanes.
+          // This warp's 32 rows, a row by D/8 lanes.
           const uint64_t keep64 = wq < 2 ? any.lo & fine.lo : any.hi & fine.hi;
-          uint32_t clear = ~(uint32_t)(wq & 1 ? keep64 >> 32 : keep64);
+          const uint32_t clear = ~(uint32_t)(wq & 1 ? keep64 >> 32 : keep64);
           const uint32_t cv = 2 * tc + 1;
           const uint32_t on = C::PAIRED && j + 1 < sg.n ? cv + 1 : cv;  // V's barrier
           if (!(ok = mbar_wait<false>(&full[on % NSTAGE], (on / NSTAGE) & 1, abort_flag,
@@ -671,13 +671,11 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           const int x = lane % (D / 8);
           uint8_t* const vt = sKV + (cv % NSTAGE) * C::TILE_BYTES + (x >> 3) * tr::HALF_BYTES +
                               wq * 32 * 128 + (x & 7) * 16;
-          while (clear) {
-            const int ra = __ffs(clear) - 1;
-            clear &= clear - 1;
-            const int rb = clear ? __ffs(clear) - 1 : ra;
-            clear &= clear - 1;
-            *reinterpret_cast<uint4*>(vt + (lane / (D / 8) & 1 ? rb : ra) * 128) =
-                make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 256 / D) {
+            const int r = r0 + lane / (D / 8);
+            if (clear >> r & 1)
+              *reinterpret_cast<uint4*>(vt + r * 128) = make_uint4(0u, 0u, 0u, 0u);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -726,6 +724,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
             for (int q = 0; q < 4; ++q) {
               const uint64_t m64 = q < 2 ? mine.lo & fine.lo : mine.hi & fine.hi;
               const uint32_t see = (uint32_t)(q & 1 ? m64 >> 32 : m64);
+              if (__all_sync(0xffffffffu, see == ~0u)) continue;  // keys before the tree
 #pragma unroll
               for (int x = 0; x < 32; ++x)
                 if (!(see >> x & 1)) sr[q][x] = __float_as_uint(hide);
@@ -1020,8 +1019,11 @@ struct TreePlan {
 };
 static TreePlan tree_host_plan(int B, int N, int Hq, int Hkv, long long cap, int D) {
   TreePlan t;
-  const int rows = N * (Hq / Hkv);
-  t.mt = rows <= tr::BM ? 1 : 2;
+  // One row tile per CTA up to 128 rows, and where two would leave the last CTA of
+  // a few half empty (D = 128, 336 rows: 68.5 us, with two 74.0; 600 rows 75.6 and
+  // 80.0); else two (192 rows: 73.3 us, with one 82.3; 512 rows 68.2 and 75.3).
+  const int rows = N * (Hq / Hkv), tiles = (rows + tr::BM - 1) / tr::BM;
+  t.mt = tiles <= 5 && tiles % 2 == 1 ? 1 : 2;
   const int rt = t.mt * tr::BM;
   t.n_rt = (rows + rt - 1) / rt;
   t.rt_rows = rows < rt ? rows : rt;
