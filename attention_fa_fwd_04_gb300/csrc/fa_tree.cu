@@ -16,17 +16,18 @@
 // 128-key tiles of the paged cache (S = Q K^T and O += P V, both accumulated in
 // tensor memory, P written back over S as PV's operand).
 //   CTA = MT warpgroups of softmax (one 128-row tile each), one TMA producer
-//   warp, one MMA warp.  MT = 1 (up to 128 rows per kv head): S is
+//   warp, one MMA warp.  MT = 1 (one, three or five row tiles): S is
 //   double-buffered, so S of the next tile runs under this tile's softmax.
 //   MT = 2: two row tiles share every K/V tile, one's MMAs under the other's
 //   softmax.
 // Split: lengths are device data.  All K/V tiles of all (sequence, kv head)
-// units form one list, cut into equal ranges, one per group of n_rt CTAs (one
+// units, with a few places after each for what a stretch costs beside its tiles,
+// form one list, cut into equal ranges, one per group of n_rt CTAs (one
 // CTA per row tile, side by side, so that they share K/V through L2).  A range
 // may end inside a unit; its part of that unit goes to fp32 partials (O, max,
 // sum) that a second kernel merges.  A unit inside one range is finished in
-// place.  So every SM streams the same number of tiles whatever the lengths,
-// and a CTA writes at most two partials.
+// place.  So every SM is busy for about the same time whatever the lengths, and a
+// CTA writes at most two partials.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -86,7 +87,7 @@ struct TreeParams {
   const int32_t* parents;  // [B, N]
   float* part_o;           // [CTAs][2][D / 4][rt_rows][4] unnormalised partial outputs
   float* part_ml;          // [CTAs][2][rt_rows][2] (max in log2 units, sum)
-  long long* start;        // [B + 1] first tile of each sequence in the list
+  long long* start;        // [B + 1] place of each sequence in the list, then the slack
   int B, N, Hq, Hkv, G, rows, rt_rows, n_rt, groups;
   int page_size, max_pages, num_pages, box;
   float c;  // scale * log2(e)
@@ -112,17 +113,28 @@ __device__ __forceinline__ int div_small(long long a, int c) {
   return a >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)c) : (int)(a / c);
 }
 
-// A CTA's place in the tile list.
+// The list: the tiles of every unit (sequence, kv head), each unit's followed by
+// `slack` places without a tile.  A stretch costs about that many tiles beside its
+// own (Q, masks, the masked last tile, the epilogue), so equal shares of the list
+// take about equal times: 16 sequences of up to 16384 tokens, 256 rows per kv head
+// 132.8 us, without slack 140.4, with 2 places 138.1, with 8 135.8; 48 of up to
+// 931, 2 rows 34.4, 39.1, 35.5 and 35.1.  Where there is no more than a tile per
+// group there is no slack.
+constexpr int kSlack = 4;
+
+// A CTA's place in the list.
 struct TreeWalk {
-  long long x, hi;  // next and last tile of the range
-  long long first;  // first tile of sequence b
+  long long x, hi;  // next and last place of the range
+  long long first;  // first place of sequence b
   int b, T;         // sequence and its tiles per kv head
+  int slack;
+  __device__ __forceinline__ int places() const { return T > 0 ? T + slack : 0; }
 };
 struct TreeSeg {
   int b, hkv, t0, n, T, L;
 };
 
-// Groups in use: every one of them has a tile (a group without one between two
+// Groups in use: every one of them has a place (a group without one between two
 // of a unit's would leave the merge a partial that nobody wrote).
 __device__ __forceinline__ long long tree_groups(const TreeParams& p, long long total) {
   return total < p.groups ? total : p.groups;
@@ -135,13 +147,16 @@ __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
   w.first = 0;
   w.b = 0;
   w.T = 0;
-  auto range = [&](long long total) {
+  // tiles: per kv head, of the n sequences that have any.
+  auto range = [&](long long tiles, int n) {
+    w.slack = tiles * p.Hkv > p.groups ? kSlack : 0;
+    const long long total = (tiles + (long long)n * w.slack) * p.Hkv;
     const long long G = tree_groups(p, total);
     w.x = g < G ? mul_div(total, g, G) : 0;
     w.hi = g < G ? mul_div(total, g + 1, G) : 0;
     return w.x < w.hi;
   };
-  // The sequence of lane l (tiles T, inclusive sum inc on top of `before`) is
+  // The sequence of lane l (tiles T, inclusive places inc on top of `before`) is
   // the first that ends past the range's start.
   auto find = [&](int b0, int T, long long inc, long long before) {
     const uint32_t past = __ballot_sync(0xffffffffu, w.x < (before + inc) * p.Hkv);
@@ -149,30 +164,41 @@ __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
     const int l = __ffs(past) - 1;
     w.b = b0 + l;
     w.T = __shfl_sync(0xffffffffu, T, l);
-    w.first = (before + __shfl_sync(0xffffffffu, inc, l) - w.T) * p.Hkv;
+    w.first = (before + __shfl_sync(0xffffffffu, inc, l) - w.places()) * p.Hkv;
     return true;
   };
+  const uint32_t upto = 0xffffffffu >> (31 - lane);  // lanes up to this one
   if (p.B <= 32) {  // one load, 32-bit sums (a sequence has at most 2^24 tiles)
     const int T = lane < p.B ? tree_tiles(p, lane) : 0;
+    const uint32_t some = __ballot_sync(0xffffffffu, T > 0);
     int inc = T;
     for (int o = 1; o < p.B; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (range((long long)__shfl_sync(0xffffffffu, inc, p.B - 1) * p.Hkv)) find(0, T, inc, 0);
+    if (range(__shfl_sync(0xffffffffu, inc, p.B - 1), __popc(some)))
+      find(0, T, inc + w.slack * __popc(some & upto), 0);
     return w;
   }
   long long sum = 0;
+  int n = 0;
 #pragma unroll 4
-  for (int b = lane; b < p.B; b += 32) sum += tree_tiles(p, b);
+  for (int b = lane; b < p.B; b += 32) {
+    const int T = tree_tiles(p, b);
+    sum += T;
+    n += T > 0;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (!range(sum * p.Hkv)) return w;
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (!range(sum, n)) return w;
   long long before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
     const int T = b < p.B ? tree_tiles(p, b) : 0;
-    long long inc = T;
+    long long inc = T > 0 ? T + w.slack : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -186,16 +212,20 @@ __device__ TreeWalk tree_plan(const TreeParams& p, int g) {
 
 // The next stretch of one unit's tiles in the range.
 __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, TreeSeg* s) {
-  if (w.x >= w.hi) return false;
-  while (w.x >= w.first + (long long)w.T * p.Hkv) {
-    w.first += (long long)w.T * p.Hkv;
-    if (++w.b >= p.B) return false;  // (the range ends at the list's end)
-    w.T = tree_tiles(p, w.b);
+  for (;;) {
+    if (w.x >= w.hi) return false;
+    while (w.x >= w.first + (long long)w.places() * p.Hkv) {
+      w.first += (long long)w.places() * p.Hkv;
+      if (++w.b >= p.B) return false;  // (the range ends at the list's end)
+      w.T = tree_tiles(p, w.b);
+    }
+    const long long off = w.x - w.first;
+    s->hkv = div_small(off, w.places());
+    s->t0 = (int)(off - (long long)s->hkv * w.places());
+    if (s->t0 < w.T) break;
+    w.x += w.places() - s->t0;  // slack
   }
-  const long long off = w.x - w.first;
   s->b = w.b;
-  s->hkv = div_small(off, w.T);
-  s->t0 = (int)(off - (long long)s->hkv * w.T);
   s->T = w.T;
   s->L = tree_len(p, w.b);
   const long long left = w.hi - w.x;
@@ -471,8 +501,8 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
     if (blockIdx.x == 0) {
       long long before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long Tb = b0 + lane < p.B ? (long long)tree_tiles(p, b0 + lane) * p.Hkv : 0;
-        long long inc = Tb;
+        const int T = b0 + lane < p.B ? tree_tiles(p, b0 + lane) : 0;
+        long long inc = T > 0 ? (long long)(T + w.slack) * p.Hkv : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -485,7 +515,10 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
       }
-      if (lane == 0) p.start[0] = 0;
+      if (lane == 0) {
+        p.start[0] = 0;
+        p.start[p.B + 1] = w.slack;
+      }
     }
    } else if (warp == W_MMA) {
     // ============================ MMA issuer (lane 0) ============================
@@ -904,11 +937,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
   const long long first = p.start[b], after = p.start[b + 1], total = p.start[p.B];
-  const int T_b = div_small(after - first, p.Hkv);
+  const int places = div_small(after - first, p.Hkv);
   int g0 = 0, g1 = -1;  // groups of the unit's tiles
-  if (T_b > 0) {
-    const long long u0 = first + (long long)hkv * T_b, u1 = u0 + T_b - 1;
-    // Group of tile t: the largest g with total * g / G <= t.
+  if (places > 0) {
+    const long long u0 = first + (long long)hkv * places;
+    const long long u1 = u0 + places - p.start[p.B + 1] - 1;
+    // Group of place t: the largest g with total * g / G <= t.
     const long long G = tree_groups(p, total);
     g0 = (int)((u0 + 1) * G > 0xffffffffll ? ((u0 + 1) * G - 1) / total
                                            : (uint32_t)((u0 + 1) * G - 1) / (uint32_t)total);
@@ -1036,7 +1070,7 @@ static TreePlan tree_host_plan(int B, int N, int Hq, int Hkv, long long cap, int
   const size_t slots = (size_t)t.groups * t.n_rt * 2 * t.rt_rows;
   t.o_floats = slots * D;
   t.ml_floats = slots * 2;
-  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 5) * sizeof(long long);
+  t.bytes = (t.o_floats + t.ml_floats) * sizeof(float) + ((size_t)B + 6) * sizeof(long long);
   return t;
 }
 
@@ -1186,9 +1220,9 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   cudaError_t e = fa::scratch_alloc(&scratch, t.bytes, stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "tree decode scratch");
   p.start = static_cast<long long*>(scratch);
-  // (B + 1) 8-byte entries, then the partials 32-byte aligned.
+  // (B + 2) 8-byte entries, then the partials 32-byte aligned.
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
-                                      (((size_t)B + 1) * 8 + 31) / 32 * 32);
+                                      (((size_t)B + 2) * 8 + 31) / 32 * 32);
   p.part_ml = p.part_o + t.o_floats;
   int r;
   const bool bf16 = dtype == FA_BF16;

@@ -63,7 +63,9 @@ def check(fa, t, scale, status=None):
     (2, 16, 8, 1, 64, 64, [128, 300], torch.float16),        # 128 rows: one full row tile
     (1, 43, 3, 1, 128, 128, [515], torch.bfloat16),          # 129 rows: a second tile of one row
     (2, 64, 4, 1, 128, 32, [64, 700], torch.bfloat16),       # 256 rows; a tree without a prompt
-    (1, 64, 5, 1, 64, 256, [257], torch.float16),            # 320 rows: two CTAs per unit
+    (1, 64, 5, 1, 64, 256, [257], torch.float16),            # 320 rows: three CTAs per unit
+    (1, 56, 16, 1, 128, 64, [700], torch.bfloat16),          # 896 rows: four CTAs, half of the last
+    (2, 61, 27, 3, 64, 64, [400, 61], torch.float16),        # 549 rows: five CTAs, one row tile each
     (3, 5, 16, 16, 64, 32, [5, 260, 131], torch.bfloat16),   # MHA
     (1, 64, 16, 1, 128, 64, [900], torch.bfloat16),          # 1024 rows, MQA
     (2, 33, 4, 4, 128, 128, [161, 1100], torch.float16),
@@ -80,6 +82,19 @@ def test_ragged_batches_with_padding(fa, B, Hq, Hkv):
     rng = random.Random(B)
     lens = [rng.choice([0, 3, 6, 7, 64, 127, 128, 129, rng.randint(7, 400)]) for _ in range(B)]
     check(fa, inputs(B, 6, Hq, Hkv, 64, 32, lens, torch.bfloat16, seed=B), 0.125)
+
+
+@pytest.mark.parametrize("seed", range(5))
+def test_shares_that_end_anywhere(fa, seed):
+    """Short and long sequences side by side: shares of the list that begin and
+    end in the middle of units, between them, and in none."""
+    rng = random.Random(100 + seed)
+    B, N, Hkv = rng.choice([7, 31, 33, 60]), rng.randint(1, 5), rng.choice([1, 2, 5])
+    Hq = Hkv * rng.choice([1, 3, 60])
+    if Hq > 60:
+        B = 7
+    lens = [rng.choice([0, N, 128, 129, 500, rng.randint(N, 700), rng.randint(N, 2600)]) for _ in range(B)]
+    check(fa, inputs(B, N, Hq, Hkv, 64, 64, lens, torch.bfloat16, seed=seed), 0.125)
 
 
 def test_every_sequence_is_padding(fa):
