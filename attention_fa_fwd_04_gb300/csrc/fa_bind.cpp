@@ -5,8 +5,7 @@
 //
 // Why native: these calls last 2 to 20 us on the GPU, and a decoding step makes
 // them one after another, so the host's time per call is what the caller waits
-// for.  The same checks in Python, through ctypes, took 12 to 28 us per call on
-// the machine's host cores.
+// for.  The same checks in Python, through ctypes, took 12 to 28 us per call.
 //
 // The library's entry points are handed over as addresses (bind), so that this
 // module and the ctypes binding use the one loaded copy.
