@@ -84,15 +84,16 @@ def test_layers_past_2_31_elements(fa):
             assert (pool[layer, 29, 62] == 3 * sign).all() and (pool[layer, 29, 63] == 4 * sign).all()
 
 
-def test_heads_past_2_31_elements(fa):
-    """The last of 135000 tokens of 128 + 8 heads, forward and gradient."""
-    T, Hq, Hkv, D = 135000, 128, 8, 128
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(135000, 128, 8, 128), (8500001, 4, 2, 64)])
+def test_heads_past_2_31_elements(fa, T, Hq, Hkv, D):
+    """The last tokens, forward and gradient: a token in several steps, and
+    several tokens in one."""
     assert T * Hq * D > 2 ** 31
     g = torch.Generator(device="cuda").manual_seed(3)
     qkv = torch.empty(T, Hq + Hkv, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
     q, k = qkv[:, :Hq], qkv[:, Hq:]
     w = torch.empty(D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
-    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    f = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).float()
     pos = torch.arange(T, dtype=torch.int32, device="cuda")
     qo, ko = fa.qk_norm_rope(q, k, w, w, f.cuda(), pos, 1e-6)
     at = [0, 65535, 131071, 131072, T - 1]
