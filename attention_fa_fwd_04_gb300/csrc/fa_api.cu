@@ -382,7 +382,6 @@ extern "C" int fa_set_wait_limit_ns(unsigned long long ns) {
   if (r == 0) r = fa::set_backward_wait_limit(ns);
   if (r == 0) r = fa::set_tree_wait_limit(ns);
   if (r == 0) r = fa::set_rope_wait_limit(ns);
-  if (r == 0) r = fa::set_verify_wait_limit(ns);
   return cuda_status(r, "wait limit set");
 }
 

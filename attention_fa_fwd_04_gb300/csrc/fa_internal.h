@@ -88,7 +88,6 @@ int set_decode_wait_limit(unsigned long long ns);
 int set_backward_wait_limit(unsigned long long ns);
 int set_tree_wait_limit(unsigned long long ns);
 int set_rope_wait_limit(unsigned long long ns);
-int set_verify_wait_limit(unsigned long long ns);
 
 // Stream-ordered scratch (free it with cudaFreeAsync on the stream) from a pool
 // of this library's that keeps up to 256 MiB of freed memory per device: the

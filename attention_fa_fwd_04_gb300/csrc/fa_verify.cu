@@ -23,20 +23,15 @@
 // nodes where more than one child is tried), once from HBM and for further
 // rejected siblings from L2; in fact the latency of the passes over a row that
 // the sequence with the most rejections needs one after another: 64 trees of 32
-// nodes over 128000 tokens take 41.3 us (1.6 TB/s of the rows where they stop;
-// at most five passes of about 10000 clocks: the loads' latency 1400, 7 further
-// stages 1000 or less each, the sums 1300, the walk 800 to 1900), one chain of 5
-// over 32000 tokens 5.9 us.  The tests themselves
+// nodes over 128000 tokens take 34.5 us (1.9 TB/s of the rows where they stop; at
+// most five passes of 6000 to 8000 clocks: the first loads' latency 1000, the
+// walk 800 to 1900, the sums' meeting 900), one chain of 5 over 32000 tokens 5.2 us.
+// The tests themselves
 // read single elements: those of all nodes are fetched at once, and the walk
 // runs on shared memory, in one warp of each CTA.  A cluster of up to 8 CTAs
 // takes one sequence: every CTA walks (the same way), and for a mass each sums
 // its part of the row and pushes its sum to the others, onto a barrier that
-// counts the sums (43.5 us with a cluster barrier after each pass, 1150 clocks).
-//
-// Tried without gain: 16-byte asynchronous copies by every lane in place of bulk
-// copies (43.2 against 43.4 us, without q 24.4 against 19.9), the row's first
-// stages fetched again before the sums meet (44.6 against 43.4: the next child is
-// often accepted, and its row is another).
+// counts the sums (2 us less than with a cluster barrier after each pass, 1150 clocks).
 #include <math.h>
 
 #include "fa.h"
@@ -51,12 +46,6 @@ namespace vf {
 constexpr int CLUSTER = 8;  // CTAs per sequence, at most
 constexpr int SM_WARPS = 32;  // resident per SM, as two blocks of 16 warps or four of 8
 constexpr int MAX_N = 64;
-// Each warp streams its part of a row through a ring of its own: 256 elements
-// of p and of q per stage.
-constexpr int STAGES = 3;
-constexpr int STAGE_ELEMS = 256;
-constexpr int RING_BYTES = STAGES * 2 * STAGE_ELEMS * 4;
-constexpr int smem(int warps) { return warps * (RING_BYTES + STAGES * 8); }
 }  // namespace vf
 
 struct VerifyParams {
@@ -266,99 +255,44 @@ __device__ __forceinline__ void gather(Pair2& acc, const Pair2 (&r)[2]) {
   }
 }
 
-// Sum of what is left in [va, vb) of a row, over the warp.  Rows that are not
-// aligned: plain loads, four per lane and 128 elements.
-template <bool DRAFT>
-__device__ __forceinline__ Pair sum_plain(const float* pr, const float* qr, int va, int vb,
+// Sum of what is left in [va, vb) of a row, over the warp, by loads into
+// registers, four tokens per lane and 128: 16 bytes at once where rows are aligned
+// (VEC).  LEVEL as in left4.  All loads of an iteration come before its sums: 512
+// tokens of p, or 256 of p and of q (64 trees of 32 nodes, 128000 tokens: 34.5 us,
+// half as many 43.5; a ring of bulk copies per warp, three iterations ahead, 42.8:
+// a copy's latency is longer than a load's, and a pass is too short to hide it).
+template <bool DRAFT, bool VEC, int LEVEL>
+__device__ __forceinline__ Pair sum_loads(const float* pr, const float* qr, int va, int vb,
                                           const Rejected& rj) {
-  const bool use_q = DRAFT && rj.n > 0;
-  Pair2 acc{both(0.f), both(0.f)};
-#pragma unroll 2
-  for (int v = va + (threadIdx.x & 31); v < vb; v += 128) {
-    const float4 a = clean4(load4<false, 32>(pr, v, vb));
-    const float4 d = use_q ? clean4(load4<false, 32>(qr, v, vb)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    Pair2 r[2];
-    left4<DRAFT, 32, 2>(a, d, v, rj, r);
-    gather(acc, r);
-  }
-  return warp_sum(lane_sum(acc));
-}
-// Aligned rows: bulk copies into the warp's ring, STAGES ahead of the sums.
-struct Ring {
-  uint8_t* data;
-  uint64_t* full;
-  uint32_t n;  // stages used so far
-  volatile int* abort_flag;
-};
-template <bool DRAFT, int LEVEL>
-__device__ __forceinline__ Pair sum_ring(const float* pr, const float* qr, int va, int vb,
-                                         const Rejected& rj, Ring& ring) {
-  constexpr int E = vf::STAGE_ELEMS;
-  const int lane = threadIdx.x & 31;
   constexpr bool use_q = DRAFT && LEVEL > 0;
-  const int n = (vb - va + E - 1) / E;
-  auto fetch = [&](int i) {
-    if (i >= n || lane != 0) return;
-    const int v = va + i * E, st = (ring.n + i) % vf::STAGES;
-    const uint32_t bytes = (uint32_t)(vb - v < E ? vb - v : E) * 4;
-    uint8_t* to = ring.data + st * 2 * E * 4;
-    mbar_arrive_expect_tx(&ring.full[st], use_q ? 2 * bytes : bytes);
-    bulk_load(to, pr + v, bytes, &ring.full[st]);
-    if (use_q) bulk_load(to + E * 4, qr + v, bytes, &ring.full[st]);
-  };
-  // An accumulator per 128 elements of a stage: independent chains.
-  Pair2 acc[E / 128];
+  constexpr int ST = VEC ? 1 : 32;  // the lane's tokens: side by side, or every 32nd
+  constexpr int G = use_q ? 2 : 4;
+  Pair2 acc[2] = {{both(0.f), both(0.f)}, {both(0.f), both(0.f)}};
+  for (int v = va + (threadIdx.x & 31) * (VEC ? 4 : 1); v < vb; v += 128 * G) {
+    float4 a[G], d[G];
 #pragma unroll
-  for (int g = 0; g < E / 128; ++g) acc[g] = {both(0.f), both(0.f)};
-  for (int i = 0; i < vf::STAGES; ++i) fetch(i);
-  int i = 0;
-  for (; i < n; ++i) {
-    const uint32_t k = ring.n + i;
-    if (!mbar_wait<true>(&ring.full[k % vf::STAGES], (k / vf::STAGES) & 1, ring.abort_flag,
-                         &g_verify_err, 22))
-      break;
-    __syncwarp();
-    const float* at = reinterpret_cast<const float*>(ring.data + (k % vf::STAGES) * 2 * E * 4);
-    const int v = va + i * E + lane * 4;
-    float4 a[E / 128], d[E / 128];
+    for (int g = 0; g < G; ++g) {
+      a[g] = load4<VEC, ST>(pr, v + 128 * g, vb);
+      d[g] = use_q ? load4<VEC, ST>(qr, v + 128 * g, vb) : a[g];
+    }
     uint32_t top = 0;
 #pragma unroll
-    for (int g = 0; g < E / 128; ++g) {
-      a[g] = *reinterpret_cast<const float4*>(at + g * 128 + lane * 4);
-      // (Past the row's end the stage holds an earlier one's values.)
-      if (v + g * 128 >= vb) a[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-      top = max(top, bits4(a[g]));
-      d[g] = a[g];
-      if constexpr (use_q) {
-        d[g] = *reinterpret_cast<const float4*>(at + E + g * 128 + lane * 4);
-        if (v + g * 128 >= vb) d[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-        top = max(top, bits4(d[g]));
-      }
-    }
-    if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+    for (int g = 0; g < G; ++g) top = max(top, use_q ? max(bits4(a[g]), bits4(d[g])) : bits4(a[g]));
+    if (top >= 0x7f800000u) {
 #pragma unroll
-      for (int g = 0; g < E / 128; ++g) {
+      for (int g = 0; g < G; ++g) {
         a[g] = clean4(a[g]);
         d[g] = clean4(d[g]);
       }
     }
-    Pair2 r[E / 128][2];
 #pragma unroll
-    for (int g = 0; g < E / 128; ++g) left4<DRAFT, 1, LEVEL>(a[g], d[g], v + g * 128, rj, r[g]);
-#pragma unroll
-    for (int g = 0; g < E / 128; ++g) gather(acc[g], r[g]);
-    __syncwarp();  // the stage has been read
-    fetch(i + vf::STAGES);
+    for (int g = 0; g < G; ++g) {
+      Pair2 r[2];
+      left4<DRAFT, ST, LEVEL>(a[g], d[g], v + 128 * g, rj, r);
+      gather(acc[g & 1], r);
+    }
   }
-  // A wait that gave up: the loads in flight land before anything else.
-  for (int j = i; j < n && j < i + vf::STAGES; ++j)
-    mbar_wait_drain(&ring.full[(ring.n + j) % vf::STAGES], ((ring.n + j) / vf::STAGES) & 1);
-  __syncwarp();
-  ring.n += i < n ? (i + vf::STAGES < n ? i + vf::STAGES : n) : n;
-  Pair t = lane_sum(acc[0]);
-#pragma unroll
-  for (int g = 1; g < E / 128; ++g) t = add_loose(t, lane_sum(acc[g]));
-  return warp_sum(t);
+  return warp_sum(add_loose(lane_sum(acc[0]), lane_sum(acc[1])));
 }
 
 // Whole warp: inclusive sums of n <= 32 values, one per lane.
@@ -399,9 +333,7 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
   __shared__ uint64_t s_path;
   __shared__ uint32_t s_first[2];
   __shared__ Pair s_c;
-  __shared__ int s_abort;
   __shared__ uint64_t s_sums[2];  // counts the sums that arrive in s_cta
-  extern __shared__ __align__(16) uint8_t smem[];
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), CL = p.cluster;
@@ -416,17 +348,6 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
   const int b = blockIdx.x / CL;
   const int N = p.N, V = p.V;
   const size_t node0 = (size_t)b * N;
-  Ring ring{smem + warp * vf::RING_BYTES,
-            reinterpret_cast<uint64_t*>(smem + W * vf::RING_BYTES) + warp * vf::STAGES, 0,
-            &s_abort};
-  if constexpr (VEC) {
-    if (lane == 0) {
-      for (int i = 0; i < vf::STAGES; ++i) mbar_init(&ring.full[i], 1);
-      fence_mbar_init();
-    }
-    if (tid == 0) s_abort = 0;
-  }
-
   if (tid < N) {
     // Node tid: an edge that the walk may take, or parent -2.
     int par = tid == 0 ? -1 : p.parents[node0 + tid];
@@ -463,13 +384,9 @@ __global__ void __launch_bounds__(W * 32, vf::SM_WARPS / W)
     const int va = v0 < V ? (int)v0 : V, vb = v0 + p.part < V ? (int)(v0 + p.part) : V;
     const float* pr = p.p + (node0 + cur) * V;
     const float* qr = DRAFT ? p.q + (node0 + cur) * V : nullptr;
-    Pair s;
-    if constexpr (VEC)
-      s = rj.n == 0   ? sum_ring<DRAFT, 0>(pr, qr, va, vb, rj, ring)
-          : rj.n == 1 ? sum_ring<DRAFT, 1>(pr, qr, va, vb, rj, ring)
-                      : sum_ring<DRAFT, 2>(pr, qr, va, vb, rj, ring);
-    else
-      s = sum_plain<DRAFT>(pr, qr, va, vb, rj);
+    const Pair s = rj.n == 0   ? sum_loads<DRAFT, VEC, 0>(pr, qr, va, vb, rj)
+                   : rj.n == 1 ? sum_loads<DRAFT, VEC, 1>(pr, qr, va, vb, rj)
+                               : sum_loads<DRAFT, VEC, 2>(pr, qr, va, vb, rj);
     if (lane == 0) s_warp[warp] = s;
     __syncthreads();
     ++pass;
@@ -734,7 +651,7 @@ __global__ void __launch_bounds__(cp::THREADS)
 
 template <typename P>
 static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, cudaStream_t stream,
-                                    const P& p, int cluster = 0, int smem = 0) {
+                                    const P& p, int cluster = 0) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -745,14 +662,11 @@ static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
-
-int set_verify_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
 
 int read_verify_error(unsigned int* out, int reset) {
   unsigned int v = 0;
@@ -797,12 +711,12 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   p.N = N;
   p.V = V;
   // CTAs per sequence: 8, or as few of 8 warps as leave all of them resident at
-  // once (64 sequences of 128000 tokens: 8 CTAs 41.1 us, 4 61.2 us), or twice
-  // that where a warp's part would pass 1024 tokens (200 of 32000: 4 CTAs 21.2 us,
-  // 2 23.8 us); and no more than give each warp a stage of tokens.
-  // 16 warps where the SMs are not filled and a warp's part stays above 256
-  // tokens (16 sequences of 128000: 16 warps 21.2 us, 8 23.2 us; one of 32000: 16
-  // warps 6.3 us, 8 5.8 us).
+  // once (64 sequences of 128000 tokens: 8 CTAs 34.5 us, 4 51.8 us), or twice
+  // that where a warp's part would pass 1024 tokens (200 of 32000: 4 CTAs 19.7 us,
+  // 2 22.1 us of 16 warps); and no more than give each warp 256 tokens.
+  // 16 warps where the SMs are not filled and a warp's part stays above 512
+  // tokens (8 sequences of 152064: 16 warps 20.4 us, 8 21.1 us; 16 of 50256: 16
+  // warps 15.8 us, 8 14.5 us; one of 32000: 5.8 and 5.2 us).
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
   auto part_of = [&](int cluster, int warps) {
     const int n = cluster * warps;
@@ -810,12 +724,12 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
   };
   p.cluster = fa::vf::CLUSTER;
   while (p.cluster > 1 &&
-         (part_of(p.cluster / 2, 8) <= fa::vf::STAGE_ELEMS ||
+         (part_of(p.cluster / 2, 8) <= 256 ||
           (long long)B * p.cluster > 8ll * sms ||
           ((long long)B * p.cluster > 4ll * sms && part_of(p.cluster / 2, 8) <= 1024)))
     p.cluster /= 2;
   const int warps =
-      (long long)B * p.cluster <= sms && part_of(p.cluster, 16) > fa::vf::STAGE_ELEMS ? 16 : 8;
+      (long long)B * p.cluster <= sms && part_of(p.cluster, 16) > 512 ? 16 : 8;
   p.part = part_of(p.cluster, warps);
   const bool vec = V % 4 == 0 && al(target_probs, 16) && (!draft_probs || al(draft_probs, 16));
   const dim3 grid((unsigned)B * p.cluster);
@@ -824,25 +738,9 @@ extern "C" int fa_verify_tree(const float* target_probs, const float* draft_prob
        fa::verify_kernel<true, false, 8>, fa::verify_kernel<true, true, 8>},
       {fa::verify_kernel<false, false, 16>, fa::verify_kernel<false, true, 16>,
        fa::verify_kernel<true, false, 16>, fa::verify_kernel<true, true, 16>}};
-  cudaError_t e = cudaSuccess;
-  if (vec) {
-    static int attr_set[64] = {0};
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess &&
-        (dev < 0 || dev >= 64 || !__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE))) {
-      for (int i = 0; i < 2; ++i)
-        for (int k = 1; k < 4; k += 2)
-          if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernels[i][k], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     fa::vf::smem(8 << i));
-      if (e == cudaSuccess && dev >= 0 && dev < 64)
-        __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
-    }
-  }
-  if (e == cudaSuccess)
-    e = fa::launch_dependent(kernels[warps == 16][(draft_probs ? 2 : 0) + (vec ? 1 : 0)], grid, warps * 32,
-                             stream, p, p.cluster, vec ? fa::vf::smem(warps) : 0);
+  const cudaError_t e =
+      fa::launch_dependent(kernels[warps == 16][(draft_probs ? 2 : 0) + (vec ? 1 : 0)], grid,
+                           warps * 32, stream, p, p.cluster);
   return fa::record_cuda_status(e, "tree verification launch");
 }
 

@@ -575,9 +575,8 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
 
 /*
  * fa_set_wait_limit_ns -- time limit of every device-side pipeline wait
- * (mbarrier waits of the prefill, decode, backward, norm and rotation, tree decode and
- * verification kernels) on the current
- * device; ns == 0 restores the default of 2 s.
+ * (mbarrier waits of the prefill, decode, backward, norm and rotation and tree
+ * decode kernels) on the current device; ns == 0 restores the default of 2 s.
  *
  * A wait that runs past the limit makes its CTA abort: every warp leaves its
  * loop, the loads and MMAs already in flight are waited for (each such
@@ -587,8 +586,8 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
  * default is far above any wait of a healthy call; a short limit serves as a
  * watchdog, or in tests to make the timeout path run.
  *
- * Below 1 ms the limit is a watchdog: the decode, norm and rotation and verification
- * kernels, the tree decode's loads, and the dense
+ * Below 1 ms the limit is a watchdog: the decode kernels, the norm and rotation,
+ * the tree decode's loads, and the dense
  * prefill (whose launches then use a polling instantiation of the kernel),
  * check it at every probe of every wait.  The packed-sequence prefill and the
  * backward kernels keep suspending probes of about 4 us each, so there a wait
