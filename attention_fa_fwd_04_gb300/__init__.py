@@ -554,13 +554,18 @@ _native = None
 def _load_native():
     global _native
     lib = load()
-    import torch  # noqa: F401  (its libraries must be loaded first)
+    import torch  # (its libraries must be loaded first)
     try:
         from . import _fa_bind
     except ImportError as e:
         raise ImportError(
             f"{e}: build the binding with `python -c \"import __graft_entry__ as g; g.build()\"`"
         ) from e
+    built = getattr(_fa_bind, "torch_version", "of another version")
+    if built != str(torch.__version__):
+        raise ImportError(
+            f"the binding was built against torch {built}, this is {torch.__version__}: build it "
+            f"with `python -c \"import __graft_entry__ as g; g.build()\"`")
     _fa_bind.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_append, lib.fa_qk_norm_rope_backward,
         lib.fa_decode_tree_fwd, lib.fa_verify_tree, lib.fa_compact_tree)))

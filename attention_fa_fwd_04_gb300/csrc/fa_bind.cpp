@@ -487,4 +487,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_bind", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fa_bind() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fa_bind() {
+  PyObject* m = PyModule_Create(&module);
+  // The torch whose headers were compiled in: the package checks it on loading.
+  if (m && PyModule_AddStringConstant(m, "torch_version", FA_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
