@@ -1126,13 +1126,18 @@ static int launch_tree_d(const TreeParams& p, int mt, const CUtensorMap& tk, con
                  : launch_tree_t<D, T, 2>(p, tk, tv, stream);
 }
 
-// A cache without capacity: every row is a padding sequence's.
-__global__ void tree_zero_kernel(uint16_t* o, size_t n, float* lse, size_t nl) {
+// A cache without capacity: every row is a padding sequence's, and any token is
+// past the page table.
+__global__ void tree_zero_kernel(uint16_t* o, size_t n, float* lse, size_t nl,
+                                 const int32_t* seqlens, size_t B) {
   const size_t at = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
   const size_t step = (size_t)gridDim.x * blockDim.x;
   for (size_t i = at; i < n; i += step) o[i] = 0;
   if (lse)
     for (size_t i = at; i < nl; i += step) lse[i] = -INFINITY;
+  bool past = false;
+  for (size_t i = at; i < B; i += step) past |= seqlens[i] > 0;
+  if (past) atomicOr(&g_tree_err, kErrBounds);
 }
 
 int set_tree_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
@@ -1175,15 +1180,16 @@ extern "C" int fa_decode_tree_fwd(const void* q, const void* kpages, const void*
   if ((int64_t)max_pages * page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
   if (!al(q, 16) || !al(o, 16)) return FA_ERR_INVALID_ARG;
   if (lse && !al(lse, 4)) return FA_ERR_INVALID_ARG;
+  if (!al(seqlens, 4)) return FA_ERR_INVALID_ARG;
   if (max_pages > 0 && (num_pages < 1 || !al(kpages, 16) || !al(vpages, 16) ||
-                        !al(page_table, 4) || !al(seqlens, 4) || !al(parents, 4)))
+                        !al(page_table, 4) || !al(parents, 4)))
     return FA_ERR_INVALID_ARG;
   if ((int64_t)num_pages * page_size > (1ll << 40) / (2 * D) / Hkv) return FA_ERR_INVALID_ARG;
   const fa::SetupDuringCapture setup;
   if (max_pages == 0) {
     const size_t rows = (size_t)B * N * Hq, n = rows * D;
     fa::tree_zero_kernel<<<(unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096), 256, 0,
-                           stream>>>(static_cast<uint16_t*>(o), n, lse, rows);
+                           stream>>>(static_cast<uint16_t*>(o), n, lse, rows, seqlens, (size_t)B);
     return fa::record_cuda_status(cudaGetLastError(), "tree decode zero-fill launch");
   }
   const fa::TreePlan t =

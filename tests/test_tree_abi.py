@@ -201,3 +201,8 @@ def test_token_strides(fa, shape, stride, ok):
             fa._token_stride(t)
     else:
         assert fa._token_stride(t) == ok
+
+
+def test_tree_without_pages_needs_lengths(fa):
+    assert tree(fa, maxp=0, pages=0, lens=0) == fa.FA_ERR_INVALID_ARG
+    assert tree(fa, maxp=0, pages=0, lens=FAKE + 2) == fa.FA_ERR_INVALID_ARG

@@ -216,3 +216,16 @@ def test_many_rows_long_context(fa):
         tol = 2.0 ** -8 * (size + ref.abs()) * 1.01 + 2 * (132 * tp.U32 * 0.0885 * 400 + 2.0 ** -21) * size
         assert ((out[0, :, h].double() - ref).abs() <= tol).all()
         assert ((lse[0, :, h].double() - z).abs() <= 132 * tp.U32 * 0.0885 * 400 + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("lens,bad", [([0, 0, 0], False), ([0, -4, 0], False), ([0, 9, 0], True),
+                                      ([2, 0, 0], True)])
+def test_cache_without_pages(fa, lens, bad):
+    """max_pages 0: every sequence is padding, and a length above 0 is past the
+    page table, as with pages."""
+    t = list(inputs(3, 4, 4, 2, 64, 32, [0, 0, 0], torch.bfloat16, seed=5, max_pages=1))
+    t[3] = t[3][:, :0].contiguous()
+    t[4] = torch.tensor(lens, dtype=torch.int32)
+    out, lse = run(fa, t, 0.125, fa.FA_ERR_BOUNDS if bad else None)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert fa.fa_device_error()[0] == fa.FA_OK
