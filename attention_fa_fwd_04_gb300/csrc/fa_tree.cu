@@ -100,7 +100,7 @@ __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
   return (L < p.N || (long long)L > (long long)p.max_pages * p.page_size) ? 0 : L;
 }
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
-  return (tree_len(p, b) + tr::BN - 1) / tr::BN;
+  return (int)(((uint32_t)tree_len(p, b) + tr::BN - 1) / tr::BN);  // (lengths reach 2^31 - 1)
 }
 
 // a * b / c and a / c in 32 bits where they fit: a 64-bit division is a few
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         tc_fence_after();
         const int kv0 = (sg.t0 + j) * tr::BN;
         const uint32_t bad = tile_bad[tc % tr::BAD_RING];
-        const bool masked = kv0 + tr::BN > base || bad;
+        const bool masked = kv0 > base - tr::BN || bad;
         if (masked) {
           // V rows that no query may see (unused nodes, slots past the end,
           // bad pages) can hold anything: they are cleared, since 0 * NaN in

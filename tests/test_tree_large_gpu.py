@@ -125,3 +125,39 @@ def test_probabilities_past_2_31(fa):
         way, tok = tp.verify(p[b].cpu().numpy(), None, tokens[b].tolist(), parents[b].tolist(),
                              u[b].tolist())
         assert path[b].tolist() == way + [-1] * (N - len(way)) and int(nxt[b]) == tok
+
+
+def test_length_close_to_2_31(fa):
+    """The longest lengths, whose last tile ends past 2^31: one page over and
+    over, then the page that holds the tree."""
+    page, max_pages, N, D = 115264, 18631, 4, 64
+    cap = page * max_pages
+    assert 2 ** 31 - 128 < cap < 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(8)
+    kp = torch.empty(2, page, 1, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    vp = torch.ones_like(kp)
+    q = torch.empty(1, N, 2, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    table = torch.zeros(1, max_pages, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    parents = [-1, 0, 0, 2]
+    see = torch.from_numpy(tp.tree_sees(parents, N)[0]).cuda()
+    flat, rows = kp.reshape(-1, D).double(), q.reshape(-1, D).double()
+    s = (rows @ flat.T * 0.125).reshape(N, 2, 2, page)  # node, head, page, row
+    E = 68 * tp.U32 * 0.125 * float((rows.abs() @ flat.abs().T).max())
+    body = torch.logsumexp(s[:, :, 0], -1) + np.log(max_pages - 1)
+    for L in (cap - 9, cap):
+        last = page - (cap - L)  # rows in use of the last page
+        out, lse = fa.decode_tree(q, kp, vp, table, torch.tensor([L], dtype=torch.int32, device="cuda"),
+                                  torch.tensor([parents], dtype=torch.int32, device="cuda"), 0.125,
+                                  lse=True)
+        torch.cuda.synchronize()
+        assert fa.fa_device_error()[0] == fa.FA_OK
+        tail = s[:, :, 1, :last].clone()
+        tail[:, :, last - N:][~see[:, None].expand(N, 2, N)] = -torch.inf
+        ref = torch.logaddexp(body, torch.logsumexp(tail, -1))
+        # fp32 sums of a share's 2^31 / 128 / 152 tiles one after another, each
+        # addition off by at most half a step; the scores' part as in check_tree.
+        adds = cap / 128 / 152 + 200
+        assert ((lse[0].double() - ref).abs() <= adds * tp.U32 + E + 2.0 ** -18).all()
+        # O = 1 but for its sums: eight additions per tile, which may truncate.
+        assert ((out.float() - 1).abs() <= 8 * adds * 2 * tp.U32 + adds * tp.U32 + 2.0 ** -7).all()
