@@ -251,3 +251,47 @@ def test_append_with_bad_pages_and_lengths(fa):
         want[3, 26 + s] = qkv[2, s, 2:].cpu()
     assert torch.equal(vp.cpu(), want)
     assert fa.fa_device_error()[0] == fa.FA_OK
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,dtype,il,packed", SHAPES + [
+    (2432, 16, 16, 128, 128, torch.bfloat16, False, True),
+    (4865, 16, 5, 128, 128, torch.float16, True, False),
+    (3001, 33, 31, 64, 64, torch.bfloat16, False, False),
+])
+def test_weight_gradient_to_its_own_additions(fa, T, Hq, Hkv, D, rot, dtype, il, packed):
+    """Within the additions that a lane really makes, which no lost or doubled
+    group of rows can hide in (test_weight_grad_check.py plants some)."""
+    g = torch.Generator().manual_seed(T + D + 2)
+    q, k = heads(T, Hq, Hkv, D, dtype, g, packed)
+    qw, kw = weights(D, dtype, g)
+    pos = torch.randint(0, 5000, (T,), generator=g).int()
+    f = freqs(rot)
+    go = [torch.randn(T, H, D, generator=g).to(dtype).cuda() for H in (Hq, Hkv)]
+    got = fa.qk_norm_rope_backward(*go, q, k, qw.cuda(), kw.cuda(), f.cuda(), pos.cuda(), EPS,
+                                   interleaved=il)
+    adds = tp.lane_additions(T, Hq, Hkv, D, torch.cuda.get_device_properties(0).multi_processor_count)
+    ang = tp.angles(pos.numpy(), f)
+    tp.check_weight_grad(got[2], q, qw, go[0], ang, EPS, il, adds)
+    tp.check_weight_grad(got[3], k, kw, go[1], ang, EPS, il, adds)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,dtype,il,packed", [s for s in SHAPES if s[0] > 100])
+def test_single_tokens_reach_the_weight_gradient(fa, T, Hq, Hkv, D, rot, dtype, il, packed):
+    """A gradient of zero but for a few tokens, the first and the last among
+    them: each counts once, and the other tokens' dx is zero."""
+    g = torch.Generator().manual_seed(T + D + 3)
+    q, k = heads(T, Hq, Hkv, D, dtype, g, packed)
+    qw, kw = weights(D, dtype, g)
+    pos = torch.randint(0, 5000, (T,), generator=g).int()
+    f = freqs(rot)
+    at = sorted({0, T - 1, *torch.randint(0, T, (4,), generator=g).tolist()})
+    go = [torch.zeros(T, H, D, dtype=dtype).cuda() for H in (Hq, Hkv)]
+    for x in go:
+        x[at] = torch.randn(len(at), *x.shape[1:], generator=g).to(dtype).cuda()
+    got = fa.qk_norm_rope_backward(*go, q, k, qw.cuda(), kw.cuda(), f.cuda(), pos.cuda(), EPS,
+                                   interleaved=il)
+    ang = tp.angles(pos.numpy()[at], f)
+    for x, w, gr, dx, dw in ((q, qw, go[0], got[0], got[2]), (k, kw, go[1], got[1], got[3])):
+        tp.check_weight_grad(dw, x[at], w, gr[at], ang, EPS, il, len(at) * x.shape[1])
+        dx[at] = 0
+        assert not dx.any()

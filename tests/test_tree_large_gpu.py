@@ -161,3 +161,28 @@ def test_length_close_to_2_31(fa):
         assert ((lse[0].double() - ref).abs() <= adds * tp.U32 + E + 2.0 ** -18).all()
         # O = 1 but for its sums: eight additions per tile, which may truncate.
         assert ((out.float() - 1).abs() <= 8 * adds * 2 * tp.U32 + adds * tp.U32 + 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(135000, 128, 8, 128), (8500001, 4, 2, 64)])
+def test_weight_gradient_past_2_31_elements(fa, T, Hq, Hkv, D):
+    """Single tokens on both sides of 2^31 elements, each counted once."""
+    assert T * Hq * D > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(5)
+    qkv = torch.empty(T, Hq + Hkv, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q, k = qkv[:, :Hq], qkv[:, Hq:]
+    w = torch.empty(D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    f = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).float()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    edge = 2 ** 31 // (Hq * D)
+    at = [0, 77777, edge - 1, edge, T - 1]
+    go = [torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda") for H in (Hq, Hkv)]
+    for x in go:
+        x[at] = torch.empty(5, *x.shape[1:], device="cuda").normal_(generator=g).bfloat16()
+    dq, dk, dqw, dkw = fa.qk_norm_rope_backward(*go, q, k, w, w, f.cuda(), pos, 1e-6)
+    torch.cuda.synchronize()
+    assert fa.fa_device_error()[0] == fa.FA_OK
+    ang = tp.angles(at, f)
+    for x, gr, dx, dw in ((q, go[0], dq, dqw), (k, go[1], dk, dkw)):
+        tp.check_weight_grad(dw, x[at], w, gr[at], ang, 1e-6, False, 5 * x.shape[1])
+        dx[at] = 0
+        assert not dx.any()

@@ -75,6 +75,25 @@ def norm_rope_grad(x, w, g, ang, eps, interleaved):
     return dx, (gy * x * r).sum(axes), size, (gs * np.abs(x) * r).sum(axes)
 
 
+def lane_additions(T, Hq, Hkv, D, sms):
+    """At most how many rows one lane of the gradient adds up: two blocks of 8
+    warps per SM share the rows of both parts by their cost, 256 / D rows of a
+    warp side by side and a token's last group filled up; four times an even
+    share, and 16 more for what the shares' rounding leaves."""
+    at_once = 256 // D
+    groups = T * (-(-Hq // at_once) + -(-Hkv // at_once))
+    return 4 * -(-groups // (2 * sms * 8)) + 16
+
+
+def check_weight_grad(got, x, w, g, ang, eps, interleaved, adds):
+    """A weight's gradient: 40 fp32 roundings of each product, the additions of a
+    lane (adds), and 40 of a warp, a block and the blocks."""
+    _, ref, _, size = norm_rope_grad(x, w, g, ang, eps, interleaved)
+    tol = (40 + adds + 40) * U32 * size
+    err = np.abs(f64(got) - ref)
+    assert np.all(err <= tol), f"weight gradient off by {np.max(err / np.maximum(tol, 1e-30)):.3g} bounds"
+
+
 # ---------------------------------------------------------------- tree attention
 def tree_sees(parents, N):
     """see[s][a]: node a lies on node s's way up; usable[s]."""
