@@ -439,3 +439,78 @@ def test_prefill_of_normed_heads(fa):
     for x, gr, dx in ((qkv[:, :, :Hq], dq, gq), (qkv[:, :, Hq:Hq + Hkv], dk, gk)):
         ref, _, size, _ = tp.norm_rope_grad(x, w, gr, ang, EPS, False)
         assert np.all(np.abs(tp.f64(dx) - ref) <= 2.0 ** -8 * np.abs(ref) + 97 * tp.U32 * size)
+
+
+def run_keeping(st, fa):
+    """A step, and the pools as its attention read them: behind the appends and
+    before the compaction."""
+    append, compact, kept = fa.qk_norm_rope_append, fa.compact_tree, []
+
+    class Calls:
+        qk_norm_rope_append = staticmethod(append)
+        decode_tree = staticmethod(fa.decode_tree)
+        verify_tree = staticmethod(fa.verify_tree)
+
+        @staticmethod
+        def compact_tree(*a, **kw):
+            kept.extend((st.kp.clone(), st.vp.clone()))
+            return compact(*a, **kw)
+
+    return st.run(Calls), kept
+
+
+def check_attention(st, out, kept):
+    """O and log-sum-exp on the library's own keys, to check_tree's bounds, and the
+    keys themselves to the rotation's."""
+    Hq, Hkv, N, page = st.Hq, st.Hkv, st.N, st.page
+    lens, table = st.lens.tolist(), st.table.cpu().numpy()
+    ang = tp.angles(st.pos.cpu().numpy(), st.freq)
+    for layer in range(2):
+        q, o, lse = out[0][layer]
+        k, v, x = kept[0][layer].cpu(), kept[1][layer].cpu(), st.qkv[layer].cpu()
+        tp.check_tree(o, lse, q, k, v, table, lens, st.parents.tolist(), st.D ** -0.5)
+        for b, L in enumerate(lens):
+            t = np.arange(L - N, L)
+            rows = table[b, t // page], t % page
+            tp.check_rope(k[rows], x[b, :, Hq:Hq + Hkv], st.kw, ang[b], EPS, False)
+            assert torch.equal(v[rows], x[b, :, Hq + Hkv:])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,page,max_pages,dtype", [
+    (3, 7, 4, 2, 64, 32, 6, torch.bfloat16),
+    (2, 9, 8, 2, 128, 64, 5, torch.float16),
+    (2, 40, 16, 2, 64, 96, 4, torch.bfloat16),   # 320 rows: three row tiles
+    (1, 64, 8, 2, 128, 64, 6, torch.bfloat16),   # 256 rows: two
+])
+def test_attention_of_steps_to_its_own_bounds(fa, B, N, Hq, Hkv, D, page, max_pages, dtype, captured):
+    """Steps over changing lengths, in which a wrong mask, length or row shows in
+    the log-sum-exp (test_tree_check.py plants some)."""
+    st = Step(B, N, Hq, Hkv, D, 24, page, max_pages, seed=B + N + D, dtype=dtype)
+    st.draw([N] * B)
+    run_keeping(st, fa)  # (set-up)
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, kept = run_keeping(st, fa)
+    # A prompt of other lengths in each sequence.
+    st.kp.fill_(float("nan"))
+    st.vp.fill_(float("nan"))
+    lens = [(37 * b + 51) % (max_pages * page - 4 * N) for b in range(B)]
+    for b, L in enumerate(lens):
+        t = np.arange(L)
+        rows = torch.from_numpy(st.table.cpu().numpy()[b, t // page]).long().cuda(), torch.from_numpy(t % page).cuda()
+        for pool in (st.kp, st.vp):
+            for layer in range(2):
+                pool[layer][rows] = torch.randn(L, Hkv, D, generator=st.g).to(dtype).cuda()
+    for _ in range(3):
+        st.draw([L + N for L in lens])
+        if captured:
+            graph.replay()
+        else:
+            out, kept = run_keeping(st, fa)
+        torch.cuda.synchronize()
+        assert fa.fa_device_error()[0] == fa.FA_OK
+        check_attention(st, out, kept)
+        lens = out[4].tolist()
