@@ -15,9 +15,11 @@
 //
 // The answers are whole numbers, so a sum that is off by a rounding can change
 // one.  With 128000 tokens, fp32 sums would move about one border in a hundred
-// draws; residuals and sums are therefore kept as pairs of floats (about 48
-// bits, by error-free sums and products), which costs a dozen fp32 operations
-// per element where fp64 would be bound by the few fp64 units.
+// draws; residuals and sums are therefore kept as pairs of floats (48 bits, by
+// error-free sums and products, of which a pass over a row keeps 46), which costs a
+// dozen fp32 operations per element where fp64 would be bound by the few fp64
+// units.  After rejections the residual is the difference of p and c q: its error
+// is 2^-46 of those, whatever mass Z is left, so borders are good to 2^-46 c / Z.
 //
 // Bound: two rows of V floats per sequence (the node where its walk stops, and
 // nodes where more than one child is tried), once from HBM and for further

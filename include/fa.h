@@ -358,8 +358,9 @@ int fa_prefill_host_pieces(int B, int Sq, int Sk, int causal, int n_pieces,
  *   p * inv_freq[i]: (a cos - b sin, b cos + a sin); elements at rot_dim and
  *   past it pass through.
  *
- * fp32 arithmetic, one rounding.  Angles keep fp32 accuracy at every position
- * (phases are 64-bit fixed point).  Hq or Hkv may be 0 (that side's pointers are
+ * fp32 arithmetic, one rounding.  Angles are 64-bit fixed-point phases: with
+ * frequencies up to 1 as good as fp32's rounding of the cosine and sine at
+ * |position| < 2^28, and within 2 pi 2^-23 of a radian at 2^31.  Hq or Hkv may be 0 (that side's pointers are
  * then not used).
  */
 int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
@@ -484,9 +485,11 @@ int fa_decode_tree_fwd(const void* q, const void* kpages, const void* vpages,
  * node's target row; without mass there, the token is -1.  Probabilities that
  * are not positive finite numbers count as 0.
  *
- * Tests, residuals and sums are carried to at least 46 bits, so that the
- * answers are those of 64-bit arithmetic except where u lies within about
- * 1e-13 of a border.  N <= 64 (else FA_ERR_UNSUPPORTED), 1 <= V < 2^30.  A token
+ * Tests, residuals and sums are carried to at least 46 bits of the node's rows:
+ * the answers are those of 64-bit arithmetic except where u lies within about
+ * 2^-46 C / Z of a border, Z the mass that is left at the node and C one more than
+ * the masses before it.  (1e-13 at a node's first children; 1e-11 where a draft
+ * close to the target, rejected, leaves a mass of a thousandth.)  N <= 64 (else FA_ERR_UNSUPPORTED), 1 <= V < 2^30.  A token
  * outside [0, V) or a parent that is no lower node (nor -1, -2) makes its node
  * unreachable and sets the bounds bit of fa_device_error().
  */

@@ -152,3 +152,32 @@ def test_accepted_share_follows_the_target(fa):
     share = np.bincount(first.numpy(), minlength=V) / n
     ff = f.double().numpy()
     assert np.all(np.abs(share - ff) <= 5 * np.sqrt(ff * (1 - ff) / n))
+
+
+@pytest.mark.parametrize("closeness", [1e-2, 1e-3, 1e-5])
+@pytest.mark.parametrize("V", [500, 32001, 128000])
+def test_rejections_of_a_draft_close_to_the_target(fa, V, closeness):
+    """Residuals with little mass left, several rejections deep: the children are
+    tokens that the draft makes too likely, whose residual is zero.  With masses
+    from 1e-2 down to 1e-5 borders are good to about 1e-9, and no u lies so close to
+    one."""
+    B, N = 6, 6
+    g = torch.Generator().manual_seed(V)
+    logits = torch.randn(B, N, V, generator=g) * 1.5
+    p = torch.softmax(logits, -1)
+    q = torch.softmax(logits + closeness * torch.randn(B, N, V, generator=g), -1)
+    parents = torch.zeros(B, N, dtype=torch.int32)
+    parents[:, 4:] = 3  # (reached only where node 3 is accepted)
+    tokens = torch.zeros(B, N, dtype=torch.int32)
+    u = torch.rand(B, N, generator=g)
+    u[:, 1:4] = 1 - 2.0 ** -24
+    for b in range(B):
+        over = torch.nonzero(q[b, 0] > p[b, 0] * (1 + 1e-6))[:, 0]
+        tokens[b, 1:4] = over[torch.randint(0, len(over), (3,), generator=g)].int()
+        if b % 2:  # the third by a residual of its own: accepted or not
+            under = torch.nonzero(q[b, 0] < p[b, 0])[:, 0]
+            tokens[b, 3] = int(under[torch.randint(0, len(under), (1,), generator=g)])
+            u[b, 3] = torch.rand(1, generator=g)
+            tokens[b, 4:] = tokens[b, 1:3]
+    path, count, _ = check(fa, p, q, tokens, parents, u)
+    assert (count[::2] == 1).all()  # three rejections
