@@ -843,7 +843,8 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (row_ok) {
           if (whole) {
-            if (p.lse) p.lse[qrow] = l > 0.f ? 0.6931471805599453f * (m_used + log2f(l)) : NEG_INF;
+            // (A row with a score that is NaN has a sum and a log-sum-exp that are.)
+            if (p.lse) p.lse[qrow] = l == 0.f ? NEG_INF : 0.6931471805599453f * (m_used + log2f(l));
           } else {
             reinterpret_cast<float2*>(p.part_ml)[part * p.rt_rows + rr] = make_float2(m_used, l);
           }
@@ -1043,7 +1044,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                      TreeType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
   }
   if (p.lse && chunk == 0)
-    p.lse[row] = den > 0.f ? 0.6931471805599453f * (M + log2f(den)) : -INFINITY;
+    p.lse[row] = den == 0.f ? -INFINITY : 0.6931471805599453f * (M + log2f(den));
 }
 
 // Row tiles per CTA, row-tile CTAs per unit, tile groups.

@@ -229,3 +229,27 @@ def test_cache_without_pages(fa, lens, bad):
     out, lse = run(fa, t, 0.125, fa.FA_ERR_BOUNDS if bad else None)
     assert not out.any() and torch.isneginf(lse).all()
     assert fa.fa_device_error()[0] == fa.FA_OK
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,lens", [(6, 4, 2, [90, 41]), (6, 4, 2, [2600, 41]), (64, 4, 1, [700, 64])])
+def test_rows_with_a_score_that_is_nan(fa, N, Hq, Hkv, lens):
+    """NaN in q, or in the K of a node: O and log-sum-exp of the rows that have
+    such a score are NaN (not those of a row without keys), the others as ever."""
+    t = inputs(2, N, Hq, Hkv, 64, 64, lens, torch.bfloat16, seed=N)
+    q, kp, vp, table, lens, parents = t
+    q[0, 1, 2, 5] = float("nan")
+    at = lens[1].item() - N + 2
+    kp[int(table[1, at // 64]), at % 64, 0, 3] = float("nan")
+    out, lse = run(fa, t, 0.125)
+    want = torch.zeros(2, N, Hq, dtype=torch.bool)
+    want[0, 1, 2] = True
+    see = tp.tree_sees(parents[1].tolist(), N)[0][:, 2]
+    want[1, torch.from_numpy(see), :Hq // Hkv] = True
+    assert torch.equal(torch.isnan(lse.cpu()), want)
+    assert torch.equal(torch.isnan(out.cpu()), want[..., None].expand(out.shape))
+    sound = [x.clone() for x in t]
+    sound[0].nan_to_num_(0.0)
+    sound[1].nan_to_num_(0.0)
+    o2, l2 = run(fa, sound, 0.125)
+    keep = ~want.cuda()
+    assert torch.equal(out[keep], o2[keep]) and torch.equal(lse[keep], l2[keep])
