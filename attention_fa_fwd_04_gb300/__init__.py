@@ -10,6 +10,7 @@ integers, ``stream`` a ``cudaStream_t`` value):
     fa_decode_paged_fwd, fa_backward,
     fa_decode_fwd_noalloc, fa_status_string, fa_device_error, fa_last_cuda_error,
     fa_num_sms, fa_prefill_work_item, fa_prefill_rescale_count, fa_set_wait_limit_ns,
+    fa_release_scratch,
     fa_prefill_fwd_host, fa_prefill_host_pieces, fa_qk_norm_rope, fa_qk_norm_rope_append,
     fa_qk_norm_rope_backward, fa_decode_tree_fwd, fa_verify_tree, fa_compact_tree
 Tensor conveniences (contiguous CUDA tensors, caller-owned outputs):
@@ -52,7 +53,7 @@ EXPORTS = ("fa_prefill_fwd", "fa_prefill_fwd_lse", "fa_prefill_varlen_fwd", "fa_
            "fa_decode_fwd_lse", "fa_decode_paged_fwd", "fa_backward",
            "fa_decode_fwd_noalloc", "fa_status_string", "fa_device_error", "fa_last_cuda_error",
            "fa_num_sms", "fa_prefill_work_item", "fa_prefill_rescale_count",
-           "fa_set_wait_limit_ns", "fa_prefill_fwd_host", "fa_prefill_host_pieces",
+           "fa_set_wait_limit_ns", "fa_release_scratch", "fa_prefill_fwd_host", "fa_prefill_host_pieces",
            "fa_qk_norm_rope", "fa_qk_norm_rope_append", "fa_qk_norm_rope_backward",
            "fa_decode_tree_fwd", "fa_verify_tree", "fa_compact_tree")
 
@@ -115,6 +116,8 @@ def load(path: str = LIB_PATH):
     lib.fa_prefill_rescale_count.restype = i32
     lib.fa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     lib.fa_set_wait_limit_ns.restype = i32
+    lib.fa_release_scratch.argtypes = []
+    lib.fa_release_scratch.restype = i32
     lib.fa_prefill_fwd_host.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32,
                                         i32, i32, vp]
     lib.fa_prefill_fwd_host.restype = i32
@@ -295,6 +298,12 @@ def fa_set_wait_limit_ns(ns):
     """Time limit of every device pipeline wait (0: the 2 s default);
     synchronises."""
     return load().fa_set_wait_limit_ns(int(ns))
+
+
+def fa_release_scratch():
+    """Gives the scratch memory kept for later calls on the current device back
+    to the driver."""
+    return load().fa_release_scratch()
 
 
 # ----------------------------------------------------------------------------

@@ -71,9 +71,11 @@ int sm_count() {
   return n;
 }
 
+// The scratch pools of the devices, made with a device's first call that needs one.
+static std::mutex pool_mu;
+static cudaMemPool_t pools[64];
+
 cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
-  static std::mutex mu;
-  static cudaMemPool_t pools[64];
   static bool tried[64];
   int dev = 0;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -85,7 +87,7 @@ cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
   }
   cudaMemPool_t pool = nullptr;
   {
-    std::lock_guard<std::mutex> lock(mu);
+    std::lock_guard<std::mutex> lock(pool_mu);
     if (!tried[dev]) {
       tried[dev] = true;
       cudaMemPoolProps props = {};
@@ -106,6 +108,19 @@ cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
   }
   return pool ? cudaMallocFromPoolAsync(ptr, bytes, pool, stream)
               : cudaMallocAsync(ptr, bytes, stream);
+}
+
+static int scratch_release() {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return e;
+  cudaMemPool_t pool;
+  {
+    std::lock_guard<std::mutex> lock(pool_mu);
+    pool = pools[dev];
+  }
+  const SetupDuringCapture setup;
+  return pool ? cudaMemPoolTrimTo(pool, 0) : cudaSuccess;
 }
 
 }  // namespace fa
@@ -383,6 +398,10 @@ extern "C" int fa_set_wait_limit_ns(unsigned long long ns) {
   if (r == 0) r = fa::set_tree_wait_limit(ns);
   if (r == 0) r = fa::set_rope_wait_limit(ns);
   return cuda_status(r, "wait limit set");
+}
+
+extern "C" int fa_release_scratch(void) {
+  return cuda_status(fa::scratch_release(), "scratch release");
 }
 
 extern "C" int fa_last_cuda_error(const char** site) {

@@ -603,6 +603,20 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
 int fa_set_wait_limit_ns(unsigned long long ns);
 
 /*
+ * fa_release_scratch -- gives the scratch memory that is kept for later calls on
+ * the current device back to the driver.
+ *
+ * The tree decode and the norm and rotation's gradient take their stream-ordered
+ * scratch from a memory pool of this library's, outside any framework's
+ * allocator, which keeps up to 256 MiB per device of what calls have freed (the
+ * device's default pool would give it back at every synchronisation, and the
+ * next call would wait for the driver).  Memory that calls in flight still use is
+ * kept; captured graphs own theirs.  Does not wait for the GPU.
+ * Returns FA_OK or FA_ERR_CUDA.
+ */
+int fa_release_scratch(void);
+
+/*
  * fa_prefill_work_item -- host copy of the persistent scheduler's work-item
  * decode, for inspection and tests.  Work item w in [0, n_items) maps to
  * (b, hq, qblock); a qblock is 256 query rows.  Returns the number of items

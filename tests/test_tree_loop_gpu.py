@@ -514,3 +514,27 @@ def test_attention_of_steps_to_its_own_bounds(fa, B, N, Hq, Hkv, D, page, max_pa
         assert fa.fa_device_error()[0] == fa.FA_OK
         check_attention(st, out, kept)
         lens = out[4].tolist()
+
+
+def test_kept_scratch_is_given_back(fa):
+    """fa_release_scratch: what a call freed goes back to the driver; calls before
+    and behind it are as ever, one in flight among them."""
+    st = Step(B=4, N=64, Hq=128, Hkv=8, D=128, V=8, page=64, max_pages=32, seed=40)
+    st.kp.normal_()
+    st.vp.normal_()
+    st.draw([2000, 1900, 1500, 700])
+    q = torch.randn(4, 64, 128, 128, device="cuda").to(st.dtype)
+    args = (q, st.kp[0], st.vp[0], st.table, st.lens, st.parents, 0.088)
+    ref = fa.decode_tree(*args)
+    torch.cuda.synchronize()
+    held = torch.cuda.mem_get_info()[0]
+    assert fa.fa_release_scratch() == fa.FA_OK
+    freed = torch.cuda.mem_get_info()[0] - held
+    assert freed >= 2 ** 24  # (the partials: 152 CTAs x 2 x 256 rows x 130 floats = 40 MB)
+    outs = []
+    for _ in range(3):
+        outs.append(fa.decode_tree(*args))
+        assert fa.fa_release_scratch() == fa.FA_OK
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    assert fa.fa_device_error()[0] == fa.FA_OK
