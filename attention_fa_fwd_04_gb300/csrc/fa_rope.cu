@@ -301,7 +301,7 @@ struct Turn {
 // registers per head, two head groups' chains run side by side within 128
 // registers (16384 tokens of 16 + 16 heads, before later steps: 67.7 us; one after
 // another at 80 registers and three blocks per SM 82 us; both chunks in a lane 89 us).
-// Now 65.5 us, 6.1 TB/s.
+// Now 65.0 us, 6.2 TB/s.
 template <int D, bool IL>
 struct BackMap {
   static constexpr int LPH = D / 8;
@@ -576,8 +576,11 @@ __global__ void __launch_bounds__(rp::THREADS, rp::Cfg<D, false>::BLOCKS_PER_SM)
 // lanes and moves a few KB.  Blocks walk one part each, as in the gradient; a
 // step's rows are its tokens' heads one after another, the table holds the
 // cosines and sines of its tokens, and each lane makes the factors of its own
-// row's token.  50640 tokens of 4 + 2 heads, D = 64: 19.8 us, 3.9 TB/s (11.5 us at
-// the copy bandwidth); bound by the instructions per row, half of the issue slots.
+// row's token.  50640 tokens of 4 + 2 heads, D = 64: 19.9 us, 3.9 TB/s (11.5 us at
+// the copy bandwidth); bound by latency: 16 warps per SM, each on one chain of
+// shuffles, a reciprocal root and its factors, leave half of the issue slots free.
+// With one head a step is 384 / D rows, a quarter of a head group at D = 64: 60000
+// tokens of 1 + 1 heads 18.6 us against 4.5.
 
 // Copies of a step's heads of the tokens [t0, t0 + n) into `to`; whole warp.
 template <int D, typename T>
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(kDwThreads)
 // steps and, once, the token's cosines, sines and factors.  These count as an
 // eighth of a step (forward: 8192 tokens of 32 + 8 heads 30.5 us so, 31.5 us as a
 // quarter; 8192 of 128 + 8 heads 97.9 us, 100.9 us as a sixteenth) or a sixteenth
-// (gradient: 16384 tokens of 16 + 16 heads 65.5 us so, 69.0 us as an eighth).
+// (gradient: 16384 tokens of 16 + 16 heads 65.0 us so, 69.0 us as an eighth).
 static void plan_tasks(int tokens, int steps, long long warps, int weight, int* spt, int* cpt) {
   long long best = 0;
   for (int c = 1; c <= steps && c <= 64; ++c) {
@@ -943,7 +946,7 @@ static int part_blocks(const RopeParams& p, int i, long long slots, const long l
 // there are tokens enough for more than one.  A part's step holds as many tokens
 // as take the fewest rounds of its warps, a round costing its head groups and
 // about two more.  Returns the grid size, or 0.
-// (D = 64, 50640 tokens of 4 + 2 heads: 19.8 us, a token per step 50.5; 16384 of
+// (D = 64, 50640 tokens of 4 + 2 heads: 19.9 us, a token per step 50.5; 16384 of
 // 16 + 16: 24.8 and 28.5; without room, 16384 of 32 + 4: 32.7 and 31.8, and D = 128,
 // 16384 of 16 + 4: 35.5 and 32.2.  Into pages, 4096 of 8 + 2 + 2: D = 64 7.0 and
 // 9.5, D = 128 11.7 and 10.9.  Gradient: 33841 of 8 + 4 heads 35.0 and 40.9;

@@ -7,10 +7,20 @@
 //   O = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale <q, K_j> - max),
 //   j < L - N, or j = L - N + a for an ancestor-or-self a of s.
 //
-// Bound: each K/V byte is read once per row tile, and serves N * G query rows
+// Floor: each K/V byte is read once per row tile, and serves N * G query rows
 // (G = Hq / Hkv).  128 rows are 128 flops per byte, half of what the card
-// needs to be matrix-bound, so up to about 256 rows per kv head the cache
-// stream from HBM bounds it, and the matrix units above.
+// needs to be matrix-bound, so up to about 256 rows per kv head the floor is the
+// cache stream from HBM, and the matrix units above.  What bounds it at D = 128 and
+// two to eight row tiles is near that (16 sequences of up to 16384 tokens, 256 rows,
+// 134 us against 97.5; one of 65536, 1024 rows, 187 against 142); with one row tile
+// per CTA (up to 128, 257 to 384 and 513 to 640 rows) and at D = 64 it is the softmax
+// warps, 1.3 to 1.4e12 exponentials a second on one warpgroup per SM (4 sequences of
+// up to 16000 tokens, 336 rows: 39 us at D = 128, 35 at D = 64, against 12 and 6),
+// and over many short sequences each stretch's start and end.
+//
+// P is rounded to the inputs' type for P V: in fp32 it would need another kind of
+// MMA, at half of the rate or less, twice the tensor memory, and V converted.  Each
+// term of the sum is off by at most half a step of that type, relative to itself.
 //
 // Design: the rows (s, g) of one kv head are the M of tcgen05 MMAs against
 // 128-key tiles of the paged cache (S = Q K^T and O += P V, both accumulated in
@@ -55,7 +65,8 @@ struct Cfg {
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
   // MT = 2: three warpgroups, for the register split (setmaxnreg): launched with
   // 168 registers a thread, the softmax warpgroups take 208, the third keeps 88
-  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).
+  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).  The compiler spills
+  // 344 bytes of stores and 508 of loads there (MT = 1, 253 registers: none).
   static constexpr int THREADS = MT == 1 ? 192 : 384;
   static constexpr int RT = MT * BM;  // rows per CTA
   static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 4) : 12;
