@@ -12,7 +12,8 @@ integers, ``stream`` a ``cudaStream_t`` value):
     fa_num_sms, fa_prefill_work_item, fa_prefill_rescale_count, fa_set_wait_limit_ns,
     fa_release_scratch,
     fa_prefill_fwd_host, fa_prefill_host_pieces, fa_qk_norm_rope, fa_qk_norm_rope_append,
-    fa_qk_norm_rope_backward, fa_decode_tree_fwd, fa_verify_tree, fa_compact_tree
+    fa_qk_norm_rope_backward, fa_decode_tree_fwd, fa_verify_tree, fa_compact_tree,
+    fa_decode_shared_fwd, fa_sample, fa_update_pages, fa_write_pages
 Tensor conveniences (contiguous CUDA tensors, caller-owned outputs):
     prefill(q, k, v, scale, causal, out=None, stream=None, lse=None)
     prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, scale, causal,
@@ -35,6 +36,14 @@ Tensor conveniences (contiguous CUDA tensors, caller-owned outputs):
                 -> (path, count, next_token)
     compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=None,
                  stream=None) -> seqlens_out
+    decode_shared(q, kpages, vpages, page_table, seqlens, group_starts, prefix_lens, scale,
+                  out=None, stream=None, lse=None)
+    sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+           stream=None) -> tokens, or (tokens, probs)
+    update_pages(page_table, old_lens, new_lens, free_pages, free_count, page_size, max_new,
+                 shared_pages=None, lens_out=None, free_count_out=None, stream=None)
+                 -> (lens, free_count, cu_new, slots, positions)
+    write_pages(k, v, kpages, vpages, slots, stream=None)
     (lse=True allocates the fp32 log-sum-exp output; a tensor is used as is.)
 """
 import ctypes
@@ -43,7 +52,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
 
-FA_BF16, FA_FP16 = 0, 1
+FA_BF16, FA_FP16, FA_FP32 = 0, 1, 2  # FA_FP32: logits only
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 FA_ERR_TOO_LARGE = 5
 FA_ERR_BOUNDS = 6
@@ -55,7 +64,8 @@ EXPORTS = ("fa_prefill_fwd", "fa_prefill_fwd_lse", "fa_prefill_varlen_fwd", "fa_
            "fa_num_sms", "fa_prefill_work_item", "fa_prefill_rescale_count",
            "fa_set_wait_limit_ns", "fa_release_scratch", "fa_prefill_fwd_host", "fa_prefill_host_pieces",
            "fa_qk_norm_rope", "fa_qk_norm_rope_append", "fa_qk_norm_rope_backward",
-           "fa_decode_tree_fwd", "fa_verify_tree", "fa_compact_tree")
+           "fa_decode_tree_fwd", "fa_verify_tree", "fa_compact_tree", "fa_decode_shared_fwd",
+           "fa_sample", "fa_update_pages", "fa_write_pages")
 
 _lib = None
 
@@ -139,6 +149,14 @@ def load(path: str = LIB_PATH):
     lib.fa_verify_tree.restype = i32
     lib.fa_compact_tree.argtypes = [vp] * 7 + [i32] * 8 + [vp]
     lib.fa_compact_tree.restype = i32
+    lib.fa_decode_shared_fwd.argtypes = [vp] * 9 + [i32] * 9 + [f32, i32, vp]
+    lib.fa_decode_shared_fwd.restype = i32
+    lib.fa_sample.argtypes = [vp] * 8 + [i32, i32, i64, i32, vp]
+    lib.fa_sample.restype = i32
+    lib.fa_update_pages.argtypes = [vp] * 11 + [i32] * 5 + [vp]
+    lib.fa_update_pages.restype = i32
+    lib.fa_write_pages.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [i64, i64, vp]
+    lib.fa_write_pages.restype = i32
     _lib = lib
     return lib
 
@@ -254,6 +272,34 @@ def fa_compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_ou
                     Hkv, num_pages, page_size, max_pages, D, stream):
     return load().fa_compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out,
                                   layers, B, N, Hkv, num_pages, page_size, max_pages, D, stream)
+
+
+def fa_decode_shared_fwd(q, kpages, vpages, page_table, seqlens, group_starts, prefix_lens, o, lse,
+                         B, Sq, Hq, Hkv, num_pages, page_size, max_pages, groups, D, scale, dtype,
+                         stream):
+    return load().fa_decode_shared_fwd(q, kpages, vpages, page_table, seqlens, group_starts,
+                                       prefix_lens, o, lse, B, Sq, Hq, Hkv, num_pages, page_size,
+                                       max_pages, groups, D, scale, dtype, stream)
+
+
+def fa_sample(logits, uniforms, temperature, top_k, top_p, min_p, tokens, probs, rows, V,
+              row_stride, dtype, stream):
+    return load().fa_sample(logits, uniforms, temperature, top_k, top_p, min_p, tokens, probs, rows,
+                            V, row_stride, dtype, stream)
+
+
+def fa_update_pages(page_table, old_lens, new_lens, shared_pages, free_pages, free_count, lens_out,
+                    free_count_out, cu_new, slots, positions, B, page_size, max_pages, max_free,
+                    max_new, stream):
+    return load().fa_update_pages(page_table, old_lens, new_lens, shared_pages, free_pages,
+                                  free_count, lens_out, free_count_out, cu_new, slots, positions, B,
+                                  page_size, max_pages, max_free, max_new, stream)
+
+
+def fa_write_pages(k, v, kpages, vpages, slots, T, Hkv, num_pages, page_size, D, k_stride, v_stride,
+                   stream):
+    return load().fa_write_pages(k, v, kpages, vpages, slots, T, Hkv, num_pages, page_size, D,
+                                 k_stride, v_stride, stream)
 
 
 def fa_status_string(status) -> str:
@@ -553,7 +599,7 @@ def backward(q, k, v, o, dout, lse, scale, causal, stream=None):
 
 
 # ----------------------------------------------------------------------------
-# Norm with rotary positions, and draft-tree decoding.  Checks, outputs and
+# Norm with rotary positions, draft-tree decoding, serving steps.  Checks, outputs and
 # pointers are marshalled natively (csrc/fa_bind.cpp): these calls are short, and
 # the host's time per call is what a decoding step waits for.
 # ----------------------------------------------------------------------------
@@ -577,7 +623,8 @@ def _load_native():
             f"with `python -c \"import __graft_entry__ as g; g.build()\"`")
     _fa_bind.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_append, lib.fa_qk_norm_rope_backward,
-        lib.fa_decode_tree_fwd, lib.fa_verify_tree, lib.fa_compact_tree)))
+        lib.fa_decode_tree_fwd, lib.fa_verify_tree, lib.fa_compact_tree, lib.fa_decode_shared_fwd,
+        lib.fa_sample, lib.fa_update_pages, lib.fa_write_pages)))
     _native = _fa_bind
     return _fa_bind
 
@@ -670,3 +717,68 @@ def compact_tree(kpages, vpages, page_table, seqlens, path, count, seqlens_out=N
     if type(r) is int:
         raise FAError(r, "fa_compact_tree")
     return r
+
+
+def decode_shared(q, kpages, vpages, page_table, seqlens, group_starts, prefix_lens, scale, out=None,
+                  stream=None, lse=None):
+    """decode_paged for sequences that share long prefixes, each read once for its group.
+
+    q [B,Sq,Hq,D] (or [B,Hq,D] for Sq = 1); kpages/vpages [num_pages,page_size,Hkv,D], one
+    dtype (bf16 or fp16); page_table int32 [B,max_pages] (every row lists all of its
+    sequence's pages); seqlens int32 [B] (lengths including the new tokens).  Group g is
+    the sequences group_starts[g] to group_starts[g + 1] (int32 [groups + 1], rising);
+    their first prefix_lens[g] tokens (int32 [groups]) are the same and are read through
+    the row of the first of them that is past the prefix.  Returns ``out`` like q, or (out, lse) with lse
+    [B,Sq,Hq] fp32 when lse is True or a tensor."""
+    r = (_native or _load_native()).decode_shared(q, kpages, vpages, page_table, seqlens,
+                                                  group_starts, prefix_lens, scale, out, stream, lse)
+    if type(r) is int:
+        raise FAError(r, "fa_decode_shared_fwd")
+    return r
+
+
+def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+           stream=None):
+    """The next token of every row of logits [...,V] (bf16, fp16 or float32; rows may be
+    strided), from uniforms float32 [...] in [0,1).
+
+    Per row, each optional: temperature float32 [...] (0: greedy), top_k int32 [...] (0: off),
+    top_p float32 [...] (1: off), min_p float32 [...] (0: off).  Top-k first, then top-p of
+    what it keeps, then min-p.  Returns int32 tokens [...], or (tokens, probs) with the
+    filtered distribution, float32 like logits, when probs is True or a tensor."""
+    r = (_native or _load_native()).sample(logits, uniforms, temperature, top_k, top_p, min_p, probs,
+                                           stream)
+    if type(r) is int:
+        raise FAError(r, "fa_sample")
+    return r
+
+
+def update_pages(page_table, old_lens, new_lens, free_pages, free_count, page_size, max_new,
+                 shared_pages=None, lens_out=None, free_count_out=None, stream=None):
+    """A step's bookkeeping of a paged cache: sequences that shrink (new_lens int32 [B] below
+    old_lens) give pages back to the stack free_pages int32 [max_free], whose first
+    free_count int32 [1] entries are free; those that grow take pages from its top.
+    page_table int32 [B,max_pages] and free_pages are updated in place; the first
+    shared_pages[b] (int32 [B]) entries of a row are not the sequence's own.
+
+    Returns int32 (lens [B], free_count [1], cu_new [B + 1], slots [max_new], positions
+    [max_new]): the lengths that hold now (a sequence that found no room keeps its old one),
+    the free pages left, and for every new token, sequence after sequence, its slot in the
+    cache (-1 behind the last) and its position.  lens_out may be old_lens or new_lens,
+    free_count_out may be free_count (new tensors if None)."""
+    r = (_native or _load_native()).update_pages(page_table, old_lens, new_lens, free_pages,
+                                                 free_count, page_size, max_new, shared_pages,
+                                                 lens_out, free_count_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_update_pages")
+    return r
+
+
+def write_pages(k, v, kpages, vpages, slots, stream=None):
+    """K and V rows of packed tokens into the paged cache, in place: k and v [T,Hkv,D] (or
+    [...,Hkv,D]; slices of a packed projection are fine), kpages/vpages
+    [num_pages,page_size,Hkv,D] of the same dtype, slots int32 [T] (update_pages'; a negative
+    slot's token is not written)."""
+    r = (_native or _load_native()).write_pages(k, v, kpages, vpages, slots, stream)
+    if r is not None:
+        raise FAError(r, "fa_write_pages")

@@ -23,8 +23,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_decode.cu", "fa_decode_noalloc.cu",
-           "fa_backward.cu", "fa_host.cu", "fa_rope.cu", "fa_tree.cu", "fa_verify.cu"]
-HEADERS = ["fa_ptx.cuh", "fa_internal.h"]
+           "fa_backward.cu", "fa_host.cu", "fa_rope.cu", "fa_tree.cu", "fa_verify.cu",
+           "fa_shared.cu", "fa_sample.cu", "fa_pages.cu"]
+HEADERS = ["fa_ptx.cuh", "fa_tiles.cuh", "fa_exp2_table.h", "fa_internal.h"]
 BIND = os.path.join(HERE, "_fa_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "fa_bind.cpp")
 BIND_STAMP = os.path.join(HERE, "_fa_bind.torch")  # version of the torch it was built against

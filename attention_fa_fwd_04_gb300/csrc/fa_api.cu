@@ -368,12 +368,16 @@ extern "C" int fa_device_error(int reset, unsigned int* detail) {
   if (fa::read_decode_error(&b, reset) != 0) return FA_ERR_CUDA;
   if (fa::read_backward_error(&c, reset) != 0) return FA_ERR_CUDA;
   a |= c;  // the backward kernels report in the prefill half
-  // The cache append, tree decode, verification and compaction in the decode half.
+  // What works on the paged cache, and the verification, in the decode half.
   if (fa::read_rope_error(&c, reset) != 0) return FA_ERR_CUDA;
   b |= c;
   if (fa::read_tree_error(&c, reset) != 0) return FA_ERR_CUDA;
   b |= c;
   if (fa::read_verify_error(&c, reset) != 0) return FA_ERR_CUDA;
+  b |= c;
+  if (fa::read_shared_error(&c, reset) != 0) return FA_ERR_CUDA;
+  b |= c;
+  if (fa::read_pages_error(&c, reset) != 0) return FA_ERR_CUDA;
   b |= c;
   if (detail) *detail = (a & 0xFFFFu) | (b << 16);
   if ((a | b) & 1u) return FA_ERR_TIMEOUT;
@@ -397,6 +401,7 @@ extern "C" int fa_set_wait_limit_ns(unsigned long long ns) {
   if (r == 0) r = fa::set_backward_wait_limit(ns);
   if (r == 0) r = fa::set_tree_wait_limit(ns);
   if (r == 0) r = fa::set_rope_wait_limit(ns);
+  if (r == 0) r = fa::set_shared_wait_limit(ns);
   return cuda_status(r, "wait limit set");
 }
 

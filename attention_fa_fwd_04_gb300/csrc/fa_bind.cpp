@@ -1,7 +1,8 @@
-// fa_bind.cpp -- argument marshalling of the decoding-step operators: what the
-// package's qk_norm_rope, qk_norm_rope_backward, qk_norm_rope_append,
-// decode_tree, verify_tree and compact_tree do between the caller's tensors and
-// the C ABI (checks, outputs, pointers, the stream).
+// fa_bind.cpp -- argument marshalling of the decoding-step and serving-step
+// operators: what the package's qk_norm_rope, qk_norm_rope_backward,
+// qk_norm_rope_append, decode_tree, verify_tree, compact_tree, decode_shared,
+// sample, update_pages and write_pages do between the caller's tensors and the C
+// ABI (checks, outputs, pointers, the stream).
 //
 // Why native: these calls last 2 to 20 us on the GPU, and a decoding step makes
 // them one after another, so the host's time per call is what the caller waits
@@ -31,6 +32,10 @@ decltype(&fa_qk_norm_rope_backward) p_rope_backward;
 decltype(&fa_decode_tree_fwd) p_tree;
 decltype(&fa_verify_tree) p_verify;
 decltype(&fa_compact_tree) p_compact;
+decltype(&fa_decode_shared_fwd) p_shared;
+decltype(&fa_sample) p_sample;
+decltype(&fa_update_pages) p_update;
+decltype(&fa_write_pages) p_write;
 
 struct Refused {
   PyObject* type;
@@ -331,6 +336,21 @@ PyObject* append(PyObject* const* a) {
   return st ? PyLong_FromLong(st) : wrapped({qo});
 }
 
+// The log-sum-exp output that `o` asks for: True (a new one) or a float32 tensor.
+bool lse_output(PyObject* o, at::IntArrayRef rows, const Device& dev, at::Tensor* lse) {
+  if (o == Py_None || o == Py_False) return false;
+  if (o == Py_True) {
+    *lse = fresh(rows, at::kFloat, dev);
+    return true;
+  }
+  *lse = tensor(o, "lse");
+  if (lse->scalar_type() != at::kFloat) bad_value("lse must be a float32 tensor");
+  same_shape(*lse, "lse", rows);
+  contiguous(*lse, "lse");
+  dev.has(*lse);
+  return true;
+}
+
 // (q, kpages, vpages, page_table, seqlens, parents, scale, out, stream, lse)
 PyObject* tree(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
@@ -350,16 +370,7 @@ PyObject* tree(PyObject* const* a) {
   Stream s(a[8], dev.index);
   const at::Tensor out = output(a[7], "out", q, dev);
   at::Tensor lse;
-  const bool want = a[9] != Py_None && a[9] != Py_False;
-  if (a[9] == Py_True) {
-    lse = fresh(rows, at::kFloat, dev);
-  } else if (want) {
-    lse = tensor(a[9], "lse");
-    if (lse.scalar_type() != at::kFloat) bad_value("lse must be a float32 tensor [B,N,Hq]");
-    same_shape(lse, "lse", rows);
-    contiguous(lse, "lse");
-    dev.has(lse);
-  }
+  const bool want = lse_output(a[9], rows, dev, &lse);
   const int st = unlocked(
       p_tree, q.const_data_ptr(), p.k.const_data_ptr(), p.v.const_data_ptr(), i32(p.table),
       i32(p.lens), i32(parents), out.data_ptr(),
@@ -427,15 +438,181 @@ PyObject* compact(PyObject* const* a) {
   return st ? PyLong_FromLong(st) : wrapped({out});
 }
 
+// (q, kpages, vpages, page_table, seqlens, group_starts, prefix_lens, scale, out, stream, lse)
+PyObject* shared(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  if (q.dim() != 4 && q.dim() != 3) bad_value("q must be [B,Sq,Hq,D] or [B,Hq,D]");
+  const int code = head_dtype(q, "q");
+  const int64_t B = q.size(0), Sq = q.dim() == 4 ? q.size(1) : 1, Hq = q.size(q.dim() - 2);
+  const Pages p(a[1], a[2], a[3], a[4], B, false);
+  same_dtype(p.k, "kpages", q);
+  if (p.D != q.size(q.dim() - 1)) bad_value("kpages must be [num_pages,page_size,Hkv,D]");
+  const at::Tensor &starts = tensor(a[5], "group_starts"), &prefix = tensor(a[6], "prefix_lens");
+  dims(prefix, "prefix_lens", 1, "[groups]");
+  const int64_t groups = prefix.size(0), g1[1] = {groups + 1}, rows[3] = {B, Sq, Hq};
+  int32(starts, "group_starts", g1);
+  int32(prefix, "prefix_lens", prefix.sizes());
+  contiguous(q, "q");
+  const Device dev(q);
+  p.on(dev);
+  dev.has(starts);
+  dev.has(prefix);
+  Stream s(a[9], dev.index);
+  const at::Tensor out = output(a[8], "out", q, dev);
+  at::Tensor lse;
+  const bool want = lse_output(a[10], rows, dev, &lse);
+  const int st = unlocked(
+      p_shared, q.const_data_ptr(), p.k.const_data_ptr(), p.v.const_data_ptr(), i32(p.table),
+      i32(p.lens), i32(starts), i32(prefix), out.data_ptr(),
+      want ? static_cast<float*>(lse.data_ptr()) : nullptr, narrow(B), narrow(Sq), narrow(Hq), p.Hkv,
+      p.num_pages, p.page_size, p.max_pages, narrow(groups), p.D, (float)number(a[7]), code,
+      s.handle);
+  if (st) return PyLong_FromLong(st);
+  return want ? wrapped({out, lse}) : wrapped({out});
+}
+
+// (logits, uniforms, temperature, top_k, top_p, min_p, probs, stream)
+PyObject* sample(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "logits");
+  const int64_t n = x.dim();
+  if (n < 1 || x.size(n - 1) < 1) bad_value("logits must be [...,V]");
+  const int code = x.scalar_type() == at::kFloat ? FA_FP32 : head_dtype(x, "logits (or float32)");
+  const int64_t V = x.size(n - 1);
+  const at::IntArrayRef lead = x.sizes().slice(0, n - 1);
+  // Rows at one stride, their elements side by side.
+  int64_t rows = 1, stride = -1, step = 0;
+  bool ok = x.stride(n - 1) == 1 || V == 1;
+  for (int64_t i = n - 2; i >= 0; --i) {
+    rows *= x.size(i);
+    if (x.size(i) == 1) continue;
+    if (stride < 0)
+      stride = x.stride(i);
+    else
+      ok = ok && x.stride(i) == step;
+    step = x.stride(i) * x.size(i);
+  }
+  if (stride < 0) stride = V;
+  if (rows > 0 && (!ok || stride < V))
+    bad_value("logits: elements must be contiguous and rows at one stride of at least V");
+  if (rows == 0) stride = V;
+  const Device dev(x);
+  auto setting = [&](PyObject* o, const char* name, at::ScalarType type,
+                     const char* type_name) -> const at::Tensor* {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    is_type(t, name, type, type_name);
+    same_shape(t, name, lead);
+    contiguous(t, name);
+    dev.has(t);
+    return &t;
+  };
+  const at::Tensor* u = setting(a[1], "uniforms", at::kFloat, "float32");
+  if (!u) bad_type("uniforms must be a tensor");
+  const at::Tensor* T = setting(a[2], "temperature", at::kFloat, "float32");
+  const at::Tensor* k = setting(a[3], "top_k", at::kInt, "int32");
+  const at::Tensor* tp = setting(a[4], "top_p", at::kFloat, "float32");
+  const at::Tensor* mp = setting(a[5], "min_p", at::kFloat, "float32");
+  Stream s(a[7], dev.index);
+  const at::Tensor tokens = fresh(lead, at::kInt, dev);
+  at::Tensor probs;
+  const bool want = a[6] != Py_None && a[6] != Py_False;
+  if (a[6] == Py_True) {
+    probs = fresh(x.sizes(), at::kFloat, dev);
+  } else if (want) {
+    probs = tensor(a[6], "probs");
+    is_type(probs, "probs", at::kFloat, "float32");
+    same_shape(probs, "probs", x.sizes());
+    contiguous(probs, "probs");
+    dev.has(probs);
+  }
+  const int st = unlocked(
+      p_sample, x.const_data_ptr(), f32(*u), T ? f32(*T) : nullptr, k ? i32(*k) : nullptr,
+      tp ? f32(*tp) : nullptr, mp ? f32(*mp) : nullptr, static_cast<int32_t*>(tokens.data_ptr()),
+      want ? static_cast<float*>(probs.data_ptr()) : nullptr, narrow(rows), narrow(V),
+      (long long)stride, code, s.handle);
+  if (st) return PyLong_FromLong(st);
+  return want ? wrapped({tokens, probs}) : wrapped({tokens});
+}
+
+int whole(PyObject* o, const char* name) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  if (v < INT32_MIN || v > INT32_MAX) bad_value(std::string(name) + " must be a 32-bit number");
+  return static_cast<int>(v);
+}
+
+// (page_table, old_lens, new_lens, free_pages, free_count, page_size, max_new, shared_pages,
+//  lens_out, free_count_out, stream)
+PyObject* update(PyObject* const* a) {
+  const at::Tensor &table = tensor(a[0], "page_table"), &olds = tensor(a[1], "old_lens"),
+                   &news = tensor(a[2], "new_lens"), &pages = tensor(a[3], "free_pages"),
+                   &count = tensor(a[4], "free_count");
+  dims(table, "page_table", 2, "[B,max_pages]");
+  dims(pages, "free_pages", 1, "[max_free]");
+  const int64_t B = table.size(0), b1[1] = {B}, one[1] = {1};
+  int32(table, "page_table", table.sizes());
+  int32(olds, "old_lens", b1);
+  int32(news, "new_lens", b1);
+  int32(pages, "free_pages", pages.sizes());
+  int32(count, "free_count", one);
+  const int page_size = whole(a[5], "page_size"), max_new = whole(a[6], "max_new");
+  if (max_new < 0) bad_value("max_new must not be negative");
+  const at::Tensor* shared = a[7] == Py_None ? nullptr : &tensor(a[7], "shared_pages");
+  if (shared) int32(*shared, "shared_pages", b1);
+  const Device dev(table);
+  for (const at::Tensor* t : {&olds, &news, &pages, &count}) dev.has(*t);
+  if (shared) dev.has(*shared);
+  Stream s(a[10], dev.index);
+  const at::Tensor lens = output(a[8], "lens_out", olds, dev),
+                   left = output(a[9], "free_count_out", count, dev);
+  const at::Tensor cu = fresh({B + 1}, at::kInt, dev), slots = fresh({max_new}, at::kInt, dev),
+                   pos = fresh({max_new}, at::kInt, dev);
+  auto w = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+  const int st = unlocked(p_update, w(table), i32(olds), i32(news), shared ? i32(*shared) : nullptr,
+                          w(pages), i32(count), w(lens), w(left), w(cu), w(slots), w(pos), narrow(B),
+                          page_size, narrow(table.size(1)), narrow(pages.size(0)), max_new, s.handle);
+  return st ? PyLong_FromLong(st) : wrapped({lens, left, cu, slots, pos});
+}
+
+// (k, v, kpages, vpages, slots, stream)
+PyObject* write(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kp = tensor(a[2], "kpages"),
+                   &vp = tensor(a[3], "vpages"), &slots = tensor(a[4], "slots");
+  const int64_t n = k.dim();
+  if (n < 3) bad_value("k must be [...,Hkv,D]");
+  head_dtype(k, "k");
+  same_dtype(v, "v", k);
+  same_dtype(kp, "kpages", k);
+  same_dtype(vp, "vpages", k);
+  same_shape(v, "v", k.sizes());
+  dims(kp, "kpages", 4, "[num_pages,page_size,Hkv,D]");
+  same_shape(vp, "vpages", kp.sizes());
+  if (kp.size(2) != k.size(n - 2) || kp.size(3) != k.size(n - 1))
+    bad_value("kpages must be [num_pages,page_size,Hkv,D] with k's heads");
+  contiguous(kp, "kpages");
+  contiguous(vp, "vpages");
+  int32(slots, "slots", k.sizes().slice(0, n - 2));
+  const int64_t ks = token_stride(k, "k"), vs = token_stride(v, "v");
+  const Device dev(k);
+  for (const at::Tensor* t : {&v, &kp, &vp, &slots}) dev.has(*t);
+  Stream s(a[5], dev.index);
+  const int st = unlocked(p_write, k.const_data_ptr(), v.const_data_ptr(), kp.data_ptr(),
+                          vp.data_ptr(), i32(slots), (long long)slots.numel(), narrow(kp.size(2)),
+                          narrow(kp.size(0)), narrow(kp.size(1)), narrow(kp.size(3)), (long long)ks,
+                          (long long)vs, s.handle);
+  if (st) return PyLong_FromLong(st);
+  Py_RETURN_NONE;
+}
+
 // (tensor): its token stride.
 PyObject* stride_of(PyObject* const* a) {
   return PyLong_FromLongLong(token_stride(tensor(a[0], "x"), "x"));
 }
 
-// (addresses of the library's six entry points)
+// (addresses of the library's ten entry points)
 PyObject* bind(PyObject* const* a) {
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  void* p[10];
+  for (int i = 0; i < 10; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) throw python_error();
   }
@@ -445,6 +622,10 @@ PyObject* bind(PyObject* const* a) {
   p_tree = reinterpret_cast<decltype(p_tree)>(p[3]);
   p_verify = reinterpret_cast<decltype(p_verify)>(p[4]);
   p_compact = reinterpret_cast<decltype(p_compact)>(p[5]);
+  p_shared = reinterpret_cast<decltype(p_shared)>(p[6]);
+  p_sample = reinterpret_cast<decltype(p_sample)>(p[7]);
+  p_update = reinterpret_cast<decltype(p_update)>(p[8]);
+  p_write = reinterpret_cast<decltype(p_write)>(p[9]);
   Py_RETURN_NONE;
 }
 
@@ -472,13 +653,17 @@ PyMethodDef method(const char* name) {
           METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<bind, 6>("bind"),
+PyMethodDef methods[] = {method<bind, 10>("bind"),
                          method<norm_rope, 11>("qk_norm_rope"),
                          method<norm_rope_backward, 11>("qk_norm_rope_backward"),
                          method<append, 15>("qk_norm_rope_append"),
                          method<tree, 10>("decode_tree"),
                          method<verify, 6>("verify_tree"),
                          method<compact, 8>("compact_tree"),
+                         method<shared, 11>("decode_shared"),
+                         method<sample, 8>("sample"),
+                         method<update, 11>("update_pages"),
+                         method<write, 6>("write_pages"),
                          method<stride_of, 1>("token_stride"),
                          {nullptr, nullptr, 0, nullptr}};
 

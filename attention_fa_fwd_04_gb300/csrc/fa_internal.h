@@ -76,6 +76,8 @@ int read_decode_error(unsigned int* out, int reset);
 int read_rope_error(unsigned int* out, int reset);
 int read_tree_error(unsigned int* out, int reset);
 int read_verify_error(unsigned int* out, int reset);
+int read_pages_error(unsigned int* out, int reset);
+int read_shared_error(unsigned int* out, int reset);
 
 // Rows whose prefill lazy rescale fired since the last reset (read + optionally
 // clear).  Returns a cudaError_t.
@@ -88,6 +90,7 @@ int set_decode_wait_limit(unsigned long long ns);
 int set_backward_wait_limit(unsigned long long ns);
 int set_tree_wait_limit(unsigned long long ns);
 int set_rope_wait_limit(unsigned long long ns);
+int set_shared_wait_limit(unsigned long long ns);
 
 // Stream-ordered scratch (free it with cudaFreeAsync on the stream) from a pool
 // of this library's that keeps up to 256 MiB of freed memory per device: the
@@ -112,6 +115,28 @@ class SetupDuringCapture {
   cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
   bool ok_;
 };
+
+// Launch as a programmatic dependent of the grid before it on the stream, in
+// clusters of `cluster` blocks (0: none).
+template <typename P>
+cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, cudaStream_t stream,
+                             const P& p, int cluster = 0, size_t smem = 0) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // Status of a CUDA call for the C ABI: FA_OK for 0, else FA_ERR_CUDA after
 // recording the raw error and the failing call (a static string) for

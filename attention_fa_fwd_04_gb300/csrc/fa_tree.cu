@@ -47,46 +47,15 @@
 #include "fa.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
+#include "fa_tiles.cuh"
 
 namespace fa {
 
 __device__ unsigned int g_tree_err = 0;
 
 namespace tr {
-constexpr int BM = 128;    // query rows per tile
-constexpr int BN = 128;    // keys per K/V tile
+using namespace tiles;
 constexpr int MAX_N = 64;  // tree nodes: one 64-bit ancestor mask per row
-constexpr int HALF_BYTES = 128 * 128;  // 128 rows x 64 elements x 2 bytes
-constexpr int BAD_RING = 16;  // tiles whose page faults are remembered (> tiles in flight)
-
-template <int D, int MT>
-struct Cfg {
-  static constexpr int HALVES = D / 64;
-  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
-  // MT = 2: three warpgroups, for the register split (setmaxnreg): launched with
-  // 168 registers a thread, the softmax warpgroups take 208, the third keeps 88
-  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).  The compiler spills
-  // 344 bytes of stores and 508 of loads there (MT = 1, 253 registers: none).
-  static constexpr int THREADS = MT == 1 ? 192 : 384;
-  static constexpr int RT = MT * BM;  // rows per CTA
-  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 4) : 12;
-  // MT = 2 (matrix-bound): ring positions 2g - 1 (a V) and 2g (the K after it)
-  // share a pair of slots, released by one commit, and land on one barrier: the
-  // MMA warp's instruction stream paces the kernel, and a commit or a wait
-  // less per tile shows.  MT = 1 (bound by memory) releases slots one by one.
-  static constexpr bool PAIRED = MT == 2;
-  static constexpr int NPAIR = NSTAGE / 2;
-  static_assert(NSTAGE % 2 == 0, "pairs");
-  static constexpr int SMEM_Q = MT * TILE_BYTES;
-  static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
-  static constexpr int SMEM_BAR = 512;
-  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV + SMEM_BAR;
-  static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
-  static_assert(NSTAGE / 2 + 2 < BAD_RING, "tiles in flight");
-  // Tensor memory: two S buffers (MT = 1: of alternate tiles; MT = 2: of the
-  // two row tiles), then O of each row tile.
-  static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
-};
 }  // namespace tr
 
 struct TreeParams {
@@ -112,16 +81,6 @@ __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
 }
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
   return (int)(((uint32_t)tree_len(p, b) + tr::BN - 1) / tr::BN);  // (lengths reach 2^31 - 1)
-}
-
-// a * b / c and a / c in 32 bits where they fit: a 64-bit division is a few
-// hundred instructions, and a short call makes several one after another.
-__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
-  return a <= (0xffffffffll / (b + 1)) ? (long long)((uint32_t)a * (uint32_t)b / (uint32_t)c)
-                                       : a * b / c;
-}
-__device__ __forceinline__ int div_small(long long a, int c) {
-  return a >> 32 == 0 ? (int)((uint32_t)a / (uint32_t)c) : (int)(a / c);
 }
 
 // The list: the tiles of every unit (sequence, kv head), each unit's followed by
@@ -245,13 +204,6 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& w, Tree
   return true;
 }
 
-// Bits [0, n) of a 128-bit mask held as two words (n may lie outside).
-struct Mask128 {
-  uint64_t lo, hi;
-};
-__device__ __forceinline__ uint64_t low_bits(int n) {
-  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
-}
 // The keys [0, at) and the tree's nodes `bits` from key `at` on, both relative
 // to a tile.
 __device__ __forceinline__ Mask128 tile_mask(int at, uint64_t bits) {
@@ -267,19 +219,6 @@ __device__ __forceinline__ Mask128 tile_mask(int at, uint64_t bits) {
   }
   return m;
 }
-// Keys of a tile whose pages are sound (bad: one bit per box of `box` keys).
-__device__ __forceinline__ Mask128 sound_keys(uint32_t bad, int box) {
-  Mask128 m{~0ull, ~0ull};
-  if (bad == 0) return m;
-  for (int i = 0; i < 128 / box; ++i)
-    if (bad >> i & 1) {
-      const int a = i * box, e = a + box;
-      m.lo &= ~(low_bits(e) & ~low_bits(a));
-      m.hi &= ~(low_bits(e - 64) & ~low_bits(a - 64));
-    }
-  return m;
-}
-
 // Whole warp: ancestor masks of sequence b's nodes, lane l holding nodes l and
 // l + 32, by pointer doubling (six rounds reach depth 64).  A node is unused
 // when its parent entry is -2, is not a lower node (which also sets the bounds
@@ -326,27 +265,6 @@ __device__ __forceinline__ void tree_masks(const TreeParams& p, int b, uint64_t 
   *used = w0 | w1 << 32;
 }
 
-template <typename T>
-struct TreeType {
-  static constexpr bool kBF16 = true;
-  // Largest row sum of unnormalised P that a tile may leave before the row's
-  // maximum is renewed: P fits the type and the sums fit fp32.
-  static constexpr float kBig = 1.152921504606846976e18f;  // 2^60
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-};
-template <>
-struct TreeType<__half> {
-  static constexpr bool kBF16 = false;
-  static constexpr float kBig = 32768.f;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-};
-
 template <int D, typename T, int MT>
 __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
     tree_split_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -355,7 +273,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
   using C = tr::Cfg<D, MT>;
   constexpr int NSTAGE = C::NSTAGE;
   constexpr int W_PROD = MT * 4, W_MMA = MT * 4 + 1;
-  constexpr bool kBF16 = TreeType<T>::kBF16;
+  constexpr bool kBF16 = TileType<T>::kBF16;
   constexpr float NEG_INF = -INFINITY;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -661,17 +579,9 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
     // as soon as S of the stretch before's last tile is there (no MMA reads Q
     // any more), so that the next stretch's S runs under the epilogue.
     auto load_q = [&](const TreeSeg& t) {
-      uint4 v[D / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(p.q) +
-          (((size_t)t.b * p.N + s) * p.Hq + (size_t)t.hkv * p.G + g) * D);
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) v[x] = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-      uint8_t* dst = sQ + i * C::TILE_BYTES + tid * 128;
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x)
-        *reinterpret_cast<uint4*>(dst + (x >> 3) * tr::HALF_BYTES + (((x & 7) ^ (tid & 7)) << 4)) =
-            v[x];
+      const T* const src = static_cast<const T*>(p.q) +
+                           (((size_t)t.b * p.N + s) * p.Hq + (size_t)t.hkv * p.G + g) * D;
+      put_q_row<D>(sQ + i * C::TILE_BYTES, tid, src, row_ok);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);
     };
@@ -704,124 +614,32 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
           // bad pages) can hold anything: they are cleared, since 0 * NaN in
           // P V would reach every row.
           const Mask128 any = tile_mask(base - kv0, used), fine = sound_keys(bad, p.box);
-          // This warp's 32 rows, a row by D/8 lanes.
-          const uint64_t keep64 = wq < 2 ? any.lo & fine.lo : any.hi & fine.hi;
-          const uint32_t clear = ~(uint32_t)(wq & 1 ? keep64 >> 32 : keep64);
+          const Mask128 keep{any.lo & fine.lo, any.hi & fine.hi};
           const uint32_t cv = 2 * tc + 1;
           const uint32_t on = C::PAIRED && j + 1 < sg.n ? cv + 1 : cv;  // V's barrier
           if (!(ok = mbar_wait<false>(&full[on % NSTAGE], (on / NSTAGE) & 1, abort_flag,
                                       &g_tree_err, 10)))
             break;
-          const int x = lane % (D / 8);
-          uint8_t* const vt = sKV + (cv % NSTAGE) * C::TILE_BYTES + (x >> 3) * tr::HALF_BYTES +
-                              wq * 32 * 128 + (x & 7) * 16;
-#pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 256 / D) {
-            const int r = r0 + lane / (D / 8);
-            if (clear >> r & 1)
-              *reinterpret_cast<uint4*>(vt + r * 128) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
+          clear_rows<D>(sKV + (cv % NSTAGE) * C::TILE_BYTES, wq, lane, keep);
         }
         // MT = 1: (the stretch before waited for its last P V.)  MT = 2: S of
         // this tile was issued after P V of the last, and both are done.
         bool pv_waited = MT == 2 || j == 0;
         if (warp_ok) {
-          uint32_t sr[4][32];
-          float mx = hide;
-          float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-          auto find_max = [&](uint32_t (&reg)[32]) {
-            const float* v = reinterpret_cast<const float*>(reg);
-            if (!neg) {
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) mx = max3f(mx, v[x], v[x + 1]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) mx = min3f(mx, v[x], v[x + 1]);
-            }
-          };
-          auto exp_store = [&](uint32_t (&reg)[32], int q, float top) {
-            const float* v = reinterpret_cast<const float*>(reg);
-            const float2 c2 = make_float2(c, c), nb = make_float2(-top, -top);
-            uint32_t pk[16];
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              const float2 a = __ffma2_rn(make_float2(v[2 * t], v[2 * t + 1]), c2, nb);
-              const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-              if (t & 1)
-                lb = __fadd2_rn(lb, e);
-              else
-                la = __fadd2_rn(la, e);
-              pk[t] = TreeType<T>::pack(e.x, e.y);
-            }
-            tmem_st16(tS + q * 16, pk);
-          };
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) reg_fence32(sr[q]);
-          if (masked) {
+          auto mask = [&](uint32_t (&sr)[4][32]) {
             const Mask128 fine = sound_keys(bad, p.box), mine = tile_mask(base - kv0, anc);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint64_t m64 = q < 2 ? mine.lo & fine.lo : mine.hi & fine.hi;
-              const uint32_t see = (uint32_t)(q & 1 ? m64 >> 32 : m64);
-              if (__all_sync(0xffffffffu, see == ~0u)) continue;  // keys before the tree
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!(see >> x & 1)) sr[q][x] = __float_as_uint(hide);
-            }
-          }
-          // The stretch's first tile takes its own maximum; later tiles are
-          // exponentiated against the running one, and a row takes the slow
-          // path only when its sum outgrows kBig or it had seen no key yet.
-          bool renew = j == 0;
-          if (!renew) {
-            const float top = m_used == NEG_INF ? 0.f : m_used;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) exp_store(sr[q], q, top);
-            const float lt = (la.x + la.y) + (lb.x + lb.y);
-            const bool mine = !(lt <= TreeType<T>::kBig) || m_used == NEG_INF;
-            renew = __any_sync(0xffffffffu, mine);
-          }
-          if (renew) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) find_max(sr[q]);
-            const float m_new = fmaxf(m_used, mx * c);
-            const float f = m_used == NEG_INF ? 0.f : fast_exp2(m_used - m_new);
-            const float top = m_new == NEG_INF ? 0.f : m_new;
-            if (j > 0) {
-              tmem_wait_st();
-              la = lb = make_float2(0.f, 0.f);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) exp_store(sr[q], q, top);
-            l *= f;
-            m_used = m_new;
-            if (j > 0) {
-              // O of the tiles so far, once the last of their P V is done.
-              if (!pv_waited && !(ok = mbar_wait<false>(&pv_done[i], (tc - 1) & 1, abort_flag,
-                                                        &g_tree_err, 11)))
-                break;
-              __syncwarp();
-              pv_waited = true;
-              tc_fence_after();
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(tO + q * 32, o);
-                tmem_wait_ld();
-                reg_fence32(o);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                tmem_st32(tO + q * 32, o);
-              }
-            }
-          }
-          l += (la.x + la.y) + (lb.x + lb.y);
-          tmem_wait_st();
+            hide_keys(sr, Mask128{mine.lo & fine.lo, mine.hi & fine.hi}, hide);
+          };
+          // O of the tiles so far may be rescaled once the last of their P V is done.
+          auto settled = [&] {
+            if (!pv_waited && !(ok = mbar_wait<false>(&pv_done[i], (tc - 1) & 1, abort_flag,
+                                                      &g_tree_err, 11)))
+              return false;
+            __syncwarp();
+            pv_waited = true;
+            return true;
+          };
+          if (!softmax_tile<D, T>(tS, tO, c, j == 0, masked, mask, settled, &m_used, &l)) break;
         }
         // MT = 1: one phase of pv_done per tile, each waited for before the next P
         // is handed over: the parity waits never fall two phases behind.
@@ -876,7 +694,7 @@ __global__ void __launch_bounds__(tr::Cfg<D, MT>::THREADS, 1)
               for (int y = 0; y < 4; ++y) {
                 const float e0 = __uint_as_float(o[8 * x + 2 * y]) * inv;
                 const float e1 = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
-                k[y] = live ? TreeType<T>::pack(e0, e1) : 0u;
+                k[y] = live ? TileType<T>::pack(e0, e1) : 0u;
               }
               dst[x] = make_uint4(k[0], k[1], k[2], k[3]);
             }
@@ -1041,7 +859,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     }
     if (!real) return;
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    reinterpret_cast<uint32_t*>(dst)[warp] = TreeType<T>::pack(a0 * inv, a1 * inv);
+    reinterpret_cast<uint32_t*>(dst)[warp] = TileType<T>::pack(a0 * inv, a1 * inv);
     if (warp != 0) return;
   } else {
     if (!real) return;
@@ -1049,10 +867,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       reinterpret_cast<uint4*>(dst)[e] =
-          make_uint4(TreeType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
-                     TreeType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-                     TreeType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-                     TreeType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+          make_uint4(TileType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
+                     TileType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
+                     TileType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
+                     TileType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
   }
   if (p.lse && chunk == 0)
     p.lse[row] = den == 0.f ? -INFINITY : 0.6931471805599453f * (M + log2f(den));

@@ -651,25 +651,6 @@ __global__ void __launch_bounds__(cp::THREADS)
   }
 }
 
-template <typename P>
-static cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, cudaStream_t stream,
-                                    const P& p, int cluster = 0) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 int read_verify_error(unsigned int* out, int reset) {
   unsigned int v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_verify_err, sizeof(v));

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype_t;
+typedef enum { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype_t; /* FA_FP32: logits only */
 
 typedef enum {
   FA_OK = 0,
@@ -528,6 +528,146 @@ int fa_compact_tree(void* kpages, void* vpages, const int32_t* page_table,
                     int32_t* seqlens_out, int layers, int B, int N, int Hkv, int num_pages,
                     int page_size, int max_pages, int D, cudaStream_t stream);
 
+/*
+ * fa_decode_shared_fwd -- fa_decode_paged_fwd for a batch whose sequences share
+ * long prefixes (a system prompt, a document): the keys of a prefix are read and
+ * multiplied once for all sequences of its group.
+ *
+ *   q, o             [B, Sq, Hq, D]   bf16 or fp16
+ *   kpages, vpages   [num_pages, page_size, Hkv, D]
+ *   page_table       [B, max_pages] int32, device; every row lists all pages of its
+ *                    sequence, as for fa_decode_paged_fwd
+ *   seqlens          [B] int32, device: valid lengths L including the Sq new tokens,
+ *                    clamped to [0, max_pages * page_size]
+ *   group_starts     [groups + 1] int32, device, rising: group g is the sequences
+ *                    [group_starts[g], group_starts[g + 1]); sequences before the
+ *                    first and behind the last start are in none
+ *   prefix_lens      [groups] int32, device: the first prefix_lens[g] tokens of the
+ *                    group's sequences are the same
+ *   lse              NULL, or [B, Sq, Hq] fp32: each row's log-sum-exp
+ *   page_size        a positive multiple of 32
+ *
+ * Rows are fa_decode_paged_fwd's: new token s sees the keys [0, L - Sq + s]; rows
+ * that see no key give O = 0 and lse = -inf.  The keys of a prefix are read through
+ * the row of the group's first sequence whose new tokens all see the whole prefix.
+ * (A prefix need not end with a page: the other sequences' rows then list a page of
+ * their own there, with a copy of the prefix's end that is not read.)  A sequence
+ * whose new tokens do not all see its group's whole prefix (padding of the batch is
+ * one), and one that is alone in its group, is read through its own row.
+ *
+ * Starts that do not rise or lie outside [0, B] set the bounds bit of
+ * fa_device_error(), and no prefix is shared; so does a prefix length outside [0,
+ * max_pages * page_size], which counts as 0.  A page id outside [0, num_pages) masks
+ * that page's keys and sets the bit.  Slots at L and past it, and pages past a
+ * sequence's length, may hold anything (NaN included); the K/V of keys that some new
+ * token sees must be finite, as a non-finite V reaches the rows that do not see it
+ * too.
+ *
+ * Arithmetic, truncation of long sums and NaN scores as fa_decode_tree_fwd.  Lengths,
+ * groups and prefixes are never read on the host; equal calls give equal bits.
+ * Partials live in stream-ordered scratch.  Returns FA_ERR_UNSUPPORTED for more than
+ * 1024 groups, else as fa_decode_paged_fwd.
+ */
+int fa_decode_shared_fwd(const void* q, const void* kpages, const void* vpages,
+                         const int32_t* page_table, const int32_t* seqlens,
+                         const int32_t* group_starts, const int32_t* prefix_lens, void* o,
+                         float* lse, int B, int Sq, int Hq, int Hkv, int num_pages,
+                         int page_size, int max_pages, int groups, int D, float scale, int dtype,
+                         cudaStream_t stream);
+
+/*
+ * fa_sample -- the next token of every row of logits, from given random numbers.
+ *
+ *   logits       rows of V elements, bf16, fp16 or fp32 (dtype), row r at logits + r *
+ *                row_stride elements; row_stride >= V
+ *   uniforms     [rows] fp32 in [0, 1)
+ *   temperature  [rows] fp32, or NULL: 1.  Not above 0 (or NaN): greedy, the lowest
+ *                index of the largest logit
+ *   top_k        [rows] int32, or NULL; k < 1 or k >= V: off
+ *   top_p        [rows] fp32, or NULL; 1 and above, and NaN: off
+ *   min_p        [rows] fp32, or NULL; 0 and below, and NaN: off
+ *   tokens       [rows] int32, written
+ *   probs        NULL, or [rows, V] fp32, written: the distribution that the token is
+ *                drawn from (what fa_verify_tree takes), 0 for what is not kept
+ *
+ * Weights are w = exp((logit - largest) / T).  In the order of falling logits (equal
+ * ones by index), top-k keeps the first k tokens, top-p of those the ones before
+ * which less than top_p of their weight lies, min-p the ones with w >= min_p; at
+ * least one is kept.  The token is the lowest whose cumulative kept weight, by index,
+ * exceeds u times all of it.  Logits that are NaN count as -infinity; a row without
+ * any other gets the token -1 and probabilities 0.  Where logits are +infinity they
+ * share the weight.  Temperatures below 2^-100 count as that.
+ *
+ * Weights are good to about 2^-40 and summed as pairs of floats: the answers are
+ * those of 64-bit arithmetic except where u, or top_p, lies within about 2^-40 of a
+ * border.  Equal calls give equal bits.  FA_ERR_UNSUPPORTED where V passes what eight
+ * SMs hold: about 400000 fp32 logits, 800000 of 16 bits.
+ */
+int fa_sample(const void* logits, const float* uniforms, const float* temperature,
+              const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+              float* probs, int rows, int V, long long row_stride, int dtype,
+              cudaStream_t stream);
+
+/*
+ * fa_update_pages -- page table, free pages, slot map and positions from old and new
+ * lengths: what a step's scheduler does to a paged cache, on the device.
+ *
+ *   page_table     [B, max_pages] int32, updated in place
+ *   old_lens       [B] int32: tokens that each sequence holds
+ *   new_lens       [B] int32: tokens that it shall hold (0: it has ended)
+ *   shared_pages   [B] int32, or NULL (0): leading entries of the sequence's row that
+ *                  are not its own (a shared prefix): never taken, given back or given
+ *                  slots
+ *   free_pages     [max_free] int32, a stack of page ids, updated in place
+ *   free_count     [1] int32: how many of its entries are free, from the first on
+ *   lens_out       [B] int32, written: the lengths that hold now; may be old_lens or
+ *                  new_lens
+ *   free_count_out [1] int32, written; may be free_count
+ *   cu_new         [B + 1] int32, written: where each sequence's new tokens begin in
+ *   slots, positions  [max_new] int32, written: of every new token, sequence after
+ *                  sequence, its slot in the cache (page id * page_size + row) and its
+ *                  position in the sequence; -1 and 0 behind the last
+ *   page_size      a positive multiple of 32
+ *
+ * With pages(L) = max(ceil(L / page_size), shared) a sequence that shrinks gives back
+ * its table entries [pages(new), pages(old)): they go on top of the stack, in order of
+ * sequence and entry.  Then those that grow take entries [pages(old), pages(new)) from
+ * the top, in order.  A sequence that grows keeps its old length, and takes nothing, if
+ * the pages that it and all before it need are more than there are (unless it needs
+ * none), or if its new tokens and all before it are more than max_new: lens_out tells.
+ * Table entries that are not taken, and free pages behind the new count, keep what
+ * they held.
+ *
+ * A length outside [0, max_pages * page_size] or a shared count outside [0, max_pages]
+ * leaves its sequence as it was, a free count outside [0, max_free] or pages given back
+ * that pass max_free leave everything as it was; a page id whose slot would not be an
+ * int32 gives no slot.  Each sets the bounds bit of fa_device_error().  Returns
+ * FA_ERR_UNSUPPORTED for B > 4096.
+ */
+int fa_update_pages(int32_t* page_table, const int32_t* old_lens, const int32_t* new_lens,
+                    const int32_t* shared_pages, int32_t* free_pages, const int32_t* free_count,
+                    int32_t* lens_out, int32_t* free_count_out, int32_t* cu_new, int32_t* slots,
+                    int32_t* positions, int B, int page_size, int max_pages, int max_free,
+                    int max_new, cudaStream_t stream);
+
+/*
+ * fa_write_pages -- K and V rows of T packed tokens into the cache: token t's heads go
+ * to slot slots[t].
+ *
+ *   k, v             [T, Hkv, D], 16-bit elements; token t's heads start at k + t *
+ *                    k_stride elements; strides are multiples of 8, at least Hkv * D
+ *   kpages, vpages   [num_pages, page_size, Hkv, D]
+ *   slots            [T] int32, device (fa_update_pages'): page id * page_size + row;
+ *                    negative: the token is not written
+ *
+ * A slot past the last page is skipped and sets the bounds bit of fa_device_error().
+ * Two tokens must not share a slot.  page_size is a positive multiple of 32, D 64 or
+ * 128, num_pages * page_size below 2^31.
+ */
+int fa_write_pages(const void* k, const void* v, void* kpages, void* vpages,
+                   const int32_t* slots, long long T, int Hkv, int num_pages, int page_size,
+                   int D, long long k_stride, long long v_stride, cudaStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* fa_status_string(int status);
 
@@ -539,8 +679,8 @@ const char* fa_status_string(int status);
  * offsets or page ids out of range, or an index self-check), FA_ERR_CUDA if
  * the read itself failed.
  * If detail != NULL it receives the raw bits: the prefill (and backward) word
- * in bits 0-15, the decode word (also of the cache append, tree decode,
- * verification and compaction) in bits 16-31; in each, bit 0 = a wait timed out (bits 8-15:
+ * in bits 0-15, the decode word (also of the cache append, tree and shared decode,
+ * verification, compaction, page update and page writes) in bits 16-31; in each, bit 0 = a wait timed out (bits 8-15:
  * which wait), bit 1 = a bounds check fired.  Bounds bit with site 15: the
  * D = 128 backward dK/dV kernel found its dynamic shared memory too far from
  * a 1 KiB boundary to lay out its rings, and its CTAs left without work.
@@ -582,8 +722,8 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
 
 /*
  * fa_set_wait_limit_ns -- time limit of every device-side pipeline wait
- * (mbarrier waits of the prefill, decode, backward, norm and rotation and tree
- * decode kernels) on the current device; ns == 0 restores the default of 2 s.
+ * (mbarrier waits of the prefill, decode, backward, norm and rotation, tree and
+ * shared decode kernels) on the current device; ns == 0 restores the default of 2 s.
  *
  * A wait that runs past the limit makes its CTA abort: every warp leaves its
  * loop, the loads and MMAs already in flight are waited for (each such
@@ -594,12 +734,12 @@ int fa_prefill_rescale_count(int reset, unsigned long long* count);
  * watchdog, or in tests to make the timeout path run.
  *
  * Below 1 ms the limit is a watchdog: the decode kernels, the norm and rotation,
- * the tree decode's loads, and the dense
+ * the tree and shared decode's loads, and the dense
  * prefill (whose launches then use a polling instantiation of the kernel),
  * check it at every probe of every wait.  The packed-sequence prefill and the
  * backward kernels keep suspending probes of about 4 us each, so there a wait
  * trips the watchdog only once it has lasted about two of them (so too in the
- * tree decode's arithmetic).
+ * tree and shared decode's arithmetic).
  *
  * Synchronises the current device and applies to calls enqueued afterwards.
  * Returns FA_OK or FA_ERR_CUDA.
@@ -610,7 +750,7 @@ int fa_set_wait_limit_ns(unsigned long long ns);
  * fa_release_scratch -- gives the scratch memory that is kept for later calls on
  * the current device back to the driver.
  *
- * The tree decode and the norm and rotation's gradient take their stream-ordered
+ * The tree and shared decode and the norm and rotation's gradient take their stream-ordered
  * scratch from a memory pool of this library's, outside any framework's
  * allocator, which keeps up to 256 MiB per device of what calls have freed (the
  * device's default pool would give it back at every synchronisation, and the
