@@ -14,18 +14,27 @@
 // the prefix, below that the cache stream; own keys are always bound by the stream.
 //
 // Design: every (group, kv head) and every (sequence, kv head) is a unit of rows
-// against a range of 128-key tiles, done by tcgen05 MMAs as in the tree decode (S
-// and O in tensor memory, P written back over S).  A CTA has two softmax
-// warpgroups, one TMA producer warp and one MMA warp.  Units of more than 128 rows
-// give each warpgroup a 128-row tile, and both meet every key tile; with fewer rows
-// the warpgroups take alternate key tiles of the one row tile, each with sums of its
-// own, so that the softmax of one runs beside the other's.
-// Split: lengths, prefixes and groups are device data.  The tiles of all units form
-// one list, cut into equal ranges, one per CTA.  A unit of several row-tile pairs is
-// cut into strips of keys about as long as a range, and the pairs of one strip stand
-// side by side in the list, so that the CTAs which read the same keys do so at the
-// same time and share them through L2.  Every stretch of a range leaves a partial; a
-// second kernel merges a row's.
+// against a range of keys.
+//   Units of many rows (groups; sequences of more than 16 rows) are done by tcgen05
+//   MMAs against 128-key tiles as in the tree decode (S and O in tensor memory, P
+//   written back over S).  A CTA has two softmax warpgroups, one TMA producer warp and
+//   one MMA warp.  Units of more than 128 rows give each warpgroup a 128-row tile, and
+//   both meet every key tile; with fewer rows the warpgroups take alternate key tiles of
+//   the one row tile, each with sums of its own, so that the softmax of one runs beside
+//   the other's.
+//   Sequences of up to 16 rows are a stream of their own keys: each of six warps of a
+//   CTA streams a range of its own through two tiles of 32 keys in shared memory and
+//   multiplies by mma.sync (keys as M, rows as N).  No warp waits for another, so the
+//   ends of short ranges cost nothing but themselves.
+// Split: lengths, prefixes and groups are device data.  The units of either kind form a
+// list of tiles; the CTAs are shared out between the lists by what they cost, and a list
+// is cut into equal ranges, one per CTA (one per warp).  A unit of several row-tile
+// pairs whose keys are more than L2 keeps is cut into strips about as long as a range,
+// and the pairs of one strip stand side by side in the list, so that the CTAs which read
+// the same keys do so at the same time and share them through L2.  Every stretch of a
+// range leaves a partial; a second kernel merges a row's.  Every CTA makes the lists for
+// itself, from the lengths; in the first kind of CTA one warp walks its range and tells
+// the others stretch by stretch, ahead of them.
 #include <math.h>
 
 #include <type_traits>
@@ -41,10 +50,49 @@ __device__ unsigned int g_shared_err = 0;
 
 namespace sh {
 using namespace tiles;
-constexpr int MAX_GROUPS = 1024;  // their starts lie in shared memory
+constexpr int MAX_GROUPS = 1024;  // their starts and prefixes lie in shared memory
 constexpr int THREADS = 384;
 constexpr int WARPS = THREADS / 32;
-constexpr int SLACK = 4;  // places without a tile after each stretch, for what it costs beside
+constexpr int KEPT = THREADS;  // owners whose keys a CTA keeps in shared memory
+// Places that a 128-key tile takes in its list, so that equal ranges take equal times: one
+// that two row tiles meet (1.45 us), or one row tile in turns; and places without a tile
+// after each piece, for what a stretch costs beside its tiles.  A 32-key tile of a few
+// rows is one place of the other list.
+constexpr int COST_TWO = 3, COST_ONE = 3, SLACK = 4, SLACK_FEW = 2;
+constexpr int FEW = 16;       // rows that a warp streams keys for
+constexpr int FEW_WARPS = 6;  // such warps of a CTA
+constexpr int FEW_KEYS = 32;  // keys of their tiles
+// What a place of either list costs, for the sharing out of the CTAs.
+constexpr int SHARE_MANY = 4, SHARE_FEW = 1, SHARE_FEW2 = 3;  // (up to 8 rows, up to 16)
+constexpr int RING = 4;        // stretches told ahead
+constexpr long long L2_KEEPS = 48 << 20;  // bytes of a unit's K/V, over all kv heads
+
+// A stretch of one unit's tiles.
+struct Seg {
+  int kind;      // 0 group, 1 sequence, -1 the end
+  int hkv;
+  int r0, rows;  // first query row within the unit, rows: up to 256
+  int t, n;      // first tile, tiles
+  int id;        // partial
+  int lo, hi;    // keys [lo, hi)
+  int row0;      // first sequence
+  int tab;       // sequence whose row of the page table lists the keys
+  int twice;     // other rows meet the same keys: worth keeping in L2
+};
+
+// What every CTA finds out about the list, in shared memory.
+struct Plan {
+  long long sums[2 * WARPS];
+  long long x, hi;  // this CTA's range of places
+  long long first;  // first place of owner o
+  int o, piece0;    // owner; pieces of its kind before it
+  int W, slack, groups;
+  int range, few;   // this CTA's (first) range; whether its warps stream
+  int used;         // ranges of the streaming warps
+  long long total[2];
+  int lo[KEPT], end[KEPT], tab[KEPT], len[KEPT];
+  int starts[MAX_GROUPS + 1], prefix[MAX_GROUPS];
+};
 
 template <int D>
 struct Cfg {
@@ -53,15 +101,36 @@ struct Cfg {
   static constexpr int NSTAGE = D == 128 ? 4 : 10;  // K and V tiles in flight
   static constexpr int SMEM_Q = 2 * TILE_BYTES;
   static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
-  static constexpr int SMEM_BAR = 512, SMEM_PLAN = 256;
-  static constexpr int SMEM_STARTS = (MAX_GROUPS + 4) * 4;
-  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV + SMEM_BAR + SMEM_PLAN + SMEM_STARTS;
+  static constexpr int SMEM_BAR = 512, SMEM_RING = FEW_WARPS * 288;  // (told stretches)
+  static_assert(RING * 64 <= SMEM_RING, "a ring, or a walk per streaming warp");
+  static_assert(sizeof(Seg) <= 64 && alignof(Seg) <= 64, "a stretch's slot");
+  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV +
+                                    SMEM_BAR + SMEM_RING + (int)sizeof(Plan);
   static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
   static_assert(NSTAGE / 2 + 2 < BAD_RING, "tiles in flight");
+  // Streaming warps: two tiles each, K and V.
+  static constexpr int FEW_HALF = FEW_KEYS * 128, FEW_KV = HALVES * FEW_HALF;
+  static_assert(FEW_WARPS * 4 * FEW_KV <= SMEM_Q + SMEM_KV, "streaming warps' tiles");
   // Tensor memory: S of each warpgroup, then O of each.
   static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
 };
 }  // namespace sh
+
+// Owners of units: group g is owner g, sequence b owner groups + b.  What the merge
+// knows of them.
+struct __align__(16) SharedOwner {
+  long long first;  // first place
+  int piece0;       // pieces of its kind before it
+  int lo, hi;       // keys [lo, hi)
+  int row0, rows;   // first sequence, query rows per kv head
+  int group;        // of a sequence that its group's unit covers, else -1
+};
+// ... and of the list.
+struct SharedList {
+  long long total[2];   // places of the two kinds' lists
+  int used[2];          // ranges of each
+  int W, slack[2];
+};
 
 struct SharedParams {
   const void* q;  // [B, Sq, Hq, D]
@@ -75,32 +144,72 @@ struct SharedParams {
   // unnormalised outputs, [id][2 * half][2] (max in log2 units, sum).
   float* part_o[2];
   float* part_ml[2];
-  int half[2];         // rows of a warpgroup in a slot
-  long long* first;    // [owners + 1] first place of each owner, then strip width, slack
-  int* pieces;         // [owners] pieces of the owners of its kind before it
+  int half[2];  // rows of a warpgroup in a slot
+  int few;      // sequences are streamed by warps; their partials: [id][SqG][D], [id][SqG][2]
+  SharedOwner* owner;  // [groups + B]
+  SharedList* list;
   int B, groups, Sq, Hq, Hkv, G, SqG;
   int page_size, max_pages, num_pages, box, ctas;
+  long long keep_tiles;  // tiles of a unit, all kv heads, that L2 keeps
   float c;  // scale * log2(e)
 };
 
+// The kernel's roles run different code side by side, and what does not fit the
+// instruction caches is fetched again and again (with everything inlined, 228 KB, a
+// stretch of one tile took 5 us): what is long and not in a loop over tiles is called.
+
 // a / b in 32 bits where both fit.
+__device__ __forceinline__ long long long_quotient(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : long_quotient(a, b);
 }
 
-// Owners of units: group g is owner g, sequence b owner groups + b.
-struct Shape {
-  int rows;        // query rows per kv head
-  int row0;        // first sequence
-  int tab;         // sequence whose row of the page table lists the keys
-  int lo, hi;      // keys [lo, hi)
-  int t0, T;       // first tile and tiles
-  int n_rt;        // pairs of row tiles
-  int S, len;      // strips, tiles of each but the last
-};
-__device__ __forceinline__ long long places_per_head(const Shape& s, int slack) {
-  return (long long)s.n_rt * (s.T + (long long)s.S * slack);
+// A pipeline wait of the warps beside the softmax's: the first probe here, the rest called.
+// (The softmax warps' registers leave no room for calls.)
+template <bool POLL>
+__device__ __forceinline__ bool long_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       unsigned site) {
+  return mbar_wait<POLL>(bar, parity, abort_flag, &g_shared_err, site);
 }
+template <bool POLL>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         unsigned site) {
+  const uint32_t a = smem_u32(bar);
+  if (POLL ? mbar_test_wait(a, parity) : mbar_try_wait(a, parity)) return true;
+  return long_wait<POLL>(bar, parity, abort_flag, site);
+}
+
+// A unit's tiles.
+struct Shape {
+  int t0, T;   // first tile and tiles
+  int n_rt;    // pairs of row tiles
+  int cost;    // places of a tile
+  int S, len;  // strips, tiles of each but the last
+};
+__device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int rows, int lo, int hi,
+                                          int W) {
+  Shape s;
+  const int keys = few ? sh::FEW_KEYS : sh::BN;
+  s.t0 = lo / keys;
+  s.T = hi > lo ? (int)(((uint32_t)hi + keys - 1) / keys) - s.t0 : 0;
+  s.n_rt = (rows + 2 * sh::BM - 1) / (2 * sh::BM);
+  s.cost = few ? 1 : (rows > sh::BM ? sh::COST_TWO : sh::COST_ONE);
+  s.S = 1;
+  s.len = s.T;
+  if (s.n_rt > 1 && (long long)s.T * p.Hkv > p.keep_tiles && s.T > W) {
+    const uint32_t S = ((uint32_t)s.T + W / 2) / (uint32_t)W;
+    s.len = (int)(((uint32_t)s.T + S - 1) / S);
+    s.S = (s.T + s.len - 1) / s.len;
+  }
+  return s;
+}
+__device__ __forceinline__ long long places_per_head(const Shape& s, int slack) {
+  return s.T > 0 ? (long long)s.n_rt * ((long long)s.T * s.cost + (long long)s.S * slack) : 0;
+}
+__device__ __forceinline__ long long pieces_of(const SharedParams& p, const Shape& s) {
+  return s.T > 0 ? (long long)p.Hkv * s.S * s.n_rt : 0;
+}
+
 __device__ __forceinline__ long long shared_cap(const SharedParams& p) {
   return (long long)p.max_pages * p.page_size;
 }
@@ -108,119 +217,344 @@ __device__ __forceinline__ int shared_len(const SharedParams& p, int b) {
   const int L = p.seqlens[b];
   return L < 0 ? 0 : (L > shared_cap(p) ? (int)shared_cap(p) : L);
 }
+__device__ __forceinline__ int kept_len(const SharedParams& p, const sh::Plan* pl, int b) {
+  return b < sh::KEPT ? pl->len[b] : shared_len(p, b);
+}
 // Tokens that group g shares: 0 for fewer than two members.
-__device__ __forceinline__ int group_prefix(const SharedParams& p, const int* starts, int g) {
-  if (starts[g + 1] - starts[g] < 2) return 0;
-  const int P = p.prefix[g];
+__device__ __forceinline__ int group_prefix(const SharedParams& p, const sh::Plan* pl, int g) {
+  if (pl->starts[g + 1] - pl->starts[g] < 2) return 0;
+  const int P = pl->prefix[g];
   return P < 0 || P > shared_cap(p) ? 0 : P;
 }
-// The group of sequence b, or -1.  groups: 0 where the starts are not sound.
-__device__ __forceinline__ int group_of(const int* starts, int groups, int b) {
-  if (groups == 0 || b < starts[0] || b >= starts[groups]) return -1;
-  int lo = 0, hi = groups;  // starts[lo] <= b < starts[hi]
+// The group of sequence b, or -1.
+__device__ __forceinline__ int group_of(const sh::Plan* pl, int b) {
+  if (pl->groups == 0 || b < pl->starts[0] || b >= pl->starts[pl->groups]) return -1;
+  int lo = 0, hi = pl->groups;  // starts[lo] <= b < starts[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (starts[mid] <= b)
+    if (pl->starts[mid] <= b)
       lo = mid;
     else
       hi = mid;
   }
   return lo;
 }
-// Keys of sequence b that its group's unit covers: all of the prefix, or none for a
-// sequence that is not past it.
-__device__ __forceinline__ int covered(const SharedParams& p, const int* starts, int groups,
-                                       int b, int L) {
-  const int g = group_of(starts, groups, b);
-  if (g < 0) return 0;
-  const int P = group_prefix(p, starts, g);
-  return L - p.Sq + 1 >= P ? P : 0;
-}
-// W: tiles of a CTA's range, 0 while it is not known.
-__device__ __forceinline__ Shape shape_of(const SharedParams& p, const int* starts, int groups,
-                                          int o, int W) {
-  Shape s;
+// An owner's rows and keys: a group's prefix, read through the first member that is
+// past it (none: no keys); of a sequence what its group's unit does not cover: the
+// keys behind the prefix, or all of one that is not past it.
+struct Keys {
+  int lo, hi, tab, row0, rows, group;
+};
+__device__ __forceinline__ Keys keys_of(const SharedParams& p, const sh::Plan* pl, int o) {
+  Keys k;
   if (o < p.groups) {
-    const bool real = o < groups;
-    s.lo = 0;
-    s.hi = real ? group_prefix(p, starts, o) : 0;
-    s.row0 = real ? starts[o] : 0;
-    s.rows = real ? (starts[o + 1] - starts[o]) * p.SqG : 0;
-    // The first member that is past the prefix; without one there is nothing to do.
-    s.tab = s.row0;
-    if (s.hi > 0) {
-      while (s.tab < starts[o + 1] && shared_len(p, s.tab) - p.Sq + 1 < s.hi) ++s.tab;
-      if (s.tab == starts[o + 1]) s.hi = 0;
+    const bool real = o < pl->groups;
+    k.lo = 0;
+    k.hi = real ? group_prefix(p, pl, o) : 0;
+    k.row0 = real ? pl->starts[o] : 0;
+    k.rows = real ? (pl->starts[o + 1] - pl->starts[o]) * p.SqG : 0;
+    k.tab = k.row0;
+    k.group = -1;
+    if (k.hi > 0) {
+      while (k.tab < pl->starts[o + 1] && kept_len(p, pl, k.tab) - p.Sq + 1 < k.hi) ++k.tab;
+      if (k.tab == pl->starts[o + 1]) k.hi = 0;
     }
   } else {
-    const int b = o - p.groups, L = shared_len(p, b);
-    s.row0 = s.tab = b;
-    s.rows = p.SqG;
-    s.hi = L;
-    s.lo = covered(p, starts, groups, b, L);
+    const int b = o - p.groups;
+    k.row0 = k.tab = b;
+    k.rows = p.SqG;
+    k.hi = kept_len(p, pl, b);
+    k.lo = 0;
+    k.group = group_of(pl, b);
+    if (k.group >= 0) {
+      const int P = group_prefix(p, pl, k.group);
+      if (k.hi - p.Sq + 1 >= P) k.lo = P;
+    }
+    if (k.lo == 0) k.group = -1;
   }
-  s.t0 = s.lo / sh::BN;
-  s.T = s.hi > s.lo ? (int)(((uint32_t)s.hi + sh::BN - 1) / sh::BN) - s.t0 : 0;
-  s.n_rt = (s.rows + 2 * sh::BM - 1) / (2 * sh::BM);
-  s.S = W > 0 ? max(1, s.T / W) : 1;
-  s.len = (s.T + s.S - 1) / s.S;
-  s.S = s.len > 0 ? (s.T + s.len - 1) / s.len : 1;
-  return s;
+  return k;
 }
 
-// A CTA's place in the list.
+// Inclusive sums of a and b over the block, and the totals.
+__device__ __forceinline__ void block_sums(long long& a, long long& b, long long* sums,
+                                           long long* ta, long long* tb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += x;
+      b += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    sums[2 * warp] = a;
+    sums[2 * warp + 1] = b;
+  }
+  __syncthreads();
+  // Every warp adds the warps' totals up for itself.
+  long long x = lane < sh::WARPS ? sums[2 * lane] : 0, y = lane < sh::WARPS ? sums[2 * lane + 1] : 0;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  *ta = __shfl_sync(0xffffffffu, x, sh::WARPS - 1);
+  *tb = __shfl_sync(0xffffffffu, y, sh::WARPS - 1);
+  const long long pa = __shfl_sync(0xffffffffu, x, warp ? warp - 1 : 0),
+                  pb = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+  if (warp) {
+    a += pa;
+    b += pb;
+  }
+}
+
+// Block-wide: the list, and this CTA's range of it, into *pl.  CTA 0 also writes it
+// down for the merge.
+__device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl) {
+  const int t = threadIdx.x;
+  const int owners = p.groups + p.B;
+  if (t == 0) {
+    pl->o = -1;
+    pl->groups = p.groups;
+  }
+  // Starts, prefixes and lengths at once.
+  for (int b = t; b < p.B && b < sh::KEPT; b += sh::THREADS) pl->len[b] = shared_len(p, b);
+  bool odd = false, far = false;
+  for (int i = t; p.groups > 0 && i <= p.groups; i += sh::THREADS) {
+    const int s = p.starts[i];
+    odd |= s < 0 || s > p.B || (i > 0 && s < p.starts[i - 1]);
+    pl->starts[i] = s;
+    if (i < p.groups) {
+      const int P = p.prefix[i];
+      far |= P < 0 || P > shared_cap(p);
+      pl->prefix[i] = P;
+    }
+  }
+  odd = __syncthreads_or(odd);
+  if (odd) {
+    if (t == 0) pl->groups = 0;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && (far || (odd && t == 0))) atomicOr(&g_shared_err, kErrBounds);
+  // Places of the tiles in the lists: of the groups, and of the sequences where warps
+  // stream them, else all in the first.
+  auto few = [&](int o) { return p.few && o >= p.groups; };
+  auto pieces_at = [&](int o, const Shape& s) {
+    return o < p.groups ? pieces_of(p, s) << 32 : pieces_of(p, s);
+  };
+  Keys mine = {};  // of this thread's first owner
+  long long tiles[2] = {0, 0}, all_tiles[2];
+  for (int o = t; o < owners; o += sh::THREADS) {
+    const Keys k = keys_of(p, pl, o);
+    if (o == t) {
+      mine = k;
+      pl->lo[o] = k.lo;
+      pl->end[o] = k.hi;
+      pl->tab[o] = k.tab;
+    }
+    const Shape s = shape_of(p, few(o), k.rows, k.lo, k.hi, INT32_MAX);
+    tiles[few(o)] += (long long)p.Hkv * s.n_rt * s.T * s.cost;
+  }
+  block_sums(tiles[0], tiles[1], pl->sums, &all_tiles[0], &all_tiles[1]);
+  const int n = p.ctas;
+  // CTAs of the first kind, for lists of a and z places.
+  const int share_few = p.SqG <= 8 ? sh::SHARE_FEW : sh::SHARE_FEW2;
+  auto share = [&](long long a, long long z) {
+    if (a == 0) return 0;
+    if (z == 0) return n;
+    const long long x = quotient(a * n * sh::SHARE_MANY + z * share_few / 2,
+                                 a * sh::SHARE_MANY + z * share_few);
+    return max(1, min(n - 1, (int)x));
+  };
+  const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1])) * sh::COST_TWO;
+  const long long width = quotient(all_tiles[0] + per - 1, per);
+  const int W = width < 1 ? 1 : (width > INT32_MAX ? INT32_MAX : (int)width);
+  const int slack[2] = {all_tiles[0] > (long long)n * sh::COST_TWO ? sh::SLACK : 0,
+                        all_tiles[1] > (long long)n * sh::FEW_WARPS ? sh::SLACK_FEW : 0};
+  auto places_at = [&](int o, const Keys& k) {
+    return p.Hkv * places_per_head(shape_of(p, few(o), k.rows, k.lo, k.hi, W), slack[few(o)]);
+  };
+  // Sums of places and pieces (groups' in the upper half) up to each owner; with an owner
+  // per thread they are those of the list, else they are made again chunk by chunk.
+  const bool one = owners <= sh::THREADS;
+  long long total[2], my_places = 0, my_pieces = 0, sum_places, sum_pieces, all_pieces = 0;
+  if (one) {
+    if (t < owners) {
+      my_places = places_at(t, mine);
+      my_pieces = pieces_at(t, shape_of(p, few(t), mine.rows, mine.lo, mine.hi, W));
+    }
+    sum_places = my_places;
+    sum_pieces = my_pieces;
+    if (t == 0) pl->total[0] = 0;
+    block_sums(sum_places, sum_pieces, pl->sums, &total[1], &all_pieces);
+    if (t == p.groups - 1) pl->total[0] = sum_places;
+    __syncthreads();
+    total[0] = p.few ? pl->total[0] : total[1];
+    total[1] -= total[0];
+  } else {
+    long long a = 0, z = 0;
+    for (int o = t; o < owners; o += sh::THREADS) {
+      const long long x = places_at(o, o == t ? mine : keys_of(p, pl, o));
+      if (few(o))
+        z += x;
+      else
+        a += x;
+    }
+    block_sums(a, z, pl->sums, &total[0], &total[1]);
+  }
+  // CTAs of either kind by what their lists cost; where the first has about as many pieces
+  // as CTAs, one each: then the pairs of a strip meet the same keys at the same time.
+  // Ranges in use are each as long as a tile at least, so that every one of them between
+  // the first and the last of a piece holds a tile of it.
+  int many = share(total[0], total[1]);
+  const long long pieces = (all_pieces >> 32) + (p.few ? 0 : all_pieces & 0xffffffffll);
+  if (pieces <= (total[1] > 0 ? n - 1 : n) && 8 * (pieces > many ? pieces - many : many - pieces) <= many)
+    many = (int)pieces;
+  const long long most = quotient(total[0], sh::COST_TWO);
+  const int used[2] = {most < 1 ? 1 : (int)min(most, (long long)max(many, 1)),
+                       (int)max(1ll, min(total[1], (long long)(n - many) * sh::FEW_WARPS))};
+  const int kind = (int)blockIdx.x >= many;
+  const int range = kind ? ((int)blockIdx.x - many) * sh::FEW_WARPS : (int)blockIdx.x;
+  const long long base = kind ? total[0] : 0;
+  const bool in_use = range < used[kind] && total[kind] > 0;
+  const long long x = in_use ? base + quotient(total[kind] * range, used[kind]) : 0;
+  const long long hi = in_use ? base + quotient(total[kind] * (range + 1), used[kind]) : 0;
+  long long places0 = 0, pieces0 = 0;
+  for (int o0 = 0; o0 < owners; o0 += sh::THREADS) {
+    const int o = o0 + t;
+    Keys k = mine;
+    long long end_places = 0, end_pieces = 0;
+    if (!one) {
+      if (o0 > 0 && o < owners) k = keys_of(p, pl, o);
+      my_places = my_pieces = 0;
+      if (o < owners) {
+        my_places = places_at(o, k);
+        my_pieces = pieces_at(o, shape_of(p, few(o), k.rows, k.lo, k.hi, W));
+      }
+      sum_places = my_places;
+      sum_pieces = my_pieces;
+      block_sums(sum_places, sum_pieces, pl->sums, &end_places, &end_pieces);
+    }
+    const long long first = places0 + sum_places - my_places, before = pieces0 + sum_pieces - my_pieces;
+    const int piece0 = (int)(o < p.groups ? before >> 32 : before & 0xffffffffll);
+    if (o < owners) {
+      if (first <= x && x < first + my_places && x < hi) {
+        pl->o = o;
+        pl->first = first;
+        pl->piece0 = piece0;
+      }
+      if (blockIdx.x == 0)
+        p.owner[o] = SharedOwner{first - (few(o) ? total[0] : 0), piece0, k.lo, k.hi, k.row0, k.rows,
+                                 k.group};
+    }
+    places0 += end_places;
+    pieces0 += end_pieces;
+    if (blockIdx.x != 0 && places0 > x) break;  // (block-uniform)
+  }
+  if (t == 0) {
+    pl->x = x;
+    pl->hi = hi;
+    pl->W = W;
+    pl->slack = slack[kind];
+    pl->range = range;
+    pl->few = kind;
+    pl->used = used[1];
+    pl->total[0] = total[0];
+    pl->total[1] = total[1];
+    if (blockIdx.x == 0)
+      *p.list = SharedList{{total[0], total[1]}, {used[0], used[1]}, W, {slack[0], slack[1]}};
+  }
+  __syncthreads();
+}
+
+// The stretches of a CTA's range, one after another.
 struct SharedWalk {
-  long long x, hi;  // next and last place of the range
-  long long first;  // first place of owner o
-  int o, piece0;    // owner; pieces of its kind before it
-  int W, slack, groups;
+  long long x, hi, first;
+  int o, piece0;
+  Keys k;
   Shape s;
 };
-struct SharedSeg {
-  int kind;  // 0 group, 1 sequence
-  int hkv, rt, t, n, id;
-};
-
-__device__ __forceinline__ bool shared_next(const SharedParams& p, const int* starts,
-                                            SharedWalk& w, SharedSeg* g) {
-  int s, rt, at, len;
+__device__ __forceinline__ void walk_owner(const SharedParams& p, const sh::Plan* pl, SharedWalk& w) {
+  if (w.o < sh::KEPT) {
+    w.k.lo = pl->lo[w.o];
+    w.k.hi = pl->end[w.o];
+    w.k.tab = pl->tab[w.o];
+    const bool seq = w.o >= p.groups;
+    w.k.row0 = seq ? w.o - p.groups : (w.o < pl->groups ? pl->starts[w.o] : 0);
+    w.k.rows = seq ? p.SqG : (w.o < pl->groups ? (pl->starts[w.o + 1] - pl->starts[w.o]) * p.SqG : 0);
+  } else {
+    w.k = keys_of(p, pl, w.o);
+  }
+  w.s = shape_of(p, pl->few, w.k.rows, w.k.lo, w.k.hi, pl->W);
+}
+__device__ __forceinline__ SharedWalk walk_start(const SharedParams& p, const sh::Plan* pl) {
+  SharedWalk w = {};
+  w.o = pl->o;
+  if (w.o < 0) return w;  // (x = hi: no stretch)
+  w.x = pl->x;
+  w.hi = pl->hi;
+  w.first = pl->first;
+  w.piece0 = pl->piece0;
+  walk_owner(p, pl, w);
+  return w;
+}
+__device__ __forceinline__ bool walk_next(const SharedParams& p, const sh::Plan* pl, SharedWalk& w,
+                                          int range, sh::Seg* g) {
+  int s, rt, at, n;
   for (;;) {
     if (w.x >= w.hi) return false;
-    long long per = places_per_head(w.s, w.slack);
-    while (w.x >= w.first + per * p.Hkv || w.s.T == 0) {
-      if (w.s.T > 0) {
-        w.first += per * p.Hkv;
-        w.piece0 += p.Hkv * w.s.S * w.s.n_rt;
-      }
+    long long per = places_per_head(w.s, pl->slack);
+    while (w.x >= w.first + per * p.Hkv) {
+      w.first += per * p.Hkv;
+      w.piece0 += (int)pieces_of(p, w.s);
       if (++w.o >= p.groups + p.B) return false;  // (the range ends at the list's end)
       if (w.o == p.groups) w.piece0 = 0;
-      w.s = shape_of(p, starts, w.groups, w.o, w.W);
-      per = places_per_head(w.s, w.slack);
+      walk_owner(p, pl, w);
+      per = places_per_head(w.s, pl->slack);
     }
     long long y = w.x - w.first;
     g->hkv = (int)quotient(y, per);
     y -= g->hkv * per;
-    const long long strip = (long long)w.s.n_rt * (w.s.len + w.slack);
+    const long long strip = (long long)w.s.n_rt * ((long long)w.s.len * w.s.cost + pl->slack);
     s = (int)quotient(y, strip);
-    const long long z = y - s * strip;
-    len = min(w.s.len, w.s.T - s * w.s.len);
-    rt = (int)quotient(z, len + w.slack);
-    at = (int)(z - (long long)rt * (len + w.slack));
-    if (at < len) break;
-    w.x += len + w.slack - at;  // slack
+    y -= s * strip;
+    const int len = min(w.s.len, w.s.T - s * w.s.len);
+    const long long piece = (long long)len * w.s.cost + pl->slack;
+    rt = (int)quotient(y, piece);
+    y -= rt * piece;
+    // Tiles whose first place lies in the range.
+    const long long begin = w.x - y;
+    at = (int)quotient(y + w.s.cost - 1, w.s.cost);
+    if (at < len) {
+      const long long end = quotient(w.hi - begin + w.s.cost - 1, w.s.cost);
+      n = (int)(end < len ? end : len) - at;
+      w.x = begin + (long long)(at + n) * w.s.cost;
+      if (n <= 0) return false;
+      break;
+    }
+    w.x = begin + piece;  // slack
   }
-  const long long left = w.hi - w.x;
   g->kind = w.o < p.groups ? 0 : 1;
-  g->rt = rt;
+  g->r0 = rt * 2 * sh::BM;
+  g->rows = min(2 * sh::BM, w.k.rows - g->r0);
   g->t = w.s.t0 + s * w.s.len + at;
-  g->n = len - at < left ? len - at : (int)left;
+  g->n = n;
   // Stretches in list order: each begins a piece or a CTA's range.
-  g->id = w.piece0 + (g->hkv * w.s.S + s) * w.s.n_rt + rt + (int)blockIdx.x;
-  w.x += g->n;
+  g->id = w.piece0 + (g->hkv * w.s.S + s) * w.s.n_rt + rt + range;
+  g->lo = w.k.lo;
+  g->hi = w.k.hi;
+  g->row0 = w.k.row0;
+  g->tab = w.k.tab;
+  g->twice = w.s.n_rt > 1;
   return true;
 }
 
-// Query row r of a unit: its index in [B, Sq, Hq].
+// Query row r of a unit: its index in [B, Sq, Hq], and its new token.
 __device__ __forceinline__ size_t shared_qrow(const SharedParams& p, int row0, int hkv, int r,
                                               int* s_out) {
   const int m = r / p.SqG, e = r - m * p.SqG, s = e / p.G;
@@ -228,148 +562,311 @@ __device__ __forceinline__ size_t shared_qrow(const SharedParams& p, int row0, i
   return ((size_t)(row0 + m) * p.Sq + s) * p.Hq + (size_t)hkv * p.G + (e - s * p.G);
 }
 
-// Block-wide: the list, and this CTA's range of it.  starts: shared memory for the
-// groups' starts; plan: shared scratch.  CTA 0 also writes it down for the merge.
-struct PlanScratch {
-  long long sums[2 * sh::WARPS];
-  long long first;
-  int o, piece0, sound;
-};
-__device__ __forceinline__ SharedWalk shared_plan(const SharedParams& p, int* starts,
-                                                  PlanScratch* sc) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int owners = p.groups + p.B;
-  if (t == 0) {
-    sc->sound = 1;
-    sc->o = -1;
-  }
-  for (int i = t; i <= p.groups && p.groups > 0; i += sh::THREADS) starts[i] = p.starts[i];
-  __syncthreads();
-  if (p.groups > 0) {
-    bool odd = false, far = false;
-    for (int i = t; i <= p.groups; i += sh::THREADS) {
-      odd |= starts[i] < 0 || starts[i] > p.B || (i > 0 && starts[i] < starts[i - 1]);
-      if (blockIdx.x == 0 && i < p.groups) far |= p.prefix[i] < 0 || p.prefix[i] > shared_cap(p);
-    }
-    if (odd) sc->sound = 0;
-    if ((odd && blockIdx.x == 0) || far) atomicOr(&g_shared_err, kErrBounds);
-    __syncthreads();
-  }
-  SharedWalk w;
-  w.groups = sc->sound ? p.groups : 0;
-  // Inclusive sums over the block, and totals.
-  auto scan = [&](long long& a, long long& b, long long* ta, long long* tb) {
+// The MMAs' steps of 16 along the contracted axis.  Addresses in units of 16 bytes.
+// D (tensor memory at d) = A B^T, both with D elements per row in 128-byte rows, half
+// after half (A's halves HALF_BYTES apart).
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t b_half,
+                                        uint32_t hi, uint32_t idesc) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-      if (lane >= o) {
-        a += x;
-        b += y;
+  for (int k = 0; k < D / 16; ++k)
+    mma_ss_lh(d, a + (((k >> 2) * sh::HALF_BYTES + (k & 3) * 32) >> 4), hi,
+              b + (k >> 2) * b_half + (k & 3) * 2, hi, idesc, k > 0 ? 1u : 0u);
+}
+// (+)= P (tensor memory) V.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint32_t v, uint32_t hi,
+                                        uint32_t idesc, bool add) {
+#pragma unroll
+  for (int k = 0; k < sh::BN / 16; ++k)
+    mma_ts_lh(d, p + k * 8, v + (uint32_t)((k * 16 * 128) >> 4), hi, idesc,
+              add || k > 0 ? 1u : 0u);
+}
+// A warp's rows (up to 8 NB, as the MMAs' N) against its stretch of keys.  Lane (g, tq)
+// = (lane / 4, lane % 4) holds, of row block nb, rows 8 nb + 2 tq + {0, 1}, and of O^T
+// the elements 16 dm + g (+ 8).
+template <int D, int NB>
+struct StreamRows {
+  uint32_t q[NB][D / 16][2];
+  float m[NB][2], l[NB][2], acc[NB][D / 16][4];
+};
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    mma_fp16_16816(d, a, b0, b1);
+  else
+    mma_bf16_16816(d, a, b0, b1);
+}
+// One tile of 32 keys: S^T = K Q^T (A = K rows by ldmatrix, B = Q from registers), an
+// online softmax, O^T += V^T P^T (A = V by transposing ldmatrix, B = P^T, the scores'
+// accumulator transposed per 8 x 8).  Keys [from, to) of the tile count; lim: of them the
+// rows' own limits.
+template <int D, int NB, typename T>
+__device__ __forceinline__ void stream_tile(StreamRows<D, NB>& w, uint32_t k_tile, uint32_t v_tile,
+                                            float c, bool masked, int from, int to,
+                                            const int (&lim)[NB][2]) {
+  constexpr int MB = sh::FEW_KEYS / 16, HALF = sh::FEW_KEYS * 128;
+  constexpr float NEG_INF = -INFINITY;
+  const int lane = threadIdx.x & 31, g = lane >> 2, mi = lane >> 3;
+  float sc[NB][MB][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) sc[nb][mb][0] = sc[nb][mb][1] = sc[nb][mb][2] = sc[nb][mb][3] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {  // (independent sums side by side)
+      const int tok = mb * 16 + (mi & 1) * 8 + (lane & 7), chunk = kk * 2 + (mi >> 1);
+      uint32_t a[4];
+      ldsm_x4(k_tile + (chunk >> 3) * HALF + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4), a[0], a[1],
+              a[2], a[3]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_16816<T>(sc[nb][mb], a, w.q[nb][kk][0], w.q[nb][kk][1]);
+    }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tl = mb * 16 + g + (i >> 1) * 8;
+        sc[nb][mb][i] *= c;
+        if (masked && (tl < from || tl >= to || tl >= lim[nb][i & 1])) sc[nb][mb][i] = NEG_INF;
+      }
+  uint32_t pb[NB][MB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float f[2], base[2], rs[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float mx = NEG_INF;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) mx = fmaxf(mx, fmaxf(sc[nb][mb][e], sc[nb][mb][2 + e]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float top = fmaxf(w.m[nb][e], mx);
+      base[e] = top == NEG_INF ? 0.f : top;
+      f[e] = fast_exp2(w.m[nb][e] - base[e]);
+      w.m[nb][e] = top;
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[nb][mb][i] = fast_exp2(sc[nb][mb][i] - base[i & 1]);
+        rs[i & 1] += sc[nb][mb][i];
+      }
+      pb[nb][mb][0] = movmatrix_trans(TileType<T>::pack(sc[nb][mb][0], sc[nb][mb][1]));
+      pb[nb][mb][1] = movmatrix_trans(TileType<T>::pack(sc[nb][mb][2], sc[nb][mb][3]));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w.l[nb][e] = w.l[nb][e] * f[e] + rs[e];
+    // (Mostly no row has a new maximum: the products stay as they are.)
+    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+      for (int dm = 0; dm < D / 16; ++dm) {
+        w.acc[nb][dm][0] *= f[0];
+        w.acc[nb][dm][1] *= f[1];
+        w.acc[nb][dm][2] *= f[0];
+        w.acc[nb][dm][3] *= f[1];
       }
     }
-    __syncthreads();
-    if (lane == 31) {
-      sc->sums[2 * warp] = a;
-      sc->sums[2 * warp + 1] = b;
+  }
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int dm = 0; dm < D / 16; ++dm) {
+      const int tok = mb * 16 + (mi >> 1) * 8 + (lane & 7), chunk = dm * 2 + (mi & 1);
+      uint32_t a[4];
+      ldsm_x4_t(v_tile + (chunk >> 3) * HALF + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4), a[0], a[1],
+                a[2], a[3]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_16816<T>(w.acc[nb][dm], a, pb[nb][mb][0], pb[nb][mb][1]);
     }
-    __syncthreads();
-    *ta = *tb = 0;
-    for (int i = 0; i < sh::WARPS; ++i) {
-      if (i == warp) {
-        a += *ta;
-        b += *tb;
+}
+
+// A streaming warp's walk, in shared memory (its registers hold its rows): the walk, and
+// the stretches begun, of which the loads are two tiles ahead of the arithmetic.
+struct StreamWalk {
+  SharedWalk w;
+  sh::Seg told[4];
+};
+static_assert(sizeof(StreamWalk) <= 288, "a streaming warp's walk");
+
+// One warp's range of the sequences' list, from its loads to its partials.  tiles: two
+// of K and V each; full: their barriers.  The loads run two tiles ahead of the
+// arithmetic, over the ends of stretches.
+template <int D, typename T, int NB>
+__device__ __forceinline__ void stream_keys(const SharedParams& p, const sh::Plan* pl,
+                                            const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                            uint8_t* tiles, uint64_t* full, StreamWalk* sw, int warp,
+                                            volatile int* abort_flag) {
+  using C = sh::Cfg<D>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int range = pl->range + warp;
+  if (range >= pl->used || pl->o < 0) return;
+  if (lane == 0) {
+    sw->w = walk_start(p, pl);
+    sw->w.x = pl->total[0] + quotient(pl->total[1] * range, pl->used);
+    sw->w.hi = pl->total[0] + quotient(pl->total[1] * (range + 1), pl->used);
+  }
+  const uint64_t pol = l2_policy_evict_first();
+  // The loading side: the next tile of its stretch and that one's tiles, 32 pages of the row.
+  int ld_at = 0, ld_n = 0, ld_tab = -1, ids_base = 0, ids = -1;
+  bool ld_more = true;
+  uint32_t loaded = 0, used = 0, seg_ld = 0, seg = 0;  // tiles, stretches begun
+  uint32_t bad_bits = 0;  // of the tile in either buffer: it has no page
+  // The side that computes: the next tile of its stretch, its rows.
+  int at = 0;
+  StreamRows<D, NB> r;
+  int lim0[NB][2];
+  bool ok = true;
+  for (;;) {
+    while (ld_more && loaded - used < 2) {
+      if (ld_at == ld_n) {
+        ld_at = 0;
+        if (lane == 0) {
+          sh::Seg next;
+          if (!walk_next(p, pl, sw->w, range, &next)) next.kind = -1;
+          sw->told[seg_ld & 3] = next;
+        }
+        __syncwarp();
+        if (!(ld_more = sw->told[seg_ld & 3].kind >= 0)) break;
+        ld_n = sw->told[seg_ld & 3].n;
+        ++seg_ld;
       }
-      *ta += sc->sums[2 * i];
-      *tb += sc->sums[2 * i + 1];
+      const sh::Seg& ld = sw->told[(seg_ld - 1) & 3];
+      const int buf = loaded & 1;
+      const int key = (ld.t + ld_at) * sh::FEW_KEYS, page = key / p.page_size;
+      const int row = key - page * p.page_size;
+      if (ld.tab != ld_tab || page < ids_base || page >= ids_base + 32) {
+        ld_tab = ld.tab;
+        ids_base = page;
+        ids = page + lane < p.max_pages
+                  ? p.page_table[(size_t)ld.tab * p.max_pages + page + lane]
+                  : -1;
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, page - ids_base);
+      const bool bad = id < 0 || id >= p.num_pages;
+      bad_bits = (bad_bits & ~(1u << buf)) | (uint32_t)bad << buf;
+      if (lane == 0) {
+        if (bad) {
+          atomicOr(&g_shared_err, kErrBounds);
+          mbar_arrive(&full[buf]);
+        } else {
+          mbar_arrive_expect_tx(&full[buf], 2 * C::FEW_KV);
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h) {
+            uint8_t* const dst = tiles + buf * 2 * C::FEW_KV + h * C::FEW_HALF;
+            tma_load_4d_hint(dst, tmK, &full[buf], h * 64, ld.hkv, row, id, pol);
+            tma_load_4d_hint(dst + C::FEW_KV, tmV, &full[buf], h * 64, ld.hkv, row, id, pol);
+          }
+        }
+      }
+      __syncwarp();
+      ++loaded;
+      ++ld_at;
     }
-  };
-  long long raw = 0, total = 0, unused;
-  Shape mine;  // of this thread's first owner
-  for (int o = t; o < owners; o += sh::THREADS) {
-    const Shape s = shape_of(p, starts, w.groups, o, 0);
-    if (o == t) mine = s;
-    raw += (long long)p.Hkv * s.n_rt * s.T;
-  }
-  long long zero = 0, sum;
-  scan(raw, zero, &sum, &unused);
-  const long long n = p.ctas;
-  const long long width = quotient(sum + n - 1, n);
-  w.W = width < 1 ? 1 : (width > INT32_MAX ? INT32_MAX : (int)width);
-  w.slack = sum > n ? sh::SLACK : 0;
-  auto strips = [&](Shape s) {
-    s.S = max(1, s.T / w.W);
-    s.len = (s.T + s.S - 1) / s.S;
-    s.S = s.len > 0 ? (s.T + s.len - 1) / s.len : 1;
-    return s;
-  };
-  for (int o = t; o < owners; o += sh::THREADS) {
-    const Shape s = strips(o == t ? mine : shape_of(p, starts, w.groups, o, 0));
-    if (s.T > 0) total += p.Hkv * places_per_head(s, w.slack);
-  }
-  zero = 0;
-  scan(total, zero, &sum, &unused);
-  const long long used = sum < n ? sum : n, c = blockIdx.x;
-  w.x = c < used ? mul_div(sum, (int)c, used) : 0;
-  w.hi = c < used ? mul_div(sum, (int)c + 1, used) : 0;
-  if (c >= used && c > 0) return w;  // (block-uniform)
-  long long places0 = 0, pieces0 = 0;  // pieces: groups' in the upper half, sequences' in the lower
-  for (int o0 = 0; o0 < owners; o0 += sh::THREADS) {
-    const int o = o0 + t;
-    long long places = 0, pieces = 0, my_places = 0, my_pieces = 0, all_places, all_pieces;
-    if (o < owners) {
-      const Shape s = strips(o == t ? mine : shape_of(p, starts, w.groups, o, 0));
-      if (s.T > 0) {
-        my_places = p.Hkv * places_per_head(s, w.slack);
-        my_pieces = (long long)p.Hkv * s.S * s.n_rt;
-        if (o < p.groups) my_pieces <<= 32;
+    if (used == loaded) break;
+    if (at == 0) ++seg;
+    const sh::Seg& sg = sw->told[(seg - 1) & 3];
+    if (at == 0) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        int s;
+        const int row = nb * 8 + g;
+        const bool real = row < p.SqG;
+        const uint32_t* const src = reinterpret_cast<const uint32_t*>(
+            static_cast<const T*>(p.q) + shared_qrow(p, sg.row0, sg.hkv, real ? row : 0, &s) * D);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          r.q[nb][kk][0] = real ? src[kk * 8 + tq] : 0u;
+          r.q[nb][kk][1] = real ? src[kk * 8 + 4 + tq] : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // The row of new token s sees the keys below L - Sq + s + 1.
+          const int mine = nb * 8 + 2 * tq + e;
+          lim0[nb][e] = sg.hi - p.Sq + 1 + (mine < p.SqG ? mine / p.G : 0);
+          r.m[nb][e] = -INFINITY;
+          r.l[nb][e] = 0.f;
+        }
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm)
+          r.acc[nb][dm][0] = r.acc[nb][dm][1] = r.acc[nb][dm][2] = r.acc[nb][dm][3] = 0.f;
       }
     }
-    places = my_places;
-    pieces = my_pieces;
-    scan(places, pieces, &all_places, &all_pieces);
-    const long long first = places0 + places - my_places, before = pieces0 + pieces - my_pieces;
-    const int piece0 = o < p.groups ? (int)(before >> 32) : (int)before;
-    if (o < owners) {
-      if (my_places > 0 && first <= w.x && w.x < first + my_places && w.x < w.hi) {
-        sc->o = o;
-        sc->first = first;
-        sc->piece0 = piece0;
+    const int buf = used & 1;
+    if (!(ok = mbar_wait<true>(&full[buf], (used >> 1) & 1, abort_flag, &g_shared_err, 16))) break;
+    __syncwarp();
+    uint8_t* const tile = tiles + buf * 2 * C::FEW_KV;
+    const int key0 = (sg.t + at) * sh::FEW_KEYS;
+    const int from = bad_bits >> buf & 1 ? sh::FEW_KEYS : max(sg.lo - key0, 0);
+    const int to = min(sg.hi - key0, sh::FEW_KEYS);
+    const bool masked = from > 0 || key0 + sh::FEW_KEYS > sg.hi - p.Sq + 1;
+    if (from > 0 || to < sh::FEW_KEYS) {
+      // Rows of keys that nobody sees can hold anything: they are cleared, since 0 *
+      // NaN in P V would reach every row.
+      for (int x = lane; x < 2 * C::HALVES * sh::FEW_KEYS * 8; x += 32) {
+        const int key = x >> 3 & (sh::FEW_KEYS - 1);
+        if (key < from || key >= to)
+          *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
-      if (blockIdx.x == 0) {
-        p.first[o] = first;
-        p.pieces[o] = piece0;
-      }
+      __syncwarp();
     }
-    places0 += all_places;
-    pieces0 += all_pieces;
-    if (blockIdx.x != 0 && places0 > w.x) break;  // (block-uniform)
+    int lim[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[nb][e] = lim0[nb][e] - key0;
+    const uint32_t k_tile = smem_u32(tile);
+    stream_tile<D, NB, T>(r, k_tile, k_tile + C::FEW_KV, p.c, masked, from, to, lim);
+    // The buffer's reads are done before the copy unit writes it again.
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    ++used;
+    if (++at < sg.n) continue;
+    at = 0;
+    // The lanes' parts of each row's sum, and the rows' partials.
+    const size_t slot = (size_t)sg.id * p.SqG;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = r.l[nb][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int row = nb * 8 + 2 * tq + e;
+        if (row < p.SqG) {
+          if (g == 0)
+            reinterpret_cast<float2*>(p.part_ml[1])[slot + row] = make_float2(r.m[nb][e], l);
+          float* const dst = p.part_o[1] + (slot + row) * D;
+#pragma unroll
+          for (int dm = 0; dm < D / 16; ++dm) {
+            dst[dm * 16 + g] = r.acc[nb][dm][e];
+            dst[dm * 16 + g + 8] = r.acc[nb][dm][2 + e];
+          }
+        }
+      }
   }
-  if (blockIdx.x == 0 && t == 0) {
-    p.first[owners] = places0;
-    p.first[owners + 1] = w.W;
-    p.first[owners + 2] = w.slack;
-    p.first[owners + 3] = w.groups;
-  }
-  __syncthreads();
-  w.o = sc->o;
-  w.first = sc->first;
-  w.piece0 = sc->piece0;
-  if (w.o < 0) {
-    w.hi = w.x;
-    return w;
-  }
-  w.s = shape_of(p, starts, w.groups, w.o, w.W);
-  return w;
+  // After an abort: the loads that may still be in flight, before shared memory goes.
+  if (!ok)
+    for (uint32_t u = used; u < loaded; ++u) mbar_wait_drain(&full[u & 1], (u >> 1) & 1);
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(sh::THREADS, 1)
     shared_split_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmK32,
+                        const __grid_constant__ CUtensorMap tmV32,
                         const __grid_constant__ SharedParams p) {
   using C = sh::Cfg<D>;
   constexpr int NSTAGE = C::NSTAGE;
-  constexpr int W_PROD = 8, W_MMA = 9;
+  constexpr int W_PROD = 8, W_MMA = 9, W_WALK = 10;
   constexpr bool kBF16 = TileType<T>::kBF16;
   constexpr float NEG_INF = -INFINITY;
   extern __shared__ uint8_t smem_raw[];
@@ -384,14 +881,16 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   uint64_t* p_full = s_full + 2;   // [2]
   uint64_t* pv_done = p_full + 2;  // [2] a stretch's last P V of each warpgroup
   uint64_t* drain = pv_done + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* told = drain + 1;       // [RING] a stretch stands in its slot
+  uint64_t* heard = told + sh::RING;  // [RING] all warps have read it
+  uint64_t* few_full = heard + sh::RING;  // [FEW_WARPS][2] a streaming warp's tiles
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(few_full + 2 * sh::FEW_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);
   volatile uint32_t* tile_bad = issued + 1;  // [BAD_RING]
-  static_assert(2 * C::NSTAGE * 8 + 9 * 8 + 12 + 4 * sh::BAD_RING <= C::SMEM_BAR, "barrier block");
-  PlanScratch* scratch = reinterpret_cast<PlanScratch*>(sKV + C::SMEM_KV + C::SMEM_BAR);
-  int* starts = reinterpret_cast<int*>(sKV + C::SMEM_KV + C::SMEM_BAR + C::SMEM_PLAN);
-  static_assert(sizeof(PlanScratch) <= C::SMEM_PLAN, "plan scratch");
+  static_assert(2 * C::NSTAGE * 8 + (9 + 2 * sh::RING + 2 * sh::FEW_WARPS) * 8 + 12 + 4 * sh::BAD_RING <= C::SMEM_BAR, "barrier block");
+  uint8_t* const s_ring = reinterpret_cast<uint8_t*>(full) + C::SMEM_BAR;  // stretches told
+  sh::Plan* const plan = reinterpret_cast<sh::Plan*>(s_ring + C::SMEM_RING);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -412,6 +911,11 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 2 * sh::FEW_WARPS; ++i) mbar_init(&few_full[i], 1);
+    for (int i = 0; i < sh::RING; ++i) {
+      mbar_init(&told[i], 1);
+      mbar_init(&heard[i], 10);  // producer, MMA issuer, eight softmax warps
+    }
     *abort_flag = 0;
     *issued = 0;
     fence_mbar_init();
@@ -426,11 +930,37 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   const uint32_t tmem = *tmem_holder;
   pdl_wait_primary();  // everything below reads or writes the caller's memory
 
-  SharedWalk w = shared_plan(p, starts, scratch);
-  SharedSeg sg = {};
-  // Rows of a stretch, and whether they make two row tiles.
-  auto rows_of = [&](const SharedSeg& g) {
-    return min(2 * sh::BM, w.s.rows - g.rt * 2 * sh::BM);
+  shared_plan(p, plan);
+  if (plan->few) {
+    if (warp < sh::FEW_WARPS) {
+      uint8_t* const tiles = sQ + warp * 4 * C::FEW_KV;
+      if (p.SqG <= 8)
+        stream_keys<D, T, 1>(p, plan, &tmK32, &tmV32, tiles, few_full + 2 * warp,
+                              reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
+      else
+        stream_keys<D, T, 2>(p, plan, &tmK32, &tmV32, tiles, few_full + 2 * warp,
+                              reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
+    }
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
+  // The k-th stretch of this CTA; false at the end, and where a wait gave up (*ok).
+  uint32_t seg = 0;
+  sh::Seg sg;
+  auto next_seg = [&](bool* ok, auto softmax) {
+    const int slot = seg % sh::RING;
+    const uint32_t par = (seg / sh::RING) & 1;
+    if constexpr (softmax.value)
+      *ok = mbar_wait<false>(&told[slot], par, abort_flag, &g_shared_err, 13);
+    else
+      *ok = wait_for<true>(&told[slot], par, abort_flag, 13);
+    if (!*ok) return false;
+    sg = *reinterpret_cast<const sh::Seg*>(s_ring + slot * 64);
+    if (warp != W_MMA) __syncwarp();  // (there one lane alone listens)
+    if (lane == 0) mbar_arrive(&heard[slot]);
+    ++seg;
+    return sg.kind >= 0;
   };
   if (warp >= W_PROD) {
     regs_decrease<88>();
@@ -443,10 +973,10 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
       uint32_t tc = 0;  // tiles so far: K at ring position 2 tc, V at 2 tc + 1
       bool ok = true;
-      while (ok && shared_next(p, starts, w, &sg)) {
-        const int32_t* table = p.page_table + (size_t)w.s.tab * p.max_pages;
-        const int end = w.s.hi;
-        const uint64_t pol = w.s.n_rt == 1 ? once : again;
+      while (ok && next_seg(&ok, std::false_type{})) {
+        const int32_t* table = p.page_table + (size_t)sg.tab * p.max_pages;
+        const int end = sg.hi;
+        const uint64_t pol = sg.twice ? again : once;
         // Page of this lane's box in tile t (-1: nothing to load, -2: no such
         // page) and the row in it.
         auto page_of = [&](int t, int* pos) {
@@ -470,8 +1000,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
           if (lane == 0) *issued = cnt + 1;
         };
         auto slot_free = [&](uint32_t cnt) {
-          return mbar_wait<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag,
-                                 &g_shared_err, 1);
+          return wait_for<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag, 1);
         };
         // Pages are looked up two tiles ahead.
         int pos = 0, pos_n = 0, pos_nn = 0;
@@ -504,46 +1033,36 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         const uint64_t dv = sdesc_sw128(smem_u32(sKV), sh::HALF_BYTES, 1024);
         const uint32_t sd_hi = (uint32_t)(dq >> 32);
         const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
-        // S[buf] = Q[tile] K^T, over D / 16 steps.
+        // S[buf] = Q[tile] K^T.
         auto issue_s = [&](int tile, int buf, uint32_t cnt) {
-          const uint32_t a0 = q_lo + tile * (C::TILE_BYTES >> 4);
-          const uint32_t b0 = k_lo + (cnt % NSTAGE) * (C::TILE_BYTES >> 4);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * sh::HALF_BYTES + (k & 3) * 32) >> 4;
-            mma_ss_lh(tmem + C::COL_S + buf * 128, a0 + off, sd_hi, b0 + off, sd_hi, IDESC_S,
-                      k > 0 ? 1u : 0u);
-          }
+          mma_scores<D>(tmem + C::COL_S + buf * 128, q_lo + tile * (C::TILE_BYTES >> 4),
+                        k_lo + (cnt % NSTAGE) * (C::TILE_BYTES >> 4), sh::HALF_BYTES >> 4, sd_hi,
+                        IDESC_S);
           mma_commit(&s_full[buf]);
         };
-        // O[i] (+)= P[i] V, over 128 / 16 steps.
+        // O[i] (+)= P[i] V.
         auto issue_pv = [&](int i, uint32_t cnt, bool add) {
-          const uint32_t b0 = v_lo + (cnt % NSTAGE) * (C::TILE_BYTES >> 4);
-#pragma unroll
-          for (int k = 0; k < sh::BN / 16; ++k)
-            mma_ts_lh(tmem + C::COL_O + i * D, tmem + C::COL_S + i * 128 + k * 8,
-                      b0 + (uint32_t)((k * 16 * 128) >> 4), sd_hi, IDESC_O, add || k > 0 ? 1u : 0u);
+          mma_values(tmem + C::COL_O + i * D, tmem + C::COL_S + i * 128,
+                     v_lo + (cnt % NSTAGE) * (C::TILE_BYTES >> 4), sd_hi, IDESC_O, add);
         };
-        uint32_t tc = 0, seg = 0, cw[2] = {0, 0};
+        uint32_t tc = 0, cw[2] = {0, 0};
         bool ok = true;
         auto landed = [&](uint32_t cnt, unsigned site) {
-          ok = mbar_wait<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, &g_shared_err,
-                                site);
+          ok = wait_for<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, site);
           tc_fence_after();
           return ok;
         };
         auto p_ready = [&](int i, uint32_t n) {
-          ok = mbar_wait<false>(&p_full[i], n & 1, abort_flag, &g_shared_err, 6 + i);
+          ok = wait_for<false>(&p_full[i], n & 1, abort_flag, 6 + i);
           tc_fence_after();
           return ok;
         };
-        while (ok && shared_next(p, starts, w, &sg)) {
+        while (ok && next_seg(&ok, std::false_type{})) {
           const int n = sg.n;
-          if (!(ok = mbar_wait<false>(q_full, seg & 1, abort_flag, &g_shared_err, 2))) break;
-          ++seg;
+          if (!(ok = wait_for<false>(q_full, (seg - 1) & 1, abort_flag, 2))) break;
           tc_fence_after();
           if (!landed(2 * tc, 3)) break;
-          if (rows_of(sg) > sh::BM) {  // two row tiles on every key tile
+          if (sg.rows > sh::BM) {  // two row tiles on every key tile
             issue_s(0, 0, 2 * tc);
             issue_s(1, 1, 2 * tc);
             mma_commit(&empty[(2 * tc) % NSTAGE]);
@@ -607,6 +1126,19 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         mbar_wait_drain(drain, 0);
       }
       __syncwarp();
+    } else if (warp == W_WALK && lane == 0) {
+      // ============================ the walk over the range ============================
+      SharedWalk w = walk_start(p, plan);
+      for (uint32_t k = 0;; ++k) {
+        const int slot = k % sh::RING;
+        sh::Seg g;
+        if (!walk_next(p, plan, w, plan->range, &g)) g.kind = -1;
+        if (!wait_for<true>(&heard[slot], ((k / sh::RING) & 1) ^ 1, abort_flag, 14))
+          break;
+        *reinterpret_cast<sh::Seg*>(s_ring + slot * 64) = g;
+        mbar_arrive(&told[slot]);
+        if (g.kind < 0) break;
+      }
     }
   } else {
     regs_increase<208>();
@@ -617,112 +1149,142 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
     const uint32_t tS = t_lane + C::COL_S + i * 128, tO = t_lane + C::COL_O + i * D;
     const float c = p.c;
     const float hide = c < 0.f ? -NEG_INF : NEG_INF;
-    uint32_t tc = 0, cw = 0, done = 0, seg = 0;
+    uint32_t tc = 0, cw = 0, done = 0;
     bool ok = true;
     // This thread's row of Q for a stretch (one row tile: the first warpgroup's).
-    auto load_q = [&](const SharedSeg& g) {
-      const int rows = rows_of(g), rr = i * sh::BM + tid;
-      if (rows > sh::BM || i == 0) {
+    auto load_q = [&] {
+      const int rr = i * sh::BM + tid;
+      if (sg.rows > sh::BM || i == 0) {
+        // The warp's 32 rows one after another, a row by D / 8 lanes.
         int s;
-        const bool real = rr < rows;
-        const size_t qrow = real ? shared_qrow(p, w.s.row0, g.hkv, g.rt * 2 * sh::BM + rr, &s) : 0;
-        put_q_row<D>(sQ + i * C::TILE_BYTES, tid, static_cast<const T*>(p.q) + qrow * D, real);
+        const bool real = rr < sg.rows;
+        const int qrow = real ? (int)shared_qrow(p, sg.row0, sg.hkv, sg.r0 + rr, &s) : -1;
+        constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+        const int x = lane % LANES;
+        uint4 v[32 / AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < 32 / AT_ONCE; ++k) {
+          const int from = __shfl_sync(0xffffffffu, qrow, k * AT_ONCE + lane / LANES);
+          v[k] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (size_t)max(from, 0) * D)[x];
+          if (from < 0) v[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint8_t* const dst = sQ + i * C::TILE_BYTES + (x >> 3) * sh::HALF_BYTES;
+#pragma unroll
+        for (int k = 0; k < 32 / AT_ONCE; ++k) {
+          const int row = wq * 32 + k * AT_ONCE + lane / LANES;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v[k];
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);
     };
-    bool have = shared_next(p, starts, w, &sg);
-    if (have) load_q(sg);
+    bool have = next_seg(&ok, std::true_type{});
+    if (have) load_q();
     while (have) {
-      const int rows = rows_of(sg), n = sg.n;
+      const int rows = sg.rows, n = sg.n, r0 = sg.r0;
       const bool dual = rows > sh::BM;
       const int kind = sg.kind;
       const int rr = dual ? i * sh::BM + tid : tid;
       const bool row_ok = rr < rows, warp_ok = rr - lane < rows;
-      const int lo = w.s.lo, end = w.s.hi;
-      // Keys [lo, lim) are this row's, [lo, end) somebody's; all rows see those below least.
-      int lim = end, least = end;
-      if (kind == 1) {
-        int s = 0;
-        if (row_ok) shared_qrow(p, 0, 0, sg.rt * 2 * sh::BM + rr, &s);
-        least = end - p.Sq + 1;
-        lim = least + s;
-      }
-      float m_used = NEG_INF, l = 0.f;
-      for (int j = dual ? 0 : i; j < n; j += dual ? 1 : 2) {
+      // Keys [lo, end) are somebody's; all rows see those of them below least.
+      const int lo = sg.lo, end = sg.hi, t0 = sg.t;
+      const int least = kind == 1 ? end - p.Sq + 1 : end;
+      const int half = dual ? sh::BM : p.half[kind];
+      float* const po = p.part_o[kind] + ((size_t)sg.id * (D / 4) * 2 * p.half[kind] + i * half) * 4;
+      float2* const pml = reinterpret_cast<float2*>(p.part_ml[kind]) +
+                          (size_t)sg.id * 2 * p.half[kind] + i * half + tid;
+      const size_t col = 2 * (size_t)p.half[kind];  // rows of four columns
+      // S of the j-th tile is there; V rows that no query sees are cleared (they can hold
+      // anything, and 0 * NaN in P V would reach every row).  The tile's first key and
+      // missing pages; whether some row does not see all of it.
+      int kv0 = 0;
+      uint32_t bad = 0;
+      bool masked = false;
+      auto tile_ready = [&](int j) {
         const uint32_t tj = tc + j;
-        if (!(ok = mbar_wait<false>(&s_full[i], cw & 1, abort_flag, &g_shared_err, 8 + i))) break;
+        ok = mbar_wait<false>(&s_full[i], cw & 1, abort_flag, &g_shared_err, 8 + i);
+        if (!ok) return false;
         ++cw;
         __syncwarp();
         tc_fence_after();
-        const int kv0 = (sg.t + j) * sh::BN;
-        const uint32_t bad = tile_bad[tj % sh::BAD_RING];
-        const bool masked = kv0 < lo || kv0 > least - sh::BN || bad;
+        kv0 = (t0 + j) * sh::BN;
+        bad = tile_bad[tj % sh::BAD_RING];
+        masked = kv0 < lo || kv0 > least - sh::BN || bad;
         if (masked) {
-          // V rows that no query sees can hold anything: they are cleared, since 0 *
-          // NaN in P V would reach every row.
           const Mask128 fine = sound_keys(bad, p.box);
           const uint32_t cv = 2 * tj + 1;
-          if (!(ok = mbar_wait<false>(&full[cv % NSTAGE], (cv / NSTAGE) & 1, abort_flag,
-                                      &g_shared_err, 10)))
-            break;
-          clear_rows<D>(sKV + (cv % NSTAGE) * C::TILE_BYTES, wq, lane,
-                        Mask128{fine.lo & low_bits(end - kv0) & ~low_bits(lo - kv0),
-                                fine.hi & low_bits(end - kv0 - 64) & ~low_bits(lo - kv0 - 64)});
+          ok = mbar_wait<false>(&full[cv % NSTAGE], (cv / NSTAGE) & 1, abort_flag, &g_shared_err, 10);
+          if (ok)
+            clear_rows<D>(sKV + (cv % NSTAGE) * C::TILE_BYTES, wq, lane,
+                          Mask128{fine.lo & low_bits(end - kv0) & ~low_bits(lo - kv0),
+                                  fine.hi & low_bits(end - kv0 - 64) & ~low_bits(lo - kv0 - 64)});
+        }
+        return ok;
+      };
+      // After the last tile: Q of the next stretch, then P V of this one.  False: leave.
+      const bool active = dual || i < n;
+      auto move_on = [&] {
+        tc += n;
+        have = false;
+        if (ok) have = next_seg(&ok, std::true_type{});
+        // (seg counts the next stretch by now.)
+        if (have) ok = mbar_wait<false>(q_free, seg & 1, abort_flag, &g_shared_err, 11);
+        if (!ok) return false;
+        if (have) load_q();
+        if (!active) return true;
+        ok = mbar_wait<false>(&pv_done[i], done & 1, abort_flag, &g_shared_err, 12);
+        if (!ok) return false;
+        ++done;
+        __syncwarp();
+        tc_fence_after();
+        return true;
+      };
+      {
+        int lim = end;  // this row sees the keys [lo, lim)
+        if (kind == 1) {
+          int s = 0;
+          if (row_ok) shared_qrow(p, 0, 0, r0 + rr, &s);
+          lim = least + s;
+        }
+        float m_used = NEG_INF, l = 0.f;
+        for (int j = dual ? 0 : i; j < n; j += dual ? 1 : 2) {
+          if (!tile_ready(j)) break;
+          if (warp_ok) {
+            auto mask = [&](uint32_t (&sr)[4][32]) {
+              const Mask128 fine = sound_keys(bad, p.box);
+              hide_keys(sr,
+                        Mask128{fine.lo & low_bits(lim - kv0) & ~low_bits(lo - kv0),
+                                fine.hi & low_bits(lim - kv0 - 64) & ~low_bits(lo - kv0 - 64)},
+                        hide);
+            };
+            // (S of this tile was issued after P V of this warpgroup's last: both are done.)
+            auto settled = [] { return true; };
+            softmax_tile<D, T>(tS, tO, c, j < (dual ? 1 : 2), masked, mask, settled, &m_used, &l);
+          }
+          tc_fence_before();
+          mbar_arrive(&p_full[i]);
+        }
+        if (!move_on()) break;
+        if (!active) {
+          if (row_ok) *pml = make_float2(NEG_INF, 0.f);
+          continue;
         }
         if (warp_ok) {
-          auto mask = [&](uint32_t (&sr)[4][32]) {
-            const Mask128 fine = sound_keys(bad, p.box);
-            hide_keys(sr,
-                      Mask128{fine.lo & low_bits(lim - kv0) & ~low_bits(lo - kv0),
-                              fine.hi & low_bits(lim - kv0 - 64) & ~low_bits(lo - kv0 - 64)},
-                      hide);
-          };
-          // (S of this tile was issued after P V of this warpgroup's last: both are done.)
-          auto settled = [] { return true; };
-          softmax_tile<D, T>(tS, tO, c, j < (dual ? 1 : 2), masked, mask, settled, &m_used, &l);
-        }
-        tc_fence_before();
-        mbar_arrive(&p_full[i]);
-      }
-      if (!ok) break;
-      tc += n;
-      const bool active = dual || i < n;
-      const int half = dual ? sh::BM : p.half[kind];
-      const size_t slot = (size_t)sg.id * 2 * p.half[kind] + i * half + tid;
-      float4* const po = reinterpret_cast<float4*>(p.part_o[kind]) +
-                         (size_t)sg.id * (D / 4) * 2 * p.half[kind] + i * half + tid;
-      float2* const pml = reinterpret_cast<float2*>(p.part_ml[kind]) + slot;
-      const size_t col = 2 * (size_t)p.half[kind];
-      have = shared_next(p, starts, w, &sg);
-      if (have) {
-        if (!(ok = mbar_wait<false>(q_free, seg & 1, abort_flag, &g_shared_err, 11))) break;
-        load_q(sg);
-      }
-      ++seg;
-      if (!active) {
-        if (row_ok) *pml = make_float2(NEG_INF, 0.f);
-        continue;
-      }
-      if (!(ok = mbar_wait<false>(&pv_done[i], done & 1, abort_flag, &g_shared_err, 12))) break;
-      ++done;
-      __syncwarp();
-      tc_fence_after();
-      if (warp_ok) {
-        if (row_ok) *pml = make_float2(m_used, l);
+          if (row_ok) *pml = make_float2(m_used, l);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(tO + q * 32, o);
-          tmem_wait_ld();
-          reg_fence32(o);
-          if (!row_ok) continue;
-          // [column / 4][row] of 16 bytes: the lanes' rows side by side.
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + q * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+            if (!row_ok) continue;
+            // [column / 4][row] of 16 bytes: the lanes' rows side by side.
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            po[(q * 8 + x) * col] =
-                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                            __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(po + ((q * 8 + x) * col + tid) * 4) =
+                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+          }
         }
       }
       tc_fence_before();
@@ -745,154 +1307,153 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   }
 }
 
-// Merge: a thread takes 16 columns of a row, the lanes of a warp 32 rows of one kv
-// head, so that loads are as wide as the split kernel's stores.  A row has the
-// partials of its group's unit and of its own, walked strip by strip, the next
-// partial's loads ahead of this one's sums.  KS = 1: a thread walks all of them.
-// KS = 8: the block's 8 warps share one set of 32 rows x 16 columns, each every 8th
-// strip.
-constexpr int kJoinWarps = 8;
-template <int D, typename T, int KS>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    shared_merge_kernel(const __grid_constant__ SharedParams p) {
+// Merge: a block takes up to THREADS * 4 / D rows of one (sequence, kv head).  Its first warp
+// lists where their partials are, of the group's unit and of their own (the lanes take
+// strips); then a thread takes four columns of a row and walks the list, six partials'
+// loads at a time.  With fewer rows, the threads of a row's columns share the list.
+namespace join {
+constexpr int LIST = 2048;  // partials of a row from one unit: two per CTA and strip, one per warp
+}  // namespace join
+template <int D, typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) shared_merge_kernel(
+    const __grid_constant__ SharedParams p) {
+  constexpr int RC = THREADS * 4 / D;  // rows of a block
+  static_assert(RC <= 32, "a row's threads in one warp");
+  // Lists: of the group's unit for the rows' first and last pair of row tiles; their own.
+  __shared__ int s_list[3][join::LIST];
+  __shared__ int s_count[3];
+  __shared__ int s_group[2];  // first sequence of the group, or -1; its first such pair
   pdl_launch_dependents();
+  const int t = threadIdx.x, lane = t & 31;
+  const int chunks = (p.SqG + RC - 1) / RC, unit = blockIdx.x / chunks;
+  const int first = (blockIdx.x - unit * chunks) * RC, rows = min(RC, p.SqG - first);
+  const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
   pdl_wait_primary();
-  constexpr int NC = D / 16;  // column chunks of a row
-  __shared__ float sM[KS > 1 ? KS : 1][32], sDen[KS > 1 ? KS : 1][32];
-  __shared__ float sAcc[KS > 1 ? KS : 1][16][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int all_rows = p.B * p.SqG, sets = (all_rows + 31) / 32;
-  int x, chunk;
-  if constexpr (KS == 1) {
-    x = blockIdx.x * (kJoinWarps / NC) + warp / NC;
-    chunk = warp % NC;
-    if (x >= sets * p.Hkv) return;
-  } else {
-    x = blockIdx.x / NC;
-    chunk = blockIdx.x - x * NC;
+  if (t < 96) {  // a warp for each list
+    const SharedList list = *p.list;
+    const SharedOwner own = p.owner[p.groups + b];
+    SharedOwner grp = own;
+    if (own.group >= 0) grp = p.owner[own.group];
+    const int r0 = (b - grp.row0) * p.SqG + first;  // of the group's unit
+    const int l = t >> 5;
+    if (t == 0) {
+      s_group[0] = own.group >= 0 ? grp.row0 : -1;
+      s_group[1] = r0 / (2 * sh::BM);
+    }
+    if (lane == 0) s_count[l] = 0;
+    // The range that holds place y: the largest c with total * c / used <= y.
+    auto cta_of = [&](long long y, int k) {
+      return (int)quotient((y + 1) * list.used[k] - 1, list.total[k]);
+    };
+    // (The rows' first and last pair are mostly the same one.)
+    if (l == 2 || (own.group >= 0 && (l == 0 || (r0 + rows - 1) / (2 * sh::BM) != r0 / (2 * sh::BM)))) {
+      const SharedOwner o = l < 2 ? grp : own;
+      const int rt = (l == 0 ? r0 : l == 1 ? r0 + rows - 1 : first) / (2 * sh::BM);
+      const int few = p.few && l == 2;
+      const Shape s = shape_of(p, few, o.rows, o.lo, o.hi, list.W);
+      const int slack = list.slack[few];
+      const bool two = few || min(2 * sh::BM, o.rows - rt * 2 * sh::BM) > sh::BM;
+      const long long head = o.first + hkv * places_per_head(s, slack);
+      int n = 0;
+      for (int k0 = 0; s.T > 0 && k0 < s.S; k0 += 32) {
+        const int k = k0 + lane;
+        int c0 = 0, count = 0;
+        if (k < s.S) {
+          const int len = min(s.len, s.T - k * s.len);
+          const long long piece = (long long)len * s.cost + slack;
+          const long long y =
+              head + (long long)k * s.n_rt * ((long long)s.len * s.cost + slack) + rt * piece;
+          // (A tile belongs to the range that holds its first place.)
+          c0 = cta_of(y, few);
+          count = (cta_of(y + (long long)(len - 1) * s.cost, few) - c0 + 1) << (two ? 0 : 1);
+        }
+        int inc = count;
+#pragma unroll
+        for (int o2 = 1; o2 < 32; o2 <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o2);
+          if (lane >= o2) inc += x;
+        }
+        // (One row tile: two partials of each CTA, one behind the other.)
+        const int id = o.piece0 + (hkv * s.S + k) * s.n_rt + rt + c0;
+        for (int e = 0; e < count; ++e) {
+          const int at = n + inc - count + e;
+          if (at < join::LIST) s_list[l][at] = two ? 2 * (id + e) : 2 * id + e;
+        }
+        n += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) s_count[l] = min(n, join::LIST);
+      if (n > join::LIST && lane == 0) atomicOr(&g_shared_err, kErrBounds);
+    }
   }
-  const int hkv = x / sets, R = (x - hkv * sets) * 32 + lane;
-  const bool real = R < all_rows;
-  const int owners = p.groups + p.B;
-  const long long total = p.first[owners];
-  const int W = (int)p.first[owners + 1], slack = (int)p.first[owners + 2],
-            groups = (int)p.first[owners + 3];
-  const long long ctas = total < p.ctas ? total : p.ctas;
-  float M = -INFINITY, den = 0.f, acc[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  // The partial whose loads are under way.
-  float2 ml = make_float2(-INFINITY, 0.f);
-  float4 ov[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) ov[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto join = [&](float2 a, const float4 (&v)[4]) {
+  __syncthreads();
+  int width = 1;  // rows, as a power of two; RC / width threads share a row's list
+  while (width < rows) width *= 2;
+  const int r = t % width, turn = t / width % (RC / width), col = t / RC;
+  const bool real = r < rows;
+  const int g_row = s_group[0] < 0 ? 0 : (b - s_group[0]) * p.SqG + first + (real ? r : 0);
+  const int l = g_row / (2 * sh::BM) == s_group[1] ? 0 : 1;
+  const int n0 = s_group[0] < 0 ? 0 : s_count[l], n = n0 + s_count[2];
+  const int at[2] = {g_row % (2 * sh::BM), (first + (real ? r : 0)) % (2 * sh::BM)};
+  float M = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto join_in = [&](float2 a, const float4& v) {
     if (!(a.y > 0.f || a.y != a.y)) return;  // saw no key  (NaN joins)
-    float wt;
+    float wt = 1.f;
     if (a.x > M) {
       const float f = M == -INFINITY ? 0.f : fast_exp2(M - a.x);
       den *= f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
       M = a.x;
-      wt = 1.f;
     } else {
       wt = fast_exp2(a.x - M);
     }
     den += wt * a.y;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc[4 * e] += wt * v[e].x;
-      acc[4 * e + 1] += wt * v[e].y;
-      acc[4 * e + 2] += wt * v[e].z;
-      acc[4 * e + 3] += wt * v[e].w;
-    }
+    acc.x += wt * v.x;
+    acc.y += wt * v.y;
+    acc.z += wt * v.z;
+    acc.w += wt * v.w;
   };
-  auto take = [&](int kind, long long id, int at) {
-    const size_t half2 = 2 * (size_t)p.half[kind];
-    const float2 a = reinterpret_cast<const float2*>(p.part_ml[kind])[id * half2 + at];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o[kind]) +
-                        ((size_t)id * (D / 4) + chunk * 4) * half2 + at;
-    float4 v[4];
+  constexpr int AHEAD = 6;
+  for (int k = turn; k < n; k += AHEAD * (RC / width)) {
+    float2 ml[AHEAD];
+    float4 ov[AHEAD];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = src[e * half2];
-    join(ml, ov);
-    ml = a;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ov[e] = v[e];
-  };
-  // The CTA whose range holds place y: the largest c with total * c / ctas <= y.
-  auto cta_of = [&](long long y) {
-    return (int)quotient((y + 1) * ctas - 1, total);
-  };
-  auto walk = [&](int o, int kind, int r) {  // all partials of row r of owner o
-    const Shape s = shape_of(p, p.starts, groups, o, W);
-    if (s.T == 0) return;
-    const int rt = r / (2 * sh::BM), rr = r - rt * 2 * sh::BM;
-    const bool dual = min(2 * sh::BM, s.rows - rt * 2 * sh::BM) > sh::BM;
-    const long long head = p.first[o] + hkv * places_per_head(s, slack);
-    for (int k = KS > 1 ? warp : 0; k < s.S; k += KS) {
-      const int len = min(s.len, s.T - k * s.len);
-      const long long y = head + (long long)k * s.n_rt * (s.len + slack) + (long long)rt * (len + slack);
-      const int c0 = cta_of(y), c1 = cta_of(y + len - 1);
-      const long long id = (long long)p.pieces[o] + (hkv * s.S + k) * s.n_rt + rt;
-      for (int c = c0; c <= c1; ++c) {
-        take(kind, id + c, rr);
-        if (!dual) take(kind, id + c, rr + p.half[kind]);
+    for (int u = 0; u < AHEAD; ++u) {
+      const int item = k + u * (RC / width);
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (item < n && real) {
+        const int kind = item < n0 ? 0 : 1;
+        const int e = kind ? s_list[2][item - n0] : s_list[l][item];
+        const bool few = kind && p.few;
+        // (Scratch is below 2^32 times 16 bytes.)
+        const uint32_t slots = few ? p.SqG : 2 * p.half[kind];
+        const uint32_t slot = at[kind] + (e & 1 ? p.half[kind] : 0), id = e >> 1;
+        ml[u] = reinterpret_cast<const float2*>(p.part_ml[kind])[id * slots + slot];
+        ov[u] = reinterpret_cast<const float4*>(
+            p.part_o[kind])[few ? (id * slots + slot) * (D / 4) + col
+                                : (id * (D / 4) + col) * slots + slot];
       }
     }
-  };
-  size_t row = 0;
-  if (real) {
-    const int b = R / p.SqG, r = R - b * p.SqG, s = r / p.G;
-    row = ((size_t)b * p.Sq + s) * p.Hq + (size_t)hkv * p.G + (r - s * p.G);
-    const int L = shared_len(p, b);
-    if (covered(p, p.starts, groups, b, L) > 0) {
-      const int g = group_of(p.starts, groups, b);
-      walk(g, 0, (b - p.starts[g]) * p.SqG + r);
-    }
-    walk(p.groups + b, 1, r);
-    join(ml, ov);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) join_in(ml[u], ov[u]);
   }
-  T* const dst = static_cast<T*>(p.o) + row * D + chunk * 16;
-  if constexpr (KS > 1) {
-    // The warps' results meet in shared memory; then each warp finishes two of the
-    // 16 columns.
-    sM[warp][lane] = M;
-    sDen[warp][lane] = den;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sAcc[warp][e][lane] = acc[e];
-    __syncthreads();
-    static_assert(KS == 1 || (KS == kJoinWarps && 2 * KS == 16), "two columns per warp");
-    M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) M = fmaxf(M, sM[i][lane]);
-    float a0 = 0.f, a1 = 0.f;
-    den = 0.f;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const float m = sM[i][lane];
-      const float wt = m == -INFINITY && !(sDen[i][lane] != sDen[i][lane]) ? 0.f : fast_exp2(m - M);
-      den += wt * sDen[i][lane];
-      a0 += wt * sAcc[i][2 * warp][lane];
-      a1 += wt * sAcc[i][2 * warp + 1][lane];
-    }
-    if (!real) return;
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    reinterpret_cast<uint32_t*>(dst)[warp] = TileType<T>::pack(a0 * inv, a1 * inv);
-    if (warp != 0) return;
-  } else {
-    if (!real) return;
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      reinterpret_cast<uint4*>(dst)[e] =
-          make_uint4(TileType<T>::pack(acc[8 * e] * inv, acc[8 * e + 1] * inv),
-                     TileType<T>::pack(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-                     TileType<T>::pack(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-                     TileType<T>::pack(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+  for (int o = width; o < RC; o <<= 1) {
+    const float2 a = make_float2(__shfl_xor_sync(0xffffffffu, M, o), __shfl_xor_sync(0xffffffffu, den, o));
+    const float4 v =
+        make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                    __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+    join_in(a, v);
   }
-  if (p.lse && chunk == 0)
+  if (!real || turn != 0) return;
+  const int own_r = first + r, tok = own_r / p.G;
+  const size_t row = ((size_t)b * p.Sq + tok) * p.Hq + (size_t)hkv * p.G + (own_r - tok * p.G);
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + col * 4) = make_uint2(
+      TileType<T>::pack(acc.x * inv, acc.y * inv), TileType<T>::pack(acc.z * inv, acc.w * inv));
+  if (p.lse && col == 0)
     p.lse[row] = den == 0.f ? -INFINITY : 0.6931471805599453f * (M + log2f(den));
 }
 
@@ -906,8 +1467,8 @@ __global__ void shared_zero_kernel(uint16_t* o, size_t n, float* lse, size_t nl)
 }
 
 template <int D, typename T>
-static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tk,
-                                 const CUtensorMap& tv, cudaStream_t stream) {
+static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[4],
+                                 cudaStream_t stream) {
   using C = sh::Cfg<D>;
   static int attr_set[64] = {0};
   int dev = 0;
@@ -918,7 +1479,7 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tk,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     // As in the tree decode: the merge keeps the split kernel's division of the SM.
-    for (auto k : {shared_merge_kernel<D, T, 1>, shared_merge_kernel<D, T, kJoinWarps>}) {
+    for (auto k : {shared_merge_kernel<D, T, 256>, shared_merge_kernel<D, T, 8 * D>}) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
                                (int)cudaSharedmemCarveoutMaxShared);
       if (e != cudaSuccess) return e;
@@ -935,16 +1496,15 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap& tk,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, shared_split_kernel<D, T>, tk, tv, p);
+  e = cudaLaunchKernelEx(&cfg, shared_split_kernel<D, T>, tm[0], tm[1], tm[2], tm[3], p);
   if (e != cudaSuccess) return e;
-  constexpr int NC = D / 16;
-  const long long sets = ((long long)p.B * p.SqG + 31) / 32 * p.Hkv;
-  const bool split = sets * NC <= 4 * p.ctas;
-  return split ? launch_dependent(shared_merge_kernel<D, T, kJoinWarps>, dim3((unsigned)(sets * NC)),
-                                  kJoinWarps * 32, stream, p)
-               : launch_dependent(shared_merge_kernel<D, T, 1>,
-                                  dim3((unsigned)((sets * NC + kJoinWarps - 1) / kJoinWarps)),
-                                  kJoinWarps * 32, stream, p);
+  // Blocks of 32 rows' threads while they leave SMs free: a row then has more of them.
+  const long long units = (long long)p.B * p.Hkv, wide = units * ((p.SqG + 31) / 32);
+  if (wide <= p.ctas)
+    return launch_dependent(shared_merge_kernel<D, T, 8 * D>, dim3((unsigned)wide), 8 * D, stream, p);
+  constexpr int RC = 256 * 4 / D;
+  return launch_dependent(shared_merge_kernel<D, T, 256>,
+                          dim3((unsigned)(units * ((p.SqG + RC - 1) / RC))), 256, stream, p);
 }
 
 int set_shared_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
@@ -1016,6 +1576,7 @@ extern "C" int fa_decode_shared_fwd(const void* q, const void* kpages, const voi
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.SqG = Sq * p.G;
+  p.few = p.SqG <= fa::sh::FEW;
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
@@ -1024,7 +1585,9 @@ extern "C" int fa_decode_shared_fwd(const void* q, const void* kpages, const voi
   p.c = scale * 1.4426950408889634f;
   // scale == 0: every visible score is 0; a tiny c keeps hidden keys at -inf.
   if (p.c == 0.f) p.c = 1e-30f;
+  p.keep_tiles = fa::sh::L2_KEEPS / (2 * fa::sh::BN * 2 * D);
   p.ctas = fa::sm_count() > 0 ? fa::sm_count() : 148;
+  if (p.ctas > fa::join::LIST / 8) p.ctas = fa::join::LIST / 8;
   // Slots: every piece, and one more for each boundary between CTAs' ranges.  Pieces:
   // one per (row-tile pair, kv head), and strips, of which all have at most one per CTA
   // beyond those.
@@ -1034,39 +1597,45 @@ extern "C" int fa_decode_shared_fwd(const void* q, const void* kpages, const voi
       (long long)B * ((p.SqG + pair - 1) / pair)};
   size_t slots[2], bytes = 0, at_o[2], at_ml[2];
   const size_t owners = (size_t)groups + B;
-  bytes = (owners + 4) * sizeof(long long) + (owners * sizeof(int) + 31) / 32 * 32;
+  bytes = owners * sizeof(fa::SharedOwner) + sizeof(fa::SharedList);
   bytes = (bytes + 255) / 256 * 256;
   for (int k = 0; k < 2; ++k) {
     const long long rows = k == 0 ? rows_all : p.SqG;
     p.half[k] = (int)(rows < fa::sh::BM ? rows : fa::sh::BM);
-    slots[k] = k == 0 && groups == 0 ? 0 : (size_t)units[k] * Hkv + 2 * (size_t)p.ctas;
+    const bool few = k == 1 && p.few;
+    slots[k] = k == 0 && groups == 0
+                   ? 0
+                   : (size_t)units[k] * Hkv + (few ? fa::sh::FEW_WARPS : 2) * (size_t)p.ctas;
+    const size_t in_slot = few ? p.SqG : 2 * p.half[k];
     at_o[k] = bytes;
-    bytes += slots[k] * D * 2 * p.half[k] * sizeof(float);
+    bytes += slots[k] * D * in_slot * sizeof(float);
     at_ml[k] = bytes;
-    bytes += slots[k] * 2 * 2 * p.half[k] * sizeof(float);
+    bytes += slots[k] * 2 * in_slot * sizeof(float);
     bytes = (bytes + 255) / 256 * 256;
   }
-  CUtensorMap tk, tv;
-  if (fa::encode_tmap_rows(&tk, kpages, D, Hkv, page_size, num_pages, p.box) ||
-      fa::encode_tmap_rows(&tv, vpages, D, Hkv, page_size, num_pages, p.box))
+  CUtensorMap tm[4];
+  if (fa::encode_tmap_rows(&tm[0], kpages, D, Hkv, page_size, num_pages, p.box) ||
+      fa::encode_tmap_rows(&tm[1], vpages, D, Hkv, page_size, num_pages, p.box) ||
+      fa::encode_tmap_rows(&tm[2], kpages, D, Hkv, page_size, num_pages, fa::sh::FEW_KEYS) ||
+      fa::encode_tmap_rows(&tm[3], vpages, D, Hkv, page_size, num_pages, fa::sh::FEW_KEYS))
     return fa::record_cuda_status(cudaErrorInvalidValue, "shared decode tensor maps");
   void* scratch = nullptr;
   cudaError_t e = fa::scratch_alloc(&scratch, bytes, stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "shared decode scratch");
   uint8_t* const base = static_cast<uint8_t*>(scratch);
-  p.first = reinterpret_cast<long long*>(base);
-  p.pieces = reinterpret_cast<int*>(base + (owners + 4) * sizeof(long long));
+  p.owner = reinterpret_cast<fa::SharedOwner*>(base);
+  p.list = reinterpret_cast<fa::SharedList*>(base + owners * sizeof(fa::SharedOwner));
   for (int k = 0; k < 2; ++k) {
     p.part_o[k] = reinterpret_cast<float*>(base + at_o[k]);
     p.part_ml[k] = reinterpret_cast<float*>(base + at_ml[k]);
   }
   const bool bf16 = dtype == FA_BF16;
   if (D == 64)
-    e = bf16 ? fa::launch_shared<64, __nv_bfloat16>(p, tk, tv, stream)
-             : fa::launch_shared<64, __half>(p, tk, tv, stream);
+    e = bf16 ? fa::launch_shared<64, __nv_bfloat16>(p, tm, stream)
+             : fa::launch_shared<64, __half>(p, tm, stream);
   else
-    e = bf16 ? fa::launch_shared<128, __nv_bfloat16>(p, tk, tv, stream)
-             : fa::launch_shared<128, __half>(p, tk, tv, stream);
+    e = bf16 ? fa::launch_shared<128, __nv_bfloat16>(p, tm, stream)
+             : fa::launch_shared<128, __half>(p, tm, stream);
   const cudaError_t ef = cudaFreeAsync(scratch, stream);
   if (e != cudaSuccess) return fa::record_cuda_status(e, "shared decode launch");
   return fa::record_cuda_status(ef, "shared decode cudaFreeAsync");
