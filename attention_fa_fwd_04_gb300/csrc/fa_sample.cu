@@ -10,20 +10,36 @@
 // the first m of the tokens at the border".  The token is the lowest index whose
 // cumulative kept weight (by index) exceeds u times all of it.
 //
-// Nothing is sorted.  The border is found by narrowing an interval of keys (the
-// logits' bits, made to order as whole numbers): a pass over the row counts the
-// keys of the interval in 2048 bins; for top-k the bin of the k-th is exact, for
-// top-p the counts only suggest where the border is, and the next pass adds up the
-// weights above and in the suggested bins exactly and goes on from what it finds.
+// No row is sorted.  The border is found by narrowing an interval of keys (the
+// logits' bits, made to order as whole numbers).
+//   top-k   The k-th largest of the threads' largest logits is a lower bound of the k-th
+//           logit, and for k up to a third of the threads few more than k lie above it:
+//           those become a list that every CTA ranks, and draws from.  Larger k (and rows
+//           of many equal logits): passes that count the interval's keys in 2048 bins.
+//   top-p   One pass counts logits in bins of 1/64 of the temperature, which says within
+//           about a bin where the border is; the next adds up exactly everything and what
+//           is above those bins, and lists what is in them (or counts it, where that is
+//           much); the list's weights then give the border.  Whatever the estimate
+//           missed, the sums show, and the search goes on from there.
 //
 // The answers are whole numbers.  With 128000 tokens an error of 1e-7 in the sums
-// would move one draw in fifty, so weights are pairs of floats good to 2^-40
-// (2^(j/256) from a table, the rest a short series), summed as pairs in a fixed
-// order: about 40 fp32 operations per weight, where fp64 would be bound by the few
-// fp64 units.
+// would move one draw in fifty, so weights are pairs of floats good to 2^-31 (most to
+// 2^-33; sums to 2^-36), added as pairs in a fixed order.  A weight and its addition take
+// 8 clocks of an SM for 64 tokens (packed fp32 arithmetic; the table has a copy for every
+// second lane: one of 1024 entries without copies took 16, its reads met in the banks;
+// fp64 would be bound by the few fp64 units).
 //
 // Layout: a cluster of up to 8 CTAs takes a row and keeps it in shared memory, so
-// that HBM is read once however many passes there are.
+// that HBM is read once however many passes there are.  Every thread has consecutive
+// tokens, so that its sums are also what finds the token in the end.
+//
+// Measured (device time of one call in a captured sequence): 13.3 us for one row of 32000
+// fp32 logits with top-k and top-p, 49.9 for 64 rows of 128000 bf16 with top-p and min-p
+// (HBM's share is 2.4), 25.9 for 200 of 50257 fp16 with temperature alone (3.0), 105 for
+// 512 of 32000 fp32 with top-k, top-p and the distributions written (19.4).  What bounds
+// it: the two passes of weights (about half of a row's time with top-p), and the
+// chain of meetings, scans and rankings between them (some 20000 clocks), of which two
+// resident CTAs hide part.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -41,7 +57,8 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int SEGS = CLUSTER * WARPS;  // index-ordered segments of a row, one per warp
-constexpr int SMEM_MAX = 200 * 1024;   // bytes of a CTA's part of a row
+constexpr int LIST = 512;              // tokens that a CTA ranks
+constexpr int SMEM_MAX = 180 * 1024;   // bytes of a CTA's part of a row
 }  // namespace sa
 
 struct SampleParams {
@@ -55,21 +72,26 @@ struct SampleParams {
   float* probs;  // [rows, V] or null
   long long stride;
   int V, cluster;
-  int seg;  // elements per warp: whole steps of 32 groups
+  int groups;  // 16-byte groups of the row per thread
 };
 
-// 16 bytes of logits, and the logits' order as whole numbers (NaN counts as
-// -infinity, -0 as 0).
+// Logits as they are stored, and their order as whole numbers (NaN counts as -infinity,
+// -0 as 0).
 template <typename T>
 struct Logits;
 template <>
 struct Logits<float> {
-  static constexpr int GROUP = 4, KEY_BITS = 32;
   typedef uint32_t raw;
+  static constexpr int GROUP = 4;  // elements of 16 bytes
+  static __device__ __forceinline__ float2 pair(const uint4& g, int x) {
+    return x == 0 ? make_float2(__uint_as_float(g.x), __uint_as_float(g.y))
+                  : make_float2(__uint_as_float(g.z), __uint_as_float(g.w));
+  }
+  static constexpr raw NEG = 0xff800000u;
   static __device__ __forceinline__ float value(raw r) { return __uint_as_float(r); }
   static __device__ __forceinline__ raw clean(raw r) {
     const float x = __uint_as_float(r);
-    return x != x ? 0xff800000u : __float_as_uint(x + 0.f);
+    return __float_as_uint(fmaxf(x + 0.f, -INFINITY));  // (of a NaN and a number, the number)
   }
   static __device__ __forceinline__ uint32_t key(raw r) {
     return r ^ (uint32_t)((int32_t)r >> 31 | (int32_t)0x80000000);
@@ -77,49 +99,79 @@ struct Logits<float> {
   static __device__ __forceinline__ raw unkey(uint32_t k) {
     return k & 0x80000000u ? k ^ 0x80000000u : ~k;
   }
-  static __device__ __forceinline__ raw at(const uint4& v, int e) {
-    return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+  static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
+    g = make_uint4(clean(g.x), clean(g.y), clean(g.z), clean(g.w));
+    return fmaxf(fmaxf(__uint_as_float(g.x), __uint_as_float(g.y)),
+                 fmaxf(__uint_as_float(g.z), __uint_as_float(g.w)));
   }
+  // (Rounds up where the type is narrower.)
   static __device__ __forceinline__ raw from(float x) { return clean(__float_as_uint(x)); }
-  // The lowest raw value that is at least x.
-  static __device__ __forceinline__ raw at_least(double x) { return from(__double2float_ru(x)); }
 };
+__device__ __forceinline__ uint32_t word(const uint4& g, int x) {
+  return x == 0 ? g.x : x == 1 ? g.y : x == 2 ? g.z : g.w;
+}
 template <typename H>
 struct Logits16 {
-  static constexpr int GROUP = 8, KEY_BITS = 16;
   typedef uint16_t raw;
+  static constexpr int GROUP = 8;
   static __device__ __forceinline__ uint32_t key(raw r) {
     return r & 0x8000u ? (uint16_t)~r : (uint16_t)(r | 0x8000u);
   }
   static __device__ __forceinline__ raw unkey(uint32_t k) {
     return k & 0x8000u ? (raw)(k ^ 0x8000u) : (raw)~k;
   }
-  static __device__ __forceinline__ raw at(const uint4& v, int e) {
-    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    return (raw)(e & 1 ? w >> 16 : w);
-  }
 };
 template <>
 struct Logits<__nv_bfloat16> : Logits16<__nv_bfloat16> {
+  static constexpr raw NEG = 0xff80u;
   static __device__ __forceinline__ float value(raw r) { return __uint_as_float((uint32_t)r << 16); }
-  static __device__ __forceinline__ raw clean(raw r) {
-    return (r & 0x7fffu) > 0x7f80u ? (raw)0xff80u : (r == 0x8000u ? (raw)0 : r);
+  static __device__ __forceinline__ float2 pair(const uint4& g, int x) {
+    const uint32_t w = word(g, x);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ raw from(float x) {  // (rounds up)
+  static __device__ __forceinline__ raw clean(raw r) {
+    return (r & 0x7fffu) > 0x7f80u ? NEG : (r == 0x8000u ? (raw)0 : r);
+  }
+  static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
+    const __nv_bfloat162 neg = {__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80)}, zero = {__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)};
+    __nv_bfloat162* const x = reinterpret_cast<__nv_bfloat162*>(&g);
+    __nv_bfloat162 m = neg;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __hmax2(__hadd2(x[i], zero), neg);  // (of a NaN and a number, the number)
+      m = __hmax2(m, x[i]);
+    }
+    return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
+  }
+  static __device__ __forceinline__ raw from(float x) {
     return clean(__bfloat16_as_ushort(__float2bfloat16_ru(x)));
   }
-  static __device__ __forceinline__ raw at_least(double x) { return from(__double2float_ru(x)); }
 };
 template <>
 struct Logits<__half> : Logits16<__half> {
+  static constexpr raw NEG = 0xfc00u;
   static __device__ __forceinline__ float value(raw r) { return __half2float(__ushort_as_half(r)); }
-  static __device__ __forceinline__ raw clean(raw r) {
-    return (r & 0x7fffu) > 0x7c00u ? (raw)0xfc00u : (r == 0x8000u ? (raw)0 : r);
+  static __device__ __forceinline__ float2 pair(const uint4& g, int x) {
+    const uint32_t w = word(g, x);
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
-  static __device__ __forceinline__ raw from(float x) {  // (rounds up)
+  static __device__ __forceinline__ raw clean(raw r) {
+    return (r & 0x7fffu) > 0x7c00u ? NEG : (r == 0x8000u ? (raw)0 : r);
+  }
+  static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
+    const __half2 neg = {__ushort_as_half(0xfc00), __ushort_as_half(0xfc00)}, zero = {__ushort_as_half(0), __ushort_as_half(0)};
+    __half2* const x = reinterpret_cast<__half2*>(&g);
+    __half2 m = neg;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __hmax2(__hadd2(x[i], zero), neg);  // (of a NaN and a number, the number)
+      m = __hmax2(m, x[i]);
+    }
+    return fmaxf(__half2float(m.x), __half2float(m.y));
+  }
+  static __device__ __forceinline__ raw from(float x) {
     return clean(__half_as_ushort(__float2half_ru(x)));
   }
-  static __device__ __forceinline__ raw at_least(double x) { return from(__double2float_ru(x)); }
 };
 
 // Unevaluated sum of two floats.
@@ -148,14 +200,21 @@ __device__ __forceinline__ Sum2 shfl_xor(Sum2 a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
 }
 __device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) a = sum_of(a, shfl_xor(a, o));
   return a;
+}
+__device__ __forceinline__ void warp_sum(Sum2& a, Sum2& b) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    a = sum_of(a, shfl_xor(a, o));
+    b = sum_of(b, shfl_xor(b, o));
+  }
 }
 // Sums of the lanes up to this one.
 __device__ __forceinline__ Sum2 warp_sums(Sum2 a) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const Sum2 y = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
     if (lane >= o) a = sum_of(y, a);
@@ -165,48 +224,55 @@ __device__ __forceinline__ Sum2 warp_sums(Sum2 a) {
 __device__ __forceinline__ Sum2 lane_of(Sum2 a, int l) {
   return {__shfl_sync(0xffffffffu, a.hi, l), __shfl_sync(0xffffffffu, a.lo, l)};
 }
-// (Only in one thread or warp: the SM has two fp64 units.)
-__device__ __forceinline__ double wide(Sum2 a) { return (double)a.hi + (double)a.lo; }
 
-// Weights of a row's logits.
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+// Sums of weights hi + hi q, two at once.  The sums begin at 2, the largest weight, so
+// that a sum's rounding is what three operations give.
+struct Sums {
+  float2 hi = {2.f, 2.f}, lo = {0.f, 0.f};
+  __device__ __forceinline__ void add(float2 h, float2 q) {
+    const float2 s = __fadd2_rn(hi, h), t = __fadd2_rn(s, make_float2(-hi.x, -hi.y));
+    lo = __fadd2_rn(__ffma2_rn(h, q, lo), __fadd2_rn(h, make_float2(-t.x, -t.y)));
+    hi = s;
+  }
+  __device__ __forceinline__ Sum2 all() const {
+    return sum_of(sum_of(hi.x - 2.f, lo.x), sum_of(hi.y - 2.f, lo.y));
+  }
+};
+
+// Weights of a row's logits, up to a power of two that all of them share.  In y =
+// (l - base) log2(e) / T = k / 128 + a, |a| <= 2^-8, 2^y = 2^(k / 128) 2^a: a table has the
+// first factor, a polynomial the second.  With base = 0, l needs no exact difference;
+// where |top| / T is so large that y would lose bits, base = top, and the differences that
+// matter (l within T of top) are exact.
 struct Weigher {
-  float top;         // the largest logit
-  float s_hi, s_lo;  // log2(e) / T
-  const float2* table;
-  // exp((l - top) / T) to about 2^-40 of itself; below 2^-120 it is 0.
-  __device__ __forceinline__ Sum2 operator()(float l) const {
-    const Sum2 d = sum_of(l, -top);
-    const float y = __fmul_rn(d.hi, s_hi);
-    const float y_lo = __fadd_rn(__fmaf_rn(d.hi, s_hi, -y),
-                                 __fmaf_rn(d.hi, s_lo, __fmul_rn(d.lo, s_hi)));
-    // y = k / 256 + r, |r| <= 2^-9.
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-    const float yc = fmaxf(y, -121.f);
-    const float t = __fmaf_rn(yc, 256.f, kMagic);
-    const int k = __float_as_int(t) - __float_as_int(kMagic);
-    const float r = __fmaf_rn(__fsub_rn(t, kMagic), -0.00390625f, yc);
-    // 2^(r + y_lo) - 1 = hi + lo.
-    constexpr float L_hi = 0.693147182464599609375f, L_lo = -1.904654299958e-9f;  // ln 2
-    constexpr float c2 = 0.240226506959100712f, c3 = 0.0555041086648215800f;  // ln2^2/2, ln2^3/6
-    const float hi = __fmul_rn(r, L_hi);
-    float lo = __fmaf_rn(r, L_hi, -hi);
-    lo = __fmaf_rn(r, L_lo, lo);
-    lo = __fmaf_rn(y_lo, L_hi, lo);
-    const float a2 = __fadd_rn(r, y_lo);  // (r y_lo counts: 2^-28)
-    lo = __fmaf_rn(__fmul_rn(a2, a2), __fmaf_rn(a2, c3, c2), lo);
-    const float2 T = table[k & 255];
-    // T (1 + hi + lo).
-    const float m = __fmul_rn(T.x, hi);
-    float e = __fmaf_rn(T.x, hi, -m);
-    e = __fmaf_rn(T.x, lo, e);
-    e = __fadd_rn(e, __fmaf_rn(T.y, hi, T.y));
-    const float a = __fadd_rn(T.x, m);
-    e = __fadd_rn(e, __fsub_rn(m, __fsub_rn(a, T.x)));
-    const float f = __int_as_float(((k >> 8) + 127) << 23);
-    // (l = top: exactly 1, also where both are infinite; l = -infinity has a y that
-    // is not above -120, or NaN.)
-    if (l == top) return Sum2{1.f, 0.f};
-    return y > -120.f ? Sum2{__fmul_rn(a, f), __fmul_rn(e, f)} : Sum2{0.f, 0.f};
+  float shift;            // -base
+  float s_hi, s_lo;       // log2(e) / T
+  float lowest;           // l - base that has no weight any more: 2^-126 of the largest
+  float magic;            // 1.5 * 2^16, which rounds to 1 / 128, and the exponents' bias
+  const float2* table;    // this lane's copy: entries 16 apart, no two lanes in one bank
+  // Weights of v: hi + hi * q, |q| < 2^-8.
+  __device__ __forceinline__ void operator()(float2 v, float2* hi, float2* q) const {
+    float2 d = __fadd2_rn(v, twice(shift));
+    d = make_float2(fmaxf(d.x, lowest), fmaxf(d.y, lowest));
+    const float2 t = __ffma2_rn(d, twice(s_hi), twice(magic));
+    const float2 r = __ffma2_rn(d, twice(s_hi), __fadd2_rn(twice(magic), make_float2(-t.x, -t.y)));
+    const float2 a = __ffma2_rn(d, twice(s_lo), r);
+    // ln 2, (ln 2)^2 / 2, (ln 2)^3 / 6.
+    float2 f = __ffma2_rn(a, twice(0.0555041086648215800f), twice(0.240226506959100712f));
+    f = __ffma2_rn(a, f, twice(0.693147180559945309f));
+    const uint32_t bx = __float_as_uint(t.x), by = __float_as_uint(t.y);
+    const float2 tx = table[(bx & 127u) * 16], ty = table[(by & 127u) * 16];
+    // t's bits from the seventh on are the factor's exponent; 0 where l is `lowest`.
+    const float2 e = make_float2(__uint_as_float((bx << 16) & 0xff800000u),
+                                 __uint_as_float((by << 16) & 0xff800000u));
+    *hi = __fmul2_rn(make_float2(tx.x, ty.x), e);
+    *q = __ffma2_rn(a, f, make_float2(tx.y, ty.y));
+  }
+  __device__ __forceinline__ Sum2 one(float v) const {
+    float2 h, q;
+    (*this)(twice(v), &h, &q);
+    return {h.x, __fmul_rn(h.x, q.x)};
   }
 };
 
@@ -221,6 +287,16 @@ __device__ __forceinline__ void put(uint32_t at, float a, float b) {
 __device__ __forceinline__ void put(uint32_t at, int a) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
 }
+__device__ __forceinline__ int add_remote(uint32_t at, int a) {
+  int r;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(at), "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ int get(uint32_t at) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 get4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -231,33 +307,43 @@ __device__ __forceinline__ uint4 get4(uint32_t at) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_constant__ SampleParams p) {
   using Lg = Logits<T>;
   using raw = typename Lg::raw;
+  constexpr raw NEG = Lg::NEG;
   constexpr int GROUP = Lg::GROUP;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ float2 s_table[256];
+  __shared__ float2 s_table[128 * 16];
   __shared__ __align__(16) uint32_t s_hist[2][sa::BINS];
   __shared__ float2 s_first[sa::SEGS];       // every warp's largest logit, smallest lane maximum
-  __shared__ float2 s_warp[2][3][sa::SEGS];  // per round and quantity: every warp's sum
+  __shared__ float2 s_warp[2][2][sa::SEGS];  // per round and quantity: every warp's sum
   __shared__ int s_cnt[sa::SEGS];
-  __shared__ float2 s_steps[32];
+  __shared__ __align__(16) unsigned long long s_list[sa::LIST + 8];  // tokens to rank: key, place inverted
+  __shared__ int s_rank[sa::LIST];
+  __shared__ float2 s_block[sa::WARPS + 1];
   __shared__ uint32_t s_scan[sa::WARPS];
   __shared__ float s_fscan[sa::WARPS];
-  __shared__ int s_i[4], s_cut[2];
+  __shared__ int s_i[4], s_cut, s_listed[4];
   __shared__ uint32_t s_key[2];
-  __shared__ float s_f[8];
-  __shared__ double s_d[8];
+  __shared__ float2 s_pair[5];
+  constexpr uint32_t NONE = 0xffffffffu;
+  __shared__ uint32_t s_found;  // a bin (11 bits), how many of its key (20), whether that is fewer than it has (few lie there)
+  __shared__ float2 s_low;  // T ln(min_p)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int C = p.cluster;
-  const int rank = C > 1 ? (int)(blockIdx.x % C) : 0;
-  const long long row = blockIdx.x / C;
-  const int n = p.seg * sa::WARPS;  // elements of this CTA's part, in places that begin at
-                                    // the 16 bytes the row begins in
+  const int rank = (int)(blockIdx.x & (unsigned)(C - 1));  // (C is 1, 2, 4 or 8)
+  const long long row = blockIdx.x >> (__ffs(C) - 1);
   const int segs = C * sa::WARPS, seg_id = rank * sa::WARPS + warp;
+  const int own = p.groups;  // 16-byte groups per thread, consecutive in the row
+  const int n = own * GROUP * sa::THREADS;  // elements of this CTA's part
   pdl_launch_dependents();
-  if (t < 256) s_table[t] = make_float2(kExp2Table[t][0], kExp2Table[t][1]);
+  for (int i = t; i < 128 * 16; i += sa::THREADS)
+    s_table[i] = make_float2(kExp2Table[i >> 4][0], kExp2Table[i >> 4][1]);
   for (int i = t; i < 2 * sa::BINS; i += sa::THREADS) (&s_hist[0][0])[i] = 0;
+  s_rank[t] = 0;
+  if (t < 8) s_list[sa::LIST + t] = 0;
+  static_assert(sa::LIST == sa::THREADS, "an item of the list per thread");
+  if (t < 4) s_listed[t] = 0;
   pdl_wait_primary();
 
   auto sync = [&] {  // the cluster's CTAs meet; what they stored is visible
@@ -271,31 +357,39 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
   // ---- the row into shared memory, its largest logit ----
   const T* const src = static_cast<const T*>(p.logits) + row * p.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-  const long long first = (long long)rank * n;  // place of this part's first element
+  const int first = rank * n - lead;  // token of this part's first element
   uint4* const part = reinterpret_cast<uint4*>(smem_raw);
-  const int g0 = warp * (p.seg / GROUP), g1 = g0 + p.seg / GROUP;  // this warp's groups
-  const raw NEG = Lg::from(-INFINITY);
   float temp = p.temperature ? p.temperature[row] : 1.f;
-  if (temp > 3.402823466e38f) temp = 3.402823466e38f;
+  if (temp > 0x1p99f) temp = 0x1p99f;
   const bool greedy = !(temp > 0.f);
+  const int k = p.top_k ? p.top_k[row] : 0;
+  const float tp = p.top_p ? p.top_p[row] : 1.f;
+  const float mp = p.min_p ? p.min_p[row] : 0.f;
+  const float u = p.u[row];
+  const float uu = u > 0.f ? fminf(u, 2.f) : 0.f;
   float mx = -INFINITY;
+  {
+    const int g0 = warp * 32 * own;
 #pragma unroll 4
-  for (int g = g0 + lane; g < g1; g += 32) {
-    const long long e0 = first + (long long)g * GROUP - lead;  // the group's first token
-    alignas(16) raw v[GROUP];
-    if (e0 >= 0 && e0 + GROUP <= p.V) {
-      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src + e0);
-    } else {
+    for (int i = lane; i < 32 * own; i += 32) {
+      const int e = first + (g0 + i) * GROUP;  // the group's first token
+      uint4 v;
+      if (e >= 0 && e + GROUP <= p.V) {
+        v = *reinterpret_cast<const uint4*>(src + e);
+      } else {
+        alignas(16) raw x[GROUP];
 #pragma unroll
-      for (int e = 0; e < GROUP; ++e)
-        v[e] = e0 + e >= 0 && e0 + e < p.V ? reinterpret_cast<const raw*>(src)[e0 + e] : NEG;
+        for (int j = 0; j < GROUP; ++j)
+          x[j] = e + j >= 0 && e + j < p.V ? reinterpret_cast<const raw*>(src)[e + j] : NEG;
+        v = *reinterpret_cast<uint4*>(x);
+      }
+      mx = fmaxf(mx, Lg::clean(v));
+      part[g0 + i] = v;
     }
-#pragma unroll
-    for (int e = 0; e < GROUP; ++e) {
-      v[e] = Lg::clean(v[e]);
-      mx = fmaxf(mx, Lg::value(v[e]));
-    }
-    part[g] = *reinterpret_cast<uint4*>(v);
+  }
+  if (t == sa::THREADS - 32 && mp > 0.f) {
+    const double x = fmin((double)temp * log((double)mp), 0.0);
+    s_low = make_float2((float)x, (float)(x - (double)(float)x));
   }
   {
     float hi = mx, lo = mx;
@@ -306,50 +400,124 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
     }
     if (lane < C) put(remote(&s_first[seg_id], lane), hi, lo);
   }
-  if (t == 0) {
-    const double s = fmin(1.4426950408889634 / (greedy ? 1.0 : (double)temp), 0x1p100);
-    s_f[0] = (float)s;
-    s_f[1] = (float)(s - (double)s_f[0]);
+  // log2(e) / T in two floats.
+  Weigher weigh;
+  weigh.table = s_table + (lane & 15);
+  {
+    const float tt = greedy ? 1.f : fmaxf(temp, 0x1p-99f);
+    const float inv = __fdividef(1.f, tt);  // (what it is off by goes into s_lo)
+    weigh.s_hi = 1.44269502162933349609f * inv;
+    weigh.s_lo = __fmul_rn(inv, __fadd_rn(__fmaf_rn(-weigh.s_hi, tt, 1.44269502162933349609f),
+                                          1.92596299112661746887e-8f));
   }
   sync();
-  float top = -INFINITY;
-  for (int i = lane; i < segs; i += 32) top = fmaxf(top, s_first[i].x);
+  float top = -INFINITY, least = INFINITY;
+  for (int i = lane; i < segs; i += 32) {
+    const float2 v = s_first[i];
+    top = fmaxf(top, v.x);
+    least = fminf(least, v.y);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  Weigher weigh;
-  weigh.top = top;
-  weigh.table = s_table;
-  weigh.s_hi = s_f[0];
-  weigh.s_lo = s_f[1];
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+  }
 
-  // Of every element of this warp: f(place in the part, raw value).
+  // Every group of this thread's: f(its index in the part, the group).  The lanes begin
+  // at different ones, so that they read different banks.
+  const int even = own % 8 == 0 ? 8 : own % 4 == 0 ? 4 : own % 2 == 0 ? 2 : 1;
+  const int begin = (lane & 7) * even >> 3;
   auto each = [&](auto&& f) {
-    for (int g = g0 + lane; g < g1; g += 32) {
-      const uint4 v = part[g];
-#pragma unroll
-      for (int e = 0; e < GROUP; ++e) f(g * GROUP + e, Lg::at(v, e));
+    int x = begin;
+#pragma unroll 1
+    for (int g = 0; g < own; ++g) {
+      const int i = t * own + x;
+      f(i, part[i]);
+      if (++x == own) x = 0;
     }
   };
+  // Which elements of a group lie in [lo, hi], as bits; f(raw value, index in the part) of
+  // those (few: the loop is as long as the fullest lane's).
+  auto within = [](uint4 g, float lo, float hi) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int x = 0; x < GROUP / 2; ++x) {
+      const float2 v = Lg::pair(g, x);
+      if (v.x >= lo && v.x <= hi) m |= 1u << (2 * x);
+      if (v.y >= lo && v.y <= hi) m |= 2u << (2 * x);
+    }
+    return m;
+  };
+  auto each_of = [&](uint32_t m, int i, auto&& f) {
+#pragma unroll 1
+    for (; m; m &= m - 1) {
+      const int x = i * GROUP + __ffs((int)m) - 1;
+      f(reinterpret_cast<const raw*>(part)[x], x);
+    }
+  };
+  // Logits of +infinity share the weight: they become 0 and all others -infinity.
+  const bool was_inf = top == INFINITY;
+  if (was_inf) {
+    mx = least = -INFINITY;
+    each([&](int i, uint4 g) {
+      alignas(16) raw x[GROUP];
+      *reinterpret_cast<uint4*>(x) = g;
+#pragma unroll
+      for (int j = 0; j < GROUP; ++j) {
+        x[j] = Lg::value(x[j]) == INFINITY ? (raw)0 : NEG;
+        mx = fmaxf(mx, Lg::value(x[j]));
+      }
+      part[i] = *reinterpret_cast<uint4*>(x);
+    });
+    top = 0.f;
+  }
+  const bool alive = top != -INFINITY;
+  const uint32_t kneg = Lg::key(NEG), kmax = Lg::key(Lg::from(top));
+  {
+    float y = top * weigh.s_hi;
+    weigh.shift = 0.f;
+    if (!(fabsf(y) < 1000.f)) {
+      y = 0.f;
+      weigh.shift = -top;
+    }
+    const float e = floorf(y);
+    weigh.lowest = (e - 126.5f) / weigh.s_hi;
+    weigh.magic = 98304.f + (127.f - e);
+  }
+  auto value_of = [&](uint32_t key) { return Lg::value(Lg::unkey(key)); };
+
   // Exchanges alternate between two buffers of bins and sums, so that one barrier
   // each does: a CTA fills a buffer again only after the barrier that the others
   // reach when they have read it.
   int round = 0;
   static_assert(sa::BINS == 4 * sa::THREADS, "four bins per thread");
   auto gather = [&](uint32_t (&h)[4]) {  // four bins of all CTAs together
-    uint4 s = make_uint4(0, 0, 0, 0);
-    for (int c = 0; c < C; ++c) {
-      const uint4 v = C > 1 ? get4(remote(&s_hist[round & 1][4 * t], c))
-                            : *reinterpret_cast<const uint4*>(&s_hist[round & 1][4 * t]);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+    uint4 s = *reinterpret_cast<const uint4*>(&s_hist[round & 1][4 * t]);
+    if (C > 1) {
+      uint4 v[sa::CLUSTER - 1];
+#pragma unroll
+      for (int c = 1; c < sa::CLUSTER; ++c)
+        if (c < C) v[c - 1] = get4(remote(&s_hist[round & 1][4 * t], (rank + c) & (C - 1)));
+#pragma unroll
+      for (int c = 1; c < sa::CLUSTER; ++c) {
+        if (c < C) {
+          s.x += v[c - 1].x;
+          s.y += v[c - 1].y;
+          s.z += v[c - 1].z;
+          s.w += v[c - 1].w;
+        }
+      }
     }
     h[0] = s.x;
     h[1] = s.y;
     h[2] = s.z;
     h[3] = s.w;
+  };
+  auto turn = [&] {  // (after the barrier, before the block's next one)
     *reinterpret_cast<uint4*>(&s_hist[(round & 1) ^ 1][4 * t]) = make_uint4(0, 0, 0, 0);
+    // (Other CTAs add to the next round's: the one after it.)
+    if (t == 0) s_listed[(round + 2) & 3] = 0;
+    ++round;
   };
   // Sum of the block's values before this thread's; sums: one entry per warp.
   auto sum_before = [&](auto mine, auto* sums) {
@@ -362,59 +530,271 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     x -= mine;
-    for (int i = 0; i < warp; ++i) x += sums[i];
+#pragma unroll
+    for (int i = 0; i < sa::WARPS; ++i) x += i < warp ? sums[i] : 0;
     return x;
   };
+  // The same of pairs (in warps without any it is not computed); *all: the sum of all.
+  // What every warp would compute alike one warp computes: 32 warps' instructions cost
+  // more than the barrier.
+  auto pairs_before = [&](Sum2 mine, Sum2* all) {
+    Sum2 inc{0.f, 0.f};
+    if (__any_sync(0xffffffffu, mine.hi > 0.f)) inc = warp_sums(mine);
+    if (lane == 31) s_block[warp] = make_float2(inc.hi, inc.lo);
+    __syncthreads();
+    if (warp == 0) {
+      Sum2 c = lane < sa::WARPS ? Sum2{s_block[lane].x, s_block[lane].y} : Sum2{0.f, 0.f};
+      c = warp_sums(c);
+      const Sum2 e = {__shfl_up_sync(0xffffffffu, c.hi, 1), __shfl_up_sync(0xffffffffu, c.lo, 1)};
+      __syncwarp();
+      if (lane <= sa::WARPS) s_block[lane] = lane ? make_float2(e.hi, e.lo) : make_float2(0.f, 0.f);
+    }
+    __syncthreads();
+    *all = Sum2{s_block[sa::WARPS].x, s_block[sa::WARPS].y};
+    const Sum2 c = {s_block[warp].x, s_block[warp].y};
+    const Sum2 e = {__shfl_up_sync(0xffffffffu, inc.hi, 1), __shfl_up_sync(0xffffffffu, inc.lo, 1)};
+    return lane ? sum_of(c, e) : c;
+  };
+  // The list's `count` items, mine(t) each, in falling order, in threads too; a thread
+  // compares an item to a share of the others.
+  auto ranked = [&](int count, unsigned long long mine) {
+    const int bits = max(5, 32 - __clz(max(count - 1, 0)));
+    const int item = t & ((1 << bits) - 1), parts = sa::THREADS >> bits;
+    const int per = ((count + parts - 1) / parts + 7) & ~7, j0 = (t >> bits) * per;
+    s_list[t] = mine;  // (0 past the last)
+    __syncthreads();
+    if (item < count) {
+      const unsigned long long x = s_list[item];
+      int before = 0;
+#pragma unroll 1
+      for (int j = j0; j < min(j0 + per, count); j += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s_list + j + i);
+          before += (o.x > x) + (o.y > x);
+        }
+      }
+      if (before) atomicAdd(&s_rank[item], before);
+    }
+    __syncthreads();
+    if (t < count) {
+      s_list[s_rank[t]] = mine;
+      s_rank[t] = 0;
+    }
+    __syncthreads();
+    return t < count ? s_list[t] : 0ull;
+  };
+  // One more for every CTA's list.
+  auto enlist = [&](raw l, int x) {
+    const int at = add_remote(remote(&s_listed[round & 3], 0), 1);
+    if (at < sa::LIST) {
+#pragma unroll 1
+      for (int r = 0; r < C; ++r)
+        put(remote(&s_list[at], r), __uint_as_float(~(uint32_t)(first + x)), __uint_as_float(Lg::key(l)));
+    }
+  };
   auto shift_of = [](uint32_t lo, uint32_t hi) { return max(0, 21 - __clz((int)(hi - lo))); };
+  // Lane sums v from `base` on: the first lane at which they exceed `aim`, or the last
+  // with any; *base: the sum before it.
+  auto find = [&](Sum2 v, Sum2 aim, Sum2* base) {
+    const Sum2 inc = warp_sums(v);
+    Sum2 c = {__shfl_up_sync(0xffffffffu, inc.hi, 1), __shfl_up_sync(0xffffffffu, inc.lo, 1)};
+    c = lane ? sum_of(*base, c) : *base;
+    const bool some = v.hi > 0.f;
+    const uint32_t hits = __ballot_sync(0xffffffffu, some && exceeds(sum_of(c, v), aim));
+    const uint32_t lasts = __ballot_sync(0xffffffffu, some);
+    const int l = hits ? __ffs(hits) - 1 : (lasts ? 31 - __clz((int)lasts) : 0);
+    *base = lane_of(c, l);
+    return l;
+  };
+  // Tokens that share a key: how many lie before this lane's segment(s) and lanes.
+  auto count_before = [&](int mine) {
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x - mine;
+  };
 
-  const bool alive = top != -INFINITY;
-  const uint32_t kmax = Lg::key(Lg::from(top));
+  // The key below which min_p leaves nothing: w >= min_p is l >= top + T ln(min_p).
+  auto lowest_key = [&] {
+    if (!(mp > 0.f)) return kneg;
+    const Sum2 x = sum_of(Sum2{top, 0.f}, Sum2{s_low.x, s_low.y});
+    const raw r = Lg::from(x.hi);  // (rounded up)
+    return min(kmax, Lg::key(r) + (Lg::value(r) == x.hi && x.lo > 0.f ? 1u : 0u));
+  };
   // What is kept: keys above `border`, and the first `ties` (by index) of those at it.
-  uint32_t border = 0;
+  uint32_t border = kneg;
   int ties = INT_MAX;
   bool limited = false;  // whether `ties` leaves any out
-  const int k = p.top_k ? p.top_k[row] : 0;
-  const float tp = p.top_p ? p.top_p[row] : 1.f;
-  const float mp = p.min_p ? p.min_p[row] : 0.f;
+  bool done = !alive;    // the token has been written
+  int cut = INT_MAX;     // the token of the last tie that is kept, where that is known
+  Sum2 total{0.f, 0.f}, mine{0.f, 0.f};
+  // mine: this thread's tokens of keys above `summed`, where that is not 0.
+  uint32_t summed = 0;
+  // This thread's tokens with the border's key.
+  auto count_ties = [&] {
+    int c = 0;
+    const float at = value_of(border);
+    each([&](int, uint4 g) {
+#pragma unroll
+      for (int x = 0; x < GROUP / 2; ++x) {
+        const float2 v = Lg::pair(g, x);
+        c += (v.x == at) + (v.y == at);
+      }
+    });
+    return c;
+  };
+  // The token of the last tie that is kept (c: this thread's ties; s_cnt has the warps').
+  auto find_cut = [&](int c) {
+    int in[4], sum = 0;
+    const int per = (segs + 31) / 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      in[i] = i < per && lane * per + i < segs ? s_cnt[lane * per + i] : 0;
+      sum += in[i];
+    }
+    int before = count_before(sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // (Before this warp's: as its lane says.)
+      if (lane * per + i == seg_id && i < per) s_rank[warp] = before;
+      before += in[i];
+    }
+    __syncwarp();
+    int skip = ties - s_rank[warp] - count_before(c);  // its skip-th tie is the last
+    __syncwarp();
+    if (lane == 0) s_rank[warp] = 0;
+    if (skip >= 1 && skip <= c) {
+      const raw at = Lg::unkey(border);
+      const raw* const e = reinterpret_cast<const raw*>(part) + t * own * GROUP;
+      int i = 0;
+#pragma unroll 1
+      for (; i < own * GROUP; ++i)
+        if (e[i] == at && --skip == 0) break;
+      for (int r = 0; r < C; ++r) put(remote(&s_cut, r), first + t * own * GROUP + i);
+    }
+    sync();
+    return s_cut;
+  };
   if (alive && (greedy || k == 1 || tp <= 0.f)) {
     border = kmax;
     ties = 1;
     limited = true;
   } else if (alive) {
     if (k > 0 && k < p.V) {
-      // The k-th largest is at least the w-th largest of the warps' smallest lane
-      // maxima, w = ceil(k / 32): 32 tokens of each of w warps are.
-      uint32_t lo = Lg::key(NEG), hi = kmax;
+      // The k-th largest of the lanes' maxima is no larger than the k-th largest logit,
+      // and for a small k few more than k logits are above it.
+      uint32_t lo = kneg + 1, hi = kmax;
       const int w = (k + 31) / 32;
-      if (w <= segs) {
-        if (t < segs) {
-          const float mine = s_first[t].y;
-          int above = 0;
-          for (int i = 0; i < segs; ++i) {
-            const float o = s_first[i].y;
-            above += o > mine || (o == mine && i < t);
+      if (k <= 3 * sa::LIST / 4 && 3 * k <= sa::THREADS * C) {
+        // Where the k-th of the maxima is, in 2048 bins: not below the w-th largest of
+        // the warps' smallest ones (nearly; 18 steps of a bisection).
+        uint32_t from = Lg::key(Lg::from(least)), over = kmax + 1;
+        uint32_t key4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          key4[i] = 32 * i + lane < segs ? Lg::key(Lg::from(s_first[32 * i + lane].y)) : 0u;
+        if (was_inf || warp != 0) over = from;
+#pragma unroll 1
+        for (int i = 0; i < 18 && over - from > 1; ++i) {
+          const uint32_t mid = from + (over - from) / 2;
+          int count = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) count += __popc(__ballot_sync(0xffffffffu, key4[j] >= mid));
+          if (count >= w) {
+            from = mid;
+          } else {
+            over = mid;
           }
-          if (above == w - 1) s_key[0] = Lg::key(Lg::from(mine));
+        }
+        if (t == 0) s_key[0] = from;
+        __syncthreads();
+        from = s_key[0];
+        const float vfrom = value_of(from), per = __fdividef((float)(sa::BINS - 1), top - vfrom);
+        if (mx >= vfrom) atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::BINS - 1)], 1u);
+        sync();
+        uint32_t h[4];
+        gather(h);
+        turn();
+        uint32_t before = sum_before(h[0] + h[1] + h[2] + h[3], s_scan);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // the bin that the k-th falls into
+          if (before < (uint32_t)k && (uint32_t)k <= before + h[e]) s_i[0] = 4 * t + e;
+          before += h[e];
         }
         __syncthreads();
-        lo = s_key[0];
+        lo = max(lo, Lg::key(Lg::from(top - __fdividef((float)s_i[0] + 1.01f, per))));
+        const float least_listed = value_of(lo);
+        each([&](int i, uint4 g) {
+          each_of(within(g, least_listed, INFINITY), i, enlist);
+        });
+        sync();
+        const int have = get(remote(&s_listed[round & 3], 0));
+        turn();
+        if (have <= sa::LIST) {
+          // (All CTAs alike.)
+          int count = have;
+          unsigned long long x = t < have ? s_list[t] : 0;
+          Sum2 all;
+#pragma unroll 1
+          for (int by_index = 0; by_index < 2; ++by_index) {
+            // The list in order: by logit, then what is kept of it by index.
+            x = ranked(count, x);
+            const uint32_t key = (uint32_t)(by_index ? x : x >> 32), place = ~(uint32_t)(by_index ? x >> 32 : x);
+            bool keep = t < (by_index ? count : min(have, k));
+            Sum2 w{0.f, 0.f};
+            if (keep) w = weigh.one(value_of(key));
+            const Sum2 before = pairs_before(w, &all);
+            if (!by_index) {
+              if (tp < 1.f) keep = keep && (t == 0 || exceeds(times(all, tp), before));
+              keep = keep && (t == 0 || key >= lowest_key());
+              count = __syncthreads_count(keep);
+              if (t == count - 1) {
+                s_key[1] = key;
+                s_i[3] = (int)place;
+                s_i[0] = INT_MAX;
+                s_i[1] = -1;
+              }
+              x = t < count ? x << 32 | x >> 32 : 0;
+            } else {
+              // The first that exceeds the aim, or the last with any weight.
+              const bool some = w.hi > 0.f;
+              if (some && exceeds(sum_of(before, w), times(all, uu))) atomicMin(&s_i[0], t);
+              if (some) atomicMax(&s_i[1], t);
+              __syncthreads();
+              if (rank == 0 && t == (s_i[0] < INT_MAX ? s_i[0] : s_i[1])) p.tokens[row] = (int)place;
+            }
+          }
+          done = true;
+          total = all;
+          cut = s_i[3];
+          border = s_key[1];
+        }
       }
+      // The border by counts: 2048 bins per pass.  (With fewer than k finite logits all stay.)
       int above = 0;
-      for (;;) {
+      while (!done) {
         const int shift = shift_of(lo, hi);
         const uint32_t span = hi - lo;
         uint32_t* const hist = s_hist[round & 1];
-        each([&](int, raw r) {
-          const uint32_t d = hi - Lg::key(r);
-          if (d <= span) atomicAdd(&hist[d >> shift], 1u);
+        if (t == 0) s_i[0] = -1;
+        each([&](int i, uint4 g) {
+#pragma unroll
+          for (int x = 0; x < GROUP; ++x) {
+            const uint32_t d = hi - Lg::key(reinterpret_cast<const raw*>(&g)[x]);
+            if (d <= span) atomicAdd(&hist[d >> shift], 1u);
+          }
         });
         sync();
         uint32_t h[4];
         gather(h);
-        ++round;
+        turn();
         uint32_t before = (uint32_t)above + sum_before(h[0] + h[1] + h[2] + h[3], s_scan);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the bin that the k-th falls into
+        for (int e = 0; e < 4; ++e) {
           if (before < (uint32_t)k && (uint32_t)k <= before + h[e]) {
             s_i[0] = 4 * t + e;
             s_i[1] = (int)before;
@@ -423,10 +803,10 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
           before += h[e];
         }
         __syncthreads();
-        const uint32_t b = (uint32_t)s_i[0];
+        const int b = s_i[0], in = s_i[2];
+        if (b < 0) break;
         above = s_i[1];
-        const int in = s_i[2];
-        const uint32_t new_hi = hi - (b << shift), width = (1u << shift) - 1;
+        const uint32_t new_hi = hi - ((uint32_t)b << shift), width = (1u << shift) - 1;
         lo = new_hi - lo > width ? new_hi - width : lo;
         hi = new_hi;
         if (lo == hi) {
@@ -435,354 +815,406 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
           limited = in > ties;
           break;
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
-    if (tp < 1.f) {
-      // Keys in [elo, ehi] hold the border, or all that is kept is above them; s_d[0] is
-      // the weight above.  Below elo come only, with top-k, the tokens at its border.
-      const bool had_k = ties != INT_MAX;
-      const uint32_t k_border = border;
-      const int k_ties = ties;
-      uint32_t elo = had_k ? border + 1 : Lg::key(NEG), ehi = kmax;
-      uint32_t blo = elo, bhi = ehi;
-      if (t == 0) {
-        s_d[0] = 0.0;                                                              // above
-        s_d[1] = -1.0;                                                             // the target
-        s_d[2] = had_k ? wide(weigh(Lg::value(Lg::unkey(border)))) : 0.0;          // a tie's weight
+    const uint32_t lowest = lowest_key();
+    if (!done && tp < 1.f) {
+      if (border > kneg) {
+        // What top-k leaves out goes.
+        if (limited) {
+          const int c = count_ties(), in_warp = __reduce_add_sync(0xffffffffu, c);
+          if (lane < C) put(remote(&s_cnt[seg_id], lane), in_warp);
+          sync();
+          cut = find_cut(c);
+        }
+        each([&](int i, uint4) {
+          raw* const e = reinterpret_cast<raw*>(part + i);
+#pragma unroll
+          for (int x = 0; x < GROUP; ++x) {
+            const uint32_t key = Lg::key(e[x]);
+            if (key < border || (key == border && first + i * GROUP + x > cut)) e[x] = NEG;
+          }
+        });
+        border = kneg;
+        limited = false;
+        cut = INT_MAX;
       }
-      if (!had_k) {
-        // Where the border may be, from counts in 2048 bins of 1/64 of the
-        // temperature: weights e^(-1/64) of one another.
+      // Keys in [elo, ehi] hold the border; `above` is the weight of those above.
+      uint32_t elo = kneg, ehi = kmax, blo = elo, bhi = ehi;
+      Sum2 above{0.f, 0.f}, target{0.f, 0.f};
+      bool list = false;  // whether few keys lie in [blo, bhi], to the last estimate
+      {
+        // Where the border may be, from counts in 2048 bins: of 1/256 of the temperature
+        // for the heavy tokens (two temperatures from the top), of 1/64 below.
         uint32_t* const hist = s_hist[round & 1];
-        const float to_bin = weigh.s_hi * (64.f * 0.6931471805599453f);
-        each([&](int, raw r) {
-          const float d = (top - Lg::value(r)) * to_bin;
-          if (d < (float)(sa::BINS - 1)) atomicAdd(&hist[(int)d], 1u);
+        const float per = -0.6931471805599453f * weigh.s_hi;
+        const float2 fine = twice(256.f * per), coarse = twice(64.f * per);
+        // Bins of the top: 1 and 385, but for what the sums' rounding to whole numbers adds.
+        const float fine0 = 8388609.f - fine.x * top, coarse0 = 8388993.f - coarse.x * top;
+        const float fine_top = __fmaf_rn(fine.x, top, fine0 - 8388608.f);
+        const float coarse_top = __fmaf_rn(coarse.x, top, coarse0 - 8388608.f);
+        auto below_top = [&](int b) {  // in temperatures, the middle of a bin
+          return b < 513 ? ((float)b - fine_top) * (1.f / 256.f) : ((float)b - coarse_top) * (1.f / 64.f);
+        };
+        if (t == 0) s_i[3] = -1;
+        each([&](int, uint4 g) {
+#pragma unroll
+          for (int x = 0; x < GROUP / 2; ++x) {
+            const float2 v = Lg::pair(g, x);
+            const float2 z = __ffma2_rn(v, fine, twice(fine0)), y = __ffma2_rn(v, coarse, twice(coarse0));
+            const uint32_t a = __float_as_uint(fminf(z.x, y.x)) - 0x4b000000u;
+            const uint32_t b = __float_as_uint(fminf(z.y, y.y)) - 0x4b000000u;
+            if (a < sa::BINS) atomicAdd(&hist[a], 1u);
+            if (b < sa::BINS) atomicAdd(&hist[b], 1u);
+          }
         });
         sync();
         uint32_t h[4];
         gather(h);
-        ++round;
-        float m4[4], mine = 0.f;
+        turn();
+        float m4[4], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          m4[e] = (float)h[e] * __expf(-((float)(4 * t + e) + 0.5f) * (1.f / 64.f));
-          mine += m4[e];
+          m4[e] = (float)h[e] * __expf(-below_top(4 * t + e));
+          sum += m4[e];
         }
-        if (t == 0) {
-          s_key[0] = elo;
-          s_key[1] = ehi;
-        }
-        float before = sum_before(mine, s_fscan);
-        float want = 0.f;
+        float before = sum_before(sum, s_fscan), want = 0.f;
+#pragma unroll
         for (int i = 0; i < sa::WARPS; ++i) want += s_fscan[i];
         want *= tp;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (before < want && want <= before + m4[e]) {
-            // Two bins to either side; the next pass finds out whether that was enough.
-            const int b = 4 * t + e;
-            const float w = temp * (1.f / 64.f);
-            s_key[0] = Lg::key(Lg::from(top - w * (float)(b + 3)));
-            s_key[1] = Lg::key(Lg::from(top - w * (float)(b - 2)));
-          }
+          if (before < want && want <= before + m4[e]) s_i[3] = (4 * t + e) << 1 | (3 * h[e] <= 3 * sa::LIST / 4 ? 1 : 0);
           before += m4[e];
         }
         __syncthreads();
-        bhi = min(max(s_key[1], elo), ehi);
-        blo = min(max(s_key[0], elo), bhi);
+        if (s_i[3] >= 0) {
+          // One bin to either side; the next pass finds out whether that was enough.
+          const int b = s_i[3] >> 1;
+          const float d = below_top(b), w = b < 511 ? 1.5f / 256.f : 1.5f / 64.f;
+          list = s_i[3] & 1;
+          bhi = min(max(Lg::key(Lg::from(top - temp * (d - w))), elo), ehi);
+          blo = min(max(Lg::key(Lg::from(top - temp * (d + w))), elo), bhi);
+        }
       }
-      enum { IN_TAIL, ABOVE, BELOW, INSIDE, DONE };
-      int what = had_k && border == kmax ? IN_TAIL : INSIDE;
-      if (what == IN_TAIL) __syncthreads();
-      for (bool have_total = false; what != IN_TAIL && what != DONE; have_total = true) {
+      bool dense = false;
+      for (bool have_total = false;; have_total = true) {
+        // Above min_p's border only what lies there counts.
+        if (bhi + 1 < lowest) bhi = blo = max(lowest - 1, elo);
         const int shift = shift_of(blo, bhi);
-        const uint32_t bspan = bhi - blo, espan = ehi - elo;
+        const uint32_t bspan = bhi - blo;
+        const bool lists = list && shift > 0, exact = lists || shift == 0;
+        list = false;
         uint32_t* const hist = s_hist[round & 1];
-        Sum2 sum[3] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};  // above, in and below the bins
-        each([&](int, raw r) {
-          const uint32_t key = Lg::key(r);
-          if (ehi - key > espan) return;
-          const bool in = bhi - key <= bspan, over = key > bhi;
-          if (in) atomicAdd(&hist[(bhi - key) >> shift], 1u);
-          if (!have_total || in || over) {
-            const Sum2 wt = weigh(Lg::value(r));
-            if (in)
-              sum[1] = sum_of(sum[1], wt);
-            else if (over)
-              sum[0] = sum_of(sum[0], wt);
-            else
-              sum[2] = sum_of(sum[2], wt);
-          }
-        });
+        const float vhi = value_of(bhi), vlo = value_of(blo), vtop = value_of(ehi);
+        if (t == 0) s_found = NONE;
+        // Weights above the bins and (the first time) of everything; counts in them.
+        Sum2 my_over{0.f, 0.f}, my_every{0.f, 0.f};
+        if (!have_total) {
+          Sums over, every;
+          each([&](int i, uint4 g) {
+            uint32_t m = 0;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          const Sum2 s = warp_sum(sum[q]);
-          if (lane < C) put(remote(&s_warp[round & 1][q][seg_id], lane), s.hi, s.lo);
+            for (int x = 0; x < GROUP / 2; ++x) {
+              const float2 v = Lg::pair(g, x);
+              float2 hi, q;
+              weigh(v, &hi, &q);
+              every.add(hi, q);
+              const bool a = v.x > vhi, b = v.y > vhi;
+              if (!a && v.x >= vlo) m |= 1u << (2 * x);
+              if (!b && v.y >= vlo) m |= 2u << (2 * x);
+              over.add(make_float2(a ? hi.x : 0.f, b ? hi.y : 0.f), q);
+            }
+            each_of(m, i, [&](raw l, int x) {
+              if (lists) {
+                enlist(l, x);
+              } else {
+                atomicAdd(&hist[(bhi - Lg::key(l)) >> shift], 1u);
+              }
+            });
+          });
+          my_over = over.all();
+          my_every = every.all();
+        } else {
+          each([&](int i, uint4 g) {
+            each_of(within(g, vlo, vtop), i, [&](raw l, int x) {
+              const uint32_t key = Lg::key(l);
+              if (key > bhi) {
+                my_over = sum_of(my_over, weigh.one(Lg::value(l)));
+              } else if (lists) {
+                enlist(l, x);
+              } else {
+                atomicAdd(&hist[(bhi - key) >> shift], 1u);
+              }
+            });
+          });
+        }
+        const int r = round & 1;
+        {
+          Sum2 x = my_over, y = my_every;
+          warp_sum(x, y);
+          if (lane < C) {
+            put(remote(&s_warp[r][0][seg_id], lane), x.hi, x.lo);
+            put(remote(&s_warp[r][1][seg_id], lane), y.hi, y.lo);
+          }
         }
         sync();
-        uint32_t h[4];
-        gather(h);
-        if (warp < 3) {  // one warp for each sum
-          Sum2 s{0.f, 0.f};
+        uint32_t h[4] = {0, 0, 0, 0};
+        int have = 0;
+        if (lists) {
+          have = get(remote(&s_listed[round & 3], 0));
+        } else {
+          gather(h);
+        }
+        turn();
+        if (warp == 0) {  // the sums of all warps
+          Sum2 x{0.f, 0.f}, y{0.f, 0.f};
+#pragma unroll 1
           for (int i = lane; i < segs; i += 32) {
-            const float2 v = s_warp[round & 1][warp][i];
-            s = sum_of(s, Sum2{v.x, v.y});
+            const float2 v = s_warp[r][0][i], w = s_warp[r][1][i];
+            x = sum_of(x, Sum2{v.x, v.y});
+            y = sum_of(y, Sum2{w.x, w.y});
           }
-          s = warp_sum(s);
-          if (lane == 0) s_d[4 + warp] = wide(s);
-        }
-        ++round;
-        // Counts times the weight in the middle of each bin suggest the next bins.
-        float m4[4], mine = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t off = (uint32_t)(4 * t + e) << shift;
-          m4[e] = 0.f;
-          if (h[e])
-            m4[e] = (float)h[e] *
-                    weigh(Lg::value(Lg::unkey(bhi - min(off + ((1u << shift) >> 1), bspan)))).hi;
-          mine += m4[e];
-        }
-        float before = sum_before(mine, s_fscan);  // (and s_d is there)
-        if (t == 0) {
-          if (!have_total) s_d[1] = (double)tp * (s_d[4] + s_d[5] + s_d[6] + s_d[2] * (had_k ? k_ties : 0));
-          const double A = s_d[0] + s_d[4], target = s_d[1];
-          int w = INSIDE;
-          if (A >= target && bhi != ehi) {
-            w = ABOVE;
-          } else if (A + s_d[5] < target) {
-            w = blo == elo ? IN_TAIL : BELOW;
-            s_d[0] = A + s_d[5];
-          } else {
-            s_d[0] = A;
-            if (blo == bhi) {
-              w = DONE;
-              const double m = ceil((target - A) / wide(weigh(Lg::value(Lg::unkey(blo)))));
-              s_i[1] = m < 1.0 ? 1 : (m > (double)h[0] ? (int)h[0] : (int)m);
-              s_i[2] = s_i[1] < (int)h[0];
-            }
+          warp_sum(x, y);
+          if (lane == 0) {
+            s_pair[0] = make_float2(x.hi, x.lo);
+            s_pair[1] = make_float2(y.hi, y.lo);
+            s_i[0] = INT_MAX;
           }
-          s_f[2] = (float)(target - A);
-          s_i[0] = w;
-          s_i[3] = (int)(bspan >> shift);
         }
         __syncthreads();
-        what = s_i[0];
-        if (what == ABOVE) {
+        const Sum2 A = sum_of(above, Sum2{s_pair[0].x, s_pair[0].y});
+        if (!have_total) target = times(Sum2{s_pair[1].x, s_pair[1].y}, tp);
+        if (have > sa::LIST) {  // (more than the estimate: by counts, then)
+          __syncthreads();
+          continue;
+        }
+        if (!exceeds(target, A) && bhi != ehi) {  // the border lies above the bins
           blo = elo = bhi + 1;
           bhi = ehi;
-        } else if (what == BELOW) {
-          bhi = ehi = blo - 1;
-          blo = elo;
-        } else if (what == DONE) {
-          border = blo;
-          ties = s_i[1];
-          limited = s_i[2];
-        } else if (what == INSIDE) {
-          elo = blo;
-          ehi = bhi;
-          const float want = s_f[2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (before < want && want <= before + m4[e]) s_i[3] = 4 * t + e;
-            before += m4[e];
-          }
           __syncthreads();
-          // One bin to either side, or the one key.
-          const uint32_t b = (uint32_t)s_i[3], side = shift > 0 ? 1u : 0u;
-          const uint32_t o0 = (b > side ? b - side : 0u) << shift;
-          const unsigned long long o1 = ((unsigned long long)(b + side + 1) << shift) - 1;
+          continue;
+        }
+        mine = sum_of(mine, my_over);
+        above = A;
+        ehi = bhi;
+        if (bhi < lowest) {  // (bhi + 1 is lowest)
+          border = lowest;
+          break;
+        }
+        // Counts times the bins' weights (exact where a bin is one key).
+        auto weight_of = [&](int e) {
+          const uint32_t off = ((uint32_t)(4 * t + e) << shift) + ((1u << shift) >> 1);
+          return weigh.one(value_of(bhi - min(off, bspan)));
+        };
+        auto count_of = [&](int e) { return (int)(e == 0 ? h[0] : e == 1 ? h[1] : e == 2 ? h[2] : h[3]); };
+        Sum2 sum{0.f, 0.f}, in;
+        if (h[0] | h[1] | h[2] | h[3]) {
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e)
+            if (count_of(e)) sum = sum_of(sum, times(weight_of(e), (float)count_of(e)));
+        }
+        if (lists) {
+          const unsigned long long x = ranked(have, t < have ? s_list[t] : 0ull);
+          const Sum2 w = t < have ? weigh.one(value_of((uint32_t)(x >> 32))) : Sum2{0.f, 0.f};
+          const Sum2 before = sum_of(above, pairs_before(w, &in));
+          // The first at which the target is reached is the last that is kept.
+          if (t < have && !exceeds(target, sum_of(before, w))) atomicMin(&s_i[0], t);
+          __syncthreads();
+          const int last = s_i[0];
+          if (last < have) {
+            border = (uint32_t)(s_list[last] >> 32);
+            ties = 1;
+            while (ties <= last && (uint32_t)(s_list[last - ties] >> 32) == border) ++ties;
+            limited = last + 1 < have && (uint32_t)(s_list[last + 1] >> 32) == border;
+            break;
+          }
+        }
+        Sum2 before = lists ? target : sum_of(above, pairs_before(sum, &in));
+        if (sum.hi > 0.f && exceeds(target, before) && !exceeds(target, sum_of(before, sum))) {
+          int e = 0, m;
+          for (;; ++e) {  // (the last one that has any, if the sums' rounding says none)
+            m = count_of(e);
+            const Sum2 w = weight_of(e), after = sum_of(before, times(w, (float)m));
+            if (m && (!exceeds(target, after) || e == 3 || (h[3] | (e < 2 ? h[2] : 0) | (e < 1 ? h[1] : 0)) == 0)) {
+              // So many of the key as it takes to come to the target.
+              const Sum2 need = sum_of(target, Sum2{-before.hi, -before.lo});
+              const int most = m;
+              m = max(1, min(most, (int)ceilf(__fdividef(need.hi, w.hi))));
+              while (m > 1 && !exceeds(target, sum_of(before, times(w, (float)(m - 1))))) --m;
+              while (m < most && exceeds(target, sum_of(before, times(w, (float)m)))) ++m;
+              s_found = (uint32_t)(4 * t + e) << 21 | (uint32_t)m << 1 |
+                      ((shift > 0 ? 3 * most <= 3 * sa::LIST / 4 : m < most) ? 1u : 0u);
+              break;
+            }
+            before = after;
+          }
+        }
+        __syncthreads();
+        const uint32_t found = s_found;
+        const int b = found == NONE ? -1 : (int)(found >> 21);
+        if (b >= 0 && shift == 0) {
+          border = bhi - (uint32_t)b;
+          ties = (int)(found >> 1 & 0xfffffu);
+          limited = found & 1u;
+          break;
+        }
+        if (b >= 0) {  // one bin to either side
+          list = found & 1u;
+          const uint32_t o0 = (uint32_t)max(b - 1, 0) << shift;
+          const unsigned long long o1 = ((unsigned long long)(b + 2) << shift) - 1;
           blo = o1 >= bspan ? blo : ehi - (uint32_t)o1;
           bhi = ehi - min(o0, bspan);
-          if (blo == elo && bhi == ehi && blo < bhi) blo = bhi - (bhi - blo) / 2;  // (few bins)
+        } else if (!exact) {  // its end, or below
+          bhi = bspan >> 1 > 1u << shift ? blo + (1u << shift) : blo + (bspan >> 1);
+          blo = elo;
+        } else if (blo == elo) {  // (the sums' rounding) everything
+          dense = true;
+          break;
+        } else if (blo <= lowest) {  // below the bins, and min_p's border in them
+          border = lowest;
+          dense = true;
+          break;
+        } else {  // below the bins
+          above = sum_of(above, in);
+          dense = true;
+          ehi = bhi = blo - 1;
+          blo = elo;
         }
         __syncthreads();
       }
-      if (what == IN_TAIL && had_k) {  // among the tokens at top-k's border
-        if (t == 0) {
-          // (Nothing above it: the weights are all 1.)
-          const double m = k_border == kmax ? ceil((double)tp * k_ties)
-                                            : ceil((s_d[1] - s_d[0]) / s_d[2]);
-          s_i[0] = m < 1.0 ? 1 : (m > (double)k_ties ? k_ties : (int)m);
-        }
-        __syncthreads();
-        ties = s_i[0];
-        limited = limited || ties < k_ties;
-      }
+      summed = dense ? 0u : bhi;
     }
-    if (mp > 0.f) {
-      // w >= min_p: l >= top + T ln(min_p).
-      if (t == 0)
-        s_key[0] = top == INFINITY ? kmax
-                                   : Lg::key(Lg::at_least(fmin((double)top, (double)top + (double)temp * log((double)mp))));
-      __syncthreads();
-      const uint32_t lowest = min(s_key[0], kmax);
-      if (lowest > border) {
-        border = lowest;
-        ties = INT_MAX;
-        limited = false;
-      }
+    if (!done && lowest > border) {
+      border = lowest;
+      limited = false;
     }
   }
-  // ---- ties by index: the place of the last one that is kept ----
-  long long cut = LLONG_MAX;
-  if (limited) {
+  if (!done) {
+    // ---- every warp's kept weight, and the token ----
+    // Keys from `from` on count whole; where ties are cut, those at the border by number.
+    const uint32_t from = border + (limited ? 1 : 0);
+    const float at = value_of(border);
     int c = 0;
-    each([&](int, raw r) { c += Lg::key(r) == border; });
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane < C) put(remote(&s_cnt[seg_id], lane), c);
-    sync();
-    int before = 0, owner = -1, skip = 0;
-    for (int i = 0; i < segs; ++i) {
-      if (before < ties && ties <= before + s_cnt[i]) {
-        owner = i;
-        skip = ties - before;  // its skip-th tie is the last
-      }
-      before += s_cnt[i];
-    }
-    if (owner == seg_id) {
-      int found = -1;
-      for (int gb = g0; gb < g1 && found < 0; gb += 32) {
-        const uint4 v = part[gb + lane];
-        int mine = 0;
+    if (summed == 0) {
+      const float vfrom = limited && border == kmax ? INFINITY : value_of(from);
+      Sums s;
+      each([&](int, uint4 g) {
 #pragma unroll
-        for (int e = 0; e < GROUP; ++e) mine += Lg::key(Lg::at(v, e)) == border;
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
+        for (int x = 0; x < GROUP / 2; ++x) {
+          const float2 v = Lg::pair(g, x);
+          float2 hi, q;
+          weigh(v, &hi, &q);
+          s.add(make_float2(v.x >= vfrom ? hi.x : 0.f, v.y >= vfrom ? hi.y : 0.f), q);
         }
-        int at = -1, left = skip - (inc - mine);
-        if (left > 0 && left <= mine) {
-#pragma unroll
-          for (int e = 0; e < GROUP; ++e)
-            if (Lg::key(Lg::at(v, e)) == border && --left == 0) at = (gb + lane) * GROUP + e;
-        }
-        const uint32_t who = __ballot_sync(0xffffffffu, at >= 0);
-        if (who) found = __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
-        skip -= __shfl_sync(0xffffffffu, inc, 31);
-      }
-      if (lane < C) {
-        put(remote(&s_cut[0], lane), found);
-        put(remote(&s_cut[1], lane), rank);
-      }
-    }
-    sync();
-    cut = (long long)s_cut[1] * n + s_cut[0];
-  }
-  // ---- kept weights by index, and the token ----
-  auto weight_of = [&](int i, raw r) {  // of place i of this part, 0 if it is not kept
-    const uint32_t key = Lg::key(r);
-    const bool kept = r != NEG && (key > border || (key == border && first + i <= cut));
-    return kept ? weigh(Lg::value(r)) : Sum2{0.f, 0.f};
-  };
-  Sum2 total{0.f, 0.f};
-  if (alive) {
-    Sum2 s{0.f, 0.f};
-    each([&](int i, raw r) {
-      const Sum2 w = weight_of(i, r);
-      if (w.hi > 0.f) s = sum_of(s, w);
-    });
-    s = warp_sum(s);
-    if (lane < C) put(remote(&s_warp[round & 1][0][seg_id], lane), s.hi, s.lo);
-    sync();
-    // The first of values v[0 .. count) (one or more per lane) whose cumulative sum, from
-    // `base` on, exceeds `aim`; the last above 0 if none does.  *base: the sum before it.
-    auto find = [&](const float2* v, int count, Sum2 aim, Sum2* base) {
-      const int per = (count + 31) / 32, i0 = lane * per;
-      Sum2 mine{0.f, 0.f};
-      for (int i = i0; i < min(i0 + per, count); ++i) mine = sum_of(mine, Sum2{v[i].x, v[i].y});
-      const Sum2 inc = warp_sums(mine);
-      Sum2 c = {__shfl_up_sync(0xffffffffu, inc.hi, 1), __shfl_up_sync(0xffffffffu, inc.lo, 1)};
-      c = lane ? sum_of(*base, c) : *base;
-      int hit = -1, last = -1;
-      Sum2 at_hit = c, at_last = c;
-      for (int i = i0; i < min(i0 + per, count); ++i) {
-        const Sum2 w = {v[i].x, v[i].y}, after = sum_of(c, w);
-        if (w.hi > 0.f) {
-          last = i;
-          at_last = c;
-          if (hit < 0 && exceeds(after, aim)) {
-            hit = i;
-            at_hit = c;
+      });
+      mine = s.all();
+      if (limited) c = count_ties();
+    } else if (border <= summed) {
+      const float vhi = value_of(summed);
+      each([&](int i, uint4 g) {
+        each_of(within(g, at, vhi), i, [&](raw l, int) {
+          const float v = Lg::value(l);
+          if (v == at && limited) {
+            ++c;
+          } else {
+            mine = sum_of(mine, weigh.one(v));
           }
-        }
-        c = after;
+        });
+      });
+    }
+    const int r = round & 1;
+    {
+      const Sum2 s = warp_sum(mine);
+      const int in_warp = __reduce_add_sync(0xffffffffu, c);
+      if (lane < C) {
+        put(remote(&s_warp[r][0][seg_id], lane), s.hi, s.lo);
+        put(remote(&s_cnt[seg_id], lane), in_warp);
       }
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
-      const uint32_t lasts = __ballot_sync(0xffffffffu, last >= 0);
-      const int l = hits ? __ffs(hits) - 1 : (lasts ? 31 - __clz((int)lasts) : 0);
-      *base = hits ? lane_of(at_hit, l) : lane_of(at_last, l);
-      return __shfl_sync(0xffffffffu, hits ? hit : last, l);
-    };
-    if (warp == 0) {
-      const float2* const v = s_warp[round & 1][0];
-      Sum2 all{0.f, 0.f};
-      for (int i = lane; i < segs; i += 32) all = sum_of(all, Sum2{v[i].x, v[i].y});
-      all = warp_sum(all);
-      const float u = p.u[row];
-      const Sum2 aim = times(all, u > 0.f ? fminf(u, 2.f) : 0.f);
+    }
+    sync();
+    const Sum2 tie = weigh.one(at);
+    if (warp == 0) {  // the segment
+      const int per = (segs + 31) / 32, seg0 = lane * per;
+      int ties_here = 0;
+      if (limited) {
+#pragma unroll 1
+        for (int i = seg0; i < min(seg0 + per, segs); ++i) ties_here += s_cnt[i];
+        ties_here = ties - count_before(ties_here);  // to keep from here on
+      }
+      auto segment = [&](int i, int* left) {
+        Sum2 v = {s_warp[r][0][i].x, s_warp[r][0][i].y};
+        if (limited) {
+          v = sum_of(v, times(tie, (float)max(0, min(*left, s_cnt[i]))));
+          *left -= s_cnt[i];
+        }
+        return v;
+      };
+      Sum2 sum{0.f, 0.f};
+      int left = ties_here;
+#pragma unroll 1
+      for (int i = seg0; i < min(seg0 + per, segs); ++i) sum = sum_of(sum, segment(i, &left));
+      const Sum2 all = warp_sum(sum), aim = times(all, uu);
       Sum2 base{0.f, 0.f};
-      const int owner = find(v, segs, aim, &base);
+      const int l = find(sum, aim, &base);
+      // Of that lane's: the first at which they exceed the aim, or the last with any.
+      int owner = -1, owner_left = 0;
+      Sum2 owner_base = base;
+      left = __shfl_sync(0xffffffffu, ties_here, l);
+#pragma unroll 1
+      for (int i = l * per; i < min(l * per + per, segs); ++i) {
+        const int now = left;
+        const Sum2 v = segment(i, &left);
+        if (v.hi > 0.f && (owner < 0 || !exceeds(base, aim))) {
+          owner = i;
+          owner_left = now;
+          owner_base = base;
+        }
+        base = sum_of(base, v);
+      }
       if (lane == 0) {
         s_i[0] = owner;
-        s_f[2] = aim.hi;
-        s_f[3] = aim.lo;
-        s_f[4] = base.hi;
-        s_f[5] = base.lo;
-        s_f[6] = all.hi;
-        s_f[7] = all.lo;
+        s_i[1] = owner_left;
+        s_pair[2] = make_float2(all.hi, all.lo);
+        s_pair[3] = make_float2(aim.hi, aim.lo);
+        s_pair[4] = make_float2(owner_base.hi, owner_base.lo);
       }
     }
     __syncthreads();
-    total = Sum2{s_f[6], s_f[7]};
-    if (s_i[0] / sa::WARPS == rank) {
-      // The segment's steps of 32 groups, a warp each, then the step's elements.
-      const int s0 = (s_i[0] % sa::WARPS) * (p.seg / GROUP), steps = p.seg / GROUP / 32;
-      for (int st = warp; st < steps; st += sa::WARPS) {
-        const int g = s0 + st * 32 + lane;
-        const uint4 v = part[g];
-        Sum2 mine{0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < GROUP; ++e) mine = sum_of(mine, weight_of(g * GROUP + e, Lg::at(v, e)));
-        mine = warp_sum(mine);
-        if (lane == 0) s_steps[st] = make_float2(mine.hi, mine.lo);
+    total = Sum2{s_pair[2].x, s_pair[2].y};
+    if (s_i[0] == seg_id) {
+      // Its lanes, then the tokens of one.
+      const int skip = max(0, s_i[1] - count_before(c));
+      const Sum2 aim = {s_pair[3].x, s_pair[3].y};
+      Sum2 v = mine;
+      if (limited) v = sum_of(v, times(tie, (float)min(skip, c)));
+      Sum2 base = {s_pair[4].x, s_pair[4].y};
+      const int l = find(v, aim, &base);
+      int keep = __shfl_sync(0xffffffffu, skip, l);
+      const raw* const e = reinterpret_cast<const raw*>(part) + (warp * 32 + l) * own * GROUP;
+      int token = -1;
+#pragma unroll 1
+      for (int i0 = 0; i0 < own * GROUP; i0 += 32) {
+        const float x = i0 + lane < own * GROUP ? Lg::value(e[i0 + lane]) : -INFINITY;
+        const bool is_tie = limited && x == at;
+        const uint32_t all_ties = __ballot_sync(0xffffffffu, is_tie);
+        const bool kept = is_tie ? __popc(all_ties & ((1u << lane) - 1)) < keep : x >= at;
+        keep -= __popc(all_ties);
+        Sum2 w = weigh.one(x);
+        if (!kept) w = Sum2{0.f, 0.f};
+        const uint32_t some = __ballot_sync(0xffffffffu, w.hi > 0.f);
+        if (!some) continue;
+        const Sum2 inc = warp_sums(w);
+        const uint32_t hits = __ballot_sync(0xffffffffu, w.hi > 0.f && exceeds(sum_of(base, inc), aim));
+        token = i0 + (hits ? __ffs(hits) - 1 : 31 - __clz((int)some));
+        if (hits) break;
+        base = sum_of(base, lane_of(inc, 31));
       }
-      __syncthreads();
-      if (warp == 0) {
-        const Sum2 aim = {s_f[2], s_f[3]};
-        Sum2 base = {s_f[4], s_f[5]};
-        const int st = find(s_steps, steps, aim, &base);
-        const int g = s0 + st * 32 + lane;
-        const uint4 v = part[g];
-        Sum2 w[GROUP], mine{0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < GROUP; ++e) {
-          w[e] = weight_of(g * GROUP + e, Lg::at(v, e));
-          mine = sum_of(mine, w[e]);
-        }
-        const Sum2 inc = warp_sums(mine);
-        Sum2 c = {__shfl_up_sync(0xffffffffu, inc.hi, 1), __shfl_up_sync(0xffffffffu, inc.lo, 1)};
-        c = lane ? sum_of(base, c) : base;
-        int hit = -1, last = -1;
-#pragma unroll
-        for (int e = 0; e < GROUP; ++e) {
-          c = sum_of(c, w[e]);
-          if (w[e].hi > 0.f) {
-            last = g * GROUP + e;
-            if (hit < 0 && exceeds(c, aim)) hit = last;
-          }
-        }
-        const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
-        const uint32_t lasts = __ballot_sync(0xffffffffu, last >= 0);
-        const int l = hits ? __ffs(hits) - 1 : 31 - __clz((int)lasts);
-        if (lane == l) p.tokens[row] = (int)(first + (hits ? hit : last) - lead);
-      }
+      if (lane == 0) p.tokens[row] = first + (warp * 32 + l) * own * GROUP + token;
     }
-  } else if (rank == 0 && t == 0) {
+    if (p.probs && limited) cut = find_cut(c);
+  } else if (!alive && rank == 0 && t == 0) {
     p.tokens[row] = -1;
   }
   if (p.probs) {
@@ -790,16 +1222,23 @@ __global__ void __launch_bounds__(sa::THREADS) sample_kernel(const __grid_consta
     const float i_hi = alive ? __frcp_rn(total.hi) : 0.f;
     const float i_lo = -i_hi * __fmaf_rn(total.lo, i_hi, __fmaf_rn(total.hi, i_hi, -1.f));
     float* const dst = p.probs + row * p.V;
-    const raw* const mine = reinterpret_cast<const raw*>(smem_raw);
-    for (int i = t; i < n; i += sa::THREADS) {
-      const long long e = first + i - lead;
-      if (e < 0 || e >= p.V) continue;
-      float q = 0.f;
-      if (alive) {
-        const Sum2 w = weight_of(i, mine[i]);
-        q = __fmaf_rn(w.hi, i_hi, __fmaf_rn(w.hi, i_lo, __fmul_rn(w.lo, i_hi)));
+    const raw* const e = reinterpret_cast<const raw*>(part);
+    const float at = value_of(border);
+#pragma unroll 2
+    for (int i = 2 * t; i < n; i += 2 * sa::THREADS) {
+      const float2 v = make_float2(Lg::value(e[i]), Lg::value(e[i + 1]));
+      const int x = first + i;
+      const bool a = alive && (v.x > at || (v.x == at && x <= cut));
+      const bool b = alive && (v.y > at || (v.y == at && x + 1 <= cut));
+      float2 o = make_float2(0.f, 0.f);
+      if (__any_sync(0xffffffffu, a || b)) {
+        float2 hi, q;
+        weigh(v, &hi, &q);
+        if (a) o.x = __fmaf_rn(hi.x, i_hi, __fmaf_rn(hi.x, i_lo, __fmul_rn(__fmul_rn(hi.x, q.x), i_hi)));
+        if (b) o.y = __fmaf_rn(hi.y, i_hi, __fmaf_rn(hi.y, i_lo, __fmul_rn(__fmul_rn(hi.y, q.y), i_hi)));
       }
-      dst[e] = q;
+      if (x >= 0 && x < p.V) dst[x] = o.x;
+      if (x + 1 >= 0 && x + 1 < p.V) dst[x + 1] = o.y;
     }
   }
   // No CTA leaves while another may still read its bins or write its sums.
@@ -818,7 +1257,7 @@ static cudaError_t launch_sample(SampleParams& p, long long rows, cudaStream_t s
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
   }
-  const size_t smem = (size_t)p.seg * sa::WARPS * sizeof(T);
+  const size_t smem = (size_t)p.groups * sa::THREADS * 16;
   return launch_dependent(sample_kernel<T>, dim3((unsigned)(rows * p.cluster)), sa::THREADS, stream,
                           p, p.cluster, smem);
 }
@@ -837,13 +1276,13 @@ extern "C" int fa_sample(const void* logits, const float* uniforms, const float*
   if (dtype != FA_BF16 && dtype != FA_FP16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
   if (rows > INT32_MAX / fa::sa::CLUSTER) return FA_ERR_INVALID_ARG;
   const int es = dtype == FA_FP32 ? 4 : 2, group = 16 / es;
-  // A part per CTA: whole steps of 32 groups for each warp.
-  const int step = 32 * group;
-  auto seg_of = [&](int cluster) {
-    const long long segs = (long long)cluster * fa::sa::WARPS;
-    return ((V + group - 1 + segs - 1) / segs + step - 1) / step * step;
+  // 16-byte groups per thread (the first begins where the row's alignment has it begin).
+  auto groups_of = [&](int cluster) {
+    const long long threads = (long long)cluster * fa::sa::THREADS;
+    return (((long long)V + 2 * group - 2) / group + threads - 1) / threads;
   };
-  if (seg_of(fa::sa::CLUSTER) * fa::sa::WARPS * es > fa::sa::SMEM_MAX) return FA_ERR_UNSUPPORTED;
+  auto part_of = [&](int cluster) { return groups_of(cluster) * fa::sa::THREADS * 16; };
+  if (part_of(fa::sa::CLUSTER) > fa::sa::SMEM_MAX) return FA_ERR_UNSUPPORTED;
   if (rows == 0) return FA_OK;
   if (!al(logits, es) || !al(uniforms, 4) || !al(tokens, 4)) return FA_ERR_INVALID_ARG;
   if ((temperature && !al(temperature, 4)) || (top_k && !al(top_k, 4)) ||
@@ -862,11 +1301,25 @@ extern "C" int fa_sample(const void* logits, const float* uniforms, const float*
   p.stride = row_stride;
   p.V = V;
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 148;
-  p.cluster = fa::sa::CLUSTER;
-  while (p.cluster > 1 && seg_of(p.cluster / 2) * fa::sa::WARPS * es <= fa::sa::SMEM_MAX &&
-         ((long long)rows * p.cluster > 2ll * sms || seg_of(p.cluster / 2) <= 2 * step))
-    p.cluster /= 2;
-  p.seg = (int)seg_of(p.cluster);
+  // CTAs per row, by a model of the clocks: 1.2 per element on the SM that has most of
+  // them (1.6 where it has one CTA at a time to run), 8000 per wave, 1000 more for a
+  // cluster's meetings.  Measured for 1, 2, 4 and 8: one row of 32000 27, 16, 15.9, 13.3 us;
+  // 200 of 50257 30, 26, 38, 61; 512 of 32000 129, 105, 160, 298; 64 of 128000 (2, 4, 8)
+  // 66, 50, 59.
+  double best = 0;
+  for (int c = 1; c <= fa::sa::CLUSTER; c *= 2) {
+    if (part_of(c) > fa::sa::SMEM_MAX) continue;
+    const int fits = part_of(c) + 46 * 1024 > 113 * 1024 ? 1 : 2;
+    const double ctas = (double)rows * c, waves = ctas / (fits * sms);
+    const double per_sm = ceil(ctas / sms) * (double)(groups_of(c) * group * fa::sa::THREADS);
+    const double clocks = per_sm * (fits == 1 || ctas <= sms ? 1.6 : 1.2) +
+                          (waves < 1 ? 1 : waves) * (c > 1 ? 9000 : 8000);
+    if (best == 0 || clocks < best) {
+      best = clocks;
+      p.cluster = c;
+    }
+  }
+  p.groups = (int)groups_of(p.cluster);
   cudaError_t e;
   if (dtype == FA_FP32)
     e = fa::launch_sample<float>(p, rows, stream);

@@ -596,12 +596,12 @@ int fa_decode_shared_fwd(const void* q, const void* kpages, const void* vpages,
  * least one is kept.  The token is the lowest whose cumulative kept weight, by index,
  * exceeds u times all of it.  Logits that are NaN count as -infinity; a row without
  * any other gets the token -1 and probabilities 0.  Where logits are +infinity they
- * share the weight.  Temperatures below 2^-100 count as that.
+ * share the weight.  Temperatures above 0 count as at least 2^-99 and at most 2^99.
  *
- * Weights are good to about 2^-40 and summed as pairs of floats: the answers are
- * those of 64-bit arithmetic except where u, or top_p, lies within about 2^-40 of a
- * border.  Equal calls give equal bits.  FA_ERR_UNSUPPORTED where V passes what eight
- * SMs hold: about 400000 fp32 logits, 800000 of 16 bits.
+ * Weights are good to about 2^-31 (their sums to 2^-36) and summed as pairs of floats:
+ * the answers are those of 64-bit arithmetic except where u, or top_p, lies within about
+ * 2^-32 of a border.  Equal calls give equal bits.  FA_ERR_UNSUPPORTED where V passes what eight
+ * SMs hold: about 368000 fp32 logits, 737000 of 16 bits.
  */
 int fa_sample(const void* logits, const float* uniforms, const float* temperature,
               const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
