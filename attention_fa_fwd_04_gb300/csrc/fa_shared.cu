@@ -58,12 +58,16 @@ constexpr int KEPT = THREADS;  // owners whose keys a CTA keeps in shared memory
 // that two row tiles meet (1.45 us), or one row tile in turns; and places without a tile
 // after each piece, for what a stretch costs beside its tiles.  A 32-key tile of a few
 // rows is one place of the other list.
-constexpr int COST_TWO = 3, COST_ONE = 3, SLACK = 4, SLACK_FEW = 2;
+constexpr int COST = 3, SLACK = 4, SLACK_FEW = 2;
 constexpr int FEW = 16;       // rows that a warp streams keys for
 constexpr int FEW_WARPS = 6;  // such warps of a CTA
 constexpr int FEW_KEYS = 32;  // keys of their tiles
-// What a place of either list costs, for the sharing out of the CTAs.
-constexpr int SHARE_MANY = 4, SHARE_FEW = 1, SHARE_FEW2 = 3;  // (up to 8 rows, up to 16)
+// What a place costs in time, for the sharing out of the CTAs: 8 in the list of tiles, and
+// in the streamed one 2 up to 8 rows, up to 16 rows 5 (D = 128) or 3 (D = 64).  Measured: 64
+// chats of 8 rows 75, 59, 66 us at 1, 2, 3; 32 sequences of 16 rows (D = 128) 194, 163, 145
+// at 3, 4, 5; 48 of 16 rows and 2000 keys (D = 64) 37, 41, 43 at 3, 4, 5.
+constexpr int SHARE_MANY = 8;
+constexpr int share_few(int rows, int D) { return rows <= 8 ? 2 : (D == 128 ? 5 : 3); }
 constexpr int RING = 4;        // stretches told ahead
 constexpr long long L2_KEEPS = 48 << 20;  // bytes of a unit's K/V, over all kv heads
 
@@ -145,6 +149,7 @@ struct SharedParams {
   float* part_o[2];
   float* part_ml[2];
   int half[2];  // rows of a warpgroup in a slot
+  int share_few;  // what a place of the streamed list costs, to SHARE_MANY
   int few;      // sequences are streamed by warps; their partials: [id][SqG][D], [id][SqG][2]
   SharedOwner* owner;  // [groups + B]
   SharedList* list;
@@ -154,29 +159,9 @@ struct SharedParams {
   float c;  // scale * log2(e)
 };
 
-// The kernel's roles run different code side by side, and what does not fit the
-// instruction caches is fetched again and again (with everything inlined, 228 KB, a
-// stretch of one tile took 5 us): what is long and not in a loop over tiles is called.
-
 // a / b in 32 bits where both fit.
-__device__ __forceinline__ long long long_quotient(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : long_quotient(a, b);
-}
-
-// A pipeline wait of the warps beside the softmax's: the first probe here, the rest called.
-// (The softmax warps' registers leave no room for calls.)
-template <bool POLL>
-__device__ __forceinline__ bool long_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       unsigned site) {
-  return mbar_wait<POLL>(bar, parity, abort_flag, &g_shared_err, site);
-}
-template <bool POLL>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                         unsigned site) {
-  const uint32_t a = smem_u32(bar);
-  if (POLL ? mbar_test_wait(a, parity) : mbar_try_wait(a, parity)) return true;
-  return long_wait<POLL>(bar, parity, abort_flag, site);
+  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // A unit's tiles.
@@ -193,7 +178,7 @@ __device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int r
   s.t0 = lo / keys;
   s.T = hi > lo ? (int)(((uint32_t)hi + keys - 1) / keys) - s.t0 : 0;
   s.n_rt = (rows + 2 * sh::BM - 1) / (2 * sh::BM);
-  s.cost = few ? 1 : (rows > sh::BM ? sh::COST_TWO : sh::COST_ONE);
+  s.cost = few ? 1 : sh::COST;
   s.S = 1;
   s.len = s.T;
   if (s.n_rt > 1 && (long long)s.T * p.Hkv > p.keep_tiles && s.T > W) {
@@ -363,18 +348,17 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   block_sums(tiles[0], tiles[1], pl->sums, &all_tiles[0], &all_tiles[1]);
   const int n = p.ctas;
   // CTAs of the first kind, for lists of a and z places.
-  const int share_few = p.SqG <= 8 ? sh::SHARE_FEW : sh::SHARE_FEW2;
   auto share = [&](long long a, long long z) {
     if (a == 0) return 0;
     if (z == 0) return n;
-    const long long x = quotient(a * n * sh::SHARE_MANY + z * share_few / 2,
-                                 a * sh::SHARE_MANY + z * share_few);
+    const long long x = quotient(a * n * sh::SHARE_MANY + z * p.share_few / 2,
+                                 a * sh::SHARE_MANY + z * p.share_few);
     return max(1, min(n - 1, (int)x));
   };
-  const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1])) * sh::COST_TWO;
+  const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1])) * sh::COST;
   const long long width = quotient(all_tiles[0] + per - 1, per);
   const int W = width < 1 ? 1 : (width > INT32_MAX ? INT32_MAX : (int)width);
-  const int slack[2] = {all_tiles[0] > (long long)n * sh::COST_TWO ? sh::SLACK : 0,
+  const int slack[2] = {all_tiles[0] > (long long)n * sh::COST ? sh::SLACK : 0,
                         all_tiles[1] > (long long)n * sh::FEW_WARPS ? sh::SLACK_FEW : 0};
   auto places_at = [&](int o, const Keys& k) {
     return p.Hkv * places_per_head(shape_of(p, few(o), k.rows, k.lo, k.hi, W), slack[few(o)]);
@@ -382,7 +366,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   // Sums of places and pieces (groups' in the upper half) up to each owner; with an owner
   // per thread they are those of the list, else they are made again chunk by chunk.
   const bool one = owners <= sh::THREADS;
-  long long total[2], my_places = 0, my_pieces = 0, sum_places, sum_pieces, all_pieces = 0;
+  long long total[2], my_places = 0, my_pieces = 0, sum_places, sum_pieces;
   if (one) {
     if (t < owners) {
       my_places = places_at(t, mine);
@@ -391,6 +375,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
     sum_places = my_places;
     sum_pieces = my_pieces;
     if (t == 0) pl->total[0] = 0;
+    long long all_pieces;
     block_sums(sum_places, sum_pieces, pl->sums, &total[1], &all_pieces);
     if (t == p.groups - 1) pl->total[0] = sum_places;
     __syncthreads();
@@ -407,15 +392,11 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
     }
     block_sums(a, z, pl->sums, &total[0], &total[1]);
   }
-  // CTAs of either kind by what their lists cost; where the first has about as many pieces
-  // as CTAs, one each: then the pairs of a strip meet the same keys at the same time.
-  // Ranges in use are each as long as a tile at least, so that every one of them between
-  // the first and the last of a piece holds a tile of it.
-  int many = share(total[0], total[1]);
-  const long long pieces = (all_pieces >> 32) + (p.few ? 0 : all_pieces & 0xffffffffll);
-  if (pieces <= (total[1] > 0 ? n - 1 : n) && 8 * (pieces > many ? pieces - many : many - pieces) <= many)
-    many = (int)pieces;
-  const long long most = quotient(total[0], sh::COST_TWO);
+  // CTAs of either kind by what their lists cost.  Ranges in use are each as long as a tile
+  // at least, so that every one of them between the first and the last of a piece holds a
+  // tile of it.
+  const int many = share(total[0], total[1]);
+  const long long most = quotient(total[0], sh::COST);
   const int used[2] = {most < 1 ? 1 : (int)min(most, (long long)max(many, 1)),
                        (int)max(1ll, min(total[1], (long long)(n - many) * sh::FEW_WARPS))};
   const int kind = (int)blockIdx.x >= many;
@@ -948,13 +929,9 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   // The k-th stretch of this CTA; false at the end, and where a wait gave up (*ok).
   uint32_t seg = 0;
   sh::Seg sg;
-  auto next_seg = [&](bool* ok, auto softmax) {
+  auto next_seg = [&](bool* ok) {
     const int slot = seg % sh::RING;
-    const uint32_t par = (seg / sh::RING) & 1;
-    if constexpr (softmax.value)
-      *ok = mbar_wait<false>(&told[slot], par, abort_flag, &g_shared_err, 13);
-    else
-      *ok = wait_for<true>(&told[slot], par, abort_flag, 13);
+    *ok = mbar_wait<false>(&told[slot], (seg / sh::RING) & 1, abort_flag, &g_shared_err, 13);
     if (!*ok) return false;
     sg = *reinterpret_cast<const sh::Seg*>(s_ring + slot * 64);
     if (warp != W_MMA) __syncwarp();  // (there one lane alone listens)
@@ -973,7 +950,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
       uint32_t tc = 0;  // tiles so far: K at ring position 2 tc, V at 2 tc + 1
       bool ok = true;
-      while (ok && next_seg(&ok, std::false_type{})) {
+      while (ok && next_seg(&ok)) {
         const int32_t* table = p.page_table + (size_t)sg.tab * p.max_pages;
         const int end = sg.hi;
         const uint64_t pol = sg.twice ? again : once;
@@ -1000,7 +977,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
           if (lane == 0) *issued = cnt + 1;
         };
         auto slot_free = [&](uint32_t cnt) {
-          return wait_for<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag, 1);
+          return mbar_wait<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag, &g_shared_err, 1);
         };
         // Pages are looked up two tiles ahead.
         int pos = 0, pos_n = 0, pos_nn = 0;
@@ -1048,18 +1025,18 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         uint32_t tc = 0, cw[2] = {0, 0};
         bool ok = true;
         auto landed = [&](uint32_t cnt, unsigned site) {
-          ok = wait_for<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, site);
+          ok = mbar_wait<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, &g_shared_err, site);
           tc_fence_after();
           return ok;
         };
         auto p_ready = [&](int i, uint32_t n) {
-          ok = wait_for<false>(&p_full[i], n & 1, abort_flag, 6 + i);
+          ok = mbar_wait<false>(&p_full[i], n & 1, abort_flag, &g_shared_err, 6 + i);
           tc_fence_after();
           return ok;
         };
-        while (ok && next_seg(&ok, std::false_type{})) {
+        while (ok && next_seg(&ok)) {
           const int n = sg.n;
-          if (!(ok = wait_for<false>(q_full, (seg - 1) & 1, abort_flag, 2))) break;
+          if (!(ok = mbar_wait<false>(q_full, (seg - 1) & 1, abort_flag, &g_shared_err, 2))) break;
           tc_fence_after();
           if (!landed(2 * tc, 3)) break;
           if (sg.rows > sh::BM) {  // two row tiles on every key tile
@@ -1133,7 +1110,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         const int slot = k % sh::RING;
         sh::Seg g;
         if (!walk_next(p, plan, w, plan->range, &g)) g.kind = -1;
-        if (!wait_for<true>(&heard[slot], ((k / sh::RING) & 1) ^ 1, abort_flag, 14))
+        if (!mbar_wait<true>(&heard[slot], ((k / sh::RING) & 1) ^ 1, abort_flag, &g_shared_err, 14))
           break;
         *reinterpret_cast<sh::Seg*>(s_ring + slot * 64) = g;
         mbar_arrive(&told[slot]);
@@ -1178,7 +1155,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);
     };
-    bool have = next_seg(&ok, std::true_type{});
+    bool have = next_seg(&ok);
     if (have) load_q();
     while (have) {
       const int rows = sg.rows, n = sg.n, r0 = sg.r0;
@@ -1226,7 +1203,7 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       auto move_on = [&] {
         tc += n;
         have = false;
-        if (ok) have = next_seg(&ok, std::true_type{});
+        if (ok) have = next_seg(&ok);
         // (seg counts the next stretch by now.)
         if (have) ok = mbar_wait<false>(q_free, seg & 1, abort_flag, &g_shared_err, 11);
         if (!ok) return false;
@@ -1239,52 +1216,50 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         tc_fence_after();
         return true;
       };
-      {
-        int lim = end;  // this row sees the keys [lo, lim)
-        if (kind == 1) {
-          int s = 0;
-          if (row_ok) shared_qrow(p, 0, 0, r0 + rr, &s);
-          lim = least + s;
-        }
-        float m_used = NEG_INF, l = 0.f;
-        for (int j = dual ? 0 : i; j < n; j += dual ? 1 : 2) {
-          if (!tile_ready(j)) break;
-          if (warp_ok) {
-            auto mask = [&](uint32_t (&sr)[4][32]) {
-              const Mask128 fine = sound_keys(bad, p.box);
-              hide_keys(sr,
-                        Mask128{fine.lo & low_bits(lim - kv0) & ~low_bits(lo - kv0),
-                                fine.hi & low_bits(lim - kv0 - 64) & ~low_bits(lo - kv0 - 64)},
-                        hide);
-            };
-            // (S of this tile was issued after P V of this warpgroup's last: both are done.)
-            auto settled = [] { return true; };
-            softmax_tile<D, T>(tS, tO, c, j < (dual ? 1 : 2), masked, mask, settled, &m_used, &l);
-          }
-          tc_fence_before();
-          mbar_arrive(&p_full[i]);
-        }
-        if (!move_on()) break;
-        if (!active) {
-          if (row_ok) *pml = make_float2(NEG_INF, 0.f);
-          continue;
-        }
+      int lim = end;  // this row sees the keys [lo, lim)
+      if (kind == 1) {
+        int s = 0;
+        if (row_ok) shared_qrow(p, 0, 0, r0 + rr, &s);
+        lim = least + s;
+      }
+      float m_used = NEG_INF, l = 0.f;
+      for (int j = dual ? 0 : i; j < n; j += dual ? 1 : 2) {
+        if (!tile_ready(j)) break;
         if (warp_ok) {
-          if (row_ok) *pml = make_float2(m_used, l);
+          auto mask = [&](uint32_t (&sr)[4][32]) {
+            const Mask128 fine = sound_keys(bad, p.box);
+            hide_keys(sr,
+                      Mask128{fine.lo & low_bits(lim - kv0) & ~low_bits(lo - kv0),
+                              fine.hi & low_bits(lim - kv0 - 64) & ~low_bits(lo - kv0 - 64)},
+                      hide);
+          };
+          // (S of this tile was issued after P V of this warpgroup's last: both are done.)
+          auto settled = [] { return true; };
+          softmax_tile<D, T>(tS, tO, c, j < (dual ? 1 : 2), masked, mask, settled, &m_used, &l);
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
+      }
+      if (!move_on()) break;
+      if (!active) {
+        if (row_ok) *pml = make_float2(NEG_INF, 0.f);
+        continue;
+      }
+      if (warp_ok) {
+        if (row_ok) *pml = make_float2(m_used, l);
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tO + q * 32, o);
-            tmem_wait_ld();
-            reg_fence32(o);
-            if (!row_ok) continue;
-            // [column / 4][row] of 16 bytes: the lanes' rows side by side.
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tO + q * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+          if (!row_ok) continue;
+          // [column / 4][row] of 16 bytes: the lanes' rows side by side.
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4*>(po + ((q * 8 + x) * col + tid) * 4) =
-                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-          }
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<float4*>(po + ((q * 8 + x) * col + tid) * 4) =
+                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                            __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
         }
       }
       tc_fence_before();
@@ -1498,9 +1473,10 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, shared_split_kernel<D, T>, tm[0], tm[1], tm[2], tm[3], p);
   if (e != cudaSuccess) return e;
-  // Blocks of 32 rows' threads while they leave SMs free: a row then has more of them.
+  // Blocks of 32 rows' threads while all of them are resident at once: a row then has more
+  // of them (48 sequences of 16 rows, D = 64: 31.8 us, 35.4 with small blocks).
   const long long units = (long long)p.B * p.Hkv, wide = units * ((p.SqG + 31) / 32);
-  if (wide <= p.ctas)
+  if (wide <= p.ctas * (1024 / (8 * D)))
     return launch_dependent(shared_merge_kernel<D, T, 8 * D>, dim3((unsigned)wide), 8 * D, stream, p);
   constexpr int RC = 256 * 4 / D;
   return launch_dependent(shared_merge_kernel<D, T, 256>,
@@ -1577,6 +1553,7 @@ extern "C" int fa_decode_shared_fwd(const void* q, const void* kpages, const voi
   p.G = Hq / Hkv;
   p.SqG = Sq * p.G;
   p.few = p.SqG <= fa::sh::FEW;
+  p.share_few = fa::sh::share_few(p.SqG, D);
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
