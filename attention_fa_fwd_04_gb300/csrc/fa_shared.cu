@@ -62,12 +62,13 @@ constexpr int COST = 3, SLACK = 4, SLACK_FEW = 2;
 constexpr int FEW = 16;       // rows that a warp streams keys for
 constexpr int FEW_WARPS = 6;  // such warps of a CTA
 constexpr int FEW_KEYS = 32;  // keys of their tiles
-// What a place costs in time, for the sharing out of the CTAs: 8 in the list of tiles, and
-// in the streamed one 2 up to 8 rows, up to 16 rows 5 (D = 128) or 3 (D = 64).  Measured: 64
-// chats of 8 rows 75, 59, 66 us at 1, 2, 3; 32 sequences of 16 rows (D = 128) 194, 163, 145
-// at 3, 4, 5; 48 of 16 rows and 2000 keys (D = 64) 37, 41, 43 at 3, 4, 5.
-constexpr int SHARE_MANY = 8;
-constexpr int share_few(int rows, int D) { return rows <= 8 ? 2 : (D == 128 ? 5 : 3); }
+// What a place costs in time, for the sharing out of the CTAs: 16 in the list of tiles, and
+// in the streamed one 5 up to 8 rows, up to 16 rows 10 (D = 128) or 6 (D = 64).  Measured: 64
+// sequences of 8 rows behind 8192 keys 75, 58.5, 60, 66 us at 2, 4, 5, 6, behind 32768 114 and
+// 99 at 4 and 5; 32 of 16 rows (D = 128) 194, 163, 146 at 6, 8, 10; 48 of 16 rows and 2000 keys
+// (D = 64) 37, 41, 43 at 6, 8, 10.
+constexpr int SHARE_MANY = 16;
+constexpr int share_few(int rows, int D) { return rows <= 8 ? 5 : (D == 128 ? 10 : 6); }
 constexpr int RING = 4;        // stretches told ahead
 constexpr long long L2_KEEPS = 48 << 20;  // bytes of a unit's K/V, over all kv heads
 
@@ -351,8 +352,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   auto share = [&](long long a, long long z) {
     if (a == 0) return 0;
     if (z == 0) return n;
-    const long long x = quotient(a * n * sh::SHARE_MANY + z * p.share_few / 2,
-                                 a * sh::SHARE_MANY + z * p.share_few);
+    const long long x = quotient(a * n * sh::SHARE_MANY, a * sh::SHARE_MANY + z * p.share_few);
     return max(1, min(n - 1, (int)x));
   };
   const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1])) * sh::COST;
@@ -396,7 +396,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   // at least, so that every one of them between the first and the last of a piece holds a
   // tile of it.
   const int many = share(total[0], total[1]);
-  const long long most = quotient(total[0], sh::COST);
+  const long long most = quotient(total[0], 2 * sh::COST);
   const int used[2] = {most < 1 ? 1 : (int)min(most, (long long)max(many, 1)),
                        (int)max(1ll, min(total[1], (long long)(n - many) * sh::FEW_WARPS))};
   const int kind = (int)blockIdx.x >= many;
@@ -1282,17 +1282,19 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   }
 }
 
-// Merge: a block takes up to THREADS * 4 / D rows of one (sequence, kv head).  Its first warp
-// lists where their partials are, of the group's unit and of their own (the lanes take
-// strips); then a thread takes four columns of a row and walks the list, six partials'
-// loads at a time.  With fewer rows, the threads of a row's columns share the list.
+// Merge: a block takes up to RC rows of one (sequence, kv head) and 256 / RC groups of four
+// columns.  A warp for each list finds out where their partials are, of the group's unit and
+// of their own (the lanes take strips); then a thread takes four columns of a row and
+// walks the lists, 6 or 12 partials' loads at a time.  With fewer rows than RC, the threads of a
+// row's columns share the lists.
 namespace join {
+constexpr int THREADS = 256;
+constexpr int resident(int ahead) { return ahead > 6 ? 2 : 4; }  // blocks of an SM
 constexpr int LIST = 2048;  // partials of a row from one unit: two per CTA and strip, one per warp
 }  // namespace join
-template <int D, typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) shared_merge_kernel(
+template <int D, typename T, int RC, int AHEAD>
+__global__ void __launch_bounds__(join::THREADS, join::resident(AHEAD)) shared_merge_kernel(
     const __grid_constant__ SharedParams p) {
-  constexpr int RC = THREADS * 4 / D;  // rows of a block
   static_assert(RC <= 32, "a row's threads in one warp");
   // Lists: of the group's unit for the rows' first and last pair of row tiles; their own.
   __shared__ int s_list[3][join::LIST];
@@ -1363,7 +1365,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) shared_merge_kernel(
   __syncthreads();
   int width = 1;  // rows, as a power of two; RC / width threads share a row's list
   while (width < rows) width *= 2;
-  const int r = t % width, turn = t / width % (RC / width), col = t / RC;
+  const int r = t % width, turn = t / width % (RC / width);
+  const int col = blockIdx.y * (join::THREADS / RC) + t / RC;
   const bool real = r < rows;
   const int g_row = s_group[0] < 0 ? 0 : (b - s_group[0]) * p.SqG + first + (real ? r : 0);
   const int l = g_row / (2 * sh::BM) == s_group[1] ? 0 : 1;
@@ -1391,7 +1394,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) shared_merge_kernel(
     acc.z += wt * v.z;
     acc.w += wt * v.w;
   };
-  constexpr int AHEAD = 6;
   for (int k = turn; k < n; k += AHEAD * (RC / width)) {
     float2 ml[AHEAD];
     float4 ov[AHEAD];
@@ -1445,6 +1447,7 @@ template <int D, typename T>
 static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[4],
                                  cudaStream_t stream) {
   using C = sh::Cfg<D>;
+  constexpr int ALL = join::THREADS * 4 / D;  // rows of a merge block that takes all columns
   static int attr_set[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1454,7 +1457,8 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     // As in the tree decode: the merge keeps the split kernel's division of the SM.
-    for (auto k : {shared_merge_kernel<D, T, 256>, shared_merge_kernel<D, T, 8 * D>}) {
+    for (auto k : {shared_merge_kernel<D, T, ALL, 6>, shared_merge_kernel<D, T, 32, 6>,
+                   shared_merge_kernel<D, T, 32, 12>}) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
                                (int)cudaSharedmemCarveoutMaxShared);
       if (e != cudaSuccess) return e;
@@ -1474,13 +1478,18 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[
   e = cudaLaunchKernelEx(&cfg, shared_split_kernel<D, T>, tm[0], tm[1], tm[2], tm[3], p);
   if (e != cudaSuccess) return e;
   // Blocks of 32 rows' threads while all of them are resident at once: a row then has more
-  // of them (48 sequences of 16 rows, D = 64: 31.8 us, 35.4 with small blocks).
+  // of them (48 sequences of 16 rows, D = 64: 30.6 us, 34.9 with blocks of all columns; 8 of
+  // 4 rows and 8200 keys 24.0, 26.0 with 6 loads at a time, 28.5 in both ways).
   const long long units = (long long)p.B * p.Hkv, wide = units * ((p.SqG + 31) / 32);
-  if (wide <= p.ctas * (1024 / (8 * D)))
-    return launch_dependent(shared_merge_kernel<D, T, 8 * D>, dim3((unsigned)wide), 8 * D, stream, p);
-  constexpr int RC = 256 * 4 / D;
-  return launch_dependent(shared_merge_kernel<D, T, 256>,
-                          dim3((unsigned)(units * ((p.SqG + RC - 1) / RC))), 256, stream, p);
+  auto fits = [&](int ahead) { return wide * (D / 32) <= (long long)join::resident(ahead) * p.ctas; };
+  const dim3 by_columns((unsigned)(fits(6) ? wide : 1), D / 32);
+  if (fits(12))
+    return launch_dependent(shared_merge_kernel<D, T, 32, 12>, by_columns, join::THREADS, stream, p);
+  if (fits(6))
+    return launch_dependent(shared_merge_kernel<D, T, 32, 6>, by_columns, join::THREADS, stream, p);
+  return launch_dependent(shared_merge_kernel<D, T, ALL, 6>,
+                          dim3((unsigned)(units * ((p.SqG + ALL - 1) / ALL))), join::THREADS,
+                          stream, p);
 }
 
 int set_shared_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
