@@ -58,7 +58,7 @@ constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int SEGS = CLUSTER * WARPS;  // index-ordered segments of a row, one per warp
 constexpr int LIST = 512;              // tokens that a CTA ranks
-constexpr int SMEM_MAX = 180 * 1024;   // bytes of a CTA's part of a row
+constexpr int SMEM_MAX = 176 * 1024;   // bytes of a CTA's part of a row
 }  // namespace sa
 
 struct SampleParams {
@@ -713,7 +713,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         if (t == 0) s_key[0] = from;
         __syncthreads();
         from = s_key[0];
-        const float vfrom = value_of(from), per = __fdividef((float)(sa::BINS - 1), top - vfrom);
+        // (A range that is too small, or too large, to divide by counts as one bin.)
+        const float vfrom = value_of(from), range = top - vfrom;
+        const float per = range > 0x1p-100f ? __fdividef((float)(sa::BINS - 1), range) : 0.f;
         if (mx >= vfrom) atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::BINS - 1)], 1u);
         sync();
         uint32_t h[4];
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           before += h[e];
         }
         __syncthreads();
-        lo = max(lo, Lg::key(Lg::from(top - __fdividef((float)s_i[0] + 1.01f, per))));
+        lo = range == 0.f ? kmax : max(lo, Lg::key(Lg::from(top - __fdividef((float)s_i[0] + 1.01f, per))));
         const float least_listed = value_of(lo);
         each([&](int i, uint4 g) {
           each_of(within(g, least_listed, INFINITY), i, enlist);

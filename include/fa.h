@@ -601,7 +601,7 @@ int fa_decode_shared_fwd(const void* q, const void* kpages, const void* vpages,
  * Weights are good to about 2^-31 (their sums to 2^-36) and summed as pairs of floats:
  * the answers are those of 64-bit arithmetic except where u, or top_p, lies within about
  * 2^-32 of a border.  Equal calls give equal bits.  FA_ERR_UNSUPPORTED where V passes what eight
- * SMs hold: about 368000 fp32 logits, 737000 of 16 bits.
+ * SMs hold: about 360000 fp32 logits, 720000 of 16 bits.
  */
 int fa_sample(const void* logits, const float* uniforms, const float* temperature,
               const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

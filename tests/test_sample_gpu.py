@@ -32,8 +32,9 @@ def check(fa, logits, u, T=None, k=None, p=None, m=None, probs=True, status=None
         assert margin > 1e-9, (r, margin)
         assert int(tokens[r]) == tok, r
         if pr is not None:
-            # Weights to 2^-40, their sum and quotient in pairs, one rounding to fp32;
-            # what is below fp32's normal range by its half step.
+            # Weights to 2^-31 (a hundredth of a rounding to fp32 is 2^-30.6), their sum and
+            # quotient in pairs, one rounding to fp32; what is below fp32's normal range by
+            # its half step.
             got = pr[r].double().cpu().numpy()
             err = np.abs(got - dist)
             assert np.all(err <= 2.0 ** -24 * dist * 1.01 + 2.0 ** -120), (r, err.max())
