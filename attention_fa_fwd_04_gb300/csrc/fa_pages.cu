@@ -14,9 +14,14 @@
 // the chain: lengths, sums, a page id, a store.  One cluster of up to 8 CTAs does
 // everything in one launch: every CTA makes the sums of all sequences for itself
 // (in shared memory), a cluster barrier separates the reading of lengths and count
-// from their writing in place, and the CTAs share the entries and tokens.
+// from their writing in place, another the writing of the table from the tokens' reading of
+// it, and the CTAs share the entries and tokens.  What is done in a row is done at once:
+// with one token after another, each with its own way to its page, a step of 64 sequences
+// took 6.2 us instead of 3.6, 256 sequences with 40000 new tokens 14.7 instead of 10.6.
 //
 // Write.  A copy: every row is read and written once.
+#include <type_traits>
+
 #include "fa.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -58,33 +63,30 @@ __device__ __forceinline__ long long warp_scan(long long v) {
   return v;
 }
 
-// Inclusive sums of a and b over the block, and the block's totals.  Every thread
-// must call it; sums: 2 * WARPS entries, free again after the next barrier.
-__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* sums,
-                                            long long* total_a, long long* total_b) {
+// Inclusive sums of N quantities over the block, and the block's totals.  Every thread
+// must call it; sums: N * WARPS entries, free again after the next barrier.
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long* sums, long long (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  a = warp_scan(a);
-  b = warp_scan(b);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_scan(v[i]);
   __syncthreads();
   if (lane == 31) {
-    sums[2 * warp] = a;
-    sums[2 * warp + 1] = b;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[N * warp + i] = v[i];
   }
   __syncthreads();
-  long long ta = 0, tb = 0, ba = 0, bb = 0;
 #pragma unroll
-  for (int w = 0; w < pg::WARPS; ++w) {
-    if (w == warp) {
-      ba = ta;
-      bb = tb;
+  for (int i = 0; i < N; ++i) {
+    long long all = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < pg::WARPS; ++w) {
+      if (w == warp) before = all;
+      all += sums[N * w + i];
     }
-    ta += sums[2 * w];
-    tb += sums[2 * w + 1];
+    v[i] += before;
+    total[i] = all;
   }
-  a += ba;
-  b += bb;
-  *total_a = ta;
-  *total_b = tb;
 }
 
 // The last of v[0 .. n) (rising) that is at most x; v[0] is.
@@ -103,7 +105,7 @@ __device__ __forceinline__ int last_at_most(const int* v, int n, int x) {
 __global__ void __launch_bounds__(pg::THREADS, 1)
     update_pages_kernel(const __grid_constant__ UpdateParams p) {
   extern __shared__ int s_words[];
-  __shared__ long long s_sums[2 * pg::WARPS];
+  __shared__ long long s_sums[3 * pg::WARPS];
   __shared__ int s_taken;
   const int n1 = p.B + 1;
   int* const s_old = s_words;           // old length
@@ -121,10 +123,11 @@ __global__ void __launch_bounds__(pg::THREADS, 1)
   const long long cap = (long long)p.max_pages * p.page_size;
   const int F = *p.free_count;
   bool odd = false;
-  long long R = 0;  // pages given back
+  // Pages given back, pages and tokens taken by all sequences before.
+  long long all[3] = {0, 0, 0};
   for (int b0 = 0; b0 < p.B; b0 += pg::THREADS) {
     const int b = b0 + t;
-    long long rel = 0, none = 0, total, unused;
+    long long v[3] = {0, 0, 0}, total[3];
     if (b < p.B) {
       const int o = p.old_lens[b];
       int n = p.new_lens[b];
@@ -142,53 +145,65 @@ __global__ void __launch_bounds__(pg::THREADS, 1)
       s_new[b] = n;
       s_po[b] = po;
       s_pn[b] = pn;
-      rel = po > pn ? po - pn : 0;
+      v[0] = max(po - pn, 0);
+      v[1] = max(pn - po, 0);
+      v[2] = max(n - o, 0);
     }
-    const long long mine = rel;
-    block_scan2(rel, none, s_sums, &total, &unused);
-    const long long before = R + rel - mine;
-    if (b < p.B) s_rel[b] = before > INT32_MAX ? INT32_MAX : (int)before;
-    R += total;
+    const long long mine[3] = {v[0], v[1], v[2]};
+    block_scan(v, s_sums, total);
+    if (b < p.B) {
+      int* const dst[3] = {s_rel, s_need, s_cu};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) dst[i][b] = (int)min(all[i] + v[i] - mine[i], (long long)INT32_MAX);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) all[i] += total[i];
   }
   // A stack that is no stack, or that what comes back does not fit: nothing changes.
-  const bool refuse = F < 0 || F > p.max_free || F + R > p.max_free;
+  const bool refuse = F < 0 || F > p.max_free || F + all[0] > p.max_free;
   odd |= refuse;
   if (odd && rank == 0) atomicOr(&g_pages_err, kErrBounds);
-  const long long have = refuse ? 0 : F + R;
-  long long need0 = 0, tok0 = 0, cu0 = 0;
-  for (int b0 = 0; b0 < p.B; b0 += pg::THREADS) {
-    const int b = b0 + t;
-    long long need = 0, tok = 0, need_all, tok_all, unused, cu_all;
-    if (b < p.B) {
-      if (refuse) {
-        s_new[b] = s_old[b];
-        s_pn[b] = s_po[b];
+  const long long have = refuse ? 0 : F + all[0];
+  long long cu0 = all[2];
+  if (refuse || all[1] > have || all[2] > p.max_new) {
+    // Not everything fits: which sequences do.
+    long long need0 = 0, tok0 = 0;
+    cu0 = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < p.B; b0 += pg::THREADS) {
+      const int b = b0 + t;
+      long long v[2] = {0, 0}, cu[1], v_all[2], cu_all[1];
+      if (b < p.B) {
+        if (refuse) {
+          s_new[b] = s_old[b];
+          s_pn[b] = s_po[b];
+        }
+        v[0] = max(s_pn[b] - s_po[b], 0);
+        v[1] = max(s_new[b] - s_old[b], 0);
       }
-      need = s_pn[b] > s_po[b] ? s_pn[b] - s_po[b] : 0;
-      tok = s_new[b] > s_old[b] ? s_new[b] - s_old[b] : 0;
-    }
-    const long long my_need = need, my_tok = tok;
-    block_scan2(need, tok, s_sums, &need_all, &tok_all);
-    need += need0;
-    tok += tok0;
-    const bool fits = (need <= have || my_need == 0) && tok <= p.max_new;
-    long long cu = fits ? my_tok : 0, none = 0;
-    const long long my_cu = cu;
-    block_scan2(cu, none, s_sums, &cu_all, &unused);
-    if (b < p.B) {
-      const long long before = need - my_need;
-      s_need[b] = before > INT32_MAX ? INT32_MAX : (int)before;
-      s_cu[b] = (int)(cu0 + cu - my_cu);
-      if (!fits && my_tok > 0) {
-        s_new[b] = s_old[b];
-        s_pn[b] = s_po[b];
-      } else if (my_need > 0) {
-        atomicMax(&s_taken, (int)need);
+      const long long my_need = v[0], my_tok = v[1];
+      block_scan(v, s_sums, v_all);
+      const long long need = need0 + v[0], tok = tok0 + v[1];
+      const bool fits = (need <= have || my_need == 0) && tok <= p.max_new;
+      cu[0] = fits ? my_tok : 0;
+      const long long my_cu = cu[0];
+      block_scan(cu, s_sums, cu_all);
+      if (b < p.B) {
+        s_need[b] = (int)min(need - my_need, (long long)INT32_MAX);
+        s_cu[b] = (int)(cu0 + cu[0] - my_cu);
+        if (!fits && my_tok > 0) {
+          s_new[b] = s_old[b];
+          s_pn[b] = s_po[b];
+        } else if (my_need > 0) {
+          atomicMax(&s_taken, (int)need);
+        }
       }
+      need0 += v_all[0];
+      tok0 += v_all[1];
+      cu0 += cu_all[0];
     }
-    need0 += need_all;
-    tok0 += tok_all;
-    cu0 += cu_all;
+  } else if (t == 0) {
+    s_taken = (int)all[1];
   }
   const int tokens = (int)cu0;
   // Every CTA has read the lengths and the count, which may be written in place.
@@ -222,52 +237,74 @@ __global__ void __launch_bounds__(pg::THREADS, 1)
     const int b = last_at_most(s_need, p.B, k);
     p.table[(size_t)b * p.max_pages + s_po[b] + (k - s_need[b])] = taken_page(k);
   }
-  if (!refuse)
-    for (int i = F + at; i < left; i += step) p.free_pages[i] = given(i - F);
-  const int most = INT32_MAX / p.page_size;  // ids below it have 31-bit slots
-  // Four tokens in a row per thread, mostly of one sequence and page.
-  for (long long t0 = 4ll * at; t0 < p.max_new; t0 += 4ll * step) {
-    int slot[4], pos[4];
-    int b = 0, page = -1, id = 0;
-    if (t0 < tokens) b = last_at_most(s_cu, p.B, (int)t0);
+  // The tokens' pages are in the table, then: no searches among what was given back.
+  auto arrive = [&] { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); };
+  if (n_ctas > 1) arrive();
+  // Four in a row, mostly of one sequence.
+  for (long long i0 = F + 4ll * at; !refuse && i0 < left; i0 += 4ll * step) {
+    int b = last_at_most(s_rel, p.B, (int)(i0 - F)), id[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int x = (int)t0 + e;
-      slot[e] = -1;
-      pos[e] = 0;
-      if (t0 + e < tokens) {
-        while (x - s_cu[b] >= s_new[b] - s_old[b]) {  // the next sequence with new tokens
-          ++b;
-          page = -1;
-        }
-        pos[e] = s_old[b] + (x - s_cu[b]);
-        const int pgi = (int)((uint32_t)pos[e] / (uint32_t)p.page_size);
-        if (pgi != page) {
-          page = pgi;
-          id = pgi >= s_po[b]
-                   ? taken_page(s_need[b] + (pgi - s_po[b]))
-                   : (p.shared && pgi < p.shared[b] ? -1
-                                                    : p.table[(size_t)b * p.max_pages + pgi]);
-        }
-        // (A shared page is not written: its tokens have no slot.)
-        if (id >= 0 && id < most)
-          slot[e] = id * p.page_size + (pos[e] - page * p.page_size);
-        else if (!p.shared || pgi >= p.shared[b])
-          atomicOr(&g_pages_err, kErrBounds);
-      }
+      const int i = (int)(i0 - F) + e;
+      if (i0 + e >= left) continue;
+      while (i - s_rel[b] >= s_po[b] - s_pn[b]) ++b;
+      id[e] = p.table[(size_t)b * p.max_pages + s_pn[b] + (i - s_rel[b])];
     }
-    if (p.vec && t0 + 4 <= p.max_new) {
-      *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 4; ++e)
+      if (i0 + e < left) p.free_pages[i0 + e] = id[e];
+  }
+  if (n_ctas > 1)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+  const int most = INT32_MAX / p.page_size;  // ids below it have 31-bit slots
+  // A token per thread, or four in a row: one search, then all their table entries at once.
+  auto tokens_of = [&](auto count) {
+    constexpr int N = decltype(count)::value;
+    for (long long t0 = (long long)N * at; t0 < p.max_new; t0 += (long long)N * step) {
+      int slot[N], pos[N], id[N], first[N], b = 0;
+      bool wants[N];  // (a token in a page that is not shared: those are not written)
+      if (t0 < tokens) b = last_at_most(s_cu, p.B, (int)t0);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        pos[e] = first[e] = id[e] = 0;
+        wants[e] = false;
+        if (t0 + e < tokens) {
+          const int x = (int)t0 + e;
+          while (x - s_cu[b] >= s_new[b] - s_old[b]) ++b;  // the next sequence with new tokens
+          pos[e] = s_old[b] + (x - s_cu[b]);
+          const int page = (int)((uint32_t)pos[e] / (uint32_t)p.page_size);
+          first[e] = page * p.page_size;
+          wants[e] = !(p.shared && page < p.shared[b]);
+          if (wants[e]) id[e] = p.table[(size_t)b * p.max_pages + page];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const bool fine = id[e] >= 0 && id[e] < most;
+        slot[e] = wants[e] && fine ? id[e] * p.page_size + (pos[e] - first[e]) : -1;
+        if (wants[e] && !fine) atomicOr(&g_pages_err, kErrBounds);
+      }
+      if constexpr (N == 4) {
+        if (p.vec && t0 + 4 <= p.max_new) {
+          *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+          *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+          continue;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e)
         if (t0 + e < p.max_new) {
           p.slots[t0 + e] = slot[e];
           p.positions[t0 + e] = pos[e];
         }
     }
-  }
+  };
+  if (p.max_new <= step)
+    tokens_of(std::integral_constant<int, 1>{});
+  else
+    tokens_of(std::integral_constant<int, 4>{});
 }
 
 // Rows to slots: a thread takes AHEAD chunks of 16 bytes, of K and of V, all loads
