@@ -19,7 +19,9 @@
 // with one token after another, each with its own way to its page, a step of 64 sequences
 // took 6.2 us instead of 3.6, 256 sequences with 40000 new tokens 14.7 instead of 10.6.
 //
-// Write.  A copy: every row is read and written once.
+// Write.  A copy: every row is read and written once, eight 16-byte loads per thread
+// ahead of their stores.  65536 tokens of 8 heads (D = 128) take 78 us, 6.8 TB/s, a plain
+// copy's rate; 64 tokens 2.8 us.
 #include <type_traits>
 
 #include "fa.h"
