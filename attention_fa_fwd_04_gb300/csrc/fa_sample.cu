@@ -133,7 +133,8 @@ struct Logits<__nv_bfloat16> : Logits16<__nv_bfloat16> {
     return (r & 0x7fffu) > 0x7f80u ? NEG : (r == 0x8000u ? (raw)0 : r);
   }
   static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
-    const __nv_bfloat162 neg = {__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80)}, zero = {__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)};
+    const __nv_bfloat162 neg = __bfloat162bfloat162(__ushort_as_bfloat16(NEG));
+    const __nv_bfloat162 zero = __bfloat162bfloat162(__ushort_as_bfloat16(0));
     __nv_bfloat162* const x = reinterpret_cast<__nv_bfloat162*>(&g);
     __nv_bfloat162 m = neg;
 #pragma unroll
@@ -159,7 +160,8 @@ struct Logits<__half> : Logits16<__half> {
     return (r & 0x7fffu) > 0x7c00u ? NEG : (r == 0x8000u ? (raw)0 : r);
   }
   static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
-    const __half2 neg = {__ushort_as_half(0xfc00), __ushort_as_half(0xfc00)}, zero = {__ushort_as_half(0), __ushort_as_half(0)};
+    const __half2 neg = __half2half2(__ushort_as_half(NEG));
+    const __half2 zero = __half2half2(__ushort_as_half(0));
     __half2* const x = reinterpret_cast<__half2*>(&g);
     __half2 m = neg;
 #pragma unroll
@@ -318,7 +320,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   __shared__ float2 s_first[sa::SEGS];       // every warp's largest logit, smallest lane maximum
   __shared__ float2 s_warp[2][2][sa::SEGS];  // per round and quantity: every warp's sum
   __shared__ int s_cnt[sa::SEGS];
-  __shared__ __align__(16) unsigned long long s_list[sa::LIST + 8];  // tokens to rank: key, place inverted
+  // Tokens to rank: key, index inverted.
+  __shared__ __align__(16) unsigned long long s_list[sa::LIST + 8];
   __shared__ int s_rank[sa::LIST];
   __shared__ float2 s_block[sa::WARPS + 1];
   __shared__ uint32_t s_scan[sa::WARPS];
@@ -327,7 +330,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   __shared__ uint32_t s_key[2];
   __shared__ float2 s_pair[5];
   constexpr uint32_t NONE = 0xffffffffu;
-  __shared__ uint32_t s_found;  // a bin (11 bits), how many of its key (20), whether that is fewer than it has (few lie there)
+  // A bin (11 bits), how many of its key (20), whether that is fewer than it has (where a bin
+  // is more than a key: whether few lie in it).
+  __shared__ uint32_t s_found;
   __shared__ float2 s_low;  // T ln(min_p)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int C = p.cluster;
@@ -346,14 +351,17 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   if (t < 4) s_listed[t] = 0;
   pdl_wait_primary();
 
+  auto arrive = [] { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); };
+  auto wait = [] { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); };
   auto sync = [&] {  // the cluster's CTAs meet; what they stored is visible
     if (C > 1) {
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      arrive();
+      wait();
     } else {
       __syncthreads();
     }
   };
+  if (C > 1) arrive();  // (waited for below: no CTA is written to before it runs)
   // ---- the row into shared memory, its largest logit ----
   const T* const src = static_cast<const T*>(p.logits) + row * p.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
@@ -398,6 +406,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     }
+    if (C > 1) wait();
     if (lane < C) put(remote(&s_first[seg_id], lane), hi, lo);
   }
   // log2(e) / T in two floats.
@@ -590,7 +599,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
     if (at < sa::LIST) {
 #pragma unroll 1
       for (int r = 0; r < C; ++r)
-        put(remote(&s_list[at], r), __uint_as_float(~(uint32_t)(first + x)), __uint_as_float(Lg::key(l)));
+        put(remote(&s_list[at], r), __uint_as_float(~(uint32_t)(first + x)),
+            __uint_as_float(Lg::key(l)));
     }
   };
   auto shift_of = [](uint32_t lo, uint32_t hi) { return max(0, 21 - __clz((int)(hi - lo))); };
@@ -716,7 +726,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         // (A range that is too small, or too large, to divide by counts as one bin.)
         const float vfrom = value_of(from), range = top - vfrom;
         const float per = range > 0x1p-100f ? __fdividef((float)(sa::BINS - 1), range) : 0.f;
-        if (mx >= vfrom) atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::BINS - 1)], 1u);
+        if (mx >= vfrom)
+          atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::BINS - 1)], 1u);
         sync();
         uint32_t h[4];
         gather(h);
@@ -728,7 +739,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           before += h[e];
         }
         __syncthreads();
-        lo = range == 0.f ? kmax : max(lo, Lg::key(Lg::from(top - __fdividef((float)s_i[0] + 1.01f, per))));
+        const float bound = top - __fdividef((float)s_i[0] + 1.01f, per);
+        lo = range == 0.f ? kmax : max(lo, Lg::key(Lg::from(bound)));
         const float least_listed = value_of(lo);
         each([&](int i, uint4 g) {
           each_of(within(g, least_listed, INFINITY), i, enlist);
@@ -745,7 +757,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           for (int by_index = 0; by_index < 2; ++by_index) {
             // The list in order: by logit, then what is kept of it by index.
             x = ranked(count, x);
-            const uint32_t key = (uint32_t)(by_index ? x : x >> 32), place = ~(uint32_t)(by_index ? x >> 32 : x);
+            const uint32_t key = (uint32_t)(by_index ? x : x >> 32);
+            const uint32_t place = ~(uint32_t)(by_index ? x >> 32 : x);
             bool keep = t < (by_index ? count : min(have, k));
             Sum2 w{0.f, 0.f};
             if (keep) w = weigh.one(value_of(key));
@@ -857,14 +870,16 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         const float fine_top = __fmaf_rn(fine.x, top, fine0 - 8388608.f);
         const float coarse_top = __fmaf_rn(coarse.x, top, coarse0 - 8388608.f);
         auto below_top = [&](int b) {  // in temperatures, the middle of a bin
-          return b < 513 ? ((float)b - fine_top) * (1.f / 256.f) : ((float)b - coarse_top) * (1.f / 64.f);
+          return b < 513 ? ((float)b - fine_top) * (1.f / 256.f)
+                         : ((float)b - coarse_top) * (1.f / 64.f);
         };
         if (t == 0) s_i[3] = -1;
         each([&](int, uint4 g) {
 #pragma unroll
           for (int x = 0; x < GROUP / 2; ++x) {
             const float2 v = Lg::pair(g, x);
-            const float2 z = __ffma2_rn(v, fine, twice(fine0)), y = __ffma2_rn(v, coarse, twice(coarse0));
+            const float2 z = __ffma2_rn(v, fine, twice(fine0));
+            const float2 y = __ffma2_rn(v, coarse, twice(coarse0));
             const uint32_t a = __float_as_uint(fminf(z.x, y.x)) - 0x4b000000u;
             const uint32_t b = __float_as_uint(fminf(z.y, y.y)) - 0x4b000000u;
             if (a < sa::BINS) atomicAdd(&hist[a], 1u);
@@ -887,7 +902,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         want *= tp;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (before < want && want <= before + m4[e]) s_i[3] = (4 * t + e) << 1 | (3 * h[e] <= 3 * sa::LIST / 4 ? 1 : 0);
+          if (before < want && want <= before + m4[e])
+            s_i[3] = (4 * t + e) << 1 | (h[e] <= sa::LIST / 4 ? 1 : 0);
           before += m4[e];
         }
         __syncthreads();
@@ -1010,7 +1026,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           const uint32_t off = ((uint32_t)(4 * t + e) << shift) + ((1u << shift) >> 1);
           return weigh.one(value_of(bhi - min(off, bspan)));
         };
-        auto count_of = [&](int e) { return (int)(e == 0 ? h[0] : e == 1 ? h[1] : e == 2 ? h[2] : h[3]); };
+        auto count_of = [&](int e) {
+          return (int)(e == 0 ? h[0] : e == 1 ? h[1] : e == 2 ? h[2] : h[3]);
+        };
         Sum2 sum{0.f, 0.f}, in;
         if (h[0] | h[1] | h[2] | h[3]) {
 #pragma unroll 1
@@ -1039,7 +1057,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           for (;; ++e) {  // (the last one that has any, if the sums' rounding says none)
             m = count_of(e);
             const Sum2 w = weight_of(e), after = sum_of(before, times(w, (float)m));
-            if (m && (!exceeds(target, after) || e == 3 || (h[3] | (e < 2 ? h[2] : 0) | (e < 1 ? h[1] : 0)) == 0)) {
+            const bool last = e == 3 || (h[3] | (e < 2 ? h[2] : 0) | (e < 1 ? h[1] : 0)) == 0;
+            if (m && (last || !exceeds(target, after))) {
               // So many of the key as it takes to come to the target.
               const Sum2 need = sum_of(target, Sum2{-before.hi, -before.lo});
               const int most = m;
@@ -1047,7 +1066,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
               while (m > 1 && !exceeds(target, sum_of(before, times(w, (float)(m - 1))))) --m;
               while (m < most && exceeds(target, sum_of(before, times(w, (float)m)))) ++m;
               s_found = (uint32_t)(4 * t + e) << 21 | (uint32_t)m << 1 |
-                      ((shift > 0 ? 3 * most <= 3 * sa::LIST / 4 : m < most) ? 1u : 0u);
+                      ((shift > 0 ? most <= sa::LIST / 4 : m < most) ? 1u : 0u);
               break;
             }
             before = after;
@@ -1236,8 +1255,11 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
       if (__any_sync(0xffffffffu, a || b)) {
         float2 hi, q;
         weigh(v, &hi, &q);
-        if (a) o.x = __fmaf_rn(hi.x, i_hi, __fmaf_rn(hi.x, i_lo, __fmul_rn(__fmul_rn(hi.x, q.x), i_hi)));
-        if (b) o.y = __fmaf_rn(hi.y, i_hi, __fmaf_rn(hi.y, i_lo, __fmul_rn(__fmul_rn(hi.y, q.y), i_hi)));
+        auto share = [&](float h, float q) {
+          return __fmaf_rn(h, i_hi, __fmaf_rn(h, i_lo, __fmul_rn(__fmul_rn(h, q), i_hi)));
+        };
+        if (a) o.x = share(hi.x, q.x);
+        if (b) o.y = share(hi.y, q.y);
       }
       if (x >= 0 && x < p.V) dst[x] = o.x;
       if (x + 1 >= 0 && x + 1 < p.V) dst[x + 1] = o.y;

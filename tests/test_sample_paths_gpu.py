@@ -152,3 +152,27 @@ def test_refuses_what_eight_sms_do_not_hold(fa):
         with pytest.raises(fa.FAError) as e:
             fa.sample(torch.zeros(1, V, dtype=dtype, device="cuda"), u)
         assert e.value.status == fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_nan_and_zeros_of_both_signs(fa, dtype):
+    """NaN of either sign counts as -infinity; -0 and 0 are equal, and go by index."""
+    g = gen(11)
+    V = 3000
+    x = torch.randn(6, V, generator=g)
+    x[0, ::3] = float("nan")
+    x[1, 1::2] = -float("nan")
+    x[2] = torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0)
+    x[3] = torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0)
+    x[3, ::7] = -1.0
+    x[4, ::2] = float("inf")
+    x[4, 1::4] = float("nan")
+    x[5] = float("nan")
+    x[5, 2222] = -3.0
+    x = x.to(DT[dtype])
+    assert torch.signbit(x[2]).any() and x.isnan().any()
+    u = us(6, g)
+    for k in (None, [100] * 6, [1401] * 6):
+        for p in (None, [0.71313] * 6):
+            check(fa, x, u, k=k, p=p)
+            check(fa, x, u, T=[0.0] * 6, k=k, p=p)
