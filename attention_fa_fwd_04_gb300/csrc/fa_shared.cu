@@ -876,7 +876,8 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);
   volatile uint32_t* tile_bad = issued + 1;  // [BAD_RING]
-  static_assert(2 * C::NSTAGE * 8 + (9 + 2 * sh::RING + 2 * sh::FEW_WARPS) * 8 + 12 + 4 * sh::BAD_RING <= C::SMEM_BAR, "barrier block");
+  static_assert(2 * C::NSTAGE * 8 + (9 + 2 * sh::RING + 2 * sh::FEW_WARPS) * 8 + 12 +
+                        4 * sh::BAD_RING <= C::SMEM_BAR, "barrier block");
   uint8_t* const s_ring = reinterpret_cast<uint8_t*>(full) + C::SMEM_BAR;  // stretches told
   sh::Plan* const plan = reinterpret_cast<sh::Plan*>(s_ring + C::SMEM_RING);
 
@@ -984,7 +985,8 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
           if (lane == 0) *issued = cnt + 1;
         };
         auto slot_free = [&](uint32_t cnt) {
-          return mbar_wait<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag, &g_shared_err, 1);
+          return mbar_wait<true>(&empty[cnt % NSTAGE], ((cnt / NSTAGE) & 1) ^ 1, abort_flag,
+                                 &g_shared_err, 1);
         };
         // Pages are looked up two tiles ahead.
         int pos = 0, pos_n = 0, pos_nn = 0;
@@ -1032,7 +1034,8 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
         uint32_t tc = 0, cw[2] = {0, 0};
         bool ok = true;
         auto landed = [&](uint32_t cnt, unsigned site) {
-          ok = mbar_wait<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, &g_shared_err, site);
+          ok = mbar_wait<false>(&full[cnt % NSTAGE], (cnt / NSTAGE) & 1, abort_flag, &g_shared_err,
+                                site);
           tc_fence_after();
           return ok;
         };
@@ -1149,7 +1152,8 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 32 / AT_ONCE; ++k) {
           const int from = __shfl_sync(0xffffffffu, qrow, k * AT_ONCE + lane / LANES);
-          v[k] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (size_t)max(from, 0) * D)[x];
+          const T* const row = static_cast<const T*>(p.q) + (size_t)max(from, 0) * D;
+          v[k] = reinterpret_cast<const uint4*>(row)[x];
           if (from < 0) v[k] = make_uint4(0u, 0u, 0u, 0u);
         }
         uint8_t* const dst = sQ + i * C::TILE_BYTES + (x >> 3) * sh::HALF_BYTES;
@@ -1425,7 +1429,8 @@ __global__ void __launch_bounds__(join::THREADS, join::resident(AHEAD)) shared_m
     for (int u = 0; u < AHEAD; ++u) join_in(ml[u], ov[u]);
   }
   for (int o = width; o < RC; o <<= 1) {
-    const float2 a = make_float2(__shfl_xor_sync(0xffffffffu, M, o), __shfl_xor_sync(0xffffffffu, den, o));
+    const float2 a =
+        make_float2(__shfl_xor_sync(0xffffffffu, M, o), __shfl_xor_sync(0xffffffffu, den, o));
     const float4 v =
         make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
                     __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
