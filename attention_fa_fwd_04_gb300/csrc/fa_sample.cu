@@ -33,9 +33,9 @@
 // that HBM is read once however many passes there are.  Every thread has consecutive
 // tokens, so that its sums are also what finds the token in the end.
 //
-// Measured (device time of one call in a captured sequence): 13.3 us for one row of 32000
-// fp32 logits with top-k and top-p, 49.9 for 64 rows of 128000 bf16 with top-p and min-p
-// (HBM's share is 2.4), 25.9 for 200 of 50257 fp16 with temperature alone (3.0), 105 for
+// Measured (device time of one call in a captured sequence): 12.9 us for one row of 32000
+// fp32 logits with top-k and top-p, 49.7 for 64 rows of 128000 bf16 with top-p and min-p
+// (HBM's share is 2.4), 26.4 for 200 of 50257 fp16 with temperature alone (3.0), 101 for
 // 512 of 32000 fp32 with top-k, top-p and the distributions written (19.4).  What bounds
 // it: the two passes of weights (about half of a row's time with top-p), and the
 // chain of meetings, scans and rankings between them (some 20000 clocks), of which two
@@ -327,13 +327,14 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   __shared__ uint32_t s_scan[sa::WARPS];
   __shared__ float s_fscan[sa::WARPS];
   __shared__ int s_i[4], s_cut, s_listed[4];
-  __shared__ uint32_t s_key[2];
+  __shared__ uint32_t s_border;
   __shared__ float2 s_pair[5];
   constexpr uint32_t NONE = 0xffffffffu;
   // A bin (11 bits), how many of its key (20), whether that is fewer than it has (where a bin
   // is more than a key: whether few lie in it).
   __shared__ uint32_t s_found;
   __shared__ float2 s_low;  // T ln(min_p)
+  __shared__ float s_from;  // a bound of the lanes' maxima that matter
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int C = p.cluster;
   const int rank = (int)(blockIdx.x & (unsigned)(C - 1));  // (C is 1, 2, 4 or 8)
@@ -420,17 +421,10 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
                                           1.92596299112661746887e-8f));
   }
   sync();
-  float top = -INFINITY, least = INFINITY;
-  for (int i = lane; i < segs; i += 32) {
-    const float2 v = s_first[i];
-    top = fmaxf(top, v.x);
-    least = fminf(least, v.y);
-  }
+  float top = -INFINITY;
+  for (int i = lane; i < segs; i += 32) top = fmaxf(top, s_first[i].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 
   // Every group of this thread's: f(its index in the part, the group).  The lanes begin
   // at different ones, so that they read different banks.
@@ -467,7 +461,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   // Logits of +infinity share the weight: they become 0 and all others -infinity.
   const bool was_inf = top == INFINITY;
   if (was_inf) {
-    mx = least = -INFINITY;
+    mx = -INFINITY;
     each([&](int i, uint4 g) {
       alignas(16) raw x[GROUP];
       *reinterpret_cast<uint4*>(x) = g;
@@ -700,44 +694,32 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
       uint32_t lo = kneg + 1, hi = kmax;
       const int w = (k + 31) / 32;
       if (k <= 3 * sa::LIST / 4 && 3 * k <= sa::THREADS * C) {
-        // Where the k-th of the maxima is, in 2048 bins: not below the w-th largest of
-        // the warps' smallest ones (nearly; 18 steps of a bisection).
-        uint32_t from = Lg::key(Lg::from(least)), over = kmax + 1;
-        uint32_t key4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          key4[i] = 32 * i + lane < segs ? Lg::key(Lg::from(s_first[32 * i + lane].y)) : 0u;
-        if (was_inf || warp != 0) over = from;
-#pragma unroll 1
-        for (int i = 0; i < 18 && over - from > 1; ++i) {
-          const uint32_t mid = from + (over - from) / 2;
-          int count = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) count += __popc(__ballot_sync(0xffffffffu, key4[j] >= mid));
-          if (count >= w) {
-            from = mid;
-          } else {
-            over = mid;
+        // Where the k-th of the maxima is, in 512 bins from the top down to the w-th largest of
+        // the warps' smallest ones.
+        if (t < segs) {
+          const float least = s_first[t].y;
+          int above = 0;
+#pragma unroll 8
+          for (int i = 0; i < segs; ++i) {
+            const float o = s_first[i].y;
+            above += o > least || (o == least && i < t);
           }
+          if (above == w - 1) s_from = was_inf ? -INFINITY : least;
         }
-        if (t == 0) s_key[0] = from;
         __syncthreads();
-        from = s_key[0];
         // (A range that is too small, or too large, to divide by counts as one bin.)
-        const float vfrom = value_of(from), range = top - vfrom;
-        const float per = range > 0x1p-100f ? __fdividef((float)(sa::BINS - 1), range) : 0.f;
-        if (mx >= vfrom)
-          atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::BINS - 1)], 1u);
+        const float from = s_from, range = top - from;
+        const float per = range > 0x1p-100f ? __fdividef((float)(sa::THREADS - 1), range) : 0.f;
+        if (mx >= from)
+          atomicAdd(&s_hist[round & 1][min((int)((top - mx) * per), sa::THREADS - 1)], 1u);
         sync();
-        uint32_t h[4];
-        gather(h);
-        turn();
-        uint32_t before = sum_before(h[0] + h[1] + h[2] + h[3], s_scan);
+        uint32_t h = s_hist[round & 1][t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the bin that the k-th falls into
-          if (before < (uint32_t)k && (uint32_t)k <= before + h[e]) s_i[0] = 4 * t + e;
-          before += h[e];
-        }
+        for (int c = 1; c < sa::CLUSTER; ++c)
+          if (c < C) h += (uint32_t)get(remote(&s_hist[round & 1][t], (rank + c) & (C - 1)));
+        turn();
+        const uint32_t before = sum_before(h, s_scan);
+        if (before < (uint32_t)k && (uint32_t)k <= before + h) s_i[0] = t;  // the k-th's bin
         __syncthreads();
         const float bound = top - __fdividef((float)s_i[0] + 1.01f, per);
         lo = range == 0.f ? kmax : max(lo, Lg::key(Lg::from(bound)));
@@ -768,7 +750,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
               keep = keep && (t == 0 || key >= lowest_key());
               count = __syncthreads_count(keep);
               if (t == count - 1) {
-                s_key[1] = key;
+                s_border = key;
                 s_i[3] = (int)place;
                 s_i[0] = INT_MAX;
                 s_i[1] = -1;
@@ -786,7 +768,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           done = true;
           total = all;
           cut = s_i[3];
-          border = s_key[1];
+          border = s_border;
         }
       }
       // The border by counts: 2048 bins per pass.  (With fewer than k finite logits all stay.)
