@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
     h[2] = s.z;
     h[3] = s.w;
   };
-  auto turn = [&] {  // (after the barrier, before the block's next one)
+  auto turn = [&] {  // (after the barrier, and before the block's next one, which has to follow)
     *reinterpret_cast<uint4*>(&s_hist[(round & 1) ^ 1][4 * t]) = make_uint4(0, 0, 0, 0);
     // (Other CTAs add to the next round's: the one after it.)
     if (t == 0) s_listed[(round + 2) & 3] = 0;
@@ -769,6 +769,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           total = all;
           cut = s_i[3];
           border = s_border;
+        } else {
+          __syncthreads();  // (the bins are zero before anybody counts in them)
         }
       }
       // The border by counts: 2048 bins per pass.  (With fewer than k finite logits all stay.)

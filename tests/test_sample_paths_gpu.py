@@ -176,3 +176,23 @@ def test_nan_and_zeros_of_both_signs(fa, dtype):
         for p in (None, [0.71313] * 6):
             check(fa, x, u, k=k, p=p)
             check(fa, x, u, T=[0.0] * 6, k=k, p=p)
+
+
+def test_long_lists_again_and_again(fa):
+    """Rows whose list overflows, so that the border comes from counts: many at once, many
+    times, always the tokens that the order says."""
+    g = gen(12)
+    R, V, k = 600, 777, 166
+    x = (torch.randn(R, V, generator=g) * 2).round() / 2
+    x = x.half()
+    u = torch.rand(R, generator=g).cuda()
+    ks = torch.full((R,), k, dtype=torch.int32, device="cuda")
+    order = torch.sort(x.float(), dim=-1, descending=True, stable=True).indices
+    want = torch.zeros(R, V, dtype=torch.bool).scatter_(-1, order[:, :k], True).cuda()
+    xd = x.cuda()
+    first = None
+    for _ in range(60):
+        tok, probs = fa.sample(xd, u, top_k=ks, probs=True)
+        assert torch.equal(probs > 0, want)
+        first = tok if first is None else first
+        assert torch.equal(tok, first)
