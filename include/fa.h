@@ -680,9 +680,10 @@ const char* fa_status_string(int status);
  * offsets or page ids out of range, or an index self-check), FA_ERR_CUDA if
  * the read itself failed.
  * If detail != NULL it receives the raw bits: the prefill (and backward) word
- * in bits 0-15, the decode word (also of the cache append, tree and shared decode,
- * verification, compaction, page update and page writes) in bits 16-31; in each, bit 0 = a wait timed out (bits 8-15:
- * which wait), bit 1 = a bounds check fired.  Bounds bit with site 15: the
+ * in bits 0-15, the decode word (also of the cache append, tree and shared
+ * decode, verification, compaction, page update and page writes) in bits
+ * 16-31; in each, bit 0 = a wait timed out (bits 8-15: which wait), bit 1 = a
+ * bounds check fired.  Bounds bit with site 15: the
  * D = 128 backward dK/dV kernel found its dynamic shared memory too far from
  * a 1 KiB boundary to lay out its rings, and its CTAs left without work.
  */
