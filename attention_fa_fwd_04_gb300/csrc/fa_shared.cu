@@ -39,7 +39,7 @@
 // Measured (both kernels, device time in a captured sequence; floor): 64 sequences of 8 rows
 // per kv head behind 8192 tokens 57.5 us (31.5), 32 of 16 rows behind 65536 146.5 (73.4: 956
 // TFLOP/s and 3.0 TB/s together), 48 of 16 rows in 5 groups, D = 64, 30.5 (4.2), 8 of 4 rows
-// behind 1500 18.0 (0.4).  What bounds it: with many rows the softmax (two 128-row tiles per
+// behind 1500 17.7 (0.4).  What bounds it: with many rows the softmax (two 128-row tiles per
 // key tile take 1.76 us, their MMAs 1.34) on the SMs of the prefixes and the stream on the
 // others; with few, the lists (4 us), the first tiles (8) and the merge (4 to 10).
 #include <math.h>
@@ -179,6 +179,10 @@ struct Shape {
   int cost;    // places of a tile
   int S, len;  // strips, tiles of each but the last
 };
+// Several pairs of row tiles against more keys than L2 keeps.
+__device__ __forceinline__ bool can_be_cut(const SharedParams& p, const Shape& s) {
+  return s.n_rt > 1 && (long long)s.T * p.Hkv > p.keep_tiles;
+}
 __device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int rows, int lo, int hi,
                                           int W) {
   Shape s;
@@ -189,7 +193,7 @@ __device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int r
   s.cost = few ? 1 : sh::COST;
   s.S = 1;
   s.len = s.T;
-  if (s.n_rt > 1 && (long long)s.T * p.Hkv > p.keep_tiles && s.T > W) {
+  if (can_be_cut(p, s) && s.T > W) {
     const uint32_t S = ((uint32_t)s.T + W / 2) / (uint32_t)W;
     s.len = (int)(((uint32_t)s.T + S - 1) / S);
     s.S = (s.T + s.len - 1) / s.len;
@@ -340,8 +344,12 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   auto pieces_at = [&](int o, const Shape& s) {
     return o < p.groups ? pieces_of(p, s) << 32 : pieces_of(p, s);
   };
+  // With an owner per thread, sums of tiles and pieces (groups' in the upper half) up to
+  // each owner; else the tiles of either kind.
+  const bool one = owners <= sh::THREADS;
   Keys mine = {};  // of this thread's first owner
-  long long tiles[2] = {0, 0}, all_tiles[2];
+  long long tiles[2] = {0, 0}, all_tiles[2], my_tiles = 0, my_pieces = 0, all_pieces = 0;
+  bool cut = false;  // into strips
   for (int o = t; o < owners; o += sh::THREADS) {
     const Keys k = keys_of(p, pl, o);
     if (o == t) {
@@ -352,8 +360,20 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
     }
     const Shape s = shape_of(p, few(o), k.rows, k.lo, k.hi, INT32_MAX);
     tiles[few(o)] += (long long)p.Hkv * s.n_rt * s.T * s.cost;
+    if (one) my_pieces = pieces_at(o, s);
+    cut |= can_be_cut(p, s);
   }
-  block_sums(tiles[0], tiles[1], pl->sums, &all_tiles[0], &all_tiles[1]);
+  long long sum_tiles = my_tiles = tiles[0] + tiles[1], sum_pieces = my_pieces;
+  if (one) {
+    if (t == 0) pl->total[0] = 0;
+    block_sums(sum_tiles, sum_pieces, pl->sums, &all_tiles[1], &all_pieces);
+    if (t == p.groups - 1) pl->total[0] = sum_tiles;
+    cut = __syncthreads_or(cut);
+    all_tiles[0] = p.few ? pl->total[0] : all_tiles[1];
+    all_tiles[1] -= all_tiles[0];
+  } else {
+    block_sums(tiles[0], tiles[1], pl->sums, &all_tiles[0], &all_tiles[1]);
+  }
   const int n = p.ctas;
   // CTAs of the first kind, for lists of a and z places.
   auto share = [&](long long a, long long z) {
@@ -370,19 +390,26 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   auto places_at = [&](int o, const Keys& k) {
     return p.Hkv * places_per_head(shape_of(p, few(o), k.rows, k.lo, k.hi, W), slack[few(o)]);
   };
-  // Sums of places and pieces (groups' in the upper half) up to each owner; with an owner
-  // per thread they are those of the list, else they are made again chunk by chunk.
-  const bool one = owners <= sh::THREADS;
-  long long total[2], my_places = 0, my_pieces = 0, sum_places, sum_pieces;
-  if (one) {
+  // Sums of places up to each owner; with an owner per thread they are those of the list
+  // (a piece each where nothing is cut), else they are made again chunk by chunk.
+  long long total[2], my_places = 0, sum_places = 0;
+  if (one && !cut) {
+    const long long of_groups = all_pieces >> 32, of_seqs = all_pieces & 0xffffffffll;
+    const long long g = sum_pieces >> 32, q = sum_pieces & 0xffffffffll;
+    total[0] = all_tiles[0] + slack[0] * (of_groups + (p.few ? 0 : of_seqs));
+    total[1] = p.few ? all_tiles[1] + slack[1] * of_seqs : 0;
+    my_places = my_tiles + slack[few(t)] * (t < p.groups ? my_pieces >> 32 : my_pieces);
+    sum_places = few(t) ? total[0] + (sum_tiles - all_tiles[0]) + slack[1] * q
+                        : sum_tiles + slack[0] * (g + q);
+  } else if (one) {
     if (t < owners) {
       my_places = places_at(t, mine);
       my_pieces = pieces_at(t, shape_of(p, few(t), mine.rows, mine.lo, mine.hi, W));
     }
     sum_places = my_places;
     sum_pieces = my_pieces;
+    __syncthreads();
     if (t == 0) pl->total[0] = 0;
-    long long all_pieces;
     block_sums(sum_places, sum_pieces, pl->sums, &total[1], &all_pieces);
     if (t == p.groups - 1) pl->total[0] = sum_places;
     __syncthreads();
