@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   using raw = typename Lg::raw;
   constexpr raw NEG = Lg::NEG;
   constexpr int GROUP = Lg::GROUP;
+  constexpr int AHEAD = 8;
+  constexpr uint32_t NEGS = sizeof(raw) == 2 ? NEG * 0x10001u : NEG;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float2 s_table[128 * 16];
   __shared__ __align__(16) uint32_t s_hist[2][sa::BINS];
@@ -378,22 +380,31 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   const float uu = u > 0.f ? fminf(u, 2.f) : 0.f;
   float mx = -INFINITY;
   {
-    const int g0 = warp * 32 * own;
-#pragma unroll 4
-    for (int i = lane; i < 32 * own; i += 32) {
-      const int e = first + (g0 + i) * GROUP;  // the group's first token
-      uint4 v;
-      if (e >= 0 && e + GROUP <= p.V) {
-        v = *reinterpret_cast<const uint4*>(src + e);
-      } else {
-        alignas(16) raw x[GROUP];
+    const int g0 = warp * 32 * own, from = first + g0 * GROUP;  // this warp's
+    // Eight loads ahead of what is done with them.
+    const uint4* const at = reinterpret_cast<const uint4*>(src + from);
+    for (int i0 = lane; i0 < 32 * own; i0 += 32 * AHEAD) {
+      uint4 v[AHEAD];
 #pragma unroll
-        for (int j = 0; j < GROUP; ++j)
-          x[j] = e + j >= 0 && e + j < p.V ? reinterpret_cast<const raw*>(src)[e + j] : NEG;
-        v = *reinterpret_cast<uint4*>(x);
+      for (int j = 0; j < AHEAD; ++j) {
+        const int i = i0 + 32 * j, e = from + i * GROUP;
+        v[j] = make_uint4(NEGS, NEGS, NEGS, NEGS);
+        if (i < 32 * own && e >= 0 && e + GROUP <= p.V) v[j] = at[i];
       }
-      mx = fmaxf(mx, Lg::clean(v));
-      part[g0 + i] = v;
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const int i = i0 + 32 * j, e = from + i * GROUP;
+        if (i >= 32 * own) break;
+        if ((e < 0 && e + GROUP > 0) || (e < p.V && e + GROUP > p.V)) {  // the row's ends
+          alignas(16) raw x[GROUP];
+#pragma unroll
+          for (int y = 0; y < GROUP; ++y)
+            x[y] = e + y >= 0 && e + y < p.V ? reinterpret_cast<const raw*>(src)[e + y] : NEG;
+          v[j] = *reinterpret_cast<uint4*>(x);
+        }
+        mx = fmaxf(mx, Lg::clean(v[j]));
+        part[g0 + i] = v[j];
+      }
     }
   }
   if (t == sa::THREADS - 32 && mp > 0.f) {
