@@ -582,7 +582,7 @@ __device__ __forceinline__ size_t shared_qrow(const SharedParams& p, int row0, i
 // after half (A's halves HALF_BYTES apart).
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t b_half,
-                                        uint32_t hi, uint32_t idesc) {
+                                           uint32_t hi, uint32_t idesc) {
 #pragma unroll
   for (int k = 0; k < D / 16; ++k)
     mma_ss_lh(d, a + (((k >> 2) * sh::HALF_BYTES + (k & 3) * 32) >> 4), hi,
@@ -590,7 +590,7 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, u
 }
 // (+)= P (tensor memory) V.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint32_t v, uint32_t hi,
-                                        uint32_t idesc, bool add) {
+                                           uint32_t idesc, bool add) {
 #pragma unroll
   for (int k = 0; k < sh::BN / 16; ++k)
     mma_ts_lh(d, p + k * 8, v + (uint32_t)((k * 16 * 128) >> 4), hi, idesc,
@@ -952,10 +952,10 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
       uint8_t* const tiles = sQ + warp * 4 * C::FEW_KV;
       if (p.SqG <= 8)
         stream_keys<D, T, 1>(p, plan, &tmK32, &tmV32, tiles, few_full + 2 * warp,
-                              reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
+                             reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
       else
         stream_keys<D, T, 2>(p, plan, &tmK32, &tmV32, tiles, few_full + 2 * warp,
-                              reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
+                             reinterpret_cast<StreamWalk*>(s_ring + warp * 288), warp, abort_flag);
     }
     __syncthreads();
     if (warp == W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
