@@ -92,12 +92,21 @@ struct Seg {
   int twice;     // other rows meet the same keys: worth keeping in L2
 };
 
+// A unit's tiles.
+struct Shape {
+  int t0, T;   // first tile and tiles
+  int n_rt;    // pairs of row tiles
+  int cost;    // places of a tile
+  int S, len;  // strips, tiles of each but the last
+};
+
 // What every CTA finds out about the list, in shared memory.
 struct Plan {
   long long sums[2 * WARPS];
   long long x, hi;  // this CTA's range of places
   long long first;  // first place of owner o
   int o, piece0;    // owner; pieces of its kind before it
+  Shape s;          // and its tiles
   int W, slack, groups;
   int range, few;   // this CTA's (first) range; whether its warps stream
   int used;         // ranges of the streaming warps
@@ -172,20 +181,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// A unit's tiles.
-struct Shape {
-  int t0, T;   // first tile and tiles
-  int n_rt;    // pairs of row tiles
-  int cost;    // places of a tile
-  int S, len;  // strips, tiles of each but the last
-};
 // Several pairs of row tiles against more keys than L2 keeps.
-__device__ __forceinline__ bool can_be_cut(const SharedParams& p, const Shape& s) {
+__device__ __forceinline__ bool can_be_cut(const SharedParams& p, const sh::Shape& s) {
   return s.n_rt > 1 && (long long)s.T * p.Hkv > p.keep_tiles;
 }
-__device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int rows, int lo, int hi,
+__device__ __forceinline__ sh::Shape shape_of(const SharedParams& p, bool few, int rows, int lo, int hi,
                                           int W) {
-  Shape s;
+  sh::Shape s;
   const int keys = few ? sh::FEW_KEYS : sh::BN;
   s.t0 = lo / keys;
   s.T = hi > lo ? (int)(((uint32_t)hi + keys - 1) / keys) - s.t0 : 0;
@@ -200,10 +202,10 @@ __device__ __forceinline__ Shape shape_of(const SharedParams& p, bool few, int r
   }
   return s;
 }
-__device__ __forceinline__ long long places_per_head(const Shape& s, int slack) {
+__device__ __forceinline__ long long places_per_head(const sh::Shape& s, int slack) {
   return s.T > 0 ? (long long)s.n_rt * ((long long)s.T * s.cost + (long long)s.S * slack) : 0;
 }
-__device__ __forceinline__ long long pieces_of(const SharedParams& p, const Shape& s) {
+__device__ __forceinline__ long long pieces_of(const SharedParams& p, const sh::Shape& s) {
   return s.T > 0 ? (long long)p.Hkv * s.S * s.n_rt : 0;
 }
 
@@ -341,7 +343,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   // Places of the tiles in the lists: of the groups, and of the sequences where warps
   // stream them, else all in the first.
   auto few = [&](int o) { return p.few && o >= p.groups; };
-  auto pieces_at = [&](int o, const Shape& s) {
+  auto pieces_at = [&](int o, const sh::Shape& s) {
     return o < p.groups ? pieces_of(p, s) << 32 : pieces_of(p, s);
   };
   // With an owner per thread, sums of tiles and pieces (groups' in the upper half) up to
@@ -349,6 +351,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   const bool one = owners <= sh::THREADS;
   Keys mine = {};  // of this thread's first owner
   long long tiles[2] = {0, 0}, all_tiles[2], my_tiles = 0, my_pieces = 0, all_pieces = 0;
+  sh::Shape whole = {};
   bool cut = false;  // into strips
   for (int o = t; o < owners; o += sh::THREADS) {
     const Keys k = keys_of(p, pl, o);
@@ -358,9 +361,12 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
       pl->end[o] = k.hi;
       pl->tab[o] = k.tab;
     }
-    const Shape s = shape_of(p, few(o), k.rows, k.lo, k.hi, INT32_MAX);
+    const sh::Shape s = shape_of(p, few(o), k.rows, k.lo, k.hi, INT32_MAX);
     tiles[few(o)] += (long long)p.Hkv * s.n_rt * s.T * s.cost;
-    if (one) my_pieces = pieces_at(o, s);
+    if (one) {
+      my_pieces = pieces_at(o, s);
+      whole = s;
+    }
     cut |= can_be_cut(p, s);
   }
   long long sum_tiles = my_tiles = tiles[0] + tiles[1], sum_pieces = my_pieces;
@@ -429,7 +435,12 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   // CTAs of either kind by what their lists cost.  Ranges in use are each as long as a tile
   // at least, so that every one of them between the first and the last of a piece holds a
   // tile of it.
-  const int many = share(total[0], total[1]);
+  // (Units of a tile or two cost their starts too where they have no places for them: 64
+  // sequences with a token each behind 8192 43 us, 56 without; 32 with 30 tokens behind 65536
+  // 128 and 260.)
+  const int many = share(total[0], total[1] + (one && slack[1] == 0
+                                                   ? sh::SLACK_FEW * (all_pieces & 0xffffffffll)
+                                                   : 0));
   const long long most = quotient(total[0], 2 * sh::COST);
   const int used[2] = {most < 1 ? 1 : (int)min(most, (long long)max(many, 1)),
                        (int)max(1ll, min(total[1], (long long)(n - many) * sh::FEW_WARPS))};
@@ -462,6 +473,7 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
         pl->o = o;
         pl->first = first;
         pl->piece0 = piece0;
+        pl->s = one && !cut ? whole : shape_of(p, few(o), k.rows, k.lo, k.hi, W);
       }
       if (blockIdx.x == 0)
         p.owner[o] = SharedOwner{first - (few(o) ? total[0] : 0), piece0, k.lo, k.hi, k.row0, k.rows,
@@ -492,9 +504,9 @@ struct SharedWalk {
   long long x, hi, first;
   int o, piece0;
   Keys k;
-  Shape s;
+  sh::Shape s;
 };
-__device__ __forceinline__ void walk_owner(const SharedParams& p, const sh::Plan* pl, SharedWalk& w) {
+__device__ __forceinline__ void walk_keys(const SharedParams& p, const sh::Plan* pl, SharedWalk& w) {
   if (w.o < sh::KEPT) {
     w.k.lo = pl->lo[w.o];
     w.k.hi = pl->end[w.o];
@@ -505,6 +517,9 @@ __device__ __forceinline__ void walk_owner(const SharedParams& p, const sh::Plan
   } else {
     w.k = keys_of(p, pl, w.o);
   }
+}
+__device__ __forceinline__ void walk_owner(const SharedParams& p, const sh::Plan* pl, SharedWalk& w) {
+  walk_keys(p, pl, w);
   w.s = shape_of(p, pl->few, w.k.rows, w.k.lo, w.k.hi, pl->W);
 }
 __device__ __forceinline__ SharedWalk walk_start(const SharedParams& p, const sh::Plan* pl) {
@@ -515,7 +530,8 @@ __device__ __forceinline__ SharedWalk walk_start(const SharedParams& p, const sh
   w.hi = pl->hi;
   w.first = pl->first;
   w.piece0 = pl->piece0;
-  walk_owner(p, pl, w);
+  walk_keys(p, pl, w);
+  w.s = pl->s;
   return w;
 }
 __device__ __forceinline__ bool walk_next(const SharedParams& p, const sh::Plan* pl, SharedWalk& w,
@@ -1365,7 +1381,7 @@ __global__ void __launch_bounds__(join::THREADS, join::resident(AHEAD)) shared_m
       const SharedOwner o = l < 2 ? grp : own;
       const int rt = (l == 0 ? r0 : l == 1 ? r0 + rows - 1 : first) / (2 * sh::BM);
       const int few = p.few && l == 2;
-      const Shape s = shape_of(p, few, o.rows, o.lo, o.hi, list.W);
+      const sh::Shape s = shape_of(p, few, o.rows, o.lo, o.hi, list.W);
       const int slack = list.slack[few];
       const bool two = few || min(2 * sh::BM, o.rows - rt * 2 * sh::BM) > sh::BM;
       const long long head = o.first + hkv * places_per_head(s, slack);
