@@ -1534,7 +1534,8 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[
   if (e != cudaSuccess) return e;
   // Blocks of 32 rows' threads while all of them are resident at once: a row then has more
   // of them (48 sequences of 16 rows, D = 64: 30.6 us, 34.9 with blocks of all columns; 8 of
-  // 4 rows and 8200 keys 24.0, 26.0 with 6 loads at a time, 28.5 in both ways).
+  // 4 rows and 8200 keys 24.0, 26.0 with 6 loads at a time; 64 of 8 rows, whose blocks are
+  // not all resident, 69 us, 61 with blocks of all columns).
   const long long units = (long long)p.B * p.Hkv, wide = units * ((p.SqG + 31) / 32);
   auto fits = [&](int ahead) { return wide * (D / 32) <= (long long)join::resident(ahead) * p.ctas; };
   const dim3 by_columns((unsigned)(fits(6) ? wide : 1), D / 32);
