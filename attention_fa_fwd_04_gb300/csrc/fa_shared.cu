@@ -174,6 +174,7 @@ struct SharedParams {
   int page_size, max_pages, num_pages, box, ctas;
   long long keep_tiles;  // tiles of a unit, all kv heads, that L2 keeps
   float c;  // scale * log2(e)
+  int merge_rows;  // of a merge block
 };
 
 // a / b in 32 bits where both fit.
@@ -1336,8 +1337,8 @@ __global__ void __launch_bounds__(sh::THREADS, 1)
   }
 }
 
-// Merge: a block takes up to RC rows of one (sequence, kv head) and 256 / RC groups of four
-// columns.  A warp for each list finds out where their partials are, of the group's unit and
+// Merge: a block takes up to merge_rows <= RC rows of one (sequence, kv head) and 256 / RC
+// groups of four columns.  A warp for each list finds out where their partials are, of the group's unit and
 // of their own (the lanes take strips); then a thread takes four columns of a row and
 // walks the lists, 6 or 12 partials' loads at a time.  With fewer rows than RC, the threads of a
 // row's columns share the lists.
@@ -1356,8 +1357,9 @@ __global__ void __launch_bounds__(join::THREADS, join::resident(AHEAD)) shared_m
   __shared__ int s_group[2];  // first sequence of the group, or -1; its first such pair
   pdl_launch_dependents();
   const int t = threadIdx.x, lane = t & 31;
-  const int chunks = (p.SqG + RC - 1) / RC, unit = blockIdx.x / chunks;
-  const int first = (blockIdx.x - unit * chunks) * RC, rows = min(RC, p.SqG - first);
+  const int chunks = (p.SqG + p.merge_rows - 1) / p.merge_rows, unit = blockIdx.x / chunks;
+  const int first = (blockIdx.x - unit * chunks) * p.merge_rows;
+  const int rows = min(p.merge_rows, p.SqG - first);
   const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
   pdl_wait_primary();
   if (t < 96) {  // a warp for each list
@@ -1499,7 +1501,7 @@ __global__ void shared_zero_kernel(uint16_t* o, size_t n, float* lse, size_t nl)
 }
 
 template <int D, typename T>
-static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[4],
+static cudaError_t launch_shared(SharedParams& p, const CUtensorMap (&tm)[4],
                                  cudaStream_t stream) {
   using C = sh::Cfg<D>;
   constexpr int ALL = join::THREADS * 4 / D;  // rows of a merge block that takes all columns
@@ -1536,16 +1538,24 @@ static cudaError_t launch_shared(const SharedParams& p, const CUtensorMap (&tm)[
   // of them (48 sequences of 16 rows, D = 64: 30.6 us, 34.9 with blocks of all columns; 8 of
   // 4 rows and 8200 keys 24.0, 26.0 with 6 loads at a time; 64 of 8 rows, whose blocks are
   // not all resident, 69 us, 61 with blocks of all columns).
-  const long long units = (long long)p.B * p.Hkv, wide = units * ((p.SqG + 31) / 32);
-  auto fits = [&](int ahead) { return wide * (D / 32) <= (long long)join::resident(ahead) * p.ctas; };
-  const dim3 by_columns((unsigned)(fits(6) ? wide : 1), D / 32);
-  if (fits(12))
-    return launch_dependent(shared_merge_kernel<D, T, 32, 12>, by_columns, join::THREADS, stream, p);
-  if (fits(6))
-    return launch_dependent(shared_merge_kernel<D, T, 32, 6>, by_columns, join::THREADS, stream, p);
-  return launch_dependent(shared_merge_kernel<D, T, ALL, 6>,
-                          dim3((unsigned)(units * ((p.SqG + ALL - 1) / ALL))), join::THREADS,
-                          stream, p);
+  // (And fewer rows to a block as long as they are: 3 sequences of 32 rows behind 44000
+  // keys, D = 64, 34 us instead of 90.)
+  const long long units = (long long)p.B * p.Hkv;
+  auto blocks = [&](int rows) { return units * ((p.SqG + rows - 1) / rows); };
+  auto fits = [&](int rows, int ahead) {
+    return blocks(rows) * (D / 32) <= (long long)join::resident(ahead) * p.ctas;
+  };
+  for (int rows = 1; rows <= 32; rows *= 2) {
+    p.merge_rows = rows;
+    const dim3 grid((unsigned)blocks(rows), D / 32);
+    if (fits(rows, 12))
+      return launch_dependent(shared_merge_kernel<D, T, 32, 12>, grid, join::THREADS, stream, p);
+    if (rows == 32 && fits(rows, 6))
+      return launch_dependent(shared_merge_kernel<D, T, 32, 6>, grid, join::THREADS, stream, p);
+  }
+  p.merge_rows = ALL;
+  return launch_dependent(shared_merge_kernel<D, T, ALL, 6>, dim3((unsigned)blocks(ALL)),
+                          join::THREADS, stream, p);
 }
 
 int set_shared_wait_limit(unsigned long long ns) { return set_wait_limit_this_unit(ns); }
