@@ -33,9 +33,9 @@
 // that HBM is read once however many passes there are.  Every thread has consecutive
 // tokens, so that its sums are also what finds the token in the end.
 //
-// Measured (device time of one call in a captured sequence): 12.9 us for one row of 32000
-// fp32 logits with top-k and top-p, 42.6 for 64 rows of 128000 bf16 with top-p and min-p
-// (HBM's share is 2.4), 26.5 for 200 of 50257 fp16 with temperature alone (3.0), 96 for
+// Measured (device time of one call in a captured sequence): 13.0 us for one row of 32000
+// fp32 logits with top-k and top-p, 42.9 for 64 rows of 128000 bf16 with top-p and min-p
+// (HBM's share is 2.4), 27.6 for 200 of 50257 fp16 with temperature alone (3.0), 98.5 for
 // 512 of 32000 fp32 with top-k, top-p and the distributions written (19.4).  What bounds
 // it: the two passes of weights (about half of a row's time with top-p), and the
 // chain of meetings, scans and rankings between them (some 20000 clocks), of which two
