@@ -1109,7 +1109,14 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           reach *= 16.f;
           list = true;
         }
-        __syncthreads();
+        // The next list is written into every CTA's s_list by all of them, and the last cluster
+        // barrier came before this one was ranked: they meet once more where there was a list.
+        // (Lists that nobody ranked, too long or of bins below the border, are not read after that
+        // barrier; bins, sums and lengths alternate.)
+        if (lists)
+          sync();
+        else
+          __syncthreads();
       }
       summed = dense ? 0u : bhi;
     }

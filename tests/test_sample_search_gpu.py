@@ -1,0 +1,50 @@
+"""Sampling (fa_sample): the search for top-p's border where the first estimate, counts in
+bins times the weight of a bin's middle, misses it."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_sample_gpu import DT, check
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    return t.view(torch.int32)
+
+
+def below_the_first_list(V, rng):
+    """A row, and a top_p, whose border lies below what the first list holds (temperature 1).
+    Hundreds of tokens at the lower edges of their bins (1/64 wide), so that the estimate makes
+    them too heavy; a few tokens, among which it finds the border; then, a gap below, tokens at
+    the upper edges of theirs, among whose first ones the border is."""
+    x = -60.0 + rng.normal(0, 1, V)
+    n1, n2, n3 = int(rng.integers(300, 900)), int(rng.integers(10, 60)), int(rng.integers(400, 1500))
+    at = rng.permutation(V)[:n1 + n2 + n3]
+    x[at[0]] = 0.0
+    x[at[1:n1]] = -(2.5 + (rng.integers(0, 32, n1 - 1) + 0.45) / 64)
+    x[at[n1:n1 + n2]] = -(3.2 + rng.uniform(0, 0.8, n2))
+    x[at[n1 + n2:]] = -(4.5 + (rng.integers(0, 32, n3) - 0.45) / 64)
+    x = x.astype(np.float32)
+    w = np.exp(x.astype(np.float64))
+    return x, float(w[x > -4.2].sum() / w.sum() + rng.uniform(-0.0005, 0.0015))
+
+
+# Rows and vocabularies of clusters of 1, 2, 4 and 8 CTAs.
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+@pytest.mark.parametrize("R,V", [(300, 6000), (200, 8000), (64, 8000), (40, 33000)])
+def test_border_below_the_first_list(fa, R, V, dtype):
+    """List after list, beside rows that are done sooner: the tokens and distributions of the
+    64-bit form, and the same bits every time."""
+    rng = np.random.default_rng(V + R)
+    rows = [below_the_first_list(V, rng) for _ in range(R)]
+    x = torch.from_numpy(np.stack([r[0] for r in rows])).to(DT[dtype])
+    p = [tp if r % 4 else 1.0 for r, (_, tp) in enumerate(rows)]
+    k = [0 if r % 8 else 20 for r in range(R)]
+    u = rng.random(R).astype(np.float32).tolist()
+    t0, p0 = check(fa, x, u, k=k, p=p)
+    f = lambda v, t: torch.tensor(v, dtype=t, device="cuda")  # noqa: E731
+    xd, args = x.cuda(), dict(top_k=f(k, torch.int32), top_p=f(p, torch.float32), probs=True)
+    for _ in range(100):
+        t1, p1 = fa.sample(xd, f(u, torch.float32), **args)
+        assert torch.equal(t0, t1) and torch.equal(bits(p0), bits(p1))
