@@ -897,8 +897,10 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         want *= tp;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          // (Each thread's sums have roundings of their own, so two threads may both find it; all
+          // CTAs of the cluster have to take the same.)
           if (before < want && want <= before + m4[e])
-            s_i[3] = (4 * t + e) << 1 | (h[e] <= sa::LIST / 4 ? 1 : 0);
+            atomicMax(&s_i[3], (4 * t + e) << 1 | (h[e] <= sa::LIST / 4 ? 1 : 0));
           before += m4[e];
         }
         __syncthreads();
@@ -1068,8 +1070,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
               m = max(1, min(most, (int)ceilf(__fdividef(need.hi, w.hi))));
               while (m > 1 && !exceeds(target, sum_of(before, times(w, (float)(m - 1))))) --m;
               while (m < most && exceeds(target, sum_of(before, times(w, (float)m)))) ++m;
-              s_found = (uint32_t)(4 * t + e) << 21 | (uint32_t)m << 1 |
-                      ((shift > 0 ? most <= sa::LIST / 4 : m < most) ? 1u : 0u);
+              // (The first, where the sums' rounding lets two threads find it.)
+              atomicMin(&s_found, (uint32_t)(4 * t + e) << 21 | (uint32_t)m << 1 |
+                                      ((shift > 0 ? most <= sa::LIST / 4 : m < most) ? 1u : 0u));
               break;
             }
             before = after;

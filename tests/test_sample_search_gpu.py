@@ -48,3 +48,31 @@ def test_border_below_the_first_list(fa, R, V, dtype):
     for _ in range(100):
         t1, p1 = fa.sample(xd, f(u, torch.float32), **args)
         assert torch.equal(t0, t1) and torch.equal(bits(p0), bits(p1))
+
+
+def equal_bins(n):
+    """Twelve tokens in the middle of each of the estimate's bins from 2 temperatures down, a
+    largest one; and the shares of the weight that end with a bin of the next thread's."""
+    x = np.concatenate([[0.0], -np.repeat((np.arange(513, 1100) - 385) / 64, 12)]).astype(np.float32)
+    w = np.exp(x.astype(np.float64))
+    ends = np.cumsum(w)[[12 * (4 * t - 513) for t in range(130, 130 + n)]] / w.sum()
+    return x, ends
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_top_p_on_the_estimates_borders(fa, dtype):
+    """Consecutive values of top_p around sums that end with a thread's bins: there, by the
+    rounding of its sums, more than one thread or none finds the border's bin."""
+    rng = np.random.default_rng(3)
+    x, ends = equal_bins(8)
+    p = [float(np.float32(e) + np.float32(k * 2.0 ** -24)) for e in ends for k in range(-12, 13)]
+    order = rng.permutation(len(x))
+    x = torch.from_numpy(x[order])[None].expand(len(p), -1).contiguous().to(DT[dtype])
+    u = rng.random(len(p)).astype(np.float32).tolist()
+    t0, p0 = check(fa, x, u, p=p)
+    f = lambda v: torch.tensor(v, device="cuda")  # noqa: E731
+    xd = x.cuda()
+    for at in (slice(None), slice(0, 60)):  # clusters of 2 and of 4
+        for _ in range(40):
+            t1, p1 = fa.sample(xd[at], f(u)[at], top_p=f(p)[at], probs=True)
+            assert torch.equal(t0[at], t1) and torch.equal(bits(p0[at]), bits(p1))
