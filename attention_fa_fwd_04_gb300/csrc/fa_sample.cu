@@ -59,6 +59,7 @@ constexpr int BINS = 2048;
 constexpr int SEGS = CLUSTER * WARPS;  // index-ordered segments of a row, one per warp
 constexpr int LIST = 512;              // tokens that a CTA ranks
 constexpr int SMEM_MAX = 176 * 1024;   // bytes of a CTA's part of a row
+constexpr int TRIES = 10;              // rounds of top-p's search before it halves
 }  // namespace sa
 
 struct SampleParams {
@@ -919,7 +920,16 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
       float reach = 0.25f * temp;
       auto key_of = [](float v) { return Lg::key(Lg::from(v)); };
       bool dense = false;
+      int tries = 0;
       for (bool have_total = false;; have_total = true) {
+        // After TRIES rounds [elo, ehi] is halved every time, and is exact once it is 2048 keys:
+        // 32 more at the most.  (Rows are mostly done after one to four.  Bins alone may leave all
+        // but a 2048th of the keys every third round: 24000 rounds at a temperature of 1e-7.)
+        if (++tries > sa::TRIES) {
+          blo = elo;
+          bhi = elo + ((ehi - elo) >> 1);
+          list = false;
+        }
         // Above min_p's border only what lies there counts.
         if (bhi + 1 < lowest) bhi = blo = max(lowest - 1, elo);
         const int shift = shift_of(blo, bhi);

@@ -76,3 +76,41 @@ def test_top_p_on_the_estimates_borders(fa, dtype):
         for _ in range(40):
             t1, p1 = fa.sample(xd[at], f(u)[at], top_p=f(p)[at], probs=True)
             assert torch.equal(t0[at], t1) and torch.equal(bits(p0[at]), bits(p1))
+
+
+def time_of(fa, x, u, **settings):
+    """Microseconds of a call."""
+    def run(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(n):
+            fa.sample(x, u, **settings)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b) * 1e3 / n
+    run(3)
+    return min(run(5) for _ in range(3))
+
+
+def settings_of(R, T, p):
+    return dict(temperature=torch.full((R,), T, device="cuda"), top_p=torch.full((R,), p, device="cuda"))
+
+
+@pytest.mark.parametrize("V,T,scale,p", [
+    (5000, 1e-7, 2.5, 0.9),          # differences of logits are millions of temperatures
+    (1431, 4930.0, 2.0 ** 60, 0.5),  # the same, far from 0
+    (5000, 2.0 ** -99, 2.5, 0.95),   # the lowest temperature that counts
+    (5000, 1.0, 2.0 ** -21, 1 - 2.0 ** -20),  # nearly equal logits of which nearly all stay
+])
+def test_no_row_is_looked_for_long(fa, V, T, scale, p):
+    """Rows whose border the bins do not show are found by halving: a call takes some tens of
+    rounds, not thousands (42 rounds of less than a plain call each; 20000 would be hundreds)."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(8, V, generator=g) * scale
+    if scale < 1:
+        x = 5.0 + torch.rand(8, V, generator=g) * 2 * scale - scale
+    u = torch.rand(8, generator=g).tolist()
+    check(fa, x, u, T=[T] * 8, p=[p] * 8)
+    xd, ud = x.cuda(), torch.tensor(u, device="cuda")
+    plain = torch.randn(8, V, generator=g).cuda()
+    assert time_of(fa, xd, ud, **settings_of(8, T, p)) < 42 * time_of(fa, plain, ud, **settings_of(8, 1.0, 0.9))
