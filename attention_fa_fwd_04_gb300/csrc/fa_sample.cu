@@ -862,9 +862,13 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         const float per = -0.6931471805599453f * weigh.s_hi;
         const float2 fine = twice(256.f * per), coarse = twice(64.f * per);
         // Bins of the top: 1 and 385, but for what the sums' rounding to whole numbers adds.
-        const float fine0 = 8388609.f - fine.x * top, coarse0 = 8388993.f - coarse.x * top;
-        const float fine_top = __fmaf_rn(fine.x, top, fine0 - 8388608.f);
-        const float coarse_top = __fmaf_rn(coarse.x, top, coarse0 - 8388608.f);
+        // (Of logits as the weights take them, less the largest where it is many temperatures from
+        // 0: the bins would lose their places beside it.)
+        const float2 less = twice(weigh.shift);
+        const float rest = top + weigh.shift;
+        const float fine0 = 8388609.f - fine.x * rest, coarse0 = 8388993.f - coarse.x * rest;
+        const float fine_top = __fmaf_rn(fine.x, rest, fine0 - 8388608.f);
+        const float coarse_top = __fmaf_rn(coarse.x, rest, coarse0 - 8388608.f);
         auto below_top = [&](int b) {  // in temperatures, the middle of a bin
           return b < 513 ? ((float)b - fine_top) * (1.f / 256.f)
                          : ((float)b - coarse_top) * (1.f / 64.f);
@@ -873,7 +877,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
         each([&](int, uint4 g) {
 #pragma unroll
           for (int x = 0; x < GROUP / 2; ++x) {
-            const float2 v = Lg::pair(g, x);
+            const float2 v = __fadd2_rn(Lg::pair(g, x), less);
             const float2 z = __ffma2_rn(v, fine, twice(fine0));
             const float2 y = __ffma2_rn(v, coarse, twice(coarse0));
             const uint32_t a = __float_as_uint(fminf(z.x, y.x)) - 0x4b000000u;

@@ -114,3 +114,21 @@ def test_no_row_is_looked_for_long(fa, V, T, scale, p):
     xd, ud = x.cuda(), torch.tensor(u, device="cuda")
     plain = torch.randn(8, V, generator=g).cuda()
     assert time_of(fa, xd, ud, **settings_of(8, T, p)) < 42 * time_of(fa, plain, ud, **settings_of(8, 1.0, 0.9))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,at,scale", [(1e-7, 0.0, 2.5), (0.01, 1e5, 2.0), (0.3, -3e4, 2.0), (4930.0, 0.0, 2.0 ** 60),
+                                        (2.0 ** -99, 0.0, 2.5), (1e-4, 20.0, 3.0)])
+def test_many_temperatures_from_zero(fa, T, at, scale, dtype):
+    """The estimate holds however many temperatures the logits are from 0: a call takes what one
+    near 0 does (three times is allowed; without it the search halves, six times and more)."""
+    g = torch.Generator().manual_seed(21)
+    x = (at + torch.randn(8, 5000, generator=g) * scale).to(DT[dtype])
+    u = torch.rand(8, generator=g).tolist()
+    p = [0.9013, 0.3007, 0.9991, 0.5511, 0.7023, 0.9517, 0.1111, 0.4303]
+    check(fa, x, u, T=[T] * 8, p=p)
+    check(fa, x, u, T=[T] * 8, p=p, m=[0.01] * 8, k=[0, 4000] * 4)
+    if dtype == "fp32":
+        xd, ud = x.cuda(), torch.tensor(u, device="cuda")
+        plain = torch.randn(8, 5000, generator=g).cuda()
+        assert time_of(fa, xd, ud, **settings_of(8, T, 0.9)) < 3 * time_of(fa, plain, ud, **settings_of(8, 1.0, 0.9))
