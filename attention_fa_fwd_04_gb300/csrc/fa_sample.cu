@@ -1111,7 +1111,10 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
           bhi = bspan >> 1 > 1u << shift ? blo + (1u << shift) : blo + (bspan >> 1);
           blo = min(max(key_of(vlo - reach), elo), bhi);
           reach *= 16.f;
-        } else if (blo == elo) {  // (the sums' rounding) everything
+        } else if (blo == elo) {
+          // (The sums' rounding: the keys from elo on come to the target, as an earlier look
+          // from below said, or they are all.)
+          border = elo;
           dense = true;
           break;
         } else if (blo <= lowest) {  // below the bins, and min_p's border in them
