@@ -372,8 +372,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   const int first = rank * n - lead;  // token of this part's first element
   uint4* const part = reinterpret_cast<uint4*>(smem_raw);
   float temp = p.temperature ? p.temperature[row] : 1.f;
-  if (temp > 0x1p99f) temp = 0x1p99f;
   const bool greedy = !(temp > 0.f);
+  // (Once, for the weights, min-p's border and the search's steps alike.)
+  temp = greedy ? 1.f : fminf(fmaxf(temp, 0x1p-99f), 0x1p99f);
   const int k = p.top_k ? p.top_k[row] : 0;
   const float tp = p.top_p ? p.top_p[row] : 1.f;
   const float mp = p.min_p ? p.min_p[row] : 0.f;
@@ -426,10 +427,9 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
   Weigher weigh;
   weigh.table = s_table + (lane & 15);
   {
-    const float tt = greedy ? 1.f : fmaxf(temp, 0x1p-99f);
-    const float inv = __fdividef(1.f, tt);  // (what it is off by goes into s_lo)
+    const float inv = __fdividef(1.f, temp);  // (what it is off by goes into s_lo)
     weigh.s_hi = 1.44269502162933349609f * inv;
-    weigh.s_lo = __fmul_rn(inv, __fadd_rn(__fmaf_rn(-weigh.s_hi, tt, 1.44269502162933349609f),
+    weigh.s_lo = __fmul_rn(inv, __fadd_rn(__fmaf_rn(-weigh.s_hi, temp, 1.44269502162933349609f),
                                           1.92596299112661746887e-8f));
   }
   sync();

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import serving_plain as sp
 from tests.test_sample_gpu import DT, check
 
 pytestmark = pytest.mark.gpu
@@ -154,3 +155,26 @@ def test_target_within_the_sums_rounding_of_a_border(fa, seed):
     # One of the second kind more is at most e^-4.2 / (1 + 199 e^-3) < 0.0014 of the weight, one of
     # the first missing e^-2.49 / (1 + 199 e^-3) < 0.0077.
     assert int((kept > p + 0.0014).sum()) == 0 and int((kept < p - 0.0077).sum()) == 0
+
+
+@pytest.mark.parametrize("T", [2.0 ** -149, 2.0 ** -148, 2.0 ** -130, 2.0 ** -120, 2.0 ** -100, 2.0 ** -99])
+def test_temperatures_below_the_least(fa, T):
+    """They count as 2^-99: in the weights, in min-p's border, and in how far top-p's search
+    steps.  Logits of a few such temperatures, and ordinary ones."""
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(12, 3000, generator=g) * 2
+    x[:8] *= 2.0 ** -100
+    x[0] = -1.0
+    x[0, 100], x[0, 2000] = 0.0, -(2.0 ** -100)   # weights 1 and e^-1/2
+    u = torch.rand(12, generator=g).tolist()
+    u[0] = 0.8
+    k, p, m = [0, 40, 0] * 4, [1.0, 1.0, 0.9, 0.5] * 3, [0.5, 0.0, 0.3, 0.0, 0.0, 0.2] * 2
+    f = lambda v, t=torch.float32: torch.tensor(v, dtype=t, device="cuda")  # noqa: E731
+    tokens, probs = fa.sample(x.cuda(), f(u), temperature=f([T] * 12), top_k=f(k, torch.int32), top_p=f(p),
+                              min_p=f(m), probs=True)
+    f32 = lambda v: float(np.float32(v))  # noqa: E731
+    for r in range(12):
+        tok, dist, margin = sp.sample(x[r].double().numpy(), f32(u[r]), 2.0 ** -99, k[r], f32(p[r]), f32(m[r]))
+        assert margin > 1e-9 and int(tokens[r]) == tok, r
+        assert np.array_equal(probs[r].cpu().numpy() > 0, dist > 2.0 ** -119), r
+    assert int(tokens[0]) == 2000 and int((probs[0] > 0).sum()) == 2
