@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_decode.cu", "fa_decode_noalloc.cu",
            "fa_backward.cu", "fa_host.cu", "fa_rope.cu", "fa_tree.cu", "fa_verify.cu",
            "fa_shared.cu", "fa_sample.cu", "fa_pages.cu"]
-HEADERS = ["fa_ptx.cuh", "fa_tiles.cuh", "fa_exp2_table.h", "fa_internal.h"]
+HEADERS = ["fa_ptx.cuh", "fa_tiles.cuh", "fa_exp2_table.h", "fa_shares.h", "fa_internal.h"]
 BIND = os.path.join(HERE, "_fa_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "fa_bind.cpp")
 BIND_STAMP = os.path.join(HERE, "_fa_bind.torch")  # version of the torch it was built against

@@ -49,6 +49,7 @@
 #include "fa.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
+#include "fa_shares.h"
 #include "fa_tiles.cuh"
 
 namespace fa {
@@ -69,13 +70,6 @@ constexpr int COST = 3, SLACK = 4, SLACK_FEW = 2;
 constexpr int FEW = 16;       // rows that a warp streams keys for
 constexpr int FEW_WARPS = 6;  // such warps of a CTA
 constexpr int FEW_KEYS = 32;  // keys of their tiles
-// What a place costs in time, for the sharing out of the CTAs: 16 in the list of tiles, and
-// in the streamed one 5 up to 8 rows, up to 16 rows 10 (D = 128) or 6 (D = 64).  Measured: 64
-// sequences of 8 rows behind 8192 keys 75, 58.5, 60, 66 us at 2, 4, 5, 6, behind 32768 114 and
-// 99 at 4 and 5; 32 of 16 rows (D = 128) 194, 163, 146 at 6, 8, 10; 48 of 16 rows and 2000 keys
-// (D = 64) 37, 41, 43 at 6, 8, 10.
-constexpr int SHARE_MANY = 16;
-constexpr int share_few(int rows, int D) { return rows <= 8 ? 5 : (D == 128 ? 10 : 6); }
 constexpr int RING = 4;        // stretches told ahead
 constexpr long long L2_KEEPS = 48 << 20;  // bytes of a unit's K/V, over all kv heads
 
@@ -176,11 +170,6 @@ struct SharedParams {
   float c;  // scale * log2(e)
   int merge_rows;  // of a merge block
 };
-
-// a / b in 32 bits where both fit.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
 
 // Several pairs of row tiles against more keys than L2 keeps.
 __device__ __forceinline__ bool can_be_cut(const SharedParams& p, const sh::Shape& s) {
@@ -383,13 +372,10 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   }
   const int n = p.ctas;
   // CTAs of the first kind, for lists of a and z places.
-  auto share = [&](long long a, long long z) {
-    if (a == 0) return 0;
-    if (z == 0) return n;
-    const long long x = quotient(a * n * sh::SHARE_MANY, a * sh::SHARE_MANY + z * p.share_few);
-    return max(1, min(n - 1, (int)x));
+  auto share = [&](long long a, long long z, long long starts) {
+    return sh::ctas_of_tiles(a, z, starts, n, p.share_few);
   };
-  const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1])) * sh::COST;
+  const long long per = (long long)max(1, share(all_tiles[0], all_tiles[1], 0)) * sh::COST;
   const long long width = quotient(all_tiles[0] + per - 1, per);
   const int W = width < 1 ? 1 : (width > INT32_MAX ? INT32_MAX : (int)width);
   const int slack[2] = {all_tiles[0] > (long long)n * sh::COST ? sh::SLACK : 0,
@@ -439,9 +425,8 @@ __device__ __forceinline__ void shared_plan(const SharedParams& p, sh::Plan* pl)
   // (Units of a tile or two cost their starts too where they have no places for them: 64
   // sequences with a token each behind 8192 43 us, 56 without; 32 with 30 tokens behind 65536
   // 128 and 260.)
-  const int many = share(total[0], total[1] + (one && slack[1] == 0
-                                                   ? sh::SLACK_FEW * (all_pieces & 0xffffffffll)
-                                                   : 0));
+  const int many = share(total[0], total[1],
+                         one && slack[1] == 0 ? sh::SLACK_FEW * (all_pieces & 0xffffffffll) : 0);
   const long long most = quotient(total[0], 2 * sh::COST);
   const int used[2] = {most < 1 ? 1 : (int)min(most, (long long)max(many, 1)),
                        (int)max(1ll, min(total[1], (long long)(n - many) * sh::FEW_WARPS))};
