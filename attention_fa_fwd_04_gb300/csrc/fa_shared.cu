@@ -1446,7 +1446,7 @@ __global__ void __launch_bounds__(join::THREADS, join::resident(AHEAD)) shared_m
         const int kind = item < n0 ? 0 : 1;
         const int e = kind ? s_list[2][item - n0] : s_list[l][item];
         const bool few = kind && p.few;
-        // (Scratch is below 2^32 times 16 bytes.)
+        // (Partials of either kind are at most 2^32 times 16 bytes.)
         const uint32_t slots = few ? p.SqG : 2 * p.half[kind];
         const uint32_t slot = at[kind] + (e & 1 ? p.half[kind] : 0), id = e >> 1;
         ml[u] = reinterpret_cast<const float2*>(p.part_ml[kind])[id * slots + slot];
@@ -1644,6 +1644,8 @@ extern "C" int fa_decode_shared_fwd(const void* q, const void* kpages, const voi
                    ? 0
                    : (size_t)units[k] * Hkv + (few ? fa::sh::FEW_WARPS : 2) * (size_t)p.ctas;
     const size_t in_slot = few ? p.SqG : 2 * p.half[k];
+    // The merge counts 16-byte pieces of partials in 32 bits.
+    if (slots[k] * in_slot * (D / 4) > (size_t)1 << 32) return FA_ERR_UNSUPPORTED;
     at_o[k] = bytes;
     bytes += slots[k] * D * in_slot * sizeof(float);
     at_ml[k] = bytes;

@@ -567,7 +567,9 @@ int fa_compact_tree(void* kpages, void* vpages, const int32_t* page_table,
  * groups and prefixes are never read on the host; equal calls give equal bits.
  * Partials live in stream-ordered scratch.  A few sequences behind a prefix that L2 holds
  * anyway are faster with fa_decode_paged_fwd (8 of 1700 tokens, Hq8/Hkv2: 13 us, 18 here).
- * Returns FA_ERR_UNSUPPORTED for more than 1024 groups, else as fa_decode_paged_fwd.
+ * Returns FA_ERR_UNSUPPORTED for more than 1024 groups, and where the partials of the groups or
+ * of the sequences would pass 64 GiB (67 million rows of 17 per kv head, say, at D = 128), else
+ * as fa_decode_paged_fwd.
  */
 int fa_decode_shared_fwd(const void* q, const void* kpages, const void* vpages,
                          const int32_t* page_table, const int32_t* seqlens,

@@ -40,6 +40,16 @@ def test_shared_limits_and_empty(fa):
         assert shared(fa, **kw) == fa.FA_OK
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=4_100_000, Sq=17, Hq=1, Hkv=1), dict(B=2_050_000, Sq=17, Hq=2, Hkv=2, groups=0),
+    dict(B=8_200_000, Sq=17, Hq=1, Hkv=1, D=64, groups=0), dict(B=1_000_000, Sq=16, Hq=16, Hkv=16, groups=0),
+    dict(B=1 << 20, Sq=16, Hq=64, Hkv=8, groups=1024),
+])
+def test_shared_refuses_partials_past_the_merges_index(fa, kw):
+    """More than 2^32 pieces of 16 bytes: rows in two parts of a slot, streamed rows, groups' rows."""
+    assert shared(fa, **kw) == fa.FA_ERR_UNSUPPORTED
+
+
 def sample(fa, **kw):
     a = dict(x=FAKE, u=FAKE, T=0, k=0, p=0, m=0, tok=FAKE, probs=0, rows=3, V=1000, stride=1000,
              dtype=fa.FA_FP32)
