@@ -76,8 +76,10 @@ struct SampleParams {
   int groups;  // 16-byte groups of the row per thread
 };
 
-// Logits as they are stored, and their order as whole numbers (NaN counts as -infinity,
-// -0 as 0).
+// Logits as they are stored, and their order as whole numbers, their keys (NaN counts as
+// -infinity, -0 as 0).  Negative numbers' keys are their distance below 0's, so that -0 has
+// none of its own: neighbouring keys are different values, and a comparison of values is one
+// of keys.  (The search relies on that: a key past its bounds would be past the bins.)
 template <typename T>
 struct Logits;
 template <>
@@ -95,10 +97,10 @@ struct Logits<float> {
     return __float_as_uint(fmaxf(x + 0.f, -INFINITY));  // (of a NaN and a number, the number)
   }
   static __device__ __forceinline__ uint32_t key(raw r) {
-    return r ^ (uint32_t)((int32_t)r >> 31 | (int32_t)0x80000000);
+    return r & 0x80000000u ? 0u - r : r | 0x80000000u;
   }
   static __device__ __forceinline__ raw unkey(uint32_t k) {
-    return k & 0x80000000u ? k ^ 0x80000000u : ~k;
+    return k & 0x80000000u ? k ^ 0x80000000u : 0u - k;
   }
   static __device__ __forceinline__ float clean(uint4& g) {  // all of a group's; the largest
     g = make_uint4(clean(g.x), clean(g.y), clean(g.z), clean(g.w));
@@ -116,10 +118,10 @@ struct Logits16 {
   typedef uint16_t raw;
   static constexpr int GROUP = 8;
   static __device__ __forceinline__ uint32_t key(raw r) {
-    return r & 0x8000u ? (uint16_t)~r : (uint16_t)(r | 0x8000u);
+    return r & 0x8000u ? (uint16_t)(0u - r) : (uint16_t)(r | 0x8000u);
   }
   static __device__ __forceinline__ raw unkey(uint32_t k) {
-    return k & 0x8000u ? (raw)(k ^ 0x8000u) : (raw)~k;
+    return k & 0x8000u ? (raw)(k ^ 0x8000u) : (raw)(0u - k);
   }
 };
 template <>

@@ -178,3 +178,39 @@ def test_temperatures_below_the_least(fa, T):
         assert margin > 1e-9 and int(tokens[r]) == tok, r
         assert np.array_equal(probs[r].cpu().numpy() > 0, dist > 2.0 ** -119), r
     assert int(tokens[0]) == 2000 and int((probs[0] > 0).sum()) == 2
+
+
+@pytest.mark.parametrize("dtype,unit", [("fp32", 2.0 ** -149), ("fp32", 2.0 ** -60), ("bf16", 2.0 ** -133),
+                                        ("bf16", 2.0 ** -60), ("fp16", 2.0 ** -24), ("fp16", 2.0 ** -14)])
+def test_bounds_of_the_search_around_zero(fa, dtype, unit):
+    """Logits of a few units to either side of 0, many of them 0: the search's bounds come to lie
+    between 0 and the largest negative number, and 0 is on one side of them."""
+    g = torch.Generator().manual_seed(41)
+    R, V = 48, 4999
+    x = (torch.randint(-40, 41, (R, V), generator=g).double() * unit).to(DT[dtype])
+    x[::2, ::3] = 0.0
+    x[1::4, ::5] = -0.0
+    u = torch.rand(R, generator=g).tolist()
+    p = [(r + 0.5371) / R for r in range(R)]
+    check(fa, x, u, p=p)
+    check(fa, x, u, T=[0.01 + 0.1 * r for r in range(R)], p=p, m=[0.0, 0.5] * (R // 2))
+    check(fa, x, u, p=p, k=[100 * r for r in range(R)])
+    check(fa, x, u, k=[100 * r + 1 for r in range(R)])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_min_p_that_ends_at_zero(fa, dtype):
+    """Of logits up to 0, the zeros alone with min_p = 1; of logits up to 1, those from 0 on with
+    the number before 1 / e (16-bit logits; T ln(min_p) + 1 is just below 0)."""
+    g = torch.Generator().manual_seed(42)
+    x = -torch.rand(12, 3001, generator=g) - 2.0 ** -10
+    x[:, 5:40:7] = 0.0
+    x[::3, 2000:2100] = -0.0
+    u = torch.rand(12, generator=g).tolist()
+    p = [0.1 + 0.0713 * r for r in range(12)]
+    check(fa, x.to(DT[dtype]), u, p=p, m=[1.0] * 12)
+    check(fa, x.to(DT[dtype]), u, p=p, m=[1.0] * 12, T=[0.2 + r for r in range(12)])
+    if dtype != "fp32":
+        x[:, 77] = 1.0
+        below = float(np.nextafter(np.float32(np.exp(-1.0)), np.float32(0)))
+        check(fa, x.to(DT[dtype]), u, p=[0.999 - 0.001 * r for r in range(12)], m=[below] * 12)
