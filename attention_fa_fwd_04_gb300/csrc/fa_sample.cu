@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
     }
   }
   if (t == sa::THREADS - 32 && mp > 0.f) {
-    const double x = fmin((double)temp * log((double)mp), 0.0);
+    const double x = fmin((double)temp * log((double)mp), 0.0);  // (above 1: one token is kept)
     s_low = make_float2((float)x, (float)(x - (double)(float)x));
   }
   {
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(sa::THREADS, 2) sample_kernel(const __grid_con
     sync();
     return s_cut;
   };
-  if (alive && (greedy || k == 1 || tp <= 0.f)) {
+  if (alive && (greedy || k == 1 || tp <= 0.f || mp > 1.f)) {
     border = kmax;
     ties = 1;
     limited = true;

@@ -214,3 +214,15 @@ def test_min_p_that_ends_at_zero(fa, dtype):
         x[:, 77] = 1.0
         below = float(np.nextafter(np.float32(np.exp(-1.0)), np.float32(0)))
         check(fa, x.to(DT[dtype]), u, p=[0.999 - 0.001 * r for r in range(12)], m=[below] * 12)
+
+
+@pytest.mark.parametrize("m", [1.0000001, 3.0, float("inf")])
+def test_min_p_above_1_keeps_one_token(fa, m):
+    """No weight reaches it, and one token is kept at least: the lowest of the largest, of which
+    there are several."""
+    g = torch.Generator().manual_seed(43)
+    x = torch.randn(6, 2003, generator=g).clamp(max=1.5)
+    u = torch.rand(6, generator=g).tolist()
+    for kw in (dict(), dict(p=[0.9] * 6), dict(k=[50] * 6), dict(k=[700] * 6, p=[0.5] * 6), dict(T=[0.0] * 6)):
+        tokens, probs = check(fa, x, u, m=[m] * 6, **kw)
+        assert ((probs > 0).sum(-1) == 1).all()
