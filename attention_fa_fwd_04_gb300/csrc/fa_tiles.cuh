@@ -16,35 +16,6 @@ constexpr int BM = 128;    // query rows per tile
 constexpr int BN = 128;    // keys per K/V tile
 constexpr int HALF_BYTES = 128 * 128;  // 128 rows x 64 elements x 2 bytes
 constexpr int BAD_RING = 16;  // tiles whose page faults are remembered (> tiles in flight)
-
-template <int D, int MT>
-struct Cfg {
-  static constexpr int HALVES = D / 64;
-  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
-  // MT = 2: three warpgroups, for the register split (setmaxnreg): launched with
-  // 168 registers a thread, the softmax warpgroups take 208, the third keeps 88
-  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).  The compiler spills
-  // 344 bytes of stores and 508 of loads there (MT = 1, 253 registers: none).
-  static constexpr int THREADS = MT == 1 ? 192 : 384;
-  static constexpr int RT = MT * BM;  // rows per CTA
-  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 4) : 12;
-  // MT = 2 (matrix-bound): ring positions 2g - 1 (a V) and 2g (the K after it)
-  // share a pair of slots, released by one commit, and land on one barrier: the
-  // MMA warp's instruction stream paces the kernel, and a commit or a wait
-  // less per tile shows.  MT = 1 (bound by memory) releases slots one by one.
-  static constexpr bool PAIRED = MT == 2;
-  static constexpr int NPAIR = NSTAGE / 2;
-  static_assert(NSTAGE % 2 == 0, "pairs");
-  static constexpr int SMEM_Q = MT * TILE_BYTES;
-  static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
-  static constexpr int SMEM_BAR = 512;
-  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV + SMEM_BAR;
-  static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
-  static_assert(NSTAGE / 2 + 2 < BAD_RING, "tiles in flight");
-  // Tensor memory: two S buffers (MT = 1: of alternate tiles; MT = 2: of the
-  // two row tiles), then O of each row tile.
-  static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
-};
 }  // namespace tiles
 
 // a * b / c and a / c in 32 bits where they fit: a 64-bit division is a few
@@ -98,7 +69,6 @@ struct TileType<__half> {
   }
 };
 
-
 // A row of Q (D elements; zeros if !real) as row `tid` of a 128-row tile, in the
 // swizzled layout of a TMA load.
 template <int D>
@@ -151,6 +121,8 @@ __device__ __forceinline__ void hide_keys(uint32_t (&sr)[4][32], const Mask128& 
 // A first tile takes its own maximum; later ones are exponentiated against the
 // running one, and a warp takes the slow path only when a row's sum outgrows kBig or
 // a row had seen no key yet.
+// P is rounded to the inputs' type, which the matrix instructions take (half a step, 2^-8 or
+// 2^-11, of sum p |v| / sum p); the sum is of P as it was, in fp32.
 template <int D, typename T, typename Mask, typename Settled>
 __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, float c, bool first,
                                              bool masked, Mask&& mask, Settled&& settled,

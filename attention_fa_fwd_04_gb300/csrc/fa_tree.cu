@@ -56,6 +56,35 @@ __device__ unsigned int g_tree_err = 0;
 namespace tr {
 using namespace tiles;
 constexpr int MAX_N = 64;  // tree nodes: one 64-bit ancestor mask per row
+
+template <int D, int MT>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
+  // MT = 2: three warpgroups, for the register split (setmaxnreg): launched with
+  // 168 registers a thread, the softmax warpgroups take 208, the third keeps 88
+  // (256 * 208 + 128 * 88 = 384 * 168, the launch's registers).  The compiler spills
+  // 344 bytes of stores and 508 of loads there (MT = 1, 253 registers: none).
+  static constexpr int THREADS = MT == 1 ? 192 : 384;
+  static constexpr int RT = MT * BM;  // rows per CTA
+  static constexpr int NSTAGE = D == 128 ? (MT == 1 ? 6 : 4) : 12;
+  // MT = 2 (matrix-bound): ring positions 2g - 1 (a V) and 2g (the K after it)
+  // share a pair of slots, released by one commit, and land on one barrier: the
+  // MMA warp's instruction stream paces the kernel, and a commit or a wait
+  // less per tile shows.  MT = 1 (bound by memory) releases slots one by one.
+  static constexpr bool PAIRED = MT == 2;
+  static constexpr int NPAIR = NSTAGE / 2;
+  static_assert(NSTAGE % 2 == 0, "pairs");
+  static constexpr int SMEM_Q = MT * TILE_BYTES;
+  static constexpr int SMEM_KV = NSTAGE * TILE_BYTES;
+  static constexpr int SMEM_BAR = 512;
+  static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_KV + SMEM_BAR;
+  static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
+  static_assert(NSTAGE / 2 + 2 < BAD_RING, "tiles in flight");
+  // Tensor memory: two S buffers (MT = 1: of alternate tiles; MT = 2: of the
+  // two row tiles), then O of each row tile.
+  static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
+};
 }  // namespace tr
 
 struct TreeParams {
