@@ -765,7 +765,8 @@ def update_pages(page_table, old_lens, new_lens, free_pages, free_count, page_si
     [max_new]): the lengths that hold now (a sequence that found no room keeps its old one),
     the free pages left, and for every new token, sequence after sequence, its slot in the
     cache (-1 behind the last) and its position.  lens_out may be old_lens or new_lens,
-    free_count_out may be free_count (new tensors if None)."""
+    free_count_out may be free_count (new tensors if None).  New tensors are parts of one
+    allocation, which lives as long as any of them: copy what is to outlive the step."""
     r = (_native or _load_native()).update_pages(page_table, old_lens, new_lens, free_pages,
                                                  free_count, page_size, max_new, shared_pages,
                                                  lens_out, free_count_out, stream)

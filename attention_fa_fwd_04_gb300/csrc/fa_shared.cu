@@ -37,9 +37,12 @@
 // the others stretch by stretch, ahead of them.
 //
 // Measured (both kernels, device time in a captured sequence; floor): 64 sequences of 8 rows
-// per kv head behind 8192 tokens 57.5 us (31.5), 32 of 16 rows behind 65536 146.5 (73.4: 956
-// TFLOP/s and 3.0 TB/s together), 48 of 16 rows in 5 groups, D = 64, 30.5 (4.2), 8 of 4 rows
-// behind 1500 17.7 (0.4).  What bounds it: with many rows the softmax (two 128-row tiles per
+// per kv head behind 8192 tokens 52 to 64 us over several boxes and inputs (31.5), 32 of 16 rows
+// behind 65536 145 to 148 (73.4: 956 TFLOP/s and 3.0 TB/s together; 169 where calls follow each
+// other with nothing between, whose CTAs start under the merge of the call before), 48 of 16
+// rows in 5 groups, D = 64, 30.1 (4.2), 8 of 4 rows behind 1500 17.6 (0.4), 128 of 32 rows behind
+// 128 with up to 100 keys of their own 78 (7.3).  At D = 128 the split kernel spills 96 bytes of
+// stores in 168 registers.  What bounds it: with many rows the softmax (two 128-row tiles per
 // key tile take 1.76 us, their MMAs 1.34) on the SMs of the prefixes and the stream on the
 // others; with few, the lists (4 us), the first tiles (8) and the merge (4 to 10).
 #include <math.h>
@@ -617,7 +620,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // One tile of 32 keys: S^T = K Q^T (A = K rows by ldmatrix, B = Q from registers), an
 // online softmax, O^T += V^T P^T (A = V by transposing ldmatrix, B = P^T, the scores'
 // accumulator transposed per 8 x 8).  Keys [from, to) of the tile count; lim: of them the
-// rows' own limits.
+// rows' own limits.  (P is rounded to the inputs' type, as in the tiles of many rows.)
 template <int D, int NB, typename T>
 __device__ __forceinline__ void stream_tile(StreamRows<D, NB>& w, uint32_t k_tile, uint32_t v_tile,
                                             float c, bool masked, int from, int to,
